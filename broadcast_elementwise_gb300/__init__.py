@@ -48,6 +48,12 @@ STATUS = {0: "ok", 1: "invalid_arg", 2: "unsupported_op", 3: "unsupported_type",
           8: "cuda", 9: "family"}
 DEVICE_DIV_BY_ZERO = 0x1
 DEVICE_SHIFT_RANGE = 0x2
+DEVICE_POSITION_RANGE = 0x4
+DEVICE_WAIT_LIMIT = 0x8
+NORMS = {"none": 0, "rms": 1}
+LAYOUTS = {"half": 0, "interleaved": 1}
+SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 MAX_RANK = 8
 PLAN_CACHE_CAPACITY = 8
 
@@ -66,6 +72,30 @@ class ebin_attrs(ctypes.Structure):
                 ("epsilon", ctypes.c_float), ("clip_has_min", ctypes.c_int32),
                 ("clip_has_max", ctypes.c_int32), ("with_scalar", ctypes.c_int32),
                 ("scalar_b", ctypes.c_float)]
+
+
+class ebin_rotary_attrs(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("trained_length", ctypes.c_double), ("slow_turns", ctypes.c_double),
+                ("fast_turns", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class ebin_heads_view(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class ebin_heads_attrs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("dtype_w", ctypes.c_int), ("norm", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("gradient", ctypes.c_int32),
+                ("epsilon", ctypes.c_float), ("batch", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("position_type", ctypes.c_int32),
+                ("position_strides", ctypes.c_int64 * 2), ("table_positions", ctypes.c_int64),
+                ("q", ebin_heads_view), ("k", ebin_heads_view), ("dq", ebin_heads_view),
+                ("dk", ebin_heads_view), ("q_out", ebin_heads_view),
+                ("k_out", ebin_heads_view)]
 
 
 def _load():
@@ -105,6 +135,12 @@ def _load():
         "ebin_get_device_status": (i32, [vp, ctypes.POINTER(ctypes.c_uint32)]),
         "ebin_execute_noalloc": (i32, [vp, vp, vp, vp, vp, i32, ctypes.POINTER(ctypes.c_uint32)]),
         "ebin_noalloc_read_status": (i32, [i32, vp, ctypes.POINTER(ctypes.c_uint32)]),
+        "ebin_rotary_table": (i32, [ctypes.POINTER(ebin_rotary_attrs), i64, i64, vp, vp, vp]),
+        "ebin_heads_plan_create": (i32, [ctypes.POINTER(ebin_heads_attrs), ctypes.POINTER(vp)]),
+        "ebin_heads_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
+        "ebin_heads_plan_release": (None, [vp]),
+        "ebin_heads_execute": (i32, [vp] * 11),
+        "ebin_heads_grad_execute": (i32, [vp] * 15 + [ctypes.c_size_t, vp]),
         "ebin_launch_count": (ctypes.c_uint64, []),
         "ebin_dtype_size": (ctypes.c_size_t, [i32]),
         "ebin_status_string": (ctypes.c_char_p, [i32]),
@@ -306,6 +342,42 @@ def ebin_get_device_status(stream) -> int:
     v = ctypes.c_uint32()
     _check(lib.ebin_get_device_status(stream, ctypes.byref(v)), "ebin_get_device_status")
     return v.value
+
+
+def ebin_rotary_table(attrs, first_position, positions, cos, sin, stream) -> None:
+    _check(lib.ebin_rotary_table(ctypes.byref(attrs), int(first_position), int(positions), cos,
+                                 sin, stream), "ebin_rotary_table")
+
+
+def ebin_heads_plan_create(attrs) -> int:
+    out = ctypes.c_void_p()
+    _check(lib.ebin_heads_plan_create(ctypes.byref(attrs), ctypes.byref(out)),
+           "ebin_heads_plan_create")
+    return out.value
+
+
+def ebin_heads_plan_workspace(plan) -> int:
+    v = ctypes.c_size_t()
+    _check(lib.ebin_heads_plan_workspace(plan, ctypes.byref(v)), "ebin_heads_plan_workspace")
+    return v.value
+
+
+def ebin_heads_plan_release(plan) -> None:
+    lib.ebin_heads_plan_release(plan)
+
+
+def ebin_heads_execute(plan, q, k, cos, sin, positions, wq, wk, q_out, k_out, stream) -> None:
+    st = lib.ebin_heads_execute(plan, q, k, cos, sin, positions, wq, wk, q_out, k_out, stream)
+    if st:
+        raise EbinError(st, "ebin_heads_execute")
+
+
+def ebin_heads_grad_execute(plan, dq, dk, q, k, cos, sin, positions, wq, wk, dq_out, dk_out, dwq,
+                            dwk, workspace, workspace_bytes, stream) -> None:
+    st = lib.ebin_heads_grad_execute(plan, dq, dk, q, k, cos, sin, positions, wq, wk, dq_out,
+                                     dk_out, dwq, dwk, workspace, workspace_bytes, stream)
+    if st:
+        raise EbinError(st, "ebin_heads_grad_execute")
 
 
 def ebin_launch_count() -> int:
@@ -539,3 +611,239 @@ def _output(out, plan, desc, device):
     if device is not None and out.device != device:
         raise ValueError("binary: A is on %s and out on %s" % (device, out.device))
     return out
+
+
+# ----------------------------------------------------------------- heads: rotary positions, norms
+
+def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, trained_length: float = 0.0,
+                 slow_turns: float = 1.0, fast_turns: float = 32.0, amplitude: float = 1.0,
+                 first_position: int = 0, device="cuda", stream=None):
+    """(cos, sin), float32 [positions, rotary_dim / 2], formed in binary64 on the
+    device.  scaling, for contexts longer than the trained one: "linear" divides
+    every frequency by factor, "base" stretches the base, "by_parts" divides
+    what turns fewer than slow_turns times within trained_length, keeps what
+    turns more than fast_turns times and blends between."""
+    import torch
+    attrs = ebin_rotary_attrs(int(rotary_dim), SCALINGS[scaling], float(base), float(factor),
+                              float(trained_length), float(slow_turns), float(fast_turns),
+                              float(amplitude))
+    with torch.cuda.device(torch.device(device)):
+        cos = torch.empty(int(positions), int(rotary_dim) // 2, device="cuda")
+        sin = torch.empty_like(cos)
+        ebin_rotary_table(attrs, first_position, positions, _ptr(cos), _ptr(sin), _stream(stream))
+    return cos, sin
+
+
+def _heads_view(shape, strides, what):
+    """The (batch, token, head) strides of a [batch, tokens, heads, head_dim] view."""
+    if strides is None:
+        n = [int(d) for d in shape]
+        return ebin_heads_view(n[1] * n[2] * n[3], n[2] * n[3], n[3])
+    st = [int(v) for v in strides]
+    if len(st) != 4 or (st[3] != 1 and int(shape[3]) > 1):
+        raise ValueError("%s: the last dimension of a heads view is dense (strides %s)"
+                         % (what, tuple(st)))
+    return ebin_heads_view(st[0], st[1], st[2])
+
+
+class HeadsPlan:
+    """A plan of the operators on heads: rotary positions (norm "none") or the
+    RMS norm of each head and the rotation (norm "rms"), forward or gradient.
+
+    Shapes are [batch, tokens, heads, head_dim]; strides (None = dense) are the
+    views' element strides, as ``tensor.stride()`` gives them.  ``k_shape`` None
+    leaves k out.  ``positions``: None (token t is at position t), torch.int32
+    or torch.int64: the type of a [batch, tokens] tensor of positions, its
+    element strides ``position_strides``.  Run with execute_heads, or, for
+    norm "rms" with gradient=True, execute_heads_grad.
+    """
+
+    def __init__(self, dtype, q_shape, k_shape=None, *, norm: str = "none", epsilon: float = 1e-6,
+                 weight_dtype=None, layout: str = "half", rotary_dim: int | None = None,
+                 gradient: bool = False, positions=None, position_strides=None,
+                 table_positions: int = 0, q_strides=None, k_strides=None, dq_strides=None,
+                 dk_strides=None, q_out_strides=None, k_out_strides=None):
+        q_shape = tuple(int(d) for d in q_shape)
+        k_shape = (q_shape[0], q_shape[1], 0, q_shape[3]) if k_shape is None else \
+            tuple(int(d) for d in k_shape)
+        if len(q_shape) != 4 or len(k_shape) != 4:
+            raise ValueError("HeadsPlan: shapes are [batch, tokens, heads, head_dim]")
+        if (q_shape[0], q_shape[1], q_shape[3]) != (k_shape[0], k_shape[1], k_shape[3]):
+            raise ValueError("HeadsPlan: q is %s and k %s; they differ in heads only"
+                             % (q_shape, k_shape))
+        code = _dtype_code(dtype)
+        a = ebin_heads_attrs()
+        a.dtype = code
+        a.dtype_w = code if weight_dtype is None else _dtype_code(weight_dtype)
+        a.norm, a.layout = NORMS[norm], LAYOUTS[layout]
+        a.gradient, a.epsilon = int(bool(gradient)), float(epsilon)
+        a.batch, a.tokens, a.q_heads, a.head_dim = q_shape
+        a.k_heads = k_shape[2]
+        a.rotary_dim = q_shape[3] if rotary_dim is None else int(rotary_dim)
+        a.position_type = 0 if positions is None else _dtype_code(positions)
+        ps = (q_shape[1], 1) if position_strides is None else position_strides
+        a.position_strides = (ctypes.c_int64 * 2)(int(ps[0]), int(ps[1]))
+        a.table_positions = int(table_positions)
+        for name, shape, st in (("q", q_shape, q_strides), ("k", k_shape, k_strides),
+                                ("dq", q_shape, dq_strides), ("dk", k_shape, dk_strides),
+                                ("q_out", q_shape, q_out_strides),
+                                ("k_out", k_shape, k_out_strides)):
+            setattr(a, name, _heads_view(shape, st, name))
+        self.q_shape, self.k_shape = q_shape, k_shape
+        self.handle = ebin_heads_plan_create(a)
+        self.workspace_bytes = ebin_heads_plan_workspace(self.handle)
+
+    def close(self):
+        if self.handle:
+            ebin_heads_plan_release(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def execute_heads(plan: HeadsPlan, q, k, cos, sin, positions, q_out, k_out, wq=None, wk=None,
+                  stream=None) -> None:
+    """Enqueue a rotation (either direction) or a norm with rotation on device
+    buffers laid out as the plan says (torch tensors or int addresses)."""
+    ebin_heads_execute(plan.handle, _ptr(q), _ptr(k), _ptr(cos), _ptr(sin), _ptr(positions),
+                       _ptr(wq), _ptr(wk), _ptr(q_out), _ptr(k_out), _stream(stream))
+
+
+def execute_heads_grad(plan: HeadsPlan, dq, dk, q, k, cos, sin, positions, wq, wk, dq_out, dk_out,
+                       dwq, dwk, workspace, stream=None) -> None:
+    """Enqueue the gradient of norm and rotation; ``workspace``: a uint8 device
+    tensor of at least plan.workspace_bytes."""
+    ebin_heads_grad_execute(plan.handle, _ptr(dq), _ptr(dk), _ptr(q), _ptr(k), _ptr(cos),
+                            _ptr(sin), _ptr(positions), _ptr(wq), _ptr(wk), _ptr(dq_out),
+                            _ptr(dk_out), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+                            _bytes_of(workspace), _stream(stream))
+
+
+def _bytes_of(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _same_device(where, first, *others):
+    """ValueError unless every tensor (None is passed over) is on the first one's CUDA device."""
+    if not first.is_cuda:
+        raise ValueError("%s: tensors must be on a CUDA device" % where)
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("%s: tensors are on %s and %s" % (where, first.device, t.device))
+
+
+def _heads_inputs(where, q, k, cos, sin, positions):
+    """The checks of the one-shot calls; returns the plan's keywords for the table and positions."""
+    import torch
+    _same_device(where, q, k, cos, sin, positions)
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("%s: q and k are [batch, tokens, heads, head_dim]" % where)
+    if k is not None and k.dtype != q.dtype:
+        raise ValueError("%s: q is %s and k %s" % (where, q.dtype, k.dtype))
+    kw = {"rotary_dim": 0}
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("%s: cos and sin are two [positions, rotary_dim / 2] tables" % where)
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError("%s: cos and sin are contiguous float32" % where)
+        kw = {"rotary_dim": 2 * cos.shape[1], "table_positions": cos.shape[0]}
+    if positions is not None:
+        if positions.dim() == 1:
+            positions = positions.expand(q.shape[0], -1)
+        if tuple(positions.shape) != tuple(q.shape[:2]) or \
+                positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("%s: positions are int32 or int64 [tokens] or [batch, tokens]" % where)
+        kw.update(positions=positions.dtype, position_strides=positions.stride())
+    return kw, positions
+
+
+def _heads_out(where, x, out):
+    import torch
+    if x is None:
+        return None
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.dtype != x.dtype or out.shape != x.shape or out.device != x.device:
+        raise ValueError("%s: an output is %s %s on %s; the result is %s %s on %s"
+                         % (where, out.dtype, tuple(out.shape), out.device, x.dtype,
+                            tuple(x.shape), x.device))
+    return out
+
+
+def _run_heads(where, q, k, cos, sin, positions, out, wq, wk, stream, **kw):
+    import torch
+    more, positions = _heads_inputs(where, q, k, cos, sin, positions)
+    _same_device(where, q, wq, wk)
+    qo, ko = (None, None) if out is None else out
+    qo, ko = _heads_out(where, q, qo), _heads_out(where, k, ko)
+    plan = HeadsPlan(q.dtype, q.shape, None if k is None else k.shape, q_strides=q.stride(),
+                     k_strides=None if k is None else k.stride(), q_out_strides=qo.stride(),
+                     k_out_strides=None if k is None else ko.stride(), **more, **kw)
+    with torch.cuda.device(q.device):
+        execute_heads(plan, q, k, cos, sin, positions, qo, ko, wq, wk, stream)
+    return qo, ko
+
+
+def rotary(q, k, cos, sin, positions=None, *, layout: str = "half", gradient: bool = False,
+           out=None, stream=None):
+    """Rotary positions of q and k (either may be a strided view; k may be None):
+    returns (q_out, k_out), new tensors or ``out``, which may be (q, k) itself.
+    ``gradient``: q and k are the incoming gradients, rotated back."""
+    return _run_heads("rotary", q, k, cos, sin, positions, out, None, None, stream,
+                      layout=layout, gradient=gradient)
+
+
+def _norm_weights(where, q, wq, wk):
+    """The common type of the norm weights (None where there is none)."""
+    kinds = {w.dtype for w in (wq, wk) if w is not None}
+    for w in (wq, wk):
+        if w is not None and (tuple(w.shape) != (q.shape[-1],) or not w.is_contiguous()):
+            raise ValueError("%s: a norm weight is a contiguous [head_dim] tensor" % where)
+    if len(kinds) > 1:
+        raise ValueError("%s: wq and wk have one type" % where)
+    return kinds.pop() if kinds else None
+
+
+def qk_norm_rotary(q, k, wq, wk, cos=None, sin=None, positions=None, *, epsilon: float = 1e-6,
+                   layout: str = "half", out=None, stream=None):
+    """The RMS norm of each head of q and k, times its weight (None = 1), and
+    the rotation (cos None = norm only) in one pass; returns (q_out, k_out)."""
+    wd = _norm_weights("qk_norm_rotary", q, wq, wk)
+    return _run_heads("qk_norm_rotary", q, k, cos, sin, positions, out, wq, wk, stream,
+                      norm="rms", epsilon=epsilon, layout=layout, weight_dtype=wd)
+
+
+def qk_norm_rotary_grad(dq, dk, q, k, wq, wk, cos=None, sin=None, positions=None, *,
+                        epsilon: float = 1e-6, layout: str = "half", out=None, stream=None):
+    """The gradient of qk_norm_rotary: (dq, dk, dwq, dwk) for the incoming
+    gradients dq, dk and the forward inputs q, k; dwq and dwk are float32
+    (dk and dwk None without k)."""
+    import torch
+    where = "qk_norm_rotary_grad"
+    wd = _norm_weights(where, q, wq, wk)
+    more, positions = _heads_inputs(where, q, k, cos, sin, positions)
+    _same_device(where, q, dq, dk, wq, wk)
+    for g, x in ((dq, q), (dk, k)):
+        if (g is None) != (x is None) or (g is not None and
+                                          (g.shape != x.shape or g.dtype != x.dtype)):
+            raise ValueError("%s: a gradient has its input's shape and type" % where)
+    qo, ko = (None, None) if out is None else out
+    qo, ko = _heads_out(where, q, qo), _heads_out(where, k, ko)
+    st = (lambda t: None if t is None else t.stride())
+    plan = HeadsPlan(q.dtype, q.shape, None if k is None else k.shape, norm="rms",
+                     epsilon=epsilon, layout=layout, weight_dtype=wd, gradient=True,
+                     q_strides=st(q), k_strides=st(k), dq_strides=st(dq), dk_strides=st(dk),
+                     q_out_strides=st(qo), k_out_strides=st(ko), **more)
+    dwq = torch.empty(q.shape[-1], device=q.device)
+    dwk = None if k is None else torch.empty(q.shape[-1], device=q.device)
+    work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+    with torch.cuda.device(q.device):
+        execute_heads_grad(plan, dq, dk, q, k, cos, sin, positions, wq, wk, qo, ko, dwq, dwk,
+                           work, stream)
+    return qo, ko, dwq, dwk

@@ -22,11 +22,15 @@ LIB = os.path.join(PKG, "libebin.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 GROUPS = ["arith", "mod", "pow", "cmp", "logic", "chan", "ext", "tern", "powmix"]
+LAYER = ["heads"]        # one translation unit each: ebin_<name>.cu
 N_DT = 13
 # -fmad=false: no multiply-add contraction anywhere; the kernels also use the
 # _rn intrinsics explicitly.  No fast-math.
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC",
               "-I" + INCLUDE, "-I" + CSRC]
+# The layer operators are held to error bounds, not to bit-exact steps, and may
+# contract a product and a sum.
+LAYER_FLAGS = [f for f in NVCC_FLAGS if f != "-fmad=false"]
 
 
 def _elf_matches_host(path: str) -> bool:
@@ -78,6 +82,10 @@ def _jobs():
     noalloc_obj = os.path.join(OBJDIR, "ebin_noalloc.o")
     jobs.append((noalloc_obj, [noalloc_src] + heads,
                  [nvcc, *ARCH, *NVCC_FLAGS, "-c", noalloc_src, "-o", noalloc_obj]))
+    for g in LAYER:
+        src = os.path.join(CSRC, "ebin_%s.cu" % g)
+        obj = os.path.join(OBJDIR, "ebin_%s.o" % g)
+        jobs.append((obj, [src] + heads, [nvcc, *ARCH, *LAYER_FLAGS, "-c", src, "-o", obj]))
     for g in GROUPS:
         src = os.path.join(CSRC, "k_%s.cu" % g)
         for dt in range(N_DT):

@@ -27,6 +27,7 @@
 
 #include "ebin.h"
 #include "ebin_launch.h"
+#include "ebin_layer.h"
 #include "ebin_plan.h"
 
 using ebin::Fam;
@@ -887,6 +888,16 @@ bool overlaps(const void *p, int64_t pb, const void *q, int64_t qb) {
 }
 
 }  // namespace
+
+uint32_t *ebin::stream_status_word(cudaStream_t s) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? status_word(dev, s, true) : nullptr;
+}
+
+int ebin::current_sm_count() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? sm_count(dev) : 1;
+}
 
 cudaError_t ebin::launch(const Launch &L) {
 #define EBIN_PICK(g)                                                                      \

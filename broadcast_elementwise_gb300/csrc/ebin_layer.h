@@ -1,0 +1,81 @@
+// Shared by the translation units of the layer operators (heads, matrix
+// products, epilogue gradients).  Not part of the public C ABI.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "ebin.h"
+#include "ebin_plan.h"
+
+namespace ebin {
+
+// The current stream's status word and device facts (ebin_host.cpp).
+uint32_t *stream_status_word(cudaStream_t s);
+int current_sm_count();
+
+inline bool ranges_overlap(const void *p, int64_t pb, const void *q, int64_t qb) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return pb > 0 && qb > 0 && a < b + (uintptr_t)qb && b < a + (uintptr_t)pb;
+}
+
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// a * b < EBIN_MAX_ELEMENTS for a, b >= 0, without overflow.
+inline bool product_fits(int64_t a, int64_t b, int64_t *out) {
+    if (a != 0 && b > (EBIN_MAX_ELEMENTS - 1) / a) return false;
+    *out = a * b;
+    return true;
+}
+
+// Launch with programmatic dependent launch (the kernel calls
+// griddepcontrol.wait before its first global access) and count it.
+template <class... KParams, class... Args>
+cudaError_t launch_layer(void (*kernel)(KParams...), dim3 grid, int block, size_t smem,
+                         cudaStream_t stream, int cluster, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    cfg.attrs = attr;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void layer_pdl_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void layer_pdl_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+#endif
+
+}  // namespace ebin

@@ -152,6 +152,8 @@ typedef enum ebin_family {
 /* Device status bits ("Compute, scheduling, and safety": validation before the math). */
 #define EBIN_DEVICE_DIV_BY_ZERO 0x1u  /* integer Div/Mod by 0, or integer 0 to a negative power */
 #define EBIN_DEVICE_SHIFT_RANGE 0x2u  /* BitShift count >= the element width in bits */
+#define EBIN_DEVICE_POSITION_RANGE 0x4u /* a token's position outside the rotation table */
+#define EBIN_DEVICE_WAIT_LIMIT 0x8u   /* a wait inside a matrix product ran out; its output is invalid */
 
 /*
  * Operator attributes.  Pass NULL to ebin_descriptor_create for the defaults
@@ -530,6 +532,287 @@ ebin_status ebin_execute_noalloc(ebin_plan_t plan, const void *A, const void *B,
  * CUDA.
  */
 ebin_status ebin_noalloc_read_status(int status_slot, void *stream, uint32_t *bits);
+
+/* ------------------------------------------------------------------ heads
+ *
+ * Operators on the heads of q and k before attention: rotary positions
+ * (RotaryEmbedding) and, in the same pass, the RMS norm of each head.  No
+ * counterpart in the pages.
+ *
+ * q is [batch, tokens, q_heads, head_dim] and k [batch, tokens, k_heads,
+ * head_dim], each a view with its own element strides, its last dimension
+ * dense: [batch, heads, tokens, head_dim] storage, or q and k inside one
+ * projection's output, are views.  One launch handles both; k_heads = 0
+ * leaves k out.
+ *
+ * Rotation, of the first rotary_dim = r elements of a head at position p, with
+ * the pair j = 0 .. r/2 - 1 being (a, b) = (x[j], x[j + r/2]) in the HALF
+ * layout and (x[2j], x[2j + 1]) in the INTERLEAVED one:
+ *     y_a = a cos[p, j] - b sin[p, j],   y_b = b cos[p, j] + a sin[p, j]
+ * Elements from r on pass through.  cos and sin are the caller's binary32
+ * tables [table_positions, r/2] (ebin_rotary_table fills a pair).
+ *
+ * Norm, before the rotation: x <- x * rstd * w,
+ * rstd = 1 / sqrt(mean over the head of x^2 + epsilon).
+ *
+ * Arithmetic is binary32, with one rounding to the element type at the end.
+ */
+typedef enum ebin_norm { EBIN_NORM_NONE = 0, EBIN_NORM_RMS = 1 } ebin_norm;
+typedef enum ebin_rotary_layout {
+    EBIN_ROTARY_HALF = 0,
+    EBIN_ROTARY_INTERLEAVED = 1
+} ebin_rotary_layout;
+
+/* How a table's frequencies are stretched for contexts longer than the trained one. */
+typedef enum ebin_rotary_scaling {
+    EBIN_ROTARY_SCALE_NONE = 0,
+    EBIN_ROTARY_SCALE_LINEAR = 1,   /* every frequency divided by factor */
+    EBIN_ROTARY_SCALE_BASE = 2,     /* base * factor^(r / (r - 2)) in place of base */
+    EBIN_ROTARY_SCALE_BY_PARTS = 3  /* by the turns within the trained length (below) */
+} ebin_rotary_scaling;
+
+/*
+ *   rotary_dim   r, even, 2 .. 2^16
+ *   scaling      one of ebin_rotary_scaling
+ *   base         > 0; frequency j is f_j = base^(-2j/r) radians per position
+ *   factor       >= 1 (not read for NONE)
+ *   trained_length, slow_turns, fast_turns   BY_PARTS only: a frequency that makes
+ *                t_j = trained_length f_j / 2 pi turns is kept in part
+ *                g = clamp((t_j - slow_turns) / (fast_turns - slow_turns), 0, 1):
+ *                f_j <- f_j (g + (1 - g) / factor); fast_turns > slow_turns
+ *   amplitude    multiplies both tables (1 = a plain rotation), > 0
+ */
+typedef struct ebin_rotary_attrs {
+    int32_t rotary_dim;
+    int32_t scaling;
+    double base;
+    double factor;
+    double trained_length;
+    double slow_turns;
+    double fast_turns;
+    double amplitude;
+} ebin_rotary_attrs;
+
+/*
+ * Fill cos and sin, each binary32 [positions, rotary_dim / 2] dense on the
+ * current device, for positions first_position .. first_position + positions
+ * - 1 (first_position >= 0, the last below 2^53).  Angles, cosines and sines
+ * are formed in binary64 and rounded once: a binary32 angle at position 10^5
+ * would be off by up to 0.004 radians.  Enqueued on `stream`.
+ * Errors: INVALID_ARG (NULL, a negative count), INVALID_ATTR, CUDA.
+ */
+ebin_status ebin_rotary_table(const ebin_rotary_attrs *attrs, int64_t first_position,
+                              int64_t positions, float *cos, float *sin, void *stream);
+
+/* Element strides of a [batch, tokens, heads, head_dim] view (the last is 1). */
+typedef struct ebin_heads_view {
+    int64_t batch, token, head;
+} ebin_heads_view;
+
+/*
+ *   dtype            of q, k, their gradients and the outputs: FLOAT32, FLOAT16, BFLOAT16
+ *   dtype_w          of the norm weights wq, wk: dtype or FLOAT32 (not read without a norm)
+ *   norm, layout     ebin_norm, ebin_rotary_layout
+ *   gradient         0 = forward; 1 = the gradient: without a norm the transposed rotation of
+ *                    dq and dk by ebin_heads_execute, with a norm ebin_heads_grad_execute
+ *   epsilon          of the norm, >= 0
+ *   batch, tokens, q_heads, k_heads   >= 0
+ *   head_dim         1 .. 1024
+ *   rotary_dim       even, 0 .. head_dim (0: no rotation, the tables are not read)
+ *   position_type    INT32 or INT64: positions are a device array of that type, element
+ *                    strides position_strides (batch, token; 0 allowed); or 0: token t of
+ *                    every sequence is at position t
+ *   table_positions  rows of cos and sin; a token whose position is outside them sets
+ *                    EBIN_DEVICE_POSITION_RANGE, its output rows are written as 0 and it adds
+ *                    nothing to the weight gradients
+ *   q, k             strides of the inputs x; dq, dk: of the incoming gradients (norm gradient
+ *                    only); q_out, k_out: of the outputs, which must not overlap themselves
+ */
+typedef struct ebin_heads_attrs {
+    ebin_dtype dtype;
+    ebin_dtype dtype_w;
+    int32_t norm;
+    int32_t layout;
+    int32_t gradient;
+    float epsilon;
+    int64_t batch, tokens;
+    int32_t q_heads, k_heads, head_dim, rotary_dim;
+    int32_t position_type;
+    int64_t position_strides[2];
+    int64_t table_positions;
+    ebin_heads_view q, k, dq, dk, q_out, k_out;
+} ebin_heads_attrs;
+
+typedef struct ebin_heads_plan_s *ebin_heads_plan_t;
+
+/*
+ * Check the attributes and build a plan (immutable, usable from any thread
+ * and stream; the caller owns it).  Errors: INVALID_ARG (NULL, sizes, strides
+ * that are negative or reach 2^60 elements, an output that overlaps itself),
+ * INVALID_ATTR (norm, layout, rotary_dim, epsilon, position_type),
+ * UNSUPPORTED_TYPE.
+ */
+ebin_status ebin_heads_plan_create(const ebin_heads_attrs *attrs, ebin_heads_plan_t *out);
+
+/* Bytes of device workspace the plan's execution needs (0 but for the norm gradient). */
+ebin_status ebin_heads_plan_workspace(ebin_heads_plan_t plan, size_t *bytes);
+
+/* Free a plan; work already enqueued is not affected.  NULL is ignored. */
+void ebin_heads_plan_release(ebin_heads_plan_t plan);
+
+/*
+ * Run a plan without norm (either direction) or a forward plan with one,
+ * enqueued on `stream`: q, k -> q_out, k_out.  wq and wk [head_dim] are read
+ * with a norm only (NULL = a weight of 1); cos and sin with rotary_dim > 0,
+ * positions with a position_type.  An output may be its own input (the same
+ * pointer and strides); q and k views that interleave in one buffer without
+ * sharing an element are accepted; any other overlap with an output is ALIAS.
+ * With no heads or tokens nothing is read.
+ * The first call on a stream allocates its status word (as ebin_execute's
+ * validating operators do); capture into a graph after that.
+ * Errors: INVALID_ARG (a NULL buffer with work to do, a norm-gradient plan),
+ * ALIAS, CUDA.
+ */
+ebin_status ebin_heads_execute(ebin_heads_plan_t plan, const void *q, const void *k,
+                               const float *cos, const float *sin, const void *positions,
+                               const void *wq, const void *wk, void *q_out, void *k_out,
+                               void *stream);
+
+/*
+ * The gradient of norm and rotation.  With g = the transposed rotation of the
+ * incoming dy and xhat = x rstd (recomputed from x, nothing is kept from the
+ * forward pass):
+ *     dx = rstd (g w - xhat mean(g w xhat)),   dw = sum over tokens and heads of g xhat
+ * dq, dk are the incoming gradients, q, k the forward inputs; dq_out, dk_out
+ * are written as ebin_heads_execute writes its outputs, and may be dq, dk or q,
+ * k themselves.  dwq, dwk [head_dim] binary32 are overwritten (either may be
+ * NULL: not wanted); their sums run in an order fixed by the plan and the
+ * device, so the same inputs give the same bits.  workspace: at least
+ * ebin_heads_plan_workspace bytes, 16-byte aligned, not shared with work in
+ * flight on another stream.  Errors: as ebin_heads_execute.
+ */
+ebin_status ebin_heads_grad_execute(ebin_heads_plan_t plan, const void *dq, const void *dk,
+                                    const void *q, const void *k, const float *cos,
+                                    const float *sin, const void *positions, const void *wq,
+                                    const void *wk, void *dq_out, void *dk_out, float *dwq,
+                                    float *dwk, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* ------------------------------------------------------------------ matrix products
+ *
+ * y = act(z) + residual,  z = op(A) op(B) + bias: a matrix product with its
+ * elementwise tail in the epilogue (the fused Conv -> PReLU epilogue of
+ * 0verkilll/onnx ops, ConvPReluOp, and GemmOp's transposes, as one pass).
+ *
+ * op(A) is [m, k], op(B) [k, n]; a transposed operand is stored [k, m] or
+ * [n, k].  Products of the 16-bit inputs and their sums are binary32 (the
+ * order of the sum is fixed by the plan and the device: the same inputs give
+ * the same bits), the epilogue is binary32, and y is rounded once.
+ *
+ * The gradient is the same operator: with dz from
+ * ebin_epilogue_grad_execute, dA = dz op(B)^T and dB = op(A)^T dz are products
+ * with other transposes.
+ */
+typedef enum ebin_activation {
+    EBIN_ACT_NONE = 0,
+    EBIN_ACT_RELU = 1,      /* max(z, 0); NaN stays NaN; derivative 0 at 0 */
+    EBIN_ACT_GELU = 2,      /* z Phi(z), Phi by erf */
+    EBIN_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    EBIN_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} ebin_activation;
+
+/*
+ *   dtype         of A, B, residual, preact and Y: FLOAT16 or BFLOAT16
+ *   dtype_bias    of the bias [n]: dtype or FLOAT32 (read with has_bias only)
+ *   trans_a/b     0 or 1
+ *   has_bias, has_residual   0 or 1: whether execution reads them
+ *   any_alignment 0: A and B start on 16-byte boundaries (else ebin_gemm_execute gives
+ *                 INVALID_ARG); 1: they may start anywhere
+ *   m, n, k       >= 0; k = 0 gives z = bias
+ *   lda ..        element strides between stored rows (0 = dense); inner strides are 1
+ * The tensor copy engine wants rows that start on 16-byte boundaries: an
+ * operand whose row stride is no multiple of 8 elements, or any with
+ * any_alignment, is first laid out anew in the workspace.
+ */
+typedef struct ebin_gemm_attrs {
+    ebin_dtype dtype;
+    ebin_dtype dtype_bias;
+    int32_t trans_a, trans_b;
+    int32_t activation;
+    int32_t has_bias;
+    int32_t has_residual;
+    int32_t any_alignment;
+    int64_t m, n, k;
+    int64_t lda, ldb, ldy, ld_residual, ld_preact;
+} ebin_gemm_attrs;
+
+typedef struct ebin_gemm_plan_s *ebin_gemm_plan_t;
+
+/*
+ * Check the attributes and build a plan (immutable, usable from any thread
+ * and stream; the caller owns it).  Errors: INVALID_ARG (NULL, sizes, a row
+ * stride below the row or an extent of 2^60 elements; m, n or k above 2^31 - 1),
+ * INVALID_ATTR (flags, activation), UNSUPPORTED_TYPE.
+ */
+ebin_status ebin_gemm_plan_create(const ebin_gemm_attrs *attrs, ebin_gemm_plan_t *out);
+
+/* Bytes of device workspace that execution needs (often 0). */
+ebin_status ebin_gemm_plan_workspace(ebin_gemm_plan_t plan, size_t *bytes);
+
+/* Free a plan; work already enqueued is not affected.  NULL is ignored. */
+void ebin_gemm_plan_release(ebin_gemm_plan_t plan);
+
+/*
+ * Run the product on device buffers, enqueued on `stream`.
+ *   A, B       not read (may be NULL) with k = 0
+ *   bias, residual   NULL unless the plan has them
+ *   Y          may be the residual itself (same pointer and stride)
+ *   preact     NULL, or [m, n] that receives z rounded to dtype: what the gradient reads
+ *   workspace  at least ebin_gemm_plan_workspace bytes, 16-byte aligned; not shared with
+ *              work in flight on another stream
+ * Any other overlap with Y or preact is ALIAS.  With m = 0 or n = 0 nothing
+ * is read or written.  Every wait inside the kernel has a limit; one that
+ * runs out sets EBIN_DEVICE_WAIT_LIMIT in the stream's status word, which the
+ * first call on a stream allocates (capture into a graph after that).
+ * Errors: INVALID_ARG, ALIAS, CUDA.
+ */
+ebin_status ebin_gemm_execute(ebin_gemm_plan_t plan, const void *A, const void *B,
+                              const void *bias, const void *residual, void *Y, void *preact,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The epilogue's gradient: dz = dy act'(z), dbias = the sum over rows of dy
+ * act'(z) (binary32, before the rounding of dz), in one pass over dy and z.
+ *   dtype     of dy, z and dz: FLOAT16, BFLOAT16 or FLOAT32
+ *   has_bias  whether dbias [n] binary32 is wanted
+ *   m, n      >= 0; ld_dy, ld_z, ld_dz: row strides (0 = dense)
+ * With NONE z is not read.
+ */
+typedef struct ebin_epilogue_grad_attrs {
+    ebin_dtype dtype;
+    int32_t activation;
+    int32_t has_bias;
+    int64_t m, n;
+    int64_t ld_dy, ld_z, ld_dz;
+} ebin_epilogue_grad_attrs;
+
+typedef struct ebin_epilogue_grad_plan_s *ebin_epilogue_grad_plan_t;
+
+/* As the ebin_gemm_plan_ functions, with their errors. */
+ebin_status ebin_epilogue_grad_plan_create(const ebin_epilogue_grad_attrs *attrs,
+                                           ebin_epilogue_grad_plan_t *out);
+ebin_status ebin_epilogue_grad_plan_workspace(ebin_epilogue_grad_plan_t plan, size_t *bytes);
+void ebin_epilogue_grad_plan_release(ebin_epilogue_grad_plan_t plan);
+
+/*
+ * Run it, enqueued on `stream`.  dz may be dy or z itself (same pointer and
+ * stride); any other overlap with an output is ALIAS.  With m = 0 dbias is
+ * zeroed.  The order of dbias's sums is fixed by the plan and the device.
+ * Errors: INVALID_ARG, ALIAS, CUDA.
+ */
+ebin_status ebin_epilogue_grad_execute(ebin_epilogue_grad_plan_t plan, const void *dy,
+                                       const void *z, void *dz, float *dbias, void *workspace,
+                                       size_t workspace_bytes, void *stream);
 
 /* Kernels this library has launched in this process (for launch accounting). */
 uint64_t ebin_launch_count(void);
