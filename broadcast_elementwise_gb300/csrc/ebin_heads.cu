@@ -183,10 +183,96 @@ cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode,
     return launch_layer(k_heads_any<T, HEADS_NORM_GRAD>, grid, kHeadsThreads, smem, s, 1, a, il);
 }
 
+// The vector path's layout of a head, or false where it does not apply: rows
+// that are not whole 16-byte vectors on 16-byte boundaries, halves that are
+// not (half layout), and heads of more than 64 vectors.
+bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, HeadsVecArgs &v) {
+    const int64_t V = 16 / p.isz, D = a.dim;
+    const bool il = p.at.layout == EBIN_ROTARY_INTERLEAVED;
+    if (D % V != 0 || (!il && a.half % V != 0)) return false;
+    auto fits = [&](const HeadsTensor &t, int heads) {
+        return (uintptr_t)t.p % 16 == 0 && (p.at.batch <= 1 || t.sb % V == 0) &&
+               (p.at.tokens <= 1 || t.st % V == 0) && (heads <= 1 || t.sh % V == 0);
+    };
+    for (int w = 0; w < 2; ++w) {
+        const int h = heads_of(p.at, w);
+        if (h > 0 && !(fits(a.x[w], h) && fits(a.y[w], h) && (!grad || fits(a.dy[w], h))))
+            return false;
+    }
+    v = HeadsVecArgs{};
+    v.rot_units = (int)(a.half / V);
+    v.units = il ? (int)div_up(D / V, 2)
+                 : v.rot_units + (int)div_up((D - 2 * a.half) / V, 2);
+    if (v.units > 32) return false;
+    while ((1 << v.log_lanes) < v.units) ++v.log_lanes;
+    v.table_vec = a.half % 4 == 0 && ((uintptr_t)a.cos | (uintptr_t)a.sin) % 16 == 0;
+    return true;
+}
+
+template <class T, bool IL, int MODE, int HPT>
+cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, cudaStream_t s) {
+    v.groups[0] = (int)div_up(a.heads[0], HPT);
+    v.groups[1] = (int)div_up(a.heads[1], HPT);
+    const int64_t items = a.rows * (v.groups[0] + v.groups[1]);
+    const int64_t grid = div_up(items << v.log_lanes, kHeadsThreads);
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    v.wide = (grid + 1) * kHeadsThreads >= (1ll << 32);
+    return launch_layer(k_heads_vec<T, IL, MODE, HPT>, dim3((unsigned)grid), kHeadsThreads, 0, s,
+                        1, a, v);
+}
+
+template <class T, bool IL>
+cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, cudaStream_t s) {
+    static const int resident = [] {
+        int b = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, k_heads_vec_grad<T, IL>,
+                                                          kHeadsThreads, 16384) != cudaSuccess ||
+            b < 1) {
+            cudaGetLastError();
+            b = 1;
+        }
+        return b;
+    }();
+    // one wave of CTAs, shared between q and k by their rows
+    const int per = kHeadsThreads >> v.log_lanes;
+    const int64_t all = std::min<int64_t>((int64_t)resident * current_sm_count(),
+                                          kHeadsMaxPartials);
+    const int64_t heads = a.heads[0] + a.heads[1];
+    for (int w = 0; w < 2; ++w) {
+        const int64_t most = div_up(a.rows * a.heads[w], per);
+        const int64_t share = std::max<int64_t>(1, all * a.heads[w] / heads);
+        v.ctas[w] = (int)std::min(most, share);
+        ctas[w] = v.ctas[w];
+    }
+    v.wide = a.rows * std::max(a.heads[0], a.heads[1]) >= (1ll << 31);
+    const size_t smem = sizeof(float) * per * a.dim;
+    return launch_layer(k_heads_vec_grad<T, IL>, dim3((unsigned)(v.ctas[0] + v.ctas[1])),
+                        kHeadsThreads, smem, s, 1, a, v);
+}
+
+template <class T, bool IL>
+cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, int mode, int64_t *ctas,
+                            cudaStream_t s) {
+    if (mode == HEADS_NORM_GRAD) return launch_vec_grad<T, IL>(a, v, ctas, s);
+    // Few rows: one head per item spreads them over the SMs.  Many: four heads
+    // share the token's cosines, sines and weights.
+    const bool few = (a.rows * (a.heads[0] + a.heads[1]) << v.log_lanes) <
+                     2048ll * current_sm_count();
+    if (mode == HEADS_ROTATE)
+        return few ? launch_vec<T, IL, HEADS_ROTATE, 1>(a, v, s)
+                   : launch_vec<T, IL, HEADS_ROTATE, 4>(a, v, s);
+    return few ? launch_vec<T, IL, HEADS_NORM, 1>(a, v, s)
+               : launch_vec<T, IL, HEADS_NORM, 4>(a, v, s);
+}
+
 template <class T>
 cudaError_t launch_heads(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode, int64_t *ctas,
                          cudaStream_t s) {
-    return launch_any<T>(p, a, mode, ctas, s);
+    HeadsVecArgs v;
+    if (!heads_vectors(p, a, mode == HEADS_NORM_GRAD, v))
+        return launch_any<T>(p, a, mode, ctas, s);
+    return p.at.layout == EBIN_ROTARY_INTERLEAVED ? launch_vec_mode<T, true>(a, v, mode, ctas, s)
+                                                  : launch_vec_mode<T, false>(a, v, mode, ctas, s);
 }
 
 cudaError_t launch_typed(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode, int64_t *ctas,

@@ -6,6 +6,8 @@
 // one rounding to the element type at the store.
 #pragma once
 
+#include <type_traits>
+
 #include "ebin_layer.h"
 
 namespace ebin {
@@ -174,6 +176,338 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, 
             for (int w = 0; w < kWarps; ++w) v += s_dw[w * D + j];
             a.partial[which][(int64_t)blockIdx.x * D + j] = v;
         }
+    }
+}
+
+// ------------------------------------------------------------------ 16-byte vectors
+//
+// The path of heads whose rows are whole 16-byte vectors on 16-byte
+// boundaries.  A group of L lanes (a power of two) takes a token; a lane owns
+// one unit of its heads, two vectors whose elements form V = 16 / sizeof(T)
+// pairs (a[i], b[i]):
+//   half layout          vectors at u V and half + u V for u < half / V, then
+//                        two neighbouring vectors of what passes through
+//   interleaved layout   vectors at 2 u V and (2 u + 1) V: pairs of neighbours
+// so a rotation needs no exchange between lanes, and a norm one tree over L.
+// Cosines, sines and weights stay in registers over the heads of one item.
+
+struct HeadsVecArgs {
+    int32_t log_lanes;
+    int32_t units;          // lanes of a group with work
+    int32_t rot_units;      // half layout: units that rotate
+    int32_t table_vec;      // table rows may be read 16 bytes at a time
+    int32_t groups[2];      // items of a token: groups of HPT heads of q, then of k
+    int32_t wide;           // item indices pass 32 bits
+    int32_t ctas[2];        // the gradient's CTAs for q and for k
+};
+
+template <class T, int V> struct HeadsVec {
+    uint4 w;
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float((&w.x)[i]);
+        } else {
+            const uint32_t x = (&w.x)[i / 2];
+            if constexpr (std::is_same<T, __nv_bfloat16>::value)
+                return __uint_as_float(i % 2 ? (x & 0xFFFF0000u) : (x << 16));
+            else
+                return __half2float(__ushort_as_half((unsigned short)(i % 2 ? x >> 16 : x)));
+        }
+    }
+};
+
+template <class T> __device__ __forceinline__ uint32_t heads_pack2(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    } else {
+        const __half2 p = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    }
+}
+
+template <class T> __device__ __forceinline__ uint4 heads_load(const T *p) {
+    uint4 r;
+    // not .nc: an output may be its own input
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+
+template <class T, int V>
+__device__ __forceinline__ void heads_store(T *p, const float *v) {
+    uint4 r;
+    if constexpr (sizeof(T) == 4)
+        r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                       __float_as_uint(v[3]));
+    else
+        r = make_uint4(heads_pack2<T>(v[0], v[1]), heads_pack2<T>(v[2], v[3]),
+                       heads_pack2<T>(v[V - 4], v[V - 3]), heads_pack2<T>(v[V - 2], v[V - 1]));
+    *reinterpret_cast<uint4 *>(p) = r;
+}
+
+// Where a lane's unit lies, and how its pairs read.
+template <class T, bool IL> struct HeadsUnit {
+    static constexpr int V = 16 / sizeof(T);
+    int off0, off1;    // element offsets of the two vectors
+    bool on, second;   // the lane has work; its second vector exists
+    int pairs;         // leading pairs that rotate
+    int pair0;         // the first pair's index in the table row
+
+    __device__ __forceinline__ void place(const HeadsArgs &a, const HeadsVecArgs &v, int lane) {
+        on = lane < v.units;
+        if constexpr (IL) {
+            off0 = 2 * lane * V;
+            off1 = off0 + V;
+            pair0 = lane * V;
+            pairs = min(max(a.half - pair0, 0), V);
+        } else {
+            const bool rot = lane < v.rot_units;
+            off0 = rot ? lane * V : 2 * a.half + 2 * (lane - v.rot_units) * V;
+            off1 = rot ? a.half + off0 : off0 + V;
+            pair0 = lane * V;
+            pairs = rot ? V : 0;
+        }
+        second = on && off1 < a.dim;
+    }
+    __device__ __forceinline__ void load(const T *p, uint4 &x0, uint4 &x1) const {
+        x0 = x1 = make_uint4(0, 0, 0, 0);
+        if (on) x0 = heads_load(p + off0);
+        if (second) x1 = heads_load(p + off1);
+    }
+    __device__ __forceinline__ static void open(const uint4 &x0, const uint4 &x1, float *a,
+                                                float *b) {
+        const HeadsVec<T, V> v0{x0}, v1{x1};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (IL) {
+                a[i] = i < V / 2 ? v0.at(2 * i) : v1.at(2 * i - V);
+                b[i] = i < V / 2 ? v0.at(2 * i + 1) : v1.at(2 * i + 1 - V);
+            } else {
+                a[i] = v0.at(i);
+                b[i] = v1.at(i);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *p, const float *a, const float *b) const {
+        float v0[V], v1[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (IL) {
+                v0[i] = i % 2 ? b[i / 2] : a[i / 2];
+                v1[i] = i % 2 ? b[(i + V) / 2] : a[(i + V) / 2];
+            } else {
+                v0[i] = a[i];
+                v1[i] = b[i];
+            }
+        }
+        if (on) heads_store<T, V>(p + off0, v0);
+        if (second) heads_store<T, V>(p + off1, v1);
+    }
+    __device__ __forceinline__ void angles(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
+                                           float *c, float *s) const {
+        const float *cr = a.cos + p * a.half + pair0, *sr = a.sin + p * a.half + pair0;
+        if (on && pairs == V && v.table_vec) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(cr + i));
+                const float4 y = __ldg(reinterpret_cast<const float4 *>(sr + i));
+                c[i] = x.x; c[i + 1] = x.y; c[i + 2] = x.z; c[i + 3] = x.w;
+                s[i] = y.x; s[i + 1] = y.y; s[i + 2] = y.z; s[i + 3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const bool r = on && i < pairs;
+                c[i] = r ? __ldg(cr + i) : 1.0f;
+                s[i] = r ? __ldg(sr + i) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] *= a.sign;
+    }
+    __device__ __forceinline__ void weights(const HeadsArgs &a, int which, float *wa,
+                                            float *wb) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j0 = IL ? off0 + 2 * i : off0 + i, j1 = IL ? j0 + 1 : off1 + i;
+            wa[i] = on && j0 < a.dim ? heads_weight<T>(a, which, j0) : 0.0f;
+            wb[i] = on && j1 < a.dim ? heads_weight<T>(a, which, j1) : 0.0f;
+        }
+    }
+    // a pair that does not rotate is left alone: an infinity times a zero sine is no number
+    __device__ __forceinline__ void turn(float *a, float *b, const float *c,
+                                         const float *s) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float x = a[i] * c[i] - b[i] * s[i], y = b[i] * c[i] + a[i] * s[i];
+            const bool r = i < pairs;
+            a[i] = r ? x : a[i];
+            b[i] = r ? y : b[i];
+        }
+    }
+};
+
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// Quotient and remainder of an item index by a count (32-bit when it fits).
+__device__ __forceinline__ void heads_split(int64_t i, int64_t n, int wide, int64_t &q,
+                                            int64_t &r) {
+    if (wide) {
+        q = i / n;
+        r = i - q * n;
+    } else {
+        const uint32_t qi = (uint32_t)i / (uint32_t)n;
+        q = qi;
+        r = (uint32_t)i - qi * (uint32_t)n;
+    }
+}
+
+// Rotation, and norm with rotation.  An item is a token and HPT heads of q or
+// of k; all its loads are issued before the first is used.
+template <class T, bool IL, int MODE, int HPT>
+__global__ void __launch_bounds__(kHeadsThreads)
+k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
+    constexpr int V = 16 / sizeof(T);
+    const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
+    layer_pdl_launch();
+    const int64_t item = ((int64_t)blockIdx.x * kHeadsThreads + threadIdx.x) >> v.log_lanes;
+    int64_t bs, g, b, s;
+    heads_split(item, v.groups[0] + v.groups[1], v.wide, bs, g);
+    const bool live = bs < a.rows;
+    if (!live) bs = 0;            // the group still takes part in the warp's exchanges
+    heads_split(bs, a.tokens, v.wide, b, s);
+    const int which = g >= v.groups[0];
+    const int h0 = (int)(which ? g - v.groups[0] : g) * HPT;
+    const int count = live ? min(HPT, a.heads[which] - h0) : 0;
+    HeadsUnit<T, IL> u;
+    u.place(a, v, lane);
+    const HeadsTensor tx = which ? a.x[1] : a.x[0], ty = which ? a.y[1] : a.y[0];
+    const T *x = static_cast<const T *>(tx.p) + heads_offset(tx, b, s, h0);
+    T *y = static_cast<T *>(const_cast<void *>(ty.p)) + heads_offset(ty, b, s, h0);
+    layer_pdl_wait();
+    uint4 x0[HPT], x1[HPT];
+#pragma unroll
+    for (int h = 0; h < HPT; ++h)
+        if (h < count) u.load(x + h * tx.sh, x0[h], x1[h]);
+        else x0[h] = x1[h] = make_uint4(0, 0, 0, 0);
+    const int64_t p = heads_position(a, b, s);
+    float c[V], sn[V], wa[V], wb[V];
+    u.angles(a, v, p < 0 ? 0 : p, c, sn);
+    if constexpr (MODE == HEADS_NORM) u.weights(a, which, wa, wb);
+    if (p < 0 && live && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+#pragma unroll
+    for (int h = 0; h < HPT; ++h) {
+        float va[V], vb[V];
+        u.open(x0[h], x1[h], va, vb);
+        if constexpr (MODE == HEADS_NORM) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
+            const float rstd = rsqrtf(group_sum(ss, lanes) / (float)a.dim + a.eps);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                va[i] *= rstd * wa[i];
+                vb[i] *= rstd * wb[i];
+            }
+        }
+        u.turn(va, vb, c, sn);
+        if (p < 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) va[i] = vb[i] = 0.0f;
+        }
+        if (h < count) u.store(y + h * ty.sh, va, vb);
+    }
+}
+
+// The gradient of norm and rotation.  CTAs take items of q or of k only, in
+// steps of their number, so a thread's weight-gradient sums stay in registers
+// to the end; the CTA's sums then join in shared memory and go to its row of
+// the workspace.
+template <class T, bool IL>
+__global__ void __launch_bounds__(kHeadsThreads)
+k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ float s_dw[];   // [groups of the CTA][dim]
+    const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
+    const int which = (int)blockIdx.x >= v.ctas[0];
+    const int cta = (int)blockIdx.x - (which ? v.ctas[0] : 0);
+    const int heads = a.heads[which];
+    const HeadsTensor tx = which ? a.x[1] : a.x[0], tg = which ? a.dy[1] : a.dy[0],
+                      ty = which ? a.y[1] : a.y[0];
+    const int64_t total = a.rows * heads;
+    const int per = kHeadsThreads >> v.log_lanes, group = threadIdx.x >> v.log_lanes;
+    HeadsUnit<T, IL> u;
+    u.place(a, v, lane);
+    layer_pdl_launch();
+    layer_pdl_wait();
+    float wa[V], wb[V], da[V], db[V];
+    u.weights(a, which, wa, wb);
+#pragma unroll
+    for (int i = 0; i < V; ++i) da[i] = db[i] = 0.0f;
+    bool bad = false;
+    // every lane of a warp makes the same number of steps: the exchanges are warp-wide
+    const int64_t step = (int64_t)v.ctas[which] * per;
+    for (int64_t base = (int64_t)cta * per; base < total; base += step) {
+        const int64_t row = base + group;
+        const bool live = row < total;
+        int64_t bs, h, b, s;
+        heads_split(live ? row : 0, heads, v.wide, bs, h);
+        heads_split(bs, a.tokens, v.wide, b, s);
+        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, g0 = x0, g1 = x0;
+        if (live) {
+            u.load(static_cast<const T *>(tx.p) + heads_offset(tx, b, s, h), x0, x1);
+            u.load(static_cast<const T *>(tg.p) + heads_offset(tg, b, s, h), g0, g1);
+        }
+        const int64_t p = heads_position(a, b, s);
+        float c[V], sn[V], xa[V], xb[V], ga[V], gb[V];
+        u.angles(a, v, p < 0 ? 0 : p, c, sn);
+        u.open(x0, x1, xa, xb);
+        u.open(g0, g1, ga, gb);
+        u.turn(ga, gb, c, sn);
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+            dot = fmaf(ga[i] * wa[i], xa[i], fmaf(gb[i] * wb[i], xb[i], dot));
+        }
+        ss = group_sum(ss, lanes);
+        dot = group_sum(dot, lanes);
+        const float rstd = rsqrtf(ss / (float)a.dim + a.eps);
+        const float mean = dot * rstd / (float)a.dim;
+        const bool use = live && p >= 0;
+        bad |= live && p < 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            xa[i] *= rstd;
+            xb[i] *= rstd;
+            if (use) {
+                da[i] = fmaf(ga[i], xa[i], da[i]);
+                db[i] = fmaf(gb[i], xb[i], db[i]);
+            }
+            ga[i] = use ? rstd * (ga[i] * wa[i] - xa[i] * mean) : 0.0f;
+            gb[i] = use ? rstd * (gb[i] * wb[i] - xb[i] * mean) : 0.0f;
+        }
+        if (live)
+            u.store(static_cast<T *>(const_cast<void *>(ty.p)) + heads_offset(ty, b, s, h), ga,
+                    gb);
+    }
+    if (bad && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int j0 = IL ? u.off0 + 2 * i : u.off0 + i, j1 = IL ? j0 + 1 : u.off1 + i;
+        if (u.on && j0 < a.dim) s_dw[group * a.dim + j0] = da[i];
+        if (u.on && j1 < a.dim) s_dw[group * a.dim + j1] = db[i];
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.dim; j += kHeadsThreads) {
+        float t = 0.0f;
+        for (int r = 0; r < per; ++r) t += s_dw[r * a.dim + j];
+        a.partial[which][(int64_t)cta * a.dim + j] = t;
     }
 }
 
