@@ -98,6 +98,22 @@ class ebin_heads_attrs(ctypes.Structure):
                 ("k_out", ebin_heads_view)]
 
 
+class ebin_gemm_attrs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("dtype_bias", ctypes.c_int), ("trans_a", ctypes.c_int32),
+                ("trans_b", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("has_bias", ctypes.c_int32), ("has_residual", ctypes.c_int32),
+                ("any_alignment", ctypes.c_int32), ("m", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("ld_preact", ctypes.c_int64)]
+
+
+class ebin_epilogue_grad_attrs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("activation", ctypes.c_int32),
+                ("has_bias", ctypes.c_int32), ("m", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("ld_dy", ctypes.c_int64), ("ld_z", ctypes.c_int64), ("ld_dz", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libebin.so is not built (%s); run __graft_entry__.build() or "
@@ -141,6 +157,15 @@ def _load():
         "ebin_heads_plan_release": (None, [vp]),
         "ebin_heads_execute": (i32, [vp] * 11),
         "ebin_heads_grad_execute": (i32, [vp] * 15 + [ctypes.c_size_t, vp]),
+        "ebin_gemm_plan_create": (i32, [ctypes.POINTER(ebin_gemm_attrs), ctypes.POINTER(vp)]),
+        "ebin_gemm_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
+        "ebin_gemm_plan_release": (None, [vp]),
+        "ebin_gemm_execute": (i32, [vp] * 8 + [ctypes.c_size_t, vp]),
+        "ebin_epilogue_grad_plan_create": (i32, [ctypes.POINTER(ebin_epilogue_grad_attrs),
+                                                 ctypes.POINTER(vp)]),
+        "ebin_epilogue_grad_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
+        "ebin_epilogue_grad_plan_release": (None, [vp]),
+        "ebin_epilogue_grad_execute": (i32, [vp] * 6 + [ctypes.c_size_t, vp]),
         "ebin_launch_count": (ctypes.c_uint64, []),
         "ebin_dtype_size": (ctypes.c_size_t, [i32]),
         "ebin_status_string": (ctypes.c_char_p, [i32]),
@@ -168,17 +193,23 @@ def _shape(shape):
 
 def _ptr(x) -> int | None:
     """Device address of a tensor (or an int address, or None)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
+_current = None     # (the current device's index, its current stream's address), from torch
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current
+        if _current is None:
+            import torch
+            torch.cuda.current_stream()      # initialises CUDA, or says why it cannot
+            _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        # the address of torch.cuda.current_stream() without its Stream object (3.0 -> 0.2 us)
+        return _current[1](_current[0]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -378,6 +409,55 @@ def ebin_heads_grad_execute(plan, dq, dk, q, k, cos, sin, positions, wq, wk, dq_
                                      dk_out, dwq, dwk, workspace, workspace_bytes, stream)
     if st:
         raise EbinError(st, "ebin_heads_grad_execute")
+
+
+def ebin_gemm_plan_create(attrs) -> int:
+    out = ctypes.c_void_p()
+    _check(lib.ebin_gemm_plan_create(ctypes.byref(attrs), ctypes.byref(out)),
+           "ebin_gemm_plan_create")
+    return out.value
+
+
+def ebin_gemm_plan_workspace(plan) -> int:
+    v = ctypes.c_size_t()
+    _check(lib.ebin_gemm_plan_workspace(plan, ctypes.byref(v)), "ebin_gemm_plan_workspace")
+    return v.value
+
+
+def ebin_gemm_plan_release(plan) -> None:
+    lib.ebin_gemm_plan_release(plan)
+
+
+def ebin_gemm_execute(plan, A, B, bias, residual, Y, preact, workspace, workspace_bytes,
+                      stream) -> None:
+    st = lib.ebin_gemm_execute(plan, A, B, bias, residual, Y, preact, workspace, workspace_bytes,
+                               stream)
+    if st:
+        raise EbinError(st, "ebin_gemm_execute")
+
+
+def ebin_epilogue_grad_plan_create(attrs) -> int:
+    out = ctypes.c_void_p()
+    _check(lib.ebin_epilogue_grad_plan_create(ctypes.byref(attrs), ctypes.byref(out)),
+           "ebin_epilogue_grad_plan_create")
+    return out.value
+
+
+def ebin_epilogue_grad_plan_workspace(plan) -> int:
+    v = ctypes.c_size_t()
+    _check(lib.ebin_epilogue_grad_plan_workspace(plan, ctypes.byref(v)),
+           "ebin_epilogue_grad_plan_workspace")
+    return v.value
+
+
+def ebin_epilogue_grad_plan_release(plan) -> None:
+    lib.ebin_epilogue_grad_plan_release(plan)
+
+
+def ebin_epilogue_grad_execute(plan, dy, z, dz, dbias, workspace, workspace_bytes, stream) -> None:
+    st = lib.ebin_epilogue_grad_execute(plan, dy, z, dz, dbias, workspace, workspace_bytes, stream)
+    if st:
+        raise EbinError(st, "ebin_epilogue_grad_execute")
 
 
 def ebin_launch_count() -> int:
@@ -710,8 +790,11 @@ def execute_heads(plan: HeadsPlan, q, k, cos, sin, positions, q_out, k_out, wq=N
                   stream=None) -> None:
     """Enqueue a rotation (either direction) or a norm with rotation on device
     buffers laid out as the plan says (torch tensors or int addresses)."""
-    ebin_heads_execute(plan.handle, _ptr(q), _ptr(k), _ptr(cos), _ptr(sin), _ptr(positions),
-                       _ptr(wq), _ptr(wk), _ptr(q_out), _ptr(k_out), _stream(stream))
+    st = lib.ebin_heads_execute(plan.handle, _ptr(q), _ptr(k), _ptr(cos), _ptr(sin),
+                                _ptr(positions), _ptr(wq), _ptr(wk), _ptr(q_out), _ptr(k_out),
+                                _stream(stream))
+    if st:
+        raise EbinError(st, "ebin_heads_execute")
 
 
 def execute_heads_grad(plan: HeadsPlan, dq, dk, q, k, cos, sin, positions, wq, wk, dq_out, dk_out,
@@ -847,3 +930,152 @@ def qk_norm_rotary_grad(dq, dk, q, k, wq, wk, cos=None, sin=None, positions=None
         execute_heads_grad(plan, dq, dk, q, k, cos, sin, positions, wq, wk, qo, ko, dwq, dwk,
                            work, stream)
     return qo, ko, dwq, dwk
+
+
+# ----------------------------------------------------------------- matrix products
+
+class GemmPlan:
+    """A plan of y = act(op(A) op(B) + bias) + residual: op(A) [m, k], op(B)
+    [k, n]; a transposed operand is stored [k, m] or [n, k].  ``bias``: None, or
+    the bias's type (the operands' or float32); strides between stored rows in
+    elements (None = dense); any_alignment: A and B may start off 16 bytes."""
+
+    def __init__(self, dtype, m: int, n: int, k: int, *, trans_a: bool = False,
+                 trans_b: bool = False, bias=None, activation: str = "none",
+                 residual: bool = False, any_alignment: bool = False, lda=None, ldb=None,
+                 ldy=None, ld_residual=None, ld_preact=None):
+        code = _dtype_code(dtype)
+        a = ebin_gemm_attrs(code, code if bias is None else _dtype_code(bias), int(bool(trans_a)),
+                            int(bool(trans_b)), ACTIVATIONS[activation], int(bias is not None),
+                            int(bool(residual)), int(bool(any_alignment)), int(m), int(n), int(k),
+                            *(0 if v is None else int(v)
+                              for v in (lda, ldb, ldy, ld_residual, ld_preact)))
+        self.handle = ebin_gemm_plan_create(a)
+        self.workspace_bytes = ebin_gemm_plan_workspace(self.handle)
+
+    def close(self):
+        if self.handle:
+            ebin_gemm_plan_release(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def execute_gemm(plan: GemmPlan, A, B, y, *, bias=None, residual=None, preact=None,
+                 workspace=None, stream=None) -> None:
+    """Enqueue a product on device buffers laid out as the plan says (torch
+    tensors or int addresses); ``workspace``: a uint8 device tensor of at least
+    plan.workspace_bytes (None where that is 0)."""
+    st = lib.ebin_gemm_execute(plan.handle, _ptr(A), _ptr(B), _ptr(bias), _ptr(residual), _ptr(y),
+                               _ptr(preact), _ptr(workspace), _bytes_of(workspace),
+                               _stream(stream))
+    if st:
+        raise EbinError(st, "ebin_gemm_execute")
+
+
+class EpilogueGradPlan:
+    """A plan of dz = dy act'(z) and, with bias=True, dbias = its sum over rows."""
+
+    def __init__(self, dtype, m: int, n: int, *, activation: str = "none", bias: bool = False,
+                 ld_dy=None, ld_z=None, ld_dz=None):
+        a = ebin_epilogue_grad_attrs(_dtype_code(dtype), ACTIVATIONS[activation], int(bool(bias)),
+                                     int(m), int(n),
+                                     *(0 if v is None else int(v) for v in (ld_dy, ld_z, ld_dz)))
+        self.handle = ebin_epilogue_grad_plan_create(a)
+        self.workspace_bytes = ebin_epilogue_grad_plan_workspace(self.handle)
+
+    def close(self):
+        if self.handle:
+            ebin_epilogue_grad_plan_release(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def execute_epilogue_grad(plan: EpilogueGradPlan, dy, z, dz, dbias=None, workspace=None,
+                          stream=None) -> None:
+    """Enqueue an epilogue's gradient on device buffers laid out as the plan says."""
+    st = lib.ebin_epilogue_grad_execute(plan.handle, _ptr(dy), _ptr(z), _ptr(dz), _ptr(dbias),
+                                        _ptr(workspace), _bytes_of(workspace), _stream(stream))
+    if st:
+        raise EbinError(st, "ebin_epilogue_grad_execute")
+
+
+def _matrix(where, t, shape, dtype, device):
+    """Row stride of a [rows, columns] tensor whose rows are dense; ValueError otherwise."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError("%s: a matrix is %s, wanted %s" % (where, tuple(t.shape), shape))
+    if t.dtype != dtype or t.device != device:
+        raise ValueError("%s: a matrix is %s on %s, wanted %s on %s"
+                         % (where, t.dtype, t.device, dtype, device))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: a matrix's rows are dense (strides %s)" % (where, t.stride()))
+    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+
+
+def gemm(a, b, bias=None, residual=None, *, trans_a: bool = False, trans_b: bool = False,
+         activation: str = "none", out=None, preact=None, stream=None):
+    """y = act(op(a) op(b) + bias) + residual on 16-bit CUDA tensors, in one
+    call; a and b are matrices whose rows are dense (a row stride is fine),
+    transposed where trans_a / trans_b say so.  ``out`` may be ``residual``.
+    ``preact``: a tensor that receives the pre-activation, which the gradient
+    reads (gemm_epilogue_grad)."""
+    import torch
+    where = "gemm"
+    _same_device(where, a, b, bias, residual, out, preact)
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("gemm: a and b are matrices")
+    m, k = (a.shape[1], a.shape[0]) if trans_a else a.shape
+    kb, n = (b.shape[1], b.shape[0]) if trans_b else b.shape
+    if kb != k:
+        raise ValueError("gemm: op(a) is [%d, %d] and op(b) [%d, %d]" % (m, k, kb, n))
+    lda = _matrix(where, a, None, a.dtype, a.device)
+    ldb = _matrix(where, b, None, a.dtype, a.device)
+    if out is None:
+        out = torch.empty(m, n, dtype=a.dtype, device=a.device)
+    ld = [None if t is None else _matrix(where, t, (m, n), a.dtype, a.device)
+          for t in (out, residual, preact)]
+    if bias is not None and (tuple(bias.shape) != (n,) or not bias.is_contiguous()):
+        raise ValueError("gemm: the bias is a contiguous [%d] tensor" % n)
+    plan = GemmPlan(a.dtype, m, n, k, trans_a=trans_a, trans_b=trans_b,
+                    bias=None if bias is None else bias.dtype, activation=activation,
+                    residual=residual is not None, lda=lda, ldb=ldb, ldy=ld[0],
+                    ld_residual=ld[1], ld_preact=ld[2],
+                    any_alignment=a.data_ptr() % 16 != 0 or b.data_ptr() % 16 != 0)
+    with torch.cuda.device(a.device):
+        work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=a.device)
+        execute_gemm(plan, a, b, out, bias=bias, residual=residual, preact=preact,
+                     workspace=work, stream=stream)
+    return out
+
+
+def gemm_epilogue_grad(dy, z=None, *, activation: str = "none", bias: bool = True, out=None,
+                       stream=None):
+    """(dz, dbias) of a product's epilogue for the incoming gradient dy and the
+    pre-activation z ([m, n] matrices; z is not read without an activation);
+    dbias is float32 (None with bias=False).  ``out`` may be dy or z."""
+    import torch
+    where = "gemm_epilogue_grad"
+    _same_device(where, dy, z, out)
+    if activation != "none" and z is None:
+        raise ValueError("gemm_epilogue_grad: %s needs z" % activation)
+    if out is None:
+        out = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    shape = tuple(dy.shape)
+    ld = [None if t is None else _matrix(where, t, shape, dy.dtype, dy.device)
+          for t in (dy, z, out)]
+    plan = EpilogueGradPlan(dy.dtype, shape[0], shape[1], activation=activation, bias=bias,
+                            ld_dy=ld[0], ld_z=ld[1], ld_dz=ld[2])
+    with torch.cuda.device(dy.device):
+        dbias = torch.empty(shape[1], device=dy.device) if bias else None
+        work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dy.device)
+        execute_epilogue_grad(plan, dy, z, out, dbias, work, stream)
+    return out, dbias

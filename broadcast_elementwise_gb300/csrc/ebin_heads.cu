@@ -8,27 +8,6 @@
 
 namespace ebin {
 
-__global__ void __launch_bounds__(1024) k_heads_dw(const HeadsDwArgs a) {
-    __shared__ float s[32][33];
-    const int which = blockIdx.y, j = blockIdx.x * 32 + threadIdx.x;
-    layer_pdl_launch();
-    layer_pdl_wait();
-    float v = 0.0f;
-    if (j < a.dim && a.dw[which]) {
-        const float *p = a.partial[which] + j;
-#pragma unroll 8
-        for (int64_t c = threadIdx.y; c < a.count[which]; c += 32) v += p[c * a.dim];
-    }
-    s[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    if (threadIdx.y == 0 && j < a.dim && a.dw[which]) {
-        float t = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 32; ++r) t += s[r][threadIdx.x];
-        a.dw[which][j] = t;
-    }
-}
-
 struct TableArgs {
     int64_t first, positions;
     int32_t half, scaling;
@@ -205,6 +184,7 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
                  : v.rot_units + (int)div_up((D - 2 * a.half) / V, 2);
     if (v.units > 32) return false;
     while ((1 << v.log_lanes) < v.units) ++v.log_lanes;
+    v.weight_vec = ((uintptr_t)a.w[0] | (uintptr_t)a.w[1]) % 16 == 0;
     v.table_vec = a.half % 4 == 0 && ((uintptr_t)a.cos | (uintptr_t)a.sin) % 16 == 0;
     return true;
 }
@@ -557,22 +537,8 @@ extern "C" ebin_status ebin_heads_grad_execute(ebin_heads_plan_t plan, const voi
     int64_t ctas[2];
     if (launch_typed(p, a, HEADS_NORM_GRAD, ctas, s) != cudaSuccess) return EBIN_ERR_CUDA;
     if (!dwq && !dwk) return EBIN_OK;
-    HeadsDwArgs f{};
-    for (int w = 0; w < 2; ++w) {
-        f.partial[w] = a.partial[w];
-        f.count[w] = heads_of(p.at, w) > 0 ? ctas[w] : 0;
-        f.dw[w] = dw[w];
-    }
-    f.dim = p.at.head_dim;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)div_up(f.dim, 32), 2);
-    cfg.blockDim = dim3(32, 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    count_launch();
-    return cudaLaunchKernelEx(&cfg, k_heads_dw, f) == cudaSuccess ? EBIN_OK : EBIN_ERR_CUDA;
+    const float *partial[2] = {a.partial[0], a.partial[1]};
+    const int64_t count[2] = {heads_of(p.at, 0) > 0 ? ctas[0] : 0,
+                              heads_of(p.at, 1) > 0 ? ctas[1] : 0};
+    return launch_sum_rows(partial, count, dw, p.at.head_dim, 2, s) == cudaSuccess ? EBIN_OK : EBIN_ERR_CUDA;
 }

@@ -196,32 +196,26 @@ struct HeadsVecArgs {
     int32_t units;          // lanes of a group with work
     int32_t rot_units;      // half layout: units that rotate
     int32_t table_vec;      // table rows may be read 16 bytes at a time
+    int32_t weight_vec;     // and the weights
     int32_t groups[2];      // items of a token: groups of HPT heads of q, then of k
     int32_t wide;           // item indices pass 32 bits
     int32_t ctas[2];        // the gradient's CTAs for q and for k
 };
 
-template <class T, int V> struct HeadsVec {
-    uint4 w;
-    __device__ __forceinline__ float at(int i) const {
-        if constexpr (sizeof(T) == 4) {
-            return __uint_as_float((&w.x)[i]);
-        } else {
-            const uint32_t x = (&w.x)[i / 2];
-            if constexpr (std::is_same<T, __nv_bfloat16>::value)
-                return __uint_as_float(i % 2 ? (x & 0xFFFF0000u) : (x << 16));
-            else
-                return __half2float(__ushort_as_half((unsigned short)(i % 2 ? x >> 16 : x)));
-        }
-    }
-};
+// Two elements of a 16-bit word, or two binary32 elements, as a binary32 pair.
+template <class T> __device__ __forceinline__ float2 heads_open2(uint32_t w) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
 
-template <class T> __device__ __forceinline__ uint32_t heads_pack2(float lo, float hi) {
+template <class T> __device__ __forceinline__ uint32_t heads_pack2(float2 v) {
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        const __nv_bfloat162 p = __float22bfloat162_rn(v);
         return *reinterpret_cast<const uint32_t *>(&p);
     } else {
-        const __half2 p = __floats2half2_rn(lo, hi);
+        const __half2 p = __float22half2_rn(v);
         return *reinterpret_cast<const uint32_t *>(&p);
     }
 }
@@ -235,21 +229,13 @@ template <class T> __device__ __forceinline__ uint4 heads_load(const T *p) {
     return r;
 }
 
-template <class T, int V>
-__device__ __forceinline__ void heads_store(T *p, const float *v) {
-    uint4 r;
-    if constexpr (sizeof(T) == 4)
-        r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                       __float_as_uint(v[3]));
-    else
-        r = make_uint4(heads_pack2<T>(v[0], v[1]), heads_pack2<T>(v[2], v[3]),
-                       heads_pack2<T>(v[V - 4], v[V - 3]), heads_pack2<T>(v[V - 2], v[V - 1]));
-    *reinterpret_cast<uint4 *>(p) = r;
-}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
-// Where a lane's unit lies, and how its pairs read.
+// Where a lane's unit lies and how its pairs read: pairs 2i and 2i + 1 are
+// (a[i].x, b[i].x) and (a[i].y, b[i].y), ready for the packed binary32 pipe.
 template <class T, bool IL> struct HeadsUnit {
-    static constexpr int V = 16 / sizeof(T);
+    static constexpr int V = 16 / sizeof(T), N = V / 2;
     int off0, off1;    // element offsets of the two vectors
     bool on, second;   // the lane has work; its second vector exists
     int pairs;         // leading pairs that rotate
@@ -269,6 +255,7 @@ template <class T, bool IL> struct HeadsUnit {
             pair0 = lane * V;
             pairs = rot ? V : 0;
         }
+        if (!on) pairs = 0;
         second = on && off1 < a.dim;
     }
     __device__ __forceinline__ void load(const T *p, uint4 &x0, uint4 &x1) const {
@@ -276,83 +263,140 @@ template <class T, bool IL> struct HeadsUnit {
         if (on) x0 = heads_load(p + off0);
         if (second) x1 = heads_load(p + off1);
     }
-    __device__ __forceinline__ static void open(const uint4 &x0, const uint4 &x1, float *a,
-                                                float *b) {
-        const HeadsVec<T, V> v0{x0}, v1{x1};
+    __device__ __forceinline__ static void open(const uint4 &x0, const uint4 &x1, float2 *a,
+                                                float2 *b) {
+        if constexpr (sizeof(T) == 4) {
+            float2 e[4];
+            e[0] = make_float2(__uint_as_float(x0.x), __uint_as_float(x0.y));
+            e[1] = make_float2(__uint_as_float(x0.z), __uint_as_float(x0.w));
+            e[2] = make_float2(__uint_as_float(x1.x), __uint_as_float(x1.y));
+            e[3] = make_float2(__uint_as_float(x1.z), __uint_as_float(x1.w));
+            split(e, a, b);
+        } else {
+            float2 e[8];
+            e[0] = heads_open2<T>(x0.x);
+            e[1] = heads_open2<T>(x0.y);
+            e[2] = heads_open2<T>(x0.z);
+            e[3] = heads_open2<T>(x0.w);
+            e[4] = heads_open2<T>(x1.x);
+            e[5] = heads_open2<T>(x1.y);
+            e[6] = heads_open2<T>(x1.z);
+            e[7] = heads_open2<T>(x1.w);
+            split(e, a, b);
+        }
+    }
+    // e: the unit's elements two by two, in memory order
+    __device__ __forceinline__ static void split(const float2 *e, float2 *a, float2 *b) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < N; ++i) {
             if constexpr (IL) {
-                a[i] = i < V / 2 ? v0.at(2 * i) : v1.at(2 * i - V);
-                b[i] = i < V / 2 ? v0.at(2 * i + 1) : v1.at(2 * i + 1 - V);
+                a[i] = make_float2(e[2 * i].x, e[2 * i + 1].x);
+                b[i] = make_float2(e[2 * i].y, e[2 * i + 1].y);
             } else {
-                a[i] = v0.at(i);
-                b[i] = v1.at(i);
+                a[i] = e[i];
+                b[i] = e[N + i];
             }
         }
     }
-    __device__ __forceinline__ void store(T *p, const float *a, const float *b) const {
-        float v0[V], v1[V];
+    __device__ __forceinline__ void store(T *p, const float2 *a, const float2 *b) const {
+        float2 e[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < N; ++i) {
             if constexpr (IL) {
-                v0[i] = i % 2 ? b[i / 2] : a[i / 2];
-                v1[i] = i % 2 ? b[(i + V) / 2] : a[(i + V) / 2];
+                e[2 * i] = make_float2(a[i].x, b[i].x);
+                e[2 * i + 1] = make_float2(a[i].y, b[i].y);
             } else {
-                v0[i] = a[i];
-                v1[i] = b[i];
+                e[i] = a[i];
+                e[N + i] = b[i];
             }
         }
-        if (on) heads_store<T, V>(p + off0, v0);
-        if (second) heads_store<T, V>(p + off1, v1);
+        uint4 r0, r1;
+        if constexpr (sizeof(T) == 4) {
+            r0 = make_uint4(__float_as_uint(e[0].x), __float_as_uint(e[0].y),
+                            __float_as_uint(e[1].x), __float_as_uint(e[1].y));
+            r1 = make_uint4(__float_as_uint(e[2].x), __float_as_uint(e[2].y),
+                            __float_as_uint(e[3].x), __float_as_uint(e[3].y));
+        } else {
+            r0 = make_uint4(heads_pack2<T>(e[0]), heads_pack2<T>(e[1]), heads_pack2<T>(e[2]),
+                            heads_pack2<T>(e[3]));
+            r1 = make_uint4(heads_pack2<T>(e[V - 4]), heads_pack2<T>(e[V - 3]),
+                            heads_pack2<T>(e[V - 2]), heads_pack2<T>(e[V - 1]));
+        }
+        if (on) *reinterpret_cast<uint4 *>(p + off0) = r0;
+        if (second) *reinterpret_cast<uint4 *>(p + off1) = r1;
     }
     __device__ __forceinline__ void angles(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
-                                           float *c, float *s) const {
+                                           float2 *c, float2 *s) const {
         const float *cr = a.cos + p * a.half + pair0, *sr = a.sin + p * a.half + pair0;
-        if (on && pairs == V && v.table_vec) {
+        if (pairs == V && v.table_vec) {
 #pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(cr + i));
-                const float4 y = __ldg(reinterpret_cast<const float4 *>(sr + i));
-                c[i] = x.x; c[i + 1] = x.y; c[i + 2] = x.z; c[i + 3] = x.w;
-                s[i] = y.x; s[i + 1] = y.y; s[i + 2] = y.z; s[i + 3] = y.w;
+            for (int i = 0; i < N; i += 2) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(cr + 2 * i));
+                const float4 y = __ldg(reinterpret_cast<const float4 *>(sr + 2 * i));
+                c[i] = make_float2(x.x, x.y);
+                c[i + 1] = make_float2(x.z, x.w);
+                s[i] = make_float2(y.x, y.y);
+                s[i + 1] = make_float2(y.z, y.w);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool r = on && i < pairs;
-                c[i] = r ? __ldg(cr + i) : 1.0f;
-                s[i] = r ? __ldg(sr + i) : 0.0f;
+            for (int i = 0; i < N; ++i) {
+                c[i].x = 2 * i < pairs ? __ldg(cr + 2 * i) : 1.0f;
+                s[i].x = 2 * i < pairs ? __ldg(sr + 2 * i) : 0.0f;
+                c[i].y = 2 * i + 1 < pairs ? __ldg(cr + 2 * i + 1) : 1.0f;
+                s[i].y = 2 * i + 1 < pairs ? __ldg(sr + 2 * i + 1) : 0.0f;
             }
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] *= a.sign;
+        for (int i = 0; i < N; ++i) s[i] = __fmul2_rn(s[i], both(a.sign));
     }
-    __device__ __forceinline__ void weights(const HeadsArgs &a, int which, float *wa,
-                                            float *wb) const {
+    __device__ __forceinline__ void weights(const HeadsArgs &a, const HeadsVecArgs &v, int which,
+                                            float2 *wa, float2 *wb) const {
+        const void *w = which ? a.w[1] : a.w[0];
+        if (w && v.weight_vec && !a.w_f32) {
+            uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+            if (on) x0 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + off0));
+            if (second)
+                x1 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + off1));
+            open(x0, x1, wa, wb);
+            return;
+        }
+        float2 e[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int j0 = IL ? off0 + 2 * i : off0 + i, j1 = IL ? j0 + 1 : off1 + i;
-            wa[i] = on && j0 < a.dim ? heads_weight<T>(a, which, j0) : 0.0f;
-            wb[i] = on && j1 < a.dim ? heads_weight<T>(a, which, j1) : 0.0f;
+            const int j = (i < N ? off0 : off1 - V) + 2 * i;
+            const bool has = i < N ? on : second;
+            e[i].x = has ? heads_weight<T>(a, which, j) : 0.0f;
+            e[i].y = has ? heads_weight<T>(a, which, j + 1) : 0.0f;
         }
+        split(e, wa, wb);
     }
     // a pair that does not rotate is left alone: an infinity times a zero sine is no number
-    __device__ __forceinline__ void turn(float *a, float *b, const float *c,
-                                         const float *s) const {
+    __device__ __forceinline__ void turn(float2 *a, float2 *b, const float2 *c,
+                                         const float2 *s) const {
+        if (pairs == V) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float x = a[i] * c[i] - b[i] * s[i], y = b[i] * c[i] + a[i] * s[i];
-            const bool r = i < pairs;
-            a[i] = r ? x : a[i];
-            b[i] = r ? y : b[i];
+            for (int i = 0; i < N; ++i) {
+                const float2 x = a[i];
+                a[i] = __ffma2_rn(x, c[i], neg2(__fmul2_rn(b[i], s[i])));
+                b[i] = __ffma2_rn(x, s[i], __fmul2_rn(b[i], c[i]));
+            }
+        } else if (pairs > 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float2 x = a[i], y = b[i];
+                if (2 * i < pairs) {
+                    a[i].x = x.x * c[i].x - y.x * s[i].x;
+                    b[i].x = y.x * c[i].x + x.x * s[i].x;
+                }
+                if (2 * i + 1 < pairs) {
+                    a[i].y = x.y * c[i].y - y.y * s[i].y;
+                    b[i].y = y.y * c[i].y + x.y * s[i].y;
+                }
+            }
         }
     }
 };
-
-__device__ __forceinline__ float group_sum(float v, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
 
 // Quotient and remainder of an item index by a count (32-bit when it fits).
 __device__ __forceinline__ void heads_split(int64_t i, int64_t n, int wide, int64_t &q,
@@ -367,12 +411,18 @@ __device__ __forceinline__ void heads_split(int64_t i, int64_t n, int wide, int6
     }
 }
 
+// Keeps the compiler from holding a vector's unpacked form across this point.
+__device__ __forceinline__ void keep_packed(uint4 &x) {
+    asm volatile("" : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w));
+}
+
 // Rotation, and norm with rotation.  An item is a token and HPT heads of q or
 // of k; all its loads are issued before the first is used.
 template <class T, bool IL, int MODE, int HPT>
 __global__ void __launch_bounds__(kHeadsThreads)
 k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
-    constexpr int V = 16 / sizeof(T);
+    using Unit = HeadsUnit<T, IL>;
+    constexpr int N = Unit::N;
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
     layer_pdl_launch();
     const int64_t item = ((int64_t)blockIdx.x * kHeadsThreads + threadIdx.x) >> v.log_lanes;
@@ -384,7 +434,7 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
     const int which = g >= v.groups[0];
     const int h0 = (int)(which ? g - v.groups[0] : g) * HPT;
     const int count = live ? min(HPT, a.heads[which] - h0) : 0;
-    HeadsUnit<T, IL> u;
+    Unit u;
     u.place(a, v, lane);
     const HeadsTensor tx = which ? a.x[1] : a.x[0], ty = which ? a.y[1] : a.y[0];
     const T *x = static_cast<const T *>(tx.p) + heads_offset(tx, b, s, h0);
@@ -396,29 +446,46 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
         if (h < count) u.load(x + h * tx.sh, x0[h], x1[h]);
         else x0[h] = x1[h] = make_uint4(0, 0, 0, 0);
     const int64_t p = heads_position(a, b, s);
-    float c[V], sn[V], wa[V], wb[V];
+    float2 c[N], sn[N], wa[N], wb[N];
     u.angles(a, v, p < 0 ? 0 : p, c, sn);
-    if constexpr (MODE == HEADS_NORM) u.weights(a, which, wa, wb);
+    if constexpr (MODE == HEADS_NORM) u.weights(a, v, which, wa, wb);
     if (p < 0 && live && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+    float rstd[HPT];
+    if constexpr (MODE == HEADS_NORM) {
+        // the heads' sums cross the lanes together, so that their shuffles overlap
+#pragma unroll
+        for (int h = 0; h < HPT; ++h) {
+            float2 va[N], vb[N], ss = both(0.0f);
+            Unit::open(x0[h], x1[h], va, vb);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                ss = __ffma2_rn(va[i], va[i], __ffma2_rn(vb[i], vb[i], ss));
+            rstd[h] = ss.x + ss.y;
+            keep_packed(x0[h]);
+            keep_packed(x1[h]);
+        }
+        for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int h = 0; h < HPT; ++h) rstd[h] += __shfl_xor_sync(0xFFFFFFFFu, rstd[h], o);
+        const float inv = 1.0f / (float)a.dim;
+#pragma unroll
+        for (int h = 0; h < HPT; ++h) rstd[h] = rsqrtf(fmaf(rstd[h], inv, a.eps));
+    }
 #pragma unroll
     for (int h = 0; h < HPT; ++h) {
-        float va[V], vb[V];
-        u.open(x0[h], x1[h], va, vb);
+        float2 va[N], vb[N];
+        Unit::open(x0[h], x1[h], va, vb);
         if constexpr (MODE == HEADS_NORM) {
-            float ss = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
-            const float rstd = rsqrtf(group_sum(ss, lanes) / (float)a.dim + a.eps);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                va[i] *= rstd * wa[i];
-                vb[i] *= rstd * wb[i];
+            for (int i = 0; i < N; ++i) {
+                va[i] = __fmul2_rn(va[i], __fmul2_rn(wa[i], both(rstd[h])));
+                vb[i] = __fmul2_rn(vb[i], __fmul2_rn(wb[i], both(rstd[h])));
             }
         }
         u.turn(va, vb, c, sn);
         if (p < 0) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) va[i] = vb[i] = 0.0f;
+            for (int i = 0; i < N; ++i) va[i] = vb[i] = both(0.0f);
         }
         if (h < count) u.store(y + h * ty.sh, va, vb);
     }
@@ -431,7 +498,8 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
 template <class T, bool IL>
 __global__ void __launch_bounds__(kHeadsThreads)
 k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
-    constexpr int V = 16 / sizeof(T);
+    using Unit = HeadsUnit<T, IL>;
+    constexpr int N = Unit::N;
     extern __shared__ float s_dw[];   // [groups of the CTA][dim]
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
     const int which = (int)blockIdx.x >= v.ctas[0];
@@ -441,15 +509,16 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
                       ty = which ? a.y[1] : a.y[0];
     const int64_t total = a.rows * heads;
     const int per = kHeadsThreads >> v.log_lanes, group = threadIdx.x >> v.log_lanes;
-    HeadsUnit<T, IL> u;
+    Unit u;
     u.place(a, v, lane);
     layer_pdl_launch();
     layer_pdl_wait();
-    float wa[V], wb[V], da[V], db[V];
-    u.weights(a, which, wa, wb);
+    float2 wa[N], wb[N], da[N], db[N];
+    u.weights(a, v, which, wa, wb);
 #pragma unroll
-    for (int i = 0; i < V; ++i) da[i] = db[i] = 0.0f;
+    for (int i = 0; i < N; ++i) da[i] = db[i] = both(0.0f);
     bool bad = false;
+    const float inv = 1.0f / (float)a.dim;
     // every lane of a warp makes the same number of steps: the exchanges are warp-wide
     const int64_t step = (int64_t)v.ctas[which] * per;
     for (int64_t base = (int64_t)cta * per; base < total; base += step) {
@@ -464,33 +533,43 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
             u.load(static_cast<const T *>(tg.p) + heads_offset(tg, b, s, h), g0, g1);
         }
         const int64_t p = heads_position(a, b, s);
-        float c[V], sn[V], xa[V], xb[V], ga[V], gb[V];
-        u.angles(a, v, p < 0 ? 0 : p, c, sn);
-        u.open(x0, x1, xa, xb);
-        u.open(g0, g1, ga, gb);
-        u.turn(ga, gb, c, sn);
-        float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-            dot = fmaf(ga[i] * wa[i], xa[i], fmaf(gb[i] * wb[i], xb[i], dot));
-        }
-        ss = group_sum(ss, lanes);
-        dot = group_sum(dot, lanes);
-        const float rstd = rsqrtf(ss / (float)a.dim + a.eps);
-        const float mean = dot * rstd / (float)a.dim;
         const bool use = live && p >= 0;
         bad |= live && p < 0;
+        if (!use) x0 = x1 = g0 = g1 = make_uint4(0, 0, 0, 0);
+        float2 c[N], sn[N], xa[N], xb[N], ga[N], gb[N];
+        u.angles(a, v, p < 0 ? 0 : p, c, sn);
+        Unit::open(x0, x1, xa, xb);
+        Unit::open(g0, g1, ga, gb);
+        u.turn(ga, gb, c, sn);
+        float2 ss = both(0.0f), dot = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            xa[i] *= rstd;
-            xb[i] *= rstd;
-            if (use) {
-                da[i] = fmaf(ga[i], xa[i], da[i]);
-                db[i] = fmaf(gb[i], xb[i], db[i]);
+        for (int i = 0; i < N; ++i) {
+            ss = __ffma2_rn(xa[i], xa[i], __ffma2_rn(xb[i], xb[i], ss));
+            dot = __ffma2_rn(__fmul2_rn(ga[i], wa[i]), xa[i],
+                             __ffma2_rn(__fmul2_rn(gb[i], wb[i]), xb[i], dot));
+        }
+        ss.x += ss.y;
+        ss.y = dot.x + dot.y;
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+            ss.x += __shfl_xor_sync(0xFFFFFFFFu, ss.x, o);
+            ss.y += __shfl_xor_sync(0xFFFFFFFFu, ss.y, o);
+        }
+        const float rstd = rsqrtf(fmaf(ss.x, inv, a.eps));
+        const float2 mean = both(-ss.y * rstd * inv), r2 = both(rstd);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            xa[i] = __fmul2_rn(xa[i], r2);
+            xb[i] = __fmul2_rn(xb[i], r2);
+            if (use) {    // rstd may be infinite where nothing is used
+                da[i] = __ffma2_rn(ga[i], xa[i], da[i]);
+                db[i] = __ffma2_rn(gb[i], xb[i], db[i]);
             }
-            ga[i] = use ? rstd * (ga[i] * wa[i] - xa[i] * mean) : 0.0f;
-            gb[i] = use ? rstd * (gb[i] * wb[i] - xb[i] * mean) : 0.0f;
+            ga[i] = __fmul2_rn(__ffma2_rn(xa[i], mean, __fmul2_rn(ga[i], wa[i])), r2);
+            gb[i] = __fmul2_rn(__ffma2_rn(xb[i], mean, __fmul2_rn(gb[i], wb[i])), r2);
+        }
+        if (!use) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) ga[i] = gb[i] = both(0.0f);
         }
         if (live)
             u.store(static_cast<T *>(const_cast<void *>(ty.p)) + heads_offset(ty, b, s, h), ga,
@@ -498,10 +577,20 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     }
     if (bad && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int j0 = IL ? u.off0 + 2 * i : u.off0 + i, j1 = IL ? j0 + 1 : u.off1 + i;
-        if (u.on && j0 < a.dim) s_dw[group * a.dim + j0] = da[i];
-        if (u.on && j1 < a.dim) s_dw[group * a.dim + j1] = db[i];
+    for (int i = 0; i < N; ++i) {
+        // pairs 2i and 2i + 1 of the unit
+        const int j = IL ? (i < N / 2 ? u.off0 : u.off1 - Unit::V) + 4 * i : u.off0 + 2 * i;
+        const int k = IL ? j + 1 : u.off1 + 2 * i, next = IL ? 2 : 1;
+        const bool first = IL ? (i < N / 2 ? u.on : u.second) : u.on;
+        const bool other = IL ? first : u.second;
+        if (first) {
+            s_dw[group * a.dim + j] = da[i].x;
+            s_dw[group * a.dim + j + next] = da[i].y;
+        }
+        if (other) {
+            s_dw[group * a.dim + k] = db[i].x;
+            s_dw[group * a.dim + k + next] = db[i].y;
+        }
     }
     __syncthreads();
     for (int j = threadIdx.x; j < a.dim; j += kHeadsThreads) {
@@ -510,16 +599,5 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
         a.partial[which][(int64_t)cta * a.dim + j] = t;
     }
 }
-
-// The last step of the weight gradients: dw[j] = the sum of partial[.][j] over
-// the CTAs, in an order fixed by their number.  grid (columns / 32, 2).
-struct HeadsDwArgs {
-    const float *partial[2];
-    int64_t count[2];
-    float *dw[2];
-    int32_t dim;
-};
-
-__global__ void __launch_bounds__(1024) k_heads_dw(const HeadsDwArgs a);
 
 }  // namespace ebin

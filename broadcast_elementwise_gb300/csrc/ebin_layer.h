@@ -59,6 +59,11 @@ cudaError_t launch_layer(void (*kernel)(KParams...), dim3 grid, int block, size_
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// sum[w][j] = the sum over rows of partial[w], [count[w]][dim], for `tensors`
+// (1 or 2) tensors, in a fixed order (ebin_layer.cu).
+cudaError_t launch_sum_rows(const float *const partial[2], const int64_t count[2],
+                            float *const sum[2], int64_t dim, int tensors, cudaStream_t s);
+
 #ifdef __CUDACC__
 __device__ __forceinline__ void layer_pdl_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

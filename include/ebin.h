@@ -751,7 +751,7 @@ typedef struct ebin_gemm_plan_s *ebin_gemm_plan_t;
 /*
  * Check the attributes and build a plan (immutable, usable from any thread
  * and stream; the caller owns it).  Errors: INVALID_ARG (NULL, sizes, a row
- * stride below the row or an extent of 2^60 elements; m, n or k above 2^31 - 1),
+ * stride below the row or an extent of 2^60 elements; m, n or k above 2^30),
  * INVALID_ATTR (flags, activation), UNSUPPORTED_TYPE.
  */
 ebin_status ebin_gemm_plan_create(const ebin_gemm_attrs *attrs, ebin_gemm_plan_t *out);

@@ -96,3 +96,31 @@ def table(positions, r, amplitude=1.0, first=0, **kw):
     p = torch.arange(first, first + positions, dtype=torch.float64)[:, None]
     a = p * torch.tensor(frequencies(r, **kw), dtype=torch.float64)
     return a.cos() * amplitude, a.sin() * amplitude
+
+
+def act(z, kind):
+    if kind == "relu":
+        return torch.where(z < 0, torch.zeros_like(z), z)
+    if kind == "silu":
+        return z * torch.sigmoid(z)
+    if kind == "gelu":
+        return 0.5 * z * torch.special.erfc(-z / math.sqrt(2.0))
+    if kind == "gelu_tanh":
+        return z * torch.sigmoid(math.sqrt(8 / math.pi) * (z + 0.044715 * z ** 3))
+    return z
+
+
+def act_slope(z, kind):
+    if kind == "relu":
+        return (z > 0).double()
+    if kind == "silu":
+        return torch.sigmoid(z) + z * torch.sigmoid(z) * torch.sigmoid(-z)
+    if kind == "gelu":
+        return (0.5 * torch.special.erfc(-z / math.sqrt(2.0))
+                + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi))
+    if kind == "gelu_tanh":
+        c = math.sqrt(8 / math.pi)
+        u = c * (z + 0.044715 * z ** 3)
+        return torch.sigmoid(u) + (z * c * (1 + 3 * 0.044715 * z ** 2) * torch.sigmoid(u)
+                                   * torch.sigmoid(-u))
+    return torch.ones_like(z)
