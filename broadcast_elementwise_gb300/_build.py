@@ -86,6 +86,11 @@ def _jobs():
         src = os.path.join(CSRC, "ebin_%s.cu" % g)
         obj = os.path.join(OBJDIR, "ebin_%s.o" % g)
         jobs.append((obj, [src] + heads, [nvcc, *ARCH, *LAYER_FLAGS, "-c", src, "-o", obj]))
+    tc_src = os.path.join(CSRC, "ebin_gemm_tc.cu")
+    for dt in (1, 2):       # float16, bfloat16
+        obj = os.path.join(OBJDIR, "ebin_gemm_tc_%d.o" % dt)
+        jobs.append((obj, [tc_src] + heads,
+                     [nvcc, *ARCH, *LAYER_FLAGS, "-DEBIN_DT=%d" % dt, "-c", tc_src, "-o", obj]))
     for g in GROUPS:
         src = os.path.join(CSRC, "k_%s.cu" % g)
         for dt in range(N_DT):

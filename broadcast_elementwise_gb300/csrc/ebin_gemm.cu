@@ -2,14 +2,54 @@
 // choice and launch.
 #include <new>
 
-#include "ebin_gemm.cuh"
+#include "ebin_gemm_tc.cuh"
 
 struct ebin_gemm_plan_s {
     ebin_gemm_attrs at;
     int64_t lda, ldb, ldy, ldr, ldz;
     int64_t a_rows, a_cols, b_rows, b_cols;   // as stored
+    int64_t copy_a = -1, copy_b = -1;         // workspace offsets of their copies, or -1
     size_t workspace = 0;
 };
+
+namespace ebin {
+
+#define EBIN_DECLARE_TC(name)                                                             \
+    cudaError_t name(const CUtensorMap &, const CUtensorMap &, const TcArgs &, int bn,    \
+                     int grid, int cluster, cudaStream_t);
+EBIN_DECLARE_TC(launch_tc_f16)
+EBIN_DECLARE_TC(launch_tc_bf16)
+#undef EBIN_DECLARE_TC
+
+// Lay a matrix of 16-bit elements out anew, its rows on 16-byte boundaries:
+// a thread gathers eight elements and stores them as one vector.
+struct RepackArgs {
+    const uint16_t *src;
+    uint4 *dst;
+    int64_t rows, cols, ld, units;   // units: vectors of a row of dst
+};
+
+__global__ void __launch_bounds__(256) k_repack(const RepackArgs a, const RepackArgs b) {
+    layer_pdl_launch();
+    layer_pdl_wait();
+    const RepackArgs &r = blockIdx.y ? b : a;
+    const int64_t total = r.rows * r.units;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / r.units, c = (i - row * r.units) * 8;
+        const uint16_t *x = r.src + row * r.ld + c;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = c + 2 * j < r.cols ? x[2 * j] : 0u;
+            const uint32_t hi = c + 2 * j + 1 < r.cols ? x[2 * j + 1] : 0u;
+            w[j] = lo | hi << 16;
+        }
+        r.dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+}  // namespace ebin
 
 using namespace ebin;
 
@@ -19,32 +59,139 @@ int64_t matrix_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t isz) {
     return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * isz : 0;
 }
 
-template <class T, int ACT>
-cudaError_t launch_any(const ebin_gemm_plan_s &p, const void *A, const void *B,
-                       const GemmEpilogue &e, cudaStream_t s) {
-    GemmAnyArgs g{};
-    g.a = A;
-    g.b = B;
-    g.a_m = p.at.trans_a ? 1 : p.lda;
-    g.a_k = p.at.trans_a ? p.lda : 1;
-    g.b_k = p.at.trans_b ? 1 : p.ldb;
-    g.b_n = p.at.trans_b ? p.ldb : 1;
-    g.s = {p.at.m, p.at.n, p.at.k};
-    g.e = e;
-    const dim3 grid((unsigned)div_up(p.at.n, 64), (unsigned)div_up(p.at.m, 64));
-    return launch_layer(k_gemm_any<T, ACT>, grid, 256, 0, s, 1, g);
+int64_t round8(int64_t n) { return div_up(n, 8) * 8; }
+
+// cuTensorMapEncodeTiled, looked up through the runtime, or null.
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return (EncodeFn) nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
 }
 
-template <class T>
-cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
-                        const GemmEpilogue &e, cudaStream_t s) {
-    switch (p.at.activation) {
-    case EBIN_ACT_RELU: return launch_any<T, EBIN_ACT_RELU>(p, A, B, e, s);
-    case EBIN_ACT_GELU: return launch_any<T, EBIN_ACT_GELU>(p, A, B, e, s);
-    case EBIN_ACT_GELU_TANH: return launch_any<T, EBIN_ACT_GELU_TANH>(p, A, B, e, s);
-    case EBIN_ACT_SILU: return launch_any<T, EBIN_ACT_SILU>(p, A, B, e, s);
-    default: return launch_any<T, EBIN_ACT_NONE>(p, A, B, e, s);
+// One operand of the product as the kernel sees it.
+struct Operand {
+    const void *p;
+    int64_t rows, cols, ld;   // as stored
+    int64_t copy;             // its copy's workspace offset, or -1
+    bool mn;                  // dense across k
+};
+
+// The tensor map of an operand: boxes of 64 dense elements by `box` rows.
+bool encode(const Operand &o, int box, bool bf16, CUtensorMap *map) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows};
+    // a single row has no step; any whole number of vectors serves
+    const cuuint64_t strides[1] = {(cuuint64_t)(o.rows > 1 ? o.ld : round8(o.cols)) * 2};
+    const cuuint32_t boxes[2] = {64, (cuuint32_t)(o.mn ? kTcBK : box)};
+    const cuuint32_t steps[2] = {1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+              const_cast<void *>(o.p), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool needs_copy(const Operand &o) {
+    return (uintptr_t)o.p % 16 != 0 || (o.rows > 1 && o.ld % 8 != 0);
+}
+
+struct Shape {
+    int bn;        // accumulator columns of a tile
+    int split;     // CTAs that share a tile's k (1 for the paired kernel too)
+    bool pair;     // 256 x 256 tiles on pairs of CTAs, P = A; else P = B on single CTAs
+};
+
+// Which tiles.  128-row tiles of B against 16 to 128 rows of A, each tile's k
+// cut in up to eight, while they fit the SMs once; 256 x 256 tiles on pairs of
+// CTAs beyond that, where operand traffic counts.
+Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
+    Shape s{};
+    s.bn = at.m <= 16 ? 16 : at.m <= 32 ? 32 : at.m <= 64 ? 64 : 128;
+    s.split = 1;
+    const int64_t tiles = div_up(at.n, kTcRows) * div_up(at.m, s.bn);
+    if (tiles > sms && at.m > 64) {
+        s.pair = true;
+        s.bn = 256;
+        return s;
     }
+    const int64_t kblocks = div_up(at.k, kTcBK);
+    while (s.split < 8 && tiles * s.split * 2 <= sms && kblocks >= s.split * 8) s.split *= 2;
+    return s;
+}
+
+cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
+                        const GemmEpilogue &e, void *workspace, cudaStream_t s) {
+    const ebin_gemm_attrs &at = p.at;
+    Operand a{A, p.a_rows, p.a_cols, p.lda, p.copy_a, at.trans_a != 0};
+    Operand b{B, p.b_rows, p.b_cols, p.ldb, p.copy_b, at.trans_b == 0};
+    const bool bf16 = at.dtype == EBIN_BFLOAT16;
+    if (at.k > 0) {
+        RepackArgs r[2];
+        int count = 0;
+        int64_t most = 0;
+        for (Operand *o : {&a, &b}) {
+            if (!needs_copy(*o)) continue;
+            char *dst = static_cast<char *>(workspace) + o->copy;
+            const int64_t units = div_up(o->cols, 8);
+            r[count++] = RepackArgs{static_cast<const uint16_t *>(o->p),
+                                    reinterpret_cast<uint4 *>(dst), o->rows, o->cols, o->ld,
+                                    units};
+            most = std::max(most, o->rows * units);
+            o->p = dst;
+            o->ld = units * 8;
+        }
+        if (count > 0) {
+            const int64_t grid = std::min<int64_t>(div_up(most, 256), 16ll * current_sm_count());
+            const cudaError_t st = launch_layer(k_repack, dim3((unsigned)grid, (unsigned)count),
+                                                256, 0, s, 1, r[0], r[count - 1]);
+            if (st != cudaSuccess) return st;
+        }
+    }
+    const Shape shape = gemm_shape(at, current_sm_count());
+    const Operand &po = shape.pair ? a : b, &qo = shape.pair ? b : a;
+    TcArgs t{};
+    t.e = e;
+    t.m = at.m;
+    t.n = at.n;
+    t.kblocks = (int)div_up(at.k, kTcBK);
+    const int64_t p_rows = shape.pair ? at.m : at.n, q_rows = shape.pair ? at.n : at.m;
+    const int64_t p_tiles = div_up(p_rows, kTcRows * (shape.pair ? 2 : 1));
+    const int64_t q_tiles = div_up(q_rows, shape.bn);
+    t.p_tiles = (int)p_tiles;
+    t.q_tiles = (int)q_tiles;
+    t.p_mn = po.mn;
+    t.q_mn = qo.mn;
+    t.q_box = shape.bn / (shape.pair ? 2 : 1);
+    auto aligned = [&](const void *x, int64_t ld) { return (uintptr_t)x % 16 == 0 && ld % 8 == 0; };
+    t.vec = aligned(e.y, e.ldy) && aligned(e.z, e.z ? e.ldz : 0) &&
+            aligned(e.residual, e.residual ? e.ld_residual : 0) && (uintptr_t)e.bias % 16 == 0;
+    // two seconds, and the time that a long sum may take
+    t.limit = 4000000000ll + 100000ll * t.kblocks;
+    t.status = stream_status_word(s);
+    if (!t.status) return cudaErrorMemoryAllocation;
+    CUtensorMap maps[2] = {};
+    if (at.k > 0 && (!encode(po, kTcRows, bf16, &maps[0]) || !encode(qo, t.q_box, bf16, &maps[1])))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = p_tiles * q_tiles;
+    const int cluster = shape.pair ? 2 : shape.split;
+    const int64_t clusters = shape.pair ? std::min<int64_t>(tiles, current_sm_count() / 2) : tiles;
+    if (clusters * cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return (bf16 ? launch_tc_bf16 : launch_tc_f16)(maps[0], maps[1], t, shape.bn,
+                                                   (int)clusters * cluster, cluster, s);
 }
 
 }  // namespace
@@ -82,6 +229,17 @@ extern "C" ebin_status ebin_gemm_plan_create(const ebin_gemm_attrs *attrs, ebin_
         if (ld[i] < cols[i] || !product_fits(std::max<int64_t>(rows[i], 1), ld[i], &n)) {
             delete p;
             return EBIN_ERR_INVALID_ARG;
+        }
+    }
+    // copies of operands whose rows the tensor copies cannot take as they lie
+    if (a.m > 0 && a.n > 0 && a.k > 0) {
+        if (a.any_alignment || (p->a_rows > 1 && p->lda % 8 != 0)) {
+            p->copy_a = (int64_t)p->workspace;
+            p->workspace += (size_t)(p->a_rows * round8(p->a_cols) * 2);
+        }
+        if (a.any_alignment || (p->b_rows > 1 && p->ldb % 8 != 0)) {
+            p->copy_b = (int64_t)p->workspace;
+            p->workspace += (size_t)(p->b_rows * round8(p->b_cols) * 2);
         }
     }
     *out = p;
@@ -144,7 +302,5 @@ extern "C" ebin_status ebin_gemm_execute(ebin_gemm_plan_t plan, const void *A, c
     e.ldz = p.ldz;
     e.bias_f32 = at.dtype_bias == EBIN_FLOAT32;
     e.act = at.activation;
-    const cudaError_t st = at.dtype == EBIN_FLOAT16 ? launch_gemm<__half>(p, A, B, e, s)
-                                                    : launch_gemm<__nv_bfloat16>(p, A, B, e, s);
-    return st == cudaSuccess ? EBIN_OK : EBIN_ERR_CUDA;
+    return launch_gemm(p, A, B, e, workspace, s) == cudaSuccess ? EBIN_OK : EBIN_ERR_CUDA;
 }

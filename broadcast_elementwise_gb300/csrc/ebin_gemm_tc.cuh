@@ -1,0 +1,562 @@
+// The product on the tensor cores: operand tiles by tensor copies (TMA) into
+// swizzled shared memory, tcgen05.mma into accumulators in tensor memory, the
+// epilogue from there.
+//
+// Mathematics: D = P Q^T over k, P's rows the lanes of the accumulator (128 a
+// CTA), Q's rows its columns (BN).  A product runs either way round: P = A
+// and Q = B, or, for few rows of A, P = B and Q = A, so that the long operand
+// fills the 128 lanes.  Either operand may be dense along k or across it: the
+// shared-memory descriptors say which, nothing is transposed.
+//
+// Warps of a CTA: 0 issues the copies, 1 the matrix instructions, 2 holds the
+// tensor memory, 4.. run the epilogue.  Barriers between them: `full` and
+// `empty` per stage of operands, `tfull` and `tempty` per accumulator.  Every
+// wait has a limit; one that runs out raises EBIN_DEVICE_WAIT_LIMIT and the
+// CTA winds down (its copies and products in flight first).
+#pragma once
+
+#include <type_traits>
+
+#include <cuda.h>
+
+#include "ebin_gemm.cuh"
+
+namespace ebin {
+
+constexpr int kTcBK = 64;                    // k per stage: one 128-byte swizzle row
+constexpr int kTcRows = 128;                 // accumulator lanes of a CTA
+constexpr int kTcSmem = 227 * 1024;
+
+struct TcArgs {
+    GemmEpilogue e;
+    int64_t m, n;
+    int32_t kblocks;            // k in steps of kTcBK
+    int32_t p_tiles, q_tiles;   // tiles of P's rows (kTcRows * CTAs) and of Q's (BN)
+    int32_t p_mn, q_mn;         // the operand is dense across k
+    int32_t q_box;              // Q's rows a copy brings when it is dense along k
+    int32_t vec;                // y, z, residual and the bias take 16-byte accesses
+    long long limit;            // clocks of a wait
+    uint32_t *status;
+};
+
+__device__ __forceinline__ uint32_t tc_smem(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void tc_bar_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void tc_bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// arrive at a barrier of this cluster, by its cluster address
+__device__ __forceinline__ void tc_bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool tc_bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// Wait for the phase of the given parity; false when the limit ran out.
+__device__ __forceinline__ bool tc_bar_wait(uint32_t bar, uint32_t parity, long long limit) {
+    for (int i = 0; i < 32; ++i)
+        if (tc_bar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (clock64() - t0 < limit)
+        if (tc_bar_try(bar, parity)) return true;
+    return false;
+}
+// a CTA of this cluster's view of a shared-memory address of this CTA's layout
+__device__ __forceinline__ uint32_t tc_map(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t tc_cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t tc_cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void tc_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tc_copy(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                        uint32_t bar) {
+    if constexpr (CTAS == 2)
+        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global"
+                     ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+                     "l"(map), "r"(bar), "r"(x), "r"(y)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+                     "l"(map), "r"(bar), "r"(x), "r"(y)
+                     : "memory");
+}
+
+template <int CTAS> __device__ __forceinline__ void tc_alloc(uint32_t dst, int columns) {
+    if constexpr (CTAS == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+template <int CTAS> __device__ __forceinline__ void tc_free(uint32_t addr, int columns) {
+    if constexpr (CTAS == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr),
+                     "r"(columns));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr),
+                     "r"(columns));
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle; rows of 128 bytes, eight
+// of them 1024 bytes on (k-dense operands), or, for operands dense across k,
+// blocks of 64 k by 64 rows 8192 bytes on.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, bool mn) {
+    const uint64_t lead = mn ? 8192 >> 4 : 1, stride = 1024 >> 4;
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (lead << 16) | (stride << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t add) {
+    if constexpr (CTAS == 2)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(add)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(add)
+                     : "memory");
+}
+
+// Arrive at `bar` (of both CTAs of a pair) when the products issued so far are done.
+template <int CTAS> __device__ __forceinline__ void tc_commit(uint32_t bar) {
+    if constexpr (CTAS == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                     ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"((uint16_t)3)
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+                     "[%0];" ::"r"(bar)
+                     : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+// 16 accumulator columns of a warp's 32 lanes: thread = lane.  The load and
+// its wait are one statement: the registers hold nothing before the wait.
+__device__ __forceinline__ void tc_load16(uint32_t addr, float *v) {
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <class T> __device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    } else {
+        const __half2 p = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    }
+}
+template <class T> __device__ __forceinline__ void tc_unpack8(const uint4 &w, float *v) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            v[2 * i] = __uint_as_float(x[i] << 16);
+            v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+template <class T> __device__ __forceinline__ uint4 tc_pack8(const float *v) {
+    return make_uint4(tc_pack<T>(v[0], v[1]), tc_pack<T>(v[2], v[3]), tc_pack<T>(v[4], v[5]),
+                      tc_pack<T>(v[6], v[7]));
+}
+
+// One element's epilogue where neighbouring lanes hold neighbouring n.
+template <class T>
+__device__ __forceinline__ void tc_store_one(const GemmEpilogue &e, int64_t m, int64_t n, float z,
+                                             float bias) {
+    z += bias;
+    if (e.z) static_cast<T *>(e.z)[m * e.ldz + n] = from_f<T>(z);
+    float y = z;
+    switch (e.act) {
+    case EBIN_ACT_RELU: y = act_value<EBIN_ACT_RELU>(z); break;
+    case EBIN_ACT_GELU: y = act_value<EBIN_ACT_GELU>(z); break;
+    case EBIN_ACT_GELU_TANH: y = act_value<EBIN_ACT_GELU_TANH>(z); break;
+    case EBIN_ACT_SILU: y = act_value<EBIN_ACT_SILU>(z); break;
+    }
+    if (e.residual) y += to_f(static_cast<const T *>(e.residual)[m * e.ld_residual + n]);
+    static_cast<T *>(e.y)[m * e.ldy + n] = from_f<T>(y);
+}
+template <class T>
+__device__ __forceinline__ float tc_bias(const GemmEpilogue &e, int64_t n) {
+    if (!e.bias) return 0.0f;
+    return e.bias_f32 ? static_cast<const float *>(e.bias)[n]
+                      : to_f(static_cast<const T *>(e.bias)[n]);
+}
+
+template <int ACT> __device__ __forceinline__ void tc_act16(float *v) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
+}
+
+// 16 neighbouring columns n of row m, all inside the output, vectors aligned.
+template <class T>
+__device__ __forceinline__ void tc_store16(const GemmEpilogue &e, int64_t m, int64_t n, float *v) {
+    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
+    if (e.residual) {
+        const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(e.residual) +
+                                                         m * e.ld_residual + n);
+        r0 = r[0];
+        r1 = r[1];
+    }
+    if (e.bias) {
+        if (e.bias_f32) {
+            const float4 *b = reinterpret_cast<const float4 *>(static_cast<const float *>(e.bias) + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = __ldg(b + i);
+                v[4 * i] += f.x;
+                v[4 * i + 1] += f.y;
+                v[4 * i + 2] += f.z;
+                v[4 * i + 3] += f.w;
+            }
+        } else {
+            const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const T *>(e.bias) + n);
+            float f[16];
+            tc_unpack8<T>(__ldg(b), f);
+            tc_unpack8<T>(__ldg(b + 1), f + 8);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += f[i];
+        }
+    }
+    if (e.z) {
+        uint4 *z = reinterpret_cast<uint4 *>(static_cast<T *>(e.z) + m * e.ldz + n);
+        z[0] = tc_pack8<T>(v);
+        z[1] = tc_pack8<T>(v + 8);
+    }
+    switch (e.act) {
+    case EBIN_ACT_RELU: tc_act16<EBIN_ACT_RELU>(v); break;
+    case EBIN_ACT_GELU: tc_act16<EBIN_ACT_GELU>(v); break;
+    case EBIN_ACT_GELU_TANH: tc_act16<EBIN_ACT_GELU_TANH>(v); break;
+    case EBIN_ACT_SILU: tc_act16<EBIN_ACT_SILU>(v); break;
+    }
+    if (e.residual) {
+        float f[16];
+        tc_unpack8<T>(r0, f);
+        tc_unpack8<T>(r1, f + 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += f[i];
+    }
+    uint4 *y = reinterpret_cast<uint4 *>(static_cast<T *>(e.y) + m * e.ldy + n);
+    y[0] = tc_pack8<T>(v);
+    y[1] = tc_pack8<T>(v + 8);
+}
+
+// What a kernel's shared memory holds, in bytes.
+template <int CTAS, int BN> struct TcLayout {
+    static constexpr int kP = kTcRows * 128;
+    static constexpr int kQRows = BN / CTAS < 64 ? 64 : BN / CTAS;
+    static constexpr int kQ = kQRows * 128;
+    static constexpr int kStage = kP + kQ;
+    static constexpr int kEpilogueWarps = 4;
+    static constexpr int kScratch = kEpilogueWarps * 32 * 17 * 4;   // a warp's 32 x 16 transpose
+    static constexpr int kBarriers = 512;
+    static constexpr int kStages =
+        (kTcSmem - 1024 - kScratch - kBarriers) / kStage > 8
+            ? 8 : (kTcSmem - 1024 - kScratch - kBarriers) / kStage;
+    static constexpr int kColumns = 2 * BN < 32 ? 32 : 2 * BN;      // two accumulators
+    static constexpr int kBytes = 1024 + kStages * kStage + kScratch + kBarriers;
+    static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+};
+
+// One tile after another (SPLIT = false): clusters of CTAS CTAs take tiles in
+// steps of their number; a pair's accumulator is 256 lanes over two CTAs, the
+// leader issues the products for both, each brings its own half of Q.
+// SPLIT: the CTAs of a cluster share one tile's k and join their sums through
+// each other's shared memory, in rank order; P = B, Q = A.
+template <class T, int CTAS, int BN, bool SPLIT>
+__global__ void __launch_bounds__(TcLayout<CTAS, BN>::kThreads, 1)
+k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+          const TcArgs a) {
+    using L = TcLayout<CTAS, BN>;
+    static_assert(!SPLIT || CTAS == 1, "a split tile is a single CTA's");
+    extern __shared__ uint8_t s_raw[];
+    const uint32_t base = (tc_smem(s_raw) + 1023) & ~1023u;
+    uint8_t *const s_base = s_raw + (base - tc_smem(s_raw));
+    const uint32_t scratch = base + L::kStages * L::kStage;
+    const uint32_t bars = scratch + L::kScratch;
+    auto full = [&](int i) { return bars + 8 * i; };
+    auto empty = [&](int i) { return bars + 8 * (L::kStages + i); };
+    auto tfull = [&](int i) { return bars + 8 * (2 * L::kStages + i); };
+    auto tempty = [&](int i) { return bars + 8 * (2 * L::kStages + 2 + i); };
+    const uint32_t drain = bars + 8 * (2 * L::kStages + 4);
+    const uint32_t s_tmem = drain + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc_cluster_rank(), ranks = tc_cluster_size();
+    const bool leader = CTAS == 1 || rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            tc_bar_init(full(i), 1);
+            tc_bar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc_bar_init(tfull(i), 1);
+            tc_bar_init(tempty(i), CTAS * L::kEpilogueWarps);
+        }
+        tc_bar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tc_alloc<CTAS>(s_tmem, L::kColumns);
+    layer_pdl_launch();
+    tc_fence_before();
+    __syncthreads();
+    tc_cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_base + (s_tmem - base));
+    layer_pdl_wait();
+
+    // the work of this cluster (and, split, this CTA's part of k)
+    const int tiles = a.p_tiles * a.q_tiles;
+    const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
+    const int kb0 = SPLIT ? (int)((long long)a.kblocks * rank / ranks) : 0;
+    const int kb1 = SPLIT ? (int)((long long)a.kblocks * (rank + 1) / ranks) : a.kblocks;
+    auto place = [&](int t, int &p, int &q) {
+        // groups of eight tiles of P walk along Q: the tiles in flight form a block
+        constexpr int G = 8;
+        const int group = t / (G * a.q_tiles), in = t - group * G * a.q_tiles;
+        const int size = min(G, a.p_tiles - group * G);
+        p = group * G + in % size;
+        q = in / size;
+    };
+    bool ok = true;
+
+    if (warp == 0 && lane == 0) {
+        int it = 0;
+        for (int t = cluster; t < tiles && ok; t += clusters) {
+            int p, q;
+            place(t, p, q);
+            const int pr = (p * CTAS + (CTAS == 2 ? (int)rank : 0)) * kTcRows;
+            const int qr = q * BN + (CTAS == 2 ? (int)rank * (BN / 2) : 0);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % L::kStages;
+                if (!tc_bar_wait(empty(s), (it / L::kStages & 1) ^ 1, a.limit)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sp = base + s * L::kStage, sq = sp + L::kP;
+                const uint32_t q_bytes = a.q_mn ? L::kQ : a.q_box * 128;
+                const uint32_t bar = CTAS == 2 ? tc_map(full(s), 0) : full(s);
+                if (leader) tc_bar_expect(full(s), CTAS * (L::kP + q_bytes));
+                if (a.p_mn) {
+                    tc_copy<CTAS>(sp, &p_map, pr, kb * kTcBK, bar);
+                    tc_copy<CTAS>(sp + 8192, &p_map, pr + 64, kb * kTcBK, bar);
+                } else {
+                    tc_copy<CTAS>(sp, &p_map, kb * kTcBK, pr, bar);
+                }
+                if (a.q_mn) {
+#pragma unroll
+                    for (int i = 0; i < L::kQRows / 64; ++i)
+                        tc_copy<CTAS>(sq + 8192 * i, &q_map, qr + 64 * i, kb * kTcBK, bar);
+                } else {
+                    tc_copy<CTAS>(sq, &q_map, kb * kTcBK, qr, bar);
+                }
+            }
+        }
+        if (!ok && leader)   // wait for what is in flight
+            for (int j = max(0, it - L::kStages); j < it; ++j)
+                tc_bar_wait(full(j % L::kStages), j / L::kStages & 1, a.limit);
+    } else if (warp == 1 && lane == 0 && leader) {
+        // f32 accumulators; operands f16 or bf16, their major directions; N / 8, M / 16
+        constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+        const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a.p_mn << 15) |
+                               ((uint32_t)a.q_mn << 16) | ((uint32_t)(BN / 8) << 17) |
+                               ((uint32_t)(CTAS * kTcRows / 16) << 24);
+        const uint32_t p_step = a.p_mn ? 2048 >> 4 : 32 >> 4, q_step = a.q_mn ? 2048 >> 4 : 32 >> 4;
+        int it = 0, n = 0;
+        for (int t = cluster; t < tiles && ok; t += clusters, ++n) {
+            const int acc = n & 1;
+            if (!tc_bar_wait(tempty(acc), (n >> 1 & 1) ^ 1, a.limit)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % L::kStages;
+                if (!tc_bar_wait(full(s), it / L::kStages & 1, a.limit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sp = base + s * L::kStage;
+                uint64_t pd = tc_desc(sp, a.p_mn), qd = tc_desc(sp + L::kP, a.q_mn);
+#pragma unroll
+                for (int k = 0; k < kTcBK / 16; ++k) {
+                    tc_mma<CTAS>(tmem + acc * BN, pd, qd, idesc, kb > kb0 || k > 0);
+                    pd += p_step;
+                    qd += q_step;
+                }
+                tc_commit<CTAS>(empty(s));
+            }
+            if (ok) tc_commit<CTAS>(tfull(acc));
+        }
+        if (!ok) {   // wait for the products in flight
+            tc_commit<CTAS>(drain);
+            tc_bar_wait(drain, 0, a.limit);
+        }
+    } else if (warp >= 4 && !SPLIT) {
+        const int quarter = warp & 3;   // a warp reads its own quarter of the lanes
+        float *const s_t = reinterpret_cast<float *>(s_base + (scratch - base)) + quarter * 32 * 17;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        int n = 0;
+        for (int t = cluster; t < tiles && ok; t += clusters, ++n) {
+            int p, q;
+            place(t, p, q);
+            const int acc = n & 1;
+            ok = tc_bar_wait(tfull(acc), n >> 1 & 1, a.limit);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int64_t row0 = (int64_t)(p * CTAS + (CTAS == 2 ? (int)rank : 0)) * kTcRows +
+                                 quarter * 32;
+            const int64_t col0 = (int64_t)q * BN;
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 16) {
+                if (row0 >= a.m || col0 + c >= a.n) break;
+                float v[16];
+                tc_load16(lanes + acc * BN + c, v);
+                if (kb1 == kb0) {   // no k: nothing was summed
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                }
+                if (a.vec && col0 + c + 16 <= a.n) {
+                    if (row0 + lane < a.m) tc_store16<T>(a.e, row0 + lane, col0 + c, v);
+                } else {
+                    // off alignment or at the edge: through shared memory, so that
+                    // neighbouring lanes store neighbouring columns
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s_t[lane * 17 + i] = v[i];
+                    __syncwarp();
+                    const int64_t col = col0 + c + (lane & 15);
+                    if (col < a.n) {
+                        const float bias = tc_bias<T>(a.e, col);
+                        for (int r = lane >> 4; r < 32 && row0 + r < a.m; r += 2)
+                            tc_store_one<T>(a.e, row0 + r, col, s_t[r * 17 + (lane & 15)], bias);
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc_bar_arrive(CTAS == 2 ? tc_map(tempty(acc), 0) : tc_map(tempty(acc), rank));
+        }
+    }
+
+    if constexpr (SPLIT) {
+        // the stages are free once the products are done: they hold this CTA's sums, [BN][128]
+        float *const part = reinterpret_cast<float *>(s_base);
+        const int quarter = warp & 3;
+        if (warp >= 4) {
+            ok = tc_bar_wait(tfull(0), 0, a.limit);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+            const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 16) {
+                float v[16];
+                if (ok && kb1 > kb0) {
+                    tc_load16(lanes + c, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[(c + i) * kTcRows + quarter * 32 + lane] = v[i];
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        __syncthreads();
+        tc_cluster_sync();
+        int p, q;
+        place(cluster, p, q);
+        // P is B: lanes are n, columns are m; this CTA joins every ranks-th column
+        const int64_t row = (int64_t)p * kTcRows + (threadIdx.x & 127);
+        const int64_t col0 = (int64_t)q * BN;
+        const int first = (threadIdx.x >> 7) * (int)ranks + (int)rank;
+        if (row < a.n) {
+            const float bias = tc_bias<T>(a.e, row);
+            const uint32_t mine = base + 4 * (threadIdx.x & 127);
+            for (int c = first; c < BN && col0 + c < a.m; c += (L::kThreads >> 7) * (int)ranks) {
+                float z = 0.0f;
+                for (uint32_t r = 0; r < ranks; ++r) {
+                    float v;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(v)
+                                 : "r"(tc_map(mine + 4 * kTcRows * c, r))
+                                 : "memory");
+                    z += v;
+                }
+                tc_store_one<T>(a.e, col0 + c, row, z, bias);
+            }
+        }
+    }
+
+    if (!ok && lane == 0 && a.status) atomicOr(a.status, EBIN_DEVICE_WAIT_LIMIT);
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc_cluster_sync();
+    tc_fence_after();
+    if (warp == 2) tc_free<CTAS>(tmem, L::kColumns);
+}
+
+}  // namespace ebin
