@@ -162,6 +162,13 @@ cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode,
     return launch_layer(k_heads_any<T, HEADS_NORM_GRAD>, grid, kHeadsThreads, smem, s, 1, a, il);
 }
 
+HeadsDiv heads_div(uint32_t n) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < n) ++l;
+    const uint64_t m = (((uint64_t)1 << 32) * (((uint64_t)1 << l) - n)) / n + 1;
+    return HeadsDiv{n, (uint32_t)m, l};
+}
+
 // The vector path's layout of a head, or false where it does not apply: rows
 // that are not whole 16-byte vectors on 16-byte boundaries, halves that are
 // not (half layout), and heads of more than 64 vectors.
@@ -178,7 +185,22 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
         if (h > 0 && !(fits(a.x[w], h) && fits(a.y[w], h) && (!grad || fits(a.dy[w], h))))
             return false;
     }
+    const int64_t most = 0x7FFFFFFF;
+    if (p.rows * std::max<int64_t>(1, a.heads[0] + (int64_t)a.heads[1]) * 32 > most) return false;
     v = HeadsVecArgs{};
+    for (int w = 0; w < 2; ++w) {
+        const HeadsTensor *from[3] = {&a.x[w], &a.dy[w], &a.y[w]};
+        HeadsNear *to[3] = {&v.x[w], &v.dy[w], &v.y[w]};
+        for (int i = 0; i < 3; ++i) {
+            if (heads_of(p.at, w) == 0 || (i == 1 && !grad)) continue;
+            if (from[i]->st > most || from[i]->sh > most) return false;
+            *to[i] = HeadsNear{from[i]->p, from[i]->sb, (int32_t)from[i]->st,
+                               (int32_t)from[i]->sh};
+        }
+        v.heads[w] = heads_div((uint32_t)std::max(1, a.heads[w]));
+        v.heads[w].n = (uint32_t)a.heads[w];
+    }
+    v.tokens = heads_div((uint32_t)a.tokens);
     v.rot_units = (int)(a.half / V);
     v.units = il ? (int)div_up(D / V, 2)
                  : v.rot_units + (int)div_up((D - 2 * a.half) / V, 2);
@@ -189,34 +211,37 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
     return true;
 }
 
+// CTAs of a kernel that fit an SM at once.
+template <auto KERNEL> int heads_resident(size_t smem) {
+    static const int n = [smem] {
+        int b = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, KERNEL, kHeadsThreads, smem) !=
+                cudaSuccess || b < 1) {
+            cudaGetLastError();
+            b = 1;
+        }
+        return b;
+    }();
+    return n;
+}
+
 template <class T, bool IL, int MODE, int HPT>
 cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, cudaStream_t s) {
-    v.groups[0] = (int)div_up(a.heads[0], HPT);
-    v.groups[1] = (int)div_up(a.heads[1], HPT);
-    const int64_t items = a.rows * (v.groups[0] + v.groups[1]);
-    const int64_t grid = div_up(items << v.log_lanes, kHeadsThreads);
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    v.wide = (grid + 1) * kHeadsThreads >= (1ll << 32);
+    v.q_items = (uint32_t)div_up(a.heads[0], HPT);
+    v.per_token = heads_div(v.q_items + (uint32_t)div_up(a.heads[1], HPT));
+    v.items = (uint32_t)a.rows * v.per_token.n;
+    const int64_t grid = div_up((int64_t)v.items << v.log_lanes, kHeadsThreads);
     return launch_layer(k_heads_vec<T, IL, MODE, HPT>, dim3((unsigned)grid), kHeadsThreads, 0, s,
                         1, a, v);
 }
 
 template <class T, bool IL>
 cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, cudaStream_t s) {
-    static const int resident = [] {
-        int b = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, k_heads_vec_grad<T, IL>,
-                                                          kHeadsThreads, 16384) != cudaSuccess ||
-            b < 1) {
-            cudaGetLastError();
-            b = 1;
-        }
-        return b;
-    }();
     // one wave of CTAs, shared between q and k by their rows
     const int per = kHeadsThreads >> v.log_lanes;
-    const int64_t all = std::min<int64_t>((int64_t)resident * current_sm_count(),
-                                          kHeadsMaxPartials);
+    const int64_t all = std::min<int64_t>(
+        (int64_t)heads_resident<k_heads_vec_grad<T, IL>>(16384) * current_sm_count(),
+        kHeadsMaxPartials);
     const int64_t heads = a.heads[0] + a.heads[1];
     for (int w = 0; w < 2; ++w) {
         const int64_t most = div_up(a.rows * a.heads[w], per);
@@ -224,7 +249,6 @@ cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, c
         v.ctas[w] = (int)std::min(most, share);
         ctas[w] = v.ctas[w];
     }
-    v.wide = a.rows * std::max(a.heads[0], a.heads[1]) >= (1ll << 31);
     const size_t smem = sizeof(float) * per * a.dim;
     return launch_layer(k_heads_vec_grad<T, IL>, dim3((unsigned)(v.ctas[0] + v.ctas[1])),
                         kHeadsThreads, smem, s, 1, a, v);
@@ -235,7 +259,7 @@ cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, int mode,
                             cudaStream_t s) {
     if (mode == HEADS_NORM_GRAD) return launch_vec_grad<T, IL>(a, v, ctas, s);
     // Few rows: one head per item spreads them over the SMs.  Many: four heads
-    // share the token's cosines, sines and weights.
+    // share the token's position, cosines, sines and weights.
     const bool few = (a.rows * (a.heads[0] + a.heads[1]) << v.log_lanes) <
                      2048ll * current_sm_count();
     if (mode == HEADS_ROTATE)

@@ -191,16 +191,42 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, 
 // so a rotation needs no exchange between lanes, and a norm one tree over L.
 // Cosines, sines and weights stay in registers over the heads of one item.
 
+// Division of 32-bit indices by a launch's constant n: with 2^(l-1) < n <= 2^l
+// and m = floor(2^32 (2^l - n) / n) + 1, x / n = (hi(x m) + x) >> l exactly,
+// the sum taken in 33 bits (Granlund and Montgomery's multiplier).
+struct HeadsDiv {
+    uint32_t n, mul, shift;
+    __device__ __forceinline__ void split(uint32_t x, uint32_t &q, uint32_t &r) const {
+        q = (uint32_t)(((uint64_t)__umulhi(x, mul) + x) >> shift);
+        r = x - q * n;
+    }
+};
+
+struct HeadsNear {          // a tensor whose token and head strides fit 32 bits
+    const void *p;
+    int64_t sb;
+    int32_t st, sh;
+};
+
 struct HeadsVecArgs {
+    HeadsNear x[2], dy[2], y[2];
+    HeadsDiv per_token;     // items of a token: groups of HPT heads of q, then of k
+    HeadsDiv tokens;        // tokens of a sequence
+    HeadsDiv heads[2];      // the gradient's rows of q, of k
+    uint32_t q_items;       // of per_token
+    uint32_t items;         // of the launch
     int32_t log_lanes;
     int32_t units;          // lanes of a group with work
     int32_t rot_units;      // half layout: units that rotate
     int32_t table_vec;      // table rows may be read 16 bytes at a time
     int32_t weight_vec;     // and the weights
-    int32_t groups[2];      // items of a token: groups of HPT heads of q, then of k
-    int32_t wide;           // item indices pass 32 bits
     int32_t ctas[2];        // the gradient's CTAs for q and for k
 };
+
+__device__ __forceinline__ int64_t heads_near(const HeadsNear &t, uint32_t b, uint32_t s,
+                                              uint32_t h) {
+    return (int64_t)b * t.sb + (int64_t)(int32_t)s * t.st + (int64_t)(int32_t)h * t.sh;
+}
 
 // Two elements of a 16-bit word, or two binary32 elements, as a binary32 pair.
 template <class T> __device__ __forceinline__ float2 heads_open2(uint32_t w) {
@@ -258,10 +284,11 @@ template <class T, bool IL> struct HeadsUnit {
         if (!on) pairs = 0;
         second = on && off1 < a.dim;
     }
+    // every lane loads from inside the row: one without work (or without a
+    // second vector) repeats the row's first vector, and masks what it sums
     __device__ __forceinline__ void load(const T *p, uint4 &x0, uint4 &x1) const {
-        x0 = x1 = make_uint4(0, 0, 0, 0);
-        if (on) x0 = heads_load(p + off0);
-        if (second) x1 = heads_load(p + off1);
+        x0 = heads_load(p + (on ? off0 : 0));
+        x1 = heads_load(p + (second ? off1 : 0));
     }
     __device__ __forceinline__ static void open(const uint4 &x0, const uint4 &x1, float2 *a,
                                                 float2 *b) {
@@ -325,8 +352,9 @@ template <class T, bool IL> struct HeadsUnit {
         if (on) *reinterpret_cast<uint4 *>(p + off0) = r0;
         if (second) *reinterpret_cast<uint4 *>(p + off1) = r1;
     }
+    // c = cos, s = sin with the direction's sign, n = -s (pairs past `pairs`: 1, 0, 0)
     __device__ __forceinline__ void angles(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
-                                           float2 *c, float2 *s) const {
+                                           float2 *c, float2 *s, float2 *n) const {
         const float *cr = a.cos + p * a.half + pair0, *sr = a.sin + p * a.half + pair0;
         if (pairs == V && v.table_vec) {
 #pragma unroll
@@ -348,7 +376,10 @@ template <class T, bool IL> struct HeadsUnit {
             }
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = __fmul2_rn(s[i], both(a.sign));
+        for (int i = 0; i < N; ++i) {
+            n[i] = __fmul2_rn(s[i], both(-a.sign));
+            s[i] = __fmul2_rn(s[i], both(a.sign));
+        }
     }
     __device__ __forceinline__ void weights(const HeadsArgs &a, const HeadsVecArgs &v, int which,
                                             float2 *wa, float2 *wb) const {
@@ -371,45 +402,51 @@ template <class T, bool IL> struct HeadsUnit {
         }
         split(e, wa, wb);
     }
-    // a pair that does not rotate is left alone: an infinity times a zero sine is no number
-    __device__ __forceinline__ void turn(float2 *a, float2 *b, const float2 *c,
-                                         const float2 *s) const {
+    // a pair that does not rotate takes its factors ca, cb alone: an infinity
+    // times a zero sine would be no number
+    __device__ __forceinline__ void turn(float2 *a, float2 *b, const float2 *ca, const float2 *sa,
+                                         const float2 *nb, const float2 *cb) const {
         if (pairs == V) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float2 x = a[i];
-                a[i] = __ffma2_rn(x, c[i], neg2(__fmul2_rn(b[i], s[i])));
-                b[i] = __ffma2_rn(x, s[i], __fmul2_rn(b[i], c[i]));
+                a[i] = __ffma2_rn(x, ca[i], __fmul2_rn(b[i], nb[i]));
+                b[i] = __ffma2_rn(x, sa[i], __fmul2_rn(b[i], cb[i]));
             }
-        } else if (pairs > 0) {
+        } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float2 x = a[i], y = b[i];
+                a[i] = __fmul2_rn(x, ca[i]);
+                b[i] = __fmul2_rn(y, cb[i]);
                 if (2 * i < pairs) {
-                    a[i].x = x.x * c[i].x - y.x * s[i].x;
-                    b[i].x = y.x * c[i].x + x.x * s[i].x;
+                    a[i].x = fmaf(y.x, nb[i].x, a[i].x);
+                    b[i].x = fmaf(x.x, sa[i].x, b[i].x);
                 }
                 if (2 * i + 1 < pairs) {
-                    a[i].y = x.y * c[i].y - y.y * s[i].y;
-                    b[i].y = y.y * c[i].y + x.y * s[i].y;
+                    a[i].y = fmaf(y.y, nb[i].y, a[i].y);
+                    b[i].y = fmaf(x.y, sa[i].y, b[i].y);
                 }
             }
         }
     }
-};
-
-// Quotient and remainder of an item index by a count (32-bit when it fits).
-__device__ __forceinline__ void heads_split(int64_t i, int64_t n, int wide, int64_t &q,
-                                            int64_t &r) {
-    if (wide) {
-        q = i / n;
-        r = i - q * n;
-    } else {
-        const uint32_t qi = (uint32_t)i / (uint32_t)n;
-        q = qi;
-        r = (uint32_t)i - qi * (uint32_t)n;
+    // the sum over the lane's elements of x^2 (0 where it has none)
+    __device__ __forceinline__ float squares(const float2 *a, const float2 *b) const {
+        float2 x = both(0.0f), y = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!IL || i < N / 2) {
+                x = __ffma2_rn(a[i], a[i], x);
+                if (IL) x = __ffma2_rn(b[i], b[i], x);
+            }
+            if (!IL || i >= N / 2) {
+                if (IL) y = __ffma2_rn(a[i], a[i], y);
+                y = __ffma2_rn(b[i], b[i], y);
+            }
+        }
+        return (on ? x.x + x.y : 0.0f) + (second ? y.x + y.y : 0.0f);
     }
-}
+};
 
 // Keeps the compiler from holding a vector's unpacked form across this point.
 __device__ __forceinline__ void keep_packed(uint4 &x) {
@@ -419,48 +456,39 @@ __device__ __forceinline__ void keep_packed(uint4 &x) {
 // Rotation, and norm with rotation.  An item is a token and HPT heads of q or
 // of k; all its loads are issued before the first is used.
 template <class T, bool IL, int MODE, int HPT>
-__global__ void __launch_bounds__(kHeadsThreads)
+__global__ void __launch_bounds__(kHeadsThreads, sizeof(T) == 2 ? 3 : 1)
 k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
     using Unit = HeadsUnit<T, IL>;
     constexpr int N = Unit::N;
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
     layer_pdl_launch();
-    const int64_t item = ((int64_t)blockIdx.x * kHeadsThreads + threadIdx.x) >> v.log_lanes;
-    int64_t bs, g, b, s;
-    heads_split(item, v.groups[0] + v.groups[1], v.wide, bs, g);
-    const bool live = bs < a.rows;
-    if (!live) bs = 0;            // the group still takes part in the warp's exchanges
-    heads_split(bs, a.tokens, v.wide, b, s);
-    const int which = g >= v.groups[0];
-    const int h0 = (int)(which ? g - v.groups[0] : g) * HPT;
-    const int count = live ? min(HPT, a.heads[which] - h0) : 0;
+    uint32_t item = (blockIdx.x * kHeadsThreads + threadIdx.x) >> v.log_lanes;
+    const bool live = item < v.items;
+    if (!live) item = 0;          // the group still takes part in the warp's exchanges
+    uint32_t bs, g, b, s;
+    v.per_token.split(item, bs, g);
+    v.tokens.split(bs, b, s);
+    const bool which = g >= v.q_items;
+    const int h0 = (int)(which ? g - v.q_items : g) * HPT;
+    const int count = min(HPT, (which ? a.heads[1] : a.heads[0]) - h0);
     Unit u;
     u.place(a, v, lane);
-    const HeadsTensor tx = which ? a.x[1] : a.x[0], ty = which ? a.y[1] : a.y[0];
-    const T *x = static_cast<const T *>(tx.p) + heads_offset(tx, b, s, h0);
-    T *y = static_cast<T *>(const_cast<void *>(ty.p)) + heads_offset(ty, b, s, h0);
+    const T *const x = static_cast<const T *>(which ? v.x[1].p : v.x[0].p) +
+                       heads_near(which ? v.x[1] : v.x[0], b, s, h0);
+    const int xsh = which ? v.x[1].sh : v.x[0].sh;
     layer_pdl_wait();
+    const int64_t p = heads_position(a, b, s);
     uint4 x0[HPT], x1[HPT];
 #pragma unroll
-    for (int h = 0; h < HPT; ++h)
-        if (h < count) u.load(x + h * tx.sh, x0[h], x1[h]);
-        else x0[h] = x1[h] = make_uint4(0, 0, 0, 0);
-    const int64_t p = heads_position(a, b, s);
-    float2 c[N], sn[N], wa[N], wb[N];
-    u.angles(a, v, p < 0 ? 0 : p, c, sn);
-    if constexpr (MODE == HEADS_NORM) u.weights(a, v, which, wa, wb);
-    if (p < 0 && live && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+    for (int h = 0; h < HPT; ++h) u.load(x + (h < count ? (int64_t)h * xsh : 0), x0[h], x1[h]);
     float rstd[HPT];
     if constexpr (MODE == HEADS_NORM) {
         // the heads' sums cross the lanes together, so that their shuffles overlap
 #pragma unroll
         for (int h = 0; h < HPT; ++h) {
-            float2 va[N], vb[N], ss = both(0.0f);
+            float2 va[N], vb[N];
             Unit::open(x0[h], x1[h], va, vb);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                ss = __ffma2_rn(va[i], va[i], __ffma2_rn(vb[i], vb[i], ss));
-            rstd[h] = ss.x + ss.y;
+            rstd[h] = u.squares(va, vb);
             keep_packed(x0[h]);
             keep_packed(x1[h]);
         }
@@ -471,6 +499,25 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
 #pragma unroll
         for (int h = 0; h < HPT; ++h) rstd[h] = rsqrtf(fmaf(rstd[h], inv, a.eps));
     }
+    // a pair's factors: y_a = x_a ca + x_b nb, y_b = x_b cb + x_a sa: cos, sin and
+    // -sin, with a norm times the weights of the elements they meet
+    float2 ca[N], cb[N], sa[N], nb[N];
+    u.angles(a, v, p < 0 ? 0 : p, ca, sa, nb);
+    if constexpr (MODE == HEADS_NORM) {
+        float2 wa[N], wb[N];
+        u.weights(a, v, which, wa, wb);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            cb[i] = __fmul2_rn(ca[i], wb[i]);
+            ca[i] = __fmul2_rn(ca[i], wa[i]);
+            sa[i] = __fmul2_rn(sa[i], wa[i]);
+            nb[i] = __fmul2_rn(nb[i], wb[i]);
+        }
+    }
+    if (p < 0 && live && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+    T *const y = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p)) +
+                 heads_near(which ? v.y[1] : v.y[0], b, s, h0);
+    const int ysh = which ? v.y[1].sh : v.y[0].sh;
 #pragma unroll
     for (int h = 0; h < HPT; ++h) {
         float2 va[N], vb[N];
@@ -478,41 +525,59 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
         if constexpr (MODE == HEADS_NORM) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                va[i] = __fmul2_rn(va[i], __fmul2_rn(wa[i], both(rstd[h])));
-                vb[i] = __fmul2_rn(vb[i], __fmul2_rn(wb[i], both(rstd[h])));
+                va[i] = __fmul2_rn(va[i], both(rstd[h]));
+                vb[i] = __fmul2_rn(vb[i], both(rstd[h]));
             }
+            u.turn(va, vb, ca, sa, nb, cb);
+        } else {
+            u.turn(va, vb, ca, sa, nb, ca);
         }
-        u.turn(va, vb, c, sn);
         if (p < 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) va[i] = vb[i] = both(0.0f);
         }
-        if (h < count) u.store(y + h * ty.sh, va, vb);
+        if (live && h < count) u.store(y + (int64_t)h * ysh, va, vb);
     }
 }
 
-// The gradient of norm and rotation.  CTAs take items of q or of k only, in
+// The gradient of norm and rotation.  CTAs take rows of q or of k only, in
 // steps of their number, so a thread's weight-gradient sums stay in registers
-// to the end; the CTA's sums then join in shared memory and go to its row of
-// the workspace.
+// to the end; the next row's vectors and position are on their way while the
+// present row is worked on.  The CTA's sums then join in shared memory and go
+// to its row of the workspace.
 template <class T, bool IL>
-__global__ void __launch_bounds__(kHeadsThreads)
+__global__ void __launch_bounds__(kHeadsThreads, 2)
 k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     using Unit = HeadsUnit<T, IL>;
     constexpr int N = Unit::N;
     extern __shared__ float s_dw[];   // [groups of the CTA][dim]
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
-    const int which = (int)blockIdx.x >= v.ctas[0];
-    const int cta = (int)blockIdx.x - (which ? v.ctas[0] : 0);
-    const int heads = a.heads[which];
-    const HeadsTensor tx = which ? a.x[1] : a.x[0], tg = which ? a.dy[1] : a.dy[0],
-                      ty = which ? a.y[1] : a.y[0];
-    const int64_t total = a.rows * heads;
+    const bool which = (int)blockIdx.x >= v.ctas[0];
+    const uint32_t cta = blockIdx.x - (which ? v.ctas[0] : 0);
+    const uint32_t ctas = which ? v.ctas[1] : v.ctas[0];
+    const HeadsDiv heads = which ? v.heads[1] : v.heads[0];
+    const uint32_t total = (uint32_t)a.rows * heads.n;
     const int per = kHeadsThreads >> v.log_lanes, group = threadIdx.x >> v.log_lanes;
+    layer_pdl_launch();
     Unit u;
     u.place(a, v, lane);
-    layer_pdl_launch();
+    const T *const x = static_cast<const T *>(which ? v.x[1].p : v.x[0].p);
+    const T *const dy = static_cast<const T *>(which ? v.dy[1].p : v.dy[0].p);
+    T *const y = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p));
+    uint4 nx0, nx1, ng0, ng1;
+    int64_t np;
+    auto fetch = [&](uint32_t row) {   // a row past the end repeats row 0
+        uint32_t bs, h, b, s;
+        heads.split(row < total ? row : 0, bs, h);
+        v.tokens.split(bs, b, s);
+        np = heads_position(a, b, s);
+        u.load(x + heads_near(which ? v.x[1] : v.x[0], b, s, h), nx0, nx1);
+        u.load(dy + heads_near(which ? v.dy[1] : v.dy[0], b, s, h), ng0, ng1);
+    };
     layer_pdl_wait();
+    const uint32_t step = ctas * per;
+    uint32_t base = cta * per;
+    fetch(base + group);
     float2 wa[N], wb[N], da[N], db[N];
     u.weights(a, v, which, wa, wb);
 #pragma unroll
@@ -520,47 +585,40 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     bool bad = false;
     const float inv = 1.0f / (float)a.dim;
     // every lane of a warp makes the same number of steps: the exchanges are warp-wide
-    const int64_t step = (int64_t)v.ctas[which] * per;
-    for (int64_t base = (int64_t)cta * per; base < total; base += step) {
-        const int64_t row = base + group;
+    for (; base < total; base += step) {
+        const uint32_t row = base + group;
         const bool live = row < total;
-        int64_t bs, h, b, s;
-        heads_split(live ? row : 0, heads, v.wide, bs, h);
-        heads_split(bs, a.tokens, v.wide, b, s);
-        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, g0 = x0, g1 = x0;
-        if (live) {
-            u.load(static_cast<const T *>(tx.p) + heads_offset(tx, b, s, h), x0, x1);
-            u.load(static_cast<const T *>(tg.p) + heads_offset(tg, b, s, h), g0, g1);
+        const int64_t p = np;
+        float2 xa[N], xb[N], ga[N], gb[N];
+        Unit::open(ng0, ng1, ga, gb);
+        Unit::open(nx0, nx1, xa, xb);
+        {
+            float2 c[N], sn[N], n[N];
+            u.angles(a, v, p < 0 ? 0 : p, c, sn, n);
+            if (base + step < total) fetch(row + step);
+            u.turn(ga, gb, c, sn, n, c);
         }
-        const int64_t p = heads_position(a, b, s);
         const bool use = live && p >= 0;
         bad |= live && p < 0;
-        if (!use) x0 = x1 = g0 = g1 = make_uint4(0, 0, 0, 0);
-        float2 c[N], sn[N], xa[N], xb[N], ga[N], gb[N];
-        u.angles(a, v, p < 0 ? 0 : p, c, sn);
-        Unit::open(x0, x1, xa, xb);
-        Unit::open(g0, g1, ga, gb);
-        u.turn(ga, gb, c, sn);
-        float2 ss = both(0.0f), dot = both(0.0f);
+        float ss = u.squares(xa, xb);
+        // sum of g w x, the absent elements' weights being 0
+        float2 dot = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            ss = __ffma2_rn(xa[i], xa[i], __ffma2_rn(xb[i], xb[i], ss));
+        for (int i = 0; i < N; ++i)
             dot = __ffma2_rn(__fmul2_rn(ga[i], wa[i]), xa[i],
                              __ffma2_rn(__fmul2_rn(gb[i], wb[i]), xb[i], dot));
-        }
-        ss.x += ss.y;
-        ss.y = dot.x + dot.y;
+        float gx = dot.x + dot.y;
         for (int o = lanes >> 1; o > 0; o >>= 1) {
-            ss.x += __shfl_xor_sync(0xFFFFFFFFu, ss.x, o);
-            ss.y += __shfl_xor_sync(0xFFFFFFFFu, ss.y, o);
+            ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            gx += __shfl_xor_sync(0xFFFFFFFFu, gx, o);
         }
-        const float rstd = rsqrtf(fmaf(ss.x, inv, a.eps));
-        const float2 mean = both(-ss.y * rstd * inv), r2 = both(rstd);
+        const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
+        const float2 mean = both(-gx * rstd * inv), r2 = both(rstd);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             xa[i] = __fmul2_rn(xa[i], r2);
             xb[i] = __fmul2_rn(xb[i], r2);
-            if (use) {    // rstd may be infinite where nothing is used
+            if (use) {
                 da[i] = __ffma2_rn(ga[i], xa[i], da[i]);
                 db[i] = __ffma2_rn(gb[i], xb[i], db[i]);
             }
@@ -571,9 +629,12 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
 #pragma unroll
             for (int i = 0; i < N; ++i) ga[i] = gb[i] = both(0.0f);
         }
-        if (live)
-            u.store(static_cast<T *>(const_cast<void *>(ty.p)) + heads_offset(ty, b, s, h), ga,
-                    gb);
+        if (live) {
+            uint32_t bs, h, b, s;
+            heads.split(row, bs, h);
+            v.tokens.split(bs, b, s);
+            u.store(y + heads_near(which ? v.y[1] : v.y[0], b, s, h), ga, gb);
+        }
     }
     if (bad && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
 #pragma unroll
