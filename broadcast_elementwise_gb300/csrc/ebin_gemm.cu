@@ -116,20 +116,32 @@ struct Shape {
 };
 
 // Which tiles.  128-row tiles of B against 16 to 128 rows of A, each tile's k
-// cut in up to eight, while they fit the SMs once; 256 x 256 tiles on pairs of
-// CTAs beyond that, where operand traffic counts.
+// cut in up to eight, while they fit the SMs once; beyond that tiles of 256
+// rows of A on pairs of CTAs, where operand traffic counts, with the columns
+// (256, 224, 192 or 160) whose last wave of pairs wastes least: a wave costs
+// its columns and a fixed part.
 Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
     Shape s{};
     s.bn = at.m <= 16 ? 16 : at.m <= 32 ? 32 : at.m <= 64 ? 64 : 128;
     s.split = 1;
     const int64_t tiles = div_up(at.n, kTcRows) * div_up(at.m, s.bn);
+    const int64_t kblocks = div_up(at.k, kTcBK);
     if (tiles > sms && at.m > 64) {
         s.pair = true;
-        s.bn = 256;
+        int64_t least = 0;
+        for (int bn : {256, 224, 192, 160}) {
+            const int64_t waves = div_up(div_up(at.m, 2 * kTcRows) * div_up(at.n, bn), sms / 2);
+            const int64_t cost = waves * (bn + 16);
+            if (least == 0 || cost < least) {
+                least = cost;
+                s.bn = bn;
+            }
+        }
         return s;
     }
-    const int64_t kblocks = div_up(at.k, kTcBK);
-    while (s.split < 8 && tiles * s.split * 2 <= sms && kblocks >= s.split * 8) s.split *= 2;
+    // tiles of up to 64 columns run two to an SM
+    const int64_t room = s.bn <= 64 ? 2 * sms : sms;
+    while (s.split < 8 && tiles * s.split * 2 <= room && kblocks >= s.split * 8) s.split *= 2;
     return s;
 }
 

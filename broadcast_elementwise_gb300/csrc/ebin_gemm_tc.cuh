@@ -51,13 +51,13 @@ __device__ __forceinline__ void tc_bar_expect(uint32_t bar, uint32_t bytes) {
 }
 // arrive at a barrier of this cluster, by its cluster address
 __device__ __forceinline__ void tc_bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
 __device__ __forceinline__ bool tc_bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok)
                  : "r"(bar), "r"(parity)
@@ -92,6 +92,14 @@ __device__ __forceinline__ uint32_t tc_cluster_size() {
 __device__ __forceinline__ void tc_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool tc_elect() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(one));
+    return one != 0;
 }
 
 template <int CTAS>
@@ -219,6 +227,19 @@ template <class T> __device__ __forceinline__ uint4 tc_pack8(const float *v) {
                       tc_pack<T>(v[6], v[7]));
 }
 
+template <int ACT, int N> __device__ __forceinline__ void tc_act_all(float *v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_value<ACT>(v[i]);
+}
+template <int N> __device__ __forceinline__ void tc_act(int act, float *v) {
+    switch (act) {
+    case EBIN_ACT_RELU: tc_act_all<EBIN_ACT_RELU, N>(v); break;
+    case EBIN_ACT_GELU: tc_act_all<EBIN_ACT_GELU, N>(v); break;
+    case EBIN_ACT_GELU_TANH: tc_act_all<EBIN_ACT_GELU_TANH, N>(v); break;
+    case EBIN_ACT_SILU: tc_act_all<EBIN_ACT_SILU, N>(v); break;
+    }
+}
+
 // One element's epilogue where neighbouring lanes hold neighbouring n.
 template <class T>
 __device__ __forceinline__ void tc_store_one(const GemmEpilogue &e, int64_t m, int64_t n, float z,
@@ -226,12 +247,7 @@ __device__ __forceinline__ void tc_store_one(const GemmEpilogue &e, int64_t m, i
     z += bias;
     if (e.z) static_cast<T *>(e.z)[m * e.ldz + n] = from_f<T>(z);
     float y = z;
-    switch (e.act) {
-    case EBIN_ACT_RELU: y = act_value<EBIN_ACT_RELU>(z); break;
-    case EBIN_ACT_GELU: y = act_value<EBIN_ACT_GELU>(z); break;
-    case EBIN_ACT_GELU_TANH: y = act_value<EBIN_ACT_GELU_TANH>(z); break;
-    case EBIN_ACT_SILU: y = act_value<EBIN_ACT_SILU>(z); break;
-    }
+    tc_act<1>(e.act, &y);
     if (e.residual) y += to_f(static_cast<const T *>(e.residual)[m * e.ld_residual + n]);
     static_cast<T *>(e.y)[m * e.ldy + n] = from_f<T>(y);
 }
@@ -242,9 +258,33 @@ __device__ __forceinline__ float tc_bias(const GemmEpilogue &e, int64_t n) {
                       : to_f(static_cast<const T *>(e.bias)[n]);
 }
 
-template <int ACT> __device__ __forceinline__ void tc_act16(float *v) {
+// `most` of 16 neighbouring rows m of column n, where neighbouring lanes hold
+// neighbouring n.
+template <class T>
+__device__ __forceinline__ void tc_store_down(const GemmEpilogue &e, int64_t m, int64_t n,
+                                              float *v, int most, float bias) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
+    for (int i = 0; i < 16; ++i) v[i] += bias;
+    if (e.z) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < most) static_cast<T *>(e.z)[(m + i) * e.ldz + n] = from_f<T>(v[i]);
+    }
+    float r[16];
+    if (e.residual) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            r[i] = i < most ? to_f(static_cast<const T *>(e.residual)[(m + i) * e.ld_residual + n])
+                            : 0.0f;
+    }
+    tc_act<16>(e.act, v);
+    if (e.residual) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += r[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < most) static_cast<T *>(e.y)[(m + i) * e.ldy + n] = from_f<T>(v[i]);
 }
 
 // 16 neighbouring columns n of row m, all inside the output, vectors aligned.
@@ -282,12 +322,7 @@ __device__ __forceinline__ void tc_store16(const GemmEpilogue &e, int64_t m, int
         z[0] = tc_pack8<T>(v);
         z[1] = tc_pack8<T>(v + 8);
     }
-    switch (e.act) {
-    case EBIN_ACT_RELU: tc_act16<EBIN_ACT_RELU>(v); break;
-    case EBIN_ACT_GELU: tc_act16<EBIN_ACT_GELU>(v); break;
-    case EBIN_ACT_GELU_TANH: tc_act16<EBIN_ACT_GELU_TANH>(v); break;
-    case EBIN_ACT_SILU: tc_act16<EBIN_ACT_SILU>(v); break;
-    }
+    tc_act<16>(e.act, v);
     if (e.residual) {
         float f[16];
         tc_unpack8<T>(r0, f);
@@ -301,18 +336,22 @@ __device__ __forceinline__ void tc_store16(const GemmEpilogue &e, int64_t m, int
 }
 
 // What a kernel's shared memory holds, in bytes.
-template <int CTAS, int BN> struct TcLayout {
+template <int CTAS, int BN, bool SPLIT> struct TcLayout {
     static constexpr int kP = kTcRows * 128;
-    static constexpr int kQRows = BN / CTAS < 64 ? 64 : BN / CTAS;
+    static constexpr int kQRows = (BN / CTAS + 63) / 64 * 64;
     static constexpr int kQ = kQRows * 128;
     static constexpr int kStage = kP + kQ;
-    static constexpr int kEpilogueWarps = 4;
-    static constexpr int kScratch = kEpilogueWarps * 32 * 17 * 4;   // a warp's 32 x 16 transpose
+    static constexpr int kEpilogueWarps = SPLIT ? 4 : 8;
+    static constexpr int kScratch = SPLIT ? 0 : kEpilogueWarps * 32 * 17 * 4;   // 32 x 16 transposes
     static constexpr int kBarriers = 512;
-    static constexpr int kStages =
-        (kTcSmem - 1024 - kScratch - kBarriers) / kStage > 8
-            ? 8 : (kTcSmem - 1024 - kScratch - kBarriers) / kStage;
-    static constexpr int kColumns = 2 * BN < 32 ? 32 : 2 * BN;      // two accumulators
+    // split tiles of few columns leave room for a second CTA on the SM, whose
+    // set-up and first copies overlap this one's end
+    static constexpr int kRoom =
+        (SPLIT && BN <= 64 ? (kTcSmem - 1024) / 2 : kTcSmem) - 1024 - kScratch - kBarriers;
+    static constexpr int kStages = kRoom / kStage;
+    static constexpr int kAccumulators = SPLIT ? 1 : 2;
+    static constexpr int kAccStep = BN <= 32 ? 32 : BN <= 64 ? 64 : BN <= 128 ? 128 : 256;
+    static constexpr int kColumns = kAccumulators * kAccStep;
     static constexpr int kBytes = 1024 + kStages * kStage + kScratch + kBarriers;
     static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 };
@@ -323,10 +362,10 @@ template <int CTAS, int BN> struct TcLayout {
 // SPLIT: the CTAs of a cluster share one tile's k and join their sums through
 // each other's shared memory, in rank order; P = B, Q = A.
 template <class T, int CTAS, int BN, bool SPLIT>
-__global__ void __launch_bounds__(TcLayout<CTAS, BN>::kThreads, 1)
+__global__ void __launch_bounds__(TcLayout<CTAS, BN, SPLIT>::kThreads, 1)
 k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
           const TcArgs a) {
-    using L = TcLayout<CTAS, BN>;
+    using L = TcLayout<CTAS, BN, SPLIT>;
     static_assert(!SPLIT || CTAS == 1, "a split tile is a single CTA's");
     extern __shared__ uint8_t s_raw[];
     const uint32_t base = (tc_smem(s_raw) + 1023) & ~1023u;
@@ -339,7 +378,8 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     auto tempty = [&](int i) { return bars + 8 * (2 * L::kStages + 2 + i); };
     const uint32_t drain = bars + 8 * (2 * L::kStages + 4);
     const uint32_t s_tmem = drain + 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // uniform in the warp, so that what follows from it can stay in uniform registers
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = tc_cluster_rank(), ranks = tc_cluster_size();
     const bool leader = CTAS == 1 || rank == 0;
 
@@ -379,49 +419,60 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     };
     bool ok = true;
 
-    if (warp == 0 && lane == 0) {
-        int it = 0;
+    if (warp == 0) {
+        // the whole warp walks the loop (its values stay uniform), one lane issues
+        const bool one = tc_elect();
+        const uint32_t q_bytes = a.q_mn ? L::kQ : a.q_box * 128;
+        int s = 0, it = 0;
+        uint32_t phase = 1;
         for (int t = cluster; t < tiles && ok; t += clusters) {
             int p, q;
             place(t, p, q);
             const int pr = (p * CTAS + (CTAS == 2 ? (int)rank : 0)) * kTcRows;
             const int qr = q * BN + (CTAS == 2 ? (int)rank * (BN / 2) : 0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % L::kStages;
-                if (!tc_bar_wait(empty(s), (it / L::kStages & 1) ^ 1, a.limit)) {
+                if (!tc_bar_wait(empty(s), phase, a.limit)) {
                     ok = false;
                     break;
                 }
-                const uint32_t sp = base + s * L::kStage, sq = sp + L::kP;
-                const uint32_t q_bytes = a.q_mn ? L::kQ : a.q_box * 128;
-                const uint32_t bar = CTAS == 2 ? tc_map(full(s), 0) : full(s);
-                if (leader) tc_bar_expect(full(s), CTAS * (L::kP + q_bytes));
-                if (a.p_mn) {
-                    tc_copy<CTAS>(sp, &p_map, pr, kb * kTcBK, bar);
-                    tc_copy<CTAS>(sp + 8192, &p_map, pr + 64, kb * kTcBK, bar);
-                } else {
-                    tc_copy<CTAS>(sp, &p_map, kb * kTcBK, pr, bar);
-                }
-                if (a.q_mn) {
+                if (one) {
+                    const uint32_t sp = base + s * L::kStage, sq = sp + L::kP;
+                    const uint32_t bar = CTAS == 2 ? tc_map(full(s), 0) : full(s);
+                    if (leader) tc_bar_expect(full(s), CTAS * (L::kP + q_bytes));
+                    if (a.p_mn) {
+                        tc_copy<CTAS>(sp, &p_map, pr, kb * kTcBK, bar);
+                        tc_copy<CTAS>(sp + 8192, &p_map, pr + 64, kb * kTcBK, bar);
+                    } else {
+                        tc_copy<CTAS>(sp, &p_map, kb * kTcBK, pr, bar);
+                    }
+                    if (a.q_mn) {
 #pragma unroll
-                    for (int i = 0; i < L::kQRows / 64; ++i)
-                        tc_copy<CTAS>(sq + 8192 * i, &q_map, qr + 64 * i, kb * kTcBK, bar);
-                } else {
-                    tc_copy<CTAS>(sq, &q_map, kb * kTcBK, qr, bar);
+                        for (int i = 0; i < L::kQRows / 64; ++i)
+                            tc_copy<CTAS>(sq + 8192 * i, &q_map, qr + 64 * i, kb * kTcBK, bar);
+                    } else {
+                        tc_copy<CTAS>(sq, &q_map, kb * kTcBK, qr, bar);
+                    }
+                }
+                if (++s == L::kStages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
         }
         if (!ok && leader)   // wait for what is in flight
             for (int j = max(0, it - L::kStages); j < it; ++j)
                 tc_bar_wait(full(j % L::kStages), j / L::kStages & 1, a.limit);
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // f32 accumulators; operands f16 or bf16, their major directions; N / 8, M / 16
         constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
         const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a.p_mn << 15) |
                                ((uint32_t)a.q_mn << 16) | ((uint32_t)(BN / 8) << 17) |
                                ((uint32_t)(CTAS * kTcRows / 16) << 24);
         const uint32_t p_step = a.p_mn ? 2048 >> 4 : 32 >> 4, q_step = a.q_mn ? 2048 >> 4 : 32 >> 4;
-        int it = 0, n = 0;
+        const uint64_t p_desc = tc_desc(base, a.p_mn), q_desc = tc_desc(base + L::kP, a.q_mn);
+        const bool one = tc_elect();
+        int s = 0, n = 0;
+        uint32_t phase = 0;
         for (int t = cluster; t < tiles && ok; t += clusters, ++n) {
             const int acc = n & 1;
             if (!tc_bar_wait(tempty(acc), (n >> 1 & 1) ^ 1, a.limit)) {
@@ -429,32 +480,40 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                 break;
             }
             tc_fence_after();
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % L::kStages;
-                if (!tc_bar_wait(full(s), it / L::kStages & 1, a.limit)) {
+            const uint32_t d = tmem + acc * L::kAccStep;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!tc_bar_wait(full(s), phase, a.limit)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t sp = base + s * L::kStage;
-                uint64_t pd = tc_desc(sp, a.p_mn), qd = tc_desc(sp + L::kP, a.q_mn);
+                if (one) {
+                    // addresses stay below 2^18: no carry leaves the descriptor's field
+                    uint64_t pd = p_desc + (uint32_t)(s * (L::kStage >> 4));
+                    uint64_t qd = q_desc + (uint32_t)(s * (L::kStage >> 4));
 #pragma unroll
-                for (int k = 0; k < kTcBK / 16; ++k) {
-                    tc_mma<CTAS>(tmem + acc * BN, pd, qd, idesc, kb > kb0 || k > 0);
-                    pd += p_step;
-                    qd += q_step;
+                    for (int k = 0; k < kTcBK / 16; ++k) {
+                        tc_mma<CTAS>(d, pd, qd, idesc, kb > kb0 || k > 0);
+                        pd += p_step;
+                        qd += q_step;
+                    }
+                    tc_commit<CTAS>(empty(s));
                 }
-                tc_commit<CTAS>(empty(s));
+                if (++s == L::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
-            if (ok) tc_commit<CTAS>(tfull(acc));
+            if (ok && one) tc_commit<CTAS>(tfull(acc));
         }
         if (!ok) {   // wait for the products in flight
-            tc_commit<CTAS>(drain);
+            if (one) tc_commit<CTAS>(drain);
             tc_bar_wait(drain, 0, a.limit);
         }
     } else if (warp >= 4 && !SPLIT) {
-        const int quarter = warp & 3;   // a warp reads its own quarter of the lanes
-        float *const s_t = reinterpret_cast<float *>(s_base + (scratch - base)) + quarter * 32 * 17;
+        // a warp reads its own quarter of the lanes; two warps share a quarter's columns
+        const int quarter = warp & 3, side = (warp - 4) >> 2;
+        float *const s_t = reinterpret_cast<float *>(s_base + (scratch - base)) +
+                           (warp - 4) * 32 * 17;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         int n = 0;
         for (int t = cluster; t < tiles && ok; t += clusters, ++n) {
@@ -469,10 +528,10 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                                  quarter * 32;
             const int64_t col0 = (int64_t)q * BN;
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
+            for (int c = 16 * side; c < BN; c += 32) {
                 if (row0 >= a.m || col0 + c >= a.n) break;
                 float v[16];
-                tc_load16(lanes + acc * BN + c, v);
+                tc_load16(lanes + acc * L::kAccStep + c, v);
                 if (kb1 == kb0) {   // no k: nothing was summed
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = 0.0f;
@@ -501,51 +560,65 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     }
 
     if constexpr (SPLIT) {
+        // P is B: lanes are n, columns are m
+        int p, q;
+        place(cluster, p, q);
+        const int64_t row0 = (int64_t)p * kTcRows, col0 = (int64_t)q * BN;
+        const int quarter = warp & 3;
         // the stages are free once the products are done: they hold this CTA's sums, [BN][128]
         float *const part = reinterpret_cast<float *>(s_base);
-        const int quarter = warp & 3;
         if (warp >= 4) {
             ok = tc_bar_wait(tfull(0), 0, a.limit);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
             const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+            const int64_t n = row0 + quarter * 32 + lane;
+            const float bias = ranks == 1 && n < a.n ? tc_bias<T>(a.e, n) : 0.0f;
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
+            for (int c = 0; c < BN && col0 + c < a.m; c += 16) {
                 float v[16];
-                if (ok && kb1 > kb0) {
-                    tc_load16(lanes + c, v);
-                } else {
+                tc_load16(lanes + c, v);
+                if (!ok || kb1 == kb0) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = 0.0f;
                 }
+                if (ranks > 1) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) part[(c + i) * kTcRows + quarter * 32 + lane] = v[i];
+                    for (int i = 0; i < 16; ++i)
+                        part[(c + i) * kTcRows + quarter * 32 + lane] = v[i];
+                } else if (n < a.n) {
+                    const int most = (int)min((int64_t)16, a.m - col0 - c);
+                    tc_store_down<T>(a.e, col0 + c, n, v, most, bias);
+                }
             }
             tc_fence_before();
         }
-        __syncwarp();
-        __syncthreads();
-        tc_cluster_sync();
-        int p, q;
-        place(cluster, p, q);
-        // P is B: lanes are n, columns are m; this CTA joins every ranks-th column
-        const int64_t row = (int64_t)p * kTcRows + (threadIdx.x & 127);
-        const int64_t col0 = (int64_t)q * BN;
-        const int first = (threadIdx.x >> 7) * (int)ranks + (int)rank;
-        if (row < a.n) {
-            const float bias = tc_bias<T>(a.e, row);
-            const uint32_t mine = base + 4 * (threadIdx.x & 127);
-            for (int c = first; c < BN && col0 + c < a.m; c += (L::kThreads >> 7) * (int)ranks) {
-                float z = 0.0f;
-                for (uint32_t r = 0; r < ranks; ++r) {
-                    float v;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(v)
-                                 : "r"(tc_map(mine + 4 * kTcRows * c, r))
-                                 : "memory");
-                    z += v;
+        if (ranks > 1) {
+            __syncwarp();
+            __syncthreads();
+            tc_cluster_sync();
+            // this CTA joins every ranks-th column, in rank order
+            const int64_t n = row0 + (threadIdx.x & 127);
+            const int first = (threadIdx.x >> 7) * (int)ranks + (int)rank;
+            if (n < a.n) {
+                const float bias = tc_bias<T>(a.e, n);
+                const uint32_t mine = base + 4 * (threadIdx.x & 127);
+                for (int c = first; c < BN && col0 + c < a.m; c += (L::kThreads >> 7) * (int)ranks) {
+                    float v[8];
+#pragma unroll
+                    for (uint32_t r = 0; r < 8; ++r) {
+                        v[r] = 0.0f;
+                        if (r < ranks)
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                         : "=f"(v[r])
+                                         : "r"(tc_map(mine + 4 * kTcRows * c, r))
+                                         : "memory");
+                    }
+                    float z = v[0];
+#pragma unroll
+                    for (int r = 1; r < 8; ++r) z += v[r];
+                    tc_store_one<T>(a.e, col0 + c, n, z, bias);
                 }
-                tc_store_one<T>(a.e, col0 + c, row, z, bias);
             }
         }
     }
