@@ -24,21 +24,27 @@ template <int ACT> __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
-// The derivative, in full binary32 accuracy: it may be kept in 32 bits.
-template <int ACT> __device__ __forceinline__ float act_slope(float z) {
+// The derivative.  FAST: with the fast forms of exp and the quotient, for
+// 16-bit data; otherwise with the full ones (the result is kept in 32 bits).
+template <bool FAST> __device__ __forceinline__ float act_exp(float x) {
+    return FAST ? __expf(x) : expf(x);
+}
+template <bool FAST> __device__ __forceinline__ float act_over(float x) {
+    return FAST ? __fdividef(1.0f, x) : 1.0f / x;
+}
+template <int ACT, bool FAST> __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == EBIN_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     if constexpr (ACT == EBIN_ACT_GELU)
-        return fmaf(z * 0.398942280401f, expf(-0.5f * z * z),
+        return fmaf(z * 0.398942280401f, act_exp<FAST>(-0.5f * z * z),
                     0.5f * (1.0f + erff(z * 0.707106781187f)));
     if constexpr (ACT == EBIN_ACT_GELU_TANH) {
-        // past |u| = 2^7 the sigmoid is flat; the polynomial would be inf * 0
-        const float s = 1.0f / (1.0f + expf(-act_tanh_arg(z)));
+        const float s = act_over<FAST>(1.0f + act_exp<FAST>(-act_tanh_arg(z)));
         const float du = fmaf(z * z, 0.214064448818f, 1.59576912161f);
         const float t = s * (1.0f - s);
-        return t == 0.0f ? s : fmaf(z * t, du, s);
+        return t == 0.0f ? s : fmaf(z * t, du, s);   // flat far out, where z du may be infinite
     }
     if constexpr (ACT == EBIN_ACT_SILU) {
-        const float s = 1.0f / (1.0f + expf(-z));
+        const float s = act_over<FAST>(1.0f + act_exp<FAST>(-z));
         const float t = s * (1.0f - s);
         return t == 0.0f ? s : fmaf(z, t, s);
     }

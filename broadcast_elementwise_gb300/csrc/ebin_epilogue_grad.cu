@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kEgThreads) k_epilogue_grad(const EgArgs a) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         float d = to_f(g[k].v[i]);
-                        if constexpr (ACT != EBIN_ACT_NONE) d *= act_slope<ACT>(to_f(x[k].v[i]));
+                        if constexpr (ACT != EBIN_ACT_NONE) d *= act_slope<ACT, sizeof(T) == 2>(to_f(x[k].v[i]));
                         sum[i] += d;
                         out.v[i] = from_f<T>(d);
                     }

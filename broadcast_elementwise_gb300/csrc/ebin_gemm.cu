@@ -20,9 +20,15 @@ namespace ebin {
 EBIN_DECLARE_TC(launch_tc_f16)
 EBIN_DECLARE_TC(launch_tc_bf16)
 #undef EBIN_DECLARE_TC
+// Clusters of so many CTAs of the split kernel that the current device holds at once.
+int tc_clusters_f16(int bn, int cluster);
+int tc_clusters_bf16(int bn, int cluster);
 
-// Lay a matrix of 16-bit elements out anew, its rows on 16-byte boundaries:
-// a thread gathers eight elements and stores them as one vector.
+// Lay a matrix of 16-bit elements out anew, its rows on 16-byte boundaries.  A
+// thread makes one vector of eight elements: from the two aligned vectors that
+// hold them, shifted by the row's offset, or, where those reach past the
+// matrix, element by element.  (Gathering every element alone took 12 us for
+// [1021, 2049] and [1543, 2049] together, bound by its load instructions.)
 struct RepackArgs {
     const uint16_t *src;
     uint4 *dst;
@@ -31,21 +37,46 @@ struct RepackArgs {
 
 __global__ void __launch_bounds__(256) k_repack(const RepackArgs a, const RepackArgs b) {
     layer_pdl_launch();
-    layer_pdl_wait();
     const RepackArgs &r = blockIdx.y ? b : a;
-    const int64_t total = r.rows * r.units;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / r.units, c = (i - row * r.units) * 8;
+    const uintptr_t first = (uintptr_t)r.src;
+    const uintptr_t last = first + 2 * (uintptr_t)((r.rows - 1) * r.ld + r.cols);
+    layer_pdl_wait();
+    const int64_t row = blockIdx.x;
+    for (int64_t u = threadIdx.x; u < r.units && row < r.rows; u += 256) {
+        const int64_t c = u * 8;
         const uint16_t *x = r.src + row * r.ld + c;
-        uint32_t w[4];
+        const uintptr_t at = (uintptr_t)x, low = at & ~(uintptr_t)15;
+        const uint32_t shift = (uint32_t)(at & 15);
+        uint4 out;
+        if (c + 8 <= r.cols && low >= first && low + (shift ? 32 : 16) <= last) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(low));
+            uint4 n = make_uint4(0, 0, 0, 0);
+            if (shift) n = __ldg(reinterpret_cast<const uint4 *>(low) + 1);
+            uint32_t w[8] = {v.x, v.y, v.z, v.w, n.x, n.y, n.z, n.w};
+            if (shift & 8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = c + 2 * j < r.cols ? x[2 * j] : 0u;
-            const uint32_t hi = c + 2 * j + 1 < r.cols ? x[2 * j + 1] : 0u;
-            w[j] = lo | hi << 16;
+                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+            }
+            if (shift & 4) {
+#pragma unroll
+                for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+            }
+            if (shift & 2) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+            }
+            out = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = c + 2 * j < r.cols ? x[2 * j] : 0u;
+                const uint32_t hi = c + 2 * j + 1 < r.cols ? x[2 * j + 1] : 0u;
+                w[j] = lo | hi << 16;
+            }
+            out = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        r.dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        r.dst[row * r.units + u] = out;
     }
 }
 
@@ -116,11 +147,13 @@ struct Shape {
 };
 
 // Which tiles.  128-row tiles of B against 16 to 128 rows of A, each tile's k
-// cut in up to eight, while they fit the SMs once; beyond that tiles of 256
+// cut in up to eight while all clusters fit at once (a second wave of few costs
+// more than the longer sums); beyond that tiles of 256
 // rows of A on pairs of CTAs, where operand traffic counts, with the columns
 // (256, 224, 192 or 160) whose last wave of pairs wastes least: a wave costs
 // its columns and a fixed part.
 Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
+    const bool bf16 = at.dtype == EBIN_BFLOAT16;
     Shape s{};
     s.bn = at.m <= 16 ? 16 : at.m <= 32 ? 32 : at.m <= 64 ? 64 : 128;
     s.split = 1;
@@ -139,9 +172,9 @@ Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
         }
         return s;
     }
-    // tiles of up to 64 columns run two to an SM
-    const int64_t room = s.bn <= 64 ? 2 * sms : sms;
-    while (s.split < 8 && tiles * s.split * 2 <= room && kblocks >= s.split * 8) s.split *= 2;
+    while (s.split < 8 && kblocks >= s.split * 8 &&
+           tiles <= (bf16 ? tc_clusters_bf16 : tc_clusters_f16)(s.bn, s.split * 2))
+        s.split *= 2;
     return s;
 }
 
@@ -162,13 +195,12 @@ cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
             r[count++] = RepackArgs{static_cast<const uint16_t *>(o->p),
                                     reinterpret_cast<uint4 *>(dst), o->rows, o->cols, o->ld,
                                     units};
-            most = std::max(most, o->rows * units);
+            most = std::max(most, o->rows);
             o->p = dst;
             o->ld = units * 8;
         }
         if (count > 0) {
-            const int64_t grid = std::min<int64_t>(div_up(most, 256), 16ll * current_sm_count());
-            const cudaError_t st = launch_layer(k_repack, dim3((unsigned)grid, (unsigned)count),
+            const cudaError_t st = launch_layer(k_repack, dim3((unsigned)most, (unsigned)count),
                                                 256, 0, s, 1, r[0], r[count - 1]);
             if (st != cudaSuccess) return st;
         }
@@ -191,6 +223,9 @@ cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
     auto aligned = [&](const void *x, int64_t ld) { return (uintptr_t)x % 16 == 0 && ld % 8 == 0; };
     t.vec = aligned(e.y, e.ldy) && aligned(e.z, e.z ? e.ldz : 0) &&
             aligned(e.residual, e.residual ? e.ld_residual : 0) && (uintptr_t)e.bias % 16 == 0;
+    if (t.vec && ((uintptr_t)e.y | (uintptr_t)e.z | (uintptr_t)e.residual) % 32 == 0 &&
+        (e.ldy | (e.z ? e.ldz : 0) | (e.residual ? e.ld_residual : 0)) % 16 == 0)
+        t.vec = 2;
     // two seconds, and the time that a long sum may take
     t.limit = 4000000000ll + 100000ll * t.kblocks;
     t.status = stream_status_word(s);

@@ -7,21 +7,63 @@ namespace ebin {
 #if EBIN_DT == 1
 using GemmT = __half;
 #define EBIN_GEMM_NAME launch_tc_f16
+#define EBIN_GEMM_CLUSTERS tc_clusters_f16
 #else
 using GemmT = __nv_bfloat16;
 #define EBIN_GEMM_NAME launch_tc_bf16
+#define EBIN_GEMM_CLUSTERS tc_clusters_bf16
 #endif
+
+template <int CTAS, int BN, bool SPLIT> static cudaError_t opt_in() {
+    using L = TcLayout<CTAS, BN, SPLIT>;
+    static_assert(L::kBytes <= kTcSmem, "shared memory of a CTA");
+    static const cudaError_t opted = cudaFuncSetAttribute(
+        k_gemm_tc<GemmT, CTAS, BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    return opted;
+}
 
 template <int CTAS, int BN, bool SPLIT>
 static cudaError_t run(const CUtensorMap &p, const CUtensorMap &q, const TcArgs &a, int grid,
                        int cluster, cudaStream_t s) {
     using L = TcLayout<CTAS, BN, SPLIT>;
-    static_assert(L::kBytes <= kTcSmem, "shared memory of a CTA");
-    static const cudaError_t opted = cudaFuncSetAttribute(
-        k_gemm_tc<GemmT, CTAS, BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    const cudaError_t opted = opt_in<CTAS, BN, SPLIT>();
     if (opted != cudaSuccess) return opted;
     return launch_layer(k_gemm_tc<GemmT, CTAS, BN, SPLIT>, dim3((unsigned)grid), L::kThreads,
                         L::kBytes, s, cluster, p, q, a);
+}
+
+template <int BN, int CLUSTER> static int clusters() {
+    using L = TcLayout<1, BN, true>;
+    static const int held = [] {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(CLUSTER);
+        cfg.blockDim = dim3(L::kThreads);
+        cfg.dynamicSmemBytes = L::kBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = CLUSTER;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (opt_in<1, BN, true>() != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k_gemm_tc<GemmT, 1, BN, true>, &cfg) !=
+                cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        return n;
+    }();
+    return held;
+}
+template <int BN> static int clusters_of(int cluster) {
+    return cluster == 2 ? clusters<BN, 2>() : cluster == 4 ? clusters<BN, 4>() : clusters<BN, 8>();
+}
+
+int EBIN_GEMM_CLUSTERS(int bn, int cluster) {
+    return bn == 16 ? clusters_of<16>(cluster) : bn == 32 ? clusters_of<32>(cluster)
+         : bn == 64 ? clusters_of<64>(cluster) : clusters_of<128>(cluster);
 }
 
 // bn: the accumulator columns of a tile; grid CTAs in clusters.

@@ -34,7 +34,7 @@ struct TcArgs {
     int32_t p_tiles, q_tiles;   // tiles of P's rows (kTcRows * CTAs) and of Q's (BN)
     int32_t p_mn, q_mn;         // the operand is dense across k
     int32_t q_box;              // Q's rows a copy brings when it is dense along k
-    int32_t vec;                // y, z, residual and the bias take 16-byte accesses
+    int32_t vec;                // y, z, residual (and the bias) take 16-byte (1) or 32-byte (2) accesses
     long long limit;            // clocks of a wait
     uint32_t *status;
 };
@@ -287,16 +287,36 @@ __device__ __forceinline__ void tc_store_down(const GemmEpilogue &e, int64_t m, 
         if (i < most) static_cast<T *>(e.y)[(m + i) * e.ldy + n] = from_f<T>(v[i]);
 }
 
+// 32 bytes: in one access (a whole sector a lane) or in two.
+template <bool WIDE> __device__ __forceinline__ void tc_put32(void *p, const uint4 &a, const uint4 &b) {
+    if constexpr (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+                     "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = a;
+        static_cast<uint4 *>(p)[1] = b;
+    }
+}
+template <bool WIDE> __device__ __forceinline__ void tc_get32(const void *p, uint4 &a, uint4 &b) {
+    if constexpr (WIDE) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                       "=r"(b.w)
+                     : "l"(p)
+                     : "memory");
+    } else {
+        a = static_cast<const uint4 *>(p)[0];
+        b = static_cast<const uint4 *>(p)[1];
+    }
+}
+
 // 16 neighbouring columns n of row m, all inside the output, vectors aligned.
-template <class T>
+template <class T, bool WIDE>
 __device__ __forceinline__ void tc_store16(const GemmEpilogue &e, int64_t m, int64_t n, float *v) {
     uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-    if (e.residual) {
-        const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(e.residual) +
-                                                         m * e.ld_residual + n);
-        r0 = r[0];
-        r1 = r[1];
-    }
+    if (e.residual)
+        tc_get32<WIDE>(static_cast<const T *>(e.residual) + m * e.ld_residual + n, r0, r1);
     if (e.bias) {
         if (e.bias_f32) {
             const float4 *b = reinterpret_cast<const float4 *>(static_cast<const float *>(e.bias) + n);
@@ -317,11 +337,8 @@ __device__ __forceinline__ void tc_store16(const GemmEpilogue &e, int64_t m, int
             for (int i = 0; i < 16; ++i) v[i] += f[i];
         }
     }
-    if (e.z) {
-        uint4 *z = reinterpret_cast<uint4 *>(static_cast<T *>(e.z) + m * e.ldz + n);
-        z[0] = tc_pack8<T>(v);
-        z[1] = tc_pack8<T>(v + 8);
-    }
+    if (e.z)
+        tc_put32<WIDE>(static_cast<T *>(e.z) + m * e.ldz + n, tc_pack8<T>(v), tc_pack8<T>(v + 8));
     tc_act<16>(e.act, v);
     if (e.residual) {
         float f[16];
@@ -330,9 +347,7 @@ __device__ __forceinline__ void tc_store16(const GemmEpilogue &e, int64_t m, int
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] += f[i];
     }
-    uint4 *y = reinterpret_cast<uint4 *>(static_cast<T *>(e.y) + m * e.ldy + n);
-    y[0] = tc_pack8<T>(v);
-    y[1] = tc_pack8<T>(v + 8);
+    tc_put32<WIDE>(static_cast<T *>(e.y) + m * e.ldy + n, tc_pack8<T>(v), tc_pack8<T>(v + 8));
 }
 
 // What a kernel's shared memory holds, in bytes.
@@ -537,7 +552,10 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                     for (int i = 0; i < 16; ++i) v[i] = 0.0f;
                 }
                 if (a.vec && col0 + c + 16 <= a.n) {
-                    if (row0 + lane < a.m) tc_store16<T>(a.e, row0 + lane, col0 + c, v);
+                    if (row0 + lane < a.m) {
+                        if (a.vec == 2) tc_store16<T, true>(a.e, row0 + lane, col0 + c, v);
+                        else tc_store16<T, false>(a.e, row0 + lane, col0 + c, v);
+                    }
                 } else {
                     // off alignment or at the edge: through shared memory, so that
                     // neighbouring lanes store neighbouring columns
