@@ -16,7 +16,7 @@ namespace ebin {
 
 #define EBIN_DECLARE_TC(name)                                                             \
     cudaError_t name(const CUtensorMap &, const CUtensorMap &, const TcArgs &, int bn,    \
-                     int grid, int cluster, cudaStream_t);
+                     bool pair, int grid, int cluster, cudaStream_t);
 EBIN_DECLARE_TC(launch_tc_f16)
 EBIN_DECLARE_TC(launch_tc_bf16)
 #undef EBIN_DECLARE_TC
@@ -35,48 +35,58 @@ struct RepackArgs {
     int64_t rows, cols, ld, units;   // units: vectors of a row of dst
 };
 
+__device__ __forceinline__ uint4 repack_unit(const RepackArgs &r, int64_t row, int64_t c) {
+    const uintptr_t first = (uintptr_t)r.src;
+    const uintptr_t last = first + 2 * (uintptr_t)((r.rows - 1) * r.ld + r.cols);
+    const uint16_t *x = r.src + row * r.ld + c;
+    const uintptr_t at = (uintptr_t)x, low = at & ~(uintptr_t)15;
+    const uint32_t shift = (uint32_t)(at & 15);
+    if (c + 8 <= r.cols && low >= first && low + (shift ? 32 : 16) <= last) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(low));
+        uint4 n = make_uint4(0, 0, 0, 0);
+        if (shift) n = __ldg(reinterpret_cast<const uint4 *>(low) + 1);
+        uint32_t w[8] = {v.x, v.y, v.z, v.w, n.x, n.y, n.z, n.w};
+        if (shift & 8) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (shift & 4) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        if (shift & 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = c + 2 * j < r.cols ? x[2 * j] : 0u;
+        const uint32_t hi = c + 2 * j + 1 < r.cols ? x[2 * j + 1] : 0u;
+        w[j] = lo | hi << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A warp takes a run of a row's vectors, two a lane.
 __global__ void __launch_bounds__(256) k_repack(const RepackArgs a, const RepackArgs b) {
     layer_pdl_launch();
     const RepackArgs &r = blockIdx.y ? b : a;
-    const uintptr_t first = (uintptr_t)r.src;
-    const uintptr_t last = first + 2 * (uintptr_t)((r.rows - 1) * r.ld + r.cols);
+    const int lane = threadIdx.x & 31;
+    const int64_t runs = (r.units + 63) / 64, total = r.rows * runs;   // runs of 64 vectors
     layer_pdl_wait();
-    const int64_t row = blockIdx.x;
-    for (int64_t u = threadIdx.x; u < r.units && row < r.rows; u += 256) {
-        const int64_t c = u * 8;
-        const uint16_t *x = r.src + row * r.ld + c;
-        const uintptr_t at = (uintptr_t)x, low = at & ~(uintptr_t)15;
-        const uint32_t shift = (uint32_t)(at & 15);
-        uint4 out;
-        if (c + 8 <= r.cols && low >= first && low + (shift ? 32 : 16) <= last) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(low));
-            uint4 n = make_uint4(0, 0, 0, 0);
-            if (shift) n = __ldg(reinterpret_cast<const uint4 *>(low) + 1);
-            uint32_t w[8] = {v.x, v.y, v.z, v.w, n.x, n.y, n.z, n.w};
-            if (shift & 8) {
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total;
+         i += (int64_t)gridDim.x * 8) {
+        const int64_t row = i / runs, u = (i - row * runs) * 64 + lane;
+        uint4 x[2];
 #pragma unroll
-                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-            }
-            if (shift & 4) {
+        for (int k = 0; k < 2; ++k)
+            if (u + 32 * k < r.units) x[k] = repack_unit(r, row, (u + 32 * k) * 8);
 #pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-            }
-            if (shift & 2) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-            }
-            out = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t lo = c + 2 * j < r.cols ? x[2 * j] : 0u;
-                const uint32_t hi = c + 2 * j + 1 < r.cols ? x[2 * j + 1] : 0u;
-                w[j] = lo | hi << 16;
-            }
-            out = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        r.dst[row * r.units + u] = out;
+        for (int k = 0; k < 2; ++k)
+            if (u + 32 * k < r.units) r.dst[row * r.units + u + 32 * k] = x[k];
     }
 }
 
@@ -146,36 +156,49 @@ struct Shape {
     bool pair;     // 256 x 256 tiles on pairs of CTAs, P = A; else P = B on single CTAs
 };
 
-// Which tiles.  128-row tiles of B against 16 to 128 rows of A, each tile's k
-// cut in up to eight while all clusters fit at once (a second wave of few costs
-// more than the longer sums); beyond that tiles of 256
-// rows of A on pairs of CTAs, where operand traffic counts, with the columns
-// (256, 224, 192 or 160) whose last wave of pairs wastes least: a wave costs
-// its columns and a fixed part.
+// Which tiles: the least of an estimate in nanoseconds.  A step of k takes a
+// CTA its matrix instructions or its copies, whichever is longer (on a pair
+// 1.05 ns a column; copies at 190 bytes a ns); a tile's end costs 12 ns a column
+// once, the sums of split tiles 1.5 us more.
+//   pair   256 rows of A by 64 to 256 columns, a CTA pair each, waves of pairs
+//   split  128 columns of B by 16 to 128 rows of A, k cut in up to eight while
+//          all clusters fit at once (a second wave of few costs more than the
+//          longer sums); tiles of up to 64 rows run two to an SM
 Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
     const bool bf16 = at.dtype == EBIN_BFLOAT16;
+    const double kblocks = (double)div_up(at.k, kTcBK);
+    Shape best{};
+    double least = 0;
+    auto consider = [&](const Shape &s, double ns) {
+        if (best.bn == 0 || ns < least) {
+            best = s;
+            least = ns;
+        }
+    };
     Shape s{};
     s.bn = at.m <= 16 ? 16 : at.m <= 32 ? 32 : at.m <= 64 ? 64 : 128;
-    s.split = 1;
     const int64_t tiles = div_up(at.n, kTcRows) * div_up(at.m, s.bn);
-    const int64_t kblocks = div_up(at.k, kTcBK);
-    if (tiles > sms && at.m > 64) {
-        s.pair = true;
-        int64_t least = 0;
-        for (int bn : {256, 224, 192, 160}) {
-            const int64_t waves = div_up(div_up(at.m, 2 * kTcRows) * div_up(at.n, bn), sms / 2);
-            const int64_t cost = waves * (bn + 16);
-            if (least == 0 || cost < least) {
-                least = cost;
-                s.bn = bn;
-            }
-        }
-        return s;
+    for (s.split = 1; s.split <= 8; s.split *= 2) {
+        if (s.split > 1 && (kblocks < s.split * 4 ||
+                            tiles > (bf16 ? tc_clusters_bf16 : tc_clusters_f16)(s.bn, s.split)))
+            break;
+        const bool small = s.bn <= 64;
+        const int64_t ctas = tiles * s.split, room = small ? 2 * sms : sms;
+        const double step = small ? (ctas > sms ? 200 : 140) : 170;
+        consider(s, div_up(ctas, room) * (kblocks / s.split) * step + 12.0 * s.bn +
+                        (s.split > 1 ? 1500 : 0));
     }
-    while (s.split < 8 && kblocks >= s.split * 8 &&
-           tiles <= (bf16 ? tc_clusters_bf16 : tc_clusters_f16)(s.bn, s.split * 2))
-        s.split *= 2;
-    return s;
+    if (at.m > 64) {
+        s.split = 1;
+        s.pair = true;
+        for (int bn : {256, 224, 192, 160, 128, 64}) {
+            s.bn = bn;
+            const int64_t waves = div_up(div_up(at.m, 2 * kTcRows) * div_up(at.n, bn), sms / 2);
+            const double step = std::max(1.05 * bn, (16384 + 64.0 * bn) / 190) + 10;
+            consider(s, waves * kblocks * step + 12.0 * bn);
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
@@ -195,12 +218,13 @@ cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
             r[count++] = RepackArgs{static_cast<const uint16_t *>(o->p),
                                     reinterpret_cast<uint4 *>(dst), o->rows, o->cols, o->ld,
                                     units};
-            most = std::max(most, o->rows);
+            most = std::max(most, o->rows * div_up(units, 64));
             o->p = dst;
             o->ld = units * 8;
         }
         if (count > 0) {
-            const cudaError_t st = launch_layer(k_repack, dim3((unsigned)most, (unsigned)count),
+            const int64_t grid = std::min<int64_t>(div_up(most, 8), 16ll * current_sm_count());
+            const cudaError_t st = launch_layer(k_repack, dim3((unsigned)grid, (unsigned)count),
                                                 256, 0, s, 1, r[0], r[count - 1]);
             if (st != cudaSuccess) return st;
         }
@@ -237,8 +261,8 @@ cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
     const int cluster = shape.pair ? 2 : shape.split;
     const int64_t clusters = shape.pair ? std::min<int64_t>(tiles, current_sm_count() / 2) : tiles;
     if (clusters * cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return (bf16 ? launch_tc_bf16 : launch_tc_f16)(maps[0], maps[1], t, shape.bn,
-                                                   (int)clusters * cluster, cluster, s);
+    return (bf16 ? launch_tc_bf16 : launch_tc_f16)(
+        maps[0], maps[1], t, shape.bn, shape.pair, (int)clusters * cluster, cluster, s);
 }
 
 }  // namespace

@@ -66,13 +66,16 @@ int EBIN_GEMM_CLUSTERS(int bn, int cluster) {
          : bn == 64 ? clusters_of<64>(cluster) : clusters_of<128>(cluster);
 }
 
-// bn: the accumulator columns of a tile; grid CTAs in clusters.
+// bn: the accumulator columns of a tile (on a pair of CTAs, or split); grid CTAs
+// in clusters.
 cudaError_t EBIN_GEMM_NAME(const CUtensorMap &p, const CUtensorMap &q, const TcArgs &a, int bn,
-                           int grid, int cluster, cudaStream_t s) {
+                           bool pair, int grid, int cluster, cudaStream_t s) {
     if (bn == 256) return run<2, 256, false>(p, q, a, grid, cluster, s);
     if (bn == 224) return run<2, 224, false>(p, q, a, grid, cluster, s);
     if (bn == 192) return run<2, 192, false>(p, q, a, grid, cluster, s);
     if (bn == 160) return run<2, 160, false>(p, q, a, grid, cluster, s);
+    if (bn == 128 && pair) return run<2, 128, false>(p, q, a, grid, cluster, s);
+    if (bn == 64 && pair) return run<2, 64, false>(p, q, a, grid, cluster, s);
     if (bn == 16) return run<1, 16, true>(p, q, a, grid, cluster, s);
     if (bn == 32) return run<1, 32, true>(p, q, a, grid, cluster, s);
     if (bn == 64) return run<1, 64, true>(p, q, a, grid, cluster, s);

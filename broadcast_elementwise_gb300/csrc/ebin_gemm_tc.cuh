@@ -183,8 +183,8 @@ __device__ __forceinline__ void tc_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
 
-// 16 accumulator columns of a warp's 32 lanes: thread = lane.  The load and
-// its wait are one statement: the registers hold nothing before the wait.
+// Accumulator columns of a warp's 32 lanes: thread = lane.  The load and its
+// wait are one statement: the registers hold nothing before the wait.
 __device__ __forceinline__ void tc_load16(uint32_t addr, float *v) {
     uint32_t r[16];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -197,6 +197,23 @@ __device__ __forceinline__ void tc_load16(uint32_t addr, float *v) {
                  : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_load32(uint32_t addr, float *v) {
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+                 "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+                   "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                   "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 template <class T> __device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
@@ -258,33 +275,34 @@ __device__ __forceinline__ float tc_bias(const GemmEpilogue &e, int64_t n) {
                       : to_f(static_cast<const T *>(e.bias)[n]);
 }
 
-// `most` of 16 neighbouring rows m of column n, where neighbouring lanes hold
+// `most` (or N) neighbouring rows m of column n, where neighbouring lanes hold
 // neighbouring n.
-template <class T>
+template <class T, int N>
 __device__ __forceinline__ void tc_store_down(const GemmEpilogue &e, int64_t m, int64_t n,
                                               float *v, int most, float bias) {
+    float r[N];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += bias;
+    for (int i = 0; i < N; ++i) v[i] += bias;
+    if (e.residual) {
+        const T *p = static_cast<const T *>(e.residual) + m * e.ld_residual + n;
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = i < most ? to_f(p[i * e.ld_residual]) : 0.0f;
+    }
     if (e.z) {
+        T *p = static_cast<T *>(e.z) + m * e.ldz + n;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < most) static_cast<T *>(e.z)[(m + i) * e.ldz + n] = from_f<T>(v[i]);
+        for (int i = 0; i < N; ++i)
+            if (i < most) p[i * e.ldz] = from_f<T>(v[i]);
     }
-    float r[16];
+    tc_act<N>(e.act, v);
     if (e.residual) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            r[i] = i < most ? to_f(static_cast<const T *>(e.residual)[(m + i) * e.ld_residual + n])
-                            : 0.0f;
+        for (int i = 0; i < N; ++i) v[i] += r[i];
     }
-    tc_act<16>(e.act, v);
-    if (e.residual) {
+    T *p = static_cast<T *>(e.y) + m * e.ldy + n;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += r[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < most) static_cast<T *>(e.y)[(m + i) * e.ldy + n] = from_f<T>(v[i]);
+    for (int i = 0; i < N; ++i)
+        if (i < most) p[i * e.ldy] = from_f<T>(v[i]);
 }
 
 // 32 bytes: in one access (a whole sector a lane) or in two.
@@ -357,7 +375,7 @@ template <int CTAS, int BN, bool SPLIT> struct TcLayout {
     static constexpr int kQ = kQRows * 128;
     static constexpr int kStage = kP + kQ;
     static constexpr int kEpilogueWarps = SPLIT ? 4 : 8;
-    static constexpr int kScratch = SPLIT ? 0 : kEpilogueWarps * 32 * 17 * 4;   // 32 x 16 transposes
+    static constexpr int kScratch = SPLIT ? 0 : kEpilogueWarps * 32 * 33 * 4;   // 32 x 32 transposes
     static constexpr int kBarriers = 512;
     // split tiles of few columns leave room for a second CTA on the SM, whose
     // set-up and first copies overlap this one's end
@@ -528,7 +546,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
         // a warp reads its own quarter of the lanes; two warps share a quarter's columns
         const int quarter = warp & 3, side = (warp - 4) >> 2;
         float *const s_t = reinterpret_cast<float *>(s_base + (scratch - base)) +
-                           (warp - 4) * 32 * 17;
+                           (warp - 4) * 32 * 33;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         int n = 0;
         for (int t = cluster; t < tiles && ok; t += clusters, ++n) {
@@ -542,31 +560,42 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
             const int64_t row0 = (int64_t)(p * CTAS + (CTAS == 2 ? (int)rank : 0)) * kTcRows +
                                  quarter * 32;
             const int64_t col0 = (int64_t)q * BN;
+            const bool live = row0 < a.m;
+            if (a.vec && col0 + BN <= a.n) {
 #pragma unroll 1
-            for (int c = 16 * side; c < BN; c += 32) {
-                if (row0 >= a.m || col0 + c >= a.n) break;
-                float v[16];
-                tc_load16(lanes + acc * L::kAccStep + c, v);
-                if (kb1 == kb0) {   // no k: nothing was summed
+                for (int c = 16 * side; c < BN && live; c += 32) {
+                    float v[16];
+                    tc_load16(lanes + acc * L::kAccStep + c, v);
+                    if (kb1 == kb0) {   // no k: nothing was summed
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                }
-                if (a.vec && col0 + c + 16 <= a.n) {
+                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                    }
                     if (row0 + lane < a.m) {
                         if (a.vec == 2) tc_store16<T, true>(a.e, row0 + lane, col0 + c, v);
                         else tc_store16<T, false>(a.e, row0 + lane, col0 + c, v);
                     }
-                } else {
-                    // off alignment or at the edge: through shared memory, so that
-                    // neighbouring lanes store neighbouring columns
+                }
+            } else {
+                // off alignment or at the edge: through shared memory, so that
+                // neighbouring lanes store neighbouring columns
+#pragma unroll 1
+                for (int c = 32 * side; c < BN && live && col0 + c < a.n; c += 64) {
+                    float v[32];
+                    tc_load32(lanes + acc * L::kAccStep + c, v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s_t[lane * 17 + i] = v[i];
+                    for (int i = 0; i < 32; ++i) s_t[lane * 33 + i] = kb1 == kb0 ? 0.0f : v[i];
                     __syncwarp();
-                    const int64_t col = col0 + c + (lane & 15);
+                    const int64_t col = col0 + c + lane;
                     if (col < a.n) {
                         const float bias = tc_bias<T>(a.e, col);
-                        for (int r = lane >> 4; r < 32 && row0 + r < a.m; r += 2)
-                            tc_store_one<T>(a.e, row0 + r, col, s_t[r * 17 + (lane & 15)], bias);
+                        const int rows = (int)min((int64_t)32, a.m - row0);
+#pragma unroll 1
+                        for (int r = 0; r < rows; r += 4) {
+                            float w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[i] = s_t[(r + i) * 33 + lane];
+                            tc_store_down<T, 4>(a.e, row0 + r, col, w, rows - r, bias);
+                        }
                     }
                     __syncwarp();
                 }
@@ -606,7 +635,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                         part[(c + i) * kTcRows + quarter * 32 + lane] = v[i];
                 } else if (n < a.n) {
                     const int most = (int)min((int64_t)16, a.m - col0 - c);
-                    tc_store_down<T>(a.e, col0 + c, n, v, most, bias);
+                    tc_store_down<T, 16>(a.e, col0 + c, n, v, most, bias);
                 }
             }
             tc_fence_before();
@@ -621,21 +650,30 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
             if (n < a.n) {
                 const float bias = tc_bias<T>(a.e, n);
                 const uint32_t mine = base + 4 * (threadIdx.x & 127);
-                for (int c = first; c < BN && col0 + c < a.m; c += (L::kThreads >> 7) * (int)ranks) {
-                    float v[8];
+                const int step = (L::kThreads >> 7) * (int)ranks;
+                const int most = (int)min((int64_t)BN, a.m - col0);
+                // four columns at a time: their loads are on their way together
+                for (int c = first; c < most; c += 4 * step) {
+                    float z[4];
+                    for (uint32_t r = 0; r < ranks; ++r) {
+                        const uint32_t from = tc_map(mine, r);
+                        float v[4];
 #pragma unroll
-                    for (uint32_t r = 0; r < 8; ++r) {
-                        v[r] = 0.0f;
-                        if (r < ranks)
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                         : "=f"(v[r])
-                                         : "r"(tc_map(mine + 4 * kTcRows * c, r))
-                                         : "memory");
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] = 0.0f;
+                            if (c + i * step < most)
+                                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                             : "=f"(v[i])
+                                             : "r"(from + 4 * kTcRows * (c + i * step))
+                                             : "memory");
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[i] = r == 0 ? v[i] : z[i] + v[i];
                     }
-                    float z = v[0];
 #pragma unroll
-                    for (int r = 1; r < 8; ++r) z += v[r];
-                    tc_store_one<T>(a.e, col0 + c, n, z, bias);
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i * step < most)
+                            tc_store_one<T>(a.e, col0 + c + i * step, n, z[i], bias);
                 }
             }
         }

@@ -197,8 +197,9 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
             *to[i] = HeadsNear{from[i]->p, from[i]->sb, (int32_t)from[i]->st,
                                (int32_t)from[i]->sh};
         }
-        v.heads[w] = heads_div((uint32_t)std::max(1, a.heads[w]));
-        v.heads[w].n = (uint32_t)a.heads[w];
+        const uint32_t parts = (uint32_t)div_up(a.heads[w], kGradHeads);
+        v.heads[w] = heads_div(std::max(1u, parts));
+        v.heads[w].n = parts;
     }
     v.tokens = heads_div((uint32_t)a.tokens);
     v.rot_units = (int)(a.half / V);
@@ -244,7 +245,7 @@ cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, c
         kHeadsMaxPartials);
     const int64_t heads = a.heads[0] + a.heads[1];
     for (int w = 0; w < 2; ++w) {
-        const int64_t most = div_up(a.rows * a.heads[w], per);
+        const int64_t most = div_up(a.rows * div_up(a.heads[w], kGradHeads), per);
         const int64_t share = std::max<int64_t>(1, all * a.heads[w] / heads);
         v.ctas[w] = (int)std::min(most, share);
         ctas[w] = v.ctas[w];

@@ -212,7 +212,7 @@ struct HeadsVecArgs {
     HeadsNear x[2], dy[2], y[2];
     HeadsDiv per_token;     // items of a token: groups of HPT heads of q, then of k
     HeadsDiv tokens;        // tokens of a sequence
-    HeadsDiv heads[2];      // the gradient's rows of q, of k
+    HeadsDiv heads[2];      // the gradient's items of a token: kGradHeads heads of q, of k
     uint32_t q_items;       // of per_token
     uint32_t items;         // of the launch
     int32_t log_lanes;
@@ -540,11 +540,14 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
     }
 }
 
-// The gradient of norm and rotation.  CTAs take rows of q or of k only, in
-// steps of their number, so a thread's weight-gradient sums stay in registers
-// to the end; the next row's vectors and position are on their way while the
-// present row is worked on.  The CTA's sums then join in shared memory and go
-// to its row of the workspace.
+// The gradient of norm and rotation.  CTAs take items of q or of k only (a
+// token and kGradHeads of its heads), in steps of their number, so a thread's
+// weight-gradient sums stay in registers to the end; the next row's vectors,
+// and the next item's position, are on their way while a row is worked on.
+// The CTA's sums then join in shared memory and go to its row of the
+// workspace.
+constexpr int kGradHeads = 4;
+
 template <class T, bool IL>
 __global__ void __launch_bounds__(kHeadsThreads, 2)
 k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
@@ -555,29 +558,40 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     const bool which = (int)blockIdx.x >= v.ctas[0];
     const uint32_t cta = blockIdx.x - (which ? v.ctas[0] : 0);
     const uint32_t ctas = which ? v.ctas[1] : v.ctas[0];
-    const HeadsDiv heads = which ? v.heads[1] : v.heads[0];
-    const uint32_t total = (uint32_t)a.rows * heads.n;
+    const HeadsDiv parts = which ? v.heads[1] : v.heads[0];   // items of a token
+    const int heads = which ? a.heads[1] : a.heads[0];
+    const uint32_t total = (uint32_t)a.rows * parts.n;
     const int per = kHeadsThreads >> v.log_lanes, group = threadIdx.x >> v.log_lanes;
     layer_pdl_launch();
     Unit u;
     u.place(a, v, lane);
-    const T *const x = static_cast<const T *>(which ? v.x[1].p : v.x[0].p);
-    const T *const dy = static_cast<const T *>(which ? v.dy[1].p : v.dy[0].p);
-    T *const y = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p));
-    uint4 nx0, nx1, ng0, ng1;
+    const int xsh = which ? v.x[1].sh : v.x[0].sh, gsh = which ? v.dy[1].sh : v.dy[0].sh,
+              ysh = which ? v.y[1].sh : v.y[0].sh;
+    const T *x, *dy;   // the item's first head
+    T *y, *ny;
+    int count, ncount;
     int64_t np;
-    auto fetch = [&](uint32_t row) {   // a row past the end repeats row 0
+    uint4 nx0, nx1, ng0, ng1;
+    auto start = [&](uint32_t item) {   // an item past the end repeats the first
         uint32_t bs, h, b, s;
-        heads.split(row < total ? row : 0, bs, h);
+        parts.split(item < total ? item : 0, bs, h);
         v.tokens.split(bs, b, s);
+        h *= kGradHeads;
         np = heads_position(a, b, s);
-        u.load(x + heads_near(which ? v.x[1] : v.x[0], b, s, h), nx0, nx1);
-        u.load(dy + heads_near(which ? v.dy[1] : v.dy[0], b, s, h), ng0, ng1);
+        x = static_cast<const T *>(which ? v.x[1].p : v.x[0].p) +
+            heads_near(which ? v.x[1] : v.x[0], b, s, h);
+        dy = static_cast<const T *>(which ? v.dy[1].p : v.dy[0].p) +
+             heads_near(which ? v.dy[1] : v.dy[0], b, s, h);
+        ny = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p)) +
+             heads_near(which ? v.y[1] : v.y[0], b, s, h);
+        ncount = item < total ? min(kGradHeads, heads - (int)h) : 0;
+        u.load(x, nx0, nx1);
+        u.load(dy, ng0, ng1);
     };
     layer_pdl_wait();
     const uint32_t step = ctas * per;
     uint32_t base = cta * per;
-    fetch(base + group);
+    start(base + group);
     float2 wa[N], wb[N], da[N], db[N];
     u.weights(a, v, which, wa, wb);
 #pragma unroll
@@ -586,54 +600,63 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     const float inv = 1.0f / (float)a.dim;
     // every lane of a warp makes the same number of steps: the exchanges are warp-wide
     for (; base < total; base += step) {
-        const uint32_t row = base + group;
-        const bool live = row < total;
         const int64_t p = np;
-        float2 xa[N], xb[N], ga[N], gb[N];
-        Unit::open(ng0, ng1, ga, gb);
-        Unit::open(nx0, nx1, xa, xb);
-        {
-            float2 c[N], sn[N], n[N];
-            u.angles(a, v, p < 0 ? 0 : p, c, sn, n);
-            if (base + step < total) fetch(row + step);
-            u.turn(ga, gb, c, sn, n, c);
-        }
-        const bool use = live && p >= 0;
-        bad |= live && p < 0;
-        float ss = u.squares(xa, xb);
-        // sum of g w x, the absent elements' weights being 0
-        float2 dot = both(0.0f);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            dot = __ffma2_rn(__fmul2_rn(ga[i], wa[i]), xa[i],
-                             __ffma2_rn(__fmul2_rn(gb[i], wb[i]), xb[i], dot));
-        float gx = dot.x + dot.y;
-        for (int o = lanes >> 1; o > 0; o >>= 1) {
-            ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-            gx += __shfl_xor_sync(0xFFFFFFFFu, gx, o);
-        }
-        const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
-        const float2 mean = both(-gx * rstd * inv), r2 = both(rstd);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            xa[i] = __fmul2_rn(xa[i], r2);
-            xb[i] = __fmul2_rn(xb[i], r2);
-            if (use) {
-                da[i] = __ffma2_rn(ga[i], xa[i], da[i]);
-                db[i] = __ffma2_rn(gb[i], xb[i], db[i]);
+        count = ncount;
+        y = ny;
+        bad |= count > 0 && p < 0;
+        float2 c[N], sn[N], n[N];
+        u.angles(a, v, p < 0 ? 0 : p, c, sn, n);
+        const bool out = __any_sync(0xFFFFFFFFu, p < 0);   // rare
+#pragma unroll 1
+        for (int h = 0; h < kGradHeads; ++h) {
+            float2 xa[N], xb[N], ga[N], gb[N];
+            Unit::open(ng0, ng1, ga, gb);
+            Unit::open(nx0, nx1, xa, xb);
+            if (h + 1 < kGradHeads) {
+                if (h + 1 < count) {
+                    x += xsh;
+                    dy += gsh;
+                    u.load(x, nx0, nx1);
+                    u.load(dy, ng0, ng1);
+                }
+            } else if (base + step < total) {
+                start(base + step + group);
             }
-            ga[i] = __fmul2_rn(__ffma2_rn(xa[i], mean, __fmul2_rn(ga[i], wa[i])), r2);
-            gb[i] = __fmul2_rn(__ffma2_rn(xb[i], mean, __fmul2_rn(gb[i], wb[i])), r2);
-        }
-        if (!use) {
+            u.turn(ga, gb, c, sn, n, c);
+            float ss = u.squares(xa, xb);
+            // sum of g w x, the absent elements' weights being 0
+            float2 dot = both(0.0f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) ga[i] = gb[i] = both(0.0f);
-        }
-        if (live) {
-            uint32_t bs, h, b, s;
-            heads.split(row, bs, h);
-            v.tokens.split(bs, b, s);
-            u.store(y + heads_near(which ? v.y[1] : v.y[0], b, s, h), ga, gb);
+            for (int i = 0; i < N; ++i)
+                dot = __ffma2_rn(__fmul2_rn(ga[i], wa[i]), xa[i],
+                                 __ffma2_rn(__fmul2_rn(gb[i], wb[i]), xb[i], dot));
+            float gx = dot.x + dot.y;
+            for (int o = lanes >> 1; o > 0; o >>= 1) {
+                ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+                gx += __shfl_xor_sync(0xFFFFFFFFu, gx, o);
+            }
+            const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
+            const float2 mean = both(-gx * rstd * inv), r2 = both(rstd);
+            const bool live = h < count, use = live && p >= 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                xa[i] = __fmul2_rn(xa[i], r2);
+                xb[i] = __fmul2_rn(xb[i], r2);
+                if (use) {
+                    da[i] = __ffma2_rn(ga[i], xa[i], da[i]);
+                    db[i] = __ffma2_rn(gb[i], xb[i], db[i]);
+                }
+                ga[i] = __fmul2_rn(__ffma2_rn(xa[i], mean, __fmul2_rn(ga[i], wa[i])), r2);
+                gb[i] = __fmul2_rn(__ffma2_rn(xb[i], mean, __fmul2_rn(gb[i], wb[i])), r2);
+            }
+            if (out) {
+                if (p < 0) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) ga[i] = gb[i] = both(0.0f);
+                }
+            }
+            if (live) u.store(y, ga, gb);
+            y += ysh;
         }
     }
     if (bad && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
