@@ -201,6 +201,11 @@ def _ptr(x) -> int | None:
 _current = None     # (the current device's index, its current stream's address), from torch
 
 
+def _ptrs(*xs):
+    """_ptr of each argument, in one call (a launch-bound path passes many)."""
+    return [x if x is None or isinstance(x, int) else x.data_ptr() for x in xs]
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         global _current
@@ -790,9 +795,8 @@ def execute_heads(plan: HeadsPlan, q, k, cos, sin, positions, q_out, k_out, wq=N
                   stream=None) -> None:
     """Enqueue a rotation (either direction) or a norm with rotation on device
     buffers laid out as the plan says (torch tensors or int addresses)."""
-    st = lib.ebin_heads_execute(plan.handle, _ptr(q), _ptr(k), _ptr(cos), _ptr(sin),
-                                _ptr(positions), _ptr(wq), _ptr(wk), _ptr(q_out), _ptr(k_out),
-                                _stream(stream))
+    st = lib.ebin_heads_execute(plan.handle, *_ptrs(q, k, cos, sin, positions, wq, wk, q_out,
+                                                    k_out), _stream(stream))
     if st:
         raise EbinError(st, "ebin_heads_execute")
 
@@ -801,14 +805,13 @@ def execute_heads_grad(plan: HeadsPlan, dq, dk, q, k, cos, sin, positions, wq, w
                        dwq, dwk, workspace, stream=None) -> None:
     """Enqueue the gradient of norm and rotation; ``workspace``: a uint8 device
     tensor of at least plan.workspace_bytes."""
-    ebin_heads_grad_execute(plan.handle, _ptr(dq), _ptr(dk), _ptr(q), _ptr(k), _ptr(cos),
-                            _ptr(sin), _ptr(positions), _ptr(wq), _ptr(wk), _ptr(dq_out),
-                            _ptr(dk_out), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+    ebin_heads_grad_execute(plan.handle, *_ptrs(dq, dk, q, k, cos, sin, positions, wq, wk, dq_out,
+                                                dk_out, dwq, dwk, workspace),
                             _bytes_of(workspace), _stream(stream))
 
 
 def _bytes_of(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def _same_device(where, first, *others):
@@ -970,9 +973,8 @@ def execute_gemm(plan: GemmPlan, A, B, y, *, bias=None, residual=None, preact=No
     """Enqueue a product on device buffers laid out as the plan says (torch
     tensors or int addresses); ``workspace``: a uint8 device tensor of at least
     plan.workspace_bytes (None where that is 0)."""
-    st = lib.ebin_gemm_execute(plan.handle, _ptr(A), _ptr(B), _ptr(bias), _ptr(residual), _ptr(y),
-                               _ptr(preact), _ptr(workspace), _bytes_of(workspace),
-                               _stream(stream))
+    st = lib.ebin_gemm_execute(plan.handle, *_ptrs(A, B, bias, residual, y, preact, workspace),
+                               _bytes_of(workspace), _stream(stream))
     if st:
         raise EbinError(st, "ebin_gemm_execute")
 
@@ -1003,8 +1005,8 @@ class EpilogueGradPlan:
 def execute_epilogue_grad(plan: EpilogueGradPlan, dy, z, dz, dbias=None, workspace=None,
                           stream=None) -> None:
     """Enqueue an epilogue's gradient on device buffers laid out as the plan says."""
-    st = lib.ebin_epilogue_grad_execute(plan.handle, _ptr(dy), _ptr(z), _ptr(dz), _ptr(dbias),
-                                        _ptr(workspace), _bytes_of(workspace), _stream(stream))
+    st = lib.ebin_epilogue_grad_execute(plan.handle, *_ptrs(dy, z, dz, dbias, workspace),
+                                        _bytes_of(workspace), _stream(stream))
     if st:
         raise EbinError(st, "ebin_epilogue_grad_execute")
 

@@ -32,7 +32,9 @@ int tc_clusters_bf16(int bn, int cluster);
 struct RepackArgs {
     const uint16_t *src;
     uint4 *dst;
-    int64_t rows, cols, ld, units;   // units: vectors of a row of dst
+    int64_t rows, cols, ld;
+    int64_t units, pitch;            // vectors of a row of dst, and from row to row
+    FastDiv per_row;                 // by units
 };
 
 __device__ __forceinline__ uint4 repack_unit(const RepackArgs &r, int64_t row, int64_t c) {
@@ -70,23 +72,41 @@ __device__ __forceinline__ uint4 repack_unit(const RepackArgs &r, int64_t row, i
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A warp takes a run of a row's vectors, two a lane.
+// The vectors of the new layout one after another, kRepackVectors a thread, all
+// loads of a thread on their way before the first store.
+constexpr int kRepackVectors = 4;
+
 __global__ void __launch_bounds__(256) k_repack(const RepackArgs a, const RepackArgs b) {
     layer_pdl_launch();
     const RepackArgs &r = blockIdx.y ? b : a;
-    const int lane = threadIdx.x & 31;
-    const int64_t runs = (r.units + 63) / 64, total = r.rows * runs;   // runs of 64 vectors
+    const int64_t total = r.rows * r.units;
+    const bool narrow = total < (1ll << 31);
     layer_pdl_wait();
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total;
-         i += (int64_t)gridDim.x * 8) {
-        const int64_t row = i / runs, u = (i - row * runs) * 64 + lane;
-        uint4 x[2];
+    for (int64_t i0 = (int64_t)blockIdx.x * (256 * kRepackVectors) + threadIdx.x; i0 < total;
+         i0 += (int64_t)gridDim.x * (256 * kRepackVectors)) {
+        uint4 x[kRepackVectors];
+        int64_t at[kRepackVectors];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (u + 32 * k < r.units) x[k] = repack_unit(r, row, (u + 32 * k) * 8);
+        for (int k = 0; k < kRepackVectors; ++k) {
+            const int64_t i = i0 + 256 * k;
+            at[k] = -1;
+            if (i >= total) continue;
+            int64_t row, u;
+            if (narrow) {
+                uint32_t q, rest;
+                r.per_row.split((uint32_t)i, q, rest);
+                row = q;
+                u = rest;
+            } else {
+                row = i / r.units;
+                u = i - row * r.units;
+            }
+            at[k] = row * r.pitch + u;
+            x[k] = repack_unit(r, row, u * 8);
+        }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (u + 32 * k < r.units) r.dst[row * r.units + u + 32 * k] = x[k];
+        for (int k = 0; k < kRepackVectors; ++k)
+            if (at[k] >= 0) r.dst[at[k]] = x[k];
     }
 }
 
@@ -100,7 +120,9 @@ int64_t matrix_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t isz) {
     return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * isz : 0;
 }
 
-int64_t round8(int64_t n) { return div_up(n, 8) * 8; }
+// Row pitch of an operand's copy: whole 128-byte lines, so that a copy's rows
+// of 128 bytes do not straddle two (13.0 -> 8.9 us for [1021, 2049] x [1543, 2049]).
+int64_t copy_pitch(int64_t cols) { return div_up(cols, 64) * 64; }
 
 // cuTensorMapEncodeTiled, looked up through the runtime, or null.
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -137,7 +159,7 @@ bool encode(const Operand &o, int box, bool bf16, CUtensorMap *map) {
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows};
     // a single row has no step; any whole number of vectors serves
-    const cuuint64_t strides[1] = {(cuuint64_t)(o.rows > 1 ? o.ld : round8(o.cols)) * 2};
+    const cuuint64_t strides[1] = {(cuuint64_t)(o.rows > 1 ? o.ld : copy_pitch(o.cols)) * 2};
     const cuuint32_t boxes[2] = {64, (cuuint32_t)(o.mn ? kTcBK : box)};
     const cuuint32_t steps[2] = {1, 1};
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
@@ -217,13 +239,14 @@ cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
             const int64_t units = div_up(o->cols, 8);
             r[count++] = RepackArgs{static_cast<const uint16_t *>(o->p),
                                     reinterpret_cast<uint4 *>(dst), o->rows, o->cols, o->ld,
-                                    units};
-            most = std::max(most, o->rows * div_up(units, 64));
+                                    units, copy_pitch(o->cols) / 8, fast_div((uint32_t)units)};
+            most = std::max(most, o->rows * units);
             o->p = dst;
-            o->ld = units * 8;
+            o->ld = copy_pitch(o->cols);
         }
         if (count > 0) {
-            const int64_t grid = std::min<int64_t>(div_up(most, 8), 16ll * current_sm_count());
+            const int64_t grid = std::min<int64_t>(
+                div_up(most, 256 * kRepackVectors), 16ll * current_sm_count());
             const cudaError_t st = launch_layer(k_repack, dim3((unsigned)grid, (unsigned)count),
                                                 256, 0, s, 1, r[0], r[count - 1]);
             if (st != cudaSuccess) return st;
@@ -306,11 +329,11 @@ extern "C" ebin_status ebin_gemm_plan_create(const ebin_gemm_attrs *attrs, ebin_
     if (a.m > 0 && a.n > 0 && a.k > 0) {
         if (a.any_alignment || (p->a_rows > 1 && p->lda % 8 != 0)) {
             p->copy_a = (int64_t)p->workspace;
-            p->workspace += (size_t)(p->a_rows * round8(p->a_cols) * 2);
+            p->workspace += (size_t)(p->a_rows * copy_pitch(p->a_cols) * 2);
         }
         if (a.any_alignment || (p->b_rows > 1 && p->ldb % 8 != 0)) {
             p->copy_b = (int64_t)p->workspace;
-            p->workspace += (size_t)(p->b_rows * round8(p->b_cols) * 2);
+            p->workspace += (size_t)(p->b_rows * copy_pitch(p->b_cols) * 2);
         }
     }
     *out = p;

@@ -162,20 +162,15 @@ cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode,
     return launch_layer(k_heads_any<T, HEADS_NORM_GRAD>, grid, kHeadsThreads, smem, s, 1, a, il);
 }
 
-HeadsDiv heads_div(uint32_t n) {
-    uint32_t l = 0;
-    while (((uint64_t)1 << l) < n) ++l;
-    const uint64_t m = (((uint64_t)1 << 32) * (((uint64_t)1 << l) - n)) / n + 1;
-    return HeadsDiv{n, (uint32_t)m, l};
-}
-
 // The vector path's layout of a head, or false where it does not apply: rows
-// that are not whole 16-byte vectors on 16-byte boundaries, halves that are
-// not (half layout), and heads of more than 64 vectors.
-bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, HeadsVecArgs &v) {
+// that are not whole 16-byte vectors on 16-byte boundaries, and heads of more
+// than 64 vectors.
+bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, HeadsVecArgs &v,
+                   int &kind) {
     const int64_t V = 16 / p.isz, D = a.dim;
-    const bool il = p.at.layout == EBIN_ROTARY_INTERLEAVED;
-    if (D % V != 0 || (!il && a.half % V != 0)) return false;
+    if (D % V != 0) return false;
+    kind = p.at.layout == EBIN_ROTARY_INTERLEAVED ? HEADS_PAIRS
+         : a.half % V == 0 ? HEADS_HALF : HEADS_ODD;
     auto fits = [&](const HeadsTensor &t, int heads) {
         return (uintptr_t)t.p % 16 == 0 && (p.at.batch <= 1 || t.sb % V == 0) &&
                (p.at.tokens <= 1 || t.st % V == 0) && (heads <= 1 || t.sh % V == 0);
@@ -198,13 +193,13 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
                                (int32_t)from[i]->sh};
         }
         const uint32_t parts = (uint32_t)div_up(a.heads[w], kGradHeads);
-        v.heads[w] = heads_div(std::max(1u, parts));
+        v.heads[w] = fast_div(std::max(1u, parts));
         v.heads[w].n = parts;
     }
-    v.tokens = heads_div((uint32_t)a.tokens);
+    v.tokens = fast_div((uint32_t)a.tokens);
     v.rot_units = (int)(a.half / V);
-    v.units = il ? (int)div_up(D / V, 2)
-                 : v.rot_units + (int)div_up((D - 2 * a.half) / V, 2);
+    v.units = kind != HEADS_HALF ? (int)div_up(D / V, 2)
+                                 : v.rot_units + (int)div_up((D - 2 * a.half) / V, 2);
     if (v.units > 32) return false;
     while ((1 << v.log_lanes) < v.units) ++v.log_lanes;
     v.weight_vec = ((uintptr_t)a.w[0] | (uintptr_t)a.w[1]) % 16 == 0;
@@ -226,22 +221,24 @@ template <auto KERNEL> int heads_resident(size_t smem) {
     return n;
 }
 
-template <class T, bool IL, int MODE, int HPT>
+template <class T, int KIND, int MODE, int HPT>
 cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, cudaStream_t s) {
     v.q_items = (uint32_t)div_up(a.heads[0], HPT);
-    v.per_token = heads_div(v.q_items + (uint32_t)div_up(a.heads[1], HPT));
+    v.per_token = fast_div(v.q_items + (uint32_t)div_up(a.heads[1], HPT));
     v.items = (uint32_t)a.rows * v.per_token.n;
     const int64_t grid = div_up((int64_t)v.items << v.log_lanes, kHeadsThreads);
-    return launch_layer(k_heads_vec<T, IL, MODE, HPT>, dim3((unsigned)grid), kHeadsThreads, 0, s,
-                        1, a, v);
+    const size_t smem = KIND == HEADS_ODD
+        ? sizeof(T) * (kHeadsThreads >> v.log_lanes) * HPT * a.dim : 0;   // at most 32 KB
+    return launch_layer(k_heads_vec<T, KIND, MODE, HPT>, dim3((unsigned)grid), kHeadsThreads, smem,
+                        s, 1, a, v);
 }
 
-template <class T, bool IL>
+template <class T, int KIND>
 cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, cudaStream_t s) {
     // one wave of CTAs, shared between q and k by their rows
     const int per = kHeadsThreads >> v.log_lanes;
     const int64_t all = std::min<int64_t>(
-        (int64_t)heads_resident<k_heads_vec_grad<T, IL>>(16384) * current_sm_count(),
+        (int64_t)heads_resident<k_heads_vec_grad<T, KIND>>(16384) * current_sm_count(),
         kHeadsMaxPartials);
     const int64_t heads = a.heads[0] + a.heads[1];
     for (int w = 0; w < 2; ++w) {
@@ -250,34 +247,40 @@ cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, c
         v.ctas[w] = (int)std::min(most, share);
         ctas[w] = v.ctas[w];
     }
-    const size_t smem = sizeof(float) * per * a.dim;
-    return launch_layer(k_heads_vec_grad<T, IL>, dim3((unsigned)(v.ctas[0] + v.ctas[1])),
+    // the groups' sums; before them one group's weights, two vectors a lane, and
+    // (HEADS_ODD) the groups' rows
+    const size_t weights = (sizeof(float) * 2 * (16 / sizeof(T))) << v.log_lanes;
+    const size_t rows = KIND == HEADS_ODD ? sizeof(T) * per * a.dim : 0;
+    const size_t smem = std::max(sizeof(float) * per * a.dim, weights + rows);
+    return launch_layer(k_heads_vec_grad<T, KIND>, dim3((unsigned)(v.ctas[0] + v.ctas[1])),
                         kHeadsThreads, smem, s, 1, a, v);
 }
 
-template <class T, bool IL>
+template <class T, int KIND>
 cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, int mode, int64_t *ctas,
                             cudaStream_t s) {
-    if (mode == HEADS_NORM_GRAD) return launch_vec_grad<T, IL>(a, v, ctas, s);
+    if (mode == HEADS_NORM_GRAD) return launch_vec_grad<T, KIND>(a, v, ctas, s);
     // Few rows: one head per item spreads them over the SMs.  Many: four heads
     // share the token's position, cosines, sines and weights.
     const bool few = (a.rows * (a.heads[0] + a.heads[1]) << v.log_lanes) <
                      2048ll * current_sm_count();
     if (mode == HEADS_ROTATE)
-        return few ? launch_vec<T, IL, HEADS_ROTATE, 1>(a, v, s)
-                   : launch_vec<T, IL, HEADS_ROTATE, 4>(a, v, s);
-    return few ? launch_vec<T, IL, HEADS_NORM, 1>(a, v, s)
-               : launch_vec<T, IL, HEADS_NORM, 4>(a, v, s);
+        return few ? launch_vec<T, KIND, HEADS_ROTATE, 1>(a, v, s)
+                   : launch_vec<T, KIND, HEADS_ROTATE, 4>(a, v, s);
+    return few ? launch_vec<T, KIND, HEADS_NORM, 1>(a, v, s)
+               : launch_vec<T, KIND, HEADS_NORM, 4>(a, v, s);
 }
 
 template <class T>
 cudaError_t launch_heads(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode, int64_t *ctas,
                          cudaStream_t s) {
     HeadsVecArgs v;
-    if (!heads_vectors(p, a, mode == HEADS_NORM_GRAD, v))
+    int kind = 0;
+    if (!heads_vectors(p, a, mode == HEADS_NORM_GRAD, v, kind))
         return launch_any<T>(p, a, mode, ctas, s);
-    return p.at.layout == EBIN_ROTARY_INTERLEAVED ? launch_vec_mode<T, true>(a, v, mode, ctas, s)
-                                                  : launch_vec_mode<T, false>(a, v, mode, ctas, s);
+    if (kind == HEADS_HALF) return launch_vec_mode<T, HEADS_HALF>(a, v, mode, ctas, s);
+    if (kind == HEADS_PAIRS) return launch_vec_mode<T, HEADS_PAIRS>(a, v, mode, ctas, s);
+    return launch_vec_mode<T, HEADS_ODD>(a, v, mode, ctas, s);
 }
 
 cudaError_t launch_typed(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode, int64_t *ctas,

@@ -189,18 +189,10 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, 
 //                        two neighbouring vectors of what passes through
 //   interleaved layout   vectors at 2 u V and (2 u + 1) V: pairs of neighbours
 // so a rotation needs no exchange between lanes, and a norm one tree over L.
+//   half layout whose half is no whole number of vectors   vectors at 2 u V and
+//   (2 u + 1) V; the other element of each pair comes through shared memory
 // Cosines, sines and weights stay in registers over the heads of one item.
-
-// Division of 32-bit indices by a launch's constant n: with 2^(l-1) < n <= 2^l
-// and m = floor(2^32 (2^l - n) / n) + 1, x / n = (hi(x m) + x) >> l exactly,
-// the sum taken in 33 bits (Granlund and Montgomery's multiplier).
-struct HeadsDiv {
-    uint32_t n, mul, shift;
-    __device__ __forceinline__ void split(uint32_t x, uint32_t &q, uint32_t &r) const {
-        q = (uint32_t)(((uint64_t)__umulhi(x, mul) + x) >> shift);
-        r = x - q * n;
-    }
-};
+enum HeadsKind : int { HEADS_HALF = 0, HEADS_PAIRS = 1, HEADS_ODD = 2 };
 
 struct HeadsNear {          // a tensor whose token and head strides fit 32 bits
     const void *p;
@@ -210,9 +202,9 @@ struct HeadsNear {          // a tensor whose token and head strides fit 32 bits
 
 struct HeadsVecArgs {
     HeadsNear x[2], dy[2], y[2];
-    HeadsDiv per_token;     // items of a token: groups of HPT heads of q, then of k
-    HeadsDiv tokens;        // tokens of a sequence
-    HeadsDiv heads[2];      // the gradient's items of a token: kGradHeads heads of q, of k
+    FastDiv per_token;     // items of a token: groups of HPT heads of q, then of k
+    FastDiv tokens;        // tokens of a sequence
+    FastDiv heads[2];      // the gradient's items of a token: kGradHeads heads of q, of k
     uint32_t q_items;       // of per_token
     uint32_t items;         // of the launch
     int32_t log_lanes;
@@ -260,7 +252,8 @@ __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y
 
 // Where a lane's unit lies and how its pairs read: pairs 2i and 2i + 1 are
 // (a[i].x, b[i].x) and (a[i].y, b[i].y), ready for the packed binary32 pipe.
-template <class T, bool IL> struct HeadsUnit {
+template <class T, int KIND> struct HeadsUnit {
+    static constexpr bool IL = KIND == HEADS_PAIRS, ODD = KIND == HEADS_ODD;
     static constexpr int V = 16 / sizeof(T), N = V / 2;
     int off0, off1;    // element offsets of the two vectors
     bool on, second;   // the lane has work; its second vector exists
@@ -269,7 +262,12 @@ template <class T, bool IL> struct HeadsUnit {
 
     __device__ __forceinline__ void place(const HeadsArgs &a, const HeadsVecArgs &v, int lane) {
         on = lane < v.units;
-        if constexpr (IL) {
+        if constexpr (ODD) {
+            off0 = 2 * lane * V;
+            off1 = off0 + V;
+            pair0 = 0;
+            pairs = min(max(2 * a.half - off0, 0), 2 * V);   // leading elements that rotate
+        } else if constexpr (IL) {
             off0 = 2 * lane * V;
             off1 = off0 + V;
             pair0 = lane * V;
@@ -352,9 +350,72 @@ template <class T, bool IL> struct HeadsUnit {
         if (on) *reinterpret_cast<uint4 *>(p + off0) = r0;
         if (second) *reinterpret_cast<uint4 *>(p + off1) = r1;
     }
-    // c = cos, s = sin with the direction's sign, n = -s (pairs past `pairs`: 1, 0, 0)
-    __device__ __forceinline__ void angles(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
-                                           float2 *c, float2 *s, float2 *n) const {
+    // ODD: element k of the unit (0 .. 2 V - 1) turns with element other(k) of
+    // the row: y = x c + x_other s, s = -sin for the row's first half and sin for
+    // its second, times `sign`
+    __device__ __forceinline__ int other(int half, int k) const {
+        const int j = off0 + k;
+        return j < half ? j + half : j - half;
+    }
+    __device__ __forceinline__ void factors(const HeadsArgs &a, int64_t p, float sign, float2 *ca,
+                                            float2 *cb, float2 *sa, float2 *sb) const {
+        const float *cr = a.cos + p * a.half, *sr = a.sin + p * a.half;
+        auto one = [&](int k, float &c, float &s) {
+            c = 1.0f;
+            s = 0.0f;
+            if (k < pairs) {
+                const int j = off0 + k;
+                const bool first = j < a.half;
+                const int at = first ? j : j - a.half;
+                c = __ldg(cr + at);
+                s = __ldg(sr + at) * (first ? -sign : sign);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            one(2 * i, ca[i].x, sa[i].x);
+            one(2 * i + 1, ca[i].y, sa[i].y);
+            one(V + 2 * i, cb[i].x, sb[i].x);
+            one(V + 2 * i + 1, cb[i].y, sb[i].y);
+        }
+    }
+    // the weights that the other elements carry, into s
+    __device__ __forceinline__ void weigh_others(const HeadsArgs &a, int which, float2 *sa,
+                                                 float2 *sb) const {
+        auto one = [&](int k, float &s) {
+            if (k < pairs) s *= heads_weight<T>(a, which, other(a.half, k));
+        };
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            one(2 * i, sa[i].x);
+            one(2 * i + 1, sa[i].y);
+            one(V + 2 * i, sb[i].x);
+            one(V + 2 * i + 1, sb[i].y);
+        }
+    }
+    __device__ __forceinline__ void share(T *row, const uint4 &x0, const uint4 &x1) const {
+        if (on) *reinterpret_cast<uint4 *>(row + off0) = x0;
+        if (second) *reinterpret_cast<uint4 *>(row + off1) = x1;
+    }
+    // row: the unpacked row's other elements, as shared; scale: what a, b were scaled by
+    __device__ __forceinline__ void turn_odd(const T *row, int half, float scale, float2 *a,
+                                             float2 *b, const float2 *ca, const float2 *cb,
+                                             const float2 *sa, const float2 *sb) const {
+        auto one = [&](int k, float x, float c, float s) {
+            x *= c;
+            return k < pairs ? fmaf(to_f(row[other(half, k)]) * scale, s, x) : x;
+        };
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            a[i].x = one(2 * i, a[i].x, ca[i].x, sa[i].x);
+            a[i].y = one(2 * i + 1, a[i].y, ca[i].y, sa[i].y);
+            b[i].x = one(V + 2 * i, b[i].x, cb[i].x, sb[i].x);
+            b[i].y = one(V + 2 * i + 1, b[i].y, cb[i].y, sb[i].y);
+        }
+    }
+    // the unit's cosines and sines (pairs past `pairs`: 1 and 0)
+    __device__ __forceinline__ void table(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
+                                          float2 *c, float2 *s) const {
         const float *cr = a.cos + p * a.half + pair0, *sr = a.sin + p * a.half + pair0;
         if (pairs == V && v.table_vec) {
 #pragma unroll
@@ -375,6 +436,11 @@ template <class T, bool IL> struct HeadsUnit {
                 s[i].y = 2 * i + 1 < pairs ? __ldg(sr + 2 * i + 1) : 0.0f;
             }
         }
+    }
+    // c = cos, s = sin with the direction's sign, n = -s
+    __device__ __forceinline__ void angles(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
+                                           float2 *c, float2 *s, float2 *n) const {
+        table(a, v, p, c, s);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             n[i] = __fmul2_rn(s[i], both(-a.sign));
@@ -430,6 +496,31 @@ template <class T, bool IL> struct HeadsUnit {
             }
         }
     }
+    // the transposed rotation (a gradient's): y_a = a cos + b sin, y_b = b cos - a sin
+    __device__ __forceinline__ void turn_back(float2 *a, float2 *b, const float2 *c,
+                                              const float2 *s) const {
+        if (pairs == V) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float2 x = a[i];
+                a[i] = __ffma2_rn(x, c[i], __fmul2_rn(b[i], s[i]));
+                b[i] = __ffma2_rn(b[i], c[i], neg2(__fmul2_rn(x, s[i])));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float2 x = a[i], y = b[i];
+                if (2 * i < pairs) {
+                    a[i].x = fmaf(x.x, c[i].x, y.x * s[i].x);
+                    b[i].x = fmaf(y.x, c[i].x, -(x.x * s[i].x));
+                }
+                if (2 * i + 1 < pairs) {
+                    a[i].y = fmaf(x.y, c[i].y, y.y * s[i].y);
+                    b[i].y = fmaf(y.y, c[i].y, -(x.y * s[i].y));
+                }
+            }
+        }
+    }
     // the sum over the lane's elements of x^2 (0 where it has none)
     __device__ __forceinline__ float squares(const float2 *a, const float2 *b) const {
         float2 x = both(0.0f), y = both(0.0f);
@@ -455,10 +546,10 @@ __device__ __forceinline__ void keep_packed(uint4 &x) {
 
 // Rotation, and norm with rotation.  An item is a token and HPT heads of q or
 // of k; all its loads are issued before the first is used.
-template <class T, bool IL, int MODE, int HPT>
-__global__ void __launch_bounds__(kHeadsThreads, sizeof(T) == 2 ? 3 : 1)
+template <class T, int KIND, int MODE, int HPT>
+__global__ void __launch_bounds__(kHeadsThreads, sizeof(T) == 4 ? 1 : KIND == HEADS_ODD ? 2 : 3)
 k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
-    using Unit = HeadsUnit<T, IL>;
+    using Unit = HeadsUnit<T, KIND>;
     constexpr int N = Unit::N;
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
     layer_pdl_launch();
@@ -481,6 +572,14 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
     uint4 x0[HPT], x1[HPT];
 #pragma unroll
     for (int h = 0; h < HPT; ++h) u.load(x + (h < count ? (int64_t)h * xsh : 0), x0[h], x1[h]);
+    extern __shared__ uint4 s_rows[];   // HEADS_ODD: the groups' rows, [groups][HPT][dim]
+    T *const rows = reinterpret_cast<T *>(s_rows) +
+                    (int64_t)(threadIdx.x >> v.log_lanes) * HPT * a.dim;
+    if constexpr (Unit::ODD) {
+#pragma unroll
+        for (int h = 0; h < HPT; ++h) u.share(rows + h * a.dim, x0[h], x1[h]);
+        __syncwarp();
+    }
     float rstd[HPT];
     if constexpr (MODE == HEADS_NORM) {
         // the heads' sums cross the lanes together, so that their shuffles overlap
@@ -501,9 +600,24 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
     }
     // a pair's factors: y_a = x_a ca + x_b nb, y_b = x_b cb + x_a sa: cos, sin and
     // -sin, with a norm times the weights of the elements they meet
+    // (HEADS_ODD: y_a = x_a ca + other sa, y_b = x_b cb + other nb)
     float2 ca[N], cb[N], sa[N], nb[N];
-    u.angles(a, v, p < 0 ? 0 : p, ca, sa, nb);
-    if constexpr (MODE == HEADS_NORM) {
+    if constexpr (Unit::ODD) {
+        u.factors(a, p < 0 ? 0 : p, a.sign, ca, cb, sa, nb);
+        if constexpr (MODE == HEADS_NORM) {
+            float2 wa[N], wb[N];
+            u.weights(a, v, which, wa, wb);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                ca[i] = __fmul2_rn(ca[i], wa[i]);
+                cb[i] = __fmul2_rn(cb[i], wb[i]);
+            }
+            u.weigh_others(a, which, sa, nb);
+        }
+    } else {
+        u.angles(a, v, p < 0 ? 0 : p, ca, sa, nb);
+    }
+    if constexpr (MODE == HEADS_NORM && !Unit::ODD) {
         float2 wa[N], wb[N];
         u.weights(a, v, which, wa, wb);
 #pragma unroll
@@ -528,10 +642,12 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
                 va[i] = __fmul2_rn(va[i], both(rstd[h]));
                 vb[i] = __fmul2_rn(vb[i], both(rstd[h]));
             }
-            u.turn(va, vb, ca, sa, nb, cb);
-        } else {
-            u.turn(va, vb, ca, sa, nb, ca);
         }
+        if constexpr (Unit::ODD)
+            u.turn_odd(rows + h * a.dim, a.half, MODE == HEADS_NORM ? rstd[h] : 1.0f, va, vb, ca,
+                       cb, sa, nb);
+        else
+            u.turn(va, vb, ca, sa, nb, MODE == HEADS_NORM ? cb : ca);
         if (p < 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) va[i] = vb[i] = both(0.0f);
@@ -548,17 +664,17 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
 // workspace.
 constexpr int kGradHeads = 4;
 
-template <class T, bool IL>
+template <class T, int KIND>
 __global__ void __launch_bounds__(kHeadsThreads, 2)
 k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
-    using Unit = HeadsUnit<T, IL>;
+    using Unit = HeadsUnit<T, KIND>;
     constexpr int N = Unit::N;
-    extern __shared__ float s_dw[];   // [groups of the CTA][dim]
+    extern __shared__ float s_dw[];   // [groups of the CTA][dim], before that the weights [lanes][2 V]
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
     const bool which = (int)blockIdx.x >= v.ctas[0];
     const uint32_t cta = blockIdx.x - (which ? v.ctas[0] : 0);
     const uint32_t ctas = which ? v.ctas[1] : v.ctas[0];
-    const HeadsDiv parts = which ? v.heads[1] : v.heads[0];   // items of a token
+    const FastDiv parts = which ? v.heads[1] : v.heads[0];   // items of a token
     const int heads = which ? a.heads[1] : a.heads[0];
     const uint32_t total = (uint32_t)a.rows * parts.n;
     const int per = kHeadsThreads >> v.log_lanes, group = threadIdx.x >> v.log_lanes;
@@ -592,8 +708,20 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     const uint32_t step = ctas * per;
     uint32_t base = cta * per;
     start(base + group);
-    float2 wa[N], wb[N], da[N], db[N];
-    u.weights(a, v, which, wa, wb);
+    // a lane's weights in shared memory, in the order that it uses them: sixteen
+    // registers less
+    float4 *const s_w = reinterpret_cast<float4 *>(s_dw) + lane;
+    // HEADS_ODD: behind the weights, the groups' rows
+    T *const row = reinterpret_cast<T *>(s_dw + (2 * Unit::V << v.log_lanes)) + group * a.dim;
+    if (threadIdx.x < lanes) {
+        float2 wa[N], wb[N];
+        u.weights(a, v, which, wa, wb);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            s_w[i * lanes] = make_float4(wa[i].x, wa[i].y, wb[i].x, wb[i].y);
+    }
+    __syncthreads();
+    float2 da[N], db[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) da[i] = db[i] = both(0.0f);
     bool bad = false;
@@ -604,14 +732,20 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
         count = ncount;
         y = ny;
         bad |= count > 0 && p < 0;
-        float2 c[N], sn[N], n[N];
-        u.angles(a, v, p < 0 ? 0 : p, c, sn, n);
+        float2 c[N], sn[N], cb[N], sb[N];
+        if constexpr (Unit::ODD) u.factors(a, p < 0 ? 0 : p, -1.0f, c, cb, sn, sb);
+        else u.table(a, v, p < 0 ? 0 : p, c, sn);
         const bool out = __any_sync(0xFFFFFFFFu, p < 0);   // rare
 #pragma unroll 1
         for (int h = 0; h < kGradHeads; ++h) {
             float2 xa[N], xb[N], ga[N], gb[N];
             Unit::open(ng0, ng1, ga, gb);
             Unit::open(nx0, nx1, xa, xb);
+            if constexpr (Unit::ODD) {
+                __syncwarp();   // the row before has been read
+                u.share(row, ng0, ng1);
+                __syncwarp();
+            }
             if (h + 1 < kGradHeads) {
                 if (h + 1 < count) {
                     x += xsh;
@@ -622,14 +756,19 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
             } else if (base + step < total) {
                 start(base + step + group);
             }
-            u.turn(ga, gb, c, sn, n, c);
+            if constexpr (Unit::ODD) u.turn_odd(row, a.half, 1.0f, ga, gb, c, cb, sn, sb);
+            else u.turn_back(ga, gb, c, sn);
             float ss = u.squares(xa, xb);
             // sum of g w x, the absent elements' weights being 0
             float2 dot = both(0.0f);
+            float2 wa[N], wb[N];   // g w
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                dot = __ffma2_rn(__fmul2_rn(ga[i], wa[i]), xa[i],
-                                 __ffma2_rn(__fmul2_rn(gb[i], wb[i]), xb[i], dot));
+            for (int i = 0; i < N; ++i) {
+                const float4 w = s_w[i * lanes];
+                wa[i] = __fmul2_rn(ga[i], make_float2(w.x, w.y));
+                wb[i] = __fmul2_rn(gb[i], make_float2(w.z, w.w));
+                dot = __ffma2_rn(wa[i], xa[i], __ffma2_rn(wb[i], xb[i], dot));
+            }
             float gx = dot.x + dot.y;
             for (int o = lanes >> 1; o > 0; o >>= 1) {
                 ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
@@ -646,8 +785,8 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
                     da[i] = __ffma2_rn(ga[i], xa[i], da[i]);
                     db[i] = __ffma2_rn(gb[i], xb[i], db[i]);
                 }
-                ga[i] = __fmul2_rn(__ffma2_rn(xa[i], mean, __fmul2_rn(ga[i], wa[i])), r2);
-                gb[i] = __fmul2_rn(__ffma2_rn(xb[i], mean, __fmul2_rn(gb[i], wb[i])), r2);
+                ga[i] = __fmul2_rn(__ffma2_rn(xa[i], mean, wa[i]), r2);
+                gb[i] = __fmul2_rn(__ffma2_rn(xb[i], mean, wb[i]), r2);
             }
             if (out) {
                 if (p < 0) {
@@ -660,9 +799,11 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
         }
     }
     if (bad && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+    __syncthreads();   // the weights have been read
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         // pairs 2i and 2i + 1 of the unit
+        constexpr bool IL = Unit::IL;
         const int j = IL ? (i < N / 2 ? u.off0 : u.off1 - Unit::V) + 4 * i : u.off0 + 2 * i;
         const int k = IL ? j + 1 : u.off1 + 2 * i, next = IL ? 2 : 1;
         const bool first = IL ? (i < N / 2 ? u.on : u.second) : u.on;

@@ -33,6 +33,26 @@ inline bool product_fits(int64_t a, int64_t b, int64_t *out) {
     return true;
 }
 
+// Division of 32-bit indices by a launch's constant n: with 2^(l-1) < n <= 2^l
+// and m = floor(2^32 (2^l - n) / n) + 1, x / n = (hi(x m) + x) >> l exactly,
+// the sum taken in 33 bits (Granlund and Montgomery's multiplier).
+struct FastDiv {
+    uint32_t n, mul, shift;
+#ifdef __CUDACC__
+    __device__ __forceinline__ void split(uint32_t x, uint32_t &q, uint32_t &r) const {
+        q = (uint32_t)(((uint64_t)__umulhi(x, mul) + x) >> shift);
+        r = x - q * n;
+    }
+#endif
+};
+
+inline FastDiv fast_div(uint32_t n) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < n) ++l;
+    const uint64_t m = (((uint64_t)1 << 32) * (((uint64_t)1 << l) - n)) / n + 1;
+    return FastDiv{n, (uint32_t)m, l};
+}
+
 // Launch with programmatic dependent launch (the kernel calls
 // griddepcontrol.wait before its first global access) and count it.
 template <class... KParams, class... Args>
