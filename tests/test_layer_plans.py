@@ -114,3 +114,88 @@ def test_rotary_table_refusals():
     assert code(table, cos=None) == "invalid_arg"
     assert code(table, sin=0x1010) == "alias"
     table(positions=0, cos=None, sin=None)
+
+
+def gemm(dtype="bfloat16", m=64, n=96, k=80, **kw):
+    return eb.GemmPlan(dtype, m, n, k, **kw)
+
+
+def test_gemm_plan_refusals():
+    for dtype in ("float32", "float64", "int8"):
+        assert code(gemm, dtype) == "unsupported_type"
+    assert code(gemm, bias="float16") == "unsupported_type"
+    for sizes in ((-1, 2, 2), (2, -1, 2), (2, 2, -1), (1 << 31, 2, 2), (2, 2, 1 << 31)):
+        assert code(gemm, "bfloat16", *sizes) == "invalid_arg"
+    assert code(gemm, lda=79) == "invalid_arg"
+    assert code(gemm, trans_b=True, ldb=79) == "invalid_arg"
+    assert code(gemm, ldb=95) == "invalid_arg"
+    assert code(gemm, ldy=1 << 60) == "invalid_arg"
+    with pytest.raises(KeyError):
+        gemm(activation="tanh")
+    attrs = eb.ebin_gemm_attrs(16, 16, 0, 0, 9, 0, 0, 0, 4, 4, 4, 0, 0, 0, 0, 0)
+    assert code(eb.ebin_gemm_plan_create, attrs) == "invalid_attr"
+    attrs = eb.ebin_gemm_attrs(16, 16, 2, 0, 0, 0, 0, 0, 4, 4, 4, 0, 0, 0, 0, 0)
+    assert code(eb.ebin_gemm_plan_create, attrs) == "invalid_attr"
+
+
+def test_gemm_workspace():
+    """Copies only of operands whose rows are off 16 bytes; rows of whole 128-byte lines."""
+    assert gemm().workspace_bytes == 0
+    assert gemm(k=81).workspace_bytes == 64 * 128 * 2               # A's rows; B's are 96 wide
+    assert gemm(k=81, trans_b=True).workspace_bytes == (64 + 96) * 128 * 2
+    assert gemm(m=1, k=81).workspace_bytes == 0                     # one row has no step
+    assert gemm(any_alignment=True).workspace_bytes == (64 * 128 + 80 * 128) * 2
+    assert gemm(k=0, any_alignment=True).workspace_bytes == 0
+
+
+def test_gemm_execute_refusals():
+    def run(plan, a=0x100000, b=0x200000, bias=None, r=None, y=0x300000, z=None, work=None,
+            size=0):
+        eb.ebin_gemm_execute(plan.handle, a, b, bias, r, y, z, work, size, 0)
+
+    p = gemm()
+    for missing in ("a", "b", "y"):
+        assert code(run, p, **{missing: None}) == "invalid_arg"
+    assert code(run, gemm(bias="float32")) == "invalid_arg"
+    assert code(run, gemm(residual=True)) == "invalid_arg"
+    assert code(run, p, a=0x100002) == "invalid_arg"                # off 16 bytes
+    assert code(run, p, y=0x300001) == "invalid_arg"                # off the element size
+    assert code(run, gemm(bias="float32"), bias=0x400002) == "invalid_arg"
+    odd = gemm(k=81)
+    assert code(run, odd) == "invalid_arg"                          # no workspace
+    assert code(run, odd, work=0x800000, size=odd.workspace_bytes - 1) == "invalid_arg"
+    assert code(run, odd, work=0x800008, size=odd.workspace_bytes) == "invalid_arg"
+    assert code(run, odd, work=0x100000, size=odd.workspace_bytes) == "alias"
+    assert code(run, p, y=0x100010) == "alias"
+    assert code(run, p, y=0x200000) == "alias"
+    assert code(run, p, z=0x300000) == "alias"
+    assert code(run, gemm(residual=True), r=0x300010) == "alias"
+    assert code(run, gemm(residual=True, ldy=104), r=0x300000) == "alias"   # another stride
+    assert code(run, gemm(bias="bfloat16"), bias=0x300000) == "alias"
+    run(gemm(m=0), a=None, b=None, y=None)
+    run(gemm(n=0), a=None, b=None, y=None)
+
+
+def test_epilogue_grad_refusals():
+    def plan(dtype="bfloat16", m=16, n=24, activation="silu", bias=True, **kw):
+        return eb.EpilogueGradPlan(dtype, m, n, activation=activation, bias=bias, **kw)
+
+    assert code(plan, "float64") == "unsupported_type"
+    assert code(plan, m=-1) == "invalid_arg"
+    assert code(plan, ld_dz=23) == "invalid_arg"
+    p = plan()
+
+    def run(p, dy=0x100000, z=0x200000, dz=0x300000, db=0x400000, work=0x500000, size=None):
+        eb.ebin_epilogue_grad_execute(p.handle, dy, z, dz, db, work,
+                                      p.workspace_bytes if size is None else size, 0)
+
+    for missing in ("dy", "z", "dz", "db", "work"):
+        assert code(run, p, **{missing: None}) == "invalid_arg"
+    assert code(run, p, size=p.workspace_bytes - 1) == "invalid_arg"
+    assert code(run, p, dy=0x100001) == "invalid_arg"
+    assert code(run, p, dz=0x100002) == "alias"
+    assert code(run, plan(ld_dz=32), dz=0x100000) == "alias"
+    assert code(run, p, db=0x300000) == "alias"
+    assert code(run, p, work=0x200000) == "alias"
+    assert code(run, p, work=0x400000) == "alias"
+    run(plan(n=0), dy=None, z=None, dz=None, db=None, work=None)
