@@ -235,25 +235,26 @@ cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, cudaStream_t s) {
 
 template <class T, int KIND>
 cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, cudaStream_t s) {
+    // the ring, one group's weights (two vectors a lane) and, HEADS_ODD, the groups'
+    // rows: at most 4 KB and 8 KB of them; the sums at the end fit the ring
+    constexpr size_t most = kGradRingBytes + 4096 + (KIND == HEADS_ODD ? 8192 : 0);
+    static const cudaError_t opted = cudaFuncSetAttribute(
+        k_heads_vec_grad<T, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (opted != cudaSuccess) return opted;
     // one wave of CTAs, shared between q and k by their rows
     const int per = kHeadsThreads >> v.log_lanes;
     const int64_t all = std::min<int64_t>(
-        (int64_t)heads_resident<k_heads_vec_grad<T, KIND>>(16384) * current_sm_count(),
+        (int64_t)heads_resident<k_heads_vec_grad<T, KIND>>(most) * current_sm_count(),
         kHeadsMaxPartials);
     const int64_t heads = a.heads[0] + a.heads[1];
     for (int w = 0; w < 2; ++w) {
-        const int64_t most = div_up(a.rows * div_up(a.heads[w], kGradHeads), per);
+        const int64_t items = div_up(a.rows * div_up(a.heads[w], kGradHeads), per);
         const int64_t share = std::max<int64_t>(1, all * a.heads[w] / heads);
-        v.ctas[w] = (int)std::min(most, share);
+        v.ctas[w] = (int)std::min(items, share);
         ctas[w] = v.ctas[w];
     }
-    // the groups' sums; before them one group's weights, two vectors a lane, and
-    // (HEADS_ODD) the groups' rows
-    const size_t weights = (sizeof(float) * 2 * (16 / sizeof(T))) << v.log_lanes;
-    const size_t rows = KIND == HEADS_ODD ? sizeof(T) * per * a.dim : 0;
-    const size_t smem = std::max(sizeof(float) * per * a.dim, weights + rows);
     return launch_layer(k_heads_vec_grad<T, KIND>, dim3((unsigned)(v.ctas[0] + v.ctas[1])),
-                        kHeadsThreads, smem, s, 1, a, v);
+                        kHeadsThreads, most, s, 1, a, v);
 }
 
 template <class T, int KIND>

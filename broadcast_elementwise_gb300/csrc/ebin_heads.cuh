@@ -658,18 +658,26 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
 
 // The gradient of norm and rotation.  CTAs take items of q or of k only (a
 // token and kGradHeads of its heads), in steps of their number, so a thread's
-// weight-gradient sums stay in registers to the end; the next row's vectors,
-// and the next item's position, are on their way while a row is worked on.
-// The CTA's sums then join in shared memory and go to its row of the
-// workspace.
-constexpr int kGradHeads = 4;
+// weight-gradient sums stay in registers to the end.  Rows come through a ring
+// in shared memory, kGradAhead of them on their way: each thread copies what
+// it will read itself, so that nothing but its own copies is waited for.  The
+// CTA's sums then join in shared memory and go to its row of the workspace.
+constexpr int kGradHeads = 4, kGradRing = 4, kGradAhead = kGradRing - 1;
+constexpr int kGradRingBytes = kGradRing * 4 * kHeadsThreads * 16;
+
+__device__ __forceinline__ void heads_copy(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 
 template <class T, int KIND>
 __global__ void __launch_bounds__(kHeadsThreads, 2)
 k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     using Unit = HeadsUnit<T, KIND>;
     constexpr int N = Unit::N;
-    extern __shared__ float s_dw[];   // [groups of the CTA][dim], before that the weights [lanes][2 V]
+    // the ring [kGradRing][x, x, dy, dy][threads], after it the weights [lanes][2 V] and
+    // (HEADS_ODD) the groups' rows; at the end the sums [groups of the CTA][dim]
+    extern __shared__ uint4 s_ring[];
+    float *const s_dw = reinterpret_cast<float *>(s_ring);
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
     const bool which = (int)blockIdx.x >= v.ctas[0];
     const uint32_t cta = blockIdx.x - (which ? v.ctas[0] : 0);
@@ -683,36 +691,65 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     u.place(a, v, lane);
     const int xsh = which ? v.x[1].sh : v.x[0].sh, gsh = which ? v.dy[1].sh : v.dy[0].sh,
               ysh = which ? v.y[1].sh : v.y[0].sh;
-    const T *x, *dy;   // the item's first head
-    T *y, *ny;
-    int count, ncount;
-    int64_t np;
-    uint4 nx0, nx1, ng0, ng1;
-    auto start = [&](uint32_t item) {   // an item past the end repeats the first
-        uint32_t bs, h, b, s;
-        parts.split(item < total ? item : 0, bs, h);
-        v.tokens.split(bs, b, s);
-        h *= kGradHeads;
-        np = heads_position(a, b, s);
-        x = static_cast<const T *>(which ? v.x[1].p : v.x[0].p) +
-            heads_near(which ? v.x[1] : v.x[0], b, s, h);
-        dy = static_cast<const T *>(which ? v.dy[1].p : v.dy[0].p) +
-             heads_near(which ? v.dy[1] : v.dy[0], b, s, h);
-        ny = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p)) +
-             heads_near(which ? v.y[1] : v.y[0], b, s, h);
-        ncount = item < total ? min(kGradHeads, heads - (int)h) : 0;
-        u.load(x, nx0, nx1);
-        u.load(dy, ng0, ng1);
-    };
-    layer_pdl_wait();
     const uint32_t step = ctas * per;
-    uint32_t base = cta * per;
-    start(base + group);
+    // what is fetched runs kGradAhead rows before what is worked on: at most one item
+    const T *x = nullptr, *dy = nullptr;
+    T *ny = nullptr;
+    int ncount = 0;
+    int64_t np = 0;
+    uint32_t fetched = cta * per;   // the CTA's item being fetched, its row, and the ring's place
+    int frow = 0, fslot = 0;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring + threadIdx.x);
+    auto fetch = [&]() {
+        if (fetched < total) {
+            if (frow == 0) {
+                const uint32_t item = fetched + group;
+                uint32_t bs, h, b, s;
+                parts.split(item < total ? item : 0, bs, h);
+                v.tokens.split(bs, b, s);
+                h *= kGradHeads;
+                np = heads_position(a, b, s);
+                x = static_cast<const T *>(which ? v.x[1].p : v.x[0].p) +
+                    heads_near(which ? v.x[1] : v.x[0], b, s, h);
+                dy = static_cast<const T *>(which ? v.dy[1].p : v.dy[0].p) +
+                     heads_near(which ? v.dy[1] : v.dy[0], b, s, h);
+                ny = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p)) +
+                     heads_near(which ? v.y[1] : v.y[0], b, s, h);
+                ncount = item < total ? min(kGradHeads, heads - (int)h) : 0;
+            }
+            if (frow < ncount) {
+                const uint32_t to = ring + fslot * (4 * kHeadsThreads * 16);
+                if (u.on) {
+                    heads_copy(to, x + u.off0);
+                    heads_copy(to + 2 * kHeadsThreads * 16, dy + u.off0);
+                }
+                if (u.second) {
+                    heads_copy(to + kHeadsThreads * 16, x + u.off1);
+                    heads_copy(to + 3 * kHeadsThreads * 16, dy + u.off1);
+                }
+                x += xsh;
+                dy += gsh;
+            }
+            if (++frow == kGradHeads) {
+                frow = 0;
+                fetched += step;
+            }
+            fslot = fslot + 1 == kGradRing ? 0 : fslot + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     // a lane's weights in shared memory, in the order that it uses them: sixteen
     // registers less
-    float4 *const s_w = reinterpret_cast<float4 *>(s_dw) + lane;
-    // HEADS_ODD: behind the weights, the groups' rows
-    T *const row = reinterpret_cast<T *>(s_dw + (2 * Unit::V << v.log_lanes)) + group * a.dim;
+    float4 *const s_w = reinterpret_cast<float4 *>(s_dw + kGradRingBytes / 4) + lane;
+    T *const row = reinterpret_cast<T *>(s_dw + kGradRingBytes / 4 +
+                                         (2 * Unit::V << v.log_lanes)) + group * a.dim;
+    layer_pdl_wait();
+    // lanes without work, or without a second vector, read zeros from the ring
+    for (int i = 0; i < kGradRing * 4; ++i)
+        if (!(i & 1 ? u.second : u.on))
+            s_ring[i * kHeadsThreads + threadIdx.x] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int i = 0; i < kGradAhead; ++i) fetch();
     if (threadIdx.x < lanes) {
         float2 wa[N], wb[N];
         u.weights(a, v, which, wa, wb);
@@ -725,12 +762,13 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
 #pragma unroll
     for (int i = 0; i < N; ++i) da[i] = db[i] = both(0.0f);
     bool bad = false;
+    int slot = 0;
     const float inv = 1.0f / (float)a.dim;
     // every lane of a warp makes the same number of steps: the exchanges are warp-wide
-    for (; base < total; base += step) {
+    for (uint32_t base = cta * per; base < total; base += step) {
         const int64_t p = np;
-        count = ncount;
-        y = ny;
+        const int count = ncount;
+        T *y = ny;
         bad |= count > 0 && p < 0;
         float2 c[N], sn[N], cb[N], sb[N];
         if constexpr (Unit::ODD) u.factors(a, p < 0 ? 0 : p, -1.0f, c, cb, sn, sb);
@@ -738,24 +776,21 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
         const bool out = __any_sync(0xFFFFFFFFu, p < 0);   // rare
 #pragma unroll 1
         for (int h = 0; h < kGradHeads; ++h) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kGradAhead - 1) : "memory");
+            const uint4 *const mine = s_ring + slot * 4 * kHeadsThreads + threadIdx.x;
+            slot = slot + 1 == kGradRing ? 0 : slot + 1;
             float2 xa[N], xb[N], ga[N], gb[N];
-            Unit::open(ng0, ng1, ga, gb);
-            Unit::open(nx0, nx1, xa, xb);
-            if constexpr (Unit::ODD) {
-                __syncwarp();   // the row before has been read
-                u.share(row, ng0, ng1);
-                __syncwarp();
-            }
-            if (h + 1 < kGradHeads) {
-                if (h + 1 < count) {
-                    x += xsh;
-                    dy += gsh;
-                    u.load(x, nx0, nx1);
-                    u.load(dy, ng0, ng1);
+            {
+                const uint4 g0 = mine[2 * kHeadsThreads], g1 = mine[3 * kHeadsThreads];
+                Unit::open(g0, g1, ga, gb);
+                Unit::open(mine[0], mine[kHeadsThreads], xa, xb);
+                if constexpr (Unit::ODD) {
+                    __syncwarp();   // the row before has been read
+                    u.share(row, g0, g1);
+                    __syncwarp();
                 }
-            } else if (base + step < total) {
-                start(base + step + group);
             }
+            fetch();
             if constexpr (Unit::ODD) u.turn_odd(row, a.half, 1.0f, ga, gb, c, cb, sn, sb);
             else u.turn_back(ga, gb, c, sn);
             float ss = u.squares(xa, xb);
@@ -798,8 +833,9 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
             y += ysh;
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (bad && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
-    __syncthreads();   // the weights have been read
+    __syncthreads();   // the ring and the weights have been read
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         // pairs 2i and 2i + 1 of the unit
