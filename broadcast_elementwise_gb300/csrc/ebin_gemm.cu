@@ -213,7 +213,7 @@ Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
     if (at.m > 64) {
         s.split = 1;
         s.pair = true;
-        for (int bn : {256, 224, 192, 160, 128, 64}) {
+        for (int bn : {256, 224, 192, 160, 128, 96, 64}) {
             s.bn = bn;
             const int64_t waves = div_up(div_up(at.m, 2 * kTcRows) * div_up(at.n, bn), sms / 2);
             const double step = std::max(1.05 * bn, (16384 + 64.0 * bn) / 190) + 10;

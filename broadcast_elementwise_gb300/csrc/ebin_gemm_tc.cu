@@ -75,6 +75,7 @@ cudaError_t EBIN_GEMM_NAME(const CUtensorMap &p, const CUtensorMap &q, const TcA
     if (bn == 192) return run<2, 192, false>(p, q, a, grid, cluster, s);
     if (bn == 160) return run<2, 160, false>(p, q, a, grid, cluster, s);
     if (bn == 128 && pair) return run<2, 128, false>(p, q, a, grid, cluster, s);
+    if (bn == 96) return run<2, 96, false>(p, q, a, grid, cluster, s);
     if (bn == 64 && pair) return run<2, 64, false>(p, q, a, grid, cluster, s);
     if (bn == 16) return run<1, 16, true>(p, q, a, grid, cluster, s);
     if (bn == 32) return run<1, 32, true>(p, q, a, grid, cluster, s);

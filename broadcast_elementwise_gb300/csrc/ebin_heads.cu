@@ -192,7 +192,7 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
             *to[i] = HeadsNear{from[i]->p, from[i]->sb, (int32_t)from[i]->st,
                                (int32_t)from[i]->sh};
         }
-        const uint32_t parts = (uint32_t)div_up(a.heads[w], kGradHeads);
+        const uint32_t parts = (uint32_t)div_up(a.heads[w], kRingHeads);
         v.heads[w] = fast_div(std::max(1u, parts));
         v.heads[w].n = parts;
     }
@@ -233,11 +233,30 @@ cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, cudaStream_t s) {
                         s, 1, a, v);
 }
 
+template <class T, int KIND> cudaError_t launch_ring(const HeadsArgs &a, HeadsVecArgs v,
+                                                     cudaStream_t s) {
+    v.q_items = (uint32_t)div_up(a.heads[0], kRingHeads);
+    v.per_token = fast_div(v.q_items + (uint32_t)div_up(a.heads[1], kRingHeads));
+    v.items = (uint32_t)a.rows * v.per_token.n;
+    constexpr size_t smem = HeadsRing<T, KIND, false>::kBytes + (KIND == HEADS_ODD ? 8192 : 0);
+    static const cudaError_t opted = cudaFuncSetAttribute(
+        k_heads_ring<T, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (opted != cudaSuccess) return opted;
+    const int64_t wave = (int64_t)heads_resident<k_heads_ring<T, KIND>>(smem) * current_sm_count();
+    // Under three items a group the walk is too short to pay for itself (norm
+    // [3,1021,15,96] f32, 1.3 items: 11.5 us against 8.2 by a CTA an item; [2,4096,40,128]
+    // bf16, 5.6 items: 29.0 against 32.2).
+    if (((int64_t)v.items << v.log_lanes) < 3 * wave * kHeadsThreads)
+        return launch_vec<T, KIND, HEADS_NORM, kRingHeads>(a, v, s);
+    return launch_layer(k_heads_ring<T, KIND>, dim3((unsigned)wave), kHeadsThreads, smem, s, 1, a,
+                        v);
+}
+
 template <class T, int KIND>
 cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, cudaStream_t s) {
     // the ring, one group's weights (two vectors a lane) and, HEADS_ODD, the groups'
     // rows: at most 4 KB and 8 KB of them; the sums at the end fit the ring
-    constexpr size_t most = kGradRingBytes + 4096 + (KIND == HEADS_ODD ? 8192 : 0);
+    constexpr size_t most = HeadsRing<T, KIND, true>::kBytes + 4096 + (KIND == HEADS_ODD ? 8192 : 0);
     static const cudaError_t opted = cudaFuncSetAttribute(
         k_heads_vec_grad<T, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (opted != cudaSuccess) return opted;
@@ -248,7 +267,7 @@ cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, c
         kHeadsMaxPartials);
     const int64_t heads = a.heads[0] + a.heads[1];
     for (int w = 0; w < 2; ++w) {
-        const int64_t items = div_up(a.rows * div_up(a.heads[w], kGradHeads), per);
+        const int64_t items = div_up(a.rows * div_up(a.heads[w], kRingHeads), per);
         const int64_t share = std::max<int64_t>(1, all * a.heads[w] / heads);
         v.ctas[w] = (int)std::min(items, share);
         ctas[w] = v.ctas[w];
@@ -268,8 +287,7 @@ cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, int mode,
     if (mode == HEADS_ROTATE)
         return few ? launch_vec<T, KIND, HEADS_ROTATE, 1>(a, v, s)
                    : launch_vec<T, KIND, HEADS_ROTATE, 4>(a, v, s);
-    return few ? launch_vec<T, KIND, HEADS_NORM, 1>(a, v, s)
-               : launch_vec<T, KIND, HEADS_NORM, 4>(a, v, s);
+    return few ? launch_vec<T, KIND, HEADS_NORM, 1>(a, v, s) : launch_ring<T, KIND>(a, v, s);
 }
 
 template <class T>

@@ -204,7 +204,7 @@ struct HeadsVecArgs {
     HeadsNear x[2], dy[2], y[2];
     FastDiv per_token;     // items of a token: groups of HPT heads of q, then of k
     FastDiv tokens;        // tokens of a sequence
-    FastDiv heads[2];      // the gradient's items of a token: kGradHeads heads of q, of k
+    FastDiv heads[2];      // the gradient's items of a token: kRingHeads heads of q, of k
     uint32_t q_items;       // of per_token
     uint32_t items;         // of the launch
     int32_t log_lanes;
@@ -391,6 +391,33 @@ template <class T, int KIND> struct HeadsUnit {
             one(2 * i + 1, sa[i].y);
             one(V + 2 * i, sb[i].x);
             one(V + 2 * i + 1, sb[i].y);
+        }
+    }
+    // a pair's factors: y_a = x_a ca + x_b nb, y_b = x_b cb + x_a sa: cos, sin and
+    // -sin, with a norm times the weights of the elements they meet
+    // (ODD: y_a = x_a ca + other sa, y_b = x_b cb + other nb)
+    template <bool NORM>
+    __device__ __forceinline__ void folded(const HeadsArgs &a, const HeadsVecArgs &v, int which,
+                                           int64_t p, float2 *ca, float2 *cb, float2 *sa,
+                                           float2 *nb) const {
+        if constexpr (ODD) factors(a, p, a.sign, ca, cb, sa, nb);
+        else angles(a, v, p, ca, sa, nb);
+        if constexpr (NORM) {
+            float2 wa[N], wb[N];
+            weights(a, v, which, wa, wb);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                cb[i] = __fmul2_rn(ODD ? cb[i] : ca[i], wb[i]);
+                ca[i] = __fmul2_rn(ca[i], wa[i]);
+                if constexpr (!ODD) {
+                    sa[i] = __fmul2_rn(sa[i], wa[i]);
+                    nb[i] = __fmul2_rn(nb[i], wb[i]);
+                }
+            }
+            if constexpr (ODD) weigh_others(a, which, sa, nb);
+        } else if constexpr (!ODD) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) cb[i] = ca[i];
         }
     }
     __device__ __forceinline__ void share(T *row, const uint4 &x0, const uint4 &x1) const {
@@ -598,36 +625,8 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
 #pragma unroll
         for (int h = 0; h < HPT; ++h) rstd[h] = rsqrtf(fmaf(rstd[h], inv, a.eps));
     }
-    // a pair's factors: y_a = x_a ca + x_b nb, y_b = x_b cb + x_a sa: cos, sin and
-    // -sin, with a norm times the weights of the elements they meet
-    // (HEADS_ODD: y_a = x_a ca + other sa, y_b = x_b cb + other nb)
     float2 ca[N], cb[N], sa[N], nb[N];
-    if constexpr (Unit::ODD) {
-        u.factors(a, p < 0 ? 0 : p, a.sign, ca, cb, sa, nb);
-        if constexpr (MODE == HEADS_NORM) {
-            float2 wa[N], wb[N];
-            u.weights(a, v, which, wa, wb);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                ca[i] = __fmul2_rn(ca[i], wa[i]);
-                cb[i] = __fmul2_rn(cb[i], wb[i]);
-            }
-            u.weigh_others(a, which, sa, nb);
-        }
-    } else {
-        u.angles(a, v, p < 0 ? 0 : p, ca, sa, nb);
-    }
-    if constexpr (MODE == HEADS_NORM && !Unit::ODD) {
-        float2 wa[N], wb[N];
-        u.weights(a, v, which, wa, wb);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            cb[i] = __fmul2_rn(ca[i], wb[i]);
-            ca[i] = __fmul2_rn(ca[i], wa[i]);
-            sa[i] = __fmul2_rn(sa[i], wa[i]);
-            nb[i] = __fmul2_rn(nb[i], wb[i]);
-        }
-    }
+    u.template folded<MODE == HEADS_NORM>(a, v, which, p < 0 ? 0 : p, ca, cb, sa, nb);
     if (p < 0 && live && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
     T *const y = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p)) +
                  heads_near(which ? v.y[1] : v.y[0], b, s, h0);
@@ -647,7 +646,7 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
             u.turn_odd(rows + h * a.dim, a.half, MODE == HEADS_NORM ? rstd[h] : 1.0f, va, vb, ca,
                        cb, sa, nb);
         else
-            u.turn(va, vb, ca, sa, nb, MODE == HEADS_NORM ? cb : ca);
+            u.turn(va, vb, ca, sa, nb, cb);
         if (p < 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) va[i] = vb[i] = both(0.0f);
@@ -656,100 +655,210 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
     }
 }
 
-// The gradient of norm and rotation.  CTAs take items of q or of k only (a
-// token and kGradHeads of its heads), in steps of their number, so a thread's
-// weight-gradient sums stay in registers to the end.  Rows come through a ring
-// in shared memory, kGradAhead of them on their way: each thread copies what
-// it will read itself, so that nothing but its own copies is waited for.  The
-// CTA's sums then join in shared memory and go to its row of the workspace.
-constexpr int kGradHeads = 4, kGradRing = 4, kGradAhead = kGradRing - 1;
-constexpr int kGradRingBytes = kGradRing * 4 * kHeadsThreads * 16;
+// Rows through a ring in shared memory.  A group of lanes walks items (a token
+// and kRingHeads heads of q or of k) in steps of the launch's groups; their
+// rows are fetched kAhead before they are worked on, by asynchronous copies.
+// Each thread copies what it will read itself, so that nothing but its own
+// copies is waited for.  What is fetched runs at most one item ahead, so one
+// set of the next item's facts is enough.
+constexpr int kRingHeads = 4;
 
 __device__ __forceinline__ void heads_copy(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
+// GRAD: rows of x and of dy, of one tensor; else rows of x, of q then of k.
+template <class T, int KIND, bool GRAD> struct HeadsRing {
+    using Unit = HeadsUnit<T, KIND>;
+    static constexpr int kAhead = GRAD ? 3 : 4, kSlots = kAhead + 1;
+    static constexpr int kVectors = GRAD ? 4 : 2;             // of a thread and row
+    static constexpr int kBytes = kSlots * kVectors * kHeadsThreads * 16;
+    static_assert(kAhead <= kRingHeads, "at most one item ahead");
+
+    uint4 *mine;                // this thread's place in the ring's first vector
+    uint32_t item, step, total; // the group's item being fetched; items of the walk
+    uint32_t end;               // past the last item that any group of the CTA fetches as this one does
+    FastDiv parts;              // items of a token
+    const T *x, *dy;            // the row being fetched
+    int xsh, gsh;
+    int row, fill, slot;        // row of the item; ring slots to fill and to read
+    // of the item whose fetching began last
+    T *y;
+    int64_t position;
+    int count, ysh;
+    bool k;                     // of k
+
+    __device__ __forceinline__ void start(const HeadsArgs &a, const HeadsVecArgs &v, int one) {
+        uint32_t bs, h, b, s;
+        const bool live = item < total;   // an item past the end has no rows
+        parts.split(live ? item : 0, bs, h);
+        v.tokens.split(bs, b, s);
+        k = one >= 0 ? one == 1 : h >= v.q_items;
+        if (one < 0 && k) h -= v.q_items;
+        h *= kRingHeads;
+        position = heads_position(a, b, s);
+        x = static_cast<const T *>(k ? v.x[1].p : v.x[0].p) +
+            heads_near(k ? v.x[1] : v.x[0], b, s, h);
+        xsh = k ? v.x[1].sh : v.x[0].sh;
+        if constexpr (GRAD) {
+            dy = static_cast<const T *>(k ? v.dy[1].p : v.dy[0].p) +
+                 heads_near(k ? v.dy[1] : v.dy[0], b, s, h);
+            gsh = k ? v.dy[1].sh : v.dy[0].sh;
+        }
+        y = static_cast<T *>(const_cast<void *>(k ? v.y[1].p : v.y[0].p)) +
+            heads_near(k ? v.y[1] : v.y[0], b, s, h);
+        ysh = k ? v.y[1].sh : v.y[0].sh;
+        count = live ? min(kRingHeads, (k ? a.heads[1] : a.heads[0]) - (int)h) : 0;
+    }
+    // one: 0 or 1, the walk's tensor, or -1, both
+    __device__ __forceinline__ void fetch(const HeadsArgs &a, const HeadsVecArgs &v, const Unit &u,
+                                          int one) {
+        if (item < end) {
+            if (row == 0) start(a, v, one);
+            if (row < count) {
+                const uint32_t to = (uint32_t)__cvta_generic_to_shared(
+                    mine + fill * (kVectors * kHeadsThreads));
+                if (u.on) {
+                    heads_copy(to, x + u.off0);
+                    if constexpr (GRAD) heads_copy(to + 2 * kHeadsThreads * 16, dy + u.off0);
+                }
+                if (u.second) {
+                    heads_copy(to + kHeadsThreads * 16, x + u.off1);
+                    if constexpr (GRAD) heads_copy(to + 3 * kHeadsThreads * 16, dy + u.off1);
+                }
+                x += xsh;
+                if constexpr (GRAD) dy += gsh;
+            }
+            if (++row == kRingHeads) {
+                row = 0;
+                item += step;
+            }
+            fill = fill + 1 == kSlots ? 0 : fill + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // lanes without work, or without a second vector, read zeros
+    __device__ __forceinline__ void clear(const Unit &u) {
+        for (int i = 0; i < kSlots * kVectors; ++i)
+            if (!(i & 1 ? u.second : u.on)) mine[i * kHeadsThreads] = make_uint4(0, 0, 0, 0);
+    }
+    // the next row's vectors, once they have arrived
+    __device__ __forceinline__ const uint4 *take() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const uint4 *const p = mine + slot * (kVectors * kHeadsThreads);
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        return p;
+    }
+};
+
+// Norm and rotation of many rows: the ring's rows, a token's angles and weights
+// in registers over its item.
 template <class T, int KIND>
-__global__ void __launch_bounds__(kHeadsThreads, 2)
-k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
+__global__ void __launch_bounds__(kHeadsThreads, KIND == HEADS_ODD ? 2 : 3)
+k_heads_ring(const HeadsArgs a, const HeadsVecArgs v) {
+    using Ring = HeadsRing<T, KIND, false>;
     using Unit = HeadsUnit<T, KIND>;
     constexpr int N = Unit::N;
-    // the ring [kGradRing][x, x, dy, dy][threads], after it the weights [lanes][2 V] and
-    // (HEADS_ODD) the groups' rows; at the end the sums [groups of the CTA][dim]
-    extern __shared__ uint4 s_ring[];
-    float *const s_dw = reinterpret_cast<float *>(s_ring);
+    extern __shared__ uint4 s_ring[];   // the ring, after it (HEADS_ODD) the groups' rows
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
-    const bool which = (int)blockIdx.x >= v.ctas[0];
-    const uint32_t cta = blockIdx.x - (which ? v.ctas[0] : 0);
-    const uint32_t ctas = which ? v.ctas[1] : v.ctas[0];
-    const FastDiv parts = which ? v.heads[1] : v.heads[0];   // items of a token
-    const int heads = which ? a.heads[1] : a.heads[0];
-    const uint32_t total = (uint32_t)a.rows * parts.n;
     const int per = kHeadsThreads >> v.log_lanes, group = threadIdx.x >> v.log_lanes;
     layer_pdl_launch();
     Unit u;
     u.place(a, v, lane);
-    const int xsh = which ? v.x[1].sh : v.x[0].sh, gsh = which ? v.dy[1].sh : v.dy[0].sh,
-              ysh = which ? v.y[1].sh : v.y[0].sh;
-    const uint32_t step = ctas * per;
-    // what is fetched runs kGradAhead rows before what is worked on: at most one item
-    const T *x = nullptr, *dy = nullptr;
-    T *ny = nullptr;
-    int ncount = 0;
-    int64_t np = 0;
-    uint32_t fetched = cta * per;   // the CTA's item being fetched, its row, and the ring's place
-    int frow = 0, fslot = 0;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring + threadIdx.x);
-    auto fetch = [&]() {
-        if (fetched < total) {
-            if (frow == 0) {
-                const uint32_t item = fetched + group;
-                uint32_t bs, h, b, s;
-                parts.split(item < total ? item : 0, bs, h);
-                v.tokens.split(bs, b, s);
-                h *= kGradHeads;
-                np = heads_position(a, b, s);
-                x = static_cast<const T *>(which ? v.x[1].p : v.x[0].p) +
-                    heads_near(which ? v.x[1] : v.x[0], b, s, h);
-                dy = static_cast<const T *>(which ? v.dy[1].p : v.dy[0].p) +
-                     heads_near(which ? v.dy[1] : v.dy[0], b, s, h);
-                ny = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p)) +
-                     heads_near(which ? v.y[1] : v.y[0], b, s, h);
-                ncount = item < total ? min(kGradHeads, heads - (int)h) : 0;
+    Ring r{};
+    r.mine = s_ring + threadIdx.x;
+    r.item = blockIdx.x * per + group;
+    r.step = gridDim.x * per;
+    r.total = v.items;
+    r.end = v.items + group;
+    r.parts = v.per_token;
+    T *const shared_row = reinterpret_cast<T *>(s_ring + Ring::kBytes / 16) + group * a.dim;
+    r.clear(u);
+    layer_pdl_wait();
+#pragma unroll 1
+    for (int i = 0; i < Ring::kAhead; ++i) r.fetch(a, v, u, -1);
+    const float inv = 1.0f / (float)a.dim;
+    // every lane of a warp makes the same number of steps: the exchanges are warp-wide
+    for (uint32_t base = blockIdx.x * per; base < r.total; base += r.step) {
+        const int64_t p = r.position;
+        const int count = r.count;
+        T *y = r.y;
+        const int ysh = r.ysh;
+        if (count > 0 && p < 0 && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+        float2 ca[N], cb[N], sa[N], nb[N];
+        u.template folded<true>(a, v, r.k, p < 0 ? 0 : p, ca, cb, sa, nb);
+        const bool out = __any_sync(0xFFFFFFFFu, p < 0);   // rare
+#pragma unroll 1
+        for (int h = 0; h < kRingHeads; ++h) {
+            const uint4 *const in = r.take();
+            const uint4 x0 = in[0], x1 = in[kHeadsThreads];
+            r.fetch(a, v, u, -1);
+            float2 va[N], vb[N];
+            Unit::open(x0, x1, va, vb);
+            if constexpr (Unit::ODD) {
+                __syncwarp();   // the row before has been read
+                u.share(shared_row, x0, x1);
+                __syncwarp();
             }
-            if (frow < ncount) {
-                const uint32_t to = ring + fslot * (4 * kHeadsThreads * 16);
-                if (u.on) {
-                    heads_copy(to, x + u.off0);
-                    heads_copy(to + 2 * kHeadsThreads * 16, dy + u.off0);
+            float ss = u.squares(va, vb);
+            for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                va[i] = __fmul2_rn(va[i], both(rstd));
+                vb[i] = __fmul2_rn(vb[i], both(rstd));
+            }
+            if constexpr (Unit::ODD) u.turn_odd(shared_row, a.half, rstd, va, vb, ca, cb, sa, nb);
+            else u.turn(va, vb, ca, sa, nb, cb);
+            if (out) {
+                if (p < 0) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) va[i] = vb[i] = both(0.0f);
                 }
-                if (u.second) {
-                    heads_copy(to + kHeadsThreads * 16, x + u.off1);
-                    heads_copy(to + 3 * kHeadsThreads * 16, dy + u.off1);
-                }
-                x += xsh;
-                dy += gsh;
             }
-            if (++frow == kGradHeads) {
-                frow = 0;
-                fetched += step;
-            }
-            fslot = fslot + 1 == kGradRing ? 0 : fslot + 1;
+            if (h < count) u.store(y, va, vb);
+            y += ysh;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The gradient of norm and rotation.  CTAs take items of q or of k only, so a
+// thread's weight-gradient sums stay in registers to the end; the CTA's sums
+// then join in shared memory and go to its row of the workspace.
+template <class T, int KIND>
+__global__ void __launch_bounds__(kHeadsThreads, 2)
+k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
+    using Ring = HeadsRing<T, KIND, true>;
+    using Unit = HeadsUnit<T, KIND>;
+    constexpr int N = Unit::N;
+    // the ring, after it the weights [lanes][2 V] and (HEADS_ODD) the groups' rows; at
+    // the end the sums [groups of the CTA][dim]
+    extern __shared__ uint4 s_ring[];
+    float *const s_dw = reinterpret_cast<float *>(s_ring);
+    const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
+    const int which = (int)blockIdx.x >= v.ctas[0];
+    const uint32_t cta = blockIdx.x - (which ? v.ctas[0] : 0);
+    const int per = kHeadsThreads >> v.log_lanes, group = threadIdx.x >> v.log_lanes;
+    layer_pdl_launch();
+    Unit u;
+    u.place(a, v, lane);
+    Ring r{};
+    r.mine = s_ring + threadIdx.x;
+    r.parts = which ? v.heads[1] : v.heads[0];
+    r.total = (uint32_t)a.rows * r.parts.n;
+    r.item = cta * per + group;
+    r.step = (which ? v.ctas[1] : v.ctas[0]) * per;
+    r.end = r.total + group;
     // a lane's weights in shared memory, in the order that it uses them: sixteen
     // registers less
-    float4 *const s_w = reinterpret_cast<float4 *>(s_dw + kGradRingBytes / 4) + lane;
-    T *const row = reinterpret_cast<T *>(s_dw + kGradRingBytes / 4 +
-                                         (2 * Unit::V << v.log_lanes)) + group * a.dim;
+    float4 *const s_w = reinterpret_cast<float4 *>(s_ring + Ring::kBytes / 16) + lane;
+    T *const shared_row = reinterpret_cast<T *>(s_dw + Ring::kBytes / 4 +
+                                                (2 * Unit::V << v.log_lanes)) + group * a.dim;
+    r.clear(u);
     layer_pdl_wait();
-    // lanes without work, or without a second vector, read zeros from the ring
-    for (int i = 0; i < kGradRing * 4; ++i)
-        if (!(i & 1 ? u.second : u.on))
-            s_ring[i * kHeadsThreads + threadIdx.x] = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-    for (int i = 0; i < kGradAhead; ++i) fetch();
+    for (int i = 0; i < Ring::kAhead; ++i) r.fetch(a, v, u, which);
     if (threadIdx.x < lanes) {
         float2 wa[N], wb[N];
         u.weights(a, v, which, wa, wb);
@@ -762,36 +871,34 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
 #pragma unroll
     for (int i = 0; i < N; ++i) da[i] = db[i] = both(0.0f);
     bool bad = false;
-    int slot = 0;
     const float inv = 1.0f / (float)a.dim;
     // every lane of a warp makes the same number of steps: the exchanges are warp-wide
-    for (uint32_t base = cta * per; base < total; base += step) {
-        const int64_t p = np;
-        const int count = ncount;
-        T *y = ny;
+    for (uint32_t base = cta * per; base < r.total; base += r.step) {
+        const int64_t p = r.position;
+        const int count = r.count;
+        T *y = r.y;
+        const int ysh = r.ysh;
         bad |= count > 0 && p < 0;
         float2 c[N], sn[N], cb[N], sb[N];
         if constexpr (Unit::ODD) u.factors(a, p < 0 ? 0 : p, -1.0f, c, cb, sn, sb);
         else u.table(a, v, p < 0 ? 0 : p, c, sn);
         const bool out = __any_sync(0xFFFFFFFFu, p < 0);   // rare
 #pragma unroll 1
-        for (int h = 0; h < kGradHeads; ++h) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kGradAhead - 1) : "memory");
-            const uint4 *const mine = s_ring + slot * 4 * kHeadsThreads + threadIdx.x;
-            slot = slot + 1 == kGradRing ? 0 : slot + 1;
+        for (int h = 0; h < kRingHeads; ++h) {
+            const uint4 *const in = r.take();
             float2 xa[N], xb[N], ga[N], gb[N];
             {
-                const uint4 g0 = mine[2 * kHeadsThreads], g1 = mine[3 * kHeadsThreads];
+                const uint4 g0 = in[2 * kHeadsThreads], g1 = in[3 * kHeadsThreads];
                 Unit::open(g0, g1, ga, gb);
-                Unit::open(mine[0], mine[kHeadsThreads], xa, xb);
+                Unit::open(in[0], in[kHeadsThreads], xa, xb);
                 if constexpr (Unit::ODD) {
                     __syncwarp();   // the row before has been read
-                    u.share(row, g0, g1);
+                    u.share(shared_row, g0, g1);
                     __syncwarp();
                 }
             }
-            fetch();
-            if constexpr (Unit::ODD) u.turn_odd(row, a.half, 1.0f, ga, gb, c, cb, sn, sb);
+            r.fetch(a, v, u, which);
+            if constexpr (Unit::ODD) u.turn_odd(shared_row, a.half, 1.0f, ga, gb, c, cb, sn, sb);
             else u.turn_back(ga, gb, c, sn);
             float ss = u.squares(xa, xb);
             // sum of g w x, the absent elements' weights being 0
