@@ -17,9 +17,7 @@ using GemmT = __nv_bfloat16;
 template <int CTAS, int BN, bool SPLIT> static cudaError_t opt_in() {
     using L = TcLayout<CTAS, BN, SPLIT>;
     static_assert(L::kBytes <= kTcSmem, "shared memory of a CTA");
-    static const cudaError_t opted = cudaFuncSetAttribute(
-        k_gemm_tc<GemmT, CTAS, BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-    return opted;
+    return allow_smem<k_gemm_tc<GemmT, CTAS, BN, SPLIT>>(L::kBytes);
 }
 
 template <int CTAS, int BN, bool SPLIT>

@@ -392,8 +392,8 @@ template <int CTAS, int BN, bool SPLIT> struct TcLayout {
 // One tile after another (SPLIT = false): clusters of CTAS CTAs take tiles in
 // steps of their number; a pair's accumulator is 256 lanes over two CTAs, the
 // leader issues the products for both, each brings its own half of Q.
-// SPLIT: the CTAs of a cluster share one tile's k and join their sums through
-// each other's shared memory, in rank order; P = B, Q = A.
+// SPLIT: the CTAs of a cluster share one tile's k and join their sums in each
+// other's shared memory, in rank order; P = B, Q = A.
 template <class T, int CTAS, int BN, bool SPLIT>
 __global__ void __launch_bounds__(TcLayout<CTAS, BN, SPLIT>::kThreads, 1)
 k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
@@ -611,69 +611,74 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
         int p, q;
         place(cluster, p, q);
         const int64_t row0 = (int64_t)p * kTcRows, col0 = (int64_t)q * BN;
+        const int most = (int)min((int64_t)BN, a.m - col0);
         const int quarter = warp & 3;
-        // the stages are free once the products are done: they hold this CTA's sums, [BN][128]
-        float *const part = reinterpret_cast<float *>(s_base);
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         if (warp >= 4) {
             ok = tc_bar_wait(tfull(0), 0, a.limit);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
-            const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        }
+        if (ranks == 1) {
             const int64_t n = row0 + quarter * 32 + lane;
-            const float bias = ranks == 1 && n < a.n ? tc_bias<T>(a.e, n) : 0.0f;
+            if (warp >= 4) {
+                const float bias = n < a.n ? tc_bias<T>(a.e, n) : 0.0f;
 #pragma unroll 1
-            for (int c = 0; c < BN && col0 + c < a.m; c += 16) {
-                float v[16];
-                tc_load16(lanes + c, v);
-                if (!ok || kb1 == kb0) {
+                for (int c = 0; c < most; c += 16) {
+                    float v[16];
+                    tc_load16(lanes + c, v);
+                    if (!ok || kb1 == kb0) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                }
-                if (ranks > 1) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        part[(c + i) * kTcRows + quarter * 32 + lane] = v[i];
-                } else if (n < a.n) {
-                    const int most = (int)min((int64_t)16, a.m - col0 - c);
-                    tc_store_down<T, 16>(a.e, col0 + c, n, v, most, bias);
+                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                    }
+                    if (n < a.n) tc_store_down<T, 16>(a.e, col0 + c, n, v, most - c, bias);
                 }
             }
-            tc_fence_before();
-        }
-        if (ranks > 1) {
+        } else {
+            // Column c is joined by rank c mod ranks.  Once every CTA's products are
+            // done, the stages are free: each sends its sums to the ranks that join
+            // them, [from][column / ranks][128] there (stores that nobody waits for;
+            // reading them from each other instead: 8.1 against 7.3 us for
+            // [4,4096] x [4096,4096], and in vectors of four columns 7.6).
             __syncwarp();
             __syncthreads();
             tc_cluster_sync();
-            // this CTA joins every ranks-th column, in rank order
-            const int64_t n = row0 + (threadIdx.x & 127);
-            const int first = (threadIdx.x >> 7) * (int)ranks + (int)rank;
-            if (n < a.n) {
-                const float bias = tc_bias<T>(a.e, n);
-                const uint32_t mine = base + 4 * (threadIdx.x & 127);
-                const int step = (L::kThreads >> 7) * (int)ranks;
-                const int most = (int)min((int64_t)BN, a.m - col0);
-                // four columns at a time: their loads are on their way together
-                for (int c = first; c < most; c += 4 * step) {
-                    float z[4];
-                    for (uint32_t r = 0; r < ranks; ++r) {
-                        const uint32_t from = tc_map(mine, r);
-                        float v[4];
+            const uint32_t share = (BN / ranks) * kTcRows;   // floats that a rank receives from one
+            if (warp >= 4) {
+                const uint32_t mine = base + 4 * (rank * share + quarter * 32 + lane);
+                const uint32_t bits = ranks - 1, shift = __popc(bits);   // ranks is a power of two
+#pragma unroll 1
+                for (int c = 0; c < most; c += 16) {
+                    float v[16];
+                    tc_load16(lanes + c, v);
+                    if (!ok || kb1 == kb0) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            v[i] = 0.0f;
-                            if (c + i * step < most)
-                                asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                             : "=f"(v[i])
-                                             : "r"(from + 4 * kTcRows * (c + i * step))
-                                             : "memory");
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) z[i] = r == 0 ? v[i] : z[i] + v[i];
+                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c + i * step < most)
-                            tc_store_one<T>(a.e, col0 + c + i * step, n, z[i], bias);
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t to = tc_map(mine + 4 * kTcRows * ((c + i) >> shift),
+                                                   (c + i) & bits);
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v[i])
+                                     : "memory");
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            __syncthreads();
+            tc_cluster_sync();
+            const int64_t n = row0 + (threadIdx.x & 127);
+            if (n < a.n) {
+                const float bias = tc_bias<T>(a.e, n);
+                const float *const in = reinterpret_cast<const float *>(s_base) +
+                                        (threadIdx.x & 127);
+                for (int k = threadIdx.x >> 7;; k += L::kThreads >> 7) {
+                    const int c = k * (int)ranks + (int)rank;
+                    if (c >= most) break;
+                    float z = 0.0f;
+                    for (uint32_t r = 0; r < ranks; ++r) z += in[r * share + k * kTcRows];
+                    tc_store_one<T>(a.e, col0 + c, n, z, bias);
                 }
             }
         }

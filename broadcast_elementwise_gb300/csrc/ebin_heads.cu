@@ -239,8 +239,7 @@ template <class T, int KIND> cudaError_t launch_ring(const HeadsArgs &a, HeadsVe
     v.per_token = fast_div(v.q_items + (uint32_t)div_up(a.heads[1], kRingHeads));
     v.items = (uint32_t)a.rows * v.per_token.n;
     constexpr size_t smem = HeadsRing<T, KIND, false>::kBytes + (KIND == HEADS_ODD ? 8192 : 0);
-    static const cudaError_t opted = cudaFuncSetAttribute(
-        k_heads_ring<T, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t opted = allow_smem<k_heads_ring<T, KIND>>(smem);
     if (opted != cudaSuccess) return opted;
     const int64_t wave = (int64_t)heads_resident<k_heads_ring<T, KIND>>(smem) * current_sm_count();
     // Under three items a group the walk is too short to pay for itself (norm
@@ -257,8 +256,7 @@ cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, c
     // the ring, one group's weights (two vectors a lane) and, HEADS_ODD, the groups'
     // rows: at most 4 KB and 8 KB of them; the sums at the end fit the ring
     constexpr size_t most = HeadsRing<T, KIND, true>::kBytes + 4096 + (KIND == HEADS_ODD ? 8192 : 0);
-    static const cudaError_t opted = cudaFuncSetAttribute(
-        k_heads_vec_grad<T, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const cudaError_t opted = allow_smem<k_heads_vec_grad<T, KIND>>(most);
     if (opted != cudaSuccess) return opted;
     // one wave of CTAs, shared between q and k by their rows
     const int per = kHeadsThreads >> v.log_lanes;

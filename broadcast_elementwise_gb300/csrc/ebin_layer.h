@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -51,6 +52,20 @@ inline FastDiv fast_div(uint32_t n) {
     while (((uint64_t)1 << l) < n) ++l;
     const uint64_t m = (((uint64_t)1 << 32) * (((uint64_t)1 << l) - n)) / n + 1;
     return FastDiv{n, (uint32_t)m, l};
+}
+
+// Let KERNEL take `bytes` of dynamic shared memory on the current device (asked
+// of the runtime once per kernel and device).
+template <auto KERNEL> cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<bool> done[128];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool slot = dev >= 0 && dev < 128;
+    if (slot && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && slot) done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 // Launch with programmatic dependent launch (the kernel calls
