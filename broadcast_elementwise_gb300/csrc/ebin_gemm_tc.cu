@@ -16,16 +16,17 @@ using GemmT = __nv_bfloat16;
 
 template <int CTAS, int BN, bool SPLIT> static cudaError_t opt_in() {
     using L = TcLayout<CTAS, BN, SPLIT>;
-    static_assert(L::kBytes <= kTcSmem, "shared memory of a CTA");
     return allow_smem<k_gemm_tc<GemmT, CTAS, BN, SPLIT>>(L::kBytes);
 }
 
 template <int CTAS, int BN, bool SPLIT>
-static cudaError_t run(const CUtensorMap &p, const CUtensorMap &q, const TcArgs &a, int grid,
+static cudaError_t run(const CUtensorMap &p, const CUtensorMap &q, TcArgs a, int grid,
                        int cluster, cudaStream_t s) {
     using L = TcLayout<CTAS, BN, SPLIT>;
     const cudaError_t opted = opt_in<CTAS, BN, SPLIT>();
     if (opted != cudaSuccess) return opted;
+    a.stage = L::stage(a.q_mn);
+    a.stages = L::stages(a.q_mn);
     return launch_layer(k_gemm_tc<GemmT, CTAS, BN, SPLIT>, dim3((unsigned)grid), L::kThreads,
                         L::kBytes, s, cluster, p, q, a);
 }

@@ -34,6 +34,7 @@ struct TcArgs {
     int32_t p_tiles, q_tiles;   // tiles of P's rows (kTcRows * CTAs) and of Q's (BN)
     int32_t p_mn, q_mn;         // the operand is dense across k
     int32_t q_box;              // Q's rows a copy brings when it is dense along k
+    int32_t stage, stages;      // bytes of a stage of operands, and how many
     int32_t vec;                // y, z, residual (and the bias) take 16-byte (1) or 32-byte (2) accesses
     long long limit;            // clocks of a wait
     uint32_t *status;
@@ -368,25 +369,30 @@ __device__ __forceinline__ void tc_store16(const GemmEpilogue &e, int64_t m, int
     tc_put32<WIDE>(static_cast<T *>(e.y) + m * e.ldy + n, tc_pack8<T>(v), tc_pack8<T>(v + 8));
 }
 
-// What a kernel's shared memory holds, in bytes.
+// What a kernel's shared memory holds, in bytes.  The stages fill what is left:
+// a weight that streams from memory wants all the copies in flight that fit
+// (one CTA an SM with eight stages against two with four: [64,8192] x
+// [8192,8192] bf16 31.5 -> 28.5 us).
 template <int CTAS, int BN, bool SPLIT> struct TcLayout {
     static constexpr int kP = kTcRows * 128;
-    static constexpr int kQRows = (BN / CTAS + 63) / 64 * 64;
-    static constexpr int kQ = kQRows * 128;
-    static constexpr int kStage = kP + kQ;
+    static constexpr int kQRows = (BN / CTAS + 63) / 64 * 64;       // dense across k: blocks of 64
     static constexpr int kEpilogueWarps = SPLIT ? 4 : 8;
     static constexpr int kScratch = SPLIT ? 0 : kEpilogueWarps * 32 * 33 * 4;   // 32 x 32 transposes
     static constexpr int kBarriers = 512;
-    // split tiles of few columns leave room for a second CTA on the SM, whose
-    // set-up and first copies overlap this one's end
-    static constexpr int kRoom =
-        (SPLIT && BN <= 64 ? (kTcSmem - 1024) / 2 : kTcSmem) - 1024 - kScratch - kBarriers;
-    static constexpr int kStages = kRoom / kStage;
+    static constexpr int kRoom = kTcSmem - 1024 - kScratch - kBarriers;
     static constexpr int kAccumulators = SPLIT ? 1 : 2;
     static constexpr int kAccStep = BN <= 32 ? 32 : BN <= 64 ? 64 : BN <= 128 ? 128 : 256;
     static constexpr int kColumns = kAccumulators * kAccStep;
-    static constexpr int kBytes = 1024 + kStages * kStage + kScratch + kBarriers;
+    static constexpr int kBytes = kTcSmem;
     static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+    static constexpr int kMostStages = 12;
+    static_assert(8 * (2 * kMostStages + 5) + 8 <= kBarriers, "room for the barriers");
+    // bytes of a stage: P's rows, and Q's (rows or blocks), on 1024-byte boundaries
+    static int stage(bool q_mn) { return kP + (q_mn ? kQRows : (BN / CTAS + 7) / 8 * 8) * 128; }
+    static int stages(bool q_mn) {
+        const int n = kRoom / stage(q_mn);
+        return n > kMostStages ? kMostStages : n;
+    }
 };
 
 // One tile after another (SPLIT = false): clusters of CTAS CTAs take tiles in
@@ -403,13 +409,13 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     extern __shared__ uint8_t s_raw[];
     const uint32_t base = (tc_smem(s_raw) + 1023) & ~1023u;
     uint8_t *const s_base = s_raw + (base - tc_smem(s_raw));
-    const uint32_t scratch = base + L::kStages * L::kStage;
+    const uint32_t scratch = base + a.stages * a.stage;
     const uint32_t bars = scratch + L::kScratch;
     auto full = [&](int i) { return bars + 8 * i; };
-    auto empty = [&](int i) { return bars + 8 * (L::kStages + i); };
-    auto tfull = [&](int i) { return bars + 8 * (2 * L::kStages + i); };
-    auto tempty = [&](int i) { return bars + 8 * (2 * L::kStages + 2 + i); };
-    const uint32_t drain = bars + 8 * (2 * L::kStages + 4);
+    auto empty = [&](int i) { return bars + 8 * (L::kMostStages + i); };
+    auto tfull = [&](int i) { return bars + 8 * (2 * L::kMostStages + i); };
+    auto tempty = [&](int i) { return bars + 8 * (2 * L::kMostStages + 2 + i); };
+    const uint32_t drain = bars + 8 * (2 * L::kMostStages + 4);
     const uint32_t s_tmem = drain + 8;
     // uniform in the warp, so that what follows from it can stay in uniform registers
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -417,7 +423,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     const bool leader = CTAS == 1 || rank == 0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < L::kStages; ++i) {
+        for (int i = 0; i < a.stages; ++i) {
             tc_bar_init(full(i), 1);
             tc_bar_init(empty(i), 1);
         }
@@ -455,7 +461,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     if (warp == 0) {
         // the whole warp walks the loop (its values stay uniform), one lane issues
         const bool one = tc_elect();
-        const uint32_t q_bytes = a.q_mn ? L::kQ : a.q_box * 128;
+        const uint32_t q_bytes = (a.q_mn ? L::kQRows : a.q_box) * 128;
         int s = 0, it = 0;
         uint32_t phase = 1;
         for (int t = cluster; t < tiles && ok; t += clusters) {
@@ -469,7 +475,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                     break;
                 }
                 if (one) {
-                    const uint32_t sp = base + s * L::kStage, sq = sp + L::kP;
+                    const uint32_t sp = base + s * a.stage, sq = sp + L::kP;
                     const uint32_t bar = CTAS == 2 ? tc_map(full(s), 0) : full(s);
                     if (leader) tc_bar_expect(full(s), CTAS * (L::kP + q_bytes));
                     if (a.p_mn) {
@@ -486,15 +492,15 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                         tc_copy<CTAS>(sq, &q_map, kb * kTcBK, qr, bar);
                     }
                 }
-                if (++s == L::kStages) {
+                if (++s == a.stages) {
                     s = 0;
                     phase ^= 1;
                 }
             }
         }
         if (!ok && leader)   // wait for what is in flight
-            for (int j = max(0, it - L::kStages); j < it; ++j)
-                tc_bar_wait(full(j % L::kStages), j / L::kStages & 1, a.limit);
+            for (int j = max(0, it - a.stages); j < it; ++j)
+                tc_bar_wait(full(j % a.stages), j / a.stages & 1, a.limit);
     } else if (warp == 1 && leader) {
         // f32 accumulators; operands f16 or bf16, their major directions; N / 8, M / 16
         constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
@@ -521,8 +527,8 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                 }
                 if (one) {
                     // addresses stay below 2^18: no carry leaves the descriptor's field
-                    uint64_t pd = p_desc + (uint32_t)(s * (L::kStage >> 4));
-                    uint64_t qd = q_desc + (uint32_t)(s * (L::kStage >> 4));
+                    uint64_t pd = p_desc + (uint32_t)(s * (a.stage >> 4));
+                    uint64_t qd = q_desc + (uint32_t)(s * (a.stage >> 4));
 #pragma unroll
                     for (int k = 0; k < kTcBK / 16; ++k) {
                         tc_mma<CTAS>(d, pd, qd, idesc, kb > kb0 || k > 0);
@@ -531,7 +537,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                     }
                     tc_commit<CTAS>(empty(s));
                 }
-                if (++s == L::kStages) {
+                if (++s == a.stages) {
                     s = 0;
                     phase ^= 1;
                 }
