@@ -1,54 +1,123 @@
 // The activations of a product's epilogue and their derivatives, in binary32.
+//
+// 16-bit data takes fast forms, off by a few units of 2^-23 against the 2^-8 or
+// 2^-11 of the rounding that follows: the hardware's 2^x and 1/x, and the
+// normal distribution by formula 7.1.26 of Abramowitz and Stegun's Handbook of
+// Mathematical Functions (error below 1.5e-7):
+//     erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2),  t = 1 / (1 + 0.3275911 x),  x >= 0
+// binary32 data takes the full ones.
 #pragma once
 
 #include "ebin_layer.h"
 
 namespace ebin {
 
-// exp and the quotient are the fast forms (a few units of 2^-23, against the
-// 2^-8 or 2^-11 of the rounding to 16 bits that follows).
-__device__ __forceinline__ float act_sigmoid(float z) {
-    return __fdividef(1.0f, 1.0f + __expf(-z));
-}
+constexpr float kLog2e = 1.44269504f;
 
+__device__ __forceinline__ float act_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float act_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float act_sigmoid(float z) {
+    return act_rcp(1.0f + act_ex2(-kLog2e * z));
+}
+// Phi(z) and e = exp(-z^2 / 2); the lower tail without cancellation
+__device__ __forceinline__ float act_normal(float z, float &e) {
+    e = act_ex2(z * z * (-0.5f * kLog2e));
+    const float t = act_rcp(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.0f));
+    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    q = fmaf(q, t, 0.5f * 1.421413741f);
+    q = fmaf(q, t, 0.5f * -0.284496736f);
+    q = fmaf(q, t, 0.5f * 0.254829592f) * t * e;
+    return z < 0.0f ? q : 1.0f - q;
+}
 __device__ __forceinline__ float act_tanh_arg(float z) {   // 2 sqrt(2/pi) (z + 0.044715 z^3)
     return z * fmaf(z * z, 0.0713548162726f, 1.59576912161f);
 }
 
+// The activation, for 16-bit data.
 template <int ACT> __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == EBIN_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays
-    if constexpr (ACT == EBIN_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.707106781187f));
+    if constexpr (ACT == EBIN_ACT_GELU) {
+        float e;
+        return z * act_normal(z, e);
+    }
     // (1 + tanh u) / 2 = sigmoid(2 u)
     if constexpr (ACT == EBIN_ACT_GELU_TANH) return z * act_sigmoid(act_tanh_arg(z));
     if constexpr (ACT == EBIN_ACT_SILU) return z * act_sigmoid(z);
     return z;
 }
 
-// The derivative.  FAST: with the fast forms of exp and the quotient, for
-// 16-bit data; otherwise with the full ones (the result is kept in 32 bits).
-template <bool FAST> __device__ __forceinline__ float act_exp(float x) {
-    return FAST ? __expf(x) : expf(x);
-}
-template <bool FAST> __device__ __forceinline__ float act_over(float x) {
-    return FAST ? __fdividef(1.0f, x) : 1.0f / x;
-}
-template <int ACT, bool FAST> __device__ __forceinline__ float act_slope(float z) {
+// The derivative in full binary32.
+template <int ACT> __device__ __forceinline__ float act_slope_full(float z) {
     if constexpr (ACT == EBIN_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     if constexpr (ACT == EBIN_ACT_GELU)
-        return fmaf(z * 0.398942280401f, act_exp<FAST>(-0.5f * z * z),
+        return fmaf(z * 0.398942280401f, expf(-0.5f * z * z),
                     0.5f * (1.0f + erff(z * 0.707106781187f)));
     if constexpr (ACT == EBIN_ACT_GELU_TANH) {
-        const float s = act_over<FAST>(1.0f + act_exp<FAST>(-act_tanh_arg(z)));
+        const float s = 1.0f / (1.0f + expf(-act_tanh_arg(z)));
         const float du = fmaf(z * z, 0.214064448818f, 1.59576912161f);
         const float t = s * (1.0f - s);
         return t == 0.0f ? s : fmaf(z * t, du, s);   // flat far out, where z du may be infinite
     }
     if constexpr (ACT == EBIN_ACT_SILU) {
-        const float s = act_over<FAST>(1.0f + act_exp<FAST>(-z));
+        const float s = 1.0f / (1.0f + expf(-z));
         const float t = s * (1.0f - s);
         return t == 0.0f ? s : fmaf(z, t, s);
     }
     return 1.0f;
+}
+
+__device__ __forceinline__ float2 act_pair(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 act_ex2(float2 x) {
+    return make_float2(act_ex2(x.x), act_ex2(x.y));
+}
+__device__ __forceinline__ float2 act_rcp(float2 x) {
+    return make_float2(act_rcp(x.x), act_rcp(x.y));
+}
+
+// The derivative for 16-bit data, two at a time on the packed binary32 pipe.
+template <int ACT> __device__ __forceinline__ float2 act_slope2(float2 z) {
+    if constexpr (ACT == EBIN_ACT_RELU)
+        return make_float2(act_slope_full<ACT>(z.x), act_slope_full<ACT>(z.y));
+    if constexpr (ACT == EBIN_ACT_GELU) {
+        const float2 zz = __fmul2_rn(z, z);
+        const float2 e = act_ex2(__fmul2_rn(zz, act_pair(-0.5f * kLog2e)));
+        const float2 t = act_rcp(__ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)),
+                                            act_pair(0.3275911f * 0.70710678f), act_pair(1.0f)));
+        float2 q = __ffma2_rn(t, act_pair(0.5f * 1.061405429f), act_pair(0.5f * -1.453152027f));
+        q = __ffma2_rn(q, t, act_pair(0.5f * 1.421413741f));
+        q = __ffma2_rn(q, t, act_pair(0.5f * -0.284496736f));
+        q = __ffma2_rn(q, t, act_pair(0.5f * 0.254829592f));
+        q = __fmul2_rn(__fmul2_rn(q, t), e);
+        const float2 up = make_float2(z.x < 0.0f ? q.x : 1.0f - q.x, z.y < 0.0f ? q.y : 1.0f - q.y);
+        return __ffma2_rn(__fmul2_rn(z, act_pair(0.39894228f)), e, up);
+    }
+    if constexpr (ACT == EBIN_ACT_GELU_TANH) {
+        const float2 zz = __fmul2_rn(z, z);
+        const float2 u = __fmul2_rn(
+            z, __ffma2_rn(zz, act_pair(0.0713548163f), act_pair(1.59576912f)));
+        const float2 s = act_rcp(
+            __fadd2_rn(act_ex2(__fmul2_rn(u, act_pair(-kLog2e))), act_pair(1.0f)));
+        const float2 t = __ffma2_rn(make_float2(-s.x, -s.y), s, s);
+        const float2 du = __ffma2_rn(zz, act_pair(0.214064449f), act_pair(1.59576912f));
+        const float2 r = __ffma2_rn(__fmul2_rn(z, t), du, s);
+        // flat far out, where z du may be infinite
+        return make_float2(t.x == 0.0f ? s.x : r.x, t.y == 0.0f ? s.y : r.y);
+    }
+    if constexpr (ACT == EBIN_ACT_SILU) {
+        const float2 s = act_rcp(
+            __fadd2_rn(act_ex2(__fmul2_rn(z, act_pair(-kLog2e))), act_pair(1.0f)));
+        const float2 t = __ffma2_rn(make_float2(-s.x, -s.y), s, s);
+        return __ffma2_rn(z, t, s);
+    }
+    return act_pair(1.0f);
 }
 
 }  // namespace ebin

@@ -180,7 +180,10 @@ struct Shape {
 
 // Which tiles: the least of an estimate in nanoseconds.  A step of k takes a
 // CTA its matrix instructions or its copies, whichever is longer (on a pair
-// 1.05 ns a column; copies at 190 bytes a ns); a tile's end costs 12 ns a column
+// 1.05 ns a column; copies at 190 bytes a ns), and 24 ns that keep wide tiles,
+// which move fewer bytes a product, ahead of a narrower one's last wave where
+// that gains under a tenth ([4096,4096] x [4096,8192] on 160 columns 163 us, on
+// 256 155 us; 4096^3 on 256 columns 98 us, on 224 87 us); a tile's end costs 12 ns a column
 // once, the sums of split tiles 1.5 us more.
 //   pair   256 rows of A by 64 to 256 columns, a CTA pair each, waves of pairs
 //   split  128 columns of B by 16 to 128 rows of A, k cut in up to eight while
@@ -214,7 +217,7 @@ Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
         for (int bn : {256, 224, 192, 160, 128, 96, 64}) {
             s.bn = bn;
             const int64_t waves = div_up(div_up(at.m, 2 * kTcRows) * div_up(at.n, bn), sms / 2);
-            const double step = std::max(1.05 * bn, (16384 + 64.0 * bn) / 190) + 10;
+            const double step = std::max(1.05 * bn, (16384 + 64.0 * bn) / 190) + 24;
             consider(s, waves * kblocks * step + 12.0 * bn);
         }
     }

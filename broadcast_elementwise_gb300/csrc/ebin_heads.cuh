@@ -6,8 +6,6 @@
 // one rounding to the element type at the store.
 #pragma once
 
-#include <type_traits>
-
 #include "ebin_layer.h"
 
 namespace ebin {
@@ -220,24 +218,6 @@ __device__ __forceinline__ int64_t heads_near(const HeadsNear &t, uint32_t b, ui
     return (int64_t)b * t.sb + (int64_t)(int32_t)s * t.st + (int64_t)(int32_t)h * t.sh;
 }
 
-// Two elements of a 16-bit word, or two binary32 elements, as a binary32 pair.
-template <class T> __device__ __forceinline__ float2 heads_open2(uint32_t w) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value)
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    else
-        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-
-template <class T> __device__ __forceinline__ uint32_t heads_pack2(float2 v) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const __nv_bfloat162 p = __float22bfloat162_rn(v);
-        return *reinterpret_cast<const uint32_t *>(&p);
-    } else {
-        const __half2 p = __float22half2_rn(v);
-        return *reinterpret_cast<const uint32_t *>(&p);
-    }
-}
-
 template <class T> __device__ __forceinline__ uint4 heads_load(const T *p) {
     uint4 r;
     // not .nc: an output may be its own input
@@ -299,14 +279,14 @@ template <class T, int KIND> struct HeadsUnit {
             split(e, a, b);
         } else {
             float2 e[8];
-            e[0] = heads_open2<T>(x0.x);
-            e[1] = heads_open2<T>(x0.y);
-            e[2] = heads_open2<T>(x0.z);
-            e[3] = heads_open2<T>(x0.w);
-            e[4] = heads_open2<T>(x1.x);
-            e[5] = heads_open2<T>(x1.y);
-            e[6] = heads_open2<T>(x1.z);
-            e[7] = heads_open2<T>(x1.w);
+            e[0] = open2<T>(x0.x);
+            e[1] = open2<T>(x0.y);
+            e[2] = open2<T>(x0.z);
+            e[3] = open2<T>(x0.w);
+            e[4] = open2<T>(x1.x);
+            e[5] = open2<T>(x1.y);
+            e[6] = open2<T>(x1.z);
+            e[7] = open2<T>(x1.w);
             split(e, a, b);
         }
     }
@@ -342,10 +322,10 @@ template <class T, int KIND> struct HeadsUnit {
             r1 = make_uint4(__float_as_uint(e[2].x), __float_as_uint(e[2].y),
                             __float_as_uint(e[3].x), __float_as_uint(e[3].y));
         } else {
-            r0 = make_uint4(heads_pack2<T>(e[0]), heads_pack2<T>(e[1]), heads_pack2<T>(e[2]),
-                            heads_pack2<T>(e[3]));
-            r1 = make_uint4(heads_pack2<T>(e[V - 4]), heads_pack2<T>(e[V - 3]),
-                            heads_pack2<T>(e[V - 2]), heads_pack2<T>(e[V - 1]));
+            r0 = make_uint4(pack2<T>(e[0]), pack2<T>(e[1]), pack2<T>(e[2]),
+                            pack2<T>(e[3]));
+            r1 = make_uint4(pack2<T>(e[V - 4]), pack2<T>(e[V - 3]),
+                            pack2<T>(e[V - 2]), pack2<T>(e[V - 1]));
         }
         if (on) *reinterpret_cast<uint4 *>(p + off0) = r0;
         if (second) *reinterpret_cast<uint4 *>(p + off1) = r1;

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -115,6 +116,24 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
     return __float2bfloat16_rn(x);
+}
+
+// Two elements of a 16-bit word as a binary32 pair, and back.
+template <class T> __device__ __forceinline__ float2 open2(uint32_t w) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+template <class T> __device__ __forceinline__ uint32_t pack2(float2 v) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 p = __float22bfloat162_rn(v);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    } else {
+        const __half2 p = __float22half2_rn(v);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    }
 }
 #endif
 
