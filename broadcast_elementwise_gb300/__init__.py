@@ -17,6 +17,13 @@ Typical use::
     desc = eb.Descriptor("Mod", "float32", fmod=0, opset=28)
     plan = eb.Plan(desc, a.shape, b.shape)
     eb.execute(plan, a, b, out)
+
+What a transformer layer needs around its attention::
+
+    cos, sin = eb.rotary_table(8192, 128)
+    qkv = eb.gemm(x, w, bias, trans_b=True)      # x [rows, k], w [n, k]
+    q, k, v = qkv.view(batch, tokens, -1, 128).split([32, 8, 8], dim=2)
+    eb.qk_norm_rotary(q, k, wq, wk, cos, sin, positions, out=(q, k))
 """
 from __future__ import annotations
 

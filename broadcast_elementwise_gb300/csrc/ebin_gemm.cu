@@ -183,7 +183,7 @@ struct Shape {
 // 1.05 ns a column; copies at 190 bytes a ns), and 24 ns that keep wide tiles,
 // which move fewer bytes a product, ahead of a narrower one's last wave where
 // that gains under a tenth ([4096,4096] x [4096,8192] on 160 columns 163 us, on
-// 256 155 us; 4096^3 on 256 columns 98 us, on 224 87 us); a tile's end costs 12 ns a column
+// 256 146 us; 4096^3 on 256 columns 98 us, on 224 87 us); a tile's end costs 12 ns a column
 // once, the sums of split tiles 1.5 us more.
 //   pair   256 rows of A by 64 to 256 columns, a CTA pair each, waves of pairs
 //   split  128 columns of B by 16 to 128 rows of A, k cut in up to eight while
@@ -284,7 +284,8 @@ cudaError_t launch_gemm(const ebin_gemm_plan_s &p, const void *A, const void *B,
     const int64_t tiles = p_tiles * q_tiles;
     const int cluster = shape.pair ? 2 : shape.split;
     const int64_t clusters = shape.pair ? std::min<int64_t>(tiles, current_sm_count() / 2) : tiles;
-    if (clusters * cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (tiles > 0x7FFFFFFF || clusters * cluster > 0x7FFFFFFF)
+        return cudaErrorInvalidConfiguration;
     return (bf16 ? launch_tc_bf16 : launch_tc_f16)(
         maps[0], maps[1], t, shape.bn, shape.pair, (int)clusters * cluster, cluster, s);
 }

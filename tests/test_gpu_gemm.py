@@ -83,6 +83,51 @@ def test_product(size, ta, tb):
     assert eb.get_device_status() == 0
 
 
+# one size for every tile and split that the plan can pick on 152 SMs, and the
+# paired tiles once more where n lets rows go out in vectors
+TILES = [(270, 3650, 520), (270, 3648, 520), (779, 5700, 264), (779, 5696, 264),
+         (1672, 5572, 520), (1672, 5568, 520), (561, 4838, 1032), (561, 4832, 1032),
+         (2634, 1397, 4096), (2634, 1392, 4096), (82, 16, 40), (68, 5117, 264), (68, 5120, 264),
+         (272, 5164, 200), (4844, 43, 4096), (2418, 18, 2048), (70, 16, 2048), (1, 17, 40),
+         (1, 4647, 2048), (1, 16, 1032), (1, 16, 2048), (20, 17, 40), (17, 4705, 2048),
+         (20, 16, 1032), (22, 17, 2048), (36, 16, 40), (34, 4704, 2048), (35, 16, 1032),
+         (34, 16, 2048)]
+
+
+@pytest.mark.parametrize("size", TILES, ids=str)
+@pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False), (True, True)])
+def test_every_tile(size, ta, tb):
+    m, n, k = size
+    g = gen(11)
+    dtype = BF16 if (ta + tb) % 2 else F16
+    a = matrix(g, m, k, dtype, "dense", ta)
+    b = (matrix(g, k, n, F32, "dense", tb) / math.sqrt(k)).to(dtype)
+    bias, r = normal(g, n), normal(g, m, n, dtype=dtype)
+    pre = torch.empty(m, n, dtype=dtype, device="cuda")
+    z, y, ez, ey = reference(a, b, bias, r, "gelu", ta, tb)
+    got = eb.gemm(a, b, bias, r, trans_a=ta, trans_b=tb, activation="gelu", preact=pre)
+    check(got, y, ey, "y")
+    check(pre, z, ez, "z")
+    assert torch.equal(got, eb.gemm(a, b, bias, r, trans_a=ta, trans_b=tb, activation="gelu"))
+    assert eb.get_device_status() == 0
+
+
+def test_output_past_32_bits():
+    """y of over 2^31 elements: the last rows against the same rows alone."""
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB of device memory")
+    g = gen(12)
+    m, n, k = 70016, 32768, 64
+    a, b = normal(g, m, k, dtype=BF16), normal(g, n, k, dtype=BF16)
+    y = eb.gemm(a, b, trans_b=True)
+    for rows in (slice(0, 256), slice(65536, 65792), slice(m - 256, m)):
+        assert torch.equal(y[rows], eb.gemm(a[rows], b, trans_b=True))
+    dz, _ = eb.gemm_epilogue_grad(y, y, activation="relu", out=y)
+    for rows in (slice(0, 256), slice(m - 256, m)):
+        want = eb.gemm(a[rows], b, trans_b=True)
+        assert torch.equal(dz[rows], want.clamp_min(0))
+
+
 @pytest.mark.parametrize("size", [(1, 512, 768), (9, 264, 512), (70, 130, 200), (260, 520, 136),
                                   (1100, 700, 264)], ids=str)
 @pytest.mark.parametrize("kind", ["none", "relu", "gelu", "gelu_tanh", "silu"])

@@ -83,9 +83,17 @@ SHAPES = [
     (1, 61, 4, 4, 16, 8, "interleaved", "dense"),
 ]
 
+# enough rows that groups of lanes walk several items each
+MANY = [
+    (2, 4096, 32, 8, 128, 128, "half", "packed"),
+    (1, 9001, 20, 5, 96, 46, "half", "dense"),
+    (3, 4099, 13, 3, 80, 40, "interleaved", "packed"),
+    (1, 12001, 9, 9, 64, 32, "half", "heads_first"),
+]
+
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + MANY, ids=str)
 @pytest.mark.parametrize("gradient", [False, True])
 def test_rotary(shape, dtype, gradient):
     B, S, Hq, Hk, D, r, layout, how = shape
@@ -104,7 +112,7 @@ def test_rotary(shape, dtype, gradient):
 
 
 @pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (F16, F32), (F32, F32), (BF16, None)])
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + MANY, ids=str)
 def test_norm_rotary(shape, dtype, wdtype):
     B, S, Hq, Hk, D, r, layout, how = shape
     g = gen(2)
@@ -126,7 +134,7 @@ def test_norm_rotary(shape, dtype, wdtype):
 
 
 @pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (F16, F32), (F32, F32), (BF16, None)])
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + MANY, ids=str)
 def test_norm_rotary_gradient(shape, dtype, wdtype):
     B, S, Hq, Hk, D, r, layout, how = shape
     g = gen(3)
@@ -192,12 +200,13 @@ def test_positions_default_types_and_strides():
     assert only[1] is None and torch.equal(only[0], plain[0])
 
 
+@pytest.mark.parametrize("S", [6, 20000])
 @pytest.mark.parametrize("D,r", [(64, 64), (64, 30)])
-def test_positions_outside_the_table(D, r):
+def test_positions_outside_the_table(D, r, S):
     """Rows of a token outside the table are zeros, set the status bit and add
     nothing to the weight gradients; the others are untouched."""
     g = gen(6)
-    B, S, H = 2, 6, 3
+    B, H = 2, 3
     q, k = normal(g, B, S, H, D, dtype=BF16), normal(g, B, S, H, D, dtype=BF16)
     cos, sin = tables(16, r)
     at = torch.randint(0, 16, (B, S), generator=g, device="cuda")
@@ -214,6 +223,12 @@ def test_positions_outside_the_table(D, r):
         assert torch.equal(a[keep], b[keep])
         assert (b[~keep] == 0).all()
     w = torch.ones(D, device="cuda", dtype=BF16)
+    normed = eb.qk_norm_rotary(q, k, w, w, cos, sin, at)
+    got = eb.qk_norm_rotary(q, k, w, w, cos, sin, bad)
+    assert eb.get_device_status() == eb.DEVICE_POSITION_RANGE
+    for a, b in zip(normed, got):
+        assert torch.equal(a[keep], b[keep])
+        assert (b[~keep] == 0).all()
     zero = q.clone()
     zero[~keep] = 0
     full = eb.qk_norm_rotary_grad(zero, zero, q, k, w, w, cos, sin, at)
