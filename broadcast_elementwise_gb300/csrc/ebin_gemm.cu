@@ -183,8 +183,11 @@ struct Shape {
 // 1.05 ns a column; copies at 190 bytes a ns), and 24 ns that keep wide tiles,
 // which move fewer bytes a product, ahead of a narrower one's last wave where
 // that gains under a tenth ([4096,4096] x [4096,8192] on 160 columns 163 us, on
-// 256 146 us; 4096^3 on 256 columns 98 us, on 224 87 us); a tile's end costs 12 ns a column
-// once, the sums of split tiles 1.5 us more.
+// 256 146 us; 4096^3 on 256 columns 98 us, on 224 87 us); a tile's end costs 12 ns
+// a column once, the sums of split tiles 1.5 us more.  On single CTAs a step
+// takes 140 ns to 64 columns, 230 to 128 with every SM at it ([256,4096] x
+// [4096,4096] on pairs of 64 columns 12.6 us, on split tiles of 128 13.4;
+// [128,4096] x [4096,4096] 13.0 and 10.9).
 //   pair   256 rows of A by 64 to 256 columns, a CTA pair each, waves of pairs
 //   split  128 columns of B by 16 to 128 rows of A, k cut in up to eight while
 //          all clusters fit at once ([4,4096] x [4096,4096] cut in eight, two
@@ -207,7 +210,7 @@ Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
         if (s.split > 1 && (kblocks < s.split * 4 ||
                             tiles > (bf16 ? tc_clusters_bf16 : tc_clusters_f16)(s.bn, s.split)))
             break;
-        const double step = s.bn <= 64 ? 140 : 170;
+        const double step = s.bn <= 64 ? 140 : 230;
         consider(s, div_up(tiles * s.split, sms) * (kblocks / s.split) * step + 12.0 * s.bn +
                         (s.split > 1 ? 1500 : 0));
     }

@@ -649,18 +649,17 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                 }
             }
         } else {
-            // Column c is joined by rank c mod ranks.  Once every CTA's products are
+            // A rank joins `width` neighbouring columns.  Once every CTA's products are
             // done, the stages are free: each sends its sums to the ranks that join
-            // them, [from][column / ranks][128] there (stores that nobody waits for;
-            // reading them from each other instead: 8.1 against 7.3 us for
-            // [4,4096] x [4096,4096], and in vectors of four columns 7.6).
+            // them, [from][width / 4][128 lanes][4] there, a warp's vectors side by side
+            // ([256,4096] x [4096,4096] 13.4 us, column by column 18.7).
             __syncwarp();
             __syncthreads();
             tc_cluster_sync();
-            const uint32_t share = (BN / ranks) * kTcRows;   // floats that a rank receives from one
+            const uint32_t width = BN / ranks, shift = __popc(width - 1);   // powers of two
+            const uint32_t four = width < 4 ? width : 4;                    // columns of a vector
             if (warp >= 4) {
-                const uint32_t mine = base + 4 * (rank * share + quarter * 32 + lane);
-                const uint32_t bits = ranks - 1, shift = __popc(bits);   // ranks is a power of two
+                const uint32_t at = quarter * 32 + lane;
 #pragma unroll 1
                 for (int c = 0; c < most; c += 16) {
                     float v[16];
@@ -669,12 +668,24 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = 0.0f;
                     }
+                    auto place_of = [&](int i) {
+                        const uint32_t within = (uint32_t)(c + i) & (width - 1);
+                        return tc_map(base + 4 * (rank * width * kTcRows + within * kTcRows +
+                                                  at * four), (uint32_t)(c + i) >> shift);
+                    };
+                    if (four == 4) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t to = tc_map(mine + 4 * kTcRows * ((c + i) >> shift),
-                                                   (c + i) & bits);
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v[i])
-                                     : "memory");
+                        for (int i = 0; i < 16; i += 4)
+                            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::
+                                             "r"(place_of(i)), "f"(v[i]), "f"(v[i + 1]),
+                                         "f"(v[i + 2]), "f"(v[i + 3])
+                                         : "memory");
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2)
+                            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::
+                                             "r"(place_of(i)), "f"(v[i]), "f"(v[i + 1])
+                                         : "memory");
                     }
                 }
                 tc_fence_before();
@@ -682,17 +693,31 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
             __syncwarp();
             __syncthreads();
             tc_cluster_sync();
-            const int64_t n = row0 + (threadIdx.x & 127);
+            const int row = threadIdx.x & 127;
+            const int64_t n = row0 + row;
+            const int first = (int)(rank * width), last = min(first + (int)width, most);
             if (n < a.n) {
                 const float bias = tc_bias<T>(a.e, n);
-                const float *const in = reinterpret_cast<const float *>(s_base) +
-                                        (threadIdx.x & 127);
-                for (int k = threadIdx.x >> 7;; k += L::kThreads >> 7) {
-                    const int c = k * (int)ranks + (int)rank;
-                    if (c >= most) break;
-                    float z = 0.0f;
-                    for (uint32_t r = 0; r < ranks; ++r) z += in[r * share + k * kTcRows];
-                    tc_store_one<T>(a.e, col0 + c, n, z, bias);
+                const float *const in = reinterpret_cast<const float *>(s_base) + row * four;
+                // two threads a row, a vector of columns at a time
+                for (int c = first + (threadIdx.x >> 7) * (int)four; c < last;
+                     c += (L::kThreads >> 7) * (int)four) {
+                    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (uint32_t r = 0; r < ranks; ++r) {
+                        const float *const from = in + (r * width + (c - first)) * kTcRows;
+                        if (four == 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(from);
+                            z[0] += f.x;
+                            z[1] += f.y;
+                            z[2] += f.z;
+                            z[3] += f.w;
+                        } else {
+                            const float2 f = *reinterpret_cast<const float2 *>(from);
+                            z[0] += f.x;
+                            z[1] += f.y;
+                        }
+                    }
+                    tc_store_down<T, 4>(a.e, col0 + c, n, z, min((int)four, last - c), bias);
                 }
             }
         }

@@ -91,7 +91,7 @@ TILES = [(270, 3650, 520), (270, 3648, 520), (779, 5700, 264), (779, 5696, 264),
          (272, 5164, 200), (4844, 43, 4096), (2418, 18, 2048), (70, 16, 2048), (1, 17, 40),
          (1, 4647, 2048), (1, 16, 1032), (1, 16, 2048), (20, 17, 40), (17, 4705, 2048),
          (20, 16, 1032), (22, 17, 2048), (36, 16, 40), (34, 4704, 2048), (35, 16, 1032),
-         (34, 16, 2048)]
+         (34, 16, 2048), (561, 4838, 2048), (561, 4832, 2048), (346, 5212, 520), (65, 7305, 4096)]
 
 
 @pytest.mark.parametrize("size", TILES, ids=str)
