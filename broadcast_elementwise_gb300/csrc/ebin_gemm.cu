@@ -25,10 +25,12 @@ int tc_clusters_f16(int bn, int cluster);
 int tc_clusters_bf16(int bn, int cluster);
 
 // Lay a matrix of 16-bit elements out anew, its rows on 16-byte boundaries.  A
-// thread makes one vector of eight elements: from the two aligned vectors that
-// hold them, shifted by the row's offset, or, where those reach past the
-// matrix, element by element.  (Gathering every element alone took 12 us for
-// [1021, 2049] and [1543, 2049] together, bound by its load instructions.)
+// vector of eight elements comes from the two aligned vectors that hold them,
+// shifted by the row's offset; the first and last of the matrix, whose aligned
+// vectors reach past it, element by element.  What a row's last vector holds
+// past the row is never read.  Bound by latency: one round of loads, all of a
+// thread's on their way before the first is used ([1021,2049] and [1543,2049]
+// together 12 us element by element, 3.6 us so).
 struct RepackArgs {
     const uint16_t *src;
     uint4 *dst;
@@ -37,60 +39,25 @@ struct RepackArgs {
     FastDiv per_row;                 // by units
 };
 
-__device__ __forceinline__ uint4 repack_unit(const RepackArgs &r, int64_t row, int64_t c) {
-    const uintptr_t first = (uintptr_t)r.src;
-    const uintptr_t last = first + 2 * (uintptr_t)((r.rows - 1) * r.ld + r.cols);
-    const uint16_t *x = r.src + row * r.ld + c;
-    const uintptr_t at = (uintptr_t)x, low = at & ~(uintptr_t)15;
-    const uint32_t shift = (uint32_t)(at & 15);
-    if (c + 8 <= r.cols && low >= first && low + (shift ? 32 : 16) <= last) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(low));
-        uint4 n = make_uint4(0, 0, 0, 0);
-        if (shift) n = __ldg(reinterpret_cast<const uint4 *>(low) + 1);
-        uint32_t w[8] = {v.x, v.y, v.z, v.w, n.x, n.y, n.z, n.w};
-        if (shift & 8) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-        }
-        if (shift & 4) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-        }
-        if (shift & 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = c + 2 * j < r.cols ? x[2 * j] : 0u;
-        const uint32_t hi = c + 2 * j + 1 < r.cols ? x[2 * j + 1] : 0u;
-        w[j] = lo | hi << 16;
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The vectors of the new layout one after another, kRepackVectors a thread, all
-// loads of a thread on their way before the first store.
-constexpr int kRepackVectors = 4;
+constexpr int kRepackVectors = 2;    // of a thread
 
 __global__ void __launch_bounds__(256) k_repack(const RepackArgs a, const RepackArgs b) {
     layer_pdl_launch();
     const RepackArgs &r = blockIdx.y ? b : a;
     const int64_t total = r.rows * r.units;
     const bool narrow = total < (1ll << 31);
+    const uintptr_t first = (uintptr_t)r.src;
+    const uintptr_t last = first + 2 * (uintptr_t)((r.rows - 1) * r.ld + r.cols);
     layer_pdl_wait();
     for (int64_t i0 = (int64_t)blockIdx.x * (256 * kRepackVectors) + threadIdx.x; i0 < total;
          i0 += (int64_t)gridDim.x * (256 * kRepackVectors)) {
-        uint4 x[kRepackVectors];
-        int64_t at[kRepackVectors];
+        uint4 v[kRepackVectors], n[kRepackVectors];
+        int64_t to[kRepackVectors], c[kRepackVectors];
+        uintptr_t at[kRepackVectors];
+        bool whole[kRepackVectors];
 #pragma unroll
         for (int k = 0; k < kRepackVectors; ++k) {
-            const int64_t i = i0 + 256 * k;
-            at[k] = -1;
-            if (i >= total) continue;
+            const int64_t i = min(i0 + 256 * k, total - 1);   // one past the end repeats the last
             int64_t row, u;
             if (narrow) {
                 uint32_t q, rest;
@@ -101,12 +68,45 @@ __global__ void __launch_bounds__(256) k_repack(const RepackArgs a, const Repack
                 row = i / r.units;
                 u = i - row * r.units;
             }
-            at[k] = row * r.pitch + u;
-            x[k] = repack_unit(r, row, u * 8);
+            c[k] = u * 8;
+            to[k] = row * r.pitch + u;
+            at[k] = (uintptr_t)(r.src + row * r.ld + c[k]);
+            const uintptr_t low = at[k] & ~(uintptr_t)15;
+            whole[k] = low >= first && low + 32 <= last;
+            v[k] = n[k] = make_uint4(0, 0, 0, 0);
+            if (whole[k]) {
+                v[k] = __ldg(reinterpret_cast<const uint4 *>(low));
+                n[k] = __ldg(reinterpret_cast<const uint4 *>(low) + 1);
+            }
         }
 #pragma unroll
-        for (int k = 0; k < kRepackVectors; ++k)
-            if (at[k] >= 0) r.dst[at[k]] = x[k];
+        for (int k = 0; k < kRepackVectors; ++k) {
+            uint32_t w[8] = {v[k].x, v[k].y, v[k].z, v[k].w, n[k].x, n[k].y, n[k].z, n[k].w};
+            if (whole[k]) {
+                const uint32_t shift = (uint32_t)(at[k] & 15);
+                if (shift & 8) {
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+                }
+                if (shift & 4) {
+#pragma unroll
+                    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+                }
+                if (shift & 2) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+                }
+            } else {
+                const uint16_t *const x = reinterpret_cast<const uint16_t *>(at[k]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t lo = c[k] + 2 * j < r.cols ? x[2 * j] : 0u;
+                    const uint32_t hi = c[k] + 2 * j + 1 < r.cols ? x[2 * j + 1] : 0u;
+                    w[j] = lo | hi << 16;
+                }
+            }
+            if (i0 + 256 * k < total) r.dst[to[k]] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
