@@ -279,7 +279,9 @@ cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, int mode,
                             cudaStream_t s) {
     if (mode == HEADS_NORM_GRAD) return launch_vec_grad<T, KIND>(a, v, ctas, s);
     // Few rows: one head per item spreads them over the SMs.  Many: four heads
-    // share the token's position, cosines, sines and weights.
+    // share the token's position, cosines, sines and weights (tokens of 32 and 8
+    // heads of 128 bf16, one head an item against four: rotation of 64 1.8 and 2.2
+    // us, 512 2.8 and 3.6, 1024 4.2 and 3.9, 4096 14.2 and 10.4; norms alike).
     const bool few = (a.rows * (a.heads[0] + a.heads[1]) << v.log_lanes) <
                      2048ll * current_sm_count();
     if (mode == HEADS_ROTATE)
