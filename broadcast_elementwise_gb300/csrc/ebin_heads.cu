@@ -181,7 +181,6 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
             return false;
     }
     const int64_t most = 0x7FFFFFFF;
-    if (p.rows * std::max<int64_t>(1, a.heads[0] + (int64_t)a.heads[1]) * 32 > most) return false;
     v = HeadsVecArgs{};
     for (int w = 0; w < 2; ++w) {
         const HeadsTensor *from[3] = {&a.x[w], &a.dy[w], &a.y[w]};
@@ -202,6 +201,11 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
                                  : v.rot_units + (int)div_up((D - 2 * a.half) / V, 2);
     if (v.units > 32) return false;
     while ((1 << v.log_lanes) < v.units) ++v.log_lanes;
+    // the launch's threads, and an item past the last step, are counted in 32 bits
+    // (26 million tokens of 40 heads of 128 in 16 bits)
+    const int64_t items = div_up(a.heads[0], kRingHeads) + div_up(a.heads[1], kRingHeads);
+    if (p.rows > most >> v.log_lanes || (p.rows << v.log_lanes) > most / std::max<int64_t>(1, items))
+        return false;
     v.weight_vec = ((uintptr_t)a.w[0] | (uintptr_t)a.w[1]) % 16 == 0;
     v.table_vec = a.half % 4 == 0 && ((uintptr_t)a.cos | (uintptr_t)a.sin) % 16 == 0;
     return true;
@@ -330,6 +334,13 @@ ebin_status prepare_heads(const ebin_heads_plan_s &p, const void *const in[4],
                               (grad ? (uintptr_t)in[2 + w] : 0);
         if (mis % (uintptr_t)p.isz) return EBIN_ERR_INVALID_ARG;
     }
+    // every buffer on its own element's boundary
+    const uintptr_t ps = at.position_type ? (uintptr_t)type_size((ebin_dtype)at.position_type) : 1;
+    if (at.rotary_dim > 0 && (((uintptr_t)cos | (uintptr_t)sin) % 4 || (uintptr_t)pos % ps))
+        return EBIN_ERR_INVALID_ARG;
+    if (at.norm != EBIN_NORM_NONE &&
+        ((uintptr_t)wq | (uintptr_t)wk) % (uintptr_t)type_size(at.dtype_w))
+        return EBIN_ERR_INVALID_ARG;
     const int64_t table_bytes = at.table_positions * (at.rotary_dim / 2) * 4;
     const int64_t w_bytes = at.head_dim * type_size(at.dtype_w);
     for (int w = 0; w < 2; ++w) {
@@ -421,7 +432,7 @@ extern "C" ebin_status ebin_rotary_table(const ebin_rotary_attrs *attrs, int64_t
         first_position > (int64_t(1) << 53) - positions)
         return EBIN_ERR_INVALID_ARG;
     if (n == 0) return EBIN_OK;
-    if (!cos || !sin) return EBIN_ERR_INVALID_ARG;
+    if (!cos || !sin || ((uintptr_t)cos | (uintptr_t)sin) % 4 != 0) return EBIN_ERR_INVALID_ARG;
     if (ranges_overlap(cos, n * 4, sin, n * 4)) return EBIN_ERR_ALIAS;
     TableArgs a{};
     a.first = first_position;
@@ -546,7 +557,8 @@ extern "C" ebin_status ebin_heads_grad_execute(ebin_heads_plan_t plan, const voi
                 return EBIN_ERR_CUDA;
         return EBIN_OK;
     }
-    if (!workspace || workspace_bytes < p.workspace || (uintptr_t)workspace % 16 != 0)
+    if (!workspace || workspace_bytes < p.workspace || (uintptr_t)workspace % 16 != 0 ||
+        ((uintptr_t)dwq | (uintptr_t)dwk) % 4 != 0)
         return EBIN_ERR_INVALID_ARG;
     const void *const in[4] = {q, k, dq, dk};
     void *const out[2] = {dq_out, dk_out};

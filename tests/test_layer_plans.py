@@ -53,7 +53,11 @@ def test_heads_execute_refusals():
     for missing in ("q", "k", "cos", "sin", "qo", "ko"):
         assert code(run, p, **{missing: None}) == "invalid_arg"
     assert code(run, heads(positions="int32")) == "invalid_arg"
-    assert code(run, p, q=0x100001) == "invalid_arg"                 # off the element size
+    for off in (dict(q=0x100001), dict(ko=0x600001), dict(cos=0x300002), dict(sin=0x400001)):
+        assert code(run, p, **off) == "invalid_arg"                  # off the element size
+    assert code(run, heads(positions="int64"), pos=0x700004) == "invalid_arg"
+    assert code(run, heads(norm="rms"), wq=0x700001) == "invalid_arg"
+    assert code(run, heads(norm="rms", weight_dtype="float32"), wk=0x700002) == "invalid_arg"
     assert code(run, heads(norm="rms", gradient=True)) == "invalid_arg"
     # q is 2560 elements, 5120 bytes
     assert code(run, p, qo=0x100002) == "alias"
@@ -88,6 +92,7 @@ def test_heads_grad_refusals():
         assert code(grad, **{missing: None}) == "invalid_arg"
     assert code(grad, size=p.workspace_bytes - 1) == "invalid_arg"
     assert code(grad, work=0x10000004) == "invalid_arg"
+    assert code(grad, dwk=0xA00002) == "invalid_arg"
     assert code(grad, qo=0x300010) == "alias"
     assert code(grad, dwq=0x700000) == "alias"
     assert code(grad, dwq=0xA00010) == "alias"
@@ -112,6 +117,7 @@ def test_rotary_table_refusals():
     assert code(table, positions=-1) == "invalid_arg"
     assert code(table, first=-1) == "invalid_arg"
     assert code(table, cos=None) == "invalid_arg"
+    assert code(table, cos=0x1002) == "invalid_arg"
     assert code(table, sin=0x1010) == "alias"
     table(positions=0, cos=None, sin=None)
 
