@@ -958,8 +958,8 @@ class GemmPlan:
         a = ebin_gemm_attrs(code, code if bias is None else _dtype_code(bias), int(bool(trans_a)),
                             int(bool(trans_b)), ACTIVATIONS[activation], int(bias is not None),
                             int(bool(residual)), int(bool(any_alignment)), int(m), int(n), int(k),
-                            *(0 if v is None else int(v)
-                              for v in (lda, ldb, ldy, ld_residual, ld_preact)))
+                            *_row_strides("GemmPlan", lda=lda, ldb=ldb, ldy=ldy,
+                                          ld_residual=ld_residual, ld_preact=ld_preact))
         self.handle = ebin_gemm_plan_create(a)
         self.workspace_bytes = ebin_gemm_plan_workspace(self.handle)
 
@@ -993,7 +993,8 @@ class EpilogueGradPlan:
                  ld_dy=None, ld_z=None, ld_dz=None):
         a = ebin_epilogue_grad_attrs(_dtype_code(dtype), ACTIVATIONS[activation], int(bool(bias)),
                                      int(m), int(n),
-                                     *(0 if v is None else int(v) for v in (ld_dy, ld_z, ld_dz)))
+                                     *_row_strides("EpilogueGradPlan", ld_dy=ld_dy, ld_z=ld_z,
+                                                   ld_dz=ld_dz))
         self.handle = ebin_epilogue_grad_plan_create(a)
         self.workspace_bytes = ebin_epilogue_grad_plan_workspace(self.handle)
 
@@ -1027,14 +1028,29 @@ def _matrix(where, t, shape, dtype, device):
                          % (where, t.dtype, t.device, dtype, device))
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("%s: a matrix's rows are dense (strides %s)" % (where, t.stride()))
-    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+    width = max(1, t.shape[1])
+    step = t.stride(0) if t.shape[0] > 1 else width
+    if step < width:
+        raise ValueError("%s: a matrix's rows lie apart (strides %s); pass an expanded tensor's "
+                         "copy" % (where, t.stride()))
+    return step
+
+
+def _row_strides(where, **strides):
+    """The ABI's row strides, where 0 stands for dense rows: None gives that, and
+    0 itself, the stride of a broadcast tensor, is refused."""
+    for name, v in strides.items():
+        if v is not None and int(v) == 0:
+            raise ValueError("%s: %s is 0; rows lie apart, and None means dense" % (where, name))
+    return [0 if v is None else int(v) for v in strides.values()]
 
 
 def gemm(a, b, bias=None, residual=None, *, trans_a: bool = False, trans_b: bool = False,
          activation: str = "none", out=None, preact=None, stream=None):
     """y = act(op(a) op(b) + bias) + residual on 16-bit CUDA tensors, in one
-    call; a and b are matrices whose rows are dense (a row stride is fine),
-    transposed where trans_a / trans_b say so.  ``out`` may be ``residual``.
+    call; a and b are matrices whose rows are dense and lie apart (a row stride
+    is fine, an expanded tensor is not), transposed where trans_a / trans_b say
+    so.  ``out`` may be ``residual``.
     ``preact``: a tensor that receives the pre-activation, which the gradient
     reads (gemm_epilogue_grad)."""
     import torch
