@@ -19,7 +19,7 @@ def recorded(monkeypatch):
 
 
 def mat(*shape):
-    return torch.zeros(*shape, dtype=BF16)
+    return torch.zeros(shape, dtype=BF16)
 
 
 # ------------------------------------------------------------------ rows that lie on one another
