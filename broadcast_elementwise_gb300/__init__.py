@@ -706,6 +706,10 @@ def _output(out, plan, desc, device):
 
 
 # ----------------------------------------------------------------- heads: rotary positions, norms
+#
+# In the one-call forms below ``stream=s`` does what calling them under
+# torch.cuda.stream(s) does: the inputs are ready in s's order, and what the call
+# allocates, its results among it, is s's memory.
 
 def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
                  scaling: str = "none", factor: float = 1.0, trained_length: float = 0.0,
@@ -720,7 +724,7 @@ def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
     attrs = ebin_rotary_attrs(int(rotary_dim), SCALINGS[scaling], float(base), float(factor),
                               float(trained_length), float(slow_turns), float(fast_turns),
                               float(amplitude))
-    with torch.cuda.device(torch.device(device)):
+    with _launching(torch.device(device), stream):
         cos = torch.empty(int(positions), int(rotary_dim) // 2, device="cuda")
         sin = torch.empty_like(cos)
         ebin_rotary_table(attrs, first_position, positions, _ptr(cos), _ptr(sin), _stream(stream))
@@ -830,6 +834,21 @@ def _same_device(where, first, *others):
             raise ValueError("%s: tensors are on %s and %s" % (where, first.device, t.device))
 
 
+def _launching(device, stream):
+    """The context of a one-call form: its device and, with ``stream``, that stream as
+    torch's current one.  What torch allocates inside then belongs to the stream
+    that uses it: a workspace dropped at return is handed out again in that
+    stream's order, and no block is taken over that another stream still uses."""
+    import torch
+    if stream is None:
+        return torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device)
+    elif device.index not in (None, stream.device.index):
+        raise ValueError("the tensors are on %s and the stream on %s" % (device, stream.device))
+    return torch.cuda.stream(stream)
+
+
 def _heads_inputs(where, q, k, cos, sin, positions):
     """The checks of the one-shot calls; returns the plan's keywords for the table and positions."""
     import torch
@@ -870,15 +889,14 @@ def _heads_out(where, x, out):
 
 
 def _run_heads(where, q, k, cos, sin, positions, out, wq, wk, stream, **kw):
-    import torch
     more, positions = _heads_inputs(where, q, k, cos, sin, positions)
     _same_device(where, q, wq, wk)
     qo, ko = (None, None) if out is None else out
-    qo, ko = _heads_out(where, q, qo), _heads_out(where, k, ko)
-    plan = HeadsPlan(q.dtype, q.shape, None if k is None else k.shape, q_strides=q.stride(),
-                     k_strides=None if k is None else k.stride(), q_out_strides=qo.stride(),
-                     k_out_strides=None if k is None else ko.stride(), **more, **kw)
-    with torch.cuda.device(q.device):
+    with _launching(q.device, stream):
+        qo, ko = _heads_out(where, q, qo), _heads_out(where, k, ko)
+        plan = HeadsPlan(q.dtype, q.shape, None if k is None else k.shape, q_strides=q.stride(),
+                         k_strides=None if k is None else k.stride(), q_out_strides=qo.stride(),
+                         k_out_strides=None if k is None else ko.stride(), **more, **kw)
         execute_heads(plan, q, k, cos, sin, positions, qo, ko, wq, wk, stream)
     return qo, ko
 
@@ -927,16 +945,16 @@ def qk_norm_rotary_grad(dq, dk, q, k, wq, wk, cos=None, sin=None, positions=None
                                           (g.shape != x.shape or g.dtype != x.dtype)):
             raise ValueError("%s: a gradient has its input's shape and type" % where)
     qo, ko = (None, None) if out is None else out
-    qo, ko = _heads_out(where, q, qo), _heads_out(where, k, ko)
     st = (lambda t: None if t is None else t.stride())
-    plan = HeadsPlan(q.dtype, q.shape, None if k is None else k.shape, norm="rms",
-                     epsilon=epsilon, layout=layout, weight_dtype=wd, gradient=True,
-                     q_strides=st(q), k_strides=st(k), dq_strides=st(dq), dk_strides=st(dk),
-                     q_out_strides=st(qo), k_out_strides=st(ko), **more)
-    dwq = torch.empty(q.shape[-1], device=q.device)
-    dwk = None if k is None else torch.empty(q.shape[-1], device=q.device)
-    work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
+    with _launching(q.device, stream):
+        qo, ko = _heads_out(where, q, qo), _heads_out(where, k, ko)
+        plan = HeadsPlan(q.dtype, q.shape, None if k is None else k.shape, norm="rms",
+                         epsilon=epsilon, layout=layout, weight_dtype=wd, gradient=True,
+                         q_strides=st(q), k_strides=st(k), dq_strides=st(dq), dk_strides=st(dk),
+                         q_out_strides=st(qo), k_out_strides=st(ko), **more)
+        dwq = torch.empty(q.shape[-1], device=q.device)
+        dwk = None if k is None else torch.empty(q.shape[-1], device=q.device)
+        work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
         execute_heads_grad(plan, dq, dk, q, k, cos, sin, positions, wq, wk, qo, ko, dwq, dwk,
                            work, stream)
     return qo, ko, dwq, dwk
@@ -1064,18 +1082,18 @@ def gemm(a, b, bias=None, residual=None, *, trans_a: bool = False, trans_b: bool
         raise ValueError("gemm: op(a) is [%d, %d] and op(b) [%d, %d]" % (m, k, kb, n))
     lda = _matrix(where, a, None, a.dtype, a.device)
     ldb = _matrix(where, b, None, a.dtype, a.device)
-    if out is None:
-        out = torch.empty(m, n, dtype=a.dtype, device=a.device)
-    ld = [None if t is None else _matrix(where, t, (m, n), a.dtype, a.device)
-          for t in (out, residual, preact)]
     if bias is not None and (tuple(bias.shape) != (n,) or not bias.is_contiguous()):
         raise ValueError("gemm: the bias is a contiguous [%d] tensor" % n)
-    plan = GemmPlan(a.dtype, m, n, k, trans_a=trans_a, trans_b=trans_b,
-                    bias=None if bias is None else bias.dtype, activation=activation,
-                    residual=residual is not None, lda=lda, ldb=ldb, ldy=ld[0],
-                    ld_residual=ld[1], ld_preact=ld[2],
-                    any_alignment=a.data_ptr() % 16 != 0 or b.data_ptr() % 16 != 0)
-    with torch.cuda.device(a.device):
+    ld = [None if t is None else _matrix(where, t, (m, n), a.dtype, a.device)
+          for t in (out, residual, preact)]
+    with _launching(a.device, stream):
+        if out is None:
+            out = torch.empty(m, n, dtype=a.dtype, device=a.device)
+        plan = GemmPlan(a.dtype, m, n, k, trans_a=trans_a, trans_b=trans_b,
+                        bias=None if bias is None else bias.dtype, activation=activation,
+                        residual=residual is not None, lda=lda, ldb=ldb, ldy=ld[0],
+                        ld_residual=ld[1], ld_preact=ld[2],
+                        any_alignment=a.data_ptr() % 16 != 0 or b.data_ptr() % 16 != 0)
         work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=a.device)
         execute_gemm(plan, a, b, out, bias=bias, residual=residual, preact=preact,
                      workspace=work, stream=stream)
@@ -1092,14 +1110,14 @@ def gemm_epilogue_grad(dy, z=None, *, activation: str = "none", bias: bool = Tru
     _same_device(where, dy, z, out)
     if activation != "none" and z is None:
         raise ValueError("gemm_epilogue_grad: %s needs z" % activation)
-    if out is None:
-        out = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
     shape = tuple(dy.shape)
     ld = [None if t is None else _matrix(where, t, shape, dy.dtype, dy.device)
           for t in (dy, z, out)]
-    plan = EpilogueGradPlan(dy.dtype, shape[0], shape[1], activation=activation, bias=bias,
-                            ld_dy=ld[0], ld_z=ld[1], ld_dz=ld[2])
-    with torch.cuda.device(dy.device):
+    with _launching(dy.device, stream):
+        if out is None:
+            out = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+        plan = EpilogueGradPlan(dy.dtype, shape[0], shape[1], activation=activation, bias=bias,
+                                ld_dy=ld[0], ld_z=ld[1], ld_dz=ld[2])
         dbias = torch.empty(shape[1], device=dy.device) if bias else None
         work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dy.device)
         execute_epilogue_grad(plan, dy, z, out, dbias, work, stream)

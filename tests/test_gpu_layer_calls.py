@@ -1,0 +1,77 @@
+"""The one-call forms of the layer operators on the GPU: refusals that keep broadcast
+matrices from the kernels, and calls on another stream than torch's current one."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import broadcast_elementwise_gb300 as eb  # noqa: E402
+
+BF16 = torch.bfloat16
+
+
+def normal(seed, *shape, dtype=BF16):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def test_broadcast_matrices_are_refused():
+    a, b, row = normal(1, 8, 32), normal(2, 32, 16), normal(3, 1, 16)
+    before = eb.lib.ebin_launch_count()
+    for kw in (dict(residual=row.expand(8, 16)), dict(out=row.expand(8, 16)),
+               dict(preact=row.expand(8, 16))):
+        with pytest.raises(ValueError):
+            eb.gemm(a, b, **kw)
+    with pytest.raises(ValueError):
+        eb.gemm(normal(4, 1, 32).expand(8, 32), b)
+    y = normal(5, 8, 1).requires_grad_()
+    dy, = torch.autograd.grad(y.sum(), y)        # a scalar, expanded
+    if dy.stride() == (0, 0):
+        with pytest.raises(ValueError):
+            eb.gemm_epilogue_grad(dy)
+    assert eb.lib.ebin_launch_count() == before
+    # its copy is taken, and adds the row to every row
+    got = eb.gemm(a, b, None, row.expand(8, 16).contiguous())
+    assert torch.equal(got, eb.gemm(a, b, residual=row.repeat(8, 1)))
+
+
+def calls():
+    """(name, call) of every one-call form whose kernels use memory that the call allocates."""
+    a, b = normal(1, 300, 261), normal(2, 261, 521)       # odd rows: both are laid out anew
+    dy, z = normal(3, 4000, 264), normal(4, 4000, 264)
+    q, k = normal(5, 2, 700, 6, 64), normal(6, 2, 700, 2, 64)
+    dq, dk = normal(7, 2, 700, 6, 64), normal(8, 2, 700, 2, 64)
+    cos, sin = eb.rotary_table(700, 64)
+    return [("gemm", lambda s: [eb.gemm(a, b, stream=s)]),
+            ("gemm_epilogue_grad",
+             lambda s: list(eb.gemm_epilogue_grad(dy, z, activation="silu", stream=s))),
+            ("qk_norm_rotary", lambda s: list(eb.qk_norm_rotary(q, k, None, None, cos, sin,
+                                                               stream=s))),
+            ("qk_norm_rotary_grad",
+             lambda s: list(eb.qk_norm_rotary_grad(dq, dk, q, k, None, None, cos, sin, stream=s))),
+            ("rotary_table", lambda s: list(eb.rotary_table(900, 64, stream=s)))]
+
+
+@pytest.mark.parametrize("how", ["stream", "address"])
+def test_another_stream_beside_a_busy_current_one(how):
+    """The call's stream is held back while the current stream takes and fills blocks of
+    every size that the call used, and the other way round; results are unchanged."""
+    s = torch.cuda.Stream()
+    for name, call in calls():
+        want = call(None)
+        torch.cuda.synchronize()
+        for held in (s, torch.cuda.current_stream()):
+            with torch.cuda.stream(held):
+                torch.cuda._sleep(20_000_000)
+                dropped = [torch.full((1 << n,), 255, dtype=torch.uint8, device="cuda")
+                           for n in range(9, 23)] if held is not s else None
+            del dropped
+            got = call(s if how == "stream" else s.cuda_stream)
+            blocks = [torch.full((1 << n,), 255, dtype=torch.uint8, device="cuda")
+                      for n in range(9, 23) for _ in range(4)]
+            torch.cuda.synchronize()
+            for x, y in zip(got, want):
+                assert torch.equal(x, y), name
+            del blocks, got
+    assert eb.get_device_status(s) == 0

@@ -1,5 +1,8 @@
 """What the one-call forms of the layer operators check and pass on, on the CPU:
 tensors stand in for device ones, and the launches are recorded."""
+import contextlib
+import types
+
 import pytest
 import torch
 
@@ -75,3 +78,83 @@ def test_a_row_stride_of_zero_is_no_plan():
         with pytest.raises(ValueError, match=name):
             eb.EpilogueGradPlan(BF16, 8, 16, **{name: 0})
         eb.EpilogueGradPlan(BF16, 8, 16, **{name: 16})
+
+
+# ------------------------------------------------------------------ the stream of what a call allocates
+
+HANDLE = 0x5EA0
+
+
+@pytest.fixture
+def streams(monkeypatch, recorded):
+    """Each allocation's size and the address of the stream that was current for it, beside
+    the launches (CPU tensors, no device)."""
+    seen = types.SimpleNamespace(now=0, blocks=[], launches=recorded)
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream, self.device = handle, torch.device("cpu")
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, seen.now = seen.now, stream.cuda_stream
+        try:
+            yield
+        finally:
+            seen.now = before
+
+    empty = torch.empty
+
+    def recorded_empty(*a, **kw):
+        kw["device"] = "cpu"
+        t = empty(*a, **kw)
+        seen.blocks.append((t.nbytes, seen.now))
+        return t
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch, "empty", recorded_empty)
+    monkeypatch.setattr(eb, "_stream", lambda s: s if isinstance(s, int) else
+                        seen.now if s is None else s.cuda_stream)
+    monkeypatch.setattr(eb, "ebin_rotary_table", lambda *a: seen.launches.append(("table", a, {})))
+    seen.Stream = Stream
+    return seen
+
+
+def calls_with_memory():
+    """Each one-call form, and how many blocks it allocates."""
+    x, g = mat(2, 3, 4, 8), mat(2, 3, 2, 8)
+    cos = torch.zeros(3, 4)
+    return [("gemm", 2, lambda s: eb.gemm(mat(8, 33), mat(33, 16), stream=s)),
+            ("gemm into out", 1, lambda s: eb.gemm(mat(8, 33), mat(33, 16), out=mat(8, 16), stream=s)),
+            ("gemm_epilogue_grad", 3, lambda s: eb.gemm_epilogue_grad(mat(8, 16), stream=s)),
+            ("rotary", 2, lambda s: eb.rotary(x, g, cos, cos, stream=s)),
+            ("qk_norm_rotary", 2, lambda s: eb.qk_norm_rotary(x, g, None, None, cos, cos, stream=s)),
+            ("qk_norm_rotary_grad", 5,
+             lambda s: eb.qk_norm_rotary_grad(x, g, x, g, None, None, cos, cos, stream=s)),
+            ("rotary_table", 2, lambda s: eb.rotary_table(4, 8, stream=s))]
+
+
+@pytest.mark.parametrize("i", range(7), ids=[c[0] for c in calls_with_memory()])
+@pytest.mark.parametrize("how", ["stream", "address"])
+def test_memory_belongs_to_the_launch_stream(streams, monkeypatch, i, how):
+    """A workspace dropped at return must be handed out again in the order of the stream
+    that its kernel runs on; no block may come from another stream's pending work."""
+    monkeypatch.setattr(torch, "empty_like", lambda t, **kw: torch.empty(t.shape, dtype=t.dtype))
+    _, blocks, call = calls_with_memory()[i]
+    call(streams.Stream(HANDLE) if how == "stream" else HANDLE)
+    assert len(streams.blocks) == blocks and len(streams.launches) == 1
+    assert {at for _, at in streams.blocks} == {HANDLE}, streams.blocks
+    streams.blocks.clear()
+    call(None)
+    assert {at for _, at in streams.blocks} == {0}
+    assert streams.now == 0
+
+
+def test_a_stream_of_another_device_is_refused(streams):
+    s = streams.Stream(HANDLE)
+    s.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        eb._launching(torch.device("cuda", 0), s)
