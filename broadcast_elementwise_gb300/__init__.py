@@ -643,6 +643,21 @@ def descriptor(op: str, dtype, **attrs) -> Descriptor:
     return d
 
 
+def _launching(device, stream):
+    """The context of a one-call form: its device and, with ``stream``, that stream as
+    torch's current one.  What torch allocates inside then belongs to the stream
+    that uses it: a workspace dropped at return is handed out again in that
+    stream's order, and no block is taken over that another stream still uses."""
+    import torch
+    if stream is None:
+        return torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device)
+    elif device.index not in (None, stream.device.index):
+        raise ValueError("the tensors are on %s and the stream on %s" % (device, stream.device))
+    return torch.cuda.stream(stream)
+
+
 def binary(op: str, a, b, out=None, *, stream=None, **attrs):
     """One-shot call: returns ``out`` (allocated if None).
 
@@ -651,8 +666,8 @@ def binary(op: str, a, b, out=None, *, stream=None, **attrs):
     parameter block, which is copied.  On pinned CPU tensors (contiguous),
     the kernel reads and writes host memory in place (ebin_execute_mapped;
     ``out`` is allocated pinned); synchronise ``stream`` before reading it.
+    With ``stream`` what the call allocates on the device is that stream's memory.
     """
-    import torch
     if (b is not None and op in ("BatchNormalization", "BiasPRelu", "BiasPReluBN")
             and b.dtype != a.dtype and "dtype_b" not in attrs):
         attrs["dtype_b"] = b.dtype      # a float32 parameter block beside 16-bit or float64 x
@@ -672,13 +687,13 @@ def binary(op: str, a, b, out=None, *, stream=None, **attrs):
         return out
     if b is not None and b.device != a.device:
         raise ValueError("binary: A is on %s and B on %s" % (a.device, b.device))
-    if b is not None and not plain_b:
-        b = b.contiguous()
-    ta = None if a.is_contiguous() else tuple(a.stride())
-    tb = None if (b is None or b.is_contiguous()) else tuple(b.stride())
-    plan = Plan(desc, a.shape, b.shape if b is not None else (2,), strides_a=ta, strides_b=tb)
-    out = _output(out, plan, desc, a.device)
-    with torch.cuda.device(a.device):
+    with _launching(a.device, stream):
+        if b is not None and not plain_b:
+            b = b.contiguous()
+        ta = None if a.is_contiguous() else tuple(a.stride())
+        tb = None if (b is None or b.is_contiguous()) else tuple(b.stride())
+        plan = Plan(desc, a.shape, b.shape if b is not None else (2,), strides_a=ta, strides_b=tb)
+        out = _output(out, plan, desc, a.device)
         execute(plan, a, b, out, stream)
     return out
 
@@ -832,21 +847,6 @@ def _same_device(where, first, *others):
     for t in others:
         if t is not None and t.device != first.device:
             raise ValueError("%s: tensors are on %s and %s" % (where, first.device, t.device))
-
-
-def _launching(device, stream):
-    """The context of a one-call form: its device and, with ``stream``, that stream as
-    torch's current one.  What torch allocates inside then belongs to the stream
-    that uses it: a workspace dropped at return is handed out again in that
-    stream's order, and no block is taken over that another stream still uses."""
-    import torch
-    if stream is None:
-        return torch.cuda.device(device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device)
-    elif device.index not in (None, stream.device.index):
-        raise ValueError("the tensors are on %s and the stream on %s" % (device, stream.device))
-    return torch.cuda.stream(stream)
 
 
 def _heads_inputs(where, q, k, cos, sin, positions):

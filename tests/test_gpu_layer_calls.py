@@ -43,6 +43,8 @@ def calls():
     q, k = normal(5, 2, 700, 6, 64), normal(6, 2, 700, 2, 64)
     dq, dk = normal(7, 2, 700, 6, 64), normal(8, 2, 700, 2, 64)
     cos, sin = eb.rotary_table(700, 64)
+    x = normal(9, 8, 48, 1000, dtype=torch.float32)
+    block = normal(10, 48, 4, dtype=torch.float32).abs().t()     # copied: not contiguous
     return [("gemm", lambda s: [eb.gemm(a, b, stream=s)]),
             ("gemm_epilogue_grad",
              lambda s: list(eb.gemm_epilogue_grad(dy, z, activation="silu", stream=s))),
@@ -50,7 +52,9 @@ def calls():
                                                                stream=s))),
             ("qk_norm_rotary_grad",
              lambda s: list(eb.qk_norm_rotary_grad(dq, dk, q, k, None, None, cos, sin, stream=s))),
-            ("rotary_table", lambda s: list(eb.rotary_table(900, 64, stream=s)))]
+            ("rotary_table", lambda s: list(eb.rotary_table(900, 64, stream=s))),
+            ("binary", lambda s: [eb.binary("BatchNormalization", x, block, epsilon=1e-5,
+                                            stream=s)])]
 
 
 @pytest.mark.parametrize("how", ["stream", "address"])

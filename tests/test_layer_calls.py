@@ -153,6 +153,31 @@ def test_memory_belongs_to_the_launch_stream(streams, monkeypatch, i, how):
     assert streams.now == 0
 
 
+class OnDevice(torch.Tensor):
+    """A CPU tensor that passes for a CUDA one and notes which stream its copy was made on."""
+    is_cuda = True
+    seen = None
+
+    def contiguous(self):
+        self.seen.blocks.append((self.nbytes, self.seen.now))
+        return torch.Tensor.contiguous(self)
+
+
+@pytest.mark.parametrize("how", ["stream", "address"])
+def test_binary_memory_belongs_to_the_launch_stream(streams, monkeypatch, how):
+    monkeypatch.setattr(eb, "execute", lambda *a: streams.launches.append(a))
+    monkeypatch.setattr(OnDevice, "seen", streams)
+    x = torch.zeros(2, 4, 3).as_subclass(OnDevice)
+    block = torch.zeros(4, 4).as_subclass(OnDevice)       # a copied parameter block
+    for handle in (HANDLE, 0):
+        streams.blocks.clear()
+        s = None if not handle else streams.Stream(HANDLE) if how == "stream" else HANDLE
+        out = eb.binary("BatchNormalization", x, block, epsilon=1e-5, stream=s)
+        assert out.shape == x.shape and len(streams.blocks) == 2
+        assert {at for _, at in streams.blocks} == {handle}
+    assert len(streams.launches) == 2
+
+
 def test_a_stream_of_another_device_is_refused(streams):
     s = streams.Stream(HANDLE)
     s.device = torch.device("cuda", 1)
