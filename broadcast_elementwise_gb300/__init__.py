@@ -766,14 +766,15 @@ class HeadsPlan:
     views' element strides, as ``tensor.stride()`` gives them.  ``k_shape`` None
     leaves k out.  ``positions``: None (token t is at position t), torch.int32
     or torch.int64: the type of a [batch, tokens] tensor of positions, its
-    element strides ``position_strides``.  Run with execute_heads, or, for
-    norm "rms" with gradient=True, execute_heads_grad.
+    element strides ``position_strides``.  ``rotary_dim`` None rotates whole heads;
+    a rotation needs ``table_positions``, the rows of its tables.  Run with
+    execute_heads, or, for norm "rms" with gradient=True, execute_heads_grad.
     """
 
     def __init__(self, dtype, q_shape, k_shape=None, *, norm: str = "none", epsilon: float = 1e-6,
                  weight_dtype=None, layout: str = "half", rotary_dim: int | None = None,
                  gradient: bool = False, positions=None, position_strides=None,
-                 table_positions: int = 0, q_strides=None, k_strides=None, dq_strides=None,
+                 table_positions: int | None = None, q_strides=None, k_strides=None, dq_strides=None,
                  dk_strides=None, q_out_strides=None, k_out_strides=None):
         q_shape = tuple(int(d) for d in q_shape)
         k_shape = (q_shape[0], q_shape[1], 0, q_shape[3]) if k_shape is None else \
@@ -792,10 +793,13 @@ class HeadsPlan:
         a.batch, a.tokens, a.q_heads, a.head_dim = q_shape
         a.k_heads = k_shape[2]
         a.rotary_dim = q_shape[3] if rotary_dim is None else int(rotary_dim)
+        if a.rotary_dim > 0 and table_positions is None:
+            raise ValueError("HeadsPlan: a rotation of %d elements needs table_positions "
+                             "(rotary_dim=0: no rotation)" % a.rotary_dim)
         a.position_type = 0 if positions is None else _dtype_code(positions)
         ps = (q_shape[1], 1) if position_strides is None else position_strides
         a.position_strides = (ctypes.c_int64 * 2)(int(ps[0]), int(ps[1]))
-        a.table_positions = int(table_positions)
+        a.table_positions = int(table_positions or 0)
         for name, shape, st in (("q", q_shape, q_strides), ("k", k_shape, k_strides),
                                 ("dq", q_shape, dq_strides), ("dk", k_shape, dk_strides),
                                 ("q_out", q_shape, q_out_strides),

@@ -163,12 +163,13 @@ cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode,
 }
 
 // The vector path's layout of a head, or false where it does not apply: rows
-// that are not whole 16-byte vectors on 16-byte boundaries, and heads of more
-// than 64 vectors.
+// that are not whole 16-byte vectors on 16-byte boundaries, heads of more than 64
+// vectors, and an empty table (a token outside the table reads its first row's
+// angles there, and drops them).
 bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, HeadsVecArgs &v,
                    int &kind) {
     const int64_t V = 16 / p.isz, D = a.dim;
-    if (D % V != 0) return false;
+    if (D % V != 0 || (a.half > 0 && a.table == 0)) return false;
     kind = p.at.layout == EBIN_ROTARY_INTERLEAVED ? HEADS_PAIRS
          : a.half % V == 0 ? HEADS_HALF : HEADS_ODD;
     auto fits = [&](const HeadsTensor &t, int heads) {
@@ -324,7 +325,8 @@ ebin_status prepare_heads(const ebin_heads_plan_s &p, const void *const in[4],
                           const float *cos, const float *sin, const void *pos, const void *wq,
                           const void *wk, void *const out[2], bool grad, HeadsArgs &a) {
     const ebin_heads_attrs &at = p.at;
-    if (at.rotary_dim > 0 && (!cos || !sin || (at.position_type && !pos)))
+    if (at.rotary_dim > 0 && ((at.table_positions > 0 && (!cos || !sin)) ||
+                              (at.position_type && !pos)))
         return EBIN_ERR_INVALID_ARG;
     const int inputs = grad ? 4 : 2;
     for (int w = 0; w < 2; ++w) {

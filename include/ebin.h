@@ -622,7 +622,8 @@ typedef struct ebin_heads_view {
  *   position_type    INT32 or INT64: positions are a device array of that type, element
  *                    strides position_strides (batch, token; 0 allowed); or 0: token t of
  *                    every sequence is at position t
- *   table_positions  rows of cos and sin; a token whose position is outside them sets
+ *   table_positions  rows of cos and sin (with none the tables are not read, and may be
+ *                    NULL); a token whose position is outside them sets
  *                    EBIN_DEVICE_POSITION_RANGE, its output rows are written as 0 and it adds
  *                    nothing to the weight gradients
  *   q, k             strides of the inputs x; dq, dk: of the incoming gradients (norm gradient

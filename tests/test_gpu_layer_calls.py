@@ -79,3 +79,35 @@ def test_another_stream_beside_a_busy_current_one(how):
                 assert torch.equal(x, y), name
             del blocks, got
     assert eb.get_device_status(s) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float16, torch.float32])
+@pytest.mark.parametrize("tokens", [3, 9000])
+@pytest.mark.parametrize("D,r,layout", [(64, 64, "half"), (64, 32, "interleaved"), (64, 14, "half"),
+                                        (33, 10, "half")])
+def test_a_table_without_rows(D, r, layout, tokens, dtype):
+    """Every position is outside it: rows of zeros, the status bit, no weight gradients, and
+    no table is read (addresses of one element stand in for the tables, or none)."""
+    q, k = normal(1, 2, tokens, 3, D, dtype=dtype), normal(2, 2, tokens, 1, D, dtype=dtype)
+    one = torch.full((1,), float("nan"), device="cuda")
+    for tables in ((one, one), (None, None)):
+        for kw in (dict(), dict(gradient=True), dict(norm="rms")):
+            plan = eb.HeadsPlan(dtype, q.shape, k.shape, rotary_dim=r, layout=layout,
+                                table_positions=0, **kw)
+            qo, ko = torch.full_like(q, 7), torch.full_like(k, 7)
+            eb.execute_heads(plan, q, k, *tables, None, qo, ko)
+            assert eb.get_device_status() == eb.DEVICE_POSITION_RANGE
+            assert (qo == 0).all() and (ko == 0).all()
+        plan = eb.HeadsPlan(dtype, q.shape, k.shape, rotary_dim=r, layout=layout, norm="rms",
+                            gradient=True, table_positions=0)
+        work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        dw = torch.full((2, D), 7.0, device="cuda")
+        qo, ko = torch.full_like(q, 7), torch.full_like(k, 7)
+        eb.execute_heads_grad(plan, q, k, q, k, *tables, None, None, None, qo, ko, dw[0], dw[1],
+                              work)
+        assert eb.get_device_status() == eb.DEVICE_POSITION_RANGE
+        assert (qo == 0).all() and (ko == 0).all() and (dw == 0).all()
+    none = torch.empty(0, r // 2, device="cuda")
+    got = eb.rotary(q, k, none, none, layout=layout)
+    assert eb.get_device_status() == eb.DEVICE_POSITION_RANGE
+    assert (got[0] == 0).all() and (got[1] == 0).all()

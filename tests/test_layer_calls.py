@@ -183,3 +183,23 @@ def test_a_stream_of_another_device_is_refused(streams):
     s.device = torch.device("cuda", 1)
     with pytest.raises(ValueError, match="cuda:1"):
         eb._launching(torch.device("cuda", 0), s)
+
+
+# ------------------------------------------------------------------ tables
+
+def test_a_rotation_needs_its_tables_length():
+    for kw in (dict(), dict(rotary_dim=4), dict(norm="rms")):
+        with pytest.raises(ValueError, match="table_positions"):
+            eb.HeadsPlan(BF16, (1, 2, 3, 8), **kw)
+    eb.HeadsPlan(BF16, (1, 2, 3, 8), norm="rms", rotary_dim=0)
+    eb.HeadsPlan(BF16, (1, 2, 3, 8), table_positions=0)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses would be launched on")
+def test_an_empty_table_may_be_null():
+    """Without a row there is nothing to read: the call gets as far as the device."""
+    for rows, code in ((0, "cuda"), (1, "invalid_arg")):
+        plan = eb.HeadsPlan(BF16, (1, 2, 3, 8), table_positions=rows)
+        with pytest.raises(eb.EbinError) as e:
+            eb.execute_heads(plan, 0x100000, None, None, None, None, 0x200000, None, stream=0)
+        assert e.value.code == code
