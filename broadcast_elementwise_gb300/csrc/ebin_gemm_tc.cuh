@@ -11,8 +11,11 @@
 // Warps of a CTA: 0 issues the copies, 1 the matrix instructions, 2 holds the
 // tensor memory, 4.. run the epilogue.  Barriers between them: `full` and
 // `empty` per stage of operands, `tfull` and `tempty` per accumulator.  Every
-// wait has a limit; one that runs out raises EBIN_DEVICE_WAIT_LIMIT and the
-// CTA winds down (its copies and products in flight first).
+// wait has a limit.  One that runs out, in any warp, is told to every CTA of the
+// cluster; they meet, the leader waits (each wait again with the limit) for the
+// products and the copies that are still on their way, both CTAs' on a pair, and
+// only then is shared memory reused or left and the tensor memory given back.
+// EBIN_DEVICE_WAIT_LIMIT is raised and the output is not valid.
 //
 // What bounds it.  Large products: the matrix instructions (a pair's 256 x 256 x
 // 64 step takes 512 clocks at best) and the power they draw: [4096,4096] x
@@ -28,6 +31,7 @@
 #include <cuda.h>
 
 #include "ebin_gemm.cuh"
+#include "ebin_gemm_drain.h"
 
 namespace ebin {
 
@@ -56,6 +60,12 @@ __device__ __forceinline__ void tc_bar_init(uint32_t bar, int count) {
 }
 __device__ __forceinline__ void tc_bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// take bytes that will not come off a barrier's count
+__device__ __forceinline__ void tc_bar_count_off(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar),
+                 "r"(bytes)
                  : "memory");
 }
 // arrive at a barrier of this cluster, by its cluster address
@@ -97,6 +107,9 @@ __device__ __forceinline__ uint32_t tc_cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
+}
+__device__ __forceinline__ void tc_put_word(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void tc_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -394,7 +407,7 @@ template <int CTAS, int BN, bool SPLIT> struct TcLayout {
     static constexpr int kBytes = kTcSmem;
     static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
     static constexpr int kMostStages = 12;
-    static_assert(8 * (2 * kMostStages + 5) + 8 <= kBarriers, "room for the barriers");
+    static_assert(8 * (2 * kMostStages + 5) + 24 <= kBarriers, "room for the barriers and words");
     // bytes of a stage: P's rows, and Q's (rows or blocks), on 1024-byte boundaries
     static int stage(bool q_mn) { return kP + (q_mn ? kQRows : (BN / CTAS + 7) / 8 * 8) * 128; }
     static int stages(bool q_mn) {
@@ -425,6 +438,11 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     auto tempty = [&](int i) { return bars + 8 * (2 * L::kMostStages + 2 + i); };
     const uint32_t drain = bars + 8 * (2 * L::kMostStages + 4);
     const uint32_t s_tmem = drain + 8;
+    const uint32_t s_failed = drain + 12;   // a wait of this cluster ran out
+    const uint32_t s_issued = drain + 16;   // the leader's: steps issued by it, by its peer
+    auto word = [&](uint32_t at) {
+        return *reinterpret_cast<volatile uint32_t *>(s_base + (at - base));
+    };
     // uniform in the warp, so that what follows from it can stay in uniform registers
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = tc_cluster_rank(), ranks = tc_cluster_size();
@@ -440,6 +458,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
             tc_bar_init(tempty(i), CTAS * L::kEpilogueWarps);
         }
         tc_bar_init(drain, 1);
+        *reinterpret_cast<volatile uint32_t *>(s_base + (s_failed - base)) = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tc_alloc<CTAS>(s_tmem, L::kColumns);
@@ -448,7 +467,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     __syncthreads();
     tc_cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_base + (s_tmem - base));
+    const uint32_t tmem = word(s_tmem);
     layer_pdl_wait();
 
     // the work of this cluster (and, split, this CTA's part of k)
@@ -456,6 +475,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
     const int kb0 = SPLIT ? (int)((long long)a.kblocks * rank / ranks) : 0;
     const int kb1 = SPLIT ? (int)((long long)a.kblocks * (rank + 1) / ranks) : a.kblocks;
+    const uint32_t q_bytes = (a.q_mn ? L::kQRows : a.q_box) * 128;   // Q's, of a step
     auto place = [&](int t, int &p, int &q) {
         // groups of eight tiles of P walk along Q: the tiles in flight form a block
         constexpr int G = 8;
@@ -469,15 +489,14 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
     if (warp == 0) {
         // the whole warp walks the loop (its values stay uniform), one lane issues
         const bool one = tc_elect();
-        const uint32_t q_bytes = (a.q_mn ? L::kQRows : a.q_box) * 128;
-        int s = 0, it = 0;
+        int s = 0, issued = 0;
         uint32_t phase = 1;
         for (int t = cluster; t < tiles && ok; t += clusters) {
             int p, q;
             place(t, p, q);
             const int pr = (p * CTAS + (CTAS == 2 ? (int)rank : 0)) * kTcRows;
             const int qr = q * BN + (CTAS == 2 ? (int)rank * (BN / 2) : 0);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++issued) {
                 if (!tc_bar_wait(empty(s), phase, a.limit)) {
                     ok = false;
                     break;
@@ -506,9 +525,7 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                 }
             }
         }
-        if (!ok && leader)   // wait for what is in flight
-            for (int j = max(0, it - a.stages); j < it; ++j)
-                tc_bar_wait(full(j % a.stages), j / a.stages & 1, a.limit);
+        if (one) tc_put_word(tc_map(s_issued + (leader ? 0 : 4), leader ? rank : 0), (uint32_t)issued);
     } else if (warp == 1 && leader) {
         // f32 accumulators; operands f16 or bf16, their major directions; N / 8, M / 16
         constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
@@ -551,10 +568,6 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
                 }
             }
             if (ok && one) tc_commit<CTAS>(tfull(acc));
-        }
-        if (!ok) {   // wait for the products in flight
-            if (one) tc_commit<CTAS>(drain);
-            tc_bar_wait(drain, 0, a.limit);
         }
     } else if (warp >= 4 && !SPLIT) {
         // a warp reads its own quarter of the lanes; two warps share a quarter's columns
@@ -620,6 +633,11 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
         }
     }
 
+    // every role is over, and said so if it failed, before the cluster next meets
+    auto tell = [&] {
+        if (!ok)
+            for (uint32_t r = 0; r < ranks; ++r) tc_put_word(tc_map(s_failed, r), 1);
+    };
     if constexpr (SPLIT) {
         // P is B: lanes are n, columns are m
         int p, q;
@@ -653,82 +671,104 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
             // done, the stages are free: each sends its sums to the ranks that join
             // them, [from][width / 4][128 lanes][4] there, a warp's vectors side by side
             // ([256,4096] x [4096,4096] 13.4 us, column by column 18.7).
+            tell();
             __syncwarp();
             __syncthreads();
             tc_cluster_sync();
-            const uint32_t width = BN / ranks, shift = __popc(width - 1);   // powers of two
-            const uint32_t four = width < 4 ? width : 4;                    // columns of a vector
-            if (warp >= 4) {
-                const uint32_t at = quarter * 32 + lane;
+            if (!word(s_failed)) {   // the same in every CTA of the cluster
+                const uint32_t width = BN / ranks, shift = __popc(width - 1);   // powers of two
+                const uint32_t four = width < 4 ? width : 4;                    // columns of a vector
+                if (warp >= 4) {
+                    const uint32_t at = quarter * 32 + lane;
 #pragma unroll 1
-                for (int c = 0; c < most; c += 16) {
-                    float v[16];
-                    tc_load16(lanes + c, v);
-                    if (!ok || kb1 == kb0) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                    }
-                    auto place_of = [&](int i) {
-                        const uint32_t within = (uint32_t)(c + i) & (width - 1);
-                        return tc_map(base + 4 * (rank * width * kTcRows + within * kTcRows +
-                                                  at * four), (uint32_t)(c + i) >> shift);
-                    };
-                    if (four == 4) {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::
-                                             "r"(place_of(i)), "f"(v[i]), "f"(v[i + 1]),
-                                         "f"(v[i + 2]), "f"(v[i + 3])
-                                         : "memory");
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2)
-                            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::
-                                             "r"(place_of(i)), "f"(v[i]), "f"(v[i + 1])
-                                         : "memory");
-                    }
-                }
-                tc_fence_before();
-            }
-            __syncwarp();
-            __syncthreads();
-            tc_cluster_sync();
-            const int row = threadIdx.x & 127;
-            const int64_t n = row0 + row;
-            const int first = (int)(rank * width), last = min(first + (int)width, most);
-            if (n < a.n) {
-                const float bias = tc_bias<T>(a.e, n);
-                const float *const in = reinterpret_cast<const float *>(s_base) + row * four;
-                // two threads a row, a vector of columns at a time
-                for (int c = first + (threadIdx.x >> 7) * (int)four; c < last;
-                     c += (L::kThreads >> 7) * (int)four) {
-                    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (uint32_t r = 0; r < ranks; ++r) {
-                        const float *const from = in + (r * width + (c - first)) * kTcRows;
+                    for (int c = 0; c < most; c += 16) {
+                        float v[16];
+                        tc_load16(lanes + c, v);
+                        auto place_of = [&](int i) {
+                            const uint32_t within = (uint32_t)(c + i) & (width - 1);
+                            return tc_map(base + 4 * (rank * width * kTcRows + within * kTcRows +
+                                                      at * four), (uint32_t)(c + i) >> shift);
+                        };
                         if (four == 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(from);
-                            z[0] += f.x;
-                            z[1] += f.y;
-                            z[2] += f.z;
-                            z[3] += f.w;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::
+                                                 "r"(place_of(i)), "f"(v[i]), "f"(v[i + 1]),
+                                             "f"(v[i + 2]), "f"(v[i + 3])
+                                             : "memory");
                         } else {
-                            const float2 f = *reinterpret_cast<const float2 *>(from);
-                            z[0] += f.x;
-                            z[1] += f.y;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2)
+                                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::
+                                                 "r"(place_of(i)), "f"(v[i]), "f"(v[i + 1])
+                                             : "memory");
                         }
                     }
-                    tc_store_down<T, 4>(a.e, col0 + c, n, z, min((int)four, last - c), bias);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                __syncthreads();
+                tc_cluster_sync();
+                const int row = threadIdx.x & 127;
+                const int64_t n = row0 + row;
+                const int first = (int)(rank * width), last = min(first + (int)width, most);
+                if (n < a.n) {
+                    const float bias = tc_bias<T>(a.e, n);
+                    const float *const in = reinterpret_cast<const float *>(s_base) + row * four;
+                    // two threads a row, a vector of columns at a time
+                    for (int c = first + (threadIdx.x >> 7) * (int)four; c < last;
+                         c += (L::kThreads >> 7) * (int)four) {
+                        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        for (uint32_t r = 0; r < ranks; ++r) {
+                            const float *const from = in + (r * width + (c - first)) * kTcRows;
+                            if (four == 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(from);
+                                z[0] += f.x;
+                                z[1] += f.y;
+                                z[2] += f.z;
+                                z[3] += f.w;
+                            } else {
+                                const float2 f = *reinterpret_cast<const float2 *>(from);
+                                z[0] += f.x;
+                                z[1] += f.y;
+                            }
+                        }
+                        tc_store_down<T, 4>(a.e, col0 + c, n, z, min((int)four, last - c), bias);
+                    }
                 }
             }
         }
     }
 
-    if (!ok && lane == 0 && a.status) atomicOr(a.status, EBIN_DEVICE_WAIT_LIMIT);
+    tell();
     tc_fence_before();
     __syncwarp();
     __syncthreads();
     tc_cluster_sync();
     tc_fence_after();
+    if (word(s_failed)) {   // wind down: what is on its way first
+        if (threadIdx.x == 0 && a.status) atomicOr(a.status, EBIN_DEVICE_WAIT_LIMIT);
+        if (warp == 0 && leader) {
+            const int own = (int)word(s_issued), peer = CTAS == 2 ? (int)word(s_issued + 4) : own;
+            const int end = tc_drain_end(own, peer);
+            for (int j = tc_drain_first(own, peer, a.stages); j < end; ++j) {
+                const uint32_t bar = full(j % a.stages);
+                const TcDrain todo = tc_drain_step(j, own, peer);
+                if (lane == 0 && todo == TC_DRAIN_EXPECT) tc_bar_expect(bar, L::kP + q_bytes);
+                if (lane == 0 && todo == TC_DRAIN_COUNT_OFF) tc_bar_count_off(bar, L::kP + q_bytes);
+                if (!__all_sync(0xFFFFFFFFu, tc_bar_wait(bar, j / a.stages & 1, a.limit))) break;
+            }
+        }
+        if (warp == 1) {
+            if (leader && tc_elect()) tc_commit<CTAS>(drain);
+            __syncwarp();
+            tc_bar_wait(drain, 0, a.limit);
+        }
+        __syncwarp();
+        __syncthreads();
+        tc_cluster_sync();
+        tc_fence_after();
+    }
     if (warp == 2) tc_free<CTAS>(tmem, L::kColumns);
 }
 
