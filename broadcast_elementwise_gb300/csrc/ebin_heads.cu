@@ -102,23 +102,61 @@ struct Placed {
     int64_t span;   // elements
 };
 
-// Whether two views share an element (conservatively: true when unsure).
-// Ranges apart never do.  Views that step through one buffer with the same
-// batch and token strides do not when, within a token's step, their heads lie
-// apart: q and k of one projection's output.
+// A step taken c times, lo <= c <= hi.
+struct Walk {
+    int64_t step, lo, hi;
+};
+
+// Whether some counts c put the sum of c step within `width` of `target`.  Walks in
+// falling order of their steps, so that each level of nested strides leaves one or
+// two counts to try; past `tries` the answer is yes.
+bool walks_meet(const Walk *w, int n, int64_t target, int64_t width, int &tries) {
+    if (--tries < 0) return true;
+    int64_t lo = 0, hi = 0;   // what the walks after the first can add
+    for (int i = 1; i < n; ++i) {
+        lo += w[i].lo * w[i].step;
+        hi += w[i].hi * w[i].step;
+    }
+    if (n == 0) return target > -width && target < width;
+    // c step lies in (target - hi - width, target - lo + width)
+    const int64_t from = target - hi - width, to = target - lo + width, s = w->step;
+    const int64_t first = from >= 0 ? from / s + 1 : -((-from - 1) / s);
+    const int64_t last = to > 0 ? (to - 1) / s : -((-to) / s) - 1;
+    for (int64_t c = std::max(first, w->lo); c <= std::min(last, w->hi); ++c)
+        if (walks_meet(w + 1, n - 1, target - c * s, width, tries)) return true;
+    return false;
+}
+
+// Whether two views share an element (true when the search for one gets too
+// long).  Rows of head_dim elements of x and y share one when their starts are
+// less than head_dim apart: y's first start less x's is then within head_dim
+// of a sum of x's steps forward and y's back.
 bool heads_share(const ebin_heads_attrs &a, const Placed &x, const Placed &y, int64_t isz) {
     if (!ranges_overlap(x.p, x.span * isz, y.p, y.span * isz)) return false;
-    if (x.v->token != y.v->token || (a.batch > 1 && x.v->batch != y.v->batch)) return true;
-    const int64_t step = x.v->token;
-    if (step <= 0 || (a.batch > 1 && x.v->batch % step != 0)) return true;
     const int64_t d = (int64_t)((intptr_t)y.p - (intptr_t)x.p);
     if (d % isz != 0) return true;
-    int64_t off = (d / isz) % step;
-    if (off < 0) off += step;
-    const int64_t wx = (x.heads - 1) * x.v->head + a.head_dim;
-    const int64_t wy = (y.heads - 1) * y.v->head + a.head_dim;
-    // x takes [0, wx) of each step, y takes [off, off + wy)
-    return !(wx <= off && off + wy <= step);
+    const int64_t nx[3] = {a.batch, a.tokens, x.heads}, ny[3] = {a.batch, a.tokens, y.heads};
+    const int64_t sx[3] = {x.v->batch, x.v->token, x.v->head};
+    const int64_t sy[3] = {y.v->batch, y.v->token, y.v->head};
+    Walk w[6];
+    int n = 0;
+    auto add = [&](int64_t step, int64_t lo, int64_t hi) {
+        if (step == 0 || lo == hi) return;   // goes nowhere
+        for (int i = 0; i < n; ++i)
+            if (w[i].step == step) {
+                w[i].lo += lo;
+                w[i].hi += hi;
+                return;
+            }
+        w[n++] = Walk{step, lo, hi};
+    };
+    for (int i = 0; i < 3; ++i) {
+        add(sx[i], 0, nx[i] - 1);
+        add(sy[i], 1 - ny[i], 0);
+    }
+    std::sort(w, w + n, [](const Walk &p, const Walk &q) { return p.step > q.step; });
+    int tries = 256;
+    return walks_meet(w, n, d / isz, a.head_dim, tries);
 }
 
 bool same_view(const ebin_heads_attrs &a, const Placed &x, const Placed &y) {

@@ -111,3 +111,49 @@ def test_a_table_without_rows(D, r, layout, tokens, dtype):
     got = eb.rotary(q, k, none, none, layout=layout)
     assert eb.get_device_status() == eb.DEVICE_POSITION_RANGE
     assert (got[0] == 0).all() and (got[1] == 0).all()
+
+
+def packed(order, batch, tokens, q_heads, k_heads, dim):
+    """(buffer, q, k) of one projection, its buffer laid out in the given order."""
+    h = q_heads + 2 * k_heads
+    if order == "heads, tokens":
+        x = normal(11, batch, h, tokens, dim)
+        v = x.transpose(1, 2)
+    elif order == "tokens, heads":
+        v = x = normal(11, batch, tokens, h, dim)
+    elif order == "tokens, q k v of each head":
+        x = normal(11, batch, tokens, q_heads, 3, dim)
+        return x, x[:, :, :, 0], x[:, :, :k_heads, 1]
+    else:
+        x = normal(11, batch, 3, q_heads, tokens, dim)
+        v = x.transpose(2, 3)
+        return x, v[:, 0], v[:, 1, :, :k_heads]
+    return x, v[:, :, :q_heads], v[:, :, q_heads:q_heads + k_heads]
+
+
+@pytest.mark.parametrize("order", ["tokens, heads", "heads, tokens", "tokens, q k v of each head",
+                                   "q k v, heads, tokens"])
+@pytest.mark.parametrize("tokens,D,r", [(1, 64, 64), (37, 64, 64), (37, 80, 30), (9000, 64, 32),
+                                        (21, 33, 22)])
+def test_packed_buffers_in_place(order, tokens, D, r):
+    """q and k in place in a projection's buffer, however it is laid out: what the call out of
+    place gives, and nothing else of the buffer is touched."""
+    x, q, k = packed(order, 2, tokens, 4, 2, D)
+    cos, sin = eb.rotary_table(tokens, r)
+    w = normal(12, D)
+    before, rest = x.clone(), torch.ones_like(x, dtype=torch.bool)
+    for t in (q, k):
+        rest.as_strided(t.shape, t.stride(), t.storage_offset()).fill_(False)
+    want = eb.rotary(q, k, cos, sin)
+    eb.rotary(q, k, cos, sin, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    want = eb.qk_norm_rotary(q, k, w, w, cos, sin)
+    eb.qk_norm_rotary(q, k, w, w, cos, sin, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    _, fq, fk = packed(order, 2, tokens, 4, 2, D)
+    want = eb.qk_norm_rotary_grad(q, k, fq, fk, w, w, cos, sin)
+    got = eb.qk_norm_rotary_grad(q, k, fq, fk, w, w, cos, sin, out=(q, k))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert torch.equal(x[rest], before[rest])
+    assert eb.get_device_status() == 0

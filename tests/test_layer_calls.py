@@ -1,6 +1,8 @@
 """What the one-call forms of the layer operators check and pass on, on the CPU:
 tensors stand in for device ones, and the launches are recorded."""
 import contextlib
+import itertools
+import random
 import types
 
 import pytest
@@ -9,6 +11,8 @@ import torch
 import broadcast_elementwise_gb300 as eb
 
 BF16 = torch.bfloat16
+needs_no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
+                                  reason="the addresses would be launched on")
 
 
 @pytest.fixture
@@ -195,7 +199,7 @@ def test_a_rotation_needs_its_tables_length():
     eb.HeadsPlan(BF16, (1, 2, 3, 8), table_positions=0)
 
 
-@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses would be launched on")
+@needs_no_gpu
 def test_an_empty_table_may_be_null():
     """Without a row there is nothing to read: the call gets as far as the device."""
     for rows, code in ((0, "cuda"), (1, "invalid_arg")):
@@ -203,3 +207,103 @@ def test_an_empty_table_may_be_null():
         with pytest.raises(eb.EbinError) as e:
             eb.execute_heads(plan, 0x100000, None, None, None, None, 0x200000, None, stream=0)
         assert e.value.code == code
+
+
+# ------------------------------------------------------------------ views of one buffer
+
+def outcome(fn, *a, **kw):
+    """The status of a call that cannot succeed here: "cuda" once nothing is refused."""
+    with pytest.raises(eb.EbinError) as e:
+        fn(*a, **kw)
+    return e.value.code
+
+
+def in_place(q, k):
+    """Rotate views q and k (CPU tensors for their shapes, strides and addresses) in place."""
+    plan = eb.HeadsPlan(q.dtype, q.shape, k.shape, table_positions=16, q_strides=q.stride(),
+                        k_strides=k.stride(), q_out_strides=q.stride(), k_out_strides=k.stride())
+    at = 1 << 40      # far from the tables
+    base = min(q.data_ptr(), k.data_ptr())
+    q, k = (at + t.data_ptr() - base for t in (q, k))
+    return outcome(eb.execute_heads, plan, q, k, 0x100000, 0x200000, None, q, k, stream=0)
+
+
+def packed(order, batch, tokens, q_heads, k_heads, dim):
+    """q and k of one projection, its buffer laid out in the given order."""
+    h = q_heads + 2 * k_heads
+    if order == "tokens, heads":
+        x = mat(batch, tokens, h, dim)
+    elif order == "heads, tokens":
+        x = mat(batch, h, tokens, dim).transpose(1, 2)
+    elif order == "tokens, q k v of each head":
+        x = mat(batch, tokens, q_heads, 3, dim)
+        return x[:, :, :, 0], x[:, :, :k_heads, 1]
+    else:                                    # q, k, v of a sequence one after another
+        x = mat(batch, 3, q_heads, tokens, dim).transpose(2, 3)
+        return x[:, 0], x[:, 1, :, :k_heads]
+    return x[:, :, :q_heads], x[:, :, q_heads:q_heads + k_heads]
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("order", ["tokens, heads", "heads, tokens", "tokens, q k v of each head",
+                                   "q k v, heads, tokens"])
+@pytest.mark.parametrize("sizes", [(1, 5, 4, 2, 8), (2, 5, 4, 2, 8), (3, 1, 4, 4, 8),
+                                   (2, 4096, 32, 8, 128), (7, 3, 1, 1, 2)], ids=str)
+def test_packed_views_in_place_share_nothing(order, sizes):
+    q, k = packed(order, *sizes)
+    assert in_place(q, k) == "cuda"
+
+
+@needs_no_gpu
+def test_views_that_share_are_refused():
+    q, k = packed("heads, tokens", 2, 5, 4, 2, 8)
+    x = mat(2, 8, 5, 8).transpose(1, 2)
+    assert in_place(x[:, :, :4], x[:, :, 3:5]) == "alias"
+    assert in_place(x[:, :, ::2], x[:, :, 1::2]) == "cuda"
+    assert in_place(x[:, :, ::2], x[:, :, 2:4]) == "alias"
+    y = mat(2, 5, 4, 20)
+    assert in_place(y[..., :8], y[..., 8:16]) == "cuda"
+    assert in_place(y[..., :8], y[..., 7:15]) == "alias"
+
+
+def starts(batch, tokens, heads, strides, first):
+    return [first + b * strides[0] + t * strides[1] + h * strides[2]
+            for b, t, h in itertools.product(range(batch), range(tokens), range(heads))]
+
+
+@needs_no_gpu
+def test_overlap_against_every_element():
+    """Random views against the sets of their elements: an accepted pair shares none, and
+    a refused one does (these are too small for the search to give up)."""
+    rng = random.Random(5)
+    seen = {"alias": 0, "cuda": 0}
+    while min(seen.values()) < 300 or sum(seen.values()) < 2000:
+        batch, tokens, dim = rng.randint(1, 3), rng.randint(1, 4), rng.choice([1, 2, 4])
+        heads = rng.randint(1, 3), rng.randint(1, 3)
+        views = []
+        for h in heads:
+            n = [batch, tokens, h]
+            order = rng.sample(range(3), 3)
+            strides, step = [0] * 3, dim * rng.randint(1, 4)
+            for i in order:
+                strides[i] = step
+                step = step * n[i] + rng.choice([0, 0, dim, 3])
+            views.append((h, strides))
+        if rng.random() < 0.5:                # the same steps, as views of one buffer have
+            views[1] = (heads[1], views[0][1])
+        d = rng.randint(-40, 40)
+        rows = [starts(batch, tokens, h, st, f) for (h, st), f in zip(views, (0, d))]
+        try:
+            q, k = ((batch, tokens, h, dim) for h in heads)
+            st = [tuple(s) + (1,) for _, s in views]
+            plan = eb.HeadsPlan("bfloat16", q, k, rotary_dim=0, q_strides=st[0], k_strides=st[1],
+                                q_out_strides=st[0], k_out_strides=st[1])
+        except eb.EbinError as e:             # an output that overlaps itself
+            assert e.code == "invalid_arg"
+            continue
+        at = 1 << 40
+        got = outcome(eb.execute_heads, plan, at, at + 2 * d, None, None, None, at, at + 2 * d,
+                      stream=0)
+        elements = [{r + j for r in rr for j in range(dim)} for rr in rows]
+        assert got == ("alias" if elements[0] & elements[1] else "cuda"), (views, d, dim)
+        seen[got] += 1
