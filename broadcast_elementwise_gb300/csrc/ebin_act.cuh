@@ -54,7 +54,30 @@ template <int ACT> __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
-// The derivative in full binary32.
+// Derivatives are flat, 0 or 1, far out and up to an infinite z (which a binary16
+// pre-activation past 65504 is stored as).  Past kActFar every exponential below is 0
+// or infinite, so z is held to it: the formulas would multiply an infinite z by 0.
+constexpr float kActFar = 100.0f;
+
+// A NaN stays one.  binary32, then 16-bit z alone and two to a word.
+__device__ __forceinline__ float act_near(float z) {
+    asm("max.NaN.f32 %0, %0, %1;\n\tmin.NaN.f32 %0, %0, %2;" : "+f"(z) : "f"(-kActFar), "f"(kActFar));
+    return z;
+}
+template <class T> __device__ __forceinline__ T act_near(T z) {
+    return __hmin_nan(__hmax_nan(z, from_f<T>(-kActFar)), from_f<T>(kActFar));
+}
+template <class T> __device__ __forceinline__ uint32_t act_near2(uint32_t w) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                         __nv_bfloat162>::type;
+    T2 lo, hi;
+    lo.x = lo.y = from_f<T>(-kActFar);
+    hi.x = hi.y = from_f<T>(kActFar);
+    const T2 z = __hmin2_nan(__hmax2_nan(*reinterpret_cast<const T2 *>(&w), lo), hi);
+    return *reinterpret_cast<const uint32_t *>(&z);
+}
+
+// The derivative in full binary32, |z| <= kActFar.
 template <int ACT> __device__ __forceinline__ float act_slope_full(float z) {
     if constexpr (ACT == EBIN_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     if constexpr (ACT == EBIN_ACT_GELU)
@@ -63,13 +86,11 @@ template <int ACT> __device__ __forceinline__ float act_slope_full(float z) {
     if constexpr (ACT == EBIN_ACT_GELU_TANH) {
         const float s = 1.0f / (1.0f + expf(-act_tanh_arg(z)));
         const float du = fmaf(z * z, 0.214064448818f, 1.59576912161f);
-        const float t = s * (1.0f - s);
-        return t == 0.0f ? s : fmaf(z * t, du, s);   // flat far out, where z du may be infinite
+        return fmaf(z * (s * (1.0f - s)), du, s);
     }
     if constexpr (ACT == EBIN_ACT_SILU) {
         const float s = 1.0f / (1.0f + expf(-z));
-        const float t = s * (1.0f - s);
-        return t == 0.0f ? s : fmaf(z, t, s);
+        return fmaf(z, s * (1.0f - s), s);
     }
     return 1.0f;
 }
@@ -82,7 +103,8 @@ __device__ __forceinline__ float2 act_rcp(float2 x) {
     return make_float2(act_rcp(x.x), act_rcp(x.y));
 }
 
-// The derivative for 16-bit data, two at a time on the packed binary32 pipe.
+// The derivative for 16-bit data, |z| <= kActFar, two at a time on the packed
+// binary32 pipe.
 template <int ACT> __device__ __forceinline__ float2 act_slope2(float2 z) {
     if constexpr (ACT == EBIN_ACT_RELU)
         return make_float2(act_slope_full<ACT>(z.x), act_slope_full<ACT>(z.y));
@@ -107,9 +129,7 @@ template <int ACT> __device__ __forceinline__ float2 act_slope2(float2 z) {
             __fadd2_rn(act_ex2(__fmul2_rn(u, act_pair(-kLog2e))), act_pair(1.0f)));
         const float2 t = __ffma2_rn(make_float2(-s.x, -s.y), s, s);
         const float2 du = __ffma2_rn(zz, act_pair(0.214064449f), act_pair(1.59576912f));
-        const float2 r = __ffma2_rn(__fmul2_rn(z, t), du, s);
-        // flat far out, where z du may be infinite
-        return make_float2(t.x == 0.0f ? s.x : r.x, t.y == 0.0f ? s.y : r.y);
+        return __ffma2_rn(__fmul2_rn(z, t), du, s);
     }
     if constexpr (ACT == EBIN_ACT_SILU) {
         const float2 s = act_rcp(

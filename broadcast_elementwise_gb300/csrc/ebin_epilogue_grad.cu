@@ -42,7 +42,7 @@ __device__ __forceinline__ EgVec<T, V> eg_vector(const EgVec<T, V> &g, const EgV
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 d = open2<T>(gw[i]);
-            if constexpr (ACT != EBIN_ACT_NONE) d = __fmul2_rn(d, act_slope2<ACT>(open2<T>(zw[i])));
+            if constexpr (ACT != EBIN_ACT_NONE) d = __fmul2_rn(d, act_slope2<ACT>(open2<T>(act_near2<T>(zw[i]))));
             s2[i] = __fadd2_rn(s2[i], d);
             ow[i] = pack2<T>(d);
         }
@@ -52,8 +52,9 @@ __device__ __forceinline__ EgVec<T, V> eg_vector(const EgVec<T, V> &g, const EgV
         for (int i = 0; i < V; ++i) {
             float d = to_f(g.v[i]);
             if constexpr (ACT != EBIN_ACT_NONE) {
-                if constexpr (sizeof(T) == 2) d *= act_slope2<ACT>(act_pair(to_f(z.v[i]))).x;
-                else d *= act_slope_full<ACT>(to_f(z.v[i]));
+                const float x = to_f(act_near(z.v[i]));
+                if constexpr (sizeof(T) == 2) d *= act_slope2<ACT>(act_pair(x)).x;
+                else d *= act_slope_full<ACT>(x);
             }
             sum[i] += d;
             out.v[i] = from_f<T>(d);

@@ -787,7 +787,8 @@ ebin_status ebin_gemm_execute(ebin_gemm_plan_t plan, const void *A, const void *
  *   dtype     of dy, z and dz: FLOAT16, BFLOAT16 or FLOAT32
  *   has_bias  whether dbias [n] binary32 is wanted
  *   m, n      >= 0; ld_dy, ld_z, ld_dz: row strides (0 = dense)
- * With NONE z is not read.
+ * With NONE z is not read.  At an infinite z act' is its limit, 0 or 1: a FLOAT16
+ * pre-activation past 65504 is kept as one.
  */
 typedef struct ebin_epilogue_grad_attrs {
     ebin_dtype dtype;
