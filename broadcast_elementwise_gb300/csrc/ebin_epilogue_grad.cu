@@ -7,7 +7,7 @@
 // column sums in registers; the CTA's warps join in shared memory in a fixed
 // order, the parts in a second, small launch.  16-bit data takes its slopes two
 // at a time in the fast forms of ebin_act.cuh ([4096,4096]: SiLU 34.3 us in
-// scalar form with full exp and quotient, 18.6 so; GELU with erff 43.5, 18.9).
+// scalar form with full exp and quotient, 18.5 so; GELU with erff 43.5, 19.1).
 #include <new>
 
 #include "ebin_act.cuh"
