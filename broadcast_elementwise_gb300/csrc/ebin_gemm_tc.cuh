@@ -279,17 +279,6 @@ template <int N> __device__ __forceinline__ void tc_act(int act, float *v) {
     }
 }
 
-// One element's epilogue where neighbouring lanes hold neighbouring n.
-template <class T>
-__device__ __forceinline__ void tc_store_one(const GemmEpilogue &e, int64_t m, int64_t n, float z,
-                                             float bias) {
-    z += bias;
-    if (e.z) static_cast<T *>(e.z)[m * e.ldz + n] = from_f<T>(z);
-    float y = z;
-    tc_act<1>(e.act, &y);
-    if (e.residual) y += to_f(static_cast<const T *>(e.residual)[m * e.ld_residual + n]);
-    static_cast<T *>(e.y)[m * e.ldy + n] = from_f<T>(y);
-}
 template <class T>
 __device__ __forceinline__ float tc_bias(const GemmEpilogue &e, int64_t n) {
     if (!e.bias) return 0.0f;
