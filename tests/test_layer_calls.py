@@ -307,3 +307,27 @@ def test_overlap_against_every_element():
         elements = [{r + j for r in rr for j in range(dim)} for rr in rows]
         assert got == ("alias" if elements[0] & elements[1] else "cuda"), (views, d, dim)
         seen[got] += 1
+
+
+# ------------------------------------------------------------------ the current stream
+
+def test_the_current_stream_without_torch_internals(monkeypatch):
+    """The address comes from torch's public call where its parts are missing, take other
+    arguments or disagree with it; and from the parts where they do not."""
+    now = types.SimpleNamespace(cuda_stream=HANDLE)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: now)
+    parts = {"_cuda_getDevice": lambda: 0, "_cuda_getCurrentRawStream": lambda d: HANDLE + d}
+    for broken in (dict(_cuda_getDevice=None), dict(_cuda_getCurrentRawStream=None),
+                   dict(_cuda_getCurrentRawStream=lambda: HANDLE),
+                   dict(_cuda_getDevice=lambda: 1), dict()):
+        for name, fn in {**parts, **broken}.items():
+            if fn is None:
+                monkeypatch.delattr(torch._C, name, raising=False)
+            else:
+                monkeypatch.setattr(torch._C, name, fn, raising=False)
+        monkeypatch.setattr(eb, "_current", None)
+        now.cuda_stream = HANDLE
+        assert eb._stream(None) == HANDLE
+        now.cuda_stream = HANDLE + 8
+        assert eb._stream(None) == (HANDLE + 8 if broken else HANDLE)
+    assert eb._stream(7) == 7 and eb._stream(now) == HANDLE + 8
