@@ -182,16 +182,17 @@ struct Shape {
 // CTA its matrix instructions or its copies, whichever is longer (on a pair
 // 1.05 ns a column; copies at 190 bytes a ns), and 24 ns that keep wide tiles,
 // which move fewer bytes a product, ahead of a narrower one's last wave where
-// that gains under a tenth ([4096,4096] x [4096,8192] on 160 columns 163 us, on
-// 256 146 us; 4096^3 on 256 columns 98 us, on 224 87 us); a tile's end costs 12 ns
-// a column once, the sums of split tiles 1.5 us more.  On single CTAs a step
-// takes 140 ns to 64 columns, 230 to 128 with every SM at it ([256,4096] x
-// [4096,4096] on pairs of 64 columns 12.6 us, on split tiles of 128 13.4;
-// [128,4096] x [4096,4096] 13.0 and 10.9).
+// that gains under a tenth (medians of runs in turn: [4096,4096] x [4096,8192] on
+// 160 columns 149 us, on 256 150; 4096^3 on 256 columns 96 us, on 224 85); a tile's end
+// costs 12 ns a column once, the sums of split tiles 1.5 us more.  On single CTAs a
+// step takes 140 ns to 64 columns, 230 to 128 with every SM at it (operands from
+// memory and, after the stroke, in the L2: [256,4096] x [4096,4096] on pairs of 64
+// columns 13.4 / 12.5 us, on tiles of 128 split in two 15.0 / 13.4; [128,4096] x
+// [4096,4096] on pairs of 64 13.2 / 12.4, on tiles of 128 split in four 13.1 / 10.7).
 //   pair   256 rows of A by 64 to 256 columns, a CTA pair each, waves of pairs
 //   split  128 columns of B by 16 to 128 rows of A, k cut in up to eight while
-//          all clusters fit at once ([4,4096] x [4096,4096] cut in eight, two
-//          waves of clusters: 21.4 us; in four, one wave: 9.6)
+//          all clusters fit at once ([4,4096] x [4096,4096] from memory cut in eight,
+//          two waves of clusters: 20.1 us; in four, one wave: 9.8; in two 10.2)
 Shape gemm_shape(const ebin_gemm_attrs &at, int sms) {
     const bool bf16 = at.dtype == EBIN_BFLOAT16;
     const double kblocks = (double)div_up(at.k, kTcBK);

@@ -18,12 +18,13 @@
 // EBIN_DEVICE_WAIT_LIMIT is raised and the output is not valid.
 //
 // What bounds it.  Large products: the matrix instructions (a pair's 256 x 256 x
-// 64 step takes 512 clocks at best) and the power they draw: [4096,4096] x
-// [4096,8192] bf16 with bias and GELU 146 us, 1880 TFLOP/s; 8192^3 with a
-// residual 630 to 690 us at the 1.5 to 1.7 GHz that a long run holds.  Few rows:
-// reading B: [4,4096] x [4096,4096] 6.7 us, 33.5 MB behind 2.6 us of set-up and
-// join.  In between, a CTA's copies (190 bytes a ns) and the 4 to 6 us of an
-// unoverlapped first tile and last epilogue.
+// 64 step takes 512 clocks at best) and the power they draw, so that times go by
+// the clock that the limit leaves (1.5 to 1.7 GHz in a long run): [4096,4096] x
+// [4096,8192] bf16 154 us, with bias and GELU 160 to 168, 1640 to 1720 TFLOP/s; 8192^3
+// 547 to 630 us.  Few rows: reading B, [4,4096] x [4096,4096] 9.8 us from memory: 5.0
+// us of reading at the copy's rate, the rest launch, set-up, the cluster's meetings
+// and the join (7.2 us with B in the L2).  In between, a CTA's copies (190 bytes a
+// ns) and the 4 to 6 us of an unoverlapped first tile and last epilogue.
 #pragma once
 
 #include <type_traits>
@@ -659,7 +660,8 @@ k_gemm_tc(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUt
             // A rank joins `width` neighbouring columns.  Once every CTA's products are
             // done, the stages are free: each sends its sums to the ranks that join
             // them, [from][width / 4][128 lanes][4] there, a warp's vectors side by side
-            // ([256,4096] x [4096,4096] 13.4 us, column by column 18.7).
+            // ([256,4096] x [4096,4096] on tiles of 128 columns, operands in the L2, 13.4
+            // us; column by column 18.7).
             tell();
             __syncwarp();
             __syncthreads();

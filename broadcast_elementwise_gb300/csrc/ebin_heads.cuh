@@ -3,10 +3,12 @@
 //
 // Bound by memory: every kernel but k_heads_any reads each input element once
 // and writes each output element once, and the floor is that traffic.  Measured
-// on GB300, bf16, q and k of 32 and 8 heads of 128 (copy: 6784 GB/s):
-//   rotation            [1,16384] tokens   52.7 us   6530 GB/s   k_heads_vec
-//   norm and rotation   [2,4096] tokens    29.0 us   5860 GB/s   k_heads_ring
-//   its gradient        [2,4096] tokens    46.3 us   5480 GB/s   k_heads_vec_grad
+// on GB300, bf16, q and k of 32 and 8 heads of 128, over sets of inputs that
+// together pass the L2 (copy: 6694 GB/s):
+//   rotation            [1,16384] tokens   52.5 us   6550 GB/s   k_heads_vec
+//   norm and rotation   [2,4096] tokens    29.4 us   5780 GB/s   k_heads_ring
+//   its gradient        [2,4096] tokens    46.1 us   5500 GB/s   k_heads_vec_grad
+// With 62 of the 128 rotated (HEADS_ODD), [2,4096] tokens: 47.6, 70.0 and 82.0 us.
 // Arithmetic is binary32 throughout, with one rounding to the element type at
 // the store.
 #pragma once
@@ -78,8 +80,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 // strides, any alignment.  A lane owns whole pairs (and single elements past
 // rotary_dim), so an output may be its own input; a norm reads its row twice,
 // the second time from the L1.  grid.y picks q or k; a CTA of the gradient keeps
-// its warps' weight-gradient sums in shared memory.  About a tenth of the copy's
-// rate (one element a lane and access): the path of what has no vectors.
+// its warps' weight-gradient sums in shared memory.  The path of what has no
+// vectors, one element a lane and access: an eighth of the copy's rate for heads of
+// 128 off 16 bytes (rotation of [2,4096,40,128] bf16 195 us, norm 219, its gradient
+// 271), a twentieth for heads of 33, where a row of 66 bytes takes a warp (143 us).
 template <class T, int MODE>
 __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, int interleaved) {
     extern __shared__ float s_dw[];   // HEADS_NORM_GRAD: [warps][dim]

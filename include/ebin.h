@@ -771,7 +771,8 @@ void ebin_gemm_plan_release(ebin_gemm_plan_t plan);
  *   preact     NULL, or [m, n] that receives z rounded to dtype: what the gradient reads
  *   workspace  at least ebin_gemm_plan_workspace bytes, 16-byte aligned; not shared with
  *              work in flight on another stream
- * Any other overlap with Y or preact is ALIAS.  With m = 0 or n = 0 nothing
+ * Any other overlap of the address ranges, first element to last, of Y or
+ * preact with another buffer is ALIAS.  With m = 0 or n = 0 nothing
  * is read or written.  Every wait inside the kernel has a limit; one that
  * runs out sets EBIN_DEVICE_WAIT_LIMIT in the stream's status word, which the
  * first call on a stream allocates (capture into a graph after that).
