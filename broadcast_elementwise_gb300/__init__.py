@@ -57,8 +57,9 @@ DEVICE_DIV_BY_ZERO = 0x1
 DEVICE_SHIFT_RANGE = 0x2
 DEVICE_POSITION_RANGE = 0x4
 DEVICE_WAIT_LIMIT = 0x8
-NORMS = {"none": 0, "rms": 1}
+NORMS = {"none": 0, "rms": 1, "layer": 2}
 LAYOUTS = {"half": 0, "interleaved": 1}
+AXES_ORDERS = {"blocks": 0, "dealt": 1}
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 MAX_RANK = 8
@@ -86,6 +87,11 @@ class ebin_rotary_attrs(ctypes.Structure):
                 ("base", ctypes.c_double), ("factor", ctypes.c_double),
                 ("trained_length", ctypes.c_double), ("slow_turns", ctypes.c_double),
                 ("fast_turns", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class ebin_rotary_axes(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("order", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4), ("position_stride", ctypes.c_int64)]
 
 
 class ebin_heads_view(ctypes.Structure):
@@ -119,6 +125,37 @@ class ebin_epilogue_grad_attrs(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int), ("activation", ctypes.c_int32),
                 ("has_bias", ctypes.c_int32), ("m", ctypes.c_int64), ("n", ctypes.c_int64),
                 ("ld_dy", ctypes.c_int64), ("ld_z", ctypes.c_int64), ("ld_dz", ctypes.c_int64)]
+
+
+class ebin_dropout_attrs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("dtype_bias", ctypes.c_int),
+                ("has_bias", ctypes.c_int32), ("has_residual", ctypes.c_int32),
+                ("gradient", ctypes.c_int32), ("p", ctypes.c_double), ("rows", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64)]
+
+
+class ebin_block_norm_attrs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "dtype_stream", "dtype_w", "dtype_mod")] +
+                [(n, ctypes.c_int32) for n in ("post", "pre", "has_branch", "gradient")] +
+                [(n, ctypes.c_float) for n in ("epsilon_post", "epsilon_pre", "stream_scale",
+                                               "branch_scale")] +
+                [("p", ctypes.c_double)] +
+                [(n, ctypes.c_int64) for n in ("rows", "n", "gate_rows", "mod_rows", "ld_x",
+                                               "ld_y", "ld_h", "ld_z", "ld_gate", "ld_scale",
+                                               "ld_shift", "ld_dz", "ld_dh", "ld_dx", "ld_dy")])
+
+
+class ebin_block_norm_params(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("gate", "w_post", "b_post", "w_pre", "b_pre",
+                                                "scale", "shift")] +
+                [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                 ("offset_device", ctypes.c_void_p)])
+
+
+class ebin_block_norm_grads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "w_post", "b_post", "w_pre", "b_pre",
+                                               "scale", "shift")]
 
 
 def _load():
@@ -160,6 +197,11 @@ def _load():
         "ebin_noalloc_read_status": (i32, [i32, vp, ctypes.POINTER(ctypes.c_uint32)]),
         "ebin_rotary_table": (i32, [ctypes.POINTER(ebin_rotary_attrs), i64, i64, vp, vp, vp]),
         "ebin_heads_plan_create": (i32, [ctypes.POINTER(ebin_heads_attrs), ctypes.POINTER(vp)]),
+        "ebin_rotary_table_axes": (i32, [ctypes.POINTER(ebin_rotary_attrs),
+                                         ctypes.POINTER(ebin_rotary_axes), i64, i64, vp, vp, vp]),
+        "ebin_heads_plan_create_axes": (i32, [ctypes.POINTER(ebin_heads_attrs),
+                                              ctypes.POINTER(ebin_rotary_axes),
+                                              ctypes.POINTER(vp)]),
         "ebin_heads_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
         "ebin_heads_plan_release": (None, [vp]),
         "ebin_heads_execute": (i32, [vp] * 11),
@@ -173,6 +215,22 @@ def _load():
         "ebin_epilogue_grad_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
         "ebin_epilogue_grad_plan_release": (None, [vp]),
         "ebin_epilogue_grad_execute": (i32, [vp] * 6 + [ctypes.c_size_t, vp]),
+        "ebin_dropout_plan_create": (i32, [ctypes.POINTER(ebin_dropout_attrs),
+                                           ctypes.POINTER(vp)]),
+        "ebin_dropout_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
+        "ebin_dropout_plan_release": (None, [vp]),
+        "ebin_dropout_execute": (i32, [vp] * 5 + [ctypes.c_uint64] * 2 + [vp] * 2),
+        "ebin_dropout_grad_execute": (i32, [vp] * 5 + [ctypes.c_size_t] + [ctypes.c_uint64] * 2 +
+                                      [vp] * 2),
+        "ebin_block_norm_plan_create": (i32, [ctypes.POINTER(ebin_block_norm_attrs),
+                                              ctypes.POINTER(vp)]),
+        "ebin_block_norm_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
+        "ebin_block_norm_plan_release": (None, [vp]),
+        "ebin_block_norm_execute": (i32, [vp] * 3 + [ctypes.POINTER(ebin_block_norm_params)] +
+                                    [vp] * 3),
+        "ebin_block_norm_grad_execute": (i32, [vp] * 5 + [ctypes.POINTER(ebin_block_norm_params)] +
+                                         [vp] * 2 + [ctypes.POINTER(ebin_block_norm_grads), vp,
+                                                     ctypes.c_size_t, vp]),
         "ebin_launch_count": (ctypes.c_uint64, []),
         "ebin_dtype_size": (ctypes.c_size_t, [i32]),
         "ebin_status_string": (ctypes.c_char_p, [i32]),
@@ -404,6 +462,19 @@ def ebin_rotary_table(attrs, first_position, positions, cos, sin, stream) -> Non
                                  sin, stream), "ebin_rotary_table")
 
 
+def ebin_rotary_table_axes(attrs, axes, first_position, positions, cos, sin, stream) -> None:
+    _check(lib.ebin_rotary_table_axes(ctypes.byref(attrs), ctypes.byref(axes),
+                                      int(first_position), int(positions), cos, sin, stream),
+           "ebin_rotary_table_axes")
+
+
+def ebin_heads_plan_create_axes(attrs, axes) -> int:
+    out = ctypes.c_void_p()
+    _check(lib.ebin_heads_plan_create_axes(ctypes.byref(attrs), ctypes.byref(axes),
+                                           ctypes.byref(out)), "ebin_heads_plan_create_axes")
+    return out.value
+
+
 def ebin_heads_plan_create(attrs) -> int:
     out = ctypes.c_void_p()
     _check(lib.ebin_heads_plan_create(ctypes.byref(attrs), ctypes.byref(out)),
@@ -482,6 +553,71 @@ def ebin_epilogue_grad_execute(plan, dy, z, dz, dbias, workspace, workspace_byte
     st = lib.ebin_epilogue_grad_execute(plan, dy, z, dz, dbias, workspace, workspace_bytes, stream)
     if st:
         raise EbinError(st, "ebin_epilogue_grad_execute")
+
+
+def ebin_dropout_plan_create(attrs) -> int:
+    out = ctypes.c_void_p()
+    _check(lib.ebin_dropout_plan_create(ctypes.byref(attrs), ctypes.byref(out)),
+           "ebin_dropout_plan_create")
+    return out.value
+
+
+def ebin_dropout_plan_workspace(plan) -> int:
+    v = ctypes.c_size_t()
+    _check(lib.ebin_dropout_plan_workspace(plan, ctypes.byref(v)), "ebin_dropout_plan_workspace")
+    return v.value
+
+
+def ebin_dropout_plan_release(plan) -> None:
+    lib.ebin_dropout_plan_release(plan)
+
+
+def ebin_dropout_execute(plan, x, bias, residual, y, seed, offset, offset_device, stream) -> None:
+    st = lib.ebin_dropout_execute(plan, x, bias, residual, y, seed, offset, offset_device, stream)
+    if st:
+        raise EbinError(st, "ebin_dropout_execute")
+
+
+def ebin_dropout_grad_execute(plan, dy, dx, dbias, workspace, workspace_bytes, seed, offset,
+                              offset_device, stream) -> None:
+    st = lib.ebin_dropout_grad_execute(plan, dy, dx, dbias, workspace, workspace_bytes, seed,
+                                       offset, offset_device, stream)
+    if st:
+        raise EbinError(st, "ebin_dropout_grad_execute")
+
+
+def ebin_block_norm_plan_create(attrs) -> int:
+    out = ctypes.c_void_p()
+    _check(lib.ebin_block_norm_plan_create(ctypes.byref(attrs), ctypes.byref(out)),
+           "ebin_block_norm_plan_create")
+    return out.value
+
+
+def ebin_block_norm_plan_workspace(plan) -> int:
+    v = ctypes.c_size_t()
+    _check(lib.ebin_block_norm_plan_workspace(plan, ctypes.byref(v)),
+           "ebin_block_norm_plan_workspace")
+    return v.value
+
+
+def ebin_block_norm_plan_release(plan) -> None:
+    lib.ebin_block_norm_plan_release(plan)
+
+
+def ebin_block_norm_execute(plan, x, y, params, h, z, stream) -> None:
+    """params: an ebin_block_norm_params, or None."""
+    st = lib.ebin_block_norm_execute(plan, x, y, params, h, z, stream)
+    if st:
+        raise EbinError(st, "ebin_block_norm_execute")
+
+
+def ebin_block_norm_grad_execute(plan, dz, dh, h, y, params, dx, dy, grads, workspace,
+                                 workspace_bytes, stream) -> None:
+    """params, grads: an ebin_block_norm_params and an ebin_block_norm_grads, or None."""
+    st = lib.ebin_block_norm_grad_execute(plan, dz, dh, h, y, params, dx, dy, grads, workspace,
+                                          workspace_bytes, stream)
+    if st:
+        raise EbinError(st, "ebin_block_norm_grad_execute")
 
 
 def ebin_launch_count() -> int:
@@ -738,12 +874,24 @@ def _output(out, plan, desc, device):
 # torch.cuda.stream(s) does: the inputs are ready in s's order, and what the call
 # allocates, its results among it, is s's memory.
 
+def _axes(sections, order, position_stride=0):
+    """The ABI's axes for the pairs of each axis."""
+    n = [int(v) for v in sections]
+    if not 1 <= len(n) <= 4:
+        raise ValueError("axes are 1 to 4 counts of pairs; got %s" % (tuple(n),))
+    return ebin_rotary_axes(len(n), AXES_ORDERS[order], (ctypes.c_int32 * 4)(*n),
+                            int(position_stride))
+
+
 def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
                  scaling: str = "none", factor: float = 1.0, trained_length: float = 0.0,
                  slow_turns: float = 1.0, fast_turns: float = 32.0, amplitude: float = 1.0,
-                 first_position: int = 0, device="cuda", stream=None):
+                 first_position: int = 0, axes=None, axes_order: str = "blocks", device="cuda",
+                 stream=None):
     """(cos, sin), float32 [positions, rotary_dim / 2], formed in binary64 on the
-    device.  scaling, for contexts longer than the trained one: "linear" divides
+    device.  ``axes``: the pairs of each axis, which then has frequencies of its own
+    (pair i of s: base^(-i/s)); None: one row of frequencies, which several axes may
+    share.  scaling, for contexts longer than the trained one: "linear" divides
     every frequency by factor, "base" stretches the base, "by_parts" divides
     what turns fewer than slow_turns times within trained_length, keeps what
     turns more than fast_turns times and blends between."""
@@ -754,7 +902,12 @@ def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
     with _launching(torch.device(device), stream):
         cos = torch.empty(int(positions), int(rotary_dim) // 2, device="cuda")
         sin = torch.empty_like(cos)
-        ebin_rotary_table(attrs, first_position, positions, _ptr(cos), _ptr(sin), _stream(stream))
+        if axes is None:
+            ebin_rotary_table(attrs, first_position, positions, _ptr(cos), _ptr(sin),
+                              _stream(stream))
+        else:
+            ebin_rotary_table_axes(attrs, _axes(axes, axes_order), first_position, positions,
+                                   _ptr(cos), _ptr(sin), _stream(stream))
     return cos, sin
 
 
@@ -781,13 +934,19 @@ class HeadsPlan:
     element strides ``position_strides``.  ``rotary_dim`` None rotates whole heads;
     a rotation needs ``table_positions``, the rows of its tables.  Run with
     execute_heads, or, for norm "rms" with gradient=True, execute_heads_grad.
+
+    ``axes``: the pairs of each axis (time, row, column) of a token of an image or a
+    video, rotary_dim / 2 together: each pair turns by its axis' position.  "blocks"
+    gives them out one axis after another, "dealt" pair by pair in turn.  Positions
+    are then [axes, batch, tokens], ``position_strides`` of three.
     """
 
     def __init__(self, dtype, q_shape, k_shape=None, *, norm: str = "none", epsilon: float = 1e-6,
                  weight_dtype=None, layout: str = "half", rotary_dim: int | None = None,
                  gradient: bool = False, positions=None, position_strides=None,
                  table_positions: int | None = None, q_strides=None, k_strides=None, dq_strides=None,
-                 dk_strides=None, q_out_strides=None, k_out_strides=None):
+                 dk_strides=None, q_out_strides=None, k_out_strides=None, axes=None,
+                 axes_order: str = "blocks"):
         q_shape = tuple(int(d) for d in q_shape)
         k_shape = (q_shape[0], q_shape[1], 0, q_shape[3]) if k_shape is None else \
             tuple(int(d) for d in k_shape)
@@ -809,8 +968,12 @@ class HeadsPlan:
             raise ValueError("HeadsPlan: a rotation of %d elements needs table_positions "
                              "(rotary_dim=0: no rotation)" % a.rotary_dim)
         a.position_type = 0 if positions is None else _dtype_code(positions)
-        ps = (q_shape[1], 1) if position_strides is None else position_strides
-        a.position_strides = (ctypes.c_int64 * 2)(int(ps[0]), int(ps[1]))
+        ps = (q_shape[0] * q_shape[1], q_shape[1], 1) if position_strides is None else \
+            tuple(position_strides)
+        if position_strides is not None and len(ps) != (2 if axes is None else 3):
+            raise ValueError("HeadsPlan: position_strides are %s" %
+                             ("(batch, token)" if axes is None else "(axis, batch, token)"))
+        a.position_strides = (ctypes.c_int64 * 2)(int(ps[-2]), int(ps[-1]))
         a.table_positions = int(table_positions or 0)
         for name, shape, st in (("q", q_shape, q_strides), ("k", k_shape, k_strides),
                                 ("dq", q_shape, dq_strides), ("dk", k_shape, dk_strides),
@@ -818,7 +981,8 @@ class HeadsPlan:
                                 ("k_out", k_shape, k_out_strides)):
             setattr(a, name, _heads_view(shape, st, name))
         self.q_shape, self.k_shape = q_shape, k_shape
-        self.handle = ebin_heads_plan_create(a)
+        self.handle = ebin_heads_plan_create(a) if axes is None else \
+            ebin_heads_plan_create_axes(a, _axes(axes, axes_order, ps[0]))
         self.workspace_bytes = ebin_heads_plan_workspace(self.handle)
 
     def close(self):
@@ -865,7 +1029,7 @@ def _same_device(where, first, *others):
             raise ValueError("%s: tensors are on %s and %s" % (where, first.device, t.device))
 
 
-def _heads_inputs(where, q, k, cos, sin, positions):
+def _heads_inputs(where, q, k, cos, sin, positions, axes=None, axes_order="blocks"):
     """The checks of the one-shot calls; returns the plan's keywords for the table and positions."""
     import torch
     _same_device(where, q, k, cos, sin, positions)
@@ -881,7 +1045,17 @@ def _heads_inputs(where, q, k, cos, sin, positions):
             if t.dtype != torch.float32 or not t.is_contiguous():
                 raise ValueError("%s: cos and sin are contiguous float32" % where)
         kw = {"rotary_dim": 2 * cos.shape[1], "table_positions": cos.shape[0]}
-    if positions is not None:
+    if axes is not None:
+        shape = (len(axes),) + tuple(q.shape[:2])
+        if positions is not None and positions.dim() == 2:
+            positions = positions[:, None].expand(-1, q.shape[0], -1)
+        if positions is None or tuple(positions.shape) != shape or \
+                positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("%s: positions are int32 or int64 [axes, tokens] or [axes, batch, "
+                             "tokens]" % where)
+        kw.update(positions=positions.dtype, position_strides=positions.stride(), axes=axes,
+                  axes_order=axes_order)
+    elif positions is not None:
         if positions.dim() == 1:
             positions = positions.expand(q.shape[0], -1)
         if tuple(positions.shape) != tuple(q.shape[:2]) or \
@@ -904,8 +1078,8 @@ def _heads_out(where, x, out):
     return out
 
 
-def _run_heads(where, q, k, cos, sin, positions, out, wq, wk, stream, **kw):
-    more, positions = _heads_inputs(where, q, k, cos, sin, positions)
+def _run_heads(where, q, k, cos, sin, positions, axes, axes_order, out, wq, wk, stream, **kw):
+    more, positions = _heads_inputs(where, q, k, cos, sin, positions, axes, axes_order)
     _same_device(where, q, wq, wk)
     qo, ko = (None, None) if out is None else out
     with _launching(q.device, stream):
@@ -918,12 +1092,14 @@ def _run_heads(where, q, k, cos, sin, positions, out, wq, wk, stream, **kw):
 
 
 def rotary(q, k, cos, sin, positions=None, *, layout: str = "half", gradient: bool = False,
-           out=None, stream=None):
+           axes=None, axes_order: str = "blocks", out=None, stream=None):
     """Rotary positions of q and k (either may be a strided view; k may be None):
     returns (q_out, k_out), new tensors or ``out``, which may be (q, k) itself.
-    ``gradient``: q and k are the incoming gradients, rotated back."""
-    return _run_heads("rotary", q, k, cos, sin, positions, out, None, None, stream,
-                      layout=layout, gradient=gradient)
+    ``gradient``: q and k are the incoming gradients, rotated back.  ``axes``: the pairs
+    of each axis, as in HeadsPlan; positions are then [axes, tokens] or [axes, batch,
+    tokens]."""
+    return _run_heads("rotary", q, k, cos, sin, positions, axes, axes_order, out, None, None,
+                      stream, layout=layout, gradient=gradient)
 
 
 def _norm_weights(where, q, wq, wk):
@@ -938,23 +1114,26 @@ def _norm_weights(where, q, wq, wk):
 
 
 def qk_norm_rotary(q, k, wq, wk, cos=None, sin=None, positions=None, *, epsilon: float = 1e-6,
-                   layout: str = "half", out=None, stream=None):
+                   layout: str = "half", axes=None, axes_order: str = "blocks", out=None,
+                   stream=None):
     """The RMS norm of each head of q and k, times its weight (None = 1), and
-    the rotation (cos None = norm only) in one pass; returns (q_out, k_out)."""
+    the rotation (cos None = norm only; ``axes`` as in rotary) in one pass; returns
+    (q_out, k_out)."""
     wd = _norm_weights("qk_norm_rotary", q, wq, wk)
-    return _run_heads("qk_norm_rotary", q, k, cos, sin, positions, out, wq, wk, stream,
-                      norm="rms", epsilon=epsilon, layout=layout, weight_dtype=wd)
+    return _run_heads("qk_norm_rotary", q, k, cos, sin, positions, axes, axes_order, out, wq, wk,
+                      stream, norm="rms", epsilon=epsilon, layout=layout, weight_dtype=wd)
 
 
 def qk_norm_rotary_grad(dq, dk, q, k, wq, wk, cos=None, sin=None, positions=None, *,
-                        epsilon: float = 1e-6, layout: str = "half", out=None, stream=None):
+                        epsilon: float = 1e-6, layout: str = "half", axes=None,
+                        axes_order: str = "blocks", out=None, stream=None):
     """The gradient of qk_norm_rotary: (dq, dk, dwq, dwk) for the incoming
     gradients dq, dk and the forward inputs q, k; dwq and dwk are float32
     (dk and dwk None without k)."""
     import torch
     where = "qk_norm_rotary_grad"
     wd = _norm_weights(where, q, wq, wk)
-    more, positions = _heads_inputs(where, q, k, cos, sin, positions)
+    more, positions = _heads_inputs(where, q, k, cos, sin, positions, axes, axes_order)
     _same_device(where, q, dq, dk, wq, wk)
     for g, x in ((dq, q), (dk, k)):
         if (g is None) != (x is None) or (g is not None and
@@ -1051,6 +1230,346 @@ def execute_epilogue_grad(plan: EpilogueGradPlan, dy, z, dz, dbias=None, workspa
                                         _bytes_of(workspace), _stream(stream))
     if st:
         raise EbinError(st, "ebin_epilogue_grad_execute")
+
+
+# ----------------------------------------------------------------- dropout
+#
+# ``seed`` and ``offset`` are whole numbers of 64 bits; calls that are to draw apart
+# take different offsets.  ``offset_device``: a device int64 or uint64 tensor of one
+# element that is added to offset when the kernel runs.
+
+_WORD = (1 << 64) - 1
+
+
+class DropoutPlan:
+    """A plan of y = residual + keep(x + bias) / (1 - p) on [rows, n], or, with
+    gradient=True, of dx = keep(dy) / (1 - p).  ``bias``: None, or the bias's type
+    (x's or float32); with gradient=True its presence asks for dbias.  Row
+    strides in elements (None = dense): ld_x is dy's and ld_y dx's in a gradient."""
+
+    def __init__(self, dtype, rows: int, n: int, p: float, *, bias=None, residual: bool = False,
+                 gradient: bool = False, ld_x=None, ld_residual=None, ld_y=None):
+        code = _dtype_code(dtype)
+        a = ebin_dropout_attrs(code, code if bias is None else _dtype_code(bias),
+                               int(bias is not None), int(bool(residual)), int(bool(gradient)),
+                               float(p), int(rows), int(n),
+                               *_row_strides("DropoutPlan", ld_x=ld_x, ld_residual=ld_residual,
+                                             ld_y=ld_y))
+        self.handle = ebin_dropout_plan_create(a)
+        self.workspace_bytes = ebin_dropout_plan_workspace(self.handle)
+
+    def close(self):
+        if self.handle:
+            ebin_dropout_plan_release(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def execute_dropout(plan: DropoutPlan, x, y, seed: int, offset: int = 0, *, bias=None,
+                    residual=None, offset_device=None, stream=None) -> None:
+    """Enqueue a dropout on device buffers laid out as the plan says (torch tensors or
+    int addresses)."""
+    st = lib.ebin_dropout_execute(plan.handle, *_ptrs(x, bias, residual, y), seed & _WORD,
+                                  offset & _WORD, _ptr(offset_device), _stream(stream))
+    if st:
+        raise EbinError(st, "ebin_dropout_execute")
+
+
+def execute_dropout_grad(plan: DropoutPlan, dy, dx, seed: int, offset: int = 0, *, dbias=None,
+                         workspace=None, offset_device=None, stream=None) -> None:
+    """Enqueue a dropout's gradient; ``workspace``: a uint8 device tensor of at least
+    plan.workspace_bytes (None where that is 0)."""
+    st = lib.ebin_dropout_grad_execute(plan.handle, *_ptrs(dy, dx, dbias, workspace),
+                                       _bytes_of(workspace), seed & _WORD, offset & _WORD,
+                                       _ptr(offset_device), _stream(stream))
+    if st:
+        raise EbinError(st, "ebin_dropout_grad_execute")
+
+
+def _offset_word(where, t):
+    """Checks a device offset."""
+    import torch
+    if t is not None and (t.numel() != 1 or t.dtype not in (torch.int64, torch.uint64)):
+        raise ValueError("%s: offset_device is one int64 or uint64" % where)
+
+
+def _vector(where, name, t, n):
+    """Checks a parameter [n]; returns its type."""
+    if t is None:
+        return None
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError("%s: %s is a contiguous [%d] tensor" % (where, name, n))
+    return t.dtype
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, *, bias=None, residual=None, out=None,
+            offset_device=None, stream=None):
+    """residual + keep(x + bias) / (1 - p) of a matrix x [rows, n] whose rows are dense, in
+    one call; ``out`` may be x or residual.  The same numbers draw the same mask."""
+    import torch
+    where = "dropout"
+    _same_device(where, x, bias, residual, out, offset_device)
+    _offset_word(where, offset_device)
+    if x.dim() != 2:
+        raise ValueError("dropout: x is a matrix")
+    rows, n = x.shape
+    kind = _vector(where, "the bias", bias, n)
+    ld = [None if t is None else _matrix(where, t, (rows, n), x.dtype, x.device)
+          for t in (x, residual, out)]
+    with _launching(x.device, stream):
+        if out is None:
+            out = torch.empty(rows, n, dtype=x.dtype, device=x.device)
+        plan = DropoutPlan(x.dtype, rows, n, p, bias=kind, residual=residual is not None,
+                           ld_x=ld[0], ld_residual=ld[1], ld_y=ld[2])
+        execute_dropout(plan, x, out, seed, offset, bias=bias, residual=residual,
+                        offset_device=offset_device, stream=stream)
+    return out
+
+
+def dropout_grad(dy, p: float, seed: int, offset: int = 0, *, bias: bool = False, out=None,
+                 offset_device=None, stream=None):
+    """(dx, dbias) of a dropout drawn from the same numbers, for the incoming gradient dy
+    [rows, n] (the residual's gradient is dy); dbias is float32 (None with bias=False).
+    ``out`` may be dy."""
+    import torch
+    where = "dropout_grad"
+    _same_device(where, dy, out, offset_device)
+    _offset_word(where, offset_device)
+    if dy.dim() != 2:
+        raise ValueError("dropout_grad: dy is a matrix")
+    rows, n = dy.shape
+    ld = [None if t is None else _matrix(where, t, (rows, n), dy.dtype, dy.device)
+          for t in (dy, out)]
+    with _launching(dy.device, stream):
+        if out is None:
+            out = torch.empty(rows, n, dtype=dy.dtype, device=dy.device)
+        plan = DropoutPlan(dy.dtype, rows, n, p, bias=dy.dtype if bias else None, gradient=True,
+                           ld_x=ld[0], ld_y=ld[1])
+        dbias = torch.empty(n, device=dy.device) if bias else None
+        work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dy.device)
+        execute_dropout_grad(plan, dy, out, seed, offset, dbias=dbias, workspace=work,
+                             offset_device=offset_device, stream=stream)
+    return out, dbias
+
+
+# ----------------------------------------------------------------- norms around a block
+
+class BlockNormPlan:
+    """A plan of the norms around a block on [rows, n]:
+
+        v = N_post(y) w_post + b_post
+        h = stream_scale x + branch_scale gate keep(v) / (1 - dropout)
+        z = (N_pre(h) w_pre + b_pre) (1 + scale) + shift
+
+    or, with gradient=True, of its gradient.  ``post``, ``pre``: "none" (pre: there
+    is no z), "rms" or "layer".  ``branch=False``: there is no y.  Types: y's and z's,
+    ``stream_dtype`` of x and h, ``weight_dtype`` of the norms' weights and biases,
+    ``mod_dtype`` of gate, scale and shift: dtype (None) or float32.
+    ``gate_rows`` None: gate is one row [n]; else one for each gate_rows rows;
+    ``mod_rows`` the same of scale and shift.  Row strides in elements (None = dense)."""
+
+    def __init__(self, dtype, rows: int, n: int, *, stream_dtype=None, weight_dtype=None,
+                 mod_dtype=None, post: str = "none", pre: str = "rms", branch: bool = True,
+                 epsilon: float = 1e-6, epsilon_post: float | None = None, dropout: float = 0.0,
+                 stream_scale: float = 1.0, branch_scale: float = 1.0, gate_rows=None,
+                 mod_rows=None, gradient: bool = False, ld_x=None, ld_y=None, ld_h=None,
+                 ld_z=None, ld_gate=None, ld_scale=None, ld_shift=None, ld_dz=None, ld_dh=None,
+                 ld_dx=None, ld_dy=None):
+        code = _dtype_code(dtype)
+        kinds = [code if t is None else _dtype_code(t)
+                 for t in (stream_dtype, weight_dtype, mod_dtype)]
+        for name, per in (("gate_rows", gate_rows), ("mod_rows", mod_rows)):
+            if per is not None and int(per) < 1:
+                raise ValueError("BlockNormPlan: %s is %s; None means one row for all"
+                                 % (name, per))
+        a = ebin_block_norm_attrs(
+            code, *kinds, NORMS[post], NORMS[pre], int(bool(branch)), int(bool(gradient)),
+            float(epsilon if epsilon_post is None else epsilon_post), float(epsilon),
+            float(stream_scale), float(branch_scale), float(dropout), int(rows), int(n),
+            int(gate_rows or 0), int(mod_rows or 0),
+            *_row_strides("BlockNormPlan", ld_x=ld_x, ld_y=ld_y, ld_h=ld_h, ld_z=ld_z,
+                          ld_gate=ld_gate, ld_scale=ld_scale, ld_shift=ld_shift, ld_dz=ld_dz,
+                          ld_dh=ld_dh, ld_dx=ld_dx, ld_dy=ld_dy))
+        self.handle = ebin_block_norm_plan_create(a)
+        self.workspace_bytes = ebin_block_norm_plan_workspace(self.handle)
+
+    def close(self):
+        if self.handle:
+            ebin_block_norm_plan_release(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def execute_block_norm(plan: BlockNormPlan, x, y, h, z, *, gate=None, w_post=None, b_post=None,
+                       w_pre=None, b_pre=None, scale=None, shift=None, seed: int = 0,
+                       offset: int = 0, offset_device=None, stream=None) -> None:
+    """Enqueue the forward pass on device buffers laid out as the plan says (torch
+    tensors or int addresses); h or z None: not wanted."""
+    params = ebin_block_norm_params(*_ptrs(gate, w_post, b_post, w_pre, b_pre, scale, shift),
+                                    seed & _WORD, offset & _WORD, _ptr(offset_device))
+    st = lib.ebin_block_norm_execute(plan.handle, *_ptrs(x, y), params, *_ptrs(h, z),
+                                     _stream(stream))
+    if st:
+        raise EbinError(st, "ebin_block_norm_execute")
+
+
+def execute_block_norm_grad(plan: BlockNormPlan, dz, dh, h, y, dx, dy, *, gate=None, w_post=None,
+                            b_post=None, w_pre=None, b_pre=None, scale=None, dgate=None,
+                            dw_post=None, db_post=None, dw_pre=None, db_pre=None, dscale=None,
+                            dshift=None, workspace=None, seed: int = 0, offset: int = 0,
+                            offset_device=None, stream=None) -> None:
+    """Enqueue the gradient; outputs that are None are not wanted.  ``workspace``: a uint8
+    device tensor of at least plan.workspace_bytes (None where no gradient of a parameter
+    is wanted)."""
+    params = ebin_block_norm_params(*_ptrs(gate, w_post, b_post, w_pre, b_pre, scale, None),
+                                    seed & _WORD, offset & _WORD, _ptr(offset_device))
+    grads = ebin_block_norm_grads(*_ptrs(dgate, dw_post, db_post, dw_pre, db_pre, dscale, dshift))
+    st = lib.ebin_block_norm_grad_execute(plan.handle, *_ptrs(dz, dh, h, y), params,
+                                          *_ptrs(dx, dy), grads, _ptr(workspace),
+                                          _bytes_of(workspace), _stream(stream))
+    if st:
+        raise EbinError(st, "ebin_block_norm_grad_execute")
+
+
+def _block_checks(where, stream_of, branch_of, dtype, gate, w_post, b_post, w_pre, b_pre, scale,
+                  shift, post, pre):
+    """The checks that both one-call forms share: (rows, n, the plan's keywords).
+    stream_of, branch_of: (name, tensor) pairs on the stream's and the branch's type."""
+    tensors = [t for _, t in stream_of + branch_of if t is not None]
+    first = tensors[0]
+    _same_device(where, first, *tensors[1:], gate, w_post, b_post, w_pre, b_pre, scale, shift)
+    if first.dim() != 2:
+        raise ValueError("%s: the rows are matrices [rows, n]" % where)
+    rows, n = first.shape
+    kw = {"post": post, "pre": pre}
+    stream_dtype = next((t.dtype for _, t in stream_of if t is not None), dtype)
+    kw["stream_dtype"] = stream_dtype
+    for pairs, kind in ((stream_of, stream_dtype), (branch_of, dtype)):
+        for name, t in pairs:
+            if t is not None:
+                kw["ld_" + name] = _matrix(where, t, (rows, n), kind, first.device)
+    kinds = {_vector(where, name, t, n) for name, t in
+             (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre))
+             if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("%s: the norms' weights and biases have one type" % where)
+    kw["weight_dtype"] = kinds.pop() if kinds else None
+    kinds = {t.dtype for t in (gate, scale, shift) if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("%s: gate, scale and shift have one type" % where)
+    kw["mod_dtype"] = kinds.pop() if kinds else None
+    for name, per, t in (("gate", "gate_rows", gate), ("scale", "mod_rows", scale),
+                         ("shift", "mod_rows", shift)):
+        if t is None:
+            continue
+        if t.dim() == 1:
+            _vector(where, name, t, n)
+            groups = None
+        else:
+            step = _matrix(where, t, None, t.dtype, first.device)
+            if t.shape[1] != n or t.shape[0] < 1 or rows % t.shape[0]:
+                raise ValueError("%s: %s is [n] or [groups, n], the groups dividing the rows; got "
+                                 "%s beside [%d, %d]" % (where, name, tuple(t.shape), rows, n))
+            groups = max(1, rows // t.shape[0])
+            kw["ld_" + name] = step
+        if per in kw and kw[per] != groups:
+            raise ValueError("%s: scale and shift have the same groups" % where)
+        kw[per] = groups
+    return rows, n, kw
+
+
+def block_norm(x, y=None, *, gate=None, w_post=None, b_post=None, w_pre=None, b_pre=None,
+               scale=None, shift=None, post: str = "none", pre: str = "rms",
+               epsilon: float = 1e-6, epsilon_post: float | None = None, dropout: float = 0.0,
+               seed: int = 0, offset: int = 0, offset_device=None, stream_scale: float = 1.0,
+               branch_scale: float = 1.0, dtype=None, out=None, stream=None):
+    """(h, z) of BlockNormPlan's formulas in one call: x [rows, n] the residual stream, y
+    [rows, n] a block's output (None: none), gate, scale and shift [n] or [groups, n];
+    z is None with pre="none" and h without y.  ``dtype``: z's, where there is no y to
+    give it (None: x's).  ``out``: (h, z), either of which may be an input of its type or
+    None (a new tensor)."""
+    import torch
+    where = "block_norm"
+    h, z = (None, None) if out is None else out
+    if dtype is None:
+        dtype = x.dtype if y is None else y.dtype
+    rows, n, kw = _block_checks(where, [("x", x), ("h", h)], [("y", y), ("z", z)], dtype, gate,
+                                w_post, b_post, w_pre, b_pre, scale, shift, post, pre)
+    _same_device(where, x, offset_device)
+    _offset_word(where, offset_device)
+    with _launching(x.device, stream):
+        if h is None and y is not None:
+            h = torch.empty(rows, n, dtype=x.dtype, device=x.device)
+        if z is None and pre != "none":
+            z = torch.empty(rows, n, dtype=dtype, device=x.device)
+        plan = BlockNormPlan(dtype, rows, n, branch=y is not None, epsilon=epsilon,
+                             epsilon_post=epsilon_post, dropout=dropout,
+                             stream_scale=stream_scale, branch_scale=branch_scale, **kw)
+        execute_block_norm(plan, x, y, h, z, gate=gate, w_post=w_post, b_post=b_post,
+                           w_pre=w_pre, b_pre=b_pre, scale=scale, shift=shift, seed=seed,
+                           offset=offset, offset_device=offset_device, stream=stream)
+    return h, z
+
+
+def block_norm_grad(dz, dh, h, y=None, *, gate=None, w_post=None, b_post=None, w_pre=None,
+                    b_pre=None, scale=None, shift=None, post: str = "none", pre: str = "rms",
+                    epsilon: float = 1e-6, epsilon_post: float | None = None,
+                    dropout: float = 0.0, seed: int = 0, offset: int = 0, offset_device=None,
+                    stream_scale: float = 1.0, branch_scale: float = 1.0, out=None, stream=None):
+    """The gradient of block_norm with the same arguments, for the incoming gradients dz
+    (None with pre="none") and dh (None: 0) of z and h, the h that it gave (x without y;
+    None with pre="none") and y.  Returns a dict: "x", "y" (None without y) and, float32,
+    one entry for each parameter given: "gate", "w_post", "b_post", "w_pre", "b_pre", "scale",
+    "shift".  ``out``: (dx, dy), either of which may be an input of its type or None."""
+    import torch
+    where = "block_norm_grad"
+    dx, dy = (None, None) if out is None else out
+    if pre != "none" and (dz is None or h is None):
+        raise ValueError("%s: pre=%r needs dz and h" % (where, pre))
+    if pre == "none" and dh is None:
+        raise ValueError("%s: pre='none' needs dh" % where)
+    if post != "none" and y is None:
+        raise ValueError("%s: post=%r needs y" % (where, post))
+    dtype = next(t.dtype for t in (dz, y, dh) if t is not None)
+    rows, n, kw = _block_checks(where, [("dh", dh), ("h", h), ("dx", dx)],
+                                [("dz", dz), ("y", y), ("dy", dy)], dtype, gate, w_post, b_post,
+                                w_pre, b_pre, scale, shift, post, pre)
+    like = dz if dz is not None else dh
+    _same_device(where, like, offset_device)
+    _offset_word(where, offset_device)
+    with _launching(like.device, stream):
+        if dx is None:
+            dx = torch.empty(rows, n, dtype=kw["stream_dtype"], device=like.device)
+        if dy is None and y is not None:
+            dy = torch.empty(rows, n, dtype=dtype, device=like.device)
+        # groups of no rows are no groups to the plan
+        new = torch.empty if rows else torch.zeros
+        grads = {name: None if t is None else new(t.shape, dtype=torch.float32,
+                                                  device=like.device)
+                 for name, t in (("gate", gate), ("w_post", w_post), ("b_post", b_post),
+                                 ("w_pre", w_pre), ("b_pre", b_pre), ("scale", scale),
+                                 ("shift", shift))}
+        plan = BlockNormPlan(dtype, rows, n, branch=y is not None, epsilon=epsilon,
+                             epsilon_post=epsilon_post, dropout=dropout,
+                             stream_scale=stream_scale, branch_scale=branch_scale, gradient=True,
+                             **kw)
+        work = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=like.device)
+        execute_block_norm_grad(plan, dz, dh, h, y, dx, dy, gate=gate, w_post=w_post,
+                                b_post=b_post, w_pre=w_pre, b_pre=b_pre, scale=scale,
+                                **{"d" + k: v for k, v in grads.items()}, workspace=work,
+                                seed=seed, offset=offset, offset_device=offset_device,
+                                stream=stream)
+    return {"x": dx, "y": dy, **{k: v for k, v in grads.items() if v is not None}}
 
 
 def _matrix(where, t, shape, dtype, device):

@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libebin.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 GROUPS = ["arith", "mod", "pow", "cmp", "logic", "chan", "ext", "tern", "powmix"]
-LAYER = ["layer", "heads", "epilogue_grad", "gemm"]        # one translation unit each: ebin_<name>.cu
+# one translation unit each: ebin_<name>.cu
+LAYER = ["layer", "heads", "epilogue_grad", "gemm", "dropout", "block_norm"]
 N_DT = 13
 # -fmad=false: no multiply-add contraction anywhere; the kernels also use the
 # _rn intrinsics explicitly.  No fast-math.

@@ -1,0 +1,489 @@
+// Plans of the norms around a block and their execution: attribute checks, the
+// alias rule, kernel choice and launch, and the last step of the parameters'
+// gradients.
+#include <new>
+
+#include "ebin_block.cuh"
+
+namespace ebin {
+
+constexpr int kSumLanes = 32, kSumRows = 32;
+
+// A parameter in the launch's element type.
+__device__ __forceinline__ float sums_at(const BlockSumsArgs &a, const void *p, int64_t j, int f32,
+                                         float none) {
+    if (a.dtype == EBIN_FLOAT16) return block_param<__half>(p, j, f32, none);
+    if (a.dtype == EBIN_BFLOAT16) return block_param<__nv_bfloat16>(p, j, f32, none);
+    return block_param<float>(p, j, 1, none);
+}
+
+// The sum over `count` rows of partial, [.][4][n] from `first` on, of sum k and
+// column j, in an order fixed by the count; thread row 0 gets it.
+__device__ __forceinline__ float sums_column(const float *first, int64_t count, int64_t stride,
+                                             bool live, float (*s)[kSumLanes + 1]) {
+    float v = 0.0f;
+    if (live) {
+#pragma unroll 8
+        for (int64_t c = threadIdx.y; c < count; c += kSumRows) v += first[c * stride];
+    }
+    __syncthreads();   // the last column's have been read
+    s[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    float t = 0.0f;
+    if (threadIdx.y == 0)
+#pragma unroll
+        for (int r = 0; r < kSumRows; ++r) t += s[r][threadIdx.x];
+    return t;
+}
+
+// The parameters' gradients that all rows share, from the sums of all groups.  w:
+// whether the sums carry the groups' gate and scale already.
+__device__ __forceinline__ void sums_shared(const BlockSumsArgs &a, int64_t j, const float *t,
+                                            bool weighed) {
+    const float scale = weighed && a.mod_grouped ? 1.0f
+        : 1.0f + sums_at(a, a.scale, j, a.mod_f32, 0.0f);
+    const float gate = weighed && a.gate_grouped ? 1.0f : sums_at(a, a.gate, j, a.mod_f32, 1.0f);
+    if (a.dw_pre) a.dw_pre[j] = scale * t[SUM_DZ_HH];
+    if (a.db_pre) a.db_pre[j] = scale * t[SUM_DZ];
+    if (a.dw_post) a.dw_post[j] = gate * t[SUM_E_YH];
+    if (a.db_post) a.db_post[j] = gate * t[SUM_E];
+    if (!a.mod_grouped) {
+        if (a.dscale)
+            a.dscale[j] = fmaf(t[SUM_DZ_HH], sums_at(a, a.w_pre, j, a.w_f32, 1.0f),
+                               t[SUM_DZ] * sums_at(a, a.b_pre, j, a.w_f32, 0.0f));
+        if (a.dshift) a.dshift[j] = t[SUM_DZ];
+    }
+    if (!a.gate_grouped && a.dgate)
+        a.dgate[j] = fmaf(t[SUM_E_YH], sums_at(a, a.w_post, j, a.w_f32, 1.0f),
+                          t[SUM_E] * sums_at(a, a.b_post, j, a.w_f32, 0.0f));
+}
+
+// One CTA per group and 32 columns: the group's parts joined; its gradients of gate, scale
+// and shift; then, with one group, everything, else its share of what all rows
+// have in common, into its first part's place.
+__global__ void __launch_bounds__(kSumLanes *kSumRows) k_block_sums(const BlockSumsArgs a) {
+    __shared__ float s[kSumRows][kSumLanes + 1];
+    const int64_t group = blockIdx.x / a.tiles;
+    const int64_t j = (blockIdx.x - group * a.tiles) * kSumLanes + threadIdx.x;
+    const bool live = j < a.n;
+    layer_pdl_launch();
+    layer_pdl_wait();
+    float *const at = a.partial + group * a.parts * 4 * a.n + j;
+    float t[4];
+    for (int k = 0; k < 4; ++k)
+        t[k] = a.need >> k & 1 ? sums_column(at + k * a.n, a.parts, 4 * a.n, live, s) : 0.0f;
+    if (threadIdx.y != 0 || !live) return;
+    if (a.groups == 1) {
+        sums_shared(a, j, t, false);
+        if (!a.mod_grouped && !a.gate_grouped) return;
+    }
+    if (a.mod_grouped) {
+        if (a.dscale)
+            a.dscale[group * a.n + j] =
+                fmaf(t[SUM_DZ_HH], sums_at(a, a.w_pre, j, a.w_f32, 1.0f),
+                     t[SUM_DZ] * sums_at(a, a.b_pre, j, a.w_f32, 0.0f));
+        if (a.dshift) a.dshift[group * a.n + j] = t[SUM_DZ];
+    }
+    if (a.gate_grouped && a.dgate)
+        a.dgate[group * a.n + j] =
+            fmaf(t[SUM_E_YH], sums_at(a, a.w_post, j, a.w_f32, 1.0f),
+                 t[SUM_E] * sums_at(a, a.b_post, j, a.w_f32, 0.0f));
+    if (!a.second) return;
+    const float scale = a.mod_grouped
+        ? 1.0f + sums_at(a, a.scale, group * a.ld_scale + j, a.mod_f32, 0.0f) : 1.0f;
+    const float gate = a.gate_grouped
+        ? sums_at(a, a.gate, group * a.ld_gate + j, a.mod_f32, 1.0f) : 1.0f;
+    at[SUM_DZ_HH * a.n] = scale * t[SUM_DZ_HH];
+    at[SUM_DZ * a.n] = scale * t[SUM_DZ];
+    at[SUM_E_YH * a.n] = gate * t[SUM_E_YH];
+    at[SUM_E * a.n] = gate * t[SUM_E];
+}
+
+// The groups' shares joined.
+__global__ void __launch_bounds__(kSumLanes *kSumRows) k_block_sums_all(const BlockSumsArgs a) {
+    __shared__ float s[kSumRows][kSumLanes + 1];
+    const int64_t j = (int64_t)blockIdx.x * kSumLanes + threadIdx.x;
+    layer_pdl_launch();
+    layer_pdl_wait();
+    float t[4];
+    for (int k = 0; k < 4; ++k)
+        t[k] = a.need >> k & 1 ? sums_column(a.partial + k * a.n + j, a.groups,
+                                             4 * a.n * a.parts, j < a.n, s) : 0.0f;
+    if (threadIdx.y == 0 && j < a.n) sums_shared(a, j, t, true);
+}
+
+}  // namespace ebin
+
+struct ebin_block_norm_plan_s {
+    ebin_block_norm_attrs at;      // its strides filled in
+    int64_t isz, ssz, wsz, msz;    // bytes of an element of the four types
+    uint32_t least;
+    int64_t groups = 1, group_rows = 0;
+    int64_t parts = 1, unit_rows = 0;
+    size_t workspace = 0;
+};
+
+using namespace ebin;
+
+namespace {
+
+// A matrix or a vector in memory, as bytes.
+struct Range {
+    const void *p;
+    int64_t bytes;
+    int64_t ld;      // bytes between rows; 0: not a matrix that an output may be
+    int64_t size;    // of an element
+};
+
+int64_t rows_bytes(int64_t rows, int64_t n, int64_t ld, int64_t size) {
+    return rows > 0 && n > 0 ? ((rows - 1) * ld + n) * size : 0;
+}
+
+// Whether output y may lie where it lies beside input x.
+bool apart(const Range &x, const Range &y, int64_t rows) {
+    if (!x.p || !y.p || !ranges_overlap(x.p, x.bytes, y.p, y.bytes)) return true;
+    return x.p == y.p && x.size == y.size && x.ld > 0 && y.ld > 0 && (rows <= 1 || x.ld == y.ld);
+}
+
+bool block_float(ebin_dtype t) {
+    return t == EBIN_FLOAT32 || t == EBIN_FLOAT16 || t == EBIN_BFLOAT16;
+}
+
+// The arguments that both directions share, once they have been checked.
+ebin_status prepare_block(const ebin_block_norm_plan_s &p, const ebin_block_norm_params &w,
+                          BlockArgs &a) {
+    const ebin_block_norm_attrs &at = p.at;
+    if ((w.gate && !at.has_branch) ||
+        ((uintptr_t)w.gate | (uintptr_t)w.scale | (uintptr_t)w.shift) % (uintptr_t)p.msz ||
+        ((uintptr_t)w.w_post | (uintptr_t)w.b_post | (uintptr_t)w.w_pre | (uintptr_t)w.b_pre) %
+            (uintptr_t)p.wsz || (uintptr_t)w.offset_device % 8)
+        return EBIN_ERR_INVALID_ARG;
+    const bool post = at.post != EBIN_NORM_NONE, pre = at.pre != EBIN_NORM_NONE;
+    a = BlockArgs{};
+    a.gate = w.gate;
+    a.w_post = post ? w.w_post : nullptr;
+    a.b_post = post ? w.b_post : nullptr;
+    a.w_pre = pre ? w.w_pre : nullptr;
+    a.b_pre = pre ? w.b_pre : nullptr;
+    a.scale = pre ? w.scale : nullptr;
+    a.shift = pre ? w.shift : nullptr;
+    a.ld_gate = at.ld_gate;
+    a.ld_scale = at.ld_scale;
+    a.ld_shift = at.ld_shift;
+    a.gate_rows = at.gate_rows ? at.gate_rows : at.rows;
+    a.mod_rows = at.mod_rows ? at.mod_rows : at.rows;
+    a.rows = at.rows;
+    a.n = at.n;
+    a.stream_scale = at.stream_scale;
+    a.branch_scale = at.branch_scale;
+    a.eps_post = at.epsilon_post;
+    a.eps_pre = at.epsilon_pre;
+    a.post = at.post;
+    a.pre = at.pre;
+    a.w_f32 = at.dtype_w == EBIN_FLOAT32;
+    a.mod_f32 = at.dtype_mod == EBIN_FLOAT32;
+    a.drop = drop_args(p.least, w.seed, w.offset, w.offset_device);
+    a.parts = p.parts;
+    a.unit_rows = p.unit_rows;
+    a.group_rows = p.group_rows;
+    return EBIN_OK;
+}
+
+// The small inputs that a call reads, as ranges.
+int param_ranges(const ebin_block_norm_plan_s &p, const BlockArgs &a, Range *r) {
+    const ebin_block_norm_attrs &at = p.at;
+    const int64_t w = at.n * p.wsz;
+    auto mod = [&](int64_t per, int64_t ld) {
+        return rows_bytes(per ? at.rows / per : 1, at.n, ld, p.msz);
+    };
+    int c = 0;
+    for (const void *q : {a.w_post, a.b_post, a.w_pre, a.b_pre})
+        if (q) r[c++] = Range{q, w, 0, 0};
+    if (a.gate) r[c++] = Range{a.gate, mod(at.gate_rows, at.ld_gate), 0, 0};
+    if (a.scale) r[c++] = Range{a.scale, mod(at.mod_rows, at.ld_scale), 0, 0};
+    if (a.shift) r[c++] = Range{a.shift, mod(at.mod_rows, at.ld_shift), 0, 0};
+    if (p.least && a.drop.offset_device) r[c++] = Range{a.drop.offset_device, 8, 0, 0};
+    return c;
+}
+
+cudaError_t launch_sums(void (*kernel)(const BlockSumsArgs), int64_t grid, const BlockSumsArgs &a,
+                        cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kSumLanes, kSumRows);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <class T, class S>
+cudaError_t launch_block_types(const BlockArgs &a, bool grad, int64_t units, cudaStream_t s) {
+    if (grad)
+        return launch_layer(k_block_any_grad<T, S>, dim3((unsigned)units), kBlockAnyThreads, 0, s,
+                            1, a);
+    const int64_t grid = std::min<int64_t>(a.rows, 32ll * current_sm_count());
+    return launch_layer(k_block_any<T, S>, dim3((unsigned)grid), kBlockAnyThreads, 0, s, 1, a);
+}
+
+cudaError_t launch_block(const ebin_block_norm_plan_s &p, const BlockArgs &a, bool grad,
+                         cudaStream_t s) {
+    const int64_t units = p.groups * p.parts;
+    const bool wide = p.at.dtype_stream == EBIN_FLOAT32;
+    if (p.at.dtype == EBIN_FLOAT32) return launch_block_types<float, float>(a, grad, units, s);
+    if (p.at.dtype == EBIN_FLOAT16)
+        return wide ? launch_block_types<__half, float>(a, grad, units, s)
+                    : launch_block_types<__half, __half>(a, grad, units, s);
+    return wide ? launch_block_types<__nv_bfloat16, float>(a, grad, units, s)
+                : launch_block_types<__nv_bfloat16, __nv_bfloat16>(a, grad, units, s);
+}
+
+// Parts of a group's rows: about two units to each of 152 SMs over all groups, each
+// with a row at least, and no more than 2^28 sums in the workspace where that leaves one.
+int64_t block_parts(int64_t groups, int64_t group_rows, int64_t n) {
+    const int64_t want = div_up(2 * 152, groups);
+    const int64_t room = (int64_t(1) << 26) / (groups * std::max<int64_t>(n, 1));
+    return std::max<int64_t>(1, std::min<int64_t>({want, group_rows, room}));
+}
+
+}  // namespace
+
+extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *attrs,
+                                                   ebin_block_norm_plan_t *out) {
+    if (!attrs || !out) return EBIN_ERR_INVALID_ARG;
+    *out = nullptr;
+    const ebin_block_norm_attrs &a = *attrs;
+    if (!block_float(a.dtype) || (a.dtype_stream != a.dtype && a.dtype_stream != EBIN_FLOAT32) ||
+        (a.dtype_w != a.dtype && a.dtype_w != EBIN_FLOAT32) ||
+        (a.dtype_mod != a.dtype && a.dtype_mod != EBIN_FLOAT32))
+        return EBIN_ERR_UNSUPPORTED_TYPE;
+    uint32_t least;
+    if (a.post < EBIN_NORM_NONE || a.post > EBIN_NORM_LAYER || a.pre < EBIN_NORM_NONE ||
+        a.pre > EBIN_NORM_LAYER || (a.has_branch != 0 && a.has_branch != 1) ||
+        (a.gradient != 0 && a.gradient != 1) || !(a.epsilon_post >= 0.0f) ||
+        !std::isfinite(a.epsilon_post) || !(a.epsilon_pre >= 0.0f) ||
+        !std::isfinite(a.epsilon_pre) || !std::isfinite(a.stream_scale) ||
+        !std::isfinite(a.branch_scale) || !drop_bound(a.p, &least) ||
+        (!a.has_branch && (a.post != EBIN_NORM_NONE || least != 0)))
+        return EBIN_ERR_INVALID_ATTR;
+    if (a.rows < 0 || a.n < 0 || a.rows > int64_t(1) << 30 || a.n > int64_t(1) << 24 ||
+        a.gate_rows < 0 || a.mod_rows < 0 || (a.gate_rows && a.rows % a.gate_rows) ||
+        (a.mod_rows && a.rows % a.mod_rows) ||
+        (a.gate_rows && a.mod_rows && a.gate_rows != a.mod_rows))
+        return EBIN_ERR_INVALID_ARG;
+    auto *p = new (std::nothrow) ebin_block_norm_plan_s;
+    if (!p) return EBIN_ERR_INVALID_ARG;
+    p->at = a;
+    ebin_block_norm_attrs &at = p->at;
+    for (int64_t *ld : {&at.ld_x, &at.ld_y, &at.ld_h, &at.ld_z, &at.ld_gate, &at.ld_scale,
+                        &at.ld_shift, &at.ld_dz, &at.ld_dh, &at.ld_dx, &at.ld_dy}) {
+        int64_t span;
+        if (*ld == 0) *ld = a.n;
+        if (*ld < a.n || !product_fits(std::max<int64_t>(a.rows, 1), *ld, &span)) {
+            delete p;
+            return EBIN_ERR_INVALID_ARG;
+        }
+    }
+    p->isz = (int64_t)ebin_dtype_size(a.dtype);
+    p->ssz = (int64_t)ebin_dtype_size(a.dtype_stream);
+    p->wsz = (int64_t)ebin_dtype_size(a.dtype_w);
+    p->msz = (int64_t)ebin_dtype_size(a.dtype_mod);
+    p->least = least;
+    const int64_t per = std::max(a.gate_rows, a.mod_rows);
+    if (a.rows > 0) {
+        p->group_rows = per ? per : a.rows;
+        p->groups = a.rows / p->group_rows;
+        if (a.gradient) {
+            p->parts = block_parts(p->groups, p->group_rows, a.n);
+            p->unit_rows = div_up(p->group_rows, p->parts);
+            p->parts = div_up(p->group_rows, p->unit_rows);
+            if (p->groups * div_up(a.n, kSumLanes) > 0x7FFFFFFF) {   // CTAs of the last step
+                delete p;
+                return EBIN_ERR_INVALID_ARG;
+            }
+            p->workspace = sizeof(float) * 4 * (size_t)(p->groups * p->parts * a.n);
+        }
+    }
+    *out = p;
+    return EBIN_OK;
+}
+
+extern "C" ebin_status ebin_block_norm_plan_workspace(ebin_block_norm_plan_t plan, size_t *bytes) {
+    if (!plan || !bytes) return EBIN_ERR_INVALID_ARG;
+    *bytes = plan->workspace;
+    return EBIN_OK;
+}
+
+extern "C" void ebin_block_norm_plan_release(ebin_block_norm_plan_t plan) { delete plan; }
+
+extern "C" ebin_status ebin_block_norm_execute(ebin_block_norm_plan_t plan, const void *x,
+                                               const void *y,
+                                               const ebin_block_norm_params *params, void *h,
+                                               void *z, void *stream) {
+    if (!plan || plan->at.gradient) return EBIN_ERR_INVALID_ARG;
+    const ebin_block_norm_plan_s &p = *plan;
+    const ebin_block_norm_attrs &at = p.at;
+    if (at.rows == 0 || at.n == 0) return EBIN_OK;
+    if (at.pre == EBIN_NORM_NONE) z = nullptr;
+    if (!at.has_branch) y = nullptr;
+    else if (!y) return EBIN_ERR_INVALID_ARG;
+    if (!x || ((uintptr_t)x | (uintptr_t)h) % (uintptr_t)p.ssz ||
+        ((uintptr_t)y | (uintptr_t)z) % (uintptr_t)p.isz)
+        return EBIN_ERR_INVALID_ARG;
+    BlockArgs a;
+    const ebin_status st = prepare_block(p, params ? *params : ebin_block_norm_params{}, a);
+    if (st != EBIN_OK) return st;
+    Range in[10];
+    int c = param_ranges(p, a, in);
+    in[c++] = Range{x, rows_bytes(at.rows, at.n, at.ld_x, p.ssz), at.ld_x * p.ssz, p.ssz};
+    in[c++] = Range{y, rows_bytes(at.rows, at.n, at.ld_y, p.isz), at.ld_y * p.isz, p.isz};
+    const Range out[2] = {
+        {h, rows_bytes(at.rows, at.n, at.ld_h, p.ssz), at.ld_h * p.ssz, p.ssz},
+        {z, rows_bytes(at.rows, at.n, at.ld_z, p.isz), at.ld_z * p.isz, p.isz}};
+    for (const Range &o : out)
+        for (int i = 0; i < c; ++i)
+            if (!apart(in[i], o, at.rows)) return EBIN_ERR_ALIAS;
+    if (h && z && ranges_overlap(h, out[0].bytes, z, out[1].bytes)) return EBIN_ERR_ALIAS;
+    if (!h && !z) return EBIN_OK;
+    a.x = x;
+    a.y = y;
+    a.h = h;
+    a.z = z;
+    a.ld_x = at.ld_x;
+    a.ld_y = at.ld_y;
+    a.ld_h = at.ld_h;
+    a.ld_z = at.ld_z;
+    if (!z) a.pre = EBIN_NORM_NONE;   // its sums are not wanted
+    return launch_block(p, a, false, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? EBIN_OK : EBIN_ERR_CUDA;
+}
+
+extern "C" ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan, const void *dz,
+                                                    const void *dh, const void *h, const void *y,
+                                                    const ebin_block_norm_params *params, void *dx,
+                                                    void *dy, const ebin_block_norm_grads *grads,
+                                                    void *workspace, size_t workspace_bytes,
+                                                    void *stream) {
+    if (!plan || !plan->at.gradient) return EBIN_ERR_INVALID_ARG;
+    const ebin_block_norm_plan_s &p = *plan;
+    const ebin_block_norm_attrs &at = p.at;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (at.n == 0) return EBIN_OK;
+    const ebin_block_norm_grads g = grads ? *grads : ebin_block_norm_grads{};
+    const ebin_block_norm_params w = params ? *params : ebin_block_norm_params{};
+    const bool post = at.post != EBIN_NORM_NONE, pre = at.pre != EBIN_NORM_NONE;
+    // a gradient of what does not enter the formula is refused
+    if ((!at.has_branch && (g.gate || dy)) || (!post && (g.w_post || g.b_post)) ||
+        (!pre && (g.w_pre || g.b_pre || g.scale || g.shift)))
+        return EBIN_ERR_INVALID_ARG;
+    struct Out { float *p; int64_t bytes; };
+    const int64_t row = sizeof(float) * at.n;
+    const int64_t gate_bytes = row * (at.gate_rows ? at.rows / at.gate_rows : 1);
+    const int64_t mod_bytes = row * (at.mod_rows ? at.rows / at.mod_rows : 1);
+    const Out sums[7] = {{g.gate, gate_bytes}, {g.scale, mod_bytes}, {g.shift, mod_bytes},
+                         {g.w_post, row}, {g.b_post, row}, {g.w_pre, row}, {g.b_pre, row}};
+    bool wanted = false;
+    for (const Out &o : sums) {
+        if ((uintptr_t)o.p % 4) return EBIN_ERR_INVALID_ARG;
+        wanted |= o.p != nullptr;
+    }
+    if (at.rows == 0) {
+        for (const Out &o : sums)
+            if (o.p && o.bytes > 0 && cudaMemsetAsync(o.p, 0, (size_t)o.bytes, s) != cudaSuccess)
+                return EBIN_ERR_CUDA;
+        return EBIN_OK;
+    }
+    if (!pre) dz = h = nullptr;
+    else if (!dz || !h) return EBIN_ERR_INVALID_ARG;
+    if (!post && !g.gate) y = nullptr;
+    else if (!y) return EBIN_ERR_INVALID_ARG;
+    if (((uintptr_t)h | (uintptr_t)dh | (uintptr_t)dx) % (uintptr_t)p.ssz ||
+        ((uintptr_t)y | (uintptr_t)dz | (uintptr_t)dy) % (uintptr_t)p.isz)
+        return EBIN_ERR_INVALID_ARG;
+    if (wanted && (!workspace || workspace_bytes < p.workspace || (uintptr_t)workspace % 16))
+        return EBIN_ERR_INVALID_ARG;
+    BlockArgs a;
+    const ebin_status st = prepare_block(p, w, a);
+    if (st != EBIN_OK) return st;
+    a.shift = nullptr;
+    Range in[12];
+    int c = param_ranges(p, a, in);
+    in[c++] = Range{dz, rows_bytes(at.rows, at.n, at.ld_dz, p.isz), at.ld_dz * p.isz, p.isz};
+    in[c++] = Range{dh, rows_bytes(at.rows, at.n, at.ld_dh, p.ssz), at.ld_dh * p.ssz, p.ssz};
+    in[c++] = Range{h, rows_bytes(at.rows, at.n, at.ld_h, p.ssz), at.ld_h * p.ssz, p.ssz};
+    in[c++] = Range{y, rows_bytes(at.rows, at.n, at.ld_y, p.isz), at.ld_y * p.isz, p.isz};
+    Range out[10] = {
+        {dx, rows_bytes(at.rows, at.n, at.ld_dx, p.ssz), at.ld_dx * p.ssz, p.ssz},
+        {dy, rows_bytes(at.rows, at.n, at.ld_dy, p.isz), at.ld_dy * p.isz, p.isz}};
+    int o = 2;
+    for (const Out &q : sums)
+        if (q.p) out[o++] = Range{q.p, q.bytes, 0, 0};
+    if (wanted) out[o++] = Range{workspace, (int64_t)p.workspace, 0, 0};
+    for (int k = 0; k < o; ++k) {
+        for (int i = 0; i < c; ++i)
+            if (!apart(in[i], out[k], at.rows)) return EBIN_ERR_ALIAS;
+        for (int i = 0; i < k; ++i)
+            if (out[i].p && out[k].p &&
+                ranges_overlap(out[i].p, out[i].bytes, out[k].p, out[k].bytes))
+                return EBIN_ERR_ALIAS;
+    }
+    a.x = h;
+    a.y = y;
+    a.dz = dz;
+    a.dh = dh;
+    a.h = dx;
+    a.z = dy;
+    a.ld_x = at.ld_h;
+    a.ld_y = at.ld_y;
+    a.ld_dz = at.ld_dz;
+    a.ld_dh = at.ld_dh;
+    a.ld_h = at.ld_dx;
+    a.ld_z = at.ld_dy;
+    a.partial = wanted ? static_cast<float *>(workspace) : nullptr;
+    if (g.scale || g.w_pre) a.need |= 1 << SUM_DZ_HH;
+    if (g.shift || g.b_pre || (g.scale && a.b_pre)) a.need |= 1 << SUM_DZ;
+    if (g.gate || g.w_post) a.need |= 1 << SUM_E_YH;
+    if (g.b_post || (g.gate && a.b_post)) a.need |= 1 << SUM_E;
+    if (!wanted && !dx && !dy) return EBIN_OK;
+    if (launch_block(p, a, true, s) != cudaSuccess) return EBIN_ERR_CUDA;
+    if (!wanted) return EBIN_OK;
+    BlockSumsArgs b{};
+    b.partial = a.partial;
+    b.parts = p.parts;
+    b.groups = p.groups;
+    b.n = at.n;
+    b.gate = a.gate;
+    b.w_post = a.w_post;
+    b.b_post = a.b_post;
+    b.w_pre = a.w_pre;
+    b.b_pre = a.b_pre;
+    b.scale = a.scale;
+    b.ld_gate = at.ld_gate;
+    b.ld_scale = at.ld_scale;
+    b.gate_grouped = at.gate_rows != 0;
+    b.mod_grouped = at.mod_rows != 0;
+    b.w_f32 = a.w_f32;
+    b.mod_f32 = a.mod_f32;
+    b.dtype = at.dtype;
+    b.need = a.need;
+    b.dgate = g.gate;
+    b.dw_post = g.w_post;
+    b.db_post = g.b_post;
+    b.dw_pre = g.w_pre;
+    b.db_pre = g.b_pre;
+    b.dscale = g.scale;
+    b.dshift = g.shift;
+    // what all rows share, and the groups more than one
+    b.second = p.groups > 1 && (g.w_post || g.b_post || g.w_pre || g.b_pre ||
+                                (!b.gate_grouped && g.gate) ||
+                                (!b.mod_grouped && (g.scale || g.shift)));
+    b.tiles = div_up(at.n, kSumLanes);
+    if (launch_sums(k_block_sums, b.tiles * p.groups, b, s) != cudaSuccess) return EBIN_ERR_CUDA;
+    if (b.second && launch_sums(k_block_sums_all, b.tiles, b, s) != cudaSuccess)
+        return EBIN_ERR_CUDA;
+    return EBIN_OK;
+}

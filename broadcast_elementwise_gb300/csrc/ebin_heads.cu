@@ -8,6 +8,11 @@
 
 namespace ebin {
 
+// The pairs of a table's columns: (axis' pairs, place among them) of each.
+struct TableSections {
+    uint16_t pairs[kHeadsMaxDim / 2], place[kHeadsMaxDim / 2];
+};
+
 struct TableArgs {
     int64_t first, positions;
     int32_t half, scaling;
@@ -18,7 +23,10 @@ struct TableArgs {
 
 // One thread per frequency, its positions in steps of the grid's y: the
 // frequency in binary64 once, then an angle, its cosine and its sine each.
-__global__ void __launch_bounds__(256) k_rotary_table(const TableArgs a) {
+template <bool AXES>
+__global__ void __launch_bounds__(256)
+k_rotary_table(const TableArgs a,
+               const std::conditional_t<AXES, TableSections, HeadsOne> sections) {
     layer_pdl_launch();
     layer_pdl_wait();
     const int64_t n = a.positions * a.half;
@@ -26,7 +34,10 @@ __global__ void __launch_bounds__(256) k_rotary_table(const TableArgs a) {
          i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / a.half;
         const int j = (int)(i - row * a.half);
-        double f = exp2(-a.log2_base * ((double)j / (double)a.half));
+        double part;
+        if constexpr (AXES) part = (double)sections.place[j] / (double)sections.pairs[j];
+        else part = (double)j / (double)a.half;
+        double f = exp2(-a.log2_base * part);
         if (a.scaling == EBIN_ROTARY_SCALE_LINEAR) f /= a.factor;
         if (a.scaling == EBIN_ROTARY_SCALE_BY_PARTS) {
             const double turns = a.trained * f / 6.283185307179586476925;
@@ -49,6 +60,9 @@ struct ebin_heads_plan_s {
     int64_t span[6] = {};      // storage extent in elements: q, k, dq, dk, q_out, k_out
     bool empty = false;
     size_t workspace = 0;
+    bool several = false;      // the positions have axes
+    int64_t axes_count = 1;
+    ebin::HeadsAxes axes = {};
 };
 
 using namespace ebin;
@@ -183,9 +197,9 @@ int64_t any_ctas(const ebin_heads_plan_s &p, int which, int mode) {
     return std::min(ctas, most);
 }
 
-template <class T>
-cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode, int64_t *ctas,
-                       cudaStream_t s) {
+template <class T, class AX>
+cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, const AX &ax, int mode,
+                       int64_t *ctas, cudaStream_t s) {
     ctas[0] = any_ctas(p, 0, mode);
     ctas[1] = any_ctas(p, 1, mode);
     const int64_t gx = std::max(ctas[0], ctas[1]);
@@ -193,11 +207,14 @@ cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode,
     const dim3 grid((unsigned)gx, p.at.k_heads > 0 ? 2 : 1);
     const int il = p.at.layout == EBIN_ROTARY_INTERLEAVED;
     if (mode == HEADS_ROTATE)
-        return launch_layer(k_heads_any<T, HEADS_ROTATE>, grid, kHeadsThreads, 0, s, 1, a, il);
+        return launch_layer(k_heads_any<T, HEADS_ROTATE, AX>, grid, kHeadsThreads, 0, s, 1, a, ax,
+                            il);
     if (mode == HEADS_NORM)
-        return launch_layer(k_heads_any<T, HEADS_NORM>, grid, kHeadsThreads, 0, s, 1, a, il);
+        return launch_layer(k_heads_any<T, HEADS_NORM, AX>, grid, kHeadsThreads, 0, s, 1, a, ax,
+                            il);
     const size_t smem = sizeof(float) * (kHeadsThreads / 32) * a.dim;   // <= 32 KB
-    return launch_layer(k_heads_any<T, HEADS_NORM_GRAD>, grid, kHeadsThreads, smem, s, 1, a, il);
+    return launch_layer(k_heads_any<T, HEADS_NORM_GRAD, AX>, grid, kHeadsThreads, smem, s, 1, a, ax,
+                        il);
 }
 
 // The vector path's layout of a head, or false where it does not apply: rows
@@ -264,47 +281,50 @@ template <auto KERNEL> int heads_resident(size_t smem) {
     return n;
 }
 
-template <class T, int KIND, int MODE, int HPT>
-cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, cudaStream_t s) {
+template <class T, int KIND, int MODE, int HPT, class AX>
+cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, const AX &ax, cudaStream_t s) {
     v.q_items = (uint32_t)div_up(a.heads[0], HPT);
     v.per_token = fast_div(v.q_items + (uint32_t)div_up(a.heads[1], HPT));
     v.items = (uint32_t)a.rows * v.per_token.n;
     const int64_t grid = div_up((int64_t)v.items << v.log_lanes, kHeadsThreads);
     const size_t smem = KIND == HEADS_ODD
         ? sizeof(T) * (kHeadsThreads >> v.log_lanes) * HPT * a.dim : 0;   // at most 32 KB
-    return launch_layer(k_heads_vec<T, KIND, MODE, HPT>, dim3((unsigned)grid), kHeadsThreads, smem,
-                        s, 1, a, v);
+    return launch_layer(k_heads_vec<T, KIND, MODE, HPT, AX>, dim3((unsigned)grid), kHeadsThreads,
+                        smem, s, 1, a, v, ax);
 }
 
-template <class T, int KIND> cudaError_t launch_ring(const HeadsArgs &a, HeadsVecArgs v,
-                                                     cudaStream_t s) {
+template <class T, int KIND, class AX>
+cudaError_t launch_ring(const HeadsArgs &a, HeadsVecArgs v, const AX &ax, cudaStream_t s) {
     v.q_items = (uint32_t)div_up(a.heads[0], kRingHeads);
     v.per_token = fast_div(v.q_items + (uint32_t)div_up(a.heads[1], kRingHeads));
     v.items = (uint32_t)a.rows * v.per_token.n;
-    constexpr size_t smem = HeadsRing<T, KIND, false>::kBytes + (KIND == HEADS_ODD ? 8192 : 0);
-    const cudaError_t opted = allow_smem<k_heads_ring<T, KIND>>(smem);
+    constexpr size_t smem = HeadsRing<T, KIND, false, AX>::kBytes + (KIND == HEADS_ODD ? 8192 : 0);
+    const cudaError_t opted = allow_smem<k_heads_ring<T, KIND, AX>>(smem);
     if (opted != cudaSuccess) return opted;
-    const int64_t wave = (int64_t)heads_resident<k_heads_ring<T, KIND>>(smem) * current_sm_count();
+    const int64_t wave =
+        (int64_t)heads_resident<k_heads_ring<T, KIND, AX>>(smem) * current_sm_count();
     // Under three items a group the walk is too short to pay for itself (norm
     // [3,1021,15,96] f32, 1.3 items: 11.5 us against 8.2 by a CTA an item; [2,4096,40,128]
     // bf16, 5.6 items: 29.0 against 32.2).
     if (((int64_t)v.items << v.log_lanes) < 3 * wave * kHeadsThreads)
-        return launch_vec<T, KIND, HEADS_NORM, kRingHeads>(a, v, s);
-    return launch_layer(k_heads_ring<T, KIND>, dim3((unsigned)wave), kHeadsThreads, smem, s, 1, a,
-                        v);
+        return launch_vec<T, KIND, HEADS_NORM, kRingHeads>(a, v, ax, s);
+    return launch_layer(k_heads_ring<T, KIND, AX>, dim3((unsigned)wave), kHeadsThreads, smem, s, 1,
+                        a, v, ax);
 }
 
-template <class T, int KIND>
-cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, cudaStream_t s) {
+template <class T, int KIND, class AX>
+cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, const AX &ax, int64_t *ctas,
+                            cudaStream_t s) {
     // the ring, one group's weights (two vectors a lane) and, HEADS_ODD, the groups'
     // rows: at most 4 KB and 8 KB of them; the sums at the end fit the ring
-    constexpr size_t most = HeadsRing<T, KIND, true>::kBytes + 4096 + (KIND == HEADS_ODD ? 8192 : 0);
-    const cudaError_t opted = allow_smem<k_heads_vec_grad<T, KIND>>(most);
+    constexpr size_t most =
+        HeadsRing<T, KIND, true, AX>::kBytes + 4096 + (KIND == HEADS_ODD ? 8192 : 0);
+    const cudaError_t opted = allow_smem<k_heads_vec_grad<T, KIND, AX>>(most);
     if (opted != cudaSuccess) return opted;
     // one wave of CTAs, shared between q and k by their rows
     const int per = kHeadsThreads >> v.log_lanes;
     const int64_t all = std::min<int64_t>(
-        (int64_t)heads_resident<k_heads_vec_grad<T, KIND>>(most) * current_sm_count(),
+        (int64_t)heads_resident<k_heads_vec_grad<T, KIND, AX>>(most) * current_sm_count(),
         kHeadsMaxPartials);
     const int64_t heads = a.heads[0] + a.heads[1];
     for (int w = 0; w < 2; ++w) {
@@ -313,14 +333,14 @@ cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, int64_t *ctas, c
         v.ctas[w] = (int)std::min(items, share);
         ctas[w] = v.ctas[w];
     }
-    return launch_layer(k_heads_vec_grad<T, KIND>, dim3((unsigned)(v.ctas[0] + v.ctas[1])),
-                        kHeadsThreads, most, s, 1, a, v);
+    return launch_layer(k_heads_vec_grad<T, KIND, AX>, dim3((unsigned)(v.ctas[0] + v.ctas[1])),
+                        kHeadsThreads, most, s, 1, a, v, ax);
 }
 
-template <class T, int KIND>
-cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, int mode, int64_t *ctas,
-                            cudaStream_t s) {
-    if (mode == HEADS_NORM_GRAD) return launch_vec_grad<T, KIND>(a, v, ctas, s);
+template <class T, int KIND, class AX>
+cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, const AX &ax, int mode,
+                            int64_t *ctas, cudaStream_t s) {
+    if (mode == HEADS_NORM_GRAD) return launch_vec_grad<T, KIND>(a, v, ax, ctas, s);
     // Few rows: one head per item spreads them over the SMs.  Many: four heads
     // share the token's position, cosines, sines and weights (tokens of 32 and 8
     // heads of 128 bf16, one head an item against four: rotation of 64 1.8 and 2.2
@@ -328,28 +348,44 @@ cudaError_t launch_vec_mode(const HeadsArgs &a, const HeadsVecArgs &v, int mode,
     const bool few = (a.rows * (a.heads[0] + a.heads[1]) << v.log_lanes) <
                      2048ll * current_sm_count();
     if (mode == HEADS_ROTATE)
-        return few ? launch_vec<T, KIND, HEADS_ROTATE, 1>(a, v, s)
-                   : launch_vec<T, KIND, HEADS_ROTATE, 4>(a, v, s);
-    return few ? launch_vec<T, KIND, HEADS_NORM, 1>(a, v, s) : launch_ring<T, KIND>(a, v, s);
+        return few ? launch_vec<T, KIND, HEADS_ROTATE, 1>(a, v, ax, s)
+                   : launch_vec<T, KIND, HEADS_ROTATE, 4>(a, v, ax, s);
+    return few ? launch_vec<T, KIND, HEADS_NORM, 1>(a, v, ax, s)
+               : launch_ring<T, KIND>(a, v, ax, s);
 }
 
-template <class T>
-cudaError_t launch_heads(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode, int64_t *ctas,
-                         cudaStream_t s) {
+template <class T, class AX>
+cudaError_t launch_heads(const ebin_heads_plan_s &p, const HeadsArgs &a, const AX &ax, int mode,
+                         int64_t *ctas, cudaStream_t s) {
     HeadsVecArgs v;
     int kind = 0;
     if (!heads_vectors(p, a, mode == HEADS_NORM_GRAD, v, kind))
-        return launch_any<T>(p, a, mode, ctas, s);
-    if (kind == HEADS_HALF) return launch_vec_mode<T, HEADS_HALF>(a, v, mode, ctas, s);
-    if (kind == HEADS_PAIRS) return launch_vec_mode<T, HEADS_PAIRS>(a, v, mode, ctas, s);
-    return launch_vec_mode<T, HEADS_ODD>(a, v, mode, ctas, s);
+        return launch_any<T>(p, a, ax, mode, ctas, s);
+    if (kind == HEADS_HALF) return launch_vec_mode<T, HEADS_HALF>(a, v, ax, mode, ctas, s);
+    if (kind == HEADS_PAIRS) return launch_vec_mode<T, HEADS_PAIRS>(a, v, ax, mode, ctas, s);
+    return launch_vec_mode<T, HEADS_ODD>(a, v, ax, mode, ctas, s);
+}
+
+template <class AX>
+cudaError_t launch_axes(const ebin_heads_plan_s &p, const HeadsArgs &a, const AX &ax, int mode,
+                        int64_t *ctas, cudaStream_t s) {
+    if (p.at.dtype == EBIN_FLOAT32) return launch_heads<float>(p, a, ax, mode, ctas, s);
+    if (p.at.dtype == EBIN_FLOAT16) return launch_heads<__half>(p, a, ax, mode, ctas, s);
+    return launch_heads<__nv_bfloat16>(p, a, ax, mode, ctas, s);
 }
 
 cudaError_t launch_typed(const ebin_heads_plan_s &p, const HeadsArgs &a, int mode, int64_t *ctas,
                          cudaStream_t s) {
-    if (p.at.dtype == EBIN_FLOAT32) return launch_heads<float>(p, a, mode, ctas, s);
-    if (p.at.dtype == EBIN_FLOAT16) return launch_heads<__half>(p, a, mode, ctas, s);
-    return launch_heads<__nv_bfloat16>(p, a, mode, ctas, s);
+    return p.several ? launch_axes(p, a, p.axes, mode, ctas, s)
+                     : launch_axes(p, a, HeadsOne{}, mode, ctas, s);
+}
+
+// Elements of the positions' storage.
+int64_t positions_span(const ebin_heads_plan_s &p) {
+    int64_t n = (p.at.batch - 1) * p.at.position_strides[0] +
+                (p.at.tokens - 1) * p.at.position_strides[1] + 1;
+    if (p.several) n += (p.axes_count - 1) * p.axes.ps_a;
+    return n;
 }
 
 HeadsTensor tensor_of(const ebin_heads_attrs &a, int i, const void *p) {
@@ -406,9 +442,7 @@ ebin_status prepare_heads(const ebin_heads_plan_s &p, const void *const in[4],
             return EBIN_ERR_ALIAS;
         if (at.rotary_dim > 0 && at.position_type) {
             const int64_t ps = type_size((ebin_dtype)at.position_type);
-            const int64_t n = (at.batch - 1) * at.position_strides[0] +
-                              (at.tokens - 1) * at.position_strides[1] + 1;
-            if (ranges_overlap(pos, n * ps, y.p, y_bytes)) return EBIN_ERR_ALIAS;
+            if (ranges_overlap(pos, positions_span(p) * ps, y.p, y_bytes)) return EBIN_ERR_ALIAS;
         }
     }
     a = HeadsArgs{};
@@ -449,9 +483,42 @@ bool attach_status(const ebin_heads_plan_s &p, cudaStream_t s, HeadsArgs &a) {
 
 }  // namespace
 
-extern "C" ebin_status ebin_rotary_table(const ebin_rotary_attrs *attrs, int64_t first_position,
-                                         int64_t positions, float *cos, float *sin,
-                                         void *stream) {
+namespace {
+
+// Checks axes and gives each pair its axis and its place among the axis' pairs.
+ebin_status axes_of_pairs(const ebin_rotary_axes &x, int rotary_dim, uint8_t *axis,
+                          uint16_t *place) {
+    if (x.count < 1 || x.count > kHeadsMaxAxes ||
+        (x.order != EBIN_AXES_BLOCKS && x.order != EBIN_AXES_DEALT))
+        return EBIN_ERR_INVALID_ATTR;
+    int64_t pairs = 0;
+    int most = 0;
+    for (int i = 0; i < x.count; ++i) {
+        if (x.sections[i] < 0) return EBIN_ERR_INVALID_ATTR;
+        pairs += x.sections[i];
+        most = std::max(most, x.sections[i]);
+    }
+    if (pairs < 1 || pairs > kHeadsMaxDim / 2 || 2 * pairs != rotary_dim)
+        return EBIN_ERR_INVALID_ATTR;
+    int j = 0;
+    auto give = [&](int i, int k) {
+        axis[j] = (uint8_t)i;
+        place[j++] = (uint16_t)k;
+    };
+    if (x.order == EBIN_AXES_BLOCKS) {
+        for (int i = 0; i < x.count; ++i)
+            for (int k = 0; k < x.sections[i]; ++k) give(i, k);
+    } else {
+        for (int k = 0; k < most; ++k)
+            for (int i = 0; i < x.count; ++i)
+                if (k < x.sections[i]) give(i, k);
+    }
+    return EBIN_OK;
+}
+
+ebin_status rotary_table(const ebin_rotary_attrs *attrs, const ebin_rotary_axes *axes,
+                         int64_t first_position, int64_t positions, float *cos, float *sin,
+                         void *stream) {
     if (!attrs || first_position < 0 || positions < 0) return EBIN_ERR_INVALID_ARG;
     const ebin_rotary_attrs &t = *attrs;
     if (t.rotary_dim < 2 || t.rotary_dim > 65536 || t.rotary_dim % 2 != 0 ||
@@ -467,6 +534,16 @@ extern "C" ebin_status ebin_rotary_table(const ebin_rotary_attrs *attrs, int64_t
          !(t.fast_turns > t.slow_turns) || !std::isfinite(t.fast_turns) ||
          !std::isfinite(t.slow_turns)))
         return EBIN_ERR_INVALID_ATTR;
+    TableSections sections{};
+    if (axes) {
+        // each axis has a base of its own width
+        if (t.scaling == EBIN_ROTARY_SCALE_BASE) return EBIN_ERR_INVALID_ATTR;
+        uint8_t axis[kHeadsMaxDim / 2];
+        const ebin_status st = axes_of_pairs(*axes, t.rotary_dim, axis, sections.place);
+        if (st != EBIN_OK) return st;
+        for (int j = 0; j < t.rotary_dim / 2; ++j)
+            sections.pairs[j] = (uint16_t)axes->sections[axis[j]];
+    }
     int64_t n;
     if (!product_fits(positions, t.rotary_dim / 2, &n) ||
         first_position > (int64_t(1) << 53) - positions)
@@ -490,9 +567,28 @@ extern "C" ebin_status ebin_rotary_table(const ebin_rotary_attrs *attrs, int64_t
     a.cos = cos;
     a.sin = sin;
     const int64_t grid = std::min<int64_t>(div_up(n, 256), 16ll * current_sm_count());
-    return launch_layer(k_rotary_table, dim3((unsigned)grid), 256, 0,
-                        static_cast<cudaStream_t>(stream), 1, a) == cudaSuccess
-               ? EBIN_OK : EBIN_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        axes ? launch_layer(k_rotary_table<true>, dim3((unsigned)grid), 256, 0, s, 1, a, sections)
+             : launch_layer(k_rotary_table<false>, dim3((unsigned)grid), 256, 0, s, 1, a,
+                            HeadsOne{});
+    return e == cudaSuccess ? EBIN_OK : EBIN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" ebin_status ebin_rotary_table(const ebin_rotary_attrs *attrs, int64_t first_position,
+                                         int64_t positions, float *cos, float *sin,
+                                         void *stream) {
+    return rotary_table(attrs, nullptr, first_position, positions, cos, sin, stream);
+}
+
+extern "C" ebin_status ebin_rotary_table_axes(const ebin_rotary_attrs *attrs,
+                                              const ebin_rotary_axes *axes,
+                                              int64_t first_position, int64_t positions,
+                                              float *cos, float *sin, void *stream) {
+    if (!axes) return EBIN_ERR_INVALID_ARG;
+    return rotary_table(attrs, axes, first_position, positions, cos, sin, stream);
 }
 
 extern "C" ebin_status ebin_heads_plan_create(const ebin_heads_attrs *attrs,
@@ -548,6 +644,41 @@ extern "C" ebin_status ebin_heads_plan_create(const ebin_heads_attrs *attrs,
     std::memcpy(p->span, span, sizeof(span));
     p->empty = span[4] == 0 && span[5] == 0;
     if (grad && !p->empty) p->workspace = sizeof(float) * 2 * kHeadsMaxPartials * a.head_dim;
+    *out = p;
+    return EBIN_OK;
+}
+
+extern "C" ebin_status ebin_heads_plan_create_axes(const ebin_heads_attrs *attrs,
+                                                   const ebin_rotary_axes *axes,
+                                                   ebin_heads_plan_t *out) {
+    if (out) *out = nullptr;
+    if (!attrs || !axes || !out) return EBIN_ERR_INVALID_ARG;
+    uint8_t axis[kHeadsMaxDim / 2];
+    uint16_t place[kHeadsMaxDim / 2];
+    ebin_heads_plan_t p = nullptr;
+    ebin_status st = ebin_heads_plan_create(attrs, &p);
+    if (st == EBIN_OK) st = axes_of_pairs(*axes, attrs->rotary_dim, axis, place);
+    if (st == EBIN_OK && !attrs->position_type) st = EBIN_ERR_INVALID_ATTR;
+    int64_t far;
+    if (st == EBIN_OK && (axes->position_stride < 0 ||
+                          !product_fits(kHeadsMaxAxes, axes->position_stride, &far) ||
+                          !product_fits(std::max<int64_t>(attrs->batch, 1),
+                                        attrs->position_strides[0], &far) ||
+                          !product_fits(std::max<int64_t>(attrs->tokens, 1),
+                                        attrs->position_strides[1], &far) ||
+                          attrs->table_positions > 0x7FFFFFFF))   // rows are kept in 32 bits
+        st = EBIN_ERR_INVALID_ARG;
+    if (st != EBIN_OK) {
+        ebin_heads_plan_release(p);
+        return st;
+    }
+    p->several = true;
+    p->axes_count = axes->count;
+    p->axes.ps_a = axes->position_stride;
+    for (int j = 0; j < attrs->rotary_dim / 2; ++j) {
+        p->axes.of_pair[j / 16] |= (uint32_t)axis[j] << (2 * (j % 16));
+        p->axes.used |= 1 << axis[j];
+    }
     *out = p;
     return EBIN_OK;
 }
@@ -608,9 +739,7 @@ extern "C" ebin_status ebin_heads_grad_execute(ebin_heads_plan_t plan, const voi
     // the small buffers and the workspace overlap nothing that is read or written
     const int64_t dw_bytes = sizeof(float) * p.at.head_dim;
     const int64_t pos_bytes = p.at.position_type && p.at.rotary_dim
-        ? ((p.at.batch - 1) * p.at.position_strides[0] +
-           (p.at.tokens - 1) * p.at.position_strides[1] + 1) *
-              type_size((ebin_dtype)p.at.position_type) : 0;
+        ? positions_span(p) * type_size((ebin_dtype)p.at.position_type) : 0;
     struct Range { const void *p; int64_t n; };
     const int64_t table_bytes = p.at.table_positions * (p.at.rotary_dim / 2) * 4;
     const int64_t w_bytes = p.at.head_dim * type_size(p.at.dtype_w);

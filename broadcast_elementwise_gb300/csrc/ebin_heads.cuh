@@ -63,6 +63,61 @@ __device__ __forceinline__ int64_t heads_position(const HeadsArgs &a, int64_t b,
     return (p >= 0 && p < a.table) ? p : -1;
 }
 
+// Where a token lies in the table, and which of its rows a pair reads: one position
+// for all pairs, or one for each axis of an image's or a video's token.
+struct HeadsOne {
+    struct At {
+        int64_t p;   // -1: outside the table
+        __device__ __forceinline__ bool out() const { return p < 0; }
+    };
+    __device__ __forceinline__ At at(const HeadsArgs &a, int64_t b, int64_t s) const {
+        return At{heads_position(a, b, s)};
+    }
+    __device__ __forceinline__ int64_t row(const At &at, int) const { return at.p < 0 ? 0 : at.p; }
+    // whether the four pairs from `pair` on read the same row
+    __device__ __forceinline__ bool same4(int) const { return true; }
+};
+
+constexpr int kHeadsMaxAxes = 4;
+
+struct HeadsAxes {
+    int64_t ps_a;         // position stride: axis
+    int32_t used;         // axes with pairs, by bit
+    uint32_t of_pair[kHeadsMaxDim / 32];   // two bits for each pair
+    struct At {
+        int32_t p[kHeadsMaxAxes];   // 0 for an axis without pairs
+        bool bad;                   // an axis with pairs lies outside the table
+        __device__ __forceinline__ bool out() const { return bad; }
+    };
+    __device__ __forceinline__ At at(const HeadsArgs &a, int64_t b, int64_t s) const {
+        At r;
+        r.bad = false;
+        const int64_t i = b * a.ps_b + s * a.ps_t;
+#pragma unroll
+        for (int x = 0; x < kHeadsMaxAxes; ++x) {
+            r.p[x] = 0;
+            if (used >> x & 1) {
+                const int64_t p = a.pos_size == 4
+                    ? (int64_t)static_cast<const int32_t *>(a.pos)[i + x * ps_a]
+                    : static_cast<const int64_t *>(a.pos)[i + x * ps_a];
+                const bool in = p >= 0 && p < a.table;
+                r.bad |= !in;
+                r.p[x] = in ? (int32_t)p : 0;
+            }
+        }
+        return r;
+    }
+    __device__ __forceinline__ int64_t row(const At &at, int pair) const {
+        const uint32_t x = of_pair[pair >> 4] >> (2 * (pair & 15));
+        const int32_t lo = x & 1 ? at.p[1] : at.p[0], hi = x & 1 ? at.p[3] : at.p[2];
+        return x & 2 ? hi : lo;
+    }
+    __device__ __forceinline__ bool same4(int pair) const {   // pair: a multiple of 4
+        const uint32_t x = of_pair[pair >> 4] >> (2 * (pair & 15)) & 0xFF;
+        return x == (x & 3) * 0x55;
+    }
+};
+
 template <class T>
 __device__ __forceinline__ float heads_weight(const HeadsArgs &a, int which, int j) {
     if (!a.w[which]) return 1.0f;
@@ -84,8 +139,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 // vectors, one element a lane and access: an eighth of the copy's rate for heads of
 // 128 off 16 bytes (rotation of [2,4096,40,128] bf16 195 us, norm 219, its gradient
 // 271), a twentieth for heads of 33, where a row of 66 bytes takes a warp (143 us).
-template <class T, int MODE>
-__global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, int interleaved) {
+template <class T, int MODE, class AX>
+__global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, const AX ax,
+                                                             int interleaved) {
     extern __shared__ float s_dw[];   // HEADS_NORM_GRAD: [warps][dim]
     const int which = blockIdx.y;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -109,13 +165,14 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, 
         const T *dy = nullptr;
         if constexpr (MODE == HEADS_NORM_GRAD)
             dy = static_cast<const T *>(a.dy[which].p) + heads_offset(a.dy[which], b, s, h);
-        const int64_t p = heads_position(a, b, s);
-        if (p < 0) {
+        const typename AX::At at = ax.at(a, b, s);
+        if (at.out()) {
             bad = true;
             for (int j = lane; j < D; j += 32) y[j] = from_f<T>(0.0f);
             continue;
         }
-        const float *cs = a.cos + p * half, *sn = a.sin + p * half;
+        // where pair k's cosine and sine lie
+        auto angle = [&](int k) { return ax.row(at, k) * half + k; };
         // a slot's elements: i0 and, in a rotated pair, i1
         auto first = [&](int k) { return k >= half ? k + half : (interleaved ? 2 * k : k); };
         auto second = [&](int k) { return interleaved ? 2 * k + 1 : k + half; };
@@ -134,7 +191,8 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, 
                     float g0 = to_f(dy[i0]);
                     if (k < half) {
                         const int i1 = second(k);
-                        const float d1 = to_f(dy[i1]), c = cs[k], n = sn[k];
+                        const int64_t t = angle(k);
+                        const float d1 = to_f(dy[i1]), c = a.cos[t], n = a.sin[t];
                         const float g1 = d1 * c - g0 * n;
                         g0 = g0 * c + d1 * n;
                         dot = fmaf(g1 * heads_weight<T>(a, which, i1), x1, dot);
@@ -150,7 +208,12 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, 
         for (int k = lane; k < slots; k += 32) {
             const int i0 = first(k), i1 = k < half ? second(k) : -1;
             float x0 = to_f(x[i0]) * rstd, x1 = i1 >= 0 ? to_f(x[i1]) * rstd : 0.0f;
-            const float c = i1 >= 0 ? cs[k] : 1.0f, n = i1 >= 0 ? sn[k] * a.sign : 0.0f;
+            float c = 1.0f, n = 0.0f;
+            if (i1 >= 0) {
+                const int64_t t = angle(k);
+                c = a.cos[t];
+                n = a.sin[t] * a.sign;
+            }
             if constexpr (MODE == HEADS_NORM_GRAD) {
                 float g0 = to_f(dy[i0]);
                 const float w0 = heads_weight<T>(a, which, i0);
@@ -348,18 +411,20 @@ template <class T, int KIND> struct HeadsUnit {
         const int j = off0 + k;
         return j < half ? j + half : j - half;
     }
-    __device__ __forceinline__ void factors(const HeadsArgs &a, int64_t p, float sign, float2 *ca,
+    template <class AX>
+    __device__ __forceinline__ void factors(const HeadsArgs &a, const AX &ax,
+                                            const typename AX::At &p, float sign, float2 *ca,
                                             float2 *cb, float2 *sa, float2 *sb) const {
-        const float *cr = a.cos + p * a.half, *sr = a.sin + p * a.half;
         auto one = [&](int k, float &c, float &s) {
             c = 1.0f;
             s = 0.0f;
             if (k < pairs) {
                 const int j = off0 + k;
                 const bool first = j < a.half;
-                const int at = first ? j : j - a.half;
-                c = __ldg(cr + at);
-                s = __ldg(sr + at) * (first ? -sign : sign);
+                const int pair = first ? j : j - a.half;
+                const int64_t at = ax.row(p, pair) * a.half + pair;
+                c = __ldg(a.cos + at);
+                s = __ldg(a.sin + at) * (first ? -sign : sign);
             }
         };
 #pragma unroll
@@ -387,12 +452,12 @@ template <class T, int KIND> struct HeadsUnit {
     // a pair's factors: y_a = x_a ca + x_b nb, y_b = x_b cb + x_a sa: cos, sin and
     // -sin, with a norm times the weights of the elements they meet
     // (ODD: y_a = x_a ca + other sa, y_b = x_b cb + other nb)
-    template <bool NORM>
-    __device__ __forceinline__ void folded(const HeadsArgs &a, const HeadsVecArgs &v, int which,
-                                           int64_t p, float2 *ca, float2 *cb, float2 *sa,
-                                           float2 *nb) const {
-        if constexpr (ODD) factors(a, p, a.sign, ca, cb, sa, nb);
-        else angles(a, v, p, ca, sa, nb);
+    template <bool NORM, class AX>
+    __device__ __forceinline__ void folded(const HeadsArgs &a, const HeadsVecArgs &v, const AX &ax,
+                                           int which, const typename AX::At &p, float2 *ca,
+                                           float2 *cb, float2 *sa, float2 *nb) const {
+        if constexpr (ODD) factors(a, ax, p, a.sign, ca, cb, sa, nb);
+        else angles(a, v, ax, p, ca, sa, nb);
         if constexpr (NORM) {
             float2 wa[N], wb[N];
             weights(a, v, which, wa, wb);
@@ -431,34 +496,46 @@ template <class T, int KIND> struct HeadsUnit {
             b[i].y = one(V + 2 * i + 1, b[i].y, cb[i].y, sb[i].y);
         }
     }
-    // the unit's cosines and sines (pairs past `pairs`: 1 and 0)
-    __device__ __forceinline__ void table(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
-                                          float2 *c, float2 *s) const {
-        const float *cr = a.cos + p * a.half + pair0, *sr = a.sin + p * a.half + pair0;
-        if (pairs == V && v.table_vec) {
+    // the unit's cosines and sines (pairs past `pairs`: 1 and 0); four pairs of one
+    // axis are neighbours in their row
+    template <class AX>
+    __device__ __forceinline__ void table(const HeadsArgs &a, const HeadsVecArgs &v, const AX &ax,
+                                          const typename AX::At &p, float2 *c, float2 *s) const {
+        const bool whole = pairs == V && v.table_vec;
 #pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(cr + 2 * i));
-                const float4 y = __ldg(reinterpret_cast<const float4 *>(sr + 2 * i));
+        for (int i = 0; i < N; i += 2) {
+            const int first = pair0 + 2 * i;
+            if (whole && ax.same4(first)) {
+                const int64_t at = ax.row(p, first) * a.half + first;
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
+                const float4 y = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
                 c[i] = make_float2(x.x, x.y);
                 c[i + 1] = make_float2(x.z, x.w);
                 s[i] = make_float2(y.x, y.y);
                 s[i + 1] = make_float2(y.z, y.w);
+                continue;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                c[i].x = 2 * i < pairs ? __ldg(cr + 2 * i) : 1.0f;
-                s[i].x = 2 * i < pairs ? __ldg(sr + 2 * i) : 0.0f;
-                c[i].y = 2 * i + 1 < pairs ? __ldg(cr + 2 * i + 1) : 1.0f;
-                s[i].y = 2 * i + 1 < pairs ? __ldg(sr + 2 * i + 1) : 0.0f;
-            }
+            auto one = [&](int k, float &cc, float &ss) {
+                cc = 1.0f;
+                ss = 0.0f;
+                if (2 * i + k < pairs) {
+                    const int64_t at = ax.row(p, first + k) * a.half + first + k;
+                    cc = __ldg(a.cos + at);
+                    ss = __ldg(a.sin + at);
+                }
+            };
+            one(0, c[i].x, s[i].x);
+            one(1, c[i].y, s[i].y);
+            one(2, c[i + 1].x, s[i + 1].x);
+            one(3, c[i + 1].y, s[i + 1].y);
         }
     }
     // c = cos, s = sin with the direction's sign, n = -s
-    __device__ __forceinline__ void angles(const HeadsArgs &a, const HeadsVecArgs &v, int64_t p,
-                                           float2 *c, float2 *s, float2 *n) const {
-        table(a, v, p, c, s);
+    template <class AX>
+    __device__ __forceinline__ void angles(const HeadsArgs &a, const HeadsVecArgs &v, const AX &ax,
+                                           const typename AX::At &p, float2 *c, float2 *s,
+                                           float2 *n) const {
+        table(a, v, ax, p, c, s);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             n[i] = __fmul2_rn(s[i], both(-a.sign));
@@ -566,9 +643,9 @@ __device__ __forceinline__ void keep_packed(uint4 &x) {
 // of k; all its loads are issued before the first is used.  Four heads an item
 // and three CTAs an SM (80 registers): rotation of [1,16384,40,128] bf16 52.9 us;
 // two heads 61.6, four at two CTAs 58.8; one head where rows are few.
-template <class T, int KIND, int MODE, int HPT>
+template <class T, int KIND, int MODE, int HPT, class AX>
 __global__ void __launch_bounds__(kHeadsThreads, sizeof(T) == 4 ? 1 : KIND == HEADS_ODD ? 2 : 3)
-k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
+k_heads_vec(const HeadsArgs a, const HeadsVecArgs v, const AX ax) {
     using Unit = HeadsUnit<T, KIND>;
     constexpr int N = Unit::N;
     const int lanes = 1 << v.log_lanes, lane = threadIdx.x & (lanes - 1);
@@ -588,7 +665,7 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
                        heads_near(which ? v.x[1] : v.x[0], b, s, h0);
     const int xsh = which ? v.x[1].sh : v.x[0].sh;
     layer_pdl_wait();
-    const int64_t p = heads_position(a, b, s);
+    const typename AX::At p = ax.at(a, b, s);
     uint4 x0[HPT], x1[HPT];
 #pragma unroll
     for (int h = 0; h < HPT; ++h) u.load(x + (h < count ? (int64_t)h * xsh : 0), x0[h], x1[h]);
@@ -619,8 +696,8 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
         for (int h = 0; h < HPT; ++h) rstd[h] = rsqrtf(fmaf(rstd[h], inv, a.eps));
     }
     float2 ca[N], cb[N], sa[N], nb[N];
-    u.template folded<MODE == HEADS_NORM>(a, v, which, p < 0 ? 0 : p, ca, cb, sa, nb);
-    if (p < 0 && live && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+    u.template folded<MODE == HEADS_NORM>(a, v, ax, which, p, ca, cb, sa, nb);
+    if (p.out() && live && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
     T *const y = static_cast<T *>(const_cast<void *>(which ? v.y[1].p : v.y[0].p)) +
                  heads_near(which ? v.y[1] : v.y[0], b, s, h0);
     const int ysh = which ? v.y[1].sh : v.y[0].sh;
@@ -640,7 +717,7 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v) {
                        cb, sa, nb);
         else
             u.turn(va, vb, ca, sa, nb, cb);
-        if (p < 0) {
+        if (p.out()) {
 #pragma unroll
             for (int i = 0; i < N; ++i) va[i] = vb[i] = both(0.0f);
         }
@@ -661,7 +738,7 @@ __device__ __forceinline__ void heads_copy(uint32_t to, const void *from) {
 }
 
 // GRAD: rows of x and of dy, of one tensor; else rows of x, of q then of k.
-template <class T, int KIND, bool GRAD> struct HeadsRing {
+template <class T, int KIND, bool GRAD, class AX> struct HeadsRing {
     using Unit = HeadsUnit<T, KIND>;
     static constexpr int kAhead = GRAD ? 3 : 4, kSlots = kAhead + 1;
     static constexpr int kVectors = GRAD ? 4 : 2;             // of a thread and row
@@ -677,11 +754,12 @@ template <class T, int KIND, bool GRAD> struct HeadsRing {
     int row, fill, slot;        // row of the item; ring slots to fill and to read
     // of the item whose fetching began last
     T *y;
-    int64_t position;
+    typename AX::At position;
     int count, ysh;
     bool k;                     // of k
 
-    __device__ __forceinline__ void start(const HeadsArgs &a, const HeadsVecArgs &v, int one) {
+    __device__ __forceinline__ void start(const HeadsArgs &a, const HeadsVecArgs &v, const AX &ax,
+                                          int one) {
         uint32_t bs, h, b, s;
         const bool live = item < total;   // an item past the end has no rows
         parts.split(live ? item : 0, bs, h);
@@ -689,7 +767,7 @@ template <class T, int KIND, bool GRAD> struct HeadsRing {
         k = one >= 0 ? one == 1 : h >= v.q_items;
         if (one < 0 && k) h -= v.q_items;
         h *= kRingHeads;
-        position = heads_position(a, b, s);
+        position = ax.at(a, b, s);
         x = static_cast<const T *>(k ? v.x[1].p : v.x[0].p) +
             heads_near(k ? v.x[1] : v.x[0], b, s, h);
         xsh = k ? v.x[1].sh : v.x[0].sh;
@@ -704,10 +782,10 @@ template <class T, int KIND, bool GRAD> struct HeadsRing {
         count = live ? min(kRingHeads, (k ? a.heads[1] : a.heads[0]) - (int)h) : 0;
     }
     // one: 0 or 1, the walk's tensor, or -1, both
-    __device__ __forceinline__ void fetch(const HeadsArgs &a, const HeadsVecArgs &v, const Unit &u,
-                                          int one) {
+    __device__ __forceinline__ void fetch(const HeadsArgs &a, const HeadsVecArgs &v, const AX &ax,
+                                          const Unit &u, int one) {
         if (item < end) {
-            if (row == 0) start(a, v, one);
+            if (row == 0) start(a, v, ax, one);
             if (row < count) {
                 const uint32_t to = (uint32_t)__cvta_generic_to_shared(
                     mine + fill * (kVectors * kHeadsThreads));
@@ -747,10 +825,10 @@ template <class T, int KIND, bool GRAD> struct HeadsRing {
 // Norm and rotation of many rows: the ring's rows, a token's angles and weights
 // in registers over its item.  Three CTAs an SM (80 registers): [2,4096,40,128] bf16
 // 29.0 us, two 32.2; a CTA an item, without the ring, 32.3.
-template <class T, int KIND>
+template <class T, int KIND, class AX>
 __global__ void __launch_bounds__(kHeadsThreads, KIND == HEADS_ODD ? 2 : 3)
-k_heads_ring(const HeadsArgs a, const HeadsVecArgs v) {
-    using Ring = HeadsRing<T, KIND, false>;
+k_heads_ring(const HeadsArgs a, const HeadsVecArgs v, const AX ax) {
+    using Ring = HeadsRing<T, KIND, false, AX>;
     using Unit = HeadsUnit<T, KIND>;
     constexpr int N = Unit::N;
     extern __shared__ uint4 s_ring[];   // the ring, after it (HEADS_ODD) the groups' rows
@@ -770,23 +848,23 @@ k_heads_ring(const HeadsArgs a, const HeadsVecArgs v) {
     r.clear(u);
     layer_pdl_wait();
 #pragma unroll 1
-    for (int i = 0; i < Ring::kAhead; ++i) r.fetch(a, v, u, -1);
+    for (int i = 0; i < Ring::kAhead; ++i) r.fetch(a, v, ax, u, -1);
     const float inv = 1.0f / (float)a.dim;
     // every lane of a warp makes the same number of steps: the exchanges are warp-wide
     for (uint32_t base = blockIdx.x * per; base < r.total; base += r.step) {
-        const int64_t p = r.position;
+        const typename AX::At p = r.position;
         const int count = r.count;
         T *y = r.y;
         const int ysh = r.ysh;
-        if (count > 0 && p < 0 && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
+        if (count > 0 && p.out() && lane == 0) atomicOr(a.status, EBIN_DEVICE_POSITION_RANGE);
         float2 ca[N], cb[N], sa[N], nb[N];
-        u.template folded<true>(a, v, r.k, p < 0 ? 0 : p, ca, cb, sa, nb);
-        const bool out = __any_sync(0xFFFFFFFFu, p < 0);   // rare
+        u.template folded<true>(a, v, ax, r.k, p, ca, cb, sa, nb);
+        const bool out = __any_sync(0xFFFFFFFFu, p.out());   // rare
 #pragma unroll 1
         for (int h = 0; h < kRingHeads; ++h) {
             const uint4 *const in = r.take();
             const uint4 x0 = in[0], x1 = in[kHeadsThreads];
-            r.fetch(a, v, u, -1);
+            r.fetch(a, v, ax, u, -1);
             float2 va[N], vb[N];
             Unit::open(x0, x1, va, vb);
             if constexpr (Unit::ODD) {
@@ -805,7 +883,7 @@ k_heads_ring(const HeadsArgs a, const HeadsVecArgs v) {
             if constexpr (Unit::ODD) u.turn_odd(shared_row, a.half, rstd, va, vb, ca, cb, sa, nb);
             else u.turn(va, vb, ca, sa, nb, cb);
             if (out) {
-                if (p < 0) {
+                if (p.out()) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) va[i] = vb[i] = both(0.0f);
                 }
@@ -822,10 +900,10 @@ k_heads_ring(const HeadsArgs a, const HeadsVecArgs v) {
 // then join in shared memory and go to its row of the workspace.  118 registers,
 // two CTAs an SM, 98 KB of rows on their way to them: [2,4096,40,128] bf16 46.3 us;
 // with one row ahead in registers instead 60.1.
-template <class T, int KIND>
+template <class T, int KIND, class AX>
 __global__ void __launch_bounds__(kHeadsThreads, 2)
-k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
-    using Ring = HeadsRing<T, KIND, true>;
+k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v, const AX ax) {
+    using Ring = HeadsRing<T, KIND, true, AX>;
     using Unit = HeadsUnit<T, KIND>;
     constexpr int N = Unit::N;
     // the ring, after it the weights [lanes][2 V] and (HEADS_ODD) the groups' rows; at
@@ -854,7 +932,7 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     r.clear(u);
     layer_pdl_wait();
 #pragma unroll 1
-    for (int i = 0; i < Ring::kAhead; ++i) r.fetch(a, v, u, which);
+    for (int i = 0; i < Ring::kAhead; ++i) r.fetch(a, v, ax, u, which);
     if (threadIdx.x < lanes) {
         float2 wa[N], wb[N];
         u.weights(a, v, which, wa, wb);
@@ -870,15 +948,15 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
     const float inv = 1.0f / (float)a.dim;
     // every lane of a warp makes the same number of steps: the exchanges are warp-wide
     for (uint32_t base = cta * per; base < r.total; base += r.step) {
-        const int64_t p = r.position;
+        const typename AX::At p = r.position;
         const int count = r.count;
         T *y = r.y;
         const int ysh = r.ysh;
-        bad |= count > 0 && p < 0;
+        bad |= count > 0 && p.out();
         float2 c[N], sn[N], cb[N], sb[N];
-        if constexpr (Unit::ODD) u.factors(a, p < 0 ? 0 : p, -1.0f, c, cb, sn, sb);
-        else u.table(a, v, p < 0 ? 0 : p, c, sn);
-        const bool out = __any_sync(0xFFFFFFFFu, p < 0);   // rare
+        if constexpr (Unit::ODD) u.factors(a, ax, p, -1.0f, c, cb, sn, sb);
+        else u.table(a, v, ax, p, c, sn);
+        const bool out = __any_sync(0xFFFFFFFFu, p.out());   // rare
 #pragma unroll 1
         for (int h = 0; h < kRingHeads; ++h) {
             const uint4 *const in = r.take();
@@ -893,7 +971,7 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
                     __syncwarp();
                 }
             }
-            r.fetch(a, v, u, which);
+            r.fetch(a, v, ax, u, which);
             if constexpr (Unit::ODD) u.turn_odd(shared_row, a.half, 1.0f, ga, gb, c, cb, sn, sb);
             else u.turn_back(ga, gb, c, sn);
             float ss = u.squares(xa, xb);
@@ -914,7 +992,7 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
             }
             const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
             const float2 mean = both(-gx * rstd * inv), r2 = both(rstd);
-            const bool live = h < count, use = live && p >= 0;
+            const bool live = h < count, use = live && !p.out();
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 xa[i] = __fmul2_rn(xa[i], r2);
@@ -927,7 +1005,7 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v) {
                 gb[i] = __fmul2_rn(__ffma2_rn(xb[i], mean, wb[i]), r2);
             }
             if (out) {
-                if (p < 0) {
+                if (p.out()) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) ga[i] = gb[i] = both(0.0f);
                 }

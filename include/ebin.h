@@ -557,7 +557,11 @@ ebin_status ebin_noalloc_read_status(int status_slot, void *stream, uint32_t *bi
  *
  * Arithmetic is binary32, with one rounding to the element type at the end.
  */
-typedef enum ebin_norm { EBIN_NORM_NONE = 0, EBIN_NORM_RMS = 1 } ebin_norm;
+typedef enum ebin_norm {
+    EBIN_NORM_NONE = 0,
+    EBIN_NORM_RMS = 1,
+    EBIN_NORM_LAYER = 2   /* the norms around a block only */
+} ebin_norm;
 typedef enum ebin_rotary_layout {
     EBIN_ROTARY_HALF = 0,
     EBIN_ROTARY_INTERLEAVED = 1
@@ -603,6 +607,35 @@ typedef struct ebin_rotary_attrs {
  */
 ebin_status ebin_rotary_table(const ebin_rotary_attrs *attrs, int64_t first_position,
                               int64_t positions, float *cos, float *sin, void *stream);
+
+/*
+ * The axes of a token of an image or a video (time, row, column): each pair of
+ * a head belongs to one of them and turns by that axis' position.
+ *   count      1 .. 4
+ *   order      BLOCKS: the first sections[0] pairs are axis 0's, the next sections[1]
+ *              axis 1's and so on; DEALT: pair by pair in turn to the axes that
+ *              have pairs left
+ *   sections   pairs of each axis, >= 0, rotary_dim / 2 together (at most 512)
+ *   position_stride   elements between the positions of a token's axes
+ */
+typedef enum ebin_axes_order { EBIN_AXES_BLOCKS = 0, EBIN_AXES_DEALT = 1 } ebin_axes_order;
+typedef struct ebin_rotary_axes {
+    int32_t count;
+    int32_t order;
+    int32_t sections[4];
+    int64_t position_stride;
+} ebin_rotary_axes;
+
+/*
+ * ebin_rotary_table with frequencies of each axis' own: column j, pair i of an
+ * axis of s pairs, has base^(-i/s).  (Where all axes share one row of
+ * frequencies, ebin_rotary_table's tables are the ones to give.)  BASE scaling
+ * and axes that do not make up rotary_dim / 2 pairs are INVALID_ATTR;
+ * position_stride is not read.
+ */
+ebin_status ebin_rotary_table_axes(const ebin_rotary_attrs *attrs, const ebin_rotary_axes *axes,
+                                   int64_t first_position, int64_t positions, float *cos,
+                                   float *sin, void *stream);
 
 /* Element strides of a [batch, tokens, heads, head_dim] view (the last is 1). */
 typedef struct ebin_heads_view {
@@ -654,6 +687,20 @@ typedef struct ebin_heads_plan_s *ebin_heads_plan_t;
  * UNSUPPORTED_TYPE.
  */
 ebin_status ebin_heads_plan_create(const ebin_heads_attrs *attrs, ebin_heads_plan_t *out);
+
+/*
+ * A plan whose positions have axes: with x the axis of pair j, that pair of a
+ * token at positions p is turned by cos[p[x], j] and sin[p[x], j].  The positions
+ * are a device array of position_type (not 0) with element strides
+ * axes->position_stride (axis) and position_strides (batch, token); those of an
+ * axis without pairs are not read, and a token with another outside the tables is
+ * treated as one whose only position is.  Run with ebin_heads_execute and
+ * ebin_heads_grad_execute.
+ * Errors: as ebin_heads_plan_create; INVALID_ATTR (axes, no position_type),
+ * INVALID_ARG (axes NULL, its stride, table_positions above 2^31 - 1).
+ */
+ebin_status ebin_heads_plan_create_axes(const ebin_heads_attrs *attrs,
+                                        const ebin_rotary_axes *axes, ebin_heads_plan_t *out);
 
 /* Bytes of device workspace the plan's execution needs (0 but for the norm gradient). */
 ebin_status ebin_heads_plan_workspace(ebin_heads_plan_t plan, size_t *bytes);
@@ -816,6 +863,204 @@ void ebin_epilogue_grad_plan_release(ebin_epilogue_grad_plan_t plan);
 ebin_status ebin_epilogue_grad_execute(ebin_epilogue_grad_plan_t plan, const void *dy,
                                        const void *z, void *dz, float *dbias, void *workspace,
                                        size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ dropout
+ *
+ * y = residual + keep(x + bias) / (1 - p), the mask formed where it is used and
+ * never stored: a gradient call with the same numbers forms it anew.  No
+ * counterpart in the pages.
+ *
+ * Element (row, col) draws word col % 4 of a Philox4x32-10 block (Salmon,
+ * Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011)
+ * with key (seed, seed >> 32) and counter (col / 4, row, offset, offset >> 32);
+ * it is dropped when the word lies below L = round(p 2^32), and what is kept is
+ * divided by 1 - L / 2^32.  Calls that are to draw apart take different
+ * offsets (or seeds).  A dropped element adds exactly 0, whatever x holds.
+ * Arithmetic is binary32, with one rounding to the element type.
+ */
+
+/*
+ *   dtype         of x, residual, y and the gradients: FLOAT32, FLOAT16, BFLOAT16
+ *   dtype_bias    of the bias [n]: dtype or FLOAT32 (read with has_bias only)
+ *   has_bias      forward: whether execution reads a bias; gradient: whether dbias is wanted
+ *   has_residual  forward only
+ *   gradient      0: ebin_dropout_execute, 1: ebin_dropout_grad_execute
+ *   p             0 <= p < 1 (and L below 2^32)
+ *   rows, n       0 .. 2^30
+ *   ld_x ..       element strides between rows (0 = dense); ld_x is dy's, ld_y dx's in a gradient
+ */
+typedef struct ebin_dropout_attrs {
+    ebin_dtype dtype;
+    ebin_dtype dtype_bias;
+    int32_t has_bias;
+    int32_t has_residual;
+    int32_t gradient;
+    double p;
+    int64_t rows, n;
+    int64_t ld_x, ld_residual, ld_y;
+} ebin_dropout_attrs;
+
+typedef struct ebin_dropout_plan_s *ebin_dropout_plan_t;
+
+/* As the ebin_gemm_plan_ functions, with their errors (p: INVALID_ATTR). */
+ebin_status ebin_dropout_plan_create(const ebin_dropout_attrs *attrs, ebin_dropout_plan_t *out);
+ebin_status ebin_dropout_plan_workspace(ebin_dropout_plan_t plan, size_t *bytes);
+void ebin_dropout_plan_release(ebin_dropout_plan_t plan);
+
+/*
+ * Run a forward plan on device buffers, enqueued on `stream`.  y may be x or
+ * the residual itself (same pointer and stride); any other overlap of y with
+ * an input is ALIAS.  offset_device: NULL, or a device word that is added to
+ * offset when the kernel runs, so that a captured graph whose program advances
+ * the word draws anew with each replay.
+ * Errors: INVALID_ARG (a NULL buffer with work to do, a gradient plan), ALIAS, CUDA.
+ */
+ebin_status ebin_dropout_execute(ebin_dropout_plan_t plan, const void *x, const void *bias,
+                                 const void *residual, void *y, uint64_t seed, uint64_t offset,
+                                 const uint64_t *offset_device, void *stream);
+
+/*
+ * The gradient: dx = keep(dy) / (1 - p) with the forward call's seed, offset
+ * and word (the residual's gradient is dy itself), and dbias [n] binary32, the
+ * sum over rows of dx before its rounding, in an order fixed by the plan and
+ * the device.  dx may be dy itself.  workspace: at least
+ * ebin_dropout_plan_workspace bytes, 16-byte aligned, not shared with work in
+ * flight on another stream (NULL where that is 0).  With rows = 0 dbias is
+ * zeroed.  Errors: as ebin_dropout_execute.
+ */
+ebin_status ebin_dropout_grad_execute(ebin_dropout_plan_t plan, const void *dy, void *dx,
+                                      float *dbias, void *workspace, size_t workspace_bytes,
+                                      uint64_t seed, uint64_t offset,
+                                      const uint64_t *offset_device, void *stream);
+
+/* ------------------------------------------------------------------ norms around a block
+ *
+ * What lies between the output y of one block (attention, feed-forward) and the
+ * input z of the next, over rows of n elements, in one pass:
+ *     v = N_post(y) w_post + b_post
+ *     h = stream_scale x + branch_scale gate keep(v) / (1 - p)
+ *     z = (N_pre(h) w_pre + b_pre) (1 + scale) + shift
+ * x is the residual stream and h its new state; keep is ebin_dropout_execute's,
+ * with the same numbers.  N is
+ *     NONE    N(t) = t
+ *     RMS     N(t) = t / sqrt(mean(t^2) + epsilon)
+ *     LAYER   N(t) = (t - mean(t)) / sqrt(mean((t - mean(t))^2) + epsilon)
+ * over a row.  No counterpart in the pages.
+ *
+ * gate, scale and shift are one row for all rows, or one for each group of
+ * consecutive rows (the condition of a sequence of a batch).  Weights, biases,
+ * gate, scale and shift may each be NULL: 1, 0, 1, 0 and 0.
+ * Arithmetic is binary32, with one rounding to the element type at the end: N_pre
+ * reads h before it is rounded.
+ */
+
+/*
+ *   dtype            of y, z and their gradients: FLOAT32, FLOAT16, BFLOAT16
+ *   dtype_stream     of x, h and their gradients: dtype or FLOAT32
+ *   dtype_w          of the norms' weights and biases [n]: dtype or FLOAT32
+ *   dtype_mod        of gate, scale and shift: dtype or FLOAT32
+ *   post, pre        ebin_norm; pre = NONE: there is no z
+ *   has_branch       0: there is no y, h = stream_scale x (post is NONE, p is 0)
+ *   gradient         0: ebin_block_norm_execute, 1: ebin_block_norm_grad_execute
+ *   epsilon_post/pre >= 0
+ *   stream_scale, branch_scale   finite
+ *   p                as in ebin_dropout_attrs
+ *   rows             0 .. 2^30
+ *   n                0 .. 2^24
+ *   gate_rows        0: gate is one row [n]; else gate is [rows / gate_rows, n], gate_rows divides
+ *                    rows
+ *   mod_rows         the same of scale and shift; equal to gate_rows unless one of them is 0
+ *   ld_x ..          element strides between rows (0 = dense)
+ */
+typedef struct ebin_block_norm_attrs {
+    ebin_dtype dtype, dtype_stream, dtype_w, dtype_mod;
+    int32_t post, pre;
+    int32_t has_branch;
+    int32_t gradient;
+    float epsilon_post, epsilon_pre;
+    float stream_scale, branch_scale;
+    double p;
+    int64_t rows, n;
+    int64_t gate_rows, mod_rows;
+    int64_t ld_x, ld_y, ld_h, ld_z;
+    int64_t ld_gate, ld_scale, ld_shift;
+    int64_t ld_dz, ld_dh, ld_dx, ld_dy;
+} ebin_block_norm_attrs;
+
+typedef struct ebin_block_norm_plan_s *ebin_block_norm_plan_t;
+
+/*
+ * Check the attributes and build a plan (immutable, usable from any thread
+ * and stream; the caller owns it).  Errors: INVALID_ARG (NULL, sizes, groups
+ * that do not divide the rows, a row stride below the row or an extent of 2^60
+ * elements), INVALID_ATTR (norms, flags, epsilons, scales, p), UNSUPPORTED_TYPE.
+ */
+ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *attrs,
+                                        ebin_block_norm_plan_t *out);
+
+/* Bytes of device workspace that execution needs (0 but for a gradient). */
+ebin_status ebin_block_norm_plan_workspace(ebin_block_norm_plan_t plan, size_t *bytes);
+
+/* Free a plan; work already enqueued is not affected.  NULL is ignored. */
+void ebin_block_norm_plan_release(ebin_block_norm_plan_t plan);
+
+/* The operands that may be left out (NULL), on the device. */
+typedef struct ebin_block_norm_params {
+    const void *gate, *w_post, *b_post, *w_pre, *b_pre, *scale, *shift;
+    uint64_t seed, offset;
+    const uint64_t *offset_device;   /* as ebin_dropout_execute; read with p > 0 only */
+} ebin_block_norm_params;
+
+/*
+ * Run a forward plan on device buffers, enqueued on `stream`.
+ *   x, y       y is not read without a branch
+ *   params     NULL: none of them
+ *   h          [rows, n], or NULL: not wanted
+ *   z          [rows, n], or NULL: not wanted (it is not written with pre = NONE)
+ * An output may be an input of its own type (the same pointer and row stride);
+ * any other overlap with an output is ALIAS.
+ * Errors: INVALID_ARG (a NULL buffer with work to do, a buffer off its element's
+ * boundary, a gradient plan, a gate without a branch), ALIAS, CUDA.
+ */
+ebin_status ebin_block_norm_execute(ebin_block_norm_plan_t plan, const void *x, const void *y,
+                                    const ebin_block_norm_params *params, void *h, void *z,
+                                    void *stream);
+
+/* The gradients of the parameters, binary32, overwritten; NULL: not wanted.  Those of
+ * gate, scale and shift are [groups, n] or [n], dense, as these are. */
+typedef struct ebin_block_norm_grads {
+    float *gate, *w_post, *b_post, *w_pre, *b_pre, *scale, *shift;
+} ebin_block_norm_grads;
+
+/*
+ * The gradient, for the incoming gradients dz and dh of z and h (dh NULL: 0), the
+ * held h and y and the forward call's parameters.  With hh = N_pre(h) and r its
+ * 1 / sqrt, yh and s those of y (all recomputed, nothing is kept from the
+ * forward pass), and the means over a row (those of a LAYER norm in brackets):
+ *     m = dz (1 + scale) w_pre,   D = dh + r (m - [mean(m)] - hh mean(m hh))
+ *     dx = stream_scale D,        e = branch_scale keep(D) / (1 - p)
+ *     u = e gate w_post,          dy = s (u - [mean(u)] - yh mean(u yh))
+ *     dgate = sum e v,  dw_post = sum e gate yh,  db_post = sum e gate
+ *     dscale = sum dz (hh w_pre + b_pre),  dshift = sum dz
+ *     dw_pre = sum dz (1 + scale) hh,      db_pre = sum dz (1 + scale)
+ * the sums over the rows of a group or over all rows, in an order fixed by the
+ * plan and the device, so the same inputs give the same bits.
+ *   dz, h      not read with pre = NONE
+ *   y          read with post, or where dgate is wanted
+ *   dx, dy     NULL: not wanted; either may be an input of its own type (the same
+ *              pointer and row stride), any other overlap is ALIAS
+ *   shift      in params is not read
+ *   workspace  at least ebin_block_norm_plan_workspace bytes, 16-byte aligned, not
+ *              shared with work in flight on another stream; not read (may be NULL)
+ *              where no gradient of a parameter is wanted
+ * With rows = 0 the wanted gradients of the parameters are zeroed.
+ * Errors: as ebin_block_norm_execute.
+ */
+ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan, const void *dz,
+                                         const void *dh, const void *h, const void *y,
+                                         const ebin_block_norm_params *params, void *dx, void *dy,
+                                         const ebin_block_norm_grads *grads, void *workspace,
+                                         size_t workspace_bytes, void *stream);
 
 /* Kernels this library has launched in this process (for launch accounting). */
 uint64_t ebin_launch_count(void);
