@@ -92,6 +92,11 @@ def _jobs():
         obj = os.path.join(OBJDIR, "ebin_gemm_tc_%d.o" % dt)
         jobs.append((obj, [tc_src] + heads,
                      [nvcc, *ARCH, *LAYER_FLAGS, "-DEBIN_DT=%d" % dt, "-c", tc_src, "-o", obj]))
+    rows_src = os.path.join(CSRC, "ebin_block_rows.cu")
+    for dt in range(5):     # pairs of element types
+        obj = os.path.join(OBJDIR, "ebin_block_rows_%d.o" % dt)
+        jobs.append((obj, [rows_src] + heads,
+                     [nvcc, *ARCH, *LAYER_FLAGS, "-DEBIN_DT=%d" % dt, "-c", rows_src, "-o", obj]))
     for g in GROUPS:
         src = os.path.join(CSRC, "k_%s.cu" % g)
         for dt in range(N_DT):

@@ -236,4 +236,18 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
     }
 }
 
+// The row kernels of a pair of types (0: float32, 1: float16, 2: bfloat16; 3, 4: these
+// two beside a float32 stream; ebin_block_rows.cu).  done: whether they take
+// rows of this width.
+#define EBIN_DECLARE_ROWS(dt)                                                                \
+    cudaError_t launch_block_rows_##dt(const BlockArgs &, bool vec, bool *done, cudaStream_t); \
+    cudaError_t launch_block_rows_grad_##dt(const BlockArgs &, int64_t units, bool vec,         \
+                                            bool *done, cudaStream_t);
+EBIN_DECLARE_ROWS(0)
+EBIN_DECLARE_ROWS(1)
+EBIN_DECLARE_ROWS(2)
+EBIN_DECLARE_ROWS(3)
+EBIN_DECLARE_ROWS(4)
+#undef EBIN_DECLARE_ROWS
+
 }  // namespace ebin

@@ -221,8 +221,26 @@ cudaError_t launch_sums(void (*kernel)(const BlockSumsArgs), int64_t grid, const
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// Whether every buffer of a call lies on vectors: rows that are whole vectors, each
+// starting on 16 bytes.
+bool block_vectors(const ebin_block_norm_plan_s &p, const BlockArgs &a) {
+    const int64_t V = p.ssz == 4 ? 4 : 8;   // columns of a vector
+    if (a.n % V) return false;
+    const void *all[13] = {a.x, a.y, a.dz, a.dh, a.h, a.z, a.gate, a.w_post, a.b_post, a.w_pre,
+                           a.b_pre, a.scale, a.shift};
+    for (const void *q : all)
+        if ((uintptr_t)q % 16) return false;
+    if (a.rows == 1) return true;
+    const struct { const void *p; int64_t ld; } rows[9] = {
+        {a.x, a.ld_x}, {a.y, a.ld_y}, {a.dz, a.ld_dz}, {a.dh, a.ld_dh}, {a.h, a.ld_h},
+        {a.z, a.ld_z}, {a.gate, a.ld_gate}, {a.scale, a.ld_scale}, {a.shift, a.ld_shift}};
+    for (const auto &r : rows)
+        if (r.p && r.ld % V) return false;
+    return true;
+}
+
 template <class T, class S>
-cudaError_t launch_block_types(const BlockArgs &a, bool grad, int64_t units, cudaStream_t s) {
+cudaError_t launch_block_any(const BlockArgs &a, bool grad, int64_t units, cudaStream_t s) {
     if (grad)
         return launch_layer(k_block_any_grad<T, S>, dim3((unsigned)units), kBlockAnyThreads, 0, s,
                             1, a);
@@ -233,19 +251,29 @@ cudaError_t launch_block_types(const BlockArgs &a, bool grad, int64_t units, cud
 cudaError_t launch_block(const ebin_block_norm_plan_s &p, const BlockArgs &a, bool grad,
                          cudaStream_t s) {
     const int64_t units = p.groups * p.parts;
-    const bool wide = p.at.dtype_stream == EBIN_FLOAT32;
-    if (p.at.dtype == EBIN_FLOAT32) return launch_block_types<float, float>(a, grad, units, s);
-    if (p.at.dtype == EBIN_FLOAT16)
-        return wide ? launch_block_types<__half, float>(a, grad, units, s)
-                    : launch_block_types<__half, __half>(a, grad, units, s);
-    return wide ? launch_block_types<__nv_bfloat16, float>(a, grad, units, s)
-                : launch_block_types<__nv_bfloat16, __nv_bfloat16>(a, grad, units, s);
+    const bool wide = p.ssz == 4, vec = block_vectors(p, a);
+    bool done = false;
+    cudaError_t e;
+#define EBIN_ROWS(dt, T, S)                                                                 \
+    e = grad ? launch_block_rows_grad_##dt(a, units, vec, &done, s)                          \
+             : launch_block_rows_##dt(a, vec, &done, s);                                     \
+    return done ? e : launch_block_any<T, S>(a, grad, units, s)
+    if (p.at.dtype == EBIN_FLOAT32) { EBIN_ROWS(0, float, float); }
+    if (p.at.dtype == EBIN_FLOAT16) {
+        if (wide) { EBIN_ROWS(3, __half, float); }
+        EBIN_ROWS(1, __half, __half);
+    }
+    if (wide) { EBIN_ROWS(4, __nv_bfloat16, float); }
+    EBIN_ROWS(2, __nv_bfloat16, __nv_bfloat16);
+#undef EBIN_ROWS
 }
 
-// Parts of a group's rows: about two units to each of 152 SMs over all groups, each
-// with a row at least, and no more than 2^28 sums in the workspace where that leaves one.
+// Parts of a group's rows: as many units over all groups as 152 SMs hold teams of the
+// row kernel at 128 registers (a warp for two chunks of 256 columns), each with a
+// row at least, and no more than 2^28 sums in the workspace where that leaves one.
 int64_t block_parts(int64_t groups, int64_t group_rows, int64_t n) {
-    const int64_t want = div_up(2 * 152, groups);
+    const int64_t warps = std::max<int64_t>(1, div_up(n, 512));
+    const int64_t want = div_up(152 * std::max<int64_t>(1, 16 / warps), groups);
     const int64_t room = (int64_t(1) << 26) / (groups * std::max<int64_t>(n, 1));
     return std::max<int64_t>(1, std::min<int64_t>({want, group_rows, room}));
 }

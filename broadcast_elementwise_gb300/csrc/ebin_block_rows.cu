@@ -1,0 +1,132 @@
+// The row kernels of the norms around a block, one pair of element types in each
+// compilation (-DEBIN_DT=0 .. 4).
+#include "ebin_block_rows.cuh"
+
+namespace ebin {
+
+#if EBIN_DT == 0
+using T = float;
+using S = float;
+#elif EBIN_DT == 1
+using T = __half;
+using S = __half;
+#elif EBIN_DT == 2
+using T = __nv_bfloat16;
+using S = __nv_bfloat16;
+#elif EBIN_DT == 3
+using T = __half;
+using S = float;
+#else
+using T = __nv_bfloat16;
+using S = float;
+#endif
+
+namespace {
+
+// Shared memory of an SM, what a CTA takes of it besides its rows, and the most
+// that a CTA's rows may take.
+constexpr size_t kSmSmem = 228 * 1024, kCtaSmem = 3 * 1024, kRowsSmem = 224 * 1024;
+
+template <auto KERNEL>
+cudaError_t launch_rows(const BlockArgs &a, const RowsGeom &g, int64_t grid, size_t smem,
+                        cudaStream_t s) {
+    const cudaError_t e = allow_smem<KERNEL>(kRowsSmem);
+    if (e != cudaSuccess) return e;
+    return launch_layer(KERNEL, dim3((unsigned)grid), g.warps * g.teams * 32, smem, s, 1, a, g);
+}
+
+// Rows in flight: as many as `most` where the CTAs that an SM holds by their
+// threads leave room; 0: not even one fits.
+int rows_slots(size_t row_bytes, int ctas, int most) {
+    int slots = (int)((kSmSmem / ctas - kCtaSmem) / row_bytes);
+    if (slots < 1 && row_bytes <= kRowsSmem) slots = 1;
+    return std::min(slots, most);
+}
+
+}  // namespace
+
+#define EBIN_CAT(a, b) a##b
+#define EBIN_NAME(f, dt) EBIN_CAT(f, dt)
+
+cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec, bool *done,
+                                                   cudaStream_t s) {
+    *done = false;
+    const int chunks = (int)div_up(a.n, kChunk);
+    if (chunks > 128) return cudaSuccess;
+    RowsGeom g{};
+    // few rows: a warp for each chunk; many: two chunks
+    const int vpt = chunks > 32 ? 4 : a.rows <= 304 ? 1 : 2;
+    g.warps = (int)div_up(chunks, vpt);
+    g.teams = g.warps == 1 ? 4 : 1;
+    g.gate = fast_div((uint32_t)a.gate_rows);
+    g.mod = fast_div((uint32_t)a.mod_rows);
+    const int threads = g.warps * g.teams * 32;
+    const int per_sm = std::min(1024 / threads, 16);
+    size_t smem = 0;
+    if (vec) {
+        const size_t row = (size_t)threads * vpt * 16 *
+            ((sizeof(S) == 4 ? 2 : 1) + (sizeof(T) == 4 ? 2 : 1));
+        g.slots = rows_slots(row, per_sm, 3);
+        if (g.slots < 1) return cudaSuccess;
+        smem = g.slots * row;
+    } else {
+        g.slots = 1;
+    }
+    const int64_t grid = std::min<int64_t>(div_up(a.rows, g.teams),
+                                           (int64_t)per_sm * current_sm_count());
+    *done = true;
+    if (vpt == 1)
+        return vec ? launch_rows<k_block_rows<T, S, 1, true>>(a, g, grid, smem, s)
+                   : launch_rows<k_block_rows<T, S, 1, false>>(a, g, grid, smem, s);
+    if (vpt == 2)
+        return vec ? launch_rows<k_block_rows<T, S, 2, true>>(a, g, grid, smem, s)
+                   : launch_rows<k_block_rows<T, S, 2, false>>(a, g, grid, smem, s);
+    return vec ? launch_rows<k_block_rows<T, S, 4, true>>(a, g, grid, smem, s)
+               : launch_rows<k_block_rows<T, S, 4, false>>(a, g, grid, smem, s);
+}
+
+cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, int64_t units,
+                                                        bool vec, bool *done, cudaStream_t s) {
+    *done = false;
+    const int chunks = (int)div_up(a.n, kChunk);
+    if (chunks > 64) return cudaSuccess;
+    RowsGeom g{};
+    const int vpt = chunks > 32 ? 4 : 2;
+    g.warps = (int)div_up(chunks, vpt);
+    g.teams = g.warps == 1 ? 4 : 1;
+    g.units = units;
+    g.gate = fast_div((uint32_t)a.gate_rows);
+    g.mod = fast_div((uint32_t)a.mod_rows);
+    const int threads = g.warps * g.teams * 32;
+    size_t smem = 0;
+    g.slots = 1;
+    if (vec) {
+        const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
+        const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};
+        for (int k = 0; k < 4; ++k) {
+            g.at[k] = g.vectors;
+            if (there[k]) g.vectors += vpt * (k % 2 ? t_vectors : s_vectors);
+        }
+        const size_t row = (size_t)threads * 16 * g.vectors;
+        if (row > 0) {
+            g.slots = rows_slots(row, std::min(std::max(1, 512 / threads), 16), 3);
+            if (g.slots < 1) return cudaSuccess;
+        }
+        smem = g.slots * row;
+    }
+    const int64_t grid = div_up(units, g.teams);
+    *done = true;
+    if (vpt == 4)
+        return vec ? launch_rows<k_block_rows_grad<T, S, 4, true, true, true>>(a, g, grid, smem, s)
+                   : launch_rows<k_block_rows_grad<T, S, 4, false, true, true>>(a, g, grid, smem,
+                                                                               s);
+    const bool all = a.need >> SUM_DZ & 1 || a.need >> SUM_E & 1;
+    if (all)
+        return vec ? launch_rows<k_block_rows_grad<T, S, 2, true, true, false>>(a, g, grid, smem, s)
+                   : launch_rows<k_block_rows_grad<T, S, 2, false, true, false>>(a, g, grid, smem,
+                                                                                s);
+    return vec ? launch_rows<k_block_rows_grad<T, S, 2, true, false, false>>(a, g, grid, smem, s)
+               : launch_rows<k_block_rows_grad<T, S, 2, false, false, false>>(a, g, grid, smem, s);
+}
+
+}  // namespace ebin
