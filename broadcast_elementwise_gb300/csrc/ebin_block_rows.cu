@@ -35,12 +35,25 @@ cudaError_t launch_rows(const BlockArgs &a, const RowsGeom &g, int64_t grid, siz
     return launch_layer(KERNEL, dim3((unsigned)grid), g.warps * g.teams * 32, smem, s, 1, a, g);
 }
 
-// Rows in flight: as many as `most` where the CTAs that an SM holds by their
-// threads leave room; 0: not even one fits.
-int rows_slots(size_t row_bytes, int ctas, int most) {
-    int slots = (int)((kSmSmem / ctas - kCtaSmem) / row_bytes);
-    if (slots < 1 && row_bytes <= kRowsSmem) slots = 1;
-    return std::min(slots, most);
+// Rows in flight: up to three, where the CTAs that an SM holds by their threads
+// leave room beside `more` bytes; 0: not even one fits.
+int rows_slots(size_t row_bytes, size_t more, int ctas) {
+    const size_t share = kSmSmem / ctas - kCtaSmem;
+    int slots = share > more ? (int)((share - more) / row_bytes) : 0;
+    if (slots < 1 && row_bytes + more <= kRowsSmem) slots = 1;
+    return std::min(slots, 3);
+}
+
+RowsGeom rows_geom(const BlockArgs &a, int chunks, int vpt) {
+    RowsGeom g{};
+    g.warps = (int)div_up(chunks, vpt);
+    g.joins = 1;
+    while (g.joins < g.warps) g.joins *= 2;
+    g.teams = g.warps == 1 ? 4 : 1;
+    g.slots = 1;
+    g.gate = fast_div((uint32_t)a.gate_rows);
+    g.mod = fast_div((uint32_t)a.mod_rows);
+    return g;
 }
 
 }  // namespace
@@ -53,36 +66,31 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
     *done = false;
     const int chunks = (int)div_up(a.n, kChunk);
     if (chunks > 128) return cudaSuccess;
-    RowsGeom g{};
     // few rows: a warp for each chunk; many: two chunks
     const int vpt = chunks > 32 ? 4 : a.rows <= 304 ? 1 : 2;
-    g.warps = (int)div_up(chunks, vpt);
-    g.teams = g.warps == 1 ? 4 : 1;
-    g.gate = fast_div((uint32_t)a.gate_rows);
-    g.mod = fast_div((uint32_t)a.mod_rows);
+    RowsGeom g = rows_geom(a, chunks, vpt);
     const int threads = g.warps * g.teams * 32;
     const int per_sm = std::min(1024 / threads, 16);
     size_t smem = 0;
     if (vec) {
         const size_t row = (size_t)threads * vpt * 16 *
             ((sizeof(S) == 4 ? 2 : 1) + (sizeof(T) == 4 ? 2 : 1));
-        g.slots = rows_slots(row, per_sm, 3);
+        g.slots = rows_slots(row, 0, per_sm);
         if (g.slots < 1) return cudaSuccess;
         smem = g.slots * row;
-    } else {
-        g.slots = 1;
     }
     const int64_t grid = std::min<int64_t>(div_up(a.rows, g.teams),
                                            (int64_t)per_sm * current_sm_count());
     *done = true;
-    if (vpt == 1)
-        return vec ? launch_rows<k_block_rows<T, S, 1, true>>(a, g, grid, smem, s)
-                   : launch_rows<k_block_rows<T, S, 1, false>>(a, g, grid, smem, s);
-    if (vpt == 2)
-        return vec ? launch_rows<k_block_rows<T, S, 2, true>>(a, g, grid, smem, s)
-                   : launch_rows<k_block_rows<T, S, 2, false>>(a, g, grid, smem, s);
-    return vec ? launch_rows<k_block_rows<T, S, 4, true>>(a, g, grid, smem, s)
-               : launch_rows<k_block_rows<T, S, 4, false>>(a, g, grid, smem, s);
+    const bool layer = a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
+#define EBIN_ROWS(VPT)                                                                       \
+    if (!vec) return launch_rows<k_block_rows<T, S, VPT, false, true>>(a, g, grid, smem, s);  \
+    return layer ? launch_rows<k_block_rows<T, S, VPT, true, true>>(a, g, grid, smem, s)      \
+                 : launch_rows<k_block_rows<T, S, VPT, true, false>>(a, g, grid, smem, s)
+    if (vpt == 1) { EBIN_ROWS(1); }
+    if (vpt == 2) { EBIN_ROWS(2); }
+    EBIN_ROWS(4);
+#undef EBIN_ROWS
 }
 
 cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, int64_t units,
@@ -90,16 +98,18 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, int6
     *done = false;
     const int chunks = (int)div_up(a.n, kChunk);
     if (chunks > 64) return cudaSuccess;
-    RowsGeom g{};
     const int vpt = chunks > 32 ? 4 : 2;
-    g.warps = (int)div_up(chunks, vpt);
-    g.teams = g.warps == 1 ? 4 : 1;
+    RowsGeom g = rows_geom(a, chunks, vpt);
     g.units = units;
-    g.gate = fast_div((uint32_t)a.gate_rows);
-    g.mod = fast_div((uint32_t)a.mod_rows);
     const int threads = g.warps * g.teams * 32;
-    size_t smem = 0;
-    g.slots = 1;
+    const bool has[2] = {a.scale || a.w_pre,
+                         a.gate || a.w_post || a.branch_scale != 1.0f || a.drop.least};
+    for (int f = 0; f < 2; ++f) {
+        g.factor[f] = has[f] ? g.factors : -1;
+        if (has[f]) g.factors += 2 * vpt;
+    }
+    const size_t factors = (size_t)threads * 16 * g.factors;
+    size_t smem = factors;
     if (vec) {
         const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
         const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};
@@ -109,10 +119,10 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, int6
         }
         const size_t row = (size_t)threads * 16 * g.vectors;
         if (row > 0) {
-            g.slots = rows_slots(row, std::min(std::max(1, 512 / threads), 16), 3);
+            g.slots = rows_slots(row, factors, std::min(std::max(1, 512 / threads), 16));
             if (g.slots < 1) return cudaSuccess;
         }
-        smem = g.slots * row;
+        smem += g.slots * row;
     }
     const int64_t grid = div_up(units, g.teams);
     *done = true;
@@ -120,13 +130,11 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, int6
         return vec ? launch_rows<k_block_rows_grad<T, S, 4, true, true, true>>(a, g, grid, smem, s)
                    : launch_rows<k_block_rows_grad<T, S, 4, false, true, true>>(a, g, grid, smem,
                                                                                s);
-    const bool all = a.need >> SUM_DZ & 1 || a.need >> SUM_E & 1;
-    if (all)
-        return vec ? launch_rows<k_block_rows_grad<T, S, 2, true, true, false>>(a, g, grid, smem, s)
-                   : launch_rows<k_block_rows_grad<T, S, 2, false, true, false>>(a, g, grid, smem,
-                                                                                s);
-    return vec ? launch_rows<k_block_rows_grad<T, S, 2, true, false, false>>(a, g, grid, smem, s)
-               : launch_rows<k_block_rows_grad<T, S, 2, false, false, false>>(a, g, grid, smem, s);
+    const bool full = a.need >> SUM_DZ & 1 || a.need >> SUM_E & 1 ||
+                      a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
+    if (!vec) return launch_rows<k_block_rows_grad<T, S, 2, false, true, false>>(a, g, grid, smem, s);
+    return full ? launch_rows<k_block_rows_grad<T, S, 2, true, true, false>>(a, g, grid, smem, s)
+                : launch_rows<k_block_rows_grad<T, S, 2, true, false, false>>(a, g, grid, smem, s);
 }
 
 }  // namespace ebin
