@@ -7,6 +7,14 @@
 
 namespace ebin {
 
+// The rows of a group in `parts` parts of `rows`.
+struct BlockUnits {
+    int64_t parts = 1, rows = 0;
+};
+
+// Chunks of 256 columns that a lane of the kernels of CTAs' units owns.
+constexpr int kUnitVpt = 4, kUnitGradVpt = 2;
+
 struct BlockArgs {
     // forward: x, y -> h, z; gradient: dz, dh, h, y -> dx, dy
     const void *x, *y, *dz, *dh;   // x: the gradient's h
@@ -21,8 +29,8 @@ struct BlockArgs {
     int32_t post, pre;             // ebin_norm
     int32_t w_f32, mod_f32;
     DropArgs drop;
-    // A gradient's units: the rows of a group in `parts` parts of `unit_rows`.
-    int64_t parts, unit_rows, group_rows;
+    BlockUnits cta, team;          // units of a CTA, of a team
+    int64_t groups, group_rows;
     float *partial;                // [units][4][n]: sums of dz hh, dz, e yh, e; or null
     int32_t need;                  // which of the four, by bit
 };
@@ -157,9 +165,9 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
     layer_pdl_launch();
     layer_pdl_wait();
     const uint2 offset = drop_offset(a.drop);
-    const int64_t group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
-    const int64_t r0 = group * a.group_rows + part * a.unit_rows;
-    const int64_t r1 = min(r0 + a.unit_rows, (group + 1) * a.group_rows);
+    const int64_t group = blockIdx.x / a.team.parts, part = blockIdx.x - group * a.team.parts;
+    const int64_t r0 = group * a.group_rows + part * a.team.rows;
+    const int64_t r1 = min(r0 + a.team.rows, (group + 1) * a.group_rows);
     float *const sums = a.partial ? a.partial + (int64_t)blockIdx.x * 4 * a.n : nullptr;
     if (sums)
         for (int64_t j = threadIdx.x; j < a.n; j += kBlockAnyThreads)
@@ -237,12 +245,13 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
 }
 
 // The row kernels of a pair of types (0: float32, 1: float16, 2: bfloat16; 3, 4: these
-// two beside a float32 stream; ebin_block_rows.cu).  done: whether they take
-// rows of this width.
+// two beside a float32 stream; ebin_block_rows.cu).  parts: the units of a group that
+// they took, 0 where they do not take rows of this width.
 #define EBIN_DECLARE_ROWS(dt)                                                                \
-    cudaError_t launch_block_rows_##dt(const BlockArgs &, bool vec, bool *done, cudaStream_t); \
-    cudaError_t launch_block_rows_grad_##dt(const BlockArgs &, int64_t units, bool vec,         \
-                                            bool *done, cudaStream_t);
+    cudaError_t launch_block_rows_##dt(const BlockArgs &, bool vec, int64_t *parts,           \
+                                       cudaStream_t);                                        \
+    cudaError_t launch_block_rows_grad_##dt(const BlockArgs &, bool vec, int64_t *parts,      \
+                                            cudaStream_t);
 EBIN_DECLARE_ROWS(0)
 EBIN_DECLARE_ROWS(1)
 EBIN_DECLARE_ROWS(2)

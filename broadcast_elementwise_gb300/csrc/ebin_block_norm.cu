@@ -119,7 +119,7 @@ struct ebin_block_norm_plan_s {
     int64_t isz, ssz, wsz, msz;    // bytes of an element of the four types
     uint32_t least;
     int64_t groups = 1, group_rows = 0;
-    int64_t parts = 1, unit_rows = 0;
+    ebin::BlockUnits cta, team;          // the rows' units: a CTA's, and a gradient's teams'
     size_t workspace = 0;
 };
 
@@ -183,8 +183,9 @@ ebin_status prepare_block(const ebin_block_norm_plan_s &p, const ebin_block_norm
     a.w_f32 = at.dtype_w == EBIN_FLOAT32;
     a.mod_f32 = at.dtype_mod == EBIN_FLOAT32;
     a.drop = drop_args(p.least, w.seed, w.offset, w.offset_device);
-    a.parts = p.parts;
-    a.unit_rows = p.unit_rows;
+    a.cta = p.cta;
+    a.team = p.team;
+    a.groups = p.groups;
     a.group_rows = p.group_rows;
     return EBIN_OK;
 }
@@ -240,24 +241,26 @@ bool block_vectors(const ebin_block_norm_plan_s &p, const BlockArgs &a) {
 }
 
 template <class T, class S>
-cudaError_t launch_block_any(const BlockArgs &a, bool grad, int64_t units, cudaStream_t s) {
+cudaError_t launch_block_any(const BlockArgs &a, bool grad, cudaStream_t s) {
     if (grad)
-        return launch_layer(k_block_any_grad<T, S>, dim3((unsigned)units), kBlockAnyThreads, 0, s,
-                            1, a);
+        return launch_layer(k_block_any_grad<T, S>, dim3((unsigned)(a.groups * a.team.parts)),
+                            kBlockAnyThreads, 0, s, 1, a);
     const int64_t grid = std::min<int64_t>(a.rows, 32ll * current_sm_count());
     return launch_layer(k_block_any<T, S>, dim3((unsigned)grid), kBlockAnyThreads, 0, s, 1, a);
 }
 
+// parts: the units of a group whose sums a gradient left.
 cudaError_t launch_block(const ebin_block_norm_plan_s &p, const BlockArgs &a, bool grad,
-                         cudaStream_t s) {
-    const int64_t units = p.groups * p.parts;
+                         int64_t *parts, cudaStream_t s) {
     const bool wide = p.ssz == 4, vec = block_vectors(p, a);
-    bool done = false;
     cudaError_t e;
+    *parts = 0;
 #define EBIN_ROWS(dt, T, S)                                                                 \
-    e = grad ? launch_block_rows_grad_##dt(a, units, vec, &done, s)                          \
-             : launch_block_rows_##dt(a, vec, &done, s);                                     \
-    return done ? e : launch_block_any<T, S>(a, grad, units, s)
+    e = grad ? launch_block_rows_grad_##dt(a, vec, parts, s)                                 \
+             : launch_block_rows_##dt(a, vec, parts, s);                                     \
+    if (*parts > 0 || e != cudaSuccess) return e;                                            \
+    *parts = a.team.parts;                                                                   \
+    return launch_block_any<T, S>(a, grad, s)
     if (p.at.dtype == EBIN_FLOAT32) { EBIN_ROWS(0, float, float); }
     if (p.at.dtype == EBIN_FLOAT16) {
         if (wide) { EBIN_ROWS(3, __half, float); }
@@ -268,14 +271,40 @@ cudaError_t launch_block(const ebin_block_norm_plan_s &p, const BlockArgs &a, bo
 #undef EBIN_ROWS
 }
 
-// Parts of a group's rows: as many units over all groups as 152 SMs hold teams of the
-// row kernel at 128 registers (a warp for two chunks of 256 columns), each with a
-// row at least, and no more than 2^28 sums in the workspace where that leaves one.
-int64_t block_parts(int64_t groups, int64_t group_rows, int64_t n) {
+// Of a group's rows, `parts` parts.
+BlockUnits block_units(int64_t group_rows, int64_t parts) {
+    BlockUnits u;
+    u.rows = div_up(group_rows, parts);
+    u.parts = div_up(group_rows, u.rows);
+    return u;
+}
+
+// Units of a CTA an SM: of all counts of parts the one whose last wave of 152 ends
+// first, a unit costing its teams' rows and what three more would (its tables, its
+// sums).
+BlockUnits cta_units(int64_t groups, int64_t group_rows, int64_t n, int vpt) {
+    const int64_t teams = std::max<int64_t>(1, 16 / std::max<int64_t>(1, div_up(div_up(n, 256), vpt)));
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t p = 1; p <= std::min<int64_t>(group_rows, div_up(456, groups)); ++p) {
+        const double t = (double)div_up(groups * p, 152) * (double)(div_up(div_up(group_rows, p), teams) + 3);
+        if (p == 1 || t < least) {
+            least = t;
+            best = p;
+        }
+    }
+    return block_units(group_rows, best);
+}
+
+// Units of teams: as many over all groups as 152 SMs hold teams of the row kernel at 128
+// registers (a warp for two chunks of 256 columns), each with a row at least, and
+// no more than 2^28 sums in the workspace where that leaves one.
+BlockUnits team_units(int64_t groups, int64_t group_rows, int64_t n) {
     const int64_t warps = std::max<int64_t>(1, div_up(n, 512));
     const int64_t want = div_up(152 * std::max<int64_t>(1, 16 / warps), groups);
     const int64_t room = (int64_t(1) << 26) / (groups * std::max<int64_t>(n, 1));
-    return std::max<int64_t>(1, std::min<int64_t>({want, group_rows, room}));
+    return block_units(group_rows,
+                       std::max<int64_t>(1, std::min<int64_t>({want, group_rows, room})));
 }
 
 }  // namespace
@@ -325,15 +354,15 @@ extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *
     if (a.rows > 0) {
         p->group_rows = per ? per : a.rows;
         p->groups = a.rows / p->group_rows;
+        p->cta = cta_units(p->groups, p->group_rows, a.n, a.gradient ? kUnitGradVpt : kUnitVpt);
         if (a.gradient) {
-            p->parts = block_parts(p->groups, p->group_rows, a.n);
-            p->unit_rows = div_up(p->group_rows, p->parts);
-            p->parts = div_up(p->group_rows, p->unit_rows);
             if (p->groups * div_up(a.n, kSumLanes) > 0x7FFFFFFF) {   // CTAs of the last step
                 delete p;
                 return EBIN_ERR_INVALID_ARG;
             }
-            p->workspace = sizeof(float) * 4 * (size_t)(p->groups * p->parts * a.n);
+            p->team = team_units(p->groups, p->group_rows, a.n);
+            p->workspace = sizeof(float) * 4 *
+                (size_t)(p->groups * std::max(p->cta.parts, p->team.parts) * a.n);
         }
     }
     *out = p;
@@ -386,7 +415,8 @@ extern "C" ebin_status ebin_block_norm_execute(ebin_block_norm_plan_t plan, cons
     a.ld_h = at.ld_h;
     a.ld_z = at.ld_z;
     if (!z) a.pre = EBIN_NORM_NONE;   // its sums are not wanted
-    return launch_block(p, a, false, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    int64_t parts;
+    return launch_block(p, a, false, &parts, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? EBIN_OK : EBIN_ERR_CUDA;
 }
 
@@ -477,11 +507,12 @@ extern "C" ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan,
     if (g.gate || g.w_post) a.need |= 1 << SUM_E_YH;
     if (g.b_post || (g.gate && a.b_post)) a.need |= 1 << SUM_E;
     if (!wanted && !dx && !dy) return EBIN_OK;
-    if (launch_block(p, a, true, s) != cudaSuccess) return EBIN_ERR_CUDA;
+    int64_t parts;
+    if (launch_block(p, a, true, &parts, s) != cudaSuccess) return EBIN_ERR_CUDA;
     if (!wanted) return EBIN_OK;
     BlockSumsArgs b{};
     b.partial = a.partial;
-    b.parts = p.parts;
+    b.parts = parts;
     b.groups = p.groups;
     b.n = at.n;
     b.gate = a.gate;

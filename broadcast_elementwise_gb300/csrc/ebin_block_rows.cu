@@ -21,14 +21,13 @@ using T = __nv_bfloat16;
 using S = float;
 #endif
 
-namespace {
 
 // Shared memory of an SM, what a CTA takes of it besides its rows, and the most
 // that a CTA's rows may take.
 constexpr size_t kSmSmem = 228 * 1024, kCtaSmem = 3 * 1024, kRowsSmem = 224 * 1024;
 
 template <auto KERNEL>
-cudaError_t launch_rows(const BlockArgs &a, const RowsGeom &g, int64_t grid, size_t smem,
+static cudaError_t launch_rows(const BlockArgs &a, const RowsGeom &g, int64_t grid, size_t smem,
                         cudaStream_t s) {
     const cudaError_t e = allow_smem<KERNEL>(kRowsSmem);
     if (e != cudaSuccess) return e;
@@ -37,14 +36,14 @@ cudaError_t launch_rows(const BlockArgs &a, const RowsGeom &g, int64_t grid, siz
 
 // Rows in flight: up to three, where the CTAs that an SM holds by their threads
 // leave room beside `more` bytes; 0: not even one fits.
-int rows_slots(size_t row_bytes, size_t more, int ctas) {
+static int rows_slots(size_t row_bytes, size_t more, int ctas) {
     const size_t share = kSmSmem / ctas - kCtaSmem;
     int slots = share > more ? (int)((share - more) / row_bytes) : 0;
     if (slots < 1 && row_bytes + more <= kRowsSmem) slots = 1;
     return std::min(slots, 3);
 }
 
-RowsGeom rows_geom(const BlockArgs &a, int chunks, int vpt) {
+static RowsGeom rows_geom(const BlockArgs &a, int chunks, int vpt) {
     RowsGeom g{};
     g.warps = (int)div_up(chunks, vpt);
     g.joins = 1;
@@ -56,54 +55,113 @@ RowsGeom rows_geom(const BlockArgs &a, int chunks, int vpt) {
     return g;
 }
 
-}  // namespace
 
 #define EBIN_CAT(a, b) a##b
 #define EBIN_NAME(f, dt) EBIN_CAT(f, dt)
 
-cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec, bool *done,
+// A CTA an SM takes a unit: rows on vectors, at most 8192 columns, and enough rows in
+// a unit that each team has some.
+static bool cta_takes(const BlockArgs &a, int chunks, int vpt, bool vec) {
+    return vec && chunks <= 32 && a.rows > 304 && a.cta.rows >= 2 * (16 / div_up(chunks, vpt));
+}
+
+// Its geometry, but for what lies in shared memory.
+static RowsGeom unit_geom(const BlockArgs &a, int chunks, int vpt) {
+    RowsGeom g = rows_geom(a, chunks, vpt);
+    g.teams = 16 / g.warps;
+    g.units = a.groups * a.cta.parts;
+    g.table = g.warps * vpt * 64;
+    return g;
+}
+
+cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec, int64_t *parts,
                                                    cudaStream_t s) {
-    *done = false;
+    *parts = 0;
     const int chunks = (int)div_up(a.n, kChunk);
     if (chunks > 128) return cudaSuccess;
-    // few rows: a warp for each chunk; many: two chunks
-    const int vpt = chunks > 32 ? 4 : a.rows <= 304 ? 1 : 2;
+    const bool layer = a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
+    const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
+    if (cta_takes(a, chunks, kUnitVpt, vec)) {
+        RowsGeom g = unit_geom(a, chunks, kUnitVpt);
+        const bool scaled = a.branch_scale != 1.0f || a.drop.least;
+        if (a.y && (a.gate || a.w_post || a.b_post || scaled)) g.tables |= TABLE_Y;
+        if (a.b_post) g.tables |= TABLE_Y_ADD;
+        if (a.z && (a.scale || a.w_pre)) g.tables |= TABLE_H;
+        if (a.z && (a.shift || a.b_pre)) g.tables |= TABLE_H_ADD;
+        const size_t tables = 16 * (size_t)g.table * __builtin_popcount(g.tables);
+        const int threads = g.warps * g.teams * 32;
+        g.vectors = kUnitVpt * (s_vectors + (a.y ? t_vectors : 0));
+        const size_t row = (size_t)threads * 16 * g.vectors;
+        g.slots = rows_slots(row, tables, 1);
+        if (g.slots > 0) {
+            *parts = a.cta.parts;
+            const size_t smem = tables + g.slots * row;
+            return layer ? launch_rows<k_block_unit<T, S, true>>(a, g, g.units, smem, s)
+                         : launch_rows<k_block_unit<T, S, false>>(a, g, g.units, smem, s);
+        }
+    }
+    const int vpt = chunks > 32 ? 4 : 1;
     RowsGeom g = rows_geom(a, chunks, vpt);
     const int threads = g.warps * g.teams * 32;
     const int per_sm = std::min(1024 / threads, 16);
     size_t smem = 0;
     if (vec) {
-        const size_t row = (size_t)threads * vpt * 16 *
-            ((sizeof(S) == 4 ? 2 : 1) + (sizeof(T) == 4 ? 2 : 1));
+        const size_t row = (size_t)threads * vpt * 16 * (s_vectors + t_vectors);
         g.slots = rows_slots(row, 0, per_sm);
         if (g.slots < 1) return cudaSuccess;
         smem = g.slots * row;
     }
     const int64_t grid = std::min<int64_t>(div_up(a.rows, g.teams),
                                            (int64_t)per_sm * current_sm_count());
-    *done = true;
-    const bool layer = a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
+    *parts = 1;
 #define EBIN_ROWS(VPT)                                                                       \
     if (!vec) return launch_rows<k_block_rows<T, S, VPT, false, true>>(a, g, grid, smem, s);  \
     return layer ? launch_rows<k_block_rows<T, S, VPT, true, true>>(a, g, grid, smem, s)      \
                  : launch_rows<k_block_rows<T, S, VPT, true, false>>(a, g, grid, smem, s)
     if (vpt == 1) { EBIN_ROWS(1); }
-    if (vpt == 2) { EBIN_ROWS(2); }
     EBIN_ROWS(4);
 #undef EBIN_ROWS
 }
 
-cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, int64_t units,
-                                                        bool vec, bool *done, cudaStream_t s) {
-    *done = false;
+cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool vec, int64_t *parts,
+                                                        cudaStream_t s) {
+    *parts = 0;
     const int chunks = (int)div_up(a.n, kChunk);
     if (chunks > 64) return cudaSuccess;
-    const int vpt = chunks > 32 ? 4 : 2;
-    RowsGeom g = rows_geom(a, chunks, vpt);
-    g.units = units;
-    const int threads = g.warps * g.teams * 32;
+    const bool full = a.need >> SUM_DZ & 1 || a.need >> SUM_E & 1 ||
+                      a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
     const bool has[2] = {a.scale || a.w_pre,
                          a.gate || a.w_post || a.branch_scale != 1.0f || a.drop.least};
+    const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};
+    const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
+    auto rows_at = [&](RowsGeom &g, int vpt) {   // a thread's vectors of a row
+        for (int k = 0; k < 4; ++k) {
+            g.at[k] = g.vectors;
+            if (there[k]) g.vectors += vpt * (k % 2 ? t_vectors : s_vectors);
+        }
+        return (size_t)g.warps * g.teams * 32 * 16 * g.vectors;
+    };
+    if (cta_takes(a, chunks, kUnitGradVpt, vec)) {
+        RowsGeom g = unit_geom(a, chunks, kUnitGradVpt);
+        if (has[1]) g.tables |= TABLE_Y;
+        if (has[0]) g.tables |= TABLE_H;
+        const size_t tables = 16 * (size_t)g.table * (has[0] + has[1]);
+        const size_t row = rows_at(g, kUnitGradVpt);
+        g.slots = row ? rows_slots(row, tables, 1) : 1;
+        if (g.slots > 0) {
+            // the teams' sums at the end
+            const size_t sums = g.teams > 1 ? (size_t)(full ? 4 : 2) * kUnitGradVpt * 32 *
+                                                  g.warps * 32 : 0;
+            const size_t smem = std::max(tables + g.slots * row, sums);
+            *parts = a.cta.parts;
+            return full ? launch_rows<k_block_unit_grad<T, S, true>>(a, g, g.units, smem, s)
+                        : launch_rows<k_block_unit_grad<T, S, false>>(a, g, g.units, smem, s);
+        }
+    }
+    const int vpt = chunks > 32 ? 4 : 2;
+    RowsGeom g = rows_geom(a, chunks, vpt);
+    g.units = a.groups * a.team.parts;
+    const int threads = g.warps * g.teams * 32;
     for (int f = 0; f < 2; ++f) {
         g.factor[f] = has[f] ? g.factors : -1;
         if (has[f]) g.factors += 2 * vpt;
@@ -111,30 +169,21 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, int6
     const size_t factors = (size_t)threads * 16 * g.factors;
     size_t smem = factors;
     if (vec) {
-        const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
-        const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};
-        for (int k = 0; k < 4; ++k) {
-            g.at[k] = g.vectors;
-            if (there[k]) g.vectors += vpt * (k % 2 ? t_vectors : s_vectors);
-        }
-        const size_t row = (size_t)threads * 16 * g.vectors;
+        const size_t row = rows_at(g, vpt);
         if (row > 0) {
             g.slots = rows_slots(row, factors, std::min(std::max(1, 512 / threads), 16));
             if (g.slots < 1) return cudaSuccess;
         }
         smem += g.slots * row;
     }
-    const int64_t grid = div_up(units, g.teams);
-    *done = true;
+    const int64_t grid = div_up(g.units, g.teams);
+    *parts = a.team.parts;
     if (vpt == 4)
         return vec ? launch_rows<k_block_rows_grad<T, S, 4, true, true, true>>(a, g, grid, smem, s)
                    : launch_rows<k_block_rows_grad<T, S, 4, false, true, true>>(a, g, grid, smem,
                                                                                s);
-    const bool full = a.need >> SUM_DZ & 1 || a.need >> SUM_E & 1 ||
-                      a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
-    if (!vec) return launch_rows<k_block_rows_grad<T, S, 2, false, true, false>>(a, g, grid, smem, s);
-    return full ? launch_rows<k_block_rows_grad<T, S, 2, true, true, false>>(a, g, grid, smem, s)
-                : launch_rows<k_block_rows_grad<T, S, 2, true, false, false>>(a, g, grid, smem, s);
+    return vec ? launch_rows<k_block_rows_grad<T, S, 2, true, true, false>>(a, g, grid, smem, s)
+               : launch_rows<k_block_rows_grad<T, S, 2, false, true, false>>(a, g, grid, smem, s);
 }
 
 }  // namespace ebin

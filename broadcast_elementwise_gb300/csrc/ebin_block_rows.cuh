@@ -21,6 +21,9 @@ struct RowsGeom {
     int32_t at[4], vectors;
     int32_t factor[2], factors;
     int64_t units;
+    // of a CTA that takes a unit: which of its columns' factors there are, by bit, and
+    // the 16-byte vectors of one
+    int32_t tables, table;
 };
 
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
@@ -32,6 +35,7 @@ template <class T, class S, bool VEC> struct RowsLane {
     static constexpr bool WIDE = sizeof(S) == 4;
     int lane, base, n;   // base: the chunk's first column
     bool on0, on1;       // whether the fours lie within the row (vectors)
+    int at0, at1;        // where they are read: what lies past the end reads column 0
 
     __device__ __forceinline__ void place(int lane_, int base_, int n_) {
         lane = lane_;
@@ -39,7 +43,11 @@ template <class T, class S, bool VEC> struct RowsLane {
         n = n_;
         on0 = quad(0) < n;
         on1 = WIDE ? quad(1) < n : on0;
+        at0 = on0 ? quad(0) : 0;
+        at1 = WIDE ? (on1 ? quad(1) : 0) : at0 + 4;
     }
+    // no column of the chunk lies in the row (the same for a whole warp)
+    __device__ __forceinline__ bool none() const { return base >= n; }
     // first column of four q (vectors)
     __device__ __forceinline__ int quad(int q) const {
         return base + (WIDE ? q * 128 + lane * 4 : lane * 8 + q * 4);
@@ -81,22 +89,18 @@ template <class T, class S, bool VEC> struct RowsLane {
             v[1] = open2<E>(x.y);
         }
     }
-    // the lane's columns of a row in global memory; 0 past the row's end
+    // the lane's columns of a row in global memory; past the row's end anything (vectors) or 0
     template <class E> __device__ __forceinline__ void load(const E *p, float2 *v) const {
         if constexpr (VEC) {
             if constexpr (!WIDE && sizeof(E) == 2) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (on0) x = *reinterpret_cast<const uint4 *>(p + quad(0));
+                const uint4 x = *reinterpret_cast<const uint4 *>(p + at0);
                 v[0] = open2<E>(x.x);
                 v[1] = open2<E>(x.y);
                 v[2] = open2<E>(x.z);
                 v[3] = open2<E>(x.w);
             } else {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    v[2 * q] = v[2 * q + 1] = two(0.0f);
-                    if (on(q)) open4(p + quad(q), v + 2 * q);
-                }
+                open4(p + at0, v);
+                open4(p + at1, v + 2);
             }
         } else {
 #pragma unroll
@@ -187,8 +191,11 @@ template <class T, class S, bool VEC> struct RowsLane {
 
 // A team's exchange of partial sums through shared memory, [2][8][warps]: consecutive
 // exchanges take the halves in turn, so that one barrier each is enough.
-struct Team {
+// NAMED: one of several teams of a CTA, each with a barrier of its own (1 .. 15: 0 is the
+// CTA's); else the CTA is the team, or its teams are single warps.
+template <bool NAMED> struct Team {
     int lane, warp, warps, joins;
+    int id;             // among the CTA's teams
     float *s;           // 2 * 8 * kRowsMaxWarps floats
     int half;
     float count;        // live columns of the warp that this lane stands for in joins
@@ -198,7 +205,10 @@ struct Team {
 
     template <int VPT> __device__ __forceinline__ void start(const RowsGeom &g, int n, float *sums) {
         lane = threadIdx.x & 31;
-        warp = g.teams > 1 ? 0 : threadIdx.x >> 5;
+        const int team = (threadIdx.x >> 5) / g.warps;
+        warp = (threadIdx.x >> 5) - team * g.warps;
+        id = team;
+        sums += team * g.warps;   // a team's columns of the sums
         warps = g.warps;
         joins = g.joins;
         s = sums;
@@ -225,7 +235,10 @@ struct Team {
 #pragma unroll
         for (int k = 1; k < K; ++k) mine = lane == k ? v[k] : mine;
         if (lane < K) at[lane * kRowsMaxWarps + warp] = mine;
-        __syncthreads();
+        if constexpr (NAMED)   // teams of two warps and more: at most 8
+            asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
+        else
+            __syncthreads();
         const int from = lane & (joins - 1);
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] = from < warps ? at[k * kRowsMaxWarps + from] : 0.0f;
@@ -275,20 +288,22 @@ __device__ __forceinline__ float squares8(const L &l, const float2 *v, float mea
 }
 
 // LAYER: either norm may be a layer norm; else neither is.
-template <bool LAYER, class L, int VPT>
-__device__ __forceinline__ float2 row_moments(Team &t, const L (&l)[VPT], const float2 (&v)[VPT][4],
+template <bool LAYER, class TEAM, class L, int VPT>
+__device__ __forceinline__ float2 row_moments(TEAM &t, const L (&l)[VPT], const float2 (&v)[VPT][4],
                                               int norm, float eps) {
     const bool layer = LAYER && norm == EBIN_NORM_LAYER;
     float s[1] = {0.0f}, mean = 0.0f;
     if (layer) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) s[0] += l[i].within(v[i]);
+        for (int i = 0; i < VPT; ++i)
+            if (!i || !l[i].none()) s[0] += l[i].within(v[i]);
         warp_sums(s);
         mean = s[0] * t.inv_mine;
     }
     float q[1] = {0.0f};
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) q[0] += squares8<LAYER>(l[i], v[i], mean);
+    for (int i = 0; i < VPT; ++i)
+        if (!i || !l[i].none()) q[0] += squares8<LAYER>(l[i], v[i], mean);
     warp_sums(q);
     if constexpr (LAYER) {
         float both[2] = {s[0], q[0]};
@@ -324,14 +339,13 @@ template <class L, class E> struct RowsPart {
     __device__ __forceinline__ static void fetch(const L &l, uint32_t to, int stride,
                                                  const E *row) {
         if constexpr (!L::WIDE) {
-            if (l.on0) rows_copy16(to, row + l.quad(0));
+            rows_copy16(to, row + l.at0);
+        } else if constexpr (sizeof(E) == 4) {
+            rows_copy16(to, row + l.at0);
+            rows_copy16(to + stride * 16, row + l.at1);
         } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (!l.on(q)) continue;
-                if constexpr (sizeof(E) == 4) rows_copy16(to + q * stride * 16, row + l.quad(q));
-                else rows_copy8(to + q * 8, row + l.quad(q));
-            }
+            rows_copy8(to, row + l.at0);
+            rows_copy8(to + 8, row + l.at1);
         }
     }
     __device__ __forceinline__ static void open(const uint4 *at, int stride, float2 *v) {
@@ -369,8 +383,10 @@ template <bool LAYER> __device__ __forceinline__ void norm8(float2 *v, float2 m)
     }
 }
 
+// A team, a row after another: few rows, rows off the vectors or past 8192 columns, and
+// groups of few rows.
 template <class T, class S, int VPT, bool VEC, bool LAYER>
-__global__ void __launch_bounds__(VPT == 2 ? 512 : 1024, VPT == 2 ? 2 : 1)
+__global__ void __launch_bounds__(1024, 1)
 k_block_rows(const BlockArgs a, const RowsGeom g) {
     using Lane = RowsLane<T, S, VEC>;
     using PartS = RowsPart<Lane, S>;
@@ -378,8 +394,8 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
     __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
     extern __shared__ uint4 s_rows[];   // [slots][vectors of a thread][threads]
     constexpr int kX = VPT * PartS::N, kVectors = kX + VPT * PartT::N;
-    Team t;
-    t.start<VPT>(g, (int)a.n, s_sums);
+    Team<false> t;
+    t.template start<VPT>(g, (int)a.n, s_sums);
     Lane l[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -403,12 +419,14 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
                 const S *const x = static_cast<const S *>(a.x) + next * a.ld_x;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
-                    PartS::fetch(l[i], at + i * PartS::N * threads * 16, threads, x);
+                    if (!i || !l[i].none())
+                        PartS::fetch(l[i], at + i * PartS::N * threads * 16, threads, x);
                 if (a.y) {
                     const T *const y = static_cast<const T *>(a.y) + next * a.ld_y;
 #pragma unroll
                     for (int i = 0; i < VPT; ++i)
-                        PartT::fetch(l[i], at + (kX + i * PartT::N) * threads * 16, threads, y);
+                        if (!i || !l[i].none())
+                            PartT::fetch(l[i], at + (kX + i * PartT::N) * threads * 16, threads, y);
                 }
                 next += step;
             }
@@ -434,6 +452,7 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
             }
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
+            if (i && l[i].none()) continue;
                 if constexpr (VEC) PartT::open(at + (kX + i * PartT::N) * threads, threads, v[i]);
                 else l[i].load(static_cast<const T *>(a.y) + row * a.ld_y, v[i]);
             }
@@ -441,6 +460,7 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
+            if (i && l[i].none()) continue;
             float2 x[4], p[4];
             if constexpr (VEC) PartS::open(at + i * PartS::N * threads, threads, x);
             else l[i].load(static_cast<const S *>(a.x) + row * a.ld_x, x);
@@ -481,6 +501,7 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
+            if (i && l[i].none()) continue;
             float2 p[4];
             norm8<LAYER>(v[i], mh);
             if (a.w_pre) {
@@ -522,8 +543,8 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
     constexpr int kKinds = FULL ? 4 : 2;
     __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
     extern __shared__ uint4 s_rows[];   // the rows' slots, then the factors
-    Team t;
-    t.start<VPT>(g, (int)a.n, s_sums);
+    Team<false> t;
+    t.template start<VPT>(g, (int)a.n, s_sums);
     Lane l[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -531,9 +552,9 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
     const int64_t unit = g.teams > 1 ? (int64_t)blockIdx.x * g.teams + (threadIdx.x >> 5)
                                      : blockIdx.x;
     if (unit >= g.units) return;   // a whole team, and one without barriers
-    const int64_t group = unit / a.parts, part = unit - group * a.parts;
-    const int r0 = (int)(group * a.group_rows + part * a.unit_rows);
-    const int r1 = (int)min(r0 + a.unit_rows, (group + 1) * a.group_rows);
+    const int64_t group = unit / a.team.parts, part = unit - group * a.team.parts;
+    const int r0 = (int)(group * a.group_rows + part * a.team.rows);
+    const int r1 = (int)min(r0 + a.team.rows, (group + 1) * a.group_rows);
     const int threads = blockDim.x;
     uint4 *const mine = s_rows + threadIdx.x;
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
@@ -862,6 +883,519 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
             }
             l[i].store(partial + k * a.n, s);
         }
+    }
+}
+
+// ------------------------------------------------------------------ a CTA takes a unit
+//
+// Many rows on vectors, of at most 8192 columns: one CTA an SM takes a unit,
+// consecutive rows of one group, and its teams walk them in turn.  What a column's
+// elements are multiplied by and added to lies in shared memory in binary32, formed
+// once from the parameters: two 16-byte loads in place of one and eight conversions,
+// which a row of weights in the L1 costs for each use ([8192,4096] bf16 with both
+// norms' weights: 60 us so, 48 without the weights).
+
+// A table of a factor for the lane's columns: the fours of chunk i, [2][32] vectors.
+template <class L> struct RowsTable {
+    const float4 *at;   // this lane's first
+    int warps;
+    __device__ __forceinline__ void read(int i, float2 *p) const {
+        const float4 x = at[i * warps * 64], y = at[i * warps * 64 + 32];
+        p[0] = make_float2(x.x, x.y);
+        p[1] = make_float2(x.z, x.w);
+        p[2] = make_float2(y.x, y.y);
+        p[3] = make_float2(y.z, y.w);
+    }
+    __device__ __forceinline__ void times(int i, float2 *v) const {
+        float2 p[4];
+        read(i, p);
+        mul8(v, p);
+    }
+};
+
+// value(col, q, p): a table's four values at col; written by the whole CTA.
+template <class L, class F>
+__device__ __forceinline__ void rows_fill(float4 *table, int vectors, int n, const F &value) {
+    for (int j = threadIdx.x; j < vectors; j += blockDim.x) {
+        const int lane = j & 31, q = j >> 5 & 1, base = (j >> 6) * kChunk;
+        const int col = base + (L::WIDE ? q * 128 + lane * 4 : lane * 8 + q * 4);
+        table[j] = col < n ? value(col) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+}
+
+// Four of a row of parameters in type T or binary32; `none` where there is no row.
+template <class T>
+__device__ __forceinline__ float4 params4(const void *p, int col, int f32, float none) {
+    if (!p) return make_float4(none, none, none, none);
+    if (f32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + col);
+    if constexpr (sizeof(T) == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p) + col);
+        const float2 a = open2<T>(x.x), b = open2<T>(x.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    } else {
+        return *reinterpret_cast<const float4 *>(static_cast<const T *>(p) + col);
+    }
+}
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
+    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 four(float v) { return make_float4(v, v, v, v); }
+
+enum RowsTables : int {
+    TABLE_Y = 1,       // branch_scale / (1 - p) gate w_post
+    TABLE_Y_ADD = 2,   // branch_scale / (1 - p) gate b_post
+    TABLE_H = 4,       // (1 + scale) w_pre
+    TABLE_H_ADD = 8    // (1 + scale) b_pre + shift
+};
+
+constexpr int kUnitThreads = 512;
+
+template <class T, class S, bool LAYER>
+__global__ void __launch_bounds__(kUnitThreads, 1)
+k_block_unit(const BlockArgs a, const RowsGeom g) {
+    using Lane = RowsLane<T, S, true>;
+    using PartS = RowsPart<Lane, S>;
+    using PartT = RowsPart<Lane, T>;
+    constexpr int VPT = kUnitVpt;
+    __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
+    extern __shared__ uint4 s_rows[];   // the tables, then [slots][vectors of a thread][threads]
+    constexpr int kX = VPT * PartS::N;
+    Team<true> t;
+    t.template start<VPT>(g, (int)a.n, s_sums);
+    Lane l[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        l[i].place(t.lane, (i * g.warps + t.warp) * kChunk, (int)a.n);
+    const int64_t unit = blockIdx.x, group = unit / a.cta.parts, part = unit - group * a.cta.parts;
+    const int r0 = (int)(group * a.group_rows + part * a.cta.rows);
+    const int r1 = (int)min(r0 + a.cta.rows, (group + 1) * a.group_rows);
+    const int threads = blockDim.x, step = g.teams;
+    const bool post = a.post != EBIN_NORM_NONE;
+    const float branch = a.branch_scale * (a.drop.least ? a.drop.scale : 1.0f);
+    float4 *table = reinterpret_cast<float4 *>(s_rows);
+    RowsTable<Lane> by[4];   // of bit k
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        by[k] = RowsTable<Lane>{table + t.warp * 64 + t.lane, g.warps};
+        if (g.tables >> k & 1) table += g.table;
+    }
+    uint4 *const mine = reinterpret_cast<uint4 *>(table) + threadIdx.x;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
+    layer_pdl_launch();
+    layer_pdl_wait();
+    const uint2 offset = drop_offset(a.drop);
+    const int ahead = g.slots - 1, vectors = g.vectors;
+    int fill = 0, slot = 0, next = r0 + t.id;
+    auto fetch = [&]() {
+        if (next < r1) {
+            const uint32_t at = to + fill * vectors * threads * 16;
+            const S *const x = static_cast<const S *>(a.x) + next * a.ld_x;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (!i || !l[i].none())
+                    PartS::fetch(l[i], at + i * PartS::N * threads * 16, threads, x);
+            if (a.y) {
+                const T *const y = static_cast<const T *>(a.y) + next * a.ld_y;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (!i || !l[i].none())
+                        PartT::fetch(l[i], at + (kX + i * PartT::N) * threads * 16, threads, y);
+            }
+            next += step;
+        }
+        fill = fill + 1 == g.slots ? 0 : fill + 1;
+        rows_commit();
+    };
+    for (int i = 0; i < ahead; ++i) fetch();
+    {
+        uint32_t index, rest;
+        g.gate.split((uint32_t)r0, index, rest);
+        const void *const gate = block_row<T>(a.gate, index * a.ld_gate, a.mod_f32);
+        g.mod.split((uint32_t)r0, index, rest);
+        const void *const scale = block_row<T>(a.scale, index * a.ld_scale, a.mod_f32);
+        const void *const shift = block_row<T>(a.shift, index * a.ld_shift, a.mod_f32);
+        float4 *at = reinterpret_cast<float4 *>(s_rows);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            if (!(g.tables >> k & 1)) continue;
+            const bool y = k < 2, more = k & 1;
+            rows_fill<Lane>(at, g.table, (int)a.n, [&](int col) {
+                const float4 m = y ? mul4(four(branch), params4<T>(gate, col, a.mod_f32, 1.0f))
+                                   : add4(four(1.0f), params4<T>(scale, col, a.mod_f32, 0.0f));
+                const void *const w = y ? (more ? a.b_post : a.w_post) : (more ? a.b_pre : a.w_pre);
+                float4 r = mul4(m, params4<T>(w, col, a.w_f32, more ? 0.0f : 1.0f));
+                if (k == 3) r = add4(r, params4<T>(shift, col, a.mod_f32, 0.0f));
+                return r;
+            });
+            at += g.table;
+        }
+    }
+    __syncthreads();
+    for (int row = r0 + t.id; row < r1; row += step) {
+        fetch();
+        rows_wait(ahead);
+        const uint4 *const at = mine + slot * vectors * threads;
+        slot = slot + 1 == g.slots ? 0 : slot + 1;
+        float2 v[VPT][4];
+        float2 my = make_float2(0.0f, 1.0f);
+        if (a.y) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (i && l[i].none()) continue;
+                PartT::open(at + (kX + i * PartT::N) * threads, threads, v[i]);
+            }
+            if (post) my = row_moments<LAYER>(t, l, v, a.post, a.eps_post);
+        }
+        S *const h = static_cast<S *>(a.h) + row * a.ld_h;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (i && l[i].none()) continue;
+            float2 x[4];
+            PartS::open(at + i * PartS::N * threads, threads, x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], two(a.stream_scale));
+            if (a.y) {
+                if (post) norm8<LAYER>(v[i], my);
+                if (!(g.tables & TABLE_Y_ADD)) {
+                    if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, v[i]);
+                    if (g.tables & TABLE_Y) {
+                        float2 p[4];
+                        by[0].read(i, p);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = __ffma2_rn(v[i][k], p[k], x[k]);
+                    } else {
+                        add8(x, v[i]);
+                    }
+                } else {   // with a bias the mask comes after the factor
+                    float2 p[4];
+                    by[1].read(i, p);
+                    float2 q[4];
+                    by[0].read(i, q);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[i][k] = __ffma2_rn(v[i][k], q[k], p[k]);
+                    if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, v[i]);
+                    add8(x, v[i]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i][k] = x[k];
+            if (a.h) l[i].store(h, v[i]);
+        }
+        if (!a.z) continue;
+        const float2 mh = row_moments<LAYER>(t, l, v, a.pre, a.eps_pre);
+        T *const z = static_cast<T *>(a.z) + row * a.ld_z;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (i && l[i].none()) continue;
+            norm8<LAYER>(v[i], mh);
+            if (g.tables & TABLE_H) by[2].times(i, v[i]);
+            if (g.tables & TABLE_H_ADD) {
+                float2 p[4];
+                by[3].read(i, p);
+                add8(v[i], p);
+            }
+            l[i].store(z, v[i]);
+        }
+    }
+    rows_wait(0);
+}
+
+// The gradient of such units; its sums in registers as k_block_rows_grad's, the
+// teams' joined in shared memory at the end, one after another.
+
+template <class T, class S, bool FULL>
+__global__ void __launch_bounds__(kUnitThreads, 1)
+k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
+    using Lane = RowsLane<T, S, true>;
+    using PartS = RowsPart<Lane, S>;
+    using PartT = RowsPart<Lane, T>;
+    constexpr int VPT = kUnitGradVpt, kKinds = FULL ? 4 : 2;
+    __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
+    extern __shared__ uint4 s_rows[];   // the tables, then the rows; at the end the sums
+    Team<true> t;
+    t.template start<VPT>(g, (int)a.n, s_sums);
+    Lane l[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        l[i].place(t.lane, (i * g.warps + t.warp) * kChunk, (int)a.n);
+    const int64_t unit = blockIdx.x, group = unit / a.cta.parts, part = unit - group * a.cta.parts;
+    const int r0 = (int)(group * a.group_rows + part * a.cta.rows);
+    const int r1 = (int)min(r0 + a.cta.rows, (group + 1) * a.group_rows);
+    const int threads = blockDim.x, step = g.teams;
+    const bool pre = a.pre != EBIN_NORM_NONE, post = a.post != EBIN_NORM_NONE;
+    const bool layer_h = FULL && a.pre == EBIN_NORM_LAYER;
+    const bool layer_y = FULL && a.post == EBIN_NORM_LAYER;
+    const float branch = a.branch_scale * (a.drop.least ? a.drop.scale : 1.0f);
+    float4 *table = reinterpret_cast<float4 *>(s_rows);
+    RowsTable<Lane> by_y{table + t.warp * 64 + t.lane, g.warps};
+    if (g.tables & TABLE_Y) table += g.table;
+    RowsTable<Lane> by_h{table + t.warp * 64 + t.lane, g.warps};
+    if (g.tables & TABLE_H) table += g.table;
+    uint4 *const mine = reinterpret_cast<uint4 *>(table) + threadIdx.x;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
+    layer_pdl_launch();
+    layer_pdl_wait();
+    const uint2 offset = drop_offset(a.drop);
+    const int ahead = g.slots - 1;
+    int fill = 0, slot = 0, next = r0 + t.id;
+    auto fetch = [&]() {
+        if (next < r1) {
+            const uint32_t at = to + fill * g.vectors * threads * 16;
+            const uint32_t s_step = PartS::N * threads * 16, t_step = PartT::N * threads * 16;
+            if (a.x) {
+                const S *const p = static_cast<const S *>(a.x) + next * a.ld_x;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    PartS::fetch(l[i], at + g.at[0] * threads * 16 + i * s_step, threads, p);
+            }
+            if (a.dz) {
+                const T *const p = static_cast<const T *>(a.dz) + next * a.ld_dz;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    PartT::fetch(l[i], at + g.at[1] * threads * 16 + i * t_step, threads, p);
+            }
+            if (a.dh) {
+                const S *const p = static_cast<const S *>(a.dh) + next * a.ld_dh;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    PartS::fetch(l[i], at + g.at[2] * threads * 16 + i * s_step, threads, p);
+            }
+            if (a.y) {
+                const T *const p = static_cast<const T *>(a.y) + next * a.ld_y;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    PartT::fetch(l[i], at + g.at[3] * threads * 16 + i * t_step, threads, p);
+            }
+            next += step;
+        }
+        fill = fill + 1 == g.slots ? 0 : fill + 1;
+        rows_commit();
+    };
+    for (int i = 0; i < ahead; ++i) fetch();
+    {
+        uint32_t index, rest;
+        g.gate.split((uint32_t)r0, index, rest);
+        const void *const gate = block_row<T>(a.gate, index * a.ld_gate, a.mod_f32);
+        g.mod.split((uint32_t)r0, index, rest);
+        const void *const scale = block_row<T>(a.scale, index * a.ld_scale, a.mod_f32);
+        float4 *at = reinterpret_cast<float4 *>(s_rows);
+        if (g.tables & TABLE_Y) {
+            rows_fill<Lane>(at, g.table, (int)a.n, [&](int col) {
+                return mul4(mul4(four(branch), params4<T>(gate, col, a.mod_f32, 1.0f)),
+                            params4<T>(a.w_post, col, a.w_f32, 1.0f));
+            });
+            at += g.table;
+        }
+        if (g.tables & TABLE_H)
+            rows_fill<Lane>(at, g.table, (int)a.n, [&](int col) {
+                return mul4(add4(four(1.0f), params4<T>(scale, col, a.mod_f32, 0.0f)),
+                            params4<T>(a.w_pre, col, a.w_f32, 1.0f));
+            });
+    }
+    __syncthreads();
+    float2 acc[kKinds][VPT][4];
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[k][i][j] = two(0.0f);
+    auto place = [](int kind) { return FULL ? kind : kind >> 1; };
+    for (int row = r0 + t.id; row < r1; row += step) {
+        fetch();
+        rows_wait(ahead);
+        const uint4 *const at = mine + slot * g.vectors * threads;
+        slot = slot + 1 == g.slots ? 0 : slot + 1;
+        const uint4 *const at_h = at + g.at[0] * threads, *const at_dz = at + g.at[1] * threads;
+        const uint4 *const at_dh = at + g.at[2] * threads, *const at_y = at + g.at[3] * threads;
+        auto open_s = [&](const uint4 *p, int i, float2 *v) {
+            PartS::open(p + i * PartS::N * threads, threads, v);
+        };
+        auto open_t = [&](const uint4 *p, int i, float2 *v) {
+            PartT::open(p + i * PartT::N * threads, threads, v);
+        };
+        // this warp's sums of the squares of h about their mean, of m with h less that
+        // mean, of the squares of y; FULL: of m, of h and of y
+        float w[FULL ? 6 : 3] = {};
+        float2 v[VPT][4];   // m, then D
+        float mean_h = 0.0f, mean_y = 0.0f;
+        if (FULL && (layer_h || layer_y)) {
+            float s[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float2 x[4];
+                if (layer_h) {
+                    open_s(at_h, i, x);
+                    s[0] += l[i].within(x);
+                }
+                if (layer_y) {
+                    open_t(at_y, i, x);
+                    s[1] += l[i].within(x);
+                }
+            }
+            warp_sums(s);
+            w[FULL ? 4 : 0] = s[0];
+            w[FULL ? 5 : 0] = s[1];
+            mean_h = s[0] * t.inv_mine;
+            mean_y = s[1] * t.inv_mine;
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (pre) {
+                float2 h[4], c[4];
+                open_t(at_dz, i, v[i]);
+                if (g.tables & TABLE_H) by_h.times(i, v[i]);
+                open_s(at_h, i, h);
+                if constexpr (FULL) {
+                    w[3] += l[i].within(v[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[j] = __fadd2_rn(h[j], two(-mean_h));
+                }
+                w[0] += squares8<false>(l[i], h, 0.0f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[j] = __fmul2_rn(v[i][j], h[j]);
+                w[1] += l[i].within(c);
+            }
+            if (post) {
+                float2 y[4];
+                open_t(at_y, i, y);
+                w[2] += squares8<FULL>(l[i], y, mean_y);
+            }
+        }
+        float2 mh = make_float2(0.0f, 1.0f), my = mh;
+        float c0 = 0.0f, c1 = 0.0f;   // means of m and of m hh
+        if (pre || post) {
+            if constexpr (FULL) {
+                float q[4] = {w[0], w[1], w[2], w[3]};
+                warp_sums(q);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = q[k];
+            } else {
+                warp_sums(w);
+            }
+            t.gather(w);
+            if (pre) {
+                mh = t.moments(FULL ? w[FULL ? 4 : 0] : 0.0f, w[0], layer_h, a.eps_pre);
+                if constexpr (FULL) {
+                    // the products about the row's mean
+                    float c[2] = {w[3], w[1]};
+                    if (layer_h) c[1] = fmaf(w[3], fmaf(w[4], t.inv_count, -mh.x), c[1]);
+                    t.join(c);
+                    c0 = layer_h ? c[0] * t.inv_n : 0.0f;
+                    c1 = c[1] * mh.y * t.inv_n;
+                } else {
+                    float c[1] = {w[1]};
+                    t.join(c);
+                    c1 = c[0] * mh.y * t.inv_n;
+                }
+            }
+            if (post) my = t.moments(FULL ? w[FULL ? 5 : 0] : 0.0f, w[2], layer_y, a.eps_post);
+        }
+        float2 u[VPT][4];
+        float b[FULL ? 2 : 1] = {};   // sums of u yh and (FULL) of u
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float2 d[4], yh[4];
+            if (a.dh) open_s(at_dh, i, d);
+            else d[0] = d[1] = d[2] = d[3] = two(0.0f);
+            if (pre) {
+                float2 h[4], dz[4];
+                open_s(at_h, i, h);
+                norm8<FULL>(h, mh);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 m = v[i][j];
+                    if constexpr (FULL) m = __fadd2_rn(m, two(-c0));
+                    d[j] = __ffma2_rn(__ffma2_rn(h[j], two(-c1), m), two(mh.y), d[j]);
+                }
+                open_t(at_dz, i, dz);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[0][i][j] = __ffma2_rn(dz[j], h[j], acc[0][i][j]);
+                    if constexpr (FULL) acc[1][i][j] = __fadd2_rn(acc[1][i][j], dz[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = u[i][j] = d[j];
+            // e / branch, then u
+            if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, u[i]);
+            if (a.y) {
+                open_t(at_y, i, yh);
+                if (post) norm8<FULL>(yh, my);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[place(SUM_E_YH)][i][j] = __ffma2_rn(u[i][j], yh[j],
+                                                            acc[place(SUM_E_YH)][i][j]);
+            }
+            if constexpr (FULL) add8(acc[kKinds - 1][i], u[i]);
+            if (g.tables & TABLE_Y) by_y.times(i, u[i]);
+            if (post) {
+                if constexpr (FULL) b[FULL ? 1 : 0] += l[i].within(u[i]);
+                mul8(yh, u[i]);
+                b[0] += l[i].within(yh);
+            }
+        }
+        float b0 = 0.0f, b1 = 0.0f;
+        if (post) {
+            warp_sums(b);
+            t.gather(b);
+            t.join(b);
+            b0 = b[0] * t.inv_n;
+            b1 = layer_y ? b[FULL ? 1 : 0] * t.inv_n : 0.0f;
+        }
+        T *const dy = static_cast<T *>(a.z) + row * a.ld_z;
+        S *const dx = static_cast<S *>(a.h) + row * a.ld_h;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (a.z) {
+                if (post) {
+                    float2 yh[4];
+                    open_t(at_y, i, yh);
+                    norm8<FULL>(yh, my);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (FULL) u[i][j] = __fadd2_rn(u[i][j], two(-b1));
+                        u[i][j] = __fmul2_rn(__ffma2_rn(yh[j], two(-b0), u[i][j]), two(my.y));
+                    }
+                }
+                l[i].store(dy, u[i]);
+            }
+            if (a.h) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(v[i][j], two(a.stream_scale));
+                l[i].store(dx, v[i]);
+            }
+        }
+    }
+    rows_wait(0);
+    if (!a.partial) return;
+    float2 *const sums = reinterpret_cast<float2 *>(s_rows) + t.warp * 32 + t.lane;
+    const int team_threads = g.warps * 32;
+    for (int team = 0; team < g.teams; ++team) {
+        __syncthreads();   // the rows have been read; the team before has added
+        if (t.id != team) continue;
+        float *const partial = a.partial + unit * 4 * a.n;
+#pragma unroll
+        for (int k = 0; k < kKinds; ++k)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float2 *const at = sums + (k * VPT + i) * 4 * team_threads;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (team > 0) acc[k][i][j] = __fadd2_rn(at[j * team_threads], acc[k][i][j]);
+                    if (team + 1 < g.teams) at[j * team_threads] = acc[k][i][j];
+                }
+                if (team + 1 < g.teams) continue;
+                const int kind = FULL ? k : 2 * k;
+                if (kind == SUM_E_YH || kind == SUM_E) {   // they carry their factor from here on
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[k][i][j] = __fmul2_rn(acc[k][i][j], two(branch));
+                }
+                l[i].store(partial + kind * a.n, acc[k][i]);
+            }
     }
 }
 
