@@ -12,8 +12,8 @@ struct BlockUnits {
     int64_t parts = 1, rows = 0;
 };
 
-// Chunks of 256 columns that a lane of the kernels of CTAs' units owns.
-constexpr int kUnitVpt = 4, kUnitGradVpt = 2;
+// The kernels of CTAs' units: chunks of 256 columns that a lane owns, threads and warps.
+constexpr int kUnitVpt = 4, kUnitGradVpt = 2, kUnitThreads = 512, kUnitWarps = kUnitThreads / 32;
 
 struct BlockArgs {
     // forward: x, y -> h, z; gradient: dz, dh, h, y -> dx, dy

@@ -7,7 +7,7 @@
 
 namespace ebin {
 
-constexpr int kSumLanes = 32, kSumRows = 32;
+constexpr int kSumColumns = 32, kSumRows = 32;   // of a CTA
 
 // A parameter in the launch's element type.
 __device__ __forceinline__ float sums_at(const BlockSumsArgs &a, const void *p, int64_t j, int f32,
@@ -17,23 +17,55 @@ __device__ __forceinline__ float sums_at(const BlockSumsArgs &a, const void *p, 
     return block_param<float>(p, j, 1, none);
 }
 
-// The sum over `count` rows of partial, [.][4][n] from `first` on, of sum k and
-// column j, in an order fixed by the count; thread row 0 gets it.
-__device__ __forceinline__ float sums_column(const float *first, int64_t count, int64_t stride,
-                                             bool live, float (*s)[kSumLanes + 1]) {
-    float v = 0.0f;
-    if (live) {
-#pragma unroll 8
-        for (int64_t c = threadIdx.y; c < count; c += kSumRows) v += first[c * stride];
-    }
-    __syncthreads();   // the last column's have been read
-    s[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    float t = 0.0f;
-    if (threadIdx.y == 0)
+// The sums of a CTA's 32 columns, [kind][column], over `count` rows of them that lie
+// `stride` apart from `first` on, for the kinds wanted, each n further: eight lanes of four
+// columns (V = 4; V = 1: 32 of one) take every 32nd row, all kinds' loads together, then
+// the 32 join in order: an order fixed by the count.
+template <int V>
+__device__ __forceinline__ void sums_columns(const BlockSumsArgs &a, const float *first,
+                                             int64_t count, int64_t stride, int64_t col0,
+                                             float (*s)[kSumRows][kSumColumns + 1],
+                                             float (*total)[kSumColumns]) {
+    constexpr int L = kSumColumns / V;
+    const int lane = threadIdx.x % L, row = threadIdx.x / L;
+    const int64_t col = col0 + lane * V;
+    float v[4][V];
 #pragma unroll
-        for (int r = 0; r < kSumRows; ++r) t += s[r][threadIdx.x];
-    return t;
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[k][e] = 0.0f;
+    if (col < a.n) {
+        const float *p = first + col + row * stride;
+#pragma unroll 4
+        for (int64_t c = row; c < count; c += kSumRows, p += kSumRows * stride) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (!(a.need >> k & 1)) continue;
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(p + k * a.n);
+                    v[k][0] += x.x;
+                    v[k][1] += x.y;
+                    v[k][2] += x.z;
+                    v[k][3] += x.w;
+                } else {
+                    v[k][0] += p[k * a.n];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[k][row][lane * V + e] = v[k][e];
+    __syncthreads();
+    for (int j = threadIdx.x; j < 4 * kSumColumns; j += blockDim.x) {
+        const int k = j / kSumColumns, c = j % kSumColumns;
+        float t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kSumRows; ++r) t += s[k][r][c];
+        total[k][c] = t;
+    }
+    __syncthreads();
 }
 
 // The parameters' gradients that all rows share, from the sums of all groups.  w:
@@ -61,18 +93,19 @@ __device__ __forceinline__ void sums_shared(const BlockSumsArgs &a, int64_t j, c
 // One CTA per group and 32 columns: the group's parts joined; its gradients of gate, scale
 // and shift; then, with one group, everything, else its share of what all rows
 // have in common, into its first part's place.
-__global__ void __launch_bounds__(kSumLanes *kSumRows) k_block_sums(const BlockSumsArgs a) {
-    __shared__ float s[kSumRows][kSumLanes + 1];
-    const int64_t group = blockIdx.x / a.tiles;
-    const int64_t j = (blockIdx.x - group * a.tiles) * kSumLanes + threadIdx.x;
-    const bool live = j < a.n;
+template <int V>
+__global__ void __launch_bounds__(kSumColumns *kSumRows / V) k_block_sums(const BlockSumsArgs a) {
+    __shared__ float s[4][kSumRows][kSumColumns + 1], total[4][kSumColumns];
+    const int64_t group = blockIdx.x / a.tiles, col0 = (blockIdx.x - group * a.tiles) * kSumColumns;
     layer_pdl_launch();
     layer_pdl_wait();
-    float *const at = a.partial + group * a.parts * 4 * a.n + j;
+    float *const at = a.partial + group * a.parts * 4 * a.n;
+    sums_columns<V>(a, at, a.parts, 4 * a.n, col0, s, total);
+    const int64_t j = col0 + threadIdx.x;
+    if (threadIdx.x >= kSumColumns || j >= a.n) return;
     float t[4];
-    for (int k = 0; k < 4; ++k)
-        t[k] = a.need >> k & 1 ? sums_column(at + k * a.n, a.parts, 4 * a.n, live, s) : 0.0f;
-    if (threadIdx.y != 0 || !live) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = total[k][threadIdx.x];
     if (a.groups == 1) {
         sums_shared(a, j, t, false);
         if (!a.mod_grouped && !a.gate_grouped) return;
@@ -93,23 +126,27 @@ __global__ void __launch_bounds__(kSumLanes *kSumRows) k_block_sums(const BlockS
         ? 1.0f + sums_at(a, a.scale, group * a.ld_scale + j, a.mod_f32, 0.0f) : 1.0f;
     const float gate = a.gate_grouped
         ? sums_at(a, a.gate, group * a.ld_gate + j, a.mod_f32, 1.0f) : 1.0f;
-    at[SUM_DZ_HH * a.n] = scale * t[SUM_DZ_HH];
-    at[SUM_DZ * a.n] = scale * t[SUM_DZ];
-    at[SUM_E_YH * a.n] = gate * t[SUM_E_YH];
-    at[SUM_E * a.n] = gate * t[SUM_E];
+    at[SUM_DZ_HH * a.n + j] = scale * t[SUM_DZ_HH];
+    at[SUM_DZ * a.n + j] = scale * t[SUM_DZ];
+    at[SUM_E_YH * a.n + j] = gate * t[SUM_E_YH];
+    at[SUM_E * a.n + j] = gate * t[SUM_E];
 }
 
 // The groups' shares joined.
-__global__ void __launch_bounds__(kSumLanes *kSumRows) k_block_sums_all(const BlockSumsArgs a) {
-    __shared__ float s[kSumRows][kSumLanes + 1];
-    const int64_t j = (int64_t)blockIdx.x * kSumLanes + threadIdx.x;
+template <int V>
+__global__ void __launch_bounds__(kSumColumns *kSumRows / V)
+k_block_sums_all(const BlockSumsArgs a) {
+    __shared__ float s[4][kSumRows][kSumColumns + 1], total[4][kSumColumns];
+    const int64_t col0 = (int64_t)blockIdx.x * kSumColumns;
     layer_pdl_launch();
     layer_pdl_wait();
+    sums_columns<V>(a, a.partial, a.groups, 4 * a.n * a.parts, col0, s, total);
+    const int64_t j = col0 + threadIdx.x;
+    if (threadIdx.x >= kSumColumns || j >= a.n) return;
     float t[4];
-    for (int k = 0; k < 4; ++k)
-        t[k] = a.need >> k & 1 ? sums_column(a.partial + k * a.n + j, a.groups,
-                                             4 * a.n * a.parts, j < a.n, s) : 0.0f;
-    if (threadIdx.y == 0 && j < a.n) sums_shared(a, j, t, true);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = total[k][threadIdx.x];
+    sums_shared(a, j, t, true);
 }
 
 }  // namespace ebin
@@ -207,19 +244,15 @@ int param_ranges(const ebin_block_norm_plan_s &p, const BlockArgs &a, Range *r) 
     return c;
 }
 
-cudaError_t launch_sums(void (*kernel)(const BlockSumsArgs), int64_t grid, const BlockSumsArgs &a,
-                        cudaStream_t s) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kSumLanes, kSumRows);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    count_launch();
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+cudaError_t launch_sums(const BlockSumsArgs &a, cudaStream_t s) {
+    const bool vec = a.n % 4 == 0;   // the workspace starts on 16 bytes
+    const int threads = kSumColumns * kSumRows / (vec ? 4 : 1);
+    const dim3 grid((unsigned)(a.tiles * a.groups)), tiles((unsigned)a.tiles);
+    cudaError_t e = launch_layer(vec ? k_block_sums<4> : k_block_sums<1>, grid, threads, 0, s, 1, a);
+    if (e == cudaSuccess && a.second)
+        e = launch_layer(vec ? k_block_sums_all<4> : k_block_sums_all<1>, tiles, threads, 0, s, 1,
+                         a);
+    return e;
 }
 
 // Whether every buffer of a call lies on vectors: rows that are whole vectors, each
@@ -354,9 +387,9 @@ extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *
     if (a.rows > 0) {
         p->group_rows = per ? per : a.rows;
         p->groups = a.rows / p->group_rows;
-        p->cta = cta_units(p->groups, p->group_rows, a.n, a.gradient ? kUnitGradVpt : kUnitVpt);
+        p->cta = cta_units(p->groups, p->group_rows, a.n, kUnitVpt);
         if (a.gradient) {
-            if (p->groups * div_up(a.n, kSumLanes) > 0x7FFFFFFF) {   // CTAs of the last step
+            if (p->groups * div_up(a.n, kSumColumns) > 0x7FFFFFFF) {   // CTAs of the last step
                 delete p;
                 return EBIN_ERR_INVALID_ARG;
             }
@@ -540,9 +573,7 @@ extern "C" ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan,
     b.second = p.groups > 1 && (g.w_post || g.b_post || g.w_pre || g.b_pre ||
                                 (!b.gate_grouped && g.gate) ||
                                 (!b.mod_grouped && (g.scale || g.shift)));
-    b.tiles = div_up(at.n, kSumLanes);
-    if (launch_sums(k_block_sums, b.tiles * p.groups, b, s) != cudaSuccess) return EBIN_ERR_CUDA;
-    if (b.second && launch_sums(k_block_sums_all, b.tiles, b, s) != cudaSuccess)
-        return EBIN_ERR_CUDA;
+    b.tiles = div_up(at.n, kSumColumns);
+    if (launch_sums(b, s) != cudaSuccess) return EBIN_ERR_CUDA;
     return EBIN_OK;
 }

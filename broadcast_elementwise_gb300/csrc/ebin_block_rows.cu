@@ -68,7 +68,7 @@ static bool cta_takes(const BlockArgs &a, int chunks, int vpt, bool vec) {
 // Its geometry, but for what lies in shared memory.
 static RowsGeom unit_geom(const BlockArgs &a, int chunks, int vpt) {
     RowsGeom g = rows_geom(a, chunks, vpt);
-    g.teams = 16 / g.warps;
+    g.teams = kUnitWarps / g.warps;
     g.units = a.groups * a.cta.parts;
     g.table = g.warps * vpt * 64;
     return g;
@@ -89,9 +89,8 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
         if (a.z && (a.scale || a.w_pre)) g.tables |= TABLE_H;
         if (a.z && (a.shift || a.b_pre)) g.tables |= TABLE_H_ADD;
         const size_t tables = 16 * (size_t)g.table * __builtin_popcount(g.tables);
-        const int threads = g.warps * g.teams * 32;
         g.vectors = kUnitVpt * (s_vectors + (a.y ? t_vectors : 0));
-        const size_t row = (size_t)threads * 16 * g.vectors;
+        const size_t row = (size_t)kUnitThreads * 16 * g.vectors;
         g.slots = rows_slots(row, tables, 1);
         if (g.slots > 0) {
             *parts = a.cta.parts;
@@ -134,28 +133,25 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
                          a.gate || a.w_post || a.branch_scale != 1.0f || a.drop.least};
     const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};
     const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
-    auto rows_at = [&](RowsGeom &g, int vpt) {   // a thread's vectors of a row
-        for (int k = 0; k < 4; ++k) {
-            g.at[k] = g.vectors;
-            if (there[k]) g.vectors += vpt * (k % 2 ? t_vectors : s_vectors);
-        }
-        return (size_t)g.warps * g.teams * 32 * 16 * g.vectors;
-    };
-    if (cta_takes(a, chunks, kUnitGradVpt, vec)) {
+    if (a.pre != EBIN_NORM_NONE && cta_takes(a, chunks, kUnitGradVpt, vec)) {
         RowsGeom g = unit_geom(a, chunks, kUnitGradVpt);
-        if (has[1]) g.tables |= TABLE_Y;
-        if (has[0]) g.tables |= TABLE_H;
-        const size_t tables = 16 * (size_t)g.table * (has[0] + has[1]);
-        const size_t row = rows_at(g, kUnitGradVpt);
-        g.slots = row ? rows_slots(row, tables, 1) : 1;
+        const size_t tables = 2 * 16 * (size_t)g.table;
+        g.vectors = kUnitGradVpt * (2 * s_vectors + (a.y ? 2 : 1) * t_vectors);
+        const size_t row = (size_t)g.vectors * 16 * kUnitThreads;
+        g.slots = rows_slots(row, tables, 1);
         if (g.slots > 0) {
             // the teams' sums at the end
-            const size_t sums = g.teams > 1 ? (size_t)(full ? 4 : 2) * kUnitGradVpt * 32 *
-                                                  g.warps * 32 : 0;
+            const size_t sums = g.teams > 1 ? (size_t)(full ? 4 : 2) * kUnitGradVpt *
+                                                  32 * g.warps * 32 : 0;
             const size_t smem = std::max(tables + g.slots * row, sums);
             *parts = a.cta.parts;
-            return full ? launch_rows<k_block_unit_grad<T, S, true>>(a, g, g.units, smem, s)
-                        : launch_rows<k_block_unit_grad<T, S, false>>(a, g, g.units, smem, s);
+            const bool post = a.post != EBIN_NORM_NONE;
+            if (full)
+                return post ? launch_rows<k_block_unit_grad<T, S, true, true>>(a, g, g.units, smem, s)
+                            : launch_rows<k_block_unit_grad<T, S, true, false>>(a, g, g.units, smem,
+                                                                               s);
+            return post ? launch_rows<k_block_unit_grad<T, S, false, true>>(a, g, g.units, smem, s)
+                        : launch_rows<k_block_unit_grad<T, S, false, false>>(a, g, g.units, smem, s);
         }
     }
     const int vpt = chunks > 32 ? 4 : 2;
@@ -169,7 +165,11 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
     const size_t factors = (size_t)threads * 16 * g.factors;
     size_t smem = factors;
     if (vec) {
-        const size_t row = rows_at(g, vpt);
+        for (int k = 0; k < 4; ++k) {
+            g.at[k] = g.vectors;
+            if (there[k]) g.vectors += vpt * (k % 2 ? t_vectors : s_vectors);
+        }
+        const size_t row = (size_t)g.vectors * 16 * threads;
         if (row > 0) {
             g.slots = rows_slots(row, factors, std::min(std::max(1, 512 / threads), 16));
             if (g.slots < 1) return cudaSuccess;

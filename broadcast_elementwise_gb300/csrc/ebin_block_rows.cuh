@@ -895,6 +895,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
 // which a row of weights in the L1 costs for each use ([8192,4096] bf16 with both
 // norms' weights: 60 us so, 48 without the weights).
 
+
 // A table of a factor for the lane's columns: the fours of chunk i, [2][32] vectors.
 template <class L> struct RowsTable {
     const float4 *at;   // this lane's first
@@ -951,28 +952,291 @@ enum RowsTables : int {
     TABLE_H_ADD = 8    // (1 + scale) b_pre + shift
 };
 
-constexpr int kUnitThreads = 512;
+// A lane's columns as RowsLane's with vectors, for all its chunks: those of chunk i
+// begin `stride` columns after those of chunk i - 1.
+template <class T, class S, int THREADS> struct UnitLane {
+    static constexpr bool WIDE = sizeof(S) == 4;
+    static constexpr int kStride = THREADS;   // vectors between a thread's in shared memory
+    int first, stride, n;   // the first column of chunk 0
+    int chunk;              // and the chunk's own
+
+    __device__ __forceinline__ void place(int lane, int warp, int warps, int n_) {
+        chunk = warp * kChunk;
+        first = chunk + lane * (WIDE ? 4 : 8);
+        stride = warps * kChunk;
+        n = n_;
+    }
+    // no column of chunk i lies in the row (the same for a whole warp; never of chunk 0)
+    __device__ __forceinline__ bool none(int i) const { return i && chunk + i * stride >= n; }
+    __device__ __forceinline__ int col(int i, int q) const {
+        return first + i * stride + (WIDE ? q * 128 : q * 4);
+    }
+    __device__ __forceinline__ bool on(int i, int q) const {
+        return first + i * stride + (WIDE ? q * 128 : 0) < n;
+    }
+    __device__ __forceinline__ float within(int i, const float2 *v) const {
+        const float2 a = __fadd2_rn(v[0], v[1]), b = __fadd2_rn(v[2], v[3]);
+        if constexpr (WIDE) {
+            return (on(i, 0) ? a.x + a.y : 0.0f) + (on(i, 1) ? b.x + b.y : 0.0f);
+        } else {
+            const float2 c = __fadd2_rn(a, b);
+            return on(i, 0) ? c.x + c.y : 0.0f;
+        }
+    }
+    // sum of the products of a and b
+    __device__ __forceinline__ float dot(int i, const float2 *a, const float2 *b) const {
+        if constexpr (WIDE) {
+            const float2 x = __ffma2_rn(a[1], b[1], __fmul2_rn(a[0], b[0]));
+            const float2 y = __ffma2_rn(a[3], b[3], __fmul2_rn(a[2], b[2]));
+            return (on(i, 0) ? x.x + x.y : 0.0f) + (on(i, 1) ? y.x + y.y : 0.0f);
+        } else {
+            float2 x = __fmul2_rn(a[0], b[0]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) x = __ffma2_rn(a[j], b[j], x);
+            return on(i, 0) ? x.x + x.y : 0.0f;
+        }
+    }
+    // to: the row's place in shared memory, [vectors][512]; row: at this lane's first column
+    template <class E>
+    __device__ __forceinline__ void fetch(int i, uint32_t to, const E *row) const {
+        row += i * stride;
+        if constexpr (!WIDE) {
+            if (on(i, 0)) rows_copy16(to, row);
+        } else if constexpr (sizeof(E) == 4) {
+            if (on(i, 0)) rows_copy16(to, row);
+            if (on(i, 1)) rows_copy16(to + kStride * 16, row + 128);
+        } else {
+            if (on(i, 0)) rows_copy8(to, row);
+            if (on(i, 1)) rows_copy8(to + 8, row + 128);
+        }
+    }
+    // Columns past the row's end are never copied to: zero, once, for good.
+    template <class E> __device__ __forceinline__ void clear(int i, uint4 *at) const {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if constexpr (!WIDE) {
+            if (!on(i, 0)) at[0] = zero;
+        } else if constexpr (sizeof(E) == 4) {
+            if (!on(i, 0)) at[0] = zero;
+            if (!on(i, 1)) at[kStride] = zero;
+        } else {
+            if (!on(i, 0)) reinterpret_cast<uint2 *>(at)[0] = make_uint2(0, 0);
+            if (!on(i, 1)) reinterpret_cast<uint2 *>(at)[1] = make_uint2(0, 0);
+        }
+    }
+    template <class E> __device__ __forceinline__ void store(int i, E *row, const float2 *v) const {
+        row += i * stride;
+        if constexpr (!WIDE && sizeof(E) == 2) {
+            if (on(i, 0))
+                *reinterpret_cast<uint4 *>(row) =
+                    make_uint4(pack2<E>(v[0]), pack2<E>(v[1]), pack2<E>(v[2]), pack2<E>(v[3]));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!on(i, q)) continue;
+                E *const p = row + (WIDE ? q * 128 : q * 4);
+                if constexpr (sizeof(E) == 4)
+                    *reinterpret_cast<float4 *>(p) =
+                        make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+                else
+                    *reinterpret_cast<uint2 *>(p) =
+                        make_uint2(pack2<E>(v[2 * q]), pack2<E>(v[2 * q + 1]));
+            }
+        }
+    }
+    // keep bits of chunk i, element e in bit e
+    __device__ __forceinline__ uint32_t kept(int i, const DropArgs &d, uint32_t row,
+                                             uint2 offset) const {
+        uint32_t r = 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint4 w = drop_words(d, (uint32_t)col(i, q) >> 2, row, offset);
+            r |= ((uint32_t)(w.x >= d.least) | (uint32_t)(w.y >= d.least) << 1 |
+                  (uint32_t)(w.z >= d.least) << 2 | (uint32_t)(w.w >= d.least) << 3) << (4 * q);
+        }
+        return r;
+    }
+    __device__ __forceinline__ void drop(int i, const DropArgs &d, uint32_t row, uint2 offset,
+                                         float2 *v) const {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint4 w = drop_words(d, (uint32_t)col(i, q) >> 2, row, offset);
+            v[2 * q].x = w.x >= d.least ? v[2 * q].x : 0.0f;
+            v[2 * q].y = w.y >= d.least ? v[2 * q].y : 0.0f;
+            v[2 * q + 1].x = w.z >= d.least ? v[2 * q + 1].x : 0.0f;
+            v[2 * q + 1].y = w.w >= d.least ? v[2 * q + 1].y : 0.0f;
+        }
+    }
+};
+
+// Four values' sums over a warp: lanes 8 k .. 8 k + 7 get that of v[k].  Six
+// exchanges: each halves what a lane still carries.
+__device__ __forceinline__ float warp_sums4(const float (&v)[4], int lane) {
+    const bool up = lane & 16;
+    float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+    a += __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
+    b += __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : v[3], 16);
+    const bool odd = lane & 8;
+    float r = odd ? b : a;
+    r += __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+    return r;
+}
+
+__device__ __forceinline__ float eighth_sums(float r) {   // over lanes 8 k .. 8 k + 7
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+    return r;
+}
+
+// A team of at most 16 warps, one of a CTA's: its exchanges go through [2][12][warps] floats
+// in turn, with a barrier each (1 .. 8; 0 is the CTA's, and teams of one warp have none).
+// In a join lane l stands for warps l % 8 and l % 8 + 8.
+struct UnitTeam {
+    int lane, warp, warps, id, half;
+    float *s;
+    float inv_n;
+
+    __device__ __forceinline__ void start(const RowsGeom &g, int n, float *sums) {
+        lane = threadIdx.x & 31;
+        warps = g.warps;
+        id = (threadIdx.x >> 5) / warps;
+        warp = (threadIdx.x >> 5) - id * warps;
+        s = sums + id * 24 * warps;
+        half = 0;
+        inv_n = 1.0f / (float)n;
+    }
+    __device__ __forceinline__ float *turn() {
+        half = half ? 0 : 12 * warps;
+        return s + half;
+    }
+    __device__ __forceinline__ void meet() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
+    }
+    // over the warps, of row k of what they left; the same in lanes 8 j .. 8 j + 7
+    __device__ __forceinline__ float join(const float *at, int k) const {
+        at += k * warps;
+        const int w = lane & 7;
+        float r = w < warps ? at[w] : 0.0f;
+        if (warps > 8) r += w + 8 < warps ? at[w + 8] : 0.0f;
+        return eighth_sums(r);
+    }
+    // the team's sum of v
+    __device__ __forceinline__ float sum(float v) {
+        float one[1] = {v};
+        warp_sums(one);
+        if (warps == 1) return one[0];
+        float *const at = turn();
+        if (lane == 0) at[warp] = one[0];
+        meet();
+        return join(at, 0);
+    }
+    // the team's sums of each v
+    template <int K> __device__ __forceinline__ void sums(float (&v)[K]) {
+        constexpr int G = (K + 3) / 4;
+        float r[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float four[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) four[k] = 4 * g + k < K ? v[4 * g + k] : 0.0f;
+            r[g] = warp_sums4(four, lane);
+        }
+        if (warps > 1) {
+            float *const at = turn();
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if ((lane & 7) == 0) at[(4 * g + (lane >> 3)) * warps + warp] = r[g];
+            meet();
+#pragma unroll
+            for (int g = 0; g < G; ++g) r[g] = join(at, 4 * g + (lane >> 3));
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, r[k / 4], 8 * (k % 4));
+    }
+};
+
+// (mean, 1 / deviation) of a row in registers: the mean first, then the squares about it
+// (a RMS norm: about 0).
+template <bool LAYER, class L, int VPT>
+__device__ __forceinline__ float2 unit_moments(UnitTeam &t, const L &l, const float2 (&v)[VPT][4],
+                                               int norm, float eps) {
+    float mean = 0.0f, q = 0.0f;
+    if (LAYER && norm == EBIN_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (!l.none(i)) s += l.within(i, v[i]);
+        mean = t.sum(s) * t.inv_n;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (l.none(i)) continue;
+        float2 d[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[k] = LAYER ? __fadd2_rn(v[i][k], two(-mean)) : v[i][k];
+        q += l.dot(i, d, d);
+    }
+    return make_float2(mean, rsqrtf(fmaf(t.sum(q), t.inv_n, eps)));
+}
+
+// A chunk of a thread's part of a row, as it lies in shared memory, and its pairs of
+// columns: unpacked where they are used, so that registers hold them packed.
+template <class E, int STRIDE> struct UnitWords {
+    static constexpr int N = sizeof(E) == 4 ? 2 : 1;   // vectors
+    uint4 w[N];
+    __device__ __forceinline__ void read(const uint4 *at) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = at[k * STRIDE];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ float2 pair(int j) const {
+        if constexpr (N == 2) {
+            const uint4 &x = w[j >> 1];
+            return j & 1 ? make_float2(__uint_as_float(x.z), __uint_as_float(x.w))
+                         : make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+        } else {
+            const uint4 &x = w[0];
+            return open2<E>(j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w);
+        }
+    }
+};
+
+// A tensor's rows on their way to shared memory: the next row, and its step.
+template <class E> struct RowsFrom {
+    const E *row;
+    int64_t step;
+    template <class L>
+    __device__ __forceinline__ RowsFrom(const L &l, const void *p, int64_t ld, int first, int rows)
+        : row(static_cast<const E *>(p) + (p ? first * ld + l.first : 0)), step(p ? rows * ld : 0) {}
+    template <int VPT, class L> __device__ __forceinline__ void fetch(const L &l, uint32_t to) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (!l.none(i)) l.fetch(i, to + i * RowsPart<L, E>::N * L::kStride * 16, row);
+        row += step;
+    }
+};
 
 template <class T, class S, bool LAYER>
 __global__ void __launch_bounds__(kUnitThreads, 1)
 k_block_unit(const BlockArgs a, const RowsGeom g) {
-    using Lane = RowsLane<T, S, true>;
+    using Lane = UnitLane<T, S, kUnitThreads>;
     using PartS = RowsPart<Lane, S>;
     using PartT = RowsPart<Lane, T>;
-    constexpr int VPT = kUnitVpt;
-    __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
-    extern __shared__ uint4 s_rows[];   // the tables, then [slots][vectors of a thread][threads]
-    constexpr int kX = VPT * PartS::N;
-    Team<true> t;
-    t.template start<VPT>(g, (int)a.n, s_sums);
-    Lane l[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        l[i].place(t.lane, (i * g.warps + t.warp) * kChunk, (int)a.n);
+    constexpr int VPT = kUnitVpt, kX = VPT * PartS::N;
+    __shared__ float s_sums[24 * kUnitWarps];
+    extern __shared__ uint4 s_rows[];   // the tables, then [slots][vectors of a thread][512]
+    UnitTeam t;
+    t.start(g, (int)a.n, s_sums);
+    Lane l;
+    l.place(t.lane, t.warp, g.warps, (int)a.n);
     const int64_t unit = blockIdx.x, group = unit / a.cta.parts, part = unit - group * a.cta.parts;
     const int r0 = (int)(group * a.group_rows + part * a.cta.rows);
     const int r1 = (int)min(r0 + a.cta.rows, (group + 1) * a.group_rows);
-    const int threads = blockDim.x, step = g.teams;
+    const int step = g.teams;
     const bool post = a.post != EBIN_NORM_NONE;
     const float branch = a.branch_scale * (a.drop.least ? a.drop.scale : 1.0f);
     float4 *table = reinterpret_cast<float4 *>(s_rows);
@@ -984,29 +1248,22 @@ k_block_unit(const BlockArgs a, const RowsGeom g) {
     }
     uint4 *const mine = reinterpret_cast<uint4 *>(table) + threadIdx.x;
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
+    const int ahead = g.slots - 1, slot_vectors = g.vectors * kUnitThreads;
+    const int last = ahead * slot_vectors;
+    int fill = 0, slot = 0, next = r0 + t.id;
+    RowsFrom<S> from_x(l, a.x, a.ld_x, next, step);
+    RowsFrom<T> from_y(l, a.y, a.ld_y, next, step);
     layer_pdl_launch();
     layer_pdl_wait();
     const uint2 offset = drop_offset(a.drop);
-    const int ahead = g.slots - 1, vectors = g.vectors;
-    int fill = 0, slot = 0, next = r0 + t.id;
     auto fetch = [&]() {
         if (next < r1) {
-            const uint32_t at = to + fill * vectors * threads * 16;
-            const S *const x = static_cast<const S *>(a.x) + next * a.ld_x;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (!i || !l[i].none())
-                    PartS::fetch(l[i], at + i * PartS::N * threads * 16, threads, x);
-            if (a.y) {
-                const T *const y = static_cast<const T *>(a.y) + next * a.ld_y;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    if (!i || !l[i].none())
-                        PartT::fetch(l[i], at + (kX + i * PartT::N) * threads * 16, threads, y);
-            }
+            const uint32_t at = to + fill * 16;
+            from_x.template fetch<VPT>(l, at);
+            if (a.y) from_y.template fetch<VPT>(l, at + kX * kUnitThreads * 16);
             next += step;
         }
-        fill = fill + 1 == g.slots ? 0 : fill + 1;
+        fill = fill == last ? 0 : fill + slot_vectors;
         rows_commit();
     };
     for (int i = 0; i < ahead; ++i) fetch();
@@ -1034,33 +1291,35 @@ k_block_unit(const BlockArgs a, const RowsGeom g) {
         }
     }
     __syncthreads();
-    for (int row = r0 + t.id; row < r1; row += step) {
+    S *h = static_cast<S *>(a.h) + (a.h ? (r0 + t.id) * a.ld_h + l.first : 0);
+    T *z = static_cast<T *>(a.z) + (a.z ? (r0 + t.id) * a.ld_z + l.first : 0);
+    const int64_t step_h = step * a.ld_h, step_z = step * a.ld_z;
+    for (int row = r0 + t.id; row < r1; row += step, h += step_h, z += step_z) {
         fetch();
         rows_wait(ahead);
-        const uint4 *const at = mine + slot * vectors * threads;
-        slot = slot + 1 == g.slots ? 0 : slot + 1;
+        const uint4 *const at = mine + slot;
+        slot = slot == last ? 0 : slot + slot_vectors;
         float2 v[VPT][4];
         float2 my = make_float2(0.0f, 1.0f);
         if (a.y) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                if (i && l[i].none()) continue;
-                PartT::open(at + (kX + i * PartT::N) * threads, threads, v[i]);
+                if (l.none(i)) continue;
+                PartT::open(at + (kX + i * PartT::N) * kUnitThreads, kUnitThreads, v[i]);
             }
-            if (post) my = row_moments<LAYER>(t, l, v, a.post, a.eps_post);
+            if (post) my = unit_moments<LAYER>(t, l, v, a.post, a.eps_post);
         }
-        S *const h = static_cast<S *>(a.h) + row * a.ld_h;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (i && l[i].none()) continue;
+            if (l.none(i)) continue;
             float2 x[4];
-            PartS::open(at + i * PartS::N * threads, threads, x);
+            PartS::open(at + i * PartS::N * kUnitThreads, kUnitThreads, x);
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], two(a.stream_scale));
             if (a.y) {
                 if (post) norm8<LAYER>(v[i], my);
                 if (!(g.tables & TABLE_Y_ADD)) {
-                    if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, v[i]);
+                    if (a.drop.least) l.drop(i, a.drop, (uint32_t)row, offset, v[i]);
                     if (g.tables & TABLE_Y) {
                         float2 p[4];
                         by[0].read(i, p);
@@ -1070,26 +1329,24 @@ k_block_unit(const BlockArgs a, const RowsGeom g) {
                         add8(x, v[i]);
                     }
                 } else {   // with a bias the mask comes after the factor
-                    float2 p[4];
-                    by[1].read(i, p);
-                    float2 q[4];
+                    float2 p[4], q[4];
                     by[0].read(i, q);
+                    by[1].read(i, p);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[i][k] = __ffma2_rn(v[i][k], q[k], p[k]);
-                    if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, v[i]);
+                    if (a.drop.least) l.drop(i, a.drop, (uint32_t)row, offset, v[i]);
                     add8(x, v[i]);
                 }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][k] = x[k];
-            if (a.h) l[i].store(h, v[i]);
+            if (a.h) l.store(i, h, v[i]);
         }
         if (!a.z) continue;
-        const float2 mh = row_moments<LAYER>(t, l, v, a.pre, a.eps_pre);
-        T *const z = static_cast<T *>(a.z) + row * a.ld_z;
+        const float2 mh = unit_moments<LAYER>(t, l, v, a.pre, a.eps_pre);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (i && l[i].none()) continue;
+            if (l.none(i)) continue;
             norm8<LAYER>(v[i], mh);
             if (g.tables & TABLE_H) by[2].times(i, v[i]);
             if (g.tables & TABLE_H_ADD) {
@@ -1097,81 +1354,77 @@ k_block_unit(const BlockArgs a, const RowsGeom g) {
                 by[3].read(i, p);
                 add8(v[i], p);
             }
-            l[i].store(z, v[i]);
+            l.store(i, z, v[i]);
         }
     }
     rows_wait(0);
 }
 
-// The gradient of such units; its sums in registers as k_block_rows_grad's, the
-// teams' joined in shared memory at the end, one after another.
+__device__ __forceinline__ float2 mask2(float2 v, uint32_t bits, int j) {
+    return make_float2(bits >> (2 * j) & 1 ? v.x : 0.0f, bits >> (2 * j + 1) & 1 ? v.y : 0.0f);
+}
 
-template <class T, class S, bool FULL>
+// The gradient of such units, with a pre norm; its sums in registers as
+// k_block_rows_grad's, the teams' joined in shared memory at the end, one after another.
+// A row takes one exchange (FULL, with a layer norm: one more before it, of the means).
+// What dy needs of D before D is known comes from D's parts: with t = (factor of y) (y
+// - mean) the mean of u yh is that of t D, and
+//     sum t D = sum t dh + r (sum t m - c0 sum t - r c1 sum t (h - mean)),
+// c0 and c1 the means of m and of m hh; so nothing of a row is kept in registers from
+// the sums' pass to the outputs'.  Both factors have tables.
+template <class T, class S, bool FULL, bool POST>
 __global__ void __launch_bounds__(kUnitThreads, 1)
 k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
-    using Lane = RowsLane<T, S, true>;
-    using PartS = RowsPart<Lane, S>;
-    using PartT = RowsPart<Lane, T>;
+    using Lane = UnitLane<T, S, kUnitThreads>;
+    using WordsS = UnitWords<S, kUnitThreads>;
+    using WordsT = UnitWords<T, kUnitThreads>;
     constexpr int VPT = kUnitGradVpt, kKinds = FULL ? 4 : 2;
-    __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
+    __shared__ float s_sums[24 * kUnitWarps];
     extern __shared__ uint4 s_rows[];   // the tables, then the rows; at the end the sums
-    Team<true> t;
-    t.template start<VPT>(g, (int)a.n, s_sums);
-    Lane l[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        l[i].place(t.lane, (i * g.warps + t.warp) * kChunk, (int)a.n);
+    UnitTeam t;
+    t.start(g, (int)a.n, s_sums);
+    Lane l;
+    l.place(t.lane, t.warp, g.warps, (int)a.n);
     const int64_t unit = blockIdx.x, group = unit / a.cta.parts, part = unit - group * a.cta.parts;
     const int r0 = (int)(group * a.group_rows + part * a.cta.rows);
     const int r1 = (int)min(r0 + a.cta.rows, (group + 1) * a.group_rows);
-    const int threads = blockDim.x, step = g.teams;
-    const bool pre = a.pre != EBIN_NORM_NONE, post = a.post != EBIN_NORM_NONE;
+    const int step = g.teams;
     const bool layer_h = FULL && a.pre == EBIN_NORM_LAYER;
-    const bool layer_y = FULL && a.post == EBIN_NORM_LAYER;
+    const bool layer_y = FULL && POST && a.post == EBIN_NORM_LAYER;
     const float branch = a.branch_scale * (a.drop.least ? a.drop.scale : 1.0f);
-    float4 *table = reinterpret_cast<float4 *>(s_rows);
-    RowsTable<Lane> by_y{table + t.warp * 64 + t.lane, g.warps};
-    if (g.tables & TABLE_Y) table += g.table;
-    RowsTable<Lane> by_h{table + t.warp * 64 + t.lane, g.warps};
-    if (g.tables & TABLE_H) table += g.table;
-    uint4 *const mine = reinterpret_cast<uint4 *>(table) + threadIdx.x;
+    float4 *const tables = reinterpret_cast<float4 *>(s_rows);
+    const float4 *const by_y = tables + t.warp * 64 + t.lane, *const by_h = by_y + g.table;
+    const int table_step = g.warps * 64;
+    uint4 *const mine = s_rows + 2 * g.table + threadIdx.x;
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
+    const int ahead = g.slots - 1, slot_vectors = g.vectors * kUnitThreads;
+    const int last = ahead * slot_vectors;
+    int fill = 0, slot = 0, next = r0 + t.id;
+    RowsFrom<S> from_h(l, a.x, a.ld_x, next, step), from_dh(l, a.dh, a.ld_dh, next, step);
+    RowsFrom<T> from_dz(l, a.dz, a.ld_dz, next, step), from_y(l, a.y, a.ld_y, next, step);
     layer_pdl_launch();
     layer_pdl_wait();
     const uint2 offset = drop_offset(a.drop);
-    const int ahead = g.slots - 1;
-    int fill = 0, slot = 0, next = r0 + t.id;
+    // h, dz, dh and y of a row lie behind one another
+    constexpr int kDz = VPT * WordsS::N, kDh = kDz + VPT * WordsT::N, kY = kDh + VPT * WordsS::N;
+    for (uint4 *p = mine; p <= mine + last; p += slot_vectors)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            l.template clear<S>(i, p + i * WordsS::N * kUnitThreads);
+            l.template clear<T>(i, p + (kDz + i * WordsT::N) * kUnitThreads);
+            l.template clear<S>(i, p + (kDh + i * WordsS::N) * kUnitThreads);
+            if (a.y) l.template clear<T>(i, p + (kY + i * WordsT::N) * kUnitThreads);
+        }
     auto fetch = [&]() {
         if (next < r1) {
-            const uint32_t at = to + fill * g.vectors * threads * 16;
-            const uint32_t s_step = PartS::N * threads * 16, t_step = PartT::N * threads * 16;
-            if (a.x) {
-                const S *const p = static_cast<const S *>(a.x) + next * a.ld_x;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    PartS::fetch(l[i], at + g.at[0] * threads * 16 + i * s_step, threads, p);
-            }
-            if (a.dz) {
-                const T *const p = static_cast<const T *>(a.dz) + next * a.ld_dz;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    PartT::fetch(l[i], at + g.at[1] * threads * 16 + i * t_step, threads, p);
-            }
-            if (a.dh) {
-                const S *const p = static_cast<const S *>(a.dh) + next * a.ld_dh;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    PartS::fetch(l[i], at + g.at[2] * threads * 16 + i * s_step, threads, p);
-            }
-            if (a.y) {
-                const T *const p = static_cast<const T *>(a.y) + next * a.ld_y;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    PartT::fetch(l[i], at + g.at[3] * threads * 16 + i * t_step, threads, p);
-            }
+            const uint32_t at = to + fill * 16;
+            from_h.template fetch<VPT>(l, at);
+            from_dz.template fetch<VPT>(l, at + kDz * (kUnitThreads * 16));
+            if (a.dh) from_dh.template fetch<VPT>(l, at + kDh * (kUnitThreads * 16));
+            if (a.y) from_y.template fetch<VPT>(l, at + kY * (kUnitThreads * 16));
             next += step;
         }
-        fill = fill + 1 == g.slots ? 0 : fill + 1;
+        fill = fill == last ? 0 : fill + slot_vectors;
         rows_commit();
     };
     for (int i = 0; i < ahead; ++i) fetch();
@@ -1181,19 +1434,14 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
         const void *const gate = block_row<T>(a.gate, index * a.ld_gate, a.mod_f32);
         g.mod.split((uint32_t)r0, index, rest);
         const void *const scale = block_row<T>(a.scale, index * a.ld_scale, a.mod_f32);
-        float4 *at = reinterpret_cast<float4 *>(s_rows);
-        if (g.tables & TABLE_Y) {
-            rows_fill<Lane>(at, g.table, (int)a.n, [&](int col) {
-                return mul4(mul4(four(branch), params4<T>(gate, col, a.mod_f32, 1.0f)),
-                            params4<T>(a.w_post, col, a.w_f32, 1.0f));
-            });
-            at += g.table;
-        }
-        if (g.tables & TABLE_H)
-            rows_fill<Lane>(at, g.table, (int)a.n, [&](int col) {
-                return mul4(add4(four(1.0f), params4<T>(scale, col, a.mod_f32, 0.0f)),
-                            params4<T>(a.w_pre, col, a.w_f32, 1.0f));
-            });
+        rows_fill<Lane>(tables, g.table, (int)a.n, [&](int col) {
+            return mul4(mul4(four(branch), params4<T>(gate, col, a.mod_f32, 1.0f)),
+                        params4<T>(a.w_post, col, a.w_f32, 1.0f));
+        });
+        rows_fill<Lane>(tables + g.table, g.table, (int)a.n, [&](int col) {
+            return mul4(add4(four(1.0f), params4<T>(scale, col, a.mod_f32, 0.0f)),
+                        params4<T>(a.w_pre, col, a.w_f32, 1.0f));
+        });
     }
     __syncthreads();
     float2 acc[kKinds][VPT][4];
@@ -1203,171 +1451,202 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[k][i][j] = two(0.0f);
-    auto place = [](int kind) { return FULL ? kind : kind >> 1; };
-    for (int row = r0 + t.id; row < r1; row += step) {
+    constexpr int kEYh = FULL ? (int)SUM_E_YH : 1;
+    T *dy = static_cast<T *>(a.z) + (a.z ? (r0 + t.id) * a.ld_z + l.first : 0);
+    S *dx = static_cast<S *>(a.h) + (a.h ? (r0 + t.id) * a.ld_h + l.first : 0);
+    const int64_t step_y = step * a.ld_z, step_x = step * a.ld_h;
+    auto factor = [&](const float4 *table, int i, float2 *p) {
+        const float4 x = table[i * table_step], y = table[i * table_step + 32];
+        p[0] = make_float2(x.x, x.y);
+        p[1] = make_float2(x.z, x.w);
+        p[2] = make_float2(y.x, y.y);
+        p[3] = make_float2(y.z, y.w);
+    };
+    for (int row = r0 + t.id; row < r1; row += step, dy += step_y, dx += step_x) {
         fetch();
         rows_wait(ahead);
-        const uint4 *const at = mine + slot * g.vectors * threads;
-        slot = slot + 1 == g.slots ? 0 : slot + 1;
-        const uint4 *const at_h = at + g.at[0] * threads, *const at_dz = at + g.at[1] * threads;
-        const uint4 *const at_dh = at + g.at[2] * threads, *const at_y = at + g.at[3] * threads;
-        auto open_s = [&](const uint4 *p, int i, float2 *v) {
-            PartS::open(p + i * PartS::N * threads, threads, v);
-        };
-        auto open_t = [&](const uint4 *p, int i, float2 *v) {
-            PartT::open(p + i * PartT::N * threads, threads, v);
-        };
-        // this warp's sums of the squares of h about their mean, of m with h less that
-        // mean, of the squares of y; FULL: of m, of h and of y
-        float w[FULL ? 6 : 3] = {};
-        float2 v[VPT][4];   // m, then D
-        float mean_h = 0.0f, mean_y = 0.0f;
+        const uint4 *const at = mine + slot;
+        slot = slot == last ? 0 : slot + slot_vectors;
+        auto at_h = [&](int i) { return at + i * WordsS::N * kUnitThreads; };
+        auto at_dz = [&](int i) { return at + (kDz + i * WordsT::N) * kUnitThreads; };
+        auto at_dh = [&](int i) { return at + (kDh + i * WordsS::N) * kUnitThreads; };
+        auto at_y = [&](int i) { return at + (kY + i * WordsT::N) * kUnitThreads; };
+        float2 mh = make_float2(0.0f, 1.0f), my = mh;
+        float c0 = 0.0f, c1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
         if (FULL && (layer_h || layer_y)) {
-            float s[2] = {0.0f, 0.0f};
+            float2 s[3] = {two(0.0f), two(0.0f), two(0.0f)};   // of h, y and m: 0 past the row
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                float2 x[4];
-                if (layer_h) {
-                    open_s(at_h, i, x);
-                    s[0] += l[i].within(x);
-                }
-                if (layer_y) {
-                    open_t(at_y, i, x);
-                    s[1] += l[i].within(x);
-                }
-            }
-            warp_sums(s);
-            w[FULL ? 4 : 0] = s[0];
-            w[FULL ? 5 : 0] = s[1];
-            mean_h = s[0] * t.inv_mine;
-            mean_y = s[1] * t.inv_mine;
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (pre) {
-                float2 h[4], c[4];
-                open_t(at_dz, i, v[i]);
-                if (g.tables & TABLE_H) by_h.times(i, v[i]);
-                open_s(at_h, i, h);
-                if constexpr (FULL) {
-                    w[3] += l[i].within(v[i]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = __fadd2_rn(h[j], two(-mean_h));
-                }
-                w[0] += squares8<false>(l[i], h, 0.0f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[j] = __fmul2_rn(v[i][j], h[j]);
-                w[1] += l[i].within(c);
-            }
-            if (post) {
-                float2 y[4];
-                open_t(at_y, i, y);
-                w[2] += squares8<FULL>(l[i], y, mean_y);
-            }
-        }
-        float2 mh = make_float2(0.0f, 1.0f), my = mh;
-        float c0 = 0.0f, c1 = 0.0f;   // means of m and of m hh
-        if (pre || post) {
-            if constexpr (FULL) {
-                float q[4] = {w[0], w[1], w[2], w[3]};
-                warp_sums(q);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = q[k];
-            } else {
-                warp_sums(w);
-            }
-            t.gather(w);
-            if (pre) {
-                mh = t.moments(FULL ? w[FULL ? 4 : 0] : 0.0f, w[0], layer_h, a.eps_pre);
-                if constexpr (FULL) {
-                    // the products about the row's mean
-                    float c[2] = {w[3], w[1]};
-                    if (layer_h) c[1] = fmaf(w[3], fmaf(w[4], t.inv_count, -mh.x), c[1]);
-                    t.join(c);
-                    c0 = layer_h ? c[0] * t.inv_n : 0.0f;
-                    c1 = c[1] * mh.y * t.inv_n;
-                } else {
-                    float c[1] = {w[1]};
-                    t.join(c);
-                    c1 = c[0] * mh.y * t.inv_n;
-                }
-            }
-            if (post) my = t.moments(FULL ? w[FULL ? 5 : 0] : 0.0f, w[2], layer_y, a.eps_post);
-        }
-        float2 u[VPT][4];
-        float b[FULL ? 2 : 1] = {};   // sums of u yh and (FULL) of u
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            float2 d[4], yh[4];
-            if (a.dh) open_s(at_dh, i, d);
-            else d[0] = d[1] = d[2] = d[3] = two(0.0f);
-            if (pre) {
-                float2 h[4], dz[4];
-                open_s(at_h, i, h);
-                norm8<FULL>(h, mh);
+                if (l.none(i)) continue;
+                WordsS h;
+                WordsT z, y;
+                float2 k[4];
+                h.read(at_h(i));
+                z.read(at_dz(i));
+                if (POST) y.read(at_y(i));
+                factor(by_h, i, k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float2 m = v[i][j];
-                    if constexpr (FULL) m = __fadd2_rn(m, two(-c0));
-                    d[j] = __ffma2_rn(__ffma2_rn(h[j], two(-c1), m), two(mh.y), d[j]);
-                }
-                open_t(at_dz, i, dz);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[0][i][j] = __ffma2_rn(dz[j], h[j], acc[0][i][j]);
-                    if constexpr (FULL) acc[1][i][j] = __fadd2_rn(acc[1][i][j], dz[j]);
+                    s[0] = __fadd2_rn(s[0], h.pair(j));
+                    if (POST) s[1] = __fadd2_rn(s[1], y.pair(j));
+                    s[2] = __ffma2_rn(z.pair(j), k[j], s[2]);
                 }
             }
+            float q[3];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = u[i][j] = d[j];
-            // e / branch, then u
-            if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, u[i]);
-            if (a.y) {
-                open_t(at_y, i, yh);
-                if (post) norm8<FULL>(yh, my);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[place(SUM_E_YH)][i][j] = __ffma2_rn(u[i][j], yh[j],
-                                                            acc[place(SUM_E_YH)][i][j]);
+            for (int k = 0; k < 3; ++k) q[k] = s[k].x + s[k].y;
+            t.sums(q);
+            if (layer_h) {
+                mh.x = q[0] * t.inv_n;
+                c0 = q[2] * t.inv_n;
             }
-            if constexpr (FULL) add8(acc[kKinds - 1][i], u[i]);
-            if (g.tables & TABLE_Y) by_y.times(i, u[i]);
-            if (post) {
-                if constexpr (FULL) b[FULL ? 1 : 0] += l[i].within(u[i]);
-                mul8(yh, u[i]);
-                b[0] += l[i].within(yh);
-            }
+            if (layer_y) my.x = q[1] * t.inv_n;
         }
-        float b0 = 0.0f, b1 = 0.0f;
-        if (post) {
-            warp_sums(b);
-            t.gather(b);
-            t.join(b);
-            b0 = b[0] * t.inv_n;
-            b1 = layer_y ? b[FULL ? 1 : 0] * t.inv_n : 0.0f;
-        }
-        T *const dy = static_cast<T *>(a.z) + row * a.ld_z;
-        S *const dx = static_cast<S *>(a.h) + row * a.ld_h;
+        uint32_t bits[VPT];   // POST: what is kept
+        {
+            // sums of h h, m h, y y, t dh, t m, t h, then (FULL) of t, f dh, f m, f h and f, the
+            // factor; h and y less their means
+            constexpr int K = !POST ? 2 : FULL ? 11 : 6;
+            float2 q[K];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (a.z) {
-                if (post) {
-                    float2 yh[4];
-                    open_t(at_y, i, yh);
-                    norm8<FULL>(yh, my);
+            for (int k = 0; k < K; ++k) q[k] = two(0.0f);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if constexpr (FULL) u[i][j] = __fadd2_rn(u[i][j], two(-b1));
-                        u[i][j] = __fmul2_rn(__ffma2_rn(yh[j], two(-b0), u[i][j]), two(my.y));
+            for (int i = 0; i < VPT; ++i) {
+                if (l.none(i)) continue;
+                WordsS h, d;
+                WordsT z, y;
+                float2 k[4], f[4];
+                h.read(at_h(i));
+                z.read(at_dz(i));
+                factor(by_h, i, k);
+                if constexpr (POST) {
+                    y.read(at_y(i));
+                    if (a.dh) d.read(at_dh(i));
+                    else d.zero();
+                    factor(by_y, i, f);
+                    if (a.drop.least) {
+                        bits[i] = l.kept(i, a.drop, (uint32_t)row, offset);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) f[j] = mask2(f[j], bits[i], j);
                     }
                 }
-                l[i].store(dy, u[i]);
-            }
-            if (a.h) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(v[i][j], two(a.stream_scale));
-                l[i].store(dx, v[i]);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 m = __fmul2_rn(z.pair(j), k[j]);
+                    float2 x = h.pair(j);
+                    if constexpr (FULL) {   // past the row's end still 0
+                        x = __fadd2_rn(x, two(-mh.x));
+                        if (!l.on(i, j >> 1)) x = two(0.0f);
+                    }
+                    q[0] = __ffma2_rn(x, x, q[0]);
+                    q[1] = __ffma2_rn(m, x, q[1]);
+                    if constexpr (POST) {
+                        float2 yy = y.pair(j);
+                        const float2 dh = d.pair(j);
+                        if constexpr (FULL) {
+                            yy = __fadd2_rn(yy, two(-my.x));
+                            if (!l.on(i, j >> 1)) yy = two(0.0f);
+                        }
+                        q[2] = __ffma2_rn(yy, yy, q[2]);
+                        const float2 tt = __fmul2_rn(yy, f[j]);
+                        q[3] = __ffma2_rn(tt, dh, q[3]);
+                        q[4] = __ffma2_rn(tt, m, q[4]);
+                        q[5] = __ffma2_rn(tt, x, q[5]);
+                        if constexpr (FULL) {
+                            q[6] = __fadd2_rn(q[6], tt);
+                            q[7] = __ffma2_rn(f[j], dh, q[7]);
+                            q[8] = __ffma2_rn(f[j], m, q[8]);
+                            q[9] = __ffma2_rn(f[j], x, q[9]);
+                            q[10] = __fadd2_rn(q[10], f[j]);
+                        }
+                    }
+                }
             }
+            float w[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k] = q[k].x + q[k].y;
+            t.sums(w);
+            mh.y = rsqrtf(fmaf(w[0], t.inv_n, a.eps_pre));
+            c1 = w[1] * mh.y * t.inv_n;
+            if constexpr (POST) {
+                my.y = rsqrtf(fmaf(w[2], t.inv_n, a.eps_post));
+                const float back = mh.y * c1;
+                float d = fmaf(-back, w[5], w[4]);
+                if constexpr (FULL) d = fmaf(-c0, w[6], d);
+                b0 = fmaf(mh.y, d, w[3]) * my.y * t.inv_n;
+                if (FULL && layer_y) {
+                    d = fmaf(-c0, w[FULL ? 10 : 0], fmaf(-back, w[FULL ? 9 : 0], w[FULL ? 8 : 0]));
+                    b1 = fmaf(mh.y, d, w[FULL ? 7 : 0]) * t.inv_n;
+                }
+            }
+        }
+        const float2 rh = two(mh.y), ry = two(my.y), down = two(-c1), off = two(-b0);
+        const float2 rb = two(-b1 * my.y);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (l.none(i)) continue;
+            float2 v[4];   // D, then e, then u and dy
+            {
+                WordsS h, d;
+                WordsT z;
+                float2 k[4];
+                h.read(at_h(i));
+                z.read(at_dz(i));
+                if (a.dh) d.read(at_dh(i));
+                else d.zero();
+                factor(by_h, i, k);
+                float2 out[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 x = h.pair(j);
+                    if constexpr (FULL) x = __fadd2_rn(x, two(-mh.x));
+                    x = __fmul2_rn(x, rh);
+                    const float2 dz = z.pair(j);
+                    acc[0][i][j] = __ffma2_rn(dz, x, acc[0][i][j]);
+                    float2 m;
+                    if constexpr (FULL) {
+                        acc[1][i][j] = __fadd2_rn(acc[1][i][j], dz);
+                        m = __ffma2_rn(dz, k[j], two(-c0));
+                    } else {
+                        m = __fmul2_rn(dz, k[j]);
+                    }
+                    v[j] = __ffma2_rn(__ffma2_rn(x, down, m), rh, d.pair(j));
+                    out[j] = __fmul2_rn(v[j], two(a.stream_scale));
+                }
+                if (a.h) l.store(i, dx, out);
+            }
+            if (a.drop.least) {
+                if constexpr (POST) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = mask2(v[j], bits[i], j);
+                } else {
+                    l.drop(i, a.drop, (uint32_t)row, offset, v);
+                }
+            }
+            if constexpr (FULL) add8(acc[kKinds - 1][i], v);
+            float2 f[4];
+            factor(by_y, i, f);
+            if (POST || a.y) {
+                WordsT y;
+                y.read(at_y(i));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 x = y.pair(j);
+                    if constexpr (POST) {
+                        if constexpr (FULL) x = __fadd2_rn(x, two(-my.x));
+                        x = __fmul2_rn(x, ry);
+                    }
+                    acc[kEYh][i][j] = __ffma2_rn(v[j], x, acc[kEYh][i][j]);
+                    v[j] = __fmul2_rn(v[j], f[j]);
+                    if constexpr (POST) {
+                        v[j] = __ffma2_rn(x, off, v[j]);
+                        v[j] = FULL ? __ffma2_rn(v[j], ry, rb) : __fmul2_rn(v[j], ry);
+                    }
+                }
+            } else {
+                mul8(v, f);
+            }
+            if (a.z) l.store(i, dy, v);
         }
     }
     rows_wait(0);
@@ -1377,11 +1656,12 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
     for (int team = 0; team < g.teams; ++team) {
         __syncthreads();   // the rows have been read; the team before has added
         if (t.id != team) continue;
-        float *const partial = a.partial + unit * 4 * a.n;
+        float *const partial = a.partial + unit * 4 * a.n + l.first;
 #pragma unroll
         for (int k = 0; k < kKinds; ++k)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
+                if (l.none(i)) continue;
                 float2 *const at = sums + (k * VPT + i) * 4 * team_threads;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1394,7 +1674,7 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[k][i][j] = __fmul2_rn(acc[k][i][j], two(branch));
                 }
-                l[i].store(partial + kind * a.n, acc[k][i]);
+                l.store(i, partial + kind * a.n, acc[k][i]);
             }
     }
 }
