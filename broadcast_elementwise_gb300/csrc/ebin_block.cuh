@@ -13,7 +13,9 @@ struct BlockUnits {
 };
 
 // The kernels of CTAs' units: chunks of 256 columns that a lane owns, threads and warps.
-constexpr int kUnitVpt = 4, kUnitGradVpt = 2, kUnitThreads = 512, kUnitWarps = kUnitThreads / 32;
+constexpr int kUnitVpt = 4, kUnitThreads = 512, kUnitWarps = kUnitThreads / 32;
+// A gradient's: what it keeps of a column fits 128 registers (MORE: with two layer norms).
+template <bool MORE> constexpr int kUnitGradVpt = MORE ? 1 : 2;
 
 struct BlockArgs {
     // forward: x, y -> h, z; gradient: dz, dh, h, y -> dx, dy

@@ -133,19 +133,21 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
                          a.gate || a.w_post || a.branch_scale != 1.0f || a.drop.least};
     const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};
     const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
-    if (a.pre != EBIN_NORM_NONE && cta_takes(a, chunks, kUnitGradVpt, vec)) {
-        RowsGeom g = unit_geom(a, chunks, kUnitGradVpt);
+    const bool post = a.post != EBIN_NORM_NONE;
+    const int unit_vpt = full && post ? kUnitGradVpt<true> : kUnitGradVpt<false>;
+    if (a.pre != EBIN_NORM_NONE && div_up(chunks, unit_vpt) <= kUnitWarps &&
+        cta_takes(a, chunks, unit_vpt, vec)) {
+        RowsGeom g = unit_geom(a, chunks, unit_vpt);
         const size_t tables = 2 * 16 * (size_t)g.table;
-        g.vectors = kUnitGradVpt * (2 * s_vectors + (a.y ? 2 : 1) * t_vectors);
+        g.vectors = unit_vpt * (2 * s_vectors + (a.y ? 2 : 1) * t_vectors);
         const size_t row = (size_t)g.vectors * 16 * kUnitThreads;
         g.slots = rows_slots(row, tables, 1);
         if (g.slots > 0) {
             // the teams' sums at the end
-            const size_t sums = g.teams > 1 ? (size_t)(full ? 4 : 2) * kUnitGradVpt *
+            const size_t sums = g.teams > 1 ? (size_t)(full ? 4 : 2) * unit_vpt *
                                                   32 * g.warps * 32 : 0;
             const size_t smem = std::max(tables + g.slots * row, sums);
             *parts = a.cta.parts;
-            const bool post = a.post != EBIN_NORM_NONE;
             if (full)
                 return post ? launch_rows<k_block_unit_grad<T, S, true, true>>(a, g, g.units, smem, s)
                             : launch_rows<k_block_unit_grad<T, S, true, false>>(a, g, g.units, smem,

@@ -1378,7 +1378,7 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
     using Lane = UnitLane<T, S, kUnitThreads>;
     using WordsS = UnitWords<S, kUnitThreads>;
     using WordsT = UnitWords<T, kUnitThreads>;
-    constexpr int VPT = kUnitGradVpt, kKinds = FULL ? 4 : 2;
+    constexpr int VPT = kUnitGradVpt<FULL && POST>, kKinds = FULL ? 4 : 2;
     __shared__ float s_sums[24 * kUnitWarps];
     extern __shared__ uint4 s_rows[];   // the tables, then the rows; at the end the sums
     UnitTeam t;
