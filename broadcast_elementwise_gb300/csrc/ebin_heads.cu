@@ -221,11 +221,12 @@ cudaError_t launch_any(const ebin_heads_plan_s &p, const HeadsArgs &a, const AX 
 // that are not whole 16-byte vectors on 16-byte boundaries, heads of more than 64
 // vectors, and an empty table (a token outside the table reads its first row's
 // angles there, and drops them).
-bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, HeadsVecArgs &v,
-                   int &kind) {
+template <class AX>
+bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, const AX &, bool grad,
+                   HeadsVecArgs &v, int &kind) {
     const int64_t V = 16 / p.isz, D = a.dim;
     if (D % V != 0 || (a.half > 0 && a.table == 0)) return false;
-    kind = p.at.layout == EBIN_ROTARY_INTERLEAVED ? HEADS_PAIRS
+    kind = p.at.layout == EBIN_ROTARY_INTERLEAVED ? (AX::kSeveral ? HEADS_SPREAD : HEADS_PAIRS)
          : a.half % V == 0 ? HEADS_HALF : HEADS_ODD;
     auto fits = [&](const HeadsTensor &t, int heads) {
         return (uintptr_t)t.p % 16 == 0 && (p.at.batch <= 1 || t.sb % V == 0) &&
@@ -247,7 +248,7 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
             *to[i] = HeadsNear{from[i]->p, from[i]->sb, (int32_t)from[i]->st,
                                (int32_t)from[i]->sh};
         }
-        const uint32_t parts = (uint32_t)div_up(a.heads[w], kRingHeads);
+        const uint32_t parts = (uint32_t)div_up(a.heads[w], AX::kRingHeads);
         v.heads[w] = fast_div(std::max(1u, parts));
         v.heads[w].n = parts;
     }
@@ -259,7 +260,7 @@ bool heads_vectors(const ebin_heads_plan_s &p, const HeadsArgs &a, bool grad, He
     while ((1 << v.log_lanes) < v.units) ++v.log_lanes;
     // the launch's threads, and an item past the last step, are counted in 32 bits
     // (26 million tokens of 40 heads of 128 in 16 bits)
-    const int64_t items = div_up(a.heads[0], kRingHeads) + div_up(a.heads[1], kRingHeads);
+    const int64_t items = div_up(a.heads[0], 4) + div_up(a.heads[1], 4);
     if (p.rows > most >> v.log_lanes || (p.rows << v.log_lanes) > most / std::max<int64_t>(1, items))
         return false;
     v.weight_vec = ((uintptr_t)a.w[0] | (uintptr_t)a.w[1]) % 16 == 0;
@@ -295,8 +296,9 @@ cudaError_t launch_vec(const HeadsArgs &a, HeadsVecArgs v, const AX &ax, cudaStr
 
 template <class T, int KIND, class AX>
 cudaError_t launch_ring(const HeadsArgs &a, HeadsVecArgs v, const AX &ax, cudaStream_t s) {
-    v.q_items = (uint32_t)div_up(a.heads[0], kRingHeads);
-    v.per_token = fast_div(v.q_items + (uint32_t)div_up(a.heads[1], kRingHeads));
+    const HeadsVecArgs plain = v;
+    v.q_items = (uint32_t)div_up(a.heads[0], AX::kRingHeads);
+    v.per_token = fast_div(v.q_items + (uint32_t)div_up(a.heads[1], AX::kRingHeads));
     v.items = (uint32_t)a.rows * v.per_token.n;
     constexpr size_t smem = HeadsRing<T, KIND, false, AX>::kBytes + (KIND == HEADS_ODD ? 8192 : 0);
     const cudaError_t opted = allow_smem<k_heads_ring<T, KIND, AX>>(smem);
@@ -307,7 +309,7 @@ cudaError_t launch_ring(const HeadsArgs &a, HeadsVecArgs v, const AX &ax, cudaSt
     // [3,1021,15,96] f32, 1.3 items: 11.5 us against 8.2 by a CTA an item; [2,4096,40,128]
     // bf16, 5.6 items: 29.0 against 32.2).
     if (((int64_t)v.items << v.log_lanes) < 3 * wave * kHeadsThreads)
-        return launch_vec<T, KIND, HEADS_NORM, kRingHeads>(a, v, ax, s);
+        return launch_vec<T, KIND, HEADS_NORM, 4>(a, plain, ax, s);
     return launch_layer(k_heads_ring<T, KIND, AX>, dim3((unsigned)wave), kHeadsThreads, smem, s, 1,
                         a, v, ax);
 }
@@ -328,7 +330,7 @@ cudaError_t launch_vec_grad(const HeadsArgs &a, HeadsVecArgs v, const AX &ax, in
         kHeadsMaxPartials);
     const int64_t heads = a.heads[0] + a.heads[1];
     for (int w = 0; w < 2; ++w) {
-        const int64_t items = div_up(a.rows * div_up(a.heads[w], kRingHeads), per);
+        const int64_t items = div_up(a.rows * div_up(a.heads[w], AX::kRingHeads), per);
         const int64_t share = std::max<int64_t>(1, all * a.heads[w] / heads);
         v.ctas[w] = (int)std::min(items, share);
         ctas[w] = v.ctas[w];
@@ -359,10 +361,12 @@ cudaError_t launch_heads(const ebin_heads_plan_s &p, const HeadsArgs &a, const A
                          int64_t *ctas, cudaStream_t s) {
     HeadsVecArgs v;
     int kind = 0;
-    if (!heads_vectors(p, a, mode == HEADS_NORM_GRAD, v, kind))
+    if (!heads_vectors(p, a, ax, mode == HEADS_NORM_GRAD, v, kind))
         return launch_any<T>(p, a, ax, mode, ctas, s);
     if (kind == HEADS_HALF) return launch_vec_mode<T, HEADS_HALF>(a, v, ax, mode, ctas, s);
-    if (kind == HEADS_PAIRS) return launch_vec_mode<T, HEADS_PAIRS>(a, v, ax, mode, ctas, s);
+    if (kind == HEADS_PAIRS || kind == HEADS_SPREAD)
+        return launch_vec_mode<T, AX::kSeveral ? HEADS_SPREAD : HEADS_PAIRS>(a, v, ax, mode, ctas,
+                                                                            s);
     return launch_vec_mode<T, HEADS_ODD>(a, v, ax, mode, ctas, s);
 }
 

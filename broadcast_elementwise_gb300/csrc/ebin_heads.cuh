@@ -66,6 +66,8 @@ __device__ __forceinline__ int64_t heads_position(const HeadsArgs &a, int64_t b,
 // Where a token lies in the table, and which of its rows a pair reads: one position
 // for all pairs, or one for each axis of an image's or a video's token.
 struct HeadsOne {
+    static constexpr bool kSeveral = false;
+    static constexpr int kRingHeads = 4, kAhead = 4;   // of the ring (below)
     struct At {
         int64_t p;   // -1: outside the table
         __device__ __forceinline__ bool out() const { return p < 0; }
@@ -81,6 +83,8 @@ struct HeadsOne {
 constexpr int kHeadsMaxAxes = 4;
 
 struct HeadsAxes {
+    static constexpr bool kSeveral = true;
+    static constexpr int kRingHeads = 8, kAhead = 4;
     int64_t ps_a;         // position stride: axis
     int32_t used;         // axes with pairs, by bit
     uint32_t of_pair[kHeadsMaxDim / 32];   // two bits for each pair
@@ -261,10 +265,12 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads_any(const HeadsArgs a, 
 //                        two neighbouring vectors of what passes through
 //   interleaved layout   vectors at 2 u V and (2 u + 1) V: pairs of neighbours
 // so a rotation needs no exchange between lanes, and a norm one tree over L.
+//   the same with several axes (HEADS_SPREAD)   vectors at u V and (units + u) V: a
+//   warp's accesses cover whole sectors (norm of [32760,80,128] bf16 289 -> 230 us)
 //   half layout whose half is no whole number of vectors   vectors at 2 u V and
 //   (2 u + 1) V; the other element of each pair comes through shared memory
 // Cosines, sines and weights stay in registers over the heads of one item.
-enum HeadsKind : int { HEADS_HALF = 0, HEADS_PAIRS = 1, HEADS_ODD = 2 };
+enum HeadsKind : int { HEADS_HALF = 0, HEADS_PAIRS = 1, HEADS_ODD = 2, HEADS_SPREAD = 3 };
 
 struct HeadsNear {          // a tensor whose token and head strides fit 32 bits
     const void *p;
@@ -276,7 +282,7 @@ struct HeadsVecArgs {
     HeadsNear x[2], dy[2], y[2];
     FastDiv per_token;     // items of a token: groups of HPT heads of q, then of k
     FastDiv tokens;        // tokens of a sequence
-    FastDiv heads[2];      // the gradient's items of a token: kRingHeads heads of q, of k
+    FastDiv heads[2];      // the gradient's items of a token: AX::kRingHeads heads of q, of k
     uint32_t q_items;       // of per_token
     uint32_t items;         // of the launch
     int32_t log_lanes;
@@ -307,12 +313,14 @@ __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y
 // Where a lane's unit lies and how its pairs read: pairs 2i and 2i + 1 are
 // (a[i].x, b[i].x) and (a[i].y, b[i].y), ready for the packed binary32 pipe.
 template <class T, int KIND> struct HeadsUnit {
-    static constexpr bool IL = KIND == HEADS_PAIRS, ODD = KIND == HEADS_ODD;
+    static constexpr bool SPREAD = KIND == HEADS_SPREAD, ODD = KIND == HEADS_ODD;
+    static constexpr bool IL = KIND == HEADS_PAIRS || SPREAD;
     static constexpr int V = 16 / sizeof(T), N = V / 2;
     int off0, off1;    // element offsets of the two vectors
     bool on, second;   // the lane has work; its second vector exists
     int pairs;         // leading pairs that rotate
     int pair0;         // the first pair's index in the table row
+    int pairs1, pair1; // the second vector's own (HEADS_SPREAD)
 
     __device__ __forceinline__ void place(const HeadsArgs &a, const HeadsVecArgs &v, int lane) {
         on = lane < v.units;
@@ -321,6 +329,13 @@ template <class T, int KIND> struct HeadsUnit {
             off1 = off0 + V;
             pair0 = 0;
             pairs = min(max(2 * a.half - off0, 0), 2 * V);   // leading elements that rotate
+        } else if constexpr (SPREAD) {
+            off0 = lane * V;
+            off1 = off0 + v.units * V;
+            pair0 = off0 / 2;
+            pair1 = off1 / 2;
+            pairs = min(max(a.half - pair0, 0), N);
+            pairs1 = on ? min(max(a.half - pair1, 0), N) : 0;
         } else if constexpr (IL) {
             off0 = 2 * lane * V;
             off1 = off0 + V;
@@ -335,6 +350,19 @@ template <class T, int KIND> struct HeadsUnit {
         }
         if (!on) pairs = 0;
         second = on && off1 < a.dim;
+    }
+    // whether pair k of the unit's V rotates, and whether all do
+    __device__ __forceinline__ bool turns(int k) const {
+        if constexpr (SPREAD) return k < N ? k < pairs : k - N < pairs1;
+        else return k < pairs;
+    }
+    __device__ __forceinline__ bool all_turn() const {
+        return SPREAD ? pairs + pairs1 == V : pairs == V;
+    }
+    // pair k's index in the table row
+    __device__ __forceinline__ int pair(int k) const {
+        if constexpr (SPREAD) return k < N ? pair0 + k : pair1 + k - N;
+        else return pair0 + k;
     }
     // every lane loads from inside the row: one without work (or without a
     // second vector) repeats the row's first vector, and masks what it sums
@@ -501,11 +529,12 @@ template <class T, int KIND> struct HeadsUnit {
     template <class AX>
     __device__ __forceinline__ void table(const HeadsArgs &a, const HeadsVecArgs &v, const AX &ax,
                                           const typename AX::At &p, float2 *c, float2 *s) const {
-        const bool whole = pairs == V && v.table_vec;
+        const bool whole = all_turn() && v.table_vec;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const int first = pair0 + 2 * i;
-            if (whole && ax.same4(first)) {
+            const int first = pair(2 * i);
+            // four pairs of one vector: all but binary32's with two vectors apart
+            if (!(SPREAD && N == 2) && whole && ax.same4(first)) {
                 const int64_t at = ax.row(p, first) * a.half + first;
                 const float4 x = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
                 const float4 y = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
@@ -518,8 +547,8 @@ template <class T, int KIND> struct HeadsUnit {
             auto one = [&](int k, float &cc, float &ss) {
                 cc = 1.0f;
                 ss = 0.0f;
-                if (2 * i + k < pairs) {
-                    const int64_t at = ax.row(p, first + k) * a.half + first + k;
+                if (turns(2 * i + k)) {
+                    const int64_t at = ax.row(p, pair(2 * i + k)) * a.half + pair(2 * i + k);
                     cc = __ldg(a.cos + at);
                     ss = __ldg(a.sin + at);
                 }
@@ -567,7 +596,7 @@ template <class T, int KIND> struct HeadsUnit {
     // times a zero sine would be no number
     __device__ __forceinline__ void turn(float2 *a, float2 *b, const float2 *ca, const float2 *sa,
                                          const float2 *nb, const float2 *cb) const {
-        if (pairs == V) {
+        if (all_turn()) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float2 x = a[i];
@@ -580,11 +609,11 @@ template <class T, int KIND> struct HeadsUnit {
                 const float2 x = a[i], y = b[i];
                 a[i] = __fmul2_rn(x, ca[i]);
                 b[i] = __fmul2_rn(y, cb[i]);
-                if (2 * i < pairs) {
+                if (turns(2 * i)) {
                     a[i].x = fmaf(y.x, nb[i].x, a[i].x);
                     b[i].x = fmaf(x.x, sa[i].x, b[i].x);
                 }
-                if (2 * i + 1 < pairs) {
+                if (turns(2 * i + 1)) {
                     a[i].y = fmaf(y.y, nb[i].y, a[i].y);
                     b[i].y = fmaf(x.y, sa[i].y, b[i].y);
                 }
@@ -594,7 +623,7 @@ template <class T, int KIND> struct HeadsUnit {
     // the transposed rotation (a gradient's): y_a = a cos + b sin, y_b = b cos - a sin
     __device__ __forceinline__ void turn_back(float2 *a, float2 *b, const float2 *c,
                                               const float2 *s) const {
-        if (pairs == V) {
+        if (all_turn()) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float2 x = a[i];
@@ -605,11 +634,11 @@ template <class T, int KIND> struct HeadsUnit {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float2 x = a[i], y = b[i];
-                if (2 * i < pairs) {
+                if (turns(2 * i)) {
                     a[i].x = fmaf(x.x, c[i].x, y.x * s[i].x);
                     b[i].x = fmaf(y.x, c[i].x, -(x.x * s[i].x));
                 }
-                if (2 * i + 1 < pairs) {
+                if (turns(2 * i + 1)) {
                     a[i].y = fmaf(x.y, c[i].y, y.y * s[i].y);
                     b[i].y = fmaf(y.y, c[i].y, -(x.y * s[i].y));
                 }
@@ -726,12 +755,11 @@ k_heads_vec(const HeadsArgs a, const HeadsVecArgs v, const AX ax) {
 }
 
 // Rows through a ring in shared memory.  A group of lanes walks items (a token
-// and kRingHeads heads of q or of k) in steps of the launch's groups; their
+// and AX::kRingHeads heads of q or of k) in steps of the launch's groups; their
 // rows are fetched kAhead before they are worked on, by asynchronous copies.
 // Each thread copies what it will read itself, so that nothing but its own
 // copies is waited for.  What is fetched runs at most one item ahead, so one
 // set of the next item's facts is enough.
-constexpr int kRingHeads = 4;
 
 __device__ __forceinline__ void heads_copy(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -740,7 +768,8 @@ __device__ __forceinline__ void heads_copy(uint32_t to, const void *from) {
 // GRAD: rows of x and of dy, of one tensor; else rows of x, of q then of k.
 template <class T, int KIND, bool GRAD, class AX> struct HeadsRing {
     using Unit = HeadsUnit<T, KIND>;
-    static constexpr int kAhead = GRAD ? 3 : 4, kSlots = kAhead + 1;
+    static constexpr int kRingHeads = AX::kRingHeads;
+    static constexpr int kAhead = GRAD ? 3 : AX::kAhead, kSlots = kAhead + 1;
     static constexpr int kVectors = GRAD ? 4 : 2;             // of a thread and row
     static constexpr int kBytes = kSlots * kVectors * kHeadsThreads * 16;
     static_assert(kAhead <= kRingHeads, "at most one item ahead");
@@ -861,10 +890,12 @@ k_heads_ring(const HeadsArgs a, const HeadsVecArgs v, const AX ax) {
         u.template folded<true>(a, v, ax, r.k, p, ca, cb, sa, nb);
         const bool out = __any_sync(0xFFFFFFFFu, p.out());   // rare
 #pragma unroll 1
-        for (int h = 0; h < kRingHeads; ++h) {
+        for (int h = 0; h < AX::kRingHeads; ++h) {
             const uint4 *const in = r.take();
             const uint4 x0 = in[0], x1 = in[kHeadsThreads];
             r.fetch(a, v, ax, u, -1);
+            // items of many heads: those that no group of the warp has are passed over
+            if (AX::kSeveral && !__any_sync(0xFFFFFFFFu, h < count)) continue;
             float2 va[N], vb[N];
             Unit::open(x0, x1, va, vb);
             if constexpr (Unit::ODD) {
@@ -958,7 +989,7 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v, const AX ax) {
         else u.table(a, v, ax, p, c, sn);
         const bool out = __any_sync(0xFFFFFFFFu, p.out());   // rare
 #pragma unroll 1
-        for (int h = 0; h < kRingHeads; ++h) {
+        for (int h = 0; h < AX::kRingHeads; ++h) {
             const uint4 *const in = r.take();
             float2 xa[N], xb[N], ga[N], gb[N];
             {
@@ -972,6 +1003,7 @@ k_heads_vec_grad(const HeadsArgs a, const HeadsVecArgs v, const AX ax) {
                 }
             }
             r.fetch(a, v, ax, u, which);
+            if (AX::kSeveral && !__any_sync(0xFFFFFFFFu, h < count)) continue;
             if constexpr (Unit::ODD) u.turn_odd(shared_row, a.half, 1.0f, ga, gb, c, cb, sn, sb);
             else u.turn_back(ga, gb, c, sn);
             float ss = u.squares(xa, xb);

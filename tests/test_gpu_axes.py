@@ -1,6 +1,9 @@
 """Rotary positions with several axes on the GPU: against the 64-bit form of one axis on tables
-gathered for each token, with its bounds, and bit for bit against the engine's own one-axis
-form on those tables."""
+gathered for each token, with its bounds; in the half layout bit for bit against the engine's
+own one-axis form on those tables.  (Interleaved, the two take a head's vectors in other units,
+and a unit that rotates in part sums fma(b, -s, fl(a c)) where a whole one sums fma(a, c,
+fl(-b s)): one rounded product and one fused sum each, so within the same bound, but not the
+same bits.)"""
 import pytest
 import torch
 
@@ -96,7 +99,7 @@ def test_rotary(case, dtype, gradient):
             continue
         want = ref.rotate(x.double(), c.double(), s.double(), layout, -1.0 if gradient else 1.0)
         ref.check(y, want, ref.spread(x.double(), c.double(), s.double(), layout), 4, "rotary")
-        assert torch.equal(y, z)
+        assert layout != "half" or torch.equal(y, z)
     assert eb.get_device_status() == 0
 
 
