@@ -226,11 +226,9 @@ def _load():
                                               ctypes.POINTER(vp)]),
         "ebin_block_norm_plan_workspace": (i32, [vp, ctypes.POINTER(ctypes.c_size_t)]),
         "ebin_block_norm_plan_release": (None, [vp]),
-        "ebin_block_norm_execute": (i32, [vp] * 3 + [ctypes.POINTER(ebin_block_norm_params)] +
-                                    [vp] * 3),
-        "ebin_block_norm_grad_execute": (i32, [vp] * 5 + [ctypes.POINTER(ebin_block_norm_params)] +
-                                         [vp] * 2 + [ctypes.POINTER(ebin_block_norm_grads), vp,
-                                                     ctypes.c_size_t, vp]),
+        # params and grads: a structure by reference, or its bytes
+        "ebin_block_norm_execute": (i32, [vp] * 7),
+        "ebin_block_norm_grad_execute": (i32, [vp] * 10 + [ctypes.c_size_t, vp]),
         "ebin_launch_count": (ctypes.c_uint64, []),
         "ebin_dtype_size": (ctypes.c_size_t, [i32]),
         "ebin_status_string": (ctypes.c_char_p, [i32]),
@@ -606,7 +604,7 @@ def ebin_block_norm_plan_release(plan) -> None:
 
 def ebin_block_norm_execute(plan, x, y, params, h, z, stream) -> None:
     """params: an ebin_block_norm_params, or None."""
-    st = lib.ebin_block_norm_execute(plan, x, y, params, h, z, stream)
+    st = lib.ebin_block_norm_execute(plan, x, y, params and ctypes.byref(params), h, z, stream)
     if st:
         raise EbinError(st, "ebin_block_norm_execute")
 
@@ -614,7 +612,8 @@ def ebin_block_norm_execute(plan, x, y, params, h, z, stream) -> None:
 def ebin_block_norm_grad_execute(plan, dz, dh, h, y, params, dx, dy, grads, workspace,
                                  workspace_bytes, stream) -> None:
     """params, grads: an ebin_block_norm_params and an ebin_block_norm_grads, or None."""
-    st = lib.ebin_block_norm_grad_execute(plan, dz, dh, h, y, params, dx, dy, grads, workspace,
+    st = lib.ebin_block_norm_grad_execute(plan, dz, dh, h, y, params and ctypes.byref(params), dx,
+                                          dy, grads and ctypes.byref(grads), workspace,
                                           workspace_bytes, stream)
     if st:
         raise EbinError(st, "ebin_block_norm_grad_execute")
@@ -1410,13 +1409,23 @@ class BlockNormPlan:
             pass
 
 
+# ebin_block_norm_params and ebin_block_norm_grads as bytes (a Structure takes a microsecond
+# longer to build)
+_PARAMS, _GRADS = struct.Struct("=10Q").pack, struct.Struct("=7Q").pack
+
+
+def _words(*xs):
+    """_ptr of each argument, 0 for None."""
+    return [0 if x is None else x if isinstance(x, int) else x.data_ptr() for x in xs]
+
+
 def execute_block_norm(plan: BlockNormPlan, x, y, h, z, *, gate=None, w_post=None, b_post=None,
                        w_pre=None, b_pre=None, scale=None, shift=None, seed: int = 0,
                        offset: int = 0, offset_device=None, stream=None) -> None:
     """Enqueue the forward pass on device buffers laid out as the plan says (torch
     tensors or int addresses); h or z None: not wanted."""
-    params = ebin_block_norm_params(*_ptrs(gate, w_post, b_post, w_pre, b_pre, scale, shift),
-                                    seed & _WORD, offset & _WORD, _ptr(offset_device))
+    params = _PARAMS(*_words(gate, w_post, b_post, w_pre, b_pre, scale, shift), seed & _WORD,
+                     offset & _WORD, _ptr(offset_device) or 0)
     st = lib.ebin_block_norm_execute(plan.handle, *_ptrs(x, y), params, *_ptrs(h, z),
                                      _stream(stream))
     if st:
@@ -1431,9 +1440,9 @@ def execute_block_norm_grad(plan: BlockNormPlan, dz, dh, h, y, dx, dy, *, gate=N
     """Enqueue the gradient; outputs that are None are not wanted.  ``workspace``: a uint8
     device tensor of at least plan.workspace_bytes (None where no gradient of a parameter
     is wanted)."""
-    params = ebin_block_norm_params(*_ptrs(gate, w_post, b_post, w_pre, b_pre, scale, None),
-                                    seed & _WORD, offset & _WORD, _ptr(offset_device))
-    grads = ebin_block_norm_grads(*_ptrs(dgate, dw_post, db_post, dw_pre, db_pre, dscale, dshift))
+    params = _PARAMS(*_words(gate, w_post, b_post, w_pre, b_pre, scale), 0, seed & _WORD,
+                     offset & _WORD, _ptr(offset_device) or 0)
+    grads = _GRADS(*_words(dgate, dw_post, db_post, dw_pre, db_pre, dscale, dshift))
     st = lib.ebin_block_norm_grad_execute(plan.handle, *_ptrs(dz, dh, h, y), params,
                                           *_ptrs(dx, dy), grads, _ptr(workspace),
                                           _bytes_of(workspace), _stream(stream))

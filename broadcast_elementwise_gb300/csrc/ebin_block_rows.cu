@@ -1,6 +1,6 @@
 // The row kernels of the norms around a block, one pair of element types in each
 // compilation (-DEBIN_DT=0 .. 4).
-#include "ebin_block_rows.cuh"
+#include "ebin_block_unit.cuh"
 
 namespace ebin {
 
@@ -56,13 +56,20 @@ static RowsGeom rows_geom(const BlockArgs &a, int chunks, int vpt) {
 }
 
 
+// Bytes of a CTA's rows of a tensor of E's in shared memory.
+template <class E> static size_t unit_bytes(const RowsGeom &g, int vpt, bool vec) {
+    using Lane = UnitLane<T, S, true>;
+    return vec ? (size_t)vpt * Lane::vectors<E>() * kUnitThreads * 16
+               : (size_t)vpt * g.warps * g.teams * Lane::buffer<E>();
+}
+
 #define EBIN_CAT(a, b) a##b
 #define EBIN_NAME(f, dt) EBIN_CAT(f, dt)
 
-// A CTA an SM takes a unit: rows on vectors, at most 8192 columns, and enough rows in
-// a unit that each team has some.
-static bool cta_takes(const BlockArgs &a, int chunks, int vpt, bool vec) {
-    return vec && chunks <= 32 && a.rows > 304 && a.cta.rows >= 2 * (16 / div_up(chunks, vpt));
+// A CTA an SM takes a unit: rows of at most 8192 columns, and enough of them in a unit that
+// each team has some.
+static bool cta_takes(const BlockArgs &a, int chunks, int vpt) {
+    return chunks <= 32 && a.rows > 304 && a.cta.rows >= 2 * (16 / div_up(chunks, vpt));
 }
 
 // Its geometry, but for what lies in shared memory.
@@ -81,7 +88,7 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
     if (chunks > 128) return cudaSuccess;
     const bool layer = a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
     const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
-    if (cta_takes(a, chunks, kUnitVpt, vec)) {
+    if (cta_takes(a, chunks, kUnitVpt)) {
         RowsGeom g = unit_geom(a, chunks, kUnitVpt);
         const bool scaled = a.branch_scale != 1.0f || a.drop.least;
         if (a.y && (a.gate || a.w_post || a.b_post || scaled)) g.tables |= TABLE_Y;
@@ -89,14 +96,16 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
         if (a.z && (a.scale || a.w_pre)) g.tables |= TABLE_H;
         if (a.z && (a.shift || a.b_pre)) g.tables |= TABLE_H_ADD;
         const size_t tables = 16 * (size_t)g.table * __builtin_popcount(g.tables);
-        g.vectors = kUnitVpt * (s_vectors + (a.y ? t_vectors : 0));
-        const size_t row = (size_t)kUnitThreads * 16 * g.vectors;
+        const size_t row = unit_bytes<S>(g, kUnitVpt, vec) +
+                           (a.y ? unit_bytes<T>(g, kUnitVpt, vec) : 0);
+        g.slot_bytes = (int)row;
         g.slots = rows_slots(row, tables, 1);
         if (g.slots > 0) {
             *parts = a.cta.parts;
             const size_t smem = tables + g.slots * row;
-            return layer ? launch_rows<k_block_unit<T, S, true>>(a, g, g.units, smem, s)
-                         : launch_rows<k_block_unit<T, S, false>>(a, g, g.units, smem, s);
+            if (!vec) return launch_rows<k_block_unit<T, S, true, true>>(a, g, g.units, smem, s);
+            return layer ? launch_rows<k_block_unit<T, S, true, false>>(a, g, g.units, smem, s)
+                         : launch_rows<k_block_unit<T, S, false, false>>(a, g, g.units, smem, s);
         }
     }
     const int vpt = chunks > 32 ? 4 : 1;
@@ -136,11 +145,12 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
     const bool post = a.post != EBIN_NORM_NONE;
     const int unit_vpt = full && post ? kUnitGradVpt<true> : kUnitGradVpt<false>;
     if (a.pre != EBIN_NORM_NONE && div_up(chunks, unit_vpt) <= kUnitWarps &&
-        cta_takes(a, chunks, unit_vpt, vec)) {
+        cta_takes(a, chunks, unit_vpt)) {
         RowsGeom g = unit_geom(a, chunks, unit_vpt);
         const size_t tables = 2 * 16 * (size_t)g.table;
-        g.vectors = unit_vpt * (2 * s_vectors + (a.y ? 2 : 1) * t_vectors);
-        const size_t row = (size_t)g.vectors * 16 * kUnitThreads;
+        const size_t row = 2 * unit_bytes<S>(g, unit_vpt, vec) +
+                           (a.y ? 2 : 1) * unit_bytes<T>(g, unit_vpt, vec);
+        g.slot_bytes = (int)row;
         g.slots = rows_slots(row, tables, 1);
         if (g.slots > 0) {
             // the teams' sums at the end
@@ -148,12 +158,14 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
                                                   32 * g.warps * 32 : 0;
             const size_t smem = std::max(tables + g.slots * row, sums);
             *parts = a.cta.parts;
-            if (full)
-                return post ? launch_rows<k_block_unit_grad<T, S, true, true>>(a, g, g.units, smem, s)
-                            : launch_rows<k_block_unit_grad<T, S, true, false>>(a, g, g.units, smem,
-                                                                               s);
-            return post ? launch_rows<k_block_unit_grad<T, S, false, true>>(a, g, g.units, smem, s)
-                        : launch_rows<k_block_unit_grad<T, S, false, false>>(a, g, g.units, smem, s);
+#define EBIN_UNIT(FULL, POST)                                                                \
+    return vec ? launch_rows<k_block_unit_grad<T, S, FULL, POST, false>>(a, g, g.units, smem, s) \
+               : launch_rows<k_block_unit_grad<T, S, FULL, POST, true>>(a, g, g.units, smem, s)
+            if (full && post) { EBIN_UNIT(true, true); }
+            if (full) { EBIN_UNIT(true, false); }
+            if (post) { EBIN_UNIT(false, true); }
+            EBIN_UNIT(false, false);
+#undef EBIN_UNIT
         }
     }
     const int vpt = chunks > 32 ? 4 : 2;

@@ -24,6 +24,7 @@ struct RowsGeom {
     // of a CTA that takes a unit: which of its columns' factors there are, by bit, and
     // the 16-byte vectors of one
     int32_t tables, table;
+    int32_t slot_bytes;   // of its teams' rows
 };
 
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
@@ -883,799 +884,6 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
             }
             l[i].store(partial + k * a.n, s);
         }
-    }
-}
-
-// ------------------------------------------------------------------ a CTA takes a unit
-//
-// Many rows on vectors, of at most 8192 columns: one CTA an SM takes a unit,
-// consecutive rows of one group, and its teams walk them in turn.  What a column's
-// elements are multiplied by and added to lies in shared memory in binary32, formed
-// once from the parameters: two 16-byte loads in place of one and eight conversions,
-// which a row of weights in the L1 costs for each use ([8192,4096] bf16 with both
-// norms' weights: 60 us so, 48 without the weights).
-
-
-// A table of a factor for the lane's columns: the fours of chunk i, [2][32] vectors.
-template <class L> struct RowsTable {
-    const float4 *at;   // this lane's first
-    int warps;
-    __device__ __forceinline__ void read(int i, float2 *p) const {
-        const float4 x = at[i * warps * 64], y = at[i * warps * 64 + 32];
-        p[0] = make_float2(x.x, x.y);
-        p[1] = make_float2(x.z, x.w);
-        p[2] = make_float2(y.x, y.y);
-        p[3] = make_float2(y.z, y.w);
-    }
-    __device__ __forceinline__ void times(int i, float2 *v) const {
-        float2 p[4];
-        read(i, p);
-        mul8(v, p);
-    }
-};
-
-// value(col, q, p): a table's four values at col; written by the whole CTA.
-template <class L, class F>
-__device__ __forceinline__ void rows_fill(float4 *table, int vectors, int n, const F &value) {
-    for (int j = threadIdx.x; j < vectors; j += blockDim.x) {
-        const int lane = j & 31, q = j >> 5 & 1, base = (j >> 6) * kChunk;
-        const int col = base + (L::WIDE ? q * 128 + lane * 4 : lane * 8 + q * 4);
-        table[j] = col < n ? value(col) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-}
-
-// Four of a row of parameters in type T or binary32; `none` where there is no row.
-template <class T>
-__device__ __forceinline__ float4 params4(const void *p, int col, int f32, float none) {
-    if (!p) return make_float4(none, none, none, none);
-    if (f32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + col);
-    if constexpr (sizeof(T) == 2) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p) + col);
-        const float2 a = open2<T>(x.x), b = open2<T>(x.y);
-        return make_float4(a.x, a.y, b.x, b.y);
-    } else {
-        return *reinterpret_cast<const float4 *>(static_cast<const T *>(p) + col);
-    }
-}
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
-    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
-}
-__device__ __forceinline__ float4 add4(float4 a, float4 b) {
-    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-__device__ __forceinline__ float4 four(float v) { return make_float4(v, v, v, v); }
-
-enum RowsTables : int {
-    TABLE_Y = 1,       // branch_scale / (1 - p) gate w_post
-    TABLE_Y_ADD = 2,   // branch_scale / (1 - p) gate b_post
-    TABLE_H = 4,       // (1 + scale) w_pre
-    TABLE_H_ADD = 8    // (1 + scale) b_pre + shift
-};
-
-// A lane's columns as RowsLane's with vectors, for all its chunks: those of chunk i
-// begin `stride` columns after those of chunk i - 1.
-template <class T, class S, int THREADS> struct UnitLane {
-    static constexpr bool WIDE = sizeof(S) == 4;
-    static constexpr int kStride = THREADS;   // vectors between a thread's in shared memory
-    int first, stride, n;   // the first column of chunk 0
-    int chunk;              // and the chunk's own
-
-    __device__ __forceinline__ void place(int lane, int warp, int warps, int n_) {
-        chunk = warp * kChunk;
-        first = chunk + lane * (WIDE ? 4 : 8);
-        stride = warps * kChunk;
-        n = n_;
-    }
-    // no column of chunk i lies in the row (the same for a whole warp; never of chunk 0)
-    __device__ __forceinline__ bool none(int i) const { return i && chunk + i * stride >= n; }
-    __device__ __forceinline__ int col(int i, int q) const {
-        return first + i * stride + (WIDE ? q * 128 : q * 4);
-    }
-    __device__ __forceinline__ bool on(int i, int q) const {
-        return first + i * stride + (WIDE ? q * 128 : 0) < n;
-    }
-    __device__ __forceinline__ float within(int i, const float2 *v) const {
-        const float2 a = __fadd2_rn(v[0], v[1]), b = __fadd2_rn(v[2], v[3]);
-        if constexpr (WIDE) {
-            return (on(i, 0) ? a.x + a.y : 0.0f) + (on(i, 1) ? b.x + b.y : 0.0f);
-        } else {
-            const float2 c = __fadd2_rn(a, b);
-            return on(i, 0) ? c.x + c.y : 0.0f;
-        }
-    }
-    // sum of the products of a and b
-    __device__ __forceinline__ float dot(int i, const float2 *a, const float2 *b) const {
-        if constexpr (WIDE) {
-            const float2 x = __ffma2_rn(a[1], b[1], __fmul2_rn(a[0], b[0]));
-            const float2 y = __ffma2_rn(a[3], b[3], __fmul2_rn(a[2], b[2]));
-            return (on(i, 0) ? x.x + x.y : 0.0f) + (on(i, 1) ? y.x + y.y : 0.0f);
-        } else {
-            float2 x = __fmul2_rn(a[0], b[0]);
-#pragma unroll
-            for (int j = 1; j < 4; ++j) x = __ffma2_rn(a[j], b[j], x);
-            return on(i, 0) ? x.x + x.y : 0.0f;
-        }
-    }
-    // to: the row's place in shared memory, [vectors][512]; row: at this lane's first column
-    template <class E>
-    __device__ __forceinline__ void fetch(int i, uint32_t to, const E *row) const {
-        row += i * stride;
-        if constexpr (!WIDE) {
-            if (on(i, 0)) rows_copy16(to, row);
-        } else if constexpr (sizeof(E) == 4) {
-            if (on(i, 0)) rows_copy16(to, row);
-            if (on(i, 1)) rows_copy16(to + kStride * 16, row + 128);
-        } else {
-            if (on(i, 0)) rows_copy8(to, row);
-            if (on(i, 1)) rows_copy8(to + 8, row + 128);
-        }
-    }
-    // Columns past the row's end are never copied to: zero, once, for good.
-    template <class E> __device__ __forceinline__ void clear(int i, uint4 *at) const {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        if constexpr (!WIDE) {
-            if (!on(i, 0)) at[0] = zero;
-        } else if constexpr (sizeof(E) == 4) {
-            if (!on(i, 0)) at[0] = zero;
-            if (!on(i, 1)) at[kStride] = zero;
-        } else {
-            if (!on(i, 0)) reinterpret_cast<uint2 *>(at)[0] = make_uint2(0, 0);
-            if (!on(i, 1)) reinterpret_cast<uint2 *>(at)[1] = make_uint2(0, 0);
-        }
-    }
-    template <class E> __device__ __forceinline__ void store(int i, E *row, const float2 *v) const {
-        row += i * stride;
-        if constexpr (!WIDE && sizeof(E) == 2) {
-            if (on(i, 0))
-                *reinterpret_cast<uint4 *>(row) =
-                    make_uint4(pack2<E>(v[0]), pack2<E>(v[1]), pack2<E>(v[2]), pack2<E>(v[3]));
-        } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (!on(i, q)) continue;
-                E *const p = row + (WIDE ? q * 128 : q * 4);
-                if constexpr (sizeof(E) == 4)
-                    *reinterpret_cast<float4 *>(p) =
-                        make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
-                else
-                    *reinterpret_cast<uint2 *>(p) =
-                        make_uint2(pack2<E>(v[2 * q]), pack2<E>(v[2 * q + 1]));
-            }
-        }
-    }
-    // keep bits of chunk i, element e in bit e
-    __device__ __forceinline__ uint32_t kept(int i, const DropArgs &d, uint32_t row,
-                                             uint2 offset) const {
-        uint32_t r = 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint4 w = drop_words(d, (uint32_t)col(i, q) >> 2, row, offset);
-            r |= ((uint32_t)(w.x >= d.least) | (uint32_t)(w.y >= d.least) << 1 |
-                  (uint32_t)(w.z >= d.least) << 2 | (uint32_t)(w.w >= d.least) << 3) << (4 * q);
-        }
-        return r;
-    }
-    __device__ __forceinline__ void drop(int i, const DropArgs &d, uint32_t row, uint2 offset,
-                                         float2 *v) const {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint4 w = drop_words(d, (uint32_t)col(i, q) >> 2, row, offset);
-            v[2 * q].x = w.x >= d.least ? v[2 * q].x : 0.0f;
-            v[2 * q].y = w.y >= d.least ? v[2 * q].y : 0.0f;
-            v[2 * q + 1].x = w.z >= d.least ? v[2 * q + 1].x : 0.0f;
-            v[2 * q + 1].y = w.w >= d.least ? v[2 * q + 1].y : 0.0f;
-        }
-    }
-};
-
-// Four values' sums over a warp: lanes 8 k .. 8 k + 7 get that of v[k].  Six
-// exchanges: each halves what a lane still carries.
-__device__ __forceinline__ float warp_sums4(const float (&v)[4], int lane) {
-    const bool up = lane & 16;
-    float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
-    a += __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
-    b += __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : v[3], 16);
-    const bool odd = lane & 8;
-    float r = odd ? b : a;
-    r += __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
-    return r;
-}
-
-__device__ __forceinline__ float eighth_sums(float r) {   // over lanes 8 k .. 8 k + 7
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
-    return r;
-}
-
-// A team of at most 16 warps, one of a CTA's: its exchanges go through [2][12][warps] floats
-// in turn, with a barrier each (1 .. 8; 0 is the CTA's, and teams of one warp have none).
-// In a join lane l stands for warps l % 8 and l % 8 + 8.
-struct UnitTeam {
-    int lane, warp, warps, id, half;
-    float *s;
-    float inv_n;
-
-    __device__ __forceinline__ void start(const RowsGeom &g, int n, float *sums) {
-        lane = threadIdx.x & 31;
-        warps = g.warps;
-        id = (threadIdx.x >> 5) / warps;
-        warp = (threadIdx.x >> 5) - id * warps;
-        s = sums + id * 24 * warps;
-        half = 0;
-        inv_n = 1.0f / (float)n;
-    }
-    __device__ __forceinline__ float *turn() {
-        half = half ? 0 : 12 * warps;
-        return s + half;
-    }
-    __device__ __forceinline__ void meet() const {
-        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
-    }
-    // over the warps, of row k of what they left; the same in lanes 8 j .. 8 j + 7
-    __device__ __forceinline__ float join(const float *at, int k) const {
-        at += k * warps;
-        const int w = lane & 7;
-        float r = w < warps ? at[w] : 0.0f;
-        if (warps > 8) r += w + 8 < warps ? at[w + 8] : 0.0f;
-        return eighth_sums(r);
-    }
-    // the team's sum of v
-    __device__ __forceinline__ float sum(float v) {
-        float one[1] = {v};
-        warp_sums(one);
-        if (warps == 1) return one[0];
-        float *const at = turn();
-        if (lane == 0) at[warp] = one[0];
-        meet();
-        return join(at, 0);
-    }
-    // the team's sums of each v
-    template <int K> __device__ __forceinline__ void sums(float (&v)[K]) {
-        constexpr int G = (K + 3) / 4;
-        float r[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            float four[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) four[k] = 4 * g + k < K ? v[4 * g + k] : 0.0f;
-            r[g] = warp_sums4(four, lane);
-        }
-        if (warps > 1) {
-            float *const at = turn();
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if ((lane & 7) == 0) at[(4 * g + (lane >> 3)) * warps + warp] = r[g];
-            meet();
-#pragma unroll
-            for (int g = 0; g < G; ++g) r[g] = join(at, 4 * g + (lane >> 3));
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, r[k / 4], 8 * (k % 4));
-    }
-};
-
-// (mean, 1 / deviation) of a row in registers: the mean first, then the squares about it
-// (a RMS norm: about 0).
-template <bool LAYER, class L, int VPT>
-__device__ __forceinline__ float2 unit_moments(UnitTeam &t, const L &l, const float2 (&v)[VPT][4],
-                                               int norm, float eps) {
-    float mean = 0.0f, q = 0.0f;
-    if (LAYER && norm == EBIN_NORM_LAYER) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (!l.none(i)) s += l.within(i, v[i]);
-        mean = t.sum(s) * t.inv_n;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if (l.none(i)) continue;
-        float2 d[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) d[k] = LAYER ? __fadd2_rn(v[i][k], two(-mean)) : v[i][k];
-        q += l.dot(i, d, d);
-    }
-    return make_float2(mean, rsqrtf(fmaf(t.sum(q), t.inv_n, eps)));
-}
-
-// A chunk of a thread's part of a row, as it lies in shared memory, and its pairs of
-// columns: unpacked where they are used, so that registers hold them packed.
-template <class E, int STRIDE> struct UnitWords {
-    static constexpr int N = sizeof(E) == 4 ? 2 : 1;   // vectors
-    uint4 w[N];
-    __device__ __forceinline__ void read(const uint4 *at) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = at[k * STRIDE];
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ float2 pair(int j) const {
-        if constexpr (N == 2) {
-            const uint4 &x = w[j >> 1];
-            return j & 1 ? make_float2(__uint_as_float(x.z), __uint_as_float(x.w))
-                         : make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
-        } else {
-            const uint4 &x = w[0];
-            return open2<E>(j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w);
-        }
-    }
-};
-
-// A tensor's rows on their way to shared memory: the next row, and its step.
-template <class E> struct RowsFrom {
-    const E *row;
-    int64_t step;
-    template <class L>
-    __device__ __forceinline__ RowsFrom(const L &l, const void *p, int64_t ld, int first, int rows)
-        : row(static_cast<const E *>(p) + (p ? first * ld + l.first : 0)), step(p ? rows * ld : 0) {}
-    template <int VPT, class L> __device__ __forceinline__ void fetch(const L &l, uint32_t to) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (!l.none(i)) l.fetch(i, to + i * RowsPart<L, E>::N * L::kStride * 16, row);
-        row += step;
-    }
-};
-
-template <class T, class S, bool LAYER>
-__global__ void __launch_bounds__(kUnitThreads, 1)
-k_block_unit(const BlockArgs a, const RowsGeom g) {
-    using Lane = UnitLane<T, S, kUnitThreads>;
-    using PartS = RowsPart<Lane, S>;
-    using PartT = RowsPart<Lane, T>;
-    constexpr int VPT = kUnitVpt, kX = VPT * PartS::N;
-    __shared__ float s_sums[24 * kUnitWarps];
-    extern __shared__ uint4 s_rows[];   // the tables, then [slots][vectors of a thread][512]
-    UnitTeam t;
-    t.start(g, (int)a.n, s_sums);
-    Lane l;
-    l.place(t.lane, t.warp, g.warps, (int)a.n);
-    const int64_t unit = blockIdx.x, group = unit / a.cta.parts, part = unit - group * a.cta.parts;
-    const int r0 = (int)(group * a.group_rows + part * a.cta.rows);
-    const int r1 = (int)min(r0 + a.cta.rows, (group + 1) * a.group_rows);
-    const int step = g.teams;
-    const bool post = a.post != EBIN_NORM_NONE;
-    const float branch = a.branch_scale * (a.drop.least ? a.drop.scale : 1.0f);
-    float4 *table = reinterpret_cast<float4 *>(s_rows);
-    RowsTable<Lane> by[4];   // of bit k
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        by[k] = RowsTable<Lane>{table + t.warp * 64 + t.lane, g.warps};
-        if (g.tables >> k & 1) table += g.table;
-    }
-    uint4 *const mine = reinterpret_cast<uint4 *>(table) + threadIdx.x;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
-    const int ahead = g.slots - 1, slot_vectors = g.vectors * kUnitThreads;
-    const int last = ahead * slot_vectors;
-    int fill = 0, slot = 0, next = r0 + t.id;
-    RowsFrom<S> from_x(l, a.x, a.ld_x, next, step);
-    RowsFrom<T> from_y(l, a.y, a.ld_y, next, step);
-    layer_pdl_launch();
-    layer_pdl_wait();
-    const uint2 offset = drop_offset(a.drop);
-    auto fetch = [&]() {
-        if (next < r1) {
-            const uint32_t at = to + fill * 16;
-            from_x.template fetch<VPT>(l, at);
-            if (a.y) from_y.template fetch<VPT>(l, at + kX * kUnitThreads * 16);
-            next += step;
-        }
-        fill = fill == last ? 0 : fill + slot_vectors;
-        rows_commit();
-    };
-    for (int i = 0; i < ahead; ++i) fetch();
-    {
-        uint32_t index, rest;
-        g.gate.split((uint32_t)r0, index, rest);
-        const void *const gate = block_row<T>(a.gate, index * a.ld_gate, a.mod_f32);
-        g.mod.split((uint32_t)r0, index, rest);
-        const void *const scale = block_row<T>(a.scale, index * a.ld_scale, a.mod_f32);
-        const void *const shift = block_row<T>(a.shift, index * a.ld_shift, a.mod_f32);
-        float4 *at = reinterpret_cast<float4 *>(s_rows);
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-            if (!(g.tables >> k & 1)) continue;
-            const bool y = k < 2, more = k & 1;
-            rows_fill<Lane>(at, g.table, (int)a.n, [&](int col) {
-                const float4 m = y ? mul4(four(branch), params4<T>(gate, col, a.mod_f32, 1.0f))
-                                   : add4(four(1.0f), params4<T>(scale, col, a.mod_f32, 0.0f));
-                const void *const w = y ? (more ? a.b_post : a.w_post) : (more ? a.b_pre : a.w_pre);
-                float4 r = mul4(m, params4<T>(w, col, a.w_f32, more ? 0.0f : 1.0f));
-                if (k == 3) r = add4(r, params4<T>(shift, col, a.mod_f32, 0.0f));
-                return r;
-            });
-            at += g.table;
-        }
-    }
-    __syncthreads();
-    S *h = static_cast<S *>(a.h) + (a.h ? (r0 + t.id) * a.ld_h + l.first : 0);
-    T *z = static_cast<T *>(a.z) + (a.z ? (r0 + t.id) * a.ld_z + l.first : 0);
-    const int64_t step_h = step * a.ld_h, step_z = step * a.ld_z;
-    for (int row = r0 + t.id; row < r1; row += step, h += step_h, z += step_z) {
-        fetch();
-        rows_wait(ahead);
-        const uint4 *const at = mine + slot;
-        slot = slot == last ? 0 : slot + slot_vectors;
-        float2 v[VPT][4];
-        float2 my = make_float2(0.0f, 1.0f);
-        if (a.y) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                if (l.none(i)) continue;
-                PartT::open(at + (kX + i * PartT::N) * kUnitThreads, kUnitThreads, v[i]);
-            }
-            if (post) my = unit_moments<LAYER>(t, l, v, a.post, a.eps_post);
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (l.none(i)) continue;
-            float2 x[4];
-            PartS::open(at + i * PartS::N * kUnitThreads, kUnitThreads, x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], two(a.stream_scale));
-            if (a.y) {
-                if (post) norm8<LAYER>(v[i], my);
-                if (!(g.tables & TABLE_Y_ADD)) {
-                    if (a.drop.least) l.drop(i, a.drop, (uint32_t)row, offset, v[i]);
-                    if (g.tables & TABLE_Y) {
-                        float2 p[4];
-                        by[0].read(i, p);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] = __ffma2_rn(v[i][k], p[k], x[k]);
-                    } else {
-                        add8(x, v[i]);
-                    }
-                } else {   // with a bias the mask comes after the factor
-                    float2 p[4], q[4];
-                    by[0].read(i, q);
-                    by[1].read(i, p);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[i][k] = __ffma2_rn(v[i][k], q[k], p[k]);
-                    if (a.drop.least) l.drop(i, a.drop, (uint32_t)row, offset, v[i]);
-                    add8(x, v[i]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[i][k] = x[k];
-            if (a.h) l.store(i, h, v[i]);
-        }
-        if (!a.z) continue;
-        const float2 mh = unit_moments<LAYER>(t, l, v, a.pre, a.eps_pre);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (l.none(i)) continue;
-            norm8<LAYER>(v[i], mh);
-            if (g.tables & TABLE_H) by[2].times(i, v[i]);
-            if (g.tables & TABLE_H_ADD) {
-                float2 p[4];
-                by[3].read(i, p);
-                add8(v[i], p);
-            }
-            l.store(i, z, v[i]);
-        }
-    }
-    rows_wait(0);
-}
-
-__device__ __forceinline__ float2 mask2(float2 v, uint32_t bits, int j) {
-    return make_float2(bits >> (2 * j) & 1 ? v.x : 0.0f, bits >> (2 * j + 1) & 1 ? v.y : 0.0f);
-}
-
-// The gradient of such units, with a pre norm; its sums in registers as
-// k_block_rows_grad's, the teams' joined in shared memory at the end, one after another.
-// A row takes one exchange (FULL, with a layer norm: one more before it, of the means).
-// What dy needs of D before D is known comes from D's parts: with t = (factor of y) (y
-// - mean) the mean of u yh is that of t D, and
-//     sum t D = sum t dh + r (sum t m - c0 sum t - r c1 sum t (h - mean)),
-// c0 and c1 the means of m and of m hh; so nothing of a row is kept in registers from
-// the sums' pass to the outputs'.  Both factors have tables.
-template <class T, class S, bool FULL, bool POST>
-__global__ void __launch_bounds__(kUnitThreads, 1)
-k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
-    using Lane = UnitLane<T, S, kUnitThreads>;
-    using WordsS = UnitWords<S, kUnitThreads>;
-    using WordsT = UnitWords<T, kUnitThreads>;
-    constexpr int VPT = kUnitGradVpt<FULL && POST>, kKinds = FULL ? 4 : 2;
-    __shared__ float s_sums[24 * kUnitWarps];
-    extern __shared__ uint4 s_rows[];   // the tables, then the rows; at the end the sums
-    UnitTeam t;
-    t.start(g, (int)a.n, s_sums);
-    Lane l;
-    l.place(t.lane, t.warp, g.warps, (int)a.n);
-    const int64_t unit = blockIdx.x, group = unit / a.cta.parts, part = unit - group * a.cta.parts;
-    const int r0 = (int)(group * a.group_rows + part * a.cta.rows);
-    const int r1 = (int)min(r0 + a.cta.rows, (group + 1) * a.group_rows);
-    const int step = g.teams;
-    const bool layer_h = FULL && a.pre == EBIN_NORM_LAYER;
-    const bool layer_y = FULL && POST && a.post == EBIN_NORM_LAYER;
-    const float branch = a.branch_scale * (a.drop.least ? a.drop.scale : 1.0f);
-    float4 *const tables = reinterpret_cast<float4 *>(s_rows);
-    const float4 *const by_y = tables + t.warp * 64 + t.lane, *const by_h = by_y + g.table;
-    const int table_step = g.warps * 64;
-    uint4 *const mine = s_rows + 2 * g.table + threadIdx.x;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
-    const int ahead = g.slots - 1, slot_vectors = g.vectors * kUnitThreads;
-    const int last = ahead * slot_vectors;
-    int fill = 0, slot = 0, next = r0 + t.id;
-    RowsFrom<S> from_h(l, a.x, a.ld_x, next, step), from_dh(l, a.dh, a.ld_dh, next, step);
-    RowsFrom<T> from_dz(l, a.dz, a.ld_dz, next, step), from_y(l, a.y, a.ld_y, next, step);
-    layer_pdl_launch();
-    layer_pdl_wait();
-    const uint2 offset = drop_offset(a.drop);
-    // h, dz, dh and y of a row lie behind one another
-    constexpr int kDz = VPT * WordsS::N, kDh = kDz + VPT * WordsT::N, kY = kDh + VPT * WordsS::N;
-    for (uint4 *p = mine; p <= mine + last; p += slot_vectors)
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            l.template clear<S>(i, p + i * WordsS::N * kUnitThreads);
-            l.template clear<T>(i, p + (kDz + i * WordsT::N) * kUnitThreads);
-            l.template clear<S>(i, p + (kDh + i * WordsS::N) * kUnitThreads);
-            if (a.y) l.template clear<T>(i, p + (kY + i * WordsT::N) * kUnitThreads);
-        }
-    auto fetch = [&]() {
-        if (next < r1) {
-            const uint32_t at = to + fill * 16;
-            from_h.template fetch<VPT>(l, at);
-            from_dz.template fetch<VPT>(l, at + kDz * (kUnitThreads * 16));
-            if (a.dh) from_dh.template fetch<VPT>(l, at + kDh * (kUnitThreads * 16));
-            if (a.y) from_y.template fetch<VPT>(l, at + kY * (kUnitThreads * 16));
-            next += step;
-        }
-        fill = fill == last ? 0 : fill + slot_vectors;
-        rows_commit();
-    };
-    for (int i = 0; i < ahead; ++i) fetch();
-    {
-        uint32_t index, rest;
-        g.gate.split((uint32_t)r0, index, rest);
-        const void *const gate = block_row<T>(a.gate, index * a.ld_gate, a.mod_f32);
-        g.mod.split((uint32_t)r0, index, rest);
-        const void *const scale = block_row<T>(a.scale, index * a.ld_scale, a.mod_f32);
-        rows_fill<Lane>(tables, g.table, (int)a.n, [&](int col) {
-            return mul4(mul4(four(branch), params4<T>(gate, col, a.mod_f32, 1.0f)),
-                        params4<T>(a.w_post, col, a.w_f32, 1.0f));
-        });
-        rows_fill<Lane>(tables + g.table, g.table, (int)a.n, [&](int col) {
-            return mul4(add4(four(1.0f), params4<T>(scale, col, a.mod_f32, 0.0f)),
-                        params4<T>(a.w_pre, col, a.w_f32, 1.0f));
-        });
-    }
-    __syncthreads();
-    float2 acc[kKinds][VPT][4];
-#pragma unroll
-    for (int k = 0; k < kKinds; ++k)
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[k][i][j] = two(0.0f);
-    constexpr int kEYh = FULL ? (int)SUM_E_YH : 1;
-    T *dy = static_cast<T *>(a.z) + (a.z ? (r0 + t.id) * a.ld_z + l.first : 0);
-    S *dx = static_cast<S *>(a.h) + (a.h ? (r0 + t.id) * a.ld_h + l.first : 0);
-    const int64_t step_y = step * a.ld_z, step_x = step * a.ld_h;
-    auto factor = [&](const float4 *table, int i, float2 *p) {
-        const float4 x = table[i * table_step], y = table[i * table_step + 32];
-        p[0] = make_float2(x.x, x.y);
-        p[1] = make_float2(x.z, x.w);
-        p[2] = make_float2(y.x, y.y);
-        p[3] = make_float2(y.z, y.w);
-    };
-    for (int row = r0 + t.id; row < r1; row += step, dy += step_y, dx += step_x) {
-        fetch();
-        rows_wait(ahead);
-        const uint4 *const at = mine + slot;
-        slot = slot == last ? 0 : slot + slot_vectors;
-        auto at_h = [&](int i) { return at + i * WordsS::N * kUnitThreads; };
-        auto at_dz = [&](int i) { return at + (kDz + i * WordsT::N) * kUnitThreads; };
-        auto at_dh = [&](int i) { return at + (kDh + i * WordsS::N) * kUnitThreads; };
-        auto at_y = [&](int i) { return at + (kY + i * WordsT::N) * kUnitThreads; };
-        float2 mh = make_float2(0.0f, 1.0f), my = mh;
-        float c0 = 0.0f, c1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
-        if (FULL && (layer_h || layer_y)) {
-            float2 s[3] = {two(0.0f), two(0.0f), two(0.0f)};   // of h, y and m: 0 past the row
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                if (l.none(i)) continue;
-                WordsS h;
-                WordsT z, y;
-                float2 k[4];
-                h.read(at_h(i));
-                z.read(at_dz(i));
-                if (POST) y.read(at_y(i));
-                factor(by_h, i, k);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[0] = __fadd2_rn(s[0], h.pair(j));
-                    if (POST) s[1] = __fadd2_rn(s[1], y.pair(j));
-                    s[2] = __ffma2_rn(z.pair(j), k[j], s[2]);
-                }
-            }
-            float q[3];
-#pragma unroll
-            for (int k = 0; k < 3; ++k) q[k] = s[k].x + s[k].y;
-            t.sums(q);
-            if (layer_h) {
-                mh.x = q[0] * t.inv_n;
-                c0 = q[2] * t.inv_n;
-            }
-            if (layer_y) my.x = q[1] * t.inv_n;
-        }
-        uint32_t bits[VPT];   // POST: what is kept
-        {
-            // sums of h h, m h, y y, t dh, t m, t h, then (FULL) of t, f dh, f m, f h and f, the
-            // factor; h and y less their means
-            constexpr int K = !POST ? 2 : FULL ? 11 : 6;
-            float2 q[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) q[k] = two(0.0f);
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                if (l.none(i)) continue;
-                WordsS h, d;
-                WordsT z, y;
-                float2 k[4], f[4];
-                h.read(at_h(i));
-                z.read(at_dz(i));
-                factor(by_h, i, k);
-                if constexpr (POST) {
-                    y.read(at_y(i));
-                    if (a.dh) d.read(at_dh(i));
-                    else d.zero();
-                    factor(by_y, i, f);
-                    if (a.drop.least) {
-                        bits[i] = l.kept(i, a.drop, (uint32_t)row, offset);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) f[j] = mask2(f[j], bits[i], j);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 m = __fmul2_rn(z.pair(j), k[j]);
-                    float2 x = h.pair(j);
-                    if constexpr (FULL) {   // past the row's end still 0
-                        x = __fadd2_rn(x, two(-mh.x));
-                        if (!l.on(i, j >> 1)) x = two(0.0f);
-                    }
-                    q[0] = __ffma2_rn(x, x, q[0]);
-                    q[1] = __ffma2_rn(m, x, q[1]);
-                    if constexpr (POST) {
-                        float2 yy = y.pair(j);
-                        const float2 dh = d.pair(j);
-                        if constexpr (FULL) {
-                            yy = __fadd2_rn(yy, two(-my.x));
-                            if (!l.on(i, j >> 1)) yy = two(0.0f);
-                        }
-                        q[2] = __ffma2_rn(yy, yy, q[2]);
-                        const float2 tt = __fmul2_rn(yy, f[j]);
-                        q[3] = __ffma2_rn(tt, dh, q[3]);
-                        q[4] = __ffma2_rn(tt, m, q[4]);
-                        q[5] = __ffma2_rn(tt, x, q[5]);
-                        if constexpr (FULL) {
-                            q[6] = __fadd2_rn(q[6], tt);
-                            q[7] = __ffma2_rn(f[j], dh, q[7]);
-                            q[8] = __ffma2_rn(f[j], m, q[8]);
-                            q[9] = __ffma2_rn(f[j], x, q[9]);
-                            q[10] = __fadd2_rn(q[10], f[j]);
-                        }
-                    }
-                }
-            }
-            float w[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) w[k] = q[k].x + q[k].y;
-            t.sums(w);
-            mh.y = rsqrtf(fmaf(w[0], t.inv_n, a.eps_pre));
-            c1 = w[1] * mh.y * t.inv_n;
-            if constexpr (POST) {
-                my.y = rsqrtf(fmaf(w[2], t.inv_n, a.eps_post));
-                const float back = mh.y * c1;
-                float d = fmaf(-back, w[5], w[4]);
-                if constexpr (FULL) d = fmaf(-c0, w[6], d);
-                b0 = fmaf(mh.y, d, w[3]) * my.y * t.inv_n;
-                if (FULL && layer_y) {
-                    d = fmaf(-c0, w[FULL ? 10 : 0], fmaf(-back, w[FULL ? 9 : 0], w[FULL ? 8 : 0]));
-                    b1 = fmaf(mh.y, d, w[FULL ? 7 : 0]) * t.inv_n;
-                }
-            }
-        }
-        const float2 rh = two(mh.y), ry = two(my.y), down = two(-c1), off = two(-b0);
-        const float2 rb = two(-b1 * my.y);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (l.none(i)) continue;
-            float2 v[4];   // D, then e, then u and dy
-            {
-                WordsS h, d;
-                WordsT z;
-                float2 k[4];
-                h.read(at_h(i));
-                z.read(at_dz(i));
-                if (a.dh) d.read(at_dh(i));
-                else d.zero();
-                factor(by_h, i, k);
-                float2 out[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float2 x = h.pair(j);
-                    if constexpr (FULL) x = __fadd2_rn(x, two(-mh.x));
-                    x = __fmul2_rn(x, rh);
-                    const float2 dz = z.pair(j);
-                    acc[0][i][j] = __ffma2_rn(dz, x, acc[0][i][j]);
-                    float2 m;
-                    if constexpr (FULL) {
-                        acc[1][i][j] = __fadd2_rn(acc[1][i][j], dz);
-                        m = __ffma2_rn(dz, k[j], two(-c0));
-                    } else {
-                        m = __fmul2_rn(dz, k[j]);
-                    }
-                    v[j] = __ffma2_rn(__ffma2_rn(x, down, m), rh, d.pair(j));
-                    out[j] = __fmul2_rn(v[j], two(a.stream_scale));
-                }
-                if (a.h) l.store(i, dx, out);
-            }
-            if (a.drop.least) {
-                if constexpr (POST) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = mask2(v[j], bits[i], j);
-                } else {
-                    l.drop(i, a.drop, (uint32_t)row, offset, v);
-                }
-            }
-            if constexpr (FULL) add8(acc[kKinds - 1][i], v);
-            float2 f[4];
-            factor(by_y, i, f);
-            if (POST || a.y) {
-                WordsT y;
-                y.read(at_y(i));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float2 x = y.pair(j);
-                    if constexpr (POST) {
-                        if constexpr (FULL) x = __fadd2_rn(x, two(-my.x));
-                        x = __fmul2_rn(x, ry);
-                    }
-                    acc[kEYh][i][j] = __ffma2_rn(v[j], x, acc[kEYh][i][j]);
-                    v[j] = __fmul2_rn(v[j], f[j]);
-                    if constexpr (POST) {
-                        v[j] = __ffma2_rn(x, off, v[j]);
-                        v[j] = FULL ? __ffma2_rn(v[j], ry, rb) : __fmul2_rn(v[j], ry);
-                    }
-                }
-            } else {
-                mul8(v, f);
-            }
-            if (a.z) l.store(i, dy, v);
-        }
-    }
-    rows_wait(0);
-    if (!a.partial) return;
-    float2 *const sums = reinterpret_cast<float2 *>(s_rows) + t.warp * 32 + t.lane;
-    const int team_threads = g.warps * 32;
-    for (int team = 0; team < g.teams; ++team) {
-        __syncthreads();   // the rows have been read; the team before has added
-        if (t.id != team) continue;
-        float *const partial = a.partial + unit * 4 * a.n + l.first;
-#pragma unroll
-        for (int k = 0; k < kKinds; ++k)
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                if (l.none(i)) continue;
-                float2 *const at = sums + (k * VPT + i) * 4 * team_threads;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (team > 0) acc[k][i][j] = __fadd2_rn(at[j * team_threads], acc[k][i][j]);
-                    if (team + 1 < g.teams) at[j * team_threads] = acc[k][i][j];
-                }
-                if (team + 1 < g.teams) continue;
-                const int kind = FULL ? k : 2 * k;
-                if (kind == SUM_E_YH || kind == SUM_E) {   // they carry their factor from here on
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[k][i][j] = __fmul2_rn(acc[k][i][j], two(branch));
-                }
-                l.store(i, partial + kind * a.n, acc[k][i]);
-            }
     }
 }
 

@@ -159,6 +159,56 @@ def test_rows_and_groups(rows, groups, n):
     check_gradient(t, p, "layer", "layer", 0.1)
 
 
+@pytest.mark.parametrize("dtype,stream", TYPES)
+@pytest.mark.parametrize("n", [1, 7, 77, 256, 515, 1021, 2052, 4097, 8191])
+@pytest.mark.parametrize("post,pre", [("none", "rms"), ("none", "layer"), ("rms", "rms"),
+                                      ("layer", "layer")])
+def test_many_ragged_rows(n, post, pre, dtype, stream):
+    """Enough rows that a CTA walks several, each tensor off the vectors in a way of its own."""
+    rows, groups = 636, 2
+    t, p = operands(rows, n, dtype, stream, groups, weights=dtype, mods=dtype)
+    t["x"] = matrix(31, rows, n, stream, "odd stride")
+    t["y"] = matrix(32, rows, n, dtype, "off")
+    p = valid(p, post, pre)
+    h, z = check_forward(t, p, post, pre, 0.25, 0.9, 0.5)
+    kw = dict(post=post, pre=pre, epsilon=1e-5, epsilon_post=1e-3, dropout=0.25, seed=SEED,
+              offset=OFFSET, stream_scale=0.9, branch_scale=0.5, **p)
+    for how_h, how_z in (("strided", "off"), ("odd stride", "odd stride")):
+        oh, oz = matrix(33, rows, n, stream, how_h), matrix(34, rows, n, dtype, how_z)
+        eb.block_norm(t["x"], t["y"], out=(oh, oz), **kw)
+        assert torch.equal(oh, h) and torch.equal(oz, z)
+    whole = torch.full((rows * n + 64,), 7.0, device="cuda", dtype=dtype)
+    inside = whole[33:33 + rows * n].view(rows, n)
+    eb.block_norm(t["x"], t["y"], out=(None, inside), **kw)
+    assert torch.equal(inside, z)
+    assert (whole[:33] == 7).all() and (whole[33 + rows * n:] == 7).all()
+    got = check_gradient(t, p, post, pre, 0.25, 0.9, 0.5)
+    dz, dh = matrix(21, rows, n, dtype), matrix(22, rows, n, stream)
+    dx, dy = matrix(35, rows, n, stream, "off"), matrix(36, rows, n, dtype, "odd stride")
+    eb.block_norm_grad(dz, dh, t["x"], t["y"], out=(dx, dy), **kw)
+    assert torch.equal(dx, got["x"]) and torch.equal(dy, got["y"])
+
+
+@pytest.mark.parametrize("n", [520, 523])
+@pytest.mark.parametrize("rows", [305, 1000])
+def test_many_rows_in_place(rows, n):
+    t, p = operands(rows, n, BF16, BF16, 0)
+    kw = dict(post="layer", pre="rms", dropout=0.1, **p)
+    want = eb.block_norm(t["x"], t["y"], **kw)
+    for ho, zo in (("x", "y"), ("y", "x")):
+        c = {k: v.clone() for k, v in t.items()}
+        for a, b in zip(eb.block_norm(c["x"], c["y"], out=(c[ho], c[zo]), **kw), want):
+            assert torch.equal(a, b)
+    dz, dh = matrix(21, rows, n, BF16), matrix(22, rows, n, BF16)
+    want = eb.block_norm_grad(dz, dh, t["x"], t["y"], **kw)
+    for names in (("dh", "y"), ("h", "dz"), ("dz", "dh"), ("y", "h")):
+        c = {"dz": dz.clone(), "dh": dh.clone(), "h": t["x"].clone(), "y": t["y"].clone()}
+        got = eb.block_norm_grad(c["dz"], c["dh"], c["h"], c["y"],
+                                 out=(c[names[0]], c[names[1]]), **kw)
+        for k in want:
+            assert torch.equal(got[k], want[k]), (names, k)
+
+
 def test_one_gate_beside_grouped_scales():
     for gate, mods in ((0, 4), (4, 0)):
         t, p = operands(48, 264, BF16, F32, gate)
