@@ -754,6 +754,12 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
     };
     for (int row = r0 + t.id; row < r1; row += step, dy += step_y, dx += step_x) {
         fetch();
+        // what both passes keep, drawn while the row is on its way
+        uint32_t bits[VPT];
+        if (POST && a.drop.least)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (!l.none(i)) bits[i] = l.kept(i, a.drop, (uint32_t)row, offset);
         rows_wait(ahead);
         if (RAG) __syncwarp();   // a lane reads what its neighbour copied
         const char *const at = mine + slot;
@@ -801,7 +807,6 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
             }
             if (layer_y) my.x = q[1] * t.inv_n;
         }
-        uint32_t bits[VPT];   // POST: what is kept
         {
             // sums of h h, m h, y y, t dh, t m, t h, then (FULL) of t, f dh, f m, f h and f, the
             // factor; h and y less their means
@@ -822,11 +827,9 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
                     read_y(i, y);
                     read_dh(i, d);
                     factor(by_y, i, f);
-                    if (a.drop.least) {
-                        bits[i] = l.kept(i, a.drop, (uint32_t)row, offset);
+                    if (a.drop.least)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) f[j] = mask2(f[j], bits[i], j);
-                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
