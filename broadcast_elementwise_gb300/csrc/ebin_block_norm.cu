@@ -190,20 +190,21 @@ bool block_float(ebin_dtype t) {
 ebin_status prepare_block(const ebin_block_norm_plan_s &p, const ebin_block_norm_params &w,
                           BlockArgs &a) {
     const ebin_block_norm_attrs &at = p.at;
-    if ((w.gate && !at.has_branch) ||
+    const bool post = at.post != EBIN_NORM_NONE, pre = at.pre != EBIN_NORM_NONE;
+    if ((w.gate && !at.has_branch) || (!post && (w.w_post || w.b_post)) ||
+        (!pre && (w.w_pre || w.b_pre || w.scale || w.shift)) ||
         ((uintptr_t)w.gate | (uintptr_t)w.scale | (uintptr_t)w.shift) % (uintptr_t)p.msz ||
         ((uintptr_t)w.w_post | (uintptr_t)w.b_post | (uintptr_t)w.w_pre | (uintptr_t)w.b_pre) %
             (uintptr_t)p.wsz || (uintptr_t)w.offset_device % 8)
         return EBIN_ERR_INVALID_ARG;
-    const bool post = at.post != EBIN_NORM_NONE, pre = at.pre != EBIN_NORM_NONE;
     a = BlockArgs{};
     a.gate = w.gate;
-    a.w_post = post ? w.w_post : nullptr;
-    a.b_post = post ? w.b_post : nullptr;
-    a.w_pre = pre ? w.w_pre : nullptr;
-    a.b_pre = pre ? w.b_pre : nullptr;
-    a.scale = pre ? w.scale : nullptr;
-    a.shift = pre ? w.shift : nullptr;
+    a.w_post = w.w_post;
+    a.b_post = w.b_post;
+    a.w_pre = w.w_pre;
+    a.b_pre = w.b_pre;
+    a.scale = w.scale;
+    a.shift = w.shift;
     a.ld_gate = at.ld_gate;
     a.ld_scale = at.ld_scale;
     a.ld_shift = at.ld_shift;

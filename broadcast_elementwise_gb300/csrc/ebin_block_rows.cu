@@ -119,8 +119,8 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
     if (vec) {
         const size_t row = (size_t)threads * vpt * 16 * (s_vectors + t_vectors);
         g.slots = rows_slots(row, 0, per_sm);
-        if (g.slots < 1) return cudaSuccess;
         smem = g.slots * row;
+        vec = g.slots > 0;   // rows too wide for shared memory are read where they lie
     }
     const int64_t grid = std::min<int64_t>(div_up(a.rows, g.teams),
                                            (int64_t)per_sm * current_sm_count());
@@ -146,7 +146,8 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
     const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};
     const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
     const bool post = a.post != EBIN_NORM_NONE;
-    const int unit_vpt = full && post ? kUnitGradVpt<true> : kUnitGradVpt<false>;
+    const int unit_vpt = !full ? kUnitGradVpt<false, false>
+                       : post ? kUnitGradVpt<true, true> : kUnitGradVpt<true, false>;
     if (a.pre != EBIN_NORM_NONE && div_up(chunks, unit_vpt) <= kUnitWarps &&
         cta_takes(a, chunks, unit_vpt)) {
         RowsGeom g = unit_geom(a, chunks, unit_vpt);
@@ -189,7 +190,7 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
         const size_t row = (size_t)g.vectors * 16 * threads;
         if (row > 0) {
             g.slots = rows_slots(row, factors, std::min(std::max(1, 512 / threads), 16));
-            if (g.slots < 1) return cudaSuccess;
+            vec = g.slots > 0;   // rows too wide for shared memory are read where they lie
         }
         smem += g.slots * row;
     }

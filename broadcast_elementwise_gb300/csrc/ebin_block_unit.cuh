@@ -667,7 +667,9 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
     using Lane = UnitLane<T, S, RAG>;
     using WordsS = typename Lane::template Words<S>;
     using WordsT = typename Lane::template Words<T>;
-    constexpr int VPT = kUnitGradVpt<FULL && POST>, kKinds = FULL ? 4 : 2;
+    constexpr int VPT = kUnitGradVpt<FULL, POST>;
+    // the sums kept: SUM_E is a post norm's bias' alone
+    constexpr int kKinds = !FULL ? 2 : POST ? 4 : 3;
     __shared__ float s_sums[24 * kUnitWarps];
     extern __shared__ uint4 s_rows[];   // the tables, then the rows; at the end the sums
     UnitTeam t;
@@ -917,7 +919,7 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
                     l.drop(i, a.drop, (uint32_t)row, offset, v);
                 }
             }
-            if constexpr (FULL) add8(acc[kKinds - 1][i], v);
+            if constexpr (FULL && POST) add8(acc[kKinds - 1][i], v);
             float2 f[4];
             factor(by_y, i, f);
             if (POST || a.y) {

@@ -949,7 +949,8 @@ ebin_status ebin_dropout_grad_execute(ebin_dropout_plan_t plan, const void *dy, 
  *
  * gate, scale and shift are one row for all rows, or one for each group of
  * consecutive rows (the condition of a sequence of a batch).  Weights, biases,
- * gate, scale and shift may each be NULL: 1, 0, 1, 0 and 0.
+ * gate, scale and shift may each be NULL: 1, 0, 1, 0 and 0.  Rows of any width and
+ * alignment are accepted.
  * Arithmetic is binary32, with one rounding to the element type at the end: N_pre
  * reads h before it is rounded.
  */
@@ -1020,7 +1021,8 @@ typedef struct ebin_block_norm_params {
  * An output may be an input of its own type (the same pointer and row stride);
  * any other overlap with an output is ALIAS.
  * Errors: INVALID_ARG (a NULL buffer with work to do, a buffer off its element's
- * boundary, a gradient plan, a gate without a branch), ALIAS, CUDA.
+ * boundary, a gradient plan, a gate without a branch, a parameter of a norm that
+ * is NONE; scale and shift are pre's), ALIAS, CUDA.
  */
 ebin_status ebin_block_norm_execute(ebin_block_norm_plan_t plan, const void *x, const void *y,
                                     const ebin_block_norm_params *params, void *h, void *z,

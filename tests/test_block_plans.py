@@ -139,6 +139,10 @@ def test_block_execute_refusals():
     for kw in (dict(x=0x100001), dict(h=0x300001), dict(z=0x400001), dict(gate=0x500001),
                dict(w_pre=0x500001), dict(scale=0x500001), dict(offset_device=0x500004)):
         assert code(run, p, **kw) == "invalid_arg"
+    for kw in (dict(w_post=0x500000), dict(b_post=0x500000)):
+        assert code(run, p, **kw) == "invalid_arg"                         # post is none
+    for name in ("w_pre", "b_pre", "scale", "shift"):
+        assert code(run, block(pre="none"), **{name: 0x500000}) == "invalid_arg"
     assert code(run, block(stream_dtype="float32"), x=0x100002) == "invalid_arg"
     assert code(run, block(weight_dtype="float32"), b_pre=0x500002) == "invalid_arg"
     assert code(run, block(mod_dtype="float32"), gate=0x500002) == "invalid_arg"

@@ -139,6 +139,16 @@ def test_wide_rows(n, dtype, stream):
     check_gradient(t, p, "layer", "rms", 0.1)
 
 
+@pytest.mark.parametrize("n", [8200, 12288, 16384])
+@pytest.mark.parametrize("post,pre", [("rms", "rms"), ("none", "layer")])
+@pytest.mark.parametrize("dtype,stream", [(BF16, BF16), (F32, F32), (F16, F32)])
+def test_many_wide_rows(n, post, pre, dtype, stream):
+    t, p = operands(400, n, dtype, stream, 0)
+    p = valid(p, post, pre)
+    check_forward(t, p, post, pre)
+    check_gradient(t, p, post, pre)
+
+
 @pytest.mark.parametrize("how", ["strided", "odd stride", "off"])
 @pytest.mark.parametrize("dtype,stream", TYPES)
 @pytest.mark.parametrize("n", [40, 256, 1160])
