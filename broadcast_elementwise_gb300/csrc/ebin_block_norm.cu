@@ -18,52 +18,50 @@ __device__ __forceinline__ float sums_at(const BlockSumsArgs &a, const void *p, 
 }
 
 // The sums of a CTA's 32 columns, [kind][column], over `count` rows of them that lie
-// `stride` apart from `first` on, for the kinds wanted, each n further: eight lanes of four
-// columns (V = 4; V = 1: 32 of one) take every 32nd row, all kinds' loads together, then
-// the 32 join in order: an order fixed by the count.
+// `stride` apart from `first` on, each kind n further.  1024 / V threads take a kind that is
+// wanted: lanes of V columns every 32nd row, then the 32 join in order: an order fixed by
+// the count.
 template <int V>
 __device__ __forceinline__ void sums_columns(const BlockSumsArgs &a, const float *first,
                                              int64_t count, int64_t stride, int64_t col0,
                                              float (*s)[kSumRows][kSumColumns + 1],
                                              float (*total)[kSumColumns]) {
-    constexpr int L = kSumColumns / V;
-    const int lane = threadIdx.x % L, row = threadIdx.x / L;
+    constexpr int L = kSumColumns / V, kThreads = L * kSumRows;
+    const int lane = threadIdx.x % L, row = threadIdx.x / L % kSumRows;
     const int64_t col = col0 + lane * V;
-    float v[4][V];
+    int rank = threadIdx.x / kThreads;   // among the kinds wanted
+    for (int k = 0; k < 4; ++k) {
+        if (!(a.need >> k & 1) || rank-- != 0) continue;
+        rank += blockDim.x / kThreads;   // what this thread takes next
+        float v[V];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[k][e] = 0.0f;
-    if (col < a.n) {
-        const float *p = first + col + row * stride;
-#pragma unroll 4
-        for (int64_t c = row; c < count; c += kSumRows, p += kSumRows * stride) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (!(a.need >> k & 1)) continue;
+        for (int e = 0; e < V; ++e) v[e] = 0.0f;
+        if (col < a.n) {
+            const float *p = first + k * a.n + col + row * stride;
+#pragma unroll 8
+            for (int64_t c = row; c < count; c += kSumRows, p += kSumRows * stride) {
                 if constexpr (V == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(p + k * a.n);
-                    v[k][0] += x.x;
-                    v[k][1] += x.y;
-                    v[k][2] += x.z;
-                    v[k][3] += x.w;
+                    const float4 x = *reinterpret_cast<const float4 *>(p);
+                    v[0] += x.x;
+                    v[1] += x.y;
+                    v[2] += x.z;
+                    v[3] += x.w;
                 } else {
-                    v[k][0] += p[k * a.n];
+                    v[0] += *p;
                 }
             }
         }
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[k][row][lane * V + e] = v[e];
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[k][row][lane * V + e] = v[k][e];
     __syncthreads();
     for (int j = threadIdx.x; j < 4 * kSumColumns; j += blockDim.x) {
-        const int k = j / kSumColumns, c = j % kSumColumns;
+        const int kind = j / kSumColumns, c = j % kSumColumns;
         float t = 0.0f;
+        if (a.need >> kind & 1)
 #pragma unroll
-        for (int r = 0; r < kSumRows; ++r) t += s[k][r][c];
-        total[k][c] = t;
+            for (int r = 0; r < kSumRows; ++r) t += s[kind][r][c];
+        total[kind][c] = t;
     }
     __syncthreads();
 }
@@ -94,7 +92,7 @@ __device__ __forceinline__ void sums_shared(const BlockSumsArgs &a, int64_t j, c
 // and shift; then, with one group, everything, else its share of what all rows
 // have in common, into its first part's place.
 template <int V>
-__global__ void __launch_bounds__(kSumColumns *kSumRows / V) k_block_sums(const BlockSumsArgs a) {
+__global__ void __launch_bounds__(1024) k_block_sums(const BlockSumsArgs a) {
     __shared__ float s[4][kSumRows][kSumColumns + 1], total[4][kSumColumns];
     const int64_t group = blockIdx.x / a.tiles, col0 = (blockIdx.x - group * a.tiles) * kSumColumns;
     layer_pdl_launch();
@@ -134,8 +132,7 @@ __global__ void __launch_bounds__(kSumColumns *kSumRows / V) k_block_sums(const 
 
 // The groups' shares joined.
 template <int V>
-__global__ void __launch_bounds__(kSumColumns *kSumRows / V)
-k_block_sums_all(const BlockSumsArgs a) {
+__global__ void __launch_bounds__(1024) k_block_sums_all(const BlockSumsArgs a) {
     __shared__ float s[4][kSumRows][kSumColumns + 1], total[4][kSumColumns];
     const int64_t col0 = (int64_t)blockIdx.x * kSumColumns;
     layer_pdl_launch();
@@ -246,8 +243,11 @@ int param_ranges(const ebin_block_norm_plan_s &p, const BlockArgs &a, Range *r) 
 }
 
 cudaError_t launch_sums(const BlockSumsArgs &a, cudaStream_t s) {
-    const bool vec = a.n % 4 == 0;   // the workspace starts on 16 bytes
-    const int threads = kSumColumns * kSumRows / (vec ? 4 : 1);
+    // a kind takes 256 threads (the workspace starts on 16 bytes), off the vectors one takes
+    // 1024 and the others follow
+    const bool vec = a.n % 4 == 0;
+    const int kinds = __builtin_popcount(a.need);
+    const int threads = vec ? kinds * 256 : 1024;
     const dim3 grid((unsigned)(a.tiles * a.groups)), tiles((unsigned)a.tiles);
     cudaError_t e = launch_layer(vec ? k_block_sums<4> : k_block_sums<1>, grid, threads, 0, s, 1, a);
     if (e == cudaSuccess && a.second)
