@@ -34,15 +34,16 @@ struct BlockArgs {
     DropArgs drop;
     BlockUnits cta, team;          // units of a CTA, of a team
     int64_t groups, group_rows;
-    float *partial;                // [units][4][n]: sums of dz hh, dz, e yh, e; or null
+    float *partial;                // [units][4][pad]: sums of dz hh, dz, e yh, e; or null
+    int64_t pad;                   // n in whole vectors of four
     int32_t need;                  // which of the four, by bit
 };
 
 enum BlockSum : int { SUM_DZ_HH = 0, SUM_DZ = 1, SUM_E_YH = 2, SUM_E = 3 };
 
 struct BlockSumsArgs {
-    float *partial;                // [groups * parts][4][n]
-    int64_t parts, groups, n;
+    float *partial;                // [groups * parts][4][pad]
+    int64_t parts, groups, n, pad;
     int64_t tiles;                 // of 32 columns
     const void *gate, *w_post, *b_post, *w_pre, *b_pre, *scale;
     int64_t ld_gate, ld_scale;
@@ -171,11 +172,11 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
     const int64_t group = blockIdx.x / a.team.parts, part = blockIdx.x - group * a.team.parts;
     const int64_t r0 = group * a.group_rows + part * a.team.rows;
     const int64_t r1 = min(r0 + a.team.rows, (group + 1) * a.group_rows);
-    float *const sums = a.partial ? a.partial + (int64_t)blockIdx.x * 4 * a.n : nullptr;
+    float *const sums = a.partial ? a.partial + (int64_t)blockIdx.x * 4 * a.pad : nullptr;
     if (sums)
         for (int64_t j = threadIdx.x; j < a.n; j += kBlockAnyThreads)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sums[k * a.n + j] = 0.0f;
+            for (int k = 0; k < 4; ++k) sums[k * a.pad + j] = 0.0f;
     const float inv = 1.0f / (float)a.n;
     for (int64_t row = r0; row < r1; ++row) {
         const S *h = static_cast<const S *>(a.x) + (a.x ? row * a.ld_x : 0);
@@ -233,11 +234,11 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
             if (sums) {
                 if (a.dz) {
                     const float g = to_f(dz[j]);
-                    sums[SUM_DZ_HH * a.n + j] += g * normed(j);
-                    sums[SUM_DZ * a.n + j] += g;
+                    sums[SUM_DZ_HH * a.pad + j] += g * normed(j);
+                    sums[SUM_DZ * a.pad + j] += g;
                 }
-                sums[SUM_E_YH * a.n + j] += e * yh;
-                sums[SUM_E * a.n + j] += e;
+                sums[SUM_E_YH * a.pad + j] += e * yh;
+                sums[SUM_E * a.pad + j] += e;
             }
             float u = e * weigh(j);
             if (a.post != EBIN_NORM_NONE) u = my.y * (u - b[0] - yh * b[1]);

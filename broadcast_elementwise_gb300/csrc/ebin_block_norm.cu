@@ -18,42 +18,32 @@ __device__ __forceinline__ float sums_at(const BlockSumsArgs &a, const void *p, 
 }
 
 // The sums of a CTA's 32 columns, [kind][column], over `count` rows of them that lie
-// `stride` apart from `first` on, each kind n further.  1024 / V threads take a kind that is
-// wanted: lanes of V columns every 32nd row, then the 32 join in order: an order fixed by
-// the count.
-template <int V>
+// `stride` apart from `first` on, each kind `pad` further.  256 threads take a kind that is
+// wanted: eight lanes of four columns every 32nd row, then the 32 join in order: an order
+// fixed by the count.
 __device__ __forceinline__ void sums_columns(const BlockSumsArgs &a, const float *first,
                                              int64_t count, int64_t stride, int64_t col0,
                                              float (*s)[kSumRows][kSumColumns + 1],
                                              float (*total)[kSumColumns]) {
-    constexpr int L = kSumColumns / V, kThreads = L * kSumRows;
-    const int lane = threadIdx.x % L, row = threadIdx.x / L % kSumRows;
-    const int64_t col = col0 + lane * V;
-    int rank = threadIdx.x / kThreads;   // among the kinds wanted
-    for (int k = 0; k < 4; ++k) {
-        if (!(a.need >> k & 1) || rank-- != 0) continue;
-        rank += blockDim.x / kThreads;   // what this thread takes next
-        float v[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = 0.0f;
-        if (col < a.n) {
-            const float *p = first + k * a.n + col + row * stride;
+    const int lane = threadIdx.x & 7, row = threadIdx.x >> 3 & 31;
+    int k = 0;   // this thread's kind: the bit of its rank
+    for (int rank = threadIdx.x >> 8; k < 3; ++k)
+        if (a.need >> k & 1 && rank-- == 0) break;
+    const int64_t col = col0 + lane * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (col < a.n) {   // the last vector ends in the padding
+        const float *p = first + k * a.pad + col + row * stride;
 #pragma unroll 8
-            for (int64_t c = row; c < count; c += kSumRows, p += kSumRows * stride) {
-                if constexpr (V == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(p);
-                    v[0] += x.x;
-                    v[1] += x.y;
-                    v[2] += x.z;
-                    v[3] += x.w;
-                } else {
-                    v[0] += *p;
-                }
-            }
+        for (int64_t c = row; c < count; c += kSumRows, p += kSumRows * stride) {
+            const float4 x = *reinterpret_cast<const float4 *>(p);
+            v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[k][row][lane * V + e] = v[e];
     }
+    float *const at = &s[k][row][lane * 4];
+    at[0] = v.x;
+    at[1] = v.y;
+    at[2] = v.z;
+    at[3] = v.w;
     __syncthreads();
     for (int j = threadIdx.x; j < 4 * kSumColumns; j += blockDim.x) {
         const int kind = j / kSumColumns, c = j % kSumColumns;
@@ -91,14 +81,13 @@ __device__ __forceinline__ void sums_shared(const BlockSumsArgs &a, int64_t j, c
 // One CTA per group and 32 columns: the group's parts joined; its gradients of gate, scale
 // and shift; then, with one group, everything, else its share of what all rows
 // have in common, into its first part's place.
-template <int V>
 __global__ void __launch_bounds__(1024) k_block_sums(const BlockSumsArgs a) {
     __shared__ float s[4][kSumRows][kSumColumns + 1], total[4][kSumColumns];
     const int64_t group = blockIdx.x / a.tiles, col0 = (blockIdx.x - group * a.tiles) * kSumColumns;
     layer_pdl_launch();
     layer_pdl_wait();
-    float *const at = a.partial + group * a.parts * 4 * a.n;
-    sums_columns<V>(a, at, a.parts, 4 * a.n, col0, s, total);
+    float *const at = a.partial + group * a.parts * 4 * a.pad;
+    sums_columns(a, at, a.parts, 4 * a.pad, col0, s, total);
     const int64_t j = col0 + threadIdx.x;
     if (threadIdx.x >= kSumColumns || j >= a.n) return;
     float t[4];
@@ -124,20 +113,19 @@ __global__ void __launch_bounds__(1024) k_block_sums(const BlockSumsArgs a) {
         ? 1.0f + sums_at(a, a.scale, group * a.ld_scale + j, a.mod_f32, 0.0f) : 1.0f;
     const float gate = a.gate_grouped
         ? sums_at(a, a.gate, group * a.ld_gate + j, a.mod_f32, 1.0f) : 1.0f;
-    at[SUM_DZ_HH * a.n + j] = scale * t[SUM_DZ_HH];
-    at[SUM_DZ * a.n + j] = scale * t[SUM_DZ];
-    at[SUM_E_YH * a.n + j] = gate * t[SUM_E_YH];
-    at[SUM_E * a.n + j] = gate * t[SUM_E];
+    at[SUM_DZ_HH * a.pad + j] = scale * t[SUM_DZ_HH];
+    at[SUM_DZ * a.pad + j] = scale * t[SUM_DZ];
+    at[SUM_E_YH * a.pad + j] = gate * t[SUM_E_YH];
+    at[SUM_E * a.pad + j] = gate * t[SUM_E];
 }
 
 // The groups' shares joined.
-template <int V>
 __global__ void __launch_bounds__(1024) k_block_sums_all(const BlockSumsArgs a) {
     __shared__ float s[4][kSumRows][kSumColumns + 1], total[4][kSumColumns];
     const int64_t col0 = (int64_t)blockIdx.x * kSumColumns;
     layer_pdl_launch();
     layer_pdl_wait();
-    sums_columns<V>(a, a.partial, a.groups, 4 * a.n * a.parts, col0, s, total);
+    sums_columns(a, a.partial, a.groups, 4 * a.pad * a.parts, col0, s, total);
     const int64_t j = col0 + threadIdx.x;
     if (threadIdx.x >= kSumColumns || j >= a.n) return;
     float t[4];
@@ -178,6 +166,9 @@ bool apart(const Range &x, const Range &y, int64_t rows) {
     if (!x.p || !y.p || !ranges_overlap(x.p, x.bytes, y.p, y.bytes)) return true;
     return x.p == y.p && x.size == y.size && x.ld > 0 && y.ld > 0 && (rows <= 1 || x.ld == y.ld);
 }
+
+// Columns of a row of sums: whole vectors.
+int64_t pad_of(int64_t n) { return div_up(n, 4) * 4; }
 
 bool block_float(ebin_dtype t) {
     return t == EBIN_FLOAT32 || t == EBIN_FLOAT16 || t == EBIN_BFLOAT16;
@@ -243,16 +234,11 @@ int param_ranges(const ebin_block_norm_plan_s &p, const BlockArgs &a, Range *r) 
 }
 
 cudaError_t launch_sums(const BlockSumsArgs &a, cudaStream_t s) {
-    // a kind takes 256 threads (the workspace starts on 16 bytes), off the vectors one takes
-    // 1024 and the others follow
-    const bool vec = a.n % 4 == 0;
-    const int kinds = __builtin_popcount(a.need);
-    const int threads = vec ? kinds * 256 : 1024;
-    const dim3 grid((unsigned)(a.tiles * a.groups)), tiles((unsigned)a.tiles);
-    cudaError_t e = launch_layer(vec ? k_block_sums<4> : k_block_sums<1>, grid, threads, 0, s, 1, a);
+    const int threads = 256 * __builtin_popcount(a.need);
+    cudaError_t e = launch_layer(k_block_sums, dim3((unsigned)(a.tiles * a.groups)), threads, 0, s,
+                                 1, a);
     if (e == cudaSuccess && a.second)
-        e = launch_layer(vec ? k_block_sums_all<4> : k_block_sums_all<1>, tiles, threads, 0, s, 1,
-                         a);
+        e = launch_layer(k_block_sums_all, dim3((unsigned)a.tiles), threads, 0, s, 1, a);
     return e;
 }
 
@@ -313,21 +299,24 @@ BlockUnits block_units(int64_t group_rows, int64_t parts) {
     return u;
 }
 
-// Units of a CTA an SM: of all counts of parts the one whose last wave of 152 ends
-// first, a unit costing its teams' rows and what three more would (its tables, its
-// sums).
-BlockUnits cta_units(int64_t groups, int64_t group_rows, int64_t n, int vpt) {
-    const int64_t teams = std::max<int64_t>(1, 16 / std::max<int64_t>(1, div_up(div_up(n, 256), vpt)));
-    int64_t best = 1;
-    double least = 0.0;
-    for (int64_t p = 1; p <= std::min<int64_t>(group_rows, div_up(456, groups)); ++p) {
-        const double t = (double)div_up(groups * p, 152) * (double)(div_up(div_up(group_rows, p), teams) + 3);
-        if (p == 1 || t < least) {
-            least = t;
-            best = p;
-        }
-    }
-    return block_units(group_rows, best);
+// Units of a CTA an SM.  A count of parts is judged by when its last wave of 152 ends, a
+// unit costing its teams' steps and what three more would (its tables, its sums).  Of a
+// gradient's the least within a thirtieth of the best: SMs left over are where the last
+// sums begin ([8192,4096] bf16: 147 units 69.2 us, 152 units 71.6); but a step more of few
+// costs more than that gives ([16388,1152] in four groups: 148 units 66.1, 152 units 63.7).
+BlockUnits cta_units(int64_t groups, int64_t group_rows, int64_t n, int vpt, bool gradient) {
+    const int64_t warps = std::max<int64_t>(1, div_up(div_up(n, 256), vpt));
+    const int64_t teams = std::max<int64_t>(1, kUnitWarps / warps);
+    const int64_t most = std::min<int64_t>(group_rows, div_up(3 * 152, groups));
+    auto cost = [&](int64_t p) {
+        return (double)div_up(groups * p, 152) *
+               (double)(div_up(div_up(group_rows, p), teams) + 3);
+    };
+    double least = cost(1);
+    for (int64_t p = 2; p <= most; ++p) least = std::min(least, cost(p));
+    int64_t p = 1;
+    while (cost(p) > (gradient ? 1.0 + 1.0 / 29 : 1.0) * least) ++p;
+    return block_units(group_rows, p);
 }
 
 // Units of teams: as many over all groups as 152 SMs hold teams of the row kernel at 128
@@ -388,7 +377,11 @@ extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *
     if (a.rows > 0) {
         p->group_rows = per ? per : a.rows;
         p->groups = a.rows / p->group_rows;
-        p->cta = cta_units(p->groups, p->group_rows, a.n, kUnitVpt);
+        const bool layer = a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
+        const int vpt = !a.gradient ? kUnitVpt
+                      : layer && a.post != EBIN_NORM_NONE ? kUnitGradVpt<true, true>
+                                                          : kUnitGradVpt<true, false>;
+        p->cta = cta_units(p->groups, p->group_rows, a.n, vpt, a.gradient != 0);
         if (a.gradient) {
             if (p->groups * div_up(a.n, kSumColumns) > 0x7FFFFFFF) {   // CTAs of the last step
                 delete p;
@@ -396,7 +389,7 @@ extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *
             }
             p->team = team_units(p->groups, p->group_rows, a.n);
             p->workspace = sizeof(float) * 4 *
-                (size_t)(p->groups * std::max(p->cta.parts, p->team.parts) * a.n);
+                (size_t)(p->groups * std::max(p->cta.parts, p->team.parts) * pad_of(a.n));
         }
     }
     *out = p;
@@ -536,6 +529,7 @@ extern "C" ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan,
     a.ld_h = at.ld_dx;
     a.ld_z = at.ld_dy;
     a.partial = wanted ? static_cast<float *>(workspace) : nullptr;
+    a.pad = pad_of(at.n);
     if (g.scale || g.w_pre) a.need |= 1 << SUM_DZ_HH;
     if (g.shift || g.b_pre || (g.scale && a.b_pre)) a.need |= 1 << SUM_DZ;
     if (g.gate || g.w_post) a.need |= 1 << SUM_E_YH;
@@ -549,6 +543,7 @@ extern "C" ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan,
     b.parts = parts;
     b.groups = p.groups;
     b.n = at.n;
+    b.pad = a.pad;
     b.gate = a.gate;
     b.w_post = a.w_post;
     b.b_post = a.b_post;

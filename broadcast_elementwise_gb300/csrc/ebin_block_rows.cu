@@ -66,10 +66,15 @@ template <class E> static size_t unit_bytes(const RowsGeom &g, int vpt, bool vec
 #define EBIN_CAT(a, b) a##b
 #define EBIN_NAME(f, dt) EBIN_CAT(f, dt)
 
-// A CTA an SM takes a unit: rows of at most 8192 columns, and enough of them in a unit that
-// each team has some.
-static bool cta_takes(const BlockArgs &a, int chunks, int vpt) {
-    return chunks <= 32 && a.rows > 304 && a.cta.rows >= 2 * (16 / div_up(chunks, vpt));
+// Whether a CTA an SM takes a unit: rows of at most 8192 columns, and enough of them in a
+// unit.  Forward two for each team and two waves of a row a CTA at least (a step of few
+// rows spreads over more SMs a row a team); a gradient, whose units each leave sums, half
+// its teams' unless there is but one group.
+static bool cta_takes(const BlockArgs &a, int chunks, int vpt, bool grad) {
+    if (chunks > 32) return false;
+    const int64_t teams = kUnitWarps / div_up(chunks, vpt);
+    return grad ? a.groups == 1 || 2 * a.cta.rows >= teams
+                : a.rows > 304 && a.cta.rows >= 2 * teams;
 }
 
 // Its geometry, but for what lies in shared memory.
@@ -91,7 +96,7 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
     // Off the vectors the shifts pay for 16-bit rows of more than 2048 columns ([8191,4097]
     // bf16 116 us, a team a row 198; [20000,1543] f16 with dropout 151 and 136; [4095,2050] f32
     // 44 and 36).
-    if ((vec || (sizeof(S) == 2 && chunks > 8)) && cta_takes(a, chunks, kUnitVpt)) {
+    if ((vec || (sizeof(S) == 2 && chunks > 8)) && cta_takes(a, chunks, kUnitVpt, false)) {
         RowsGeom g = unit_geom(a, chunks, kUnitVpt);
         const bool scaled = a.branch_scale != 1.0f || a.drop.least;
         if (a.y && (a.gate || a.w_post || a.b_post || scaled)) g.tables |= TABLE_Y;
@@ -149,7 +154,7 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
     const int unit_vpt = !full ? kUnitGradVpt<false, false>
                        : post ? kUnitGradVpt<true, true> : kUnitGradVpt<true, false>;
     if (a.pre != EBIN_NORM_NONE && div_up(chunks, unit_vpt) <= kUnitWarps &&
-        cta_takes(a, chunks, unit_vpt)) {
+        cta_takes(a, chunks, unit_vpt, true)) {
         RowsGeom g = unit_geom(a, chunks, unit_vpt);
         const size_t tables = 2 * 16 * (size_t)g.table;
         const size_t row = 2 * unit_bytes<S>(g, unit_vpt, vec) +

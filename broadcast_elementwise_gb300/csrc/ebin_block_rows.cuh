@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
         v[2] = __fmul2_rn(v[2], make_float2(y.x, y.y));
         v[3] = __fmul2_rn(v[3], make_float2(y.z, y.w));
     };
-    float *const partial = a.partial ? a.partial + unit * 4 * a.n : nullptr;
+    float *const partial = a.partial ? a.partial + unit * 4 * a.pad : nullptr;
     float2 acc[GLOBAL ? 1 : kKinds][VPT][4];
     if constexpr (!GLOBAL) {
 #pragma unroll
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
         if constexpr (GLOBAL) {
             if (!partial) return;
             float2 s[4];
-            float *const at = partial + kind * a.n;
+            float *const at = partial + kind * a.pad;
             if (begun) l[i].load(at, s);
             else s[0] = s[1] = s[2] = s[3] = two(0.0f);
 #pragma unroll
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
             float2 s[4];
             if constexpr (GLOBAL) {
                 if (k == SUM_DZ_HH || k == SUM_DZ) continue;
-                l[i].load(partial + k * a.n, s);
+                l[i].load(partial + k * a.pad, s);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[j] = acc[place(k)][i][j];
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[j] = __fmul2_rn(s[j], two(branch));
             }
-            l[i].store(partial + k * a.n, s);
+            l[i].store(partial + k * a.pad, s);
         }
     }
 }

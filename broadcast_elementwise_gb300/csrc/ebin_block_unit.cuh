@@ -312,20 +312,13 @@ template <class T, class S, bool RAG> struct UnitLane {
         if constexpr (W == 4) *static_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         else *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
-    // binary32 sums of chunk i's columns, into a row of them
+    // binary32 sums of chunk i's columns, into a row of them that ends on a vector
     __device__ __forceinline__ void store_sums(int i, float *row, const float2 *v) const {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float *const p = row + col(i, q);
-            const float e[4] = {v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y};
-            if constexpr (RAG) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (col(i, q) + k < n) p[k] = e[k];
-            } else {
-                if (on(i, q)) *reinterpret_cast<float4 *>(p) = make_float4(e[0], e[1], e[2], e[3]);
-            }
-        }
+        for (int q = 0; q < 2; ++q)
+            if (col(i, q) < n)
+                *reinterpret_cast<float4 *>(row + col(i, q)) =
+                    make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
     }
 
     // ---- what is kept: element e of chunk i in bit e
@@ -952,7 +945,7 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
     for (int team = 0; team < g.teams; ++team) {
         __syncthreads();   // the rows have been read; the team before has added
         if (t.id != team) continue;
-        float *const partial = a.partial + unit * 4 * a.n;
+        float *const partial = a.partial + unit * 4 * a.pad;
 #pragma unroll
         for (int k = 0; k < kKinds; ++k)
 #pragma unroll
@@ -970,7 +963,7 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[k][i][j] = __fmul2_rn(acc[k][i][j], two(branch));
                 }
-                l.store_sums(i, partial + kind * a.n, acc[k][i]);
+                l.store_sums(i, partial + kind * a.pad, acc[k][i]);
             }
     }
 }
