@@ -1,6 +1,9 @@
 // Kernels of the norms around a block: norm of the block's output, gate, dropout,
 // scaled addition to the residual stream, norm of the stream and its modulation,
-// forward and gradient.
+// forward and gradient.  Bound by memory: forward x and y in, h and z out; a gradient dz,
+// dh, h and y in, dx and dy out, and the parameters' sums.  Three sets of kernels:
+// units of a CTA (ebin_block_unit.cuh), where nearly all rows go; a row a team
+// (ebin_block_rows.cuh); and those of any width, below.
 #pragma once
 
 #include "ebin_philox.cuh"
@@ -122,7 +125,8 @@ __device__ __forceinline__ float block_keep(const BlockArgs &a, float v, int64_t
 
 // A CTA walks rows, a thread every 256th column of each, with one pass over the
 // row for each sum (from the L1 and L2 after the first): any width, any stride, any
-// alignment.  A thread reads and writes the same columns in every pass, so an output
+// alignment, for rows of more than 32768 columns ([1000,40000] bf16 329 us, a seventh of
+// the copy's rate).  A thread reads and writes the same columns in every pass, so an output
 // may be an input.
 template <class T, class S>
 __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any(const BlockArgs a) {
@@ -161,8 +165,9 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any(const BlockArgs 
     }
 }
 
-// The gradient: a CTA takes a unit, rows of one group; its column sums stay in its
-// part of the workspace, each column its thread's own.
+// The gradient, for rows of more than 16384 columns: a CTA takes a unit, rows of one group;
+// its column sums stay in its part of the workspace, each column its thread's own, read
+// and written for every row ([1000,20000] bf16 2.1 ms).
 template <class T, class S>
 __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const BlockArgs a) {
     __shared__ float s[2 * (kBlockAnyThreads / 32)];

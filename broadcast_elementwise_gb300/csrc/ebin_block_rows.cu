@@ -202,11 +202,10 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
     const int64_t grid = div_up(g.units, g.teams);
     *parts = a.team.parts;
     if (vpt == 4)
-        return vec ? launch_rows<k_block_rows_grad<T, S, 4, true, true, true>>(a, g, grid, smem, s)
-                   : launch_rows<k_block_rows_grad<T, S, 4, false, true, true>>(a, g, grid, smem,
-                                                                               s);
-    return vec ? launch_rows<k_block_rows_grad<T, S, 2, true, true, false>>(a, g, grid, smem, s)
-               : launch_rows<k_block_rows_grad<T, S, 2, false, true, false>>(a, g, grid, smem, s);
+        return vec ? launch_rows<k_block_rows_grad<T, S, 4, true, true>>(a, g, grid, smem, s)
+                   : launch_rows<k_block_rows_grad<T, S, 4, false, true>>(a, g, grid, smem, s);
+    return vec ? launch_rows<k_block_rows_grad<T, S, 2, true, false>>(a, g, grid, smem, s)
+               : launch_rows<k_block_rows_grad<T, S, 2, false, false>>(a, g, grid, smem, s);
 }
 
 }  // namespace ebin

@@ -1,6 +1,9 @@
-// The norms around a block on rows of up to 32768 elements (a gradient's: 16384): a
-// team of warps takes a row, each lane eight columns of every chunk of 256 that its
-// warp owns, and a row's data is read from memory once.
+// The norms around a block, a row a team of warps: each lane owns eight columns of every
+// chunk of 256 that its warp owns, and a row's data is read from memory once.  The
+// path of what the kernels of CTAs' units (ebin_block_unit.cuh) leave: forward few rows,
+// small groups, 32-bit rows off the vectors and rows of 8193 to 32768 columns; a
+// gradient's small groups, gradients without a norm before the next block, and rows of
+// 8193 to 16384 columns.
 #pragma once
 
 #include "ebin_block.cuh"
@@ -143,29 +146,24 @@ template <class T, class S, bool VEC> struct RowsLane {
         else load(static_cast<const T *>(p), v);
     }
 
-    // keep bits of the lane's columns of a row, element e in bit e
+    // keep bits of the lane's columns of a row, element e in bit e (columns 32 apart): a lane
+    // draws two of the chunk's 64 quads; element e's lies with lane (8 e + lane / 4) % 32, in
+    // its first for e < 4
     __device__ __forceinline__ uint32_t kept(const DropArgs &d, uint32_t row, uint2 offset) const {
         auto bits = [&](uint32_t quad) {
             const uint4 w = drop_words(d, quad, row, offset);
             return (uint32_t)(w.x >= d.least) | (uint32_t)(w.y >= d.least) << 1 |
                    (uint32_t)(w.z >= d.least) << 2 | (uint32_t)(w.w >= d.least) << 3;
         };
-        if constexpr (VEC) {
-            return bits((uint32_t)quad(0) >> 2) | bits((uint32_t)quad(1) >> 2) << 4;
-        } else {
-            // a lane draws two of the chunk's 64 quads; element e's lies with lane
-            // (8 e + lane / 4) % 32, in its first for e < 4
-            const uint32_t mine = bits((uint32_t)(base >> 2) + lane) |
-                                  bits((uint32_t)(base >> 2) + 32 + lane) << 4;
-            uint32_t r = 0;
+        const uint32_t mine = bits((uint32_t)(base >> 2) + lane) |
+                              bits((uint32_t)(base >> 2) + 32 + lane) << 4;
+        uint32_t r = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t theirs =
-                    __shfl_sync(0xFFFFFFFFu, mine, (8 * e + (lane >> 2)) & 31);
-                r |= (theirs >> ((e & 4) + (lane & 3)) & 1) << e;
-            }
-            return r;
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t theirs = __shfl_sync(0xFFFFFFFFu, mine, (8 * e + (lane >> 2)) & 31);
+            r |= (theirs >> ((e & 4) + (lane & 3)) & 1) << e;
         }
+        return r;
     }
     // exactly 0 for what is dropped
     __device__ __forceinline__ void drop(const DropArgs &d, uint32_t row, uint2 offset,
@@ -192,11 +190,9 @@ template <class T, class S, bool VEC> struct RowsLane {
 
 // A team's exchange of partial sums through shared memory, [2][8][warps]: consecutive
 // exchanges take the halves in turn, so that one barrier each is enough.
-// NAMED: one of several teams of a CTA, each with a barrier of its own (1 .. 15: 0 is the
-// CTA's); else the CTA is the team, or its teams are single warps.
-template <bool NAMED> struct Team {
+// The CTA is the team, or its teams are single warps.
+struct Team {
     int lane, warp, warps, joins;
-    int id;             // among the CTA's teams
     float *s;           // 2 * 8 * kRowsMaxWarps floats
     int half;
     float count;        // live columns of the warp that this lane stands for in joins
@@ -208,7 +204,6 @@ template <bool NAMED> struct Team {
         lane = threadIdx.x & 31;
         const int team = (threadIdx.x >> 5) / g.warps;
         warp = (threadIdx.x >> 5) - team * g.warps;
-        id = team;
         sums += team * g.warps;   // a team's columns of the sums
         warps = g.warps;
         joins = g.joins;
@@ -236,10 +231,7 @@ template <bool NAMED> struct Team {
 #pragma unroll
         for (int k = 1; k < K; ++k) mine = lane == k ? v[k] : mine;
         if (lane < K) at[lane * kRowsMaxWarps + warp] = mine;
-        if constexpr (NAMED)   // teams of two warps and more: at most 8
-            asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
-        else
-            __syncthreads();
+        __syncthreads();
         const int from = lane & (joins - 1);
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] = from < warps ? at[k * kRowsMaxWarps + from] : 0.0f;
@@ -289,8 +281,8 @@ __device__ __forceinline__ float squares8(const L &l, const float2 *v, float mea
 }
 
 // LAYER: either norm may be a layer norm; else neither is.
-template <bool LAYER, class TEAM, class L, int VPT>
-__device__ __forceinline__ float2 row_moments(TEAM &t, const L (&l)[VPT], const float2 (&v)[VPT][4],
+template <bool LAYER, class L, int VPT>
+__device__ __forceinline__ float2 row_moments(Team &t, const L (&l)[VPT], const float2 (&v)[VPT][4],
                                               int norm, float eps) {
     const bool layer = LAYER && norm == EBIN_NORM_LAYER;
     float s[1] = {0.0f}, mean = 0.0f;
@@ -384,8 +376,8 @@ template <bool LAYER> __device__ __forceinline__ void norm8(float2 *v, float2 m)
     }
 }
 
-// A team, a row after another: few rows, rows off the vectors or past 8192 columns, and
-// groups of few rows.
+// A team, a row after another.  One chunk a lane to 8192 columns, so that a row spreads over
+// many warps ([16,4096] bf16 2.3 us in a graph); four past it ([2048,16384] 86 us).
 template <class T, class S, int VPT, bool VEC, bool LAYER>
 __global__ void __launch_bounds__(1024, 1)
 k_block_rows(const BlockArgs a, const RowsGeom g) {
@@ -395,8 +387,8 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
     __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
     extern __shared__ uint4 s_rows[];   // [slots][vectors of a thread][threads]
     constexpr int kX = VPT * PartS::N, kVectors = kX + VPT * PartT::N;
-    Team<false> t;
-    t.template start<VPT>(g, (int)a.n, s_sums);
+    Team t;
+    t.start<VPT>(g, (int)a.n, s_sums);
     Lane l[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -529,23 +521,22 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
 }
 
 // The gradient.  A team takes a unit, consecutive rows of one group, and keeps its
-// columns' sums for the parameters in registers to the unit's end (FULL: the four of
-// BlockSum, and layer norms; else SUM_DZ_HH and SUM_E_YH, and none).  A row costs two
+// columns' sums for the parameters in registers to the unit's end.  A row costs two
 // exchanges: the moments of h and y with the products of m and h, then, with a post
 // norm, those of u.  A column's factors (1 + scale) w_pre and branch_scale gate w_post
 // / (1 - p) lie in shared memory, each thread's its own.
 // GLOBAL: the sums of wide rows, which registers do not hold, are kept in the
-// unit's part of the workspace.
-template <class T, class S, int VPT, bool VEC, bool FULL, bool GLOBAL>
+// unit's part of the workspace ([2048,16384] bf16 with a layer norm 164 us; with norms on
+// both sides, whose rows and factors shared memory does not hold together, 559).
+template <class T, class S, int VPT, bool VEC, bool GLOBAL>
 __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, const RowsGeom g) {
     using Lane = RowsLane<T, S, VEC>;
     using PartS = RowsPart<Lane, S>;
     using PartT = RowsPart<Lane, T>;
-    constexpr int kKinds = FULL ? 4 : 2;
     __shared__ float s_sums[2 * 8 * kRowsMaxWarps];
     extern __shared__ uint4 s_rows[];   // the rows' slots, then the factors
-    Team<false> t;
-    t.template start<VPT>(g, (int)a.n, s_sums);
+    Team t;
+    t.start<VPT>(g, (int)a.n, s_sums);
     Lane l[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -560,8 +551,8 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
     uint4 *const mine = s_rows + threadIdx.x;
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine);
     const bool pre = a.pre != EBIN_NORM_NONE, post = a.post != EBIN_NORM_NONE;
-    const bool layer_h = FULL && a.pre == EBIN_NORM_LAYER;
-    const bool layer_y = FULL && a.post == EBIN_NORM_LAYER;
+    const bool layer_h = a.pre == EBIN_NORM_LAYER;
+    const bool layer_y = a.post == EBIN_NORM_LAYER;
     const float branch = a.branch_scale * (a.drop.least ? a.drop.scale : 1.0f);
     layer_pdl_launch();
     layer_pdl_wait();
@@ -649,17 +640,15 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
         v[3] = __fmul2_rn(v[3], make_float2(y.z, y.w));
     };
     float *const partial = a.partial ? a.partial + unit * 4 * a.pad : nullptr;
-    float2 acc[GLOBAL ? 1 : kKinds][VPT][4];
+    float2 acc[GLOBAL ? 1 : 4][VPT][4];
     if constexpr (!GLOBAL) {
 #pragma unroll
-        for (int k = 0; k < kKinds; ++k)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[k][i][j] = two(0.0f);
     }
-    // kind's place among those kept
-    auto place = [](int kind) { return FULL ? kind : kind >> 1; };
     bool begun = false;
     // sums of x y (y null: x) of chunk i
     auto add = [&](int kind, int i, const float2 *x, const float2 *y) {
@@ -674,7 +663,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
                 s[j] = y ? __ffma2_rn(x[j], y[j], s[j]) : __fadd2_rn(s[j], x[j]);
             l[i].store(at, s);
         } else {
-            float2 *const s = acc[place(kind)][i];
+            float2 *const s = acc[kind][i];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 s[j] = y ? __ffma2_rn(x[j], y[j], s[j]) : __fadd2_rn(s[j], x[j]);
@@ -702,8 +691,8 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
             else l[i].load(static_cast<const T *>(a.y) + row * a.ld_y, v);
         };
         // this warp's sums of the squares of h about their mean, of m with h less that
-        // mean, of the squares of y; FULL: of m, of h and of y
-        float w[FULL ? 6 : 3] = {};
+        // mean, of the squares of y, of m, of h and of y
+        float w[6] = {};
         float2 v[VPT][4];   // m, then D
         if (pre) {
             float mean = 0.0f;
@@ -716,7 +705,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
                     s[0] += l[i].within(h);
                 }
                 warp_sums(s);
-                w[FULL ? 4 : 0] = s[0];
+                w[4] = s[0];
                 mean = s[0] * t.inv_mine;
             }
 #pragma unroll
@@ -725,11 +714,9 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
                 open_dz(i, v[i]);
                 times(0, i, v[i]);
                 open_h(i, h);
-                if constexpr (FULL) {
-                    w[3] += l[i].within(v[i]);
+                w[3] += l[i].within(v[i]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = __fadd2_rn(h[j], two(-mean));
-                }
+                for (int j = 0; j < 4; ++j) h[j] = __fadd2_rn(h[j], two(-mean));
                 w[0] += squares8<false>(l[i], h, 0.0f);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) c[j] = __fmul2_rn(v[i][j], h[j]);
@@ -747,47 +734,37 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
                     s[0] += l[i].within(y);
                 }
                 warp_sums(s);
-                w[FULL ? 5 : 0] = s[0];
+                w[5] = s[0];
                 mean = s[0] * t.inv_mine;
             }
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 float2 y[4];
                 open_y(i, y);
-                w[2] += squares8<FULL>(l[i], y, mean);
+                w[2] += squares8<true>(l[i], y, mean);
             }
         }
         float2 mh = make_float2(0.0f, 1.0f), my = mh;
         float c0 = 0.0f, c1 = 0.0f;   // means of m and of m hh
         if (pre || post) {
-            if constexpr (FULL) {
-                float q[4] = {w[0], w[1], w[2], w[3]};
-                warp_sums(q);
+            float q[4] = {w[0], w[1], w[2], w[3]};
+            warp_sums(q);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = q[k];
-            } else {
-                warp_sums(w);
-            }
+            for (int k = 0; k < 4; ++k) w[k] = q[k];
             t.gather(w);
             if (pre) {
-                mh = t.moments(FULL ? w[FULL ? 4 : 0] : 0.0f, w[0], layer_h, a.eps_pre);
-                if constexpr (FULL) {
-                    // the products about the row's mean
-                    float c[2] = {w[3], w[1]};
-                    if (layer_h) c[1] = fmaf(w[3], fmaf(w[4], t.inv_count, -mh.x), c[1]);
-                    t.join(c);
-                    c0 = layer_h ? c[0] * t.inv_n : 0.0f;
-                    c1 = c[1] * mh.y * t.inv_n;
-                } else {
-                    float c[1] = {w[1]};
-                    t.join(c);
-                    c1 = c[0] * mh.y * t.inv_n;
-                }
+                mh = t.moments(w[4], w[0], layer_h, a.eps_pre);
+                // the products about the row's mean
+                float c[2] = {w[3], w[1]};
+                if (layer_h) c[1] = fmaf(w[3], fmaf(w[4], t.inv_count, -mh.x), c[1]);
+                t.join(c);
+                c0 = layer_h ? c[0] * t.inv_n : 0.0f;
+                c1 = c[1] * mh.y * t.inv_n;
             }
-            if (post) my = t.moments(FULL ? w[FULL ? 5 : 0] : 0.0f, w[2], layer_y, a.eps_post);
+            if (post) my = t.moments(w[5], w[2], layer_y, a.eps_post);
         }
         float2 u[VPT][4];
-        float b[2] = {0.0f, 0.0f};   // sums of u yh and (FULL) of u
+        float b[2] = {0.0f, 0.0f};   // sums of u yh and of u
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float2 d[4], yh[4];
@@ -796,16 +773,15 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
             if (pre) {
                 float2 h[4], dz[4];
                 open_h(i, h);
-                norm8<FULL>(h, mh);
+                norm8<true>(h, mh);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float2 m = v[i][j];
-                    if constexpr (FULL) m = __fadd2_rn(m, two(-c0));
+                    const float2 m = __fadd2_rn(v[i][j], two(-c0));
                     d[j] = __ffma2_rn(__ffma2_rn(h[j], two(-c1), m), two(mh.y), d[j]);
                 }
                 open_dz(i, dz);
                 add(SUM_DZ_HH, i, dz, h);
-                if constexpr (FULL) add(SUM_DZ, i, dz, nullptr);
+                add(SUM_DZ, i, dz, nullptr);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[i][j] = u[i][j] = d[j];
@@ -813,30 +789,22 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
             if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, u[i]);
             if (a.y) {
                 open_y(i, yh);
-                if (post) norm8<FULL>(yh, my);
+                if (post) norm8<true>(yh, my);
                 add(SUM_E_YH, i, u[i], yh);
             }
-            if constexpr (FULL) add(SUM_E, i, u[i], nullptr);
+            add(SUM_E, i, u[i], nullptr);
             times(1, i, u[i]);
             if (post) {
-                if constexpr (FULL) b[1] += l[i].within(u[i]);
+                b[1] += l[i].within(u[i]);
                 mul8(yh, u[i]);
                 b[0] += l[i].within(yh);
             }
         }
         begun = true;
         if (post) {
-            if constexpr (FULL) {
-                warp_sums(b);
-                t.gather(b);
-                t.join(b);
-            } else {
-                float one[1] = {b[0]};
-                warp_sums(one);
-                t.gather(one);
-                t.join(one);
-                b[0] = one[0];
-            }
+            warp_sums(b);
+            t.gather(b);
+            t.join(b);
             b[0] *= t.inv_n;
             b[1] = layer_y ? b[1] * t.inv_n : 0.0f;
         }
@@ -846,10 +814,10 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
                 if (post) {
                     float2 yh[4];
                     open_y(i, yh);
-                    norm8<FULL>(yh, my);
+                    norm8<true>(yh, my);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if constexpr (FULL) u[i][j] = __fadd2_rn(u[i][j], two(-b[1]));
+                        u[i][j] = __fadd2_rn(u[i][j], two(-b[1]));
                         u[i][j] = __fmul2_rn(__ffma2_rn(yh[j], two(-b[0]), u[i][j]), two(my.y));
                     }
                 }
@@ -867,7 +835,6 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
     // the sums of e carry its factor from here on
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        if (!FULL && (k == SUM_DZ || k == SUM_E)) continue;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float2 s[4];
@@ -876,7 +843,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
                 l[i].load(partial + k * a.pad, s);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] = acc[place(k)][i][j];
+                for (int j = 0; j < 4; ++j) s[j] = acc[k][i][j];
             }
             if (k == SUM_E_YH || k == SUM_E) {
 #pragma unroll

@@ -9,6 +9,9 @@
 //   norm and rotation   [2,4096] tokens    29.4 us   5780 GB/s   k_heads_ring
 //   its gradient        [2,4096] tokens    46.1 us   5500 GB/s   k_heads_vec_grad
 // With 62 of the 128 rotated (HEADS_ODD), [2,4096] tokens: 47.6, 70.0 and 82.0 us.
+// Several axes (copy: 6756 GB/s), bf16, heads of 128:
+//   norm and rotation, interleaved, [32760] tokens of 80 heads   231 us 5810 GB/s  k_heads_ring
+//   its gradient, half layout, [2,4095] tokens of 40 heads        50 us 5050 GB/s  k_heads_vec_grad
 // Arithmetic is binary32 throughout, with one rounding to the element type at
 // the store.
 #pragma once
@@ -82,6 +85,10 @@ struct HeadsOne {
 
 constexpr int kHeadsMaxAxes = 4;
 
+// Angles gathered from several rows cost more, so that eight heads share them where one
+// position's are shared by four ([32760,80,128] interleaved 311 -> 289 us; with sixteen 297,
+// and [8190,40,128]'s gradient 50 -> 62); more rows ahead take room from the L1, where the
+// table's rows lie (four 289, six 298, eight 332).
 struct HeadsAxes {
     static constexpr bool kSeveral = true;
     static constexpr int kRingHeads = 8, kAhead = 4;
