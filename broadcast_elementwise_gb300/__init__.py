@@ -24,6 +24,13 @@ What a transformer layer needs around its attention::
     qkv = eb.gemm(x, w, bias, trans_b=True)      # x [rows, k], w [n, k]
     q, k, v = qkv.view(batch, tokens, -1, 128).split([32, 8, 8], dim=2)
     eb.qk_norm_rotary(q, k, wq, wk, cos, sin, positions, out=(q, k))
+
+Between two blocks, conditioned (gate, scale, shift [batch, n]), y a block's output::
+
+    h, z = eb.block_norm(x, y, gate=gate, scale=scale, shift=shift, pre="layer",
+                         dropout=0.1, seed=seed, offset=step)
+    grads = eb.block_norm_grad(dz, dh, h, y, gate=gate, scale=scale, shift=shift, pre="layer",
+                               dropout=0.1, seed=seed, offset=step)
 """
 from __future__ import annotations
 
