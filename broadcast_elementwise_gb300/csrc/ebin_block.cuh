@@ -114,13 +114,17 @@ __device__ __forceinline__ float2 row_moments(const F &value, int64_t n, int nor
     return make_float2(mean, rsqrtf(v[0] / (float)n + eps));
 }
 
-template <class T>
+__device__ __forceinline__ bool block_kept(const BlockArgs &a, int64_t row, int64_t j,
+                                           uint2 offset) {
+    if (!a.drop.least) return true;
+    const uint4 w = drop_words(a.drop, (uint32_t)(j >> 2), (uint32_t)row, offset);
+    const uint32_t word = (j & 2) ? ((j & 1) ? w.w : w.z) : ((j & 1) ? w.y : w.x);
+    return word >= a.drop.least;
+}
 __device__ __forceinline__ float block_keep(const BlockArgs &a, float v, int64_t row, int64_t j,
                                             uint2 offset) {
     if (!a.drop.least) return v;
-    const uint4 w = drop_words(a.drop, (uint32_t)(j >> 2), (uint32_t)row, offset);
-    const uint32_t word = (j & 2) ? ((j & 1) ? w.w : w.z) : ((j & 1) ? w.y : w.x);
-    return word >= a.drop.least ? v * a.drop.scale : 0.0f;
+    return block_kept(a, row, j, offset) ? v * a.drop.scale : 0.0f;
 }
 
 // A CTA walks rows, a thread every 256th column of each, with one pass over the
@@ -148,7 +152,7 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any(const BlockArgs 
             float v = (to_f(y[j]) - my.x) * my.y;
             v = fmaf(v, block_param<T>(a.w_post, j, a.w_f32, 1.0f),
                      block_param<T>(a.b_post, j, a.w_f32, 0.0f));
-            v = block_keep<T>(a, v, row, j, offset);
+            v = block_keep(a, v, row, j, offset);
             return fmaf(a.branch_scale * block_param<T>(gate, j, a.mod_f32, 1.0f), v, t);
         };
         const float2 mh = row_moments(stream, a.n, a.pre, a.eps_pre, s);
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
             return fmaf(mh.y, into(j) - c[0] - normed(j) * c[1], d);
         };
         auto branch = [&](int64_t j, float d) {   // e
-            return block_keep<T>(a, a.branch_scale * d, row, j, offset);
+            return block_keep(a, a.branch_scale * d, row, j, offset);
         };
         const float2 my = row_moments([&](int64_t j) { return to_f(y[j]); }, a.n, a.post,
                                       a.eps_post, s);
@@ -242,7 +246,8 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
                     sums[SUM_DZ_HH * a.pad + j] += g * normed(j);
                     sums[SUM_DZ * a.pad + j] += g;
                 }
-                sums[SUM_E_YH * a.pad + j] += e * yh;
+                // what is dropped adds nothing, whatever y is there
+                if (block_kept(a, row, j, offset)) sums[SUM_E_YH * a.pad + j] += e * yh;
                 sums[SUM_E * a.pad + j] += e;
             }
             float u = e * weigh(j);

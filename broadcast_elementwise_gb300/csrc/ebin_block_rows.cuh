@@ -32,6 +32,18 @@ struct RowsGeom {
 
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 
+// Four q of eight columns by a quad's words: exactly 0 for what is dropped, in each row.
+template <class... V>
+__device__ __forceinline__ void drop_four(uint4 w, uint32_t least, int q, V *...rows) {
+    auto one = [&](float2 *v) {
+        v[2 * q].x = w.x >= least ? v[2 * q].x : 0.0f;
+        v[2 * q].y = w.y >= least ? v[2 * q].y : 0.0f;
+        v[2 * q + 1].x = w.z >= least ? v[2 * q + 1].x : 0.0f;
+        v[2 * q + 1].y = w.w >= least ? v[2 * q + 1].y : 0.0f;
+    };
+    (one(rows), ...);
+}
+
 // Which columns a lane owns, and how it reaches them.  With vectors: eight
 // neighbours (16-bit rows), or two fours 128 columns apart (a 32-bit type takes
 // part: 16 bytes a lane and access either way); else eight columns 32 apart.
@@ -165,25 +177,24 @@ template <class T, class S, bool VEC> struct RowsLane {
         }
         return r;
     }
-    // exactly 0 for what is dropped
+    // exactly 0 for what is dropped, in each of the rows
+    template <class... V>
     __device__ __forceinline__ void drop(const DropArgs &d, uint32_t row, uint2 offset,
-                                         float2 *v) const {
+                                         V *...rows) const {
         if constexpr (VEC) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint4 w = drop_words(d, (uint32_t)quad(q) >> 2, row, offset);
-                v[2 * q].x = w.x >= d.least ? v[2 * q].x : 0.0f;
-                v[2 * q].y = w.y >= d.least ? v[2 * q].y : 0.0f;
-                v[2 * q + 1].x = w.z >= d.least ? v[2 * q + 1].x : 0.0f;
-                v[2 * q + 1].y = w.w >= d.least ? v[2 * q + 1].y : 0.0f;
-            }
+            for (int q = 0; q < 2; ++q)
+                drop_four(drop_words(d, (uint32_t)quad(q) >> 2, row, offset), d.least, q, rows...);
         } else {
             const uint32_t bits = kept(d, row, offset);
+            (drop_bits(bits, rows), ...);
+        }
+    }
+    __device__ __forceinline__ static void drop_bits(uint32_t bits, float2 *v) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[k].x = bits >> (2 * k) & 1 ? v[k].x : 0.0f;
-                v[k].y = bits >> (2 * k + 1) & 1 ? v[k].y : 0.0f;
-            }
+        for (int k = 0; k < 4; ++k) {
+            v[k].x = bits >> (2 * k) & 1 ? v[k].x : 0.0f;
+            v[k].y = bits >> (2 * k + 1) & 1 ? v[k].y : 0.0f;
         }
     }
 };
@@ -785,13 +796,15 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[i][j] = u[i][j] = d[j];
-            // e / branch, then u
-            if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, u[i]);
             if (a.y) {
                 open_y(i, yh);
                 if (post) norm8<true>(yh, my);
-                add(SUM_E_YH, i, u[i], yh);
+            } else {
+                yh[0] = yh[1] = yh[2] = yh[3] = two(0.0f);
             }
+            // e / branch, then u; what is dropped adds nothing, whatever y is there
+            if (a.drop.least) l[i].drop(a.drop, (uint32_t)row, offset, u[i], yh);
+            if (a.y) add(SUM_E_YH, i, u[i], yh);
             add(SUM_E, i, u[i], nullptr);
             times(1, i, u[i]);
             if (post) {

@@ -341,16 +341,12 @@ template <class T, class S, bool RAG> struct UnitLane {
         }
         return r;
     }
+    template <class... V>
     __device__ __forceinline__ void drop(int i, const DropArgs &d, uint32_t row, uint2 offset,
-                                         float2 *v) const {
+                                         V *...rows) const {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint4 w = drop_words(d, (uint32_t)col(i, q) >> 2, row, offset);
-            v[2 * q].x = w.x >= d.least ? v[2 * q].x : 0.0f;
-            v[2 * q].y = w.y >= d.least ? v[2 * q].y : 0.0f;
-            v[2 * q + 1].x = w.z >= d.least ? v[2 * q + 1].x : 0.0f;
-            v[2 * q + 1].y = w.w >= d.least ? v[2 * q + 1].y : 0.0f;
-        }
+        for (int q = 0; q < 2; ++q)
+            drop_four(drop_words(d, (uint32_t)col(i, q) >> 2, row, offset), d.least, q, rows...);
     }
 };
 
@@ -843,7 +839,8 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
                     q[1] = __ffma2_rn(m, x, q[1]);
                     if constexpr (POST) {
                         float2 yy = y.pair(j);
-                        const float2 dh = d.pair(j);
+                        float2 dh = d.pair(j);
+                        if (a.drop.least) dh = mask2(dh, bits[i], j);   // 0 times it may be NaN
                         if constexpr (FULL) yy = l.live(i, j, __fadd2_rn(yy, two(-my.x)));
                         q[2] = __ffma2_rn(yy, yy, q[2]);
                         const float2 tt = __fmul2_rn(yy, f[j]);
@@ -912,23 +909,28 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
                 }
                 if (a.h) l.store(i, dx, out);
             }
+            float2 x8[4];   // y
+            if (POST || a.y) {
+                WordsT y;
+                read_y(i, y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x8[j] = y.pair(j);
+            }
             if (a.drop.least) {
                 if constexpr (POST) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = mask2(v[j], bits[i], j);
-                } else {
-                    l.drop(i, a.drop, (uint32_t)row, offset, v);
+                } else {   // what is dropped adds nothing to the gate's, whatever y is there
+                    l.drop(i, a.drop, (uint32_t)row, offset, v, x8);
                 }
             }
             if constexpr (FULL && POST) add8(acc[kKinds - 1][i], v);
             float2 f[4];
             factor(by_y, i, f);
             if (POST || a.y) {
-                WordsT y;
-                read_y(i, y);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float2 x = y.pair(j);
+                    float2 x = x8[j];
                     if constexpr (POST) {
                         if constexpr (FULL) x = __fadd2_rn(x, two(-my.x));
                         x = __fmul2_rn(x, ry);

@@ -945,7 +945,8 @@ ebin_status ebin_dropout_grad_execute(ebin_dropout_plan_t plan, const void *dy, 
  *     NONE    N(t) = t
  *     RMS     N(t) = t / sqrt(mean(t^2) + epsilon)
  *     LAYER   N(t) = (t - mean(t)) / sqrt(mean((t - mean(t))^2) + epsilon)
- * over a row.  No counterpart in the pages.
+ * over a row.  What is dropped adds exactly 0 to h and to every gradient but x's,
+ * whatever dh, and without N_post y, hold there.  No counterpart in the pages.
  *
  * gate, scale and shift are one row for all rows, or one for each group of
  * consecutive rows (the condition of a sequence of a batch).  Weights, biases,

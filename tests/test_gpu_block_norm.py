@@ -302,6 +302,32 @@ def test_bad_rows_stay_alone(n):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows,groups", [(9, 0), (9, 9), (700, 0)])
+@pytest.mark.parametrize("n", [512, 1543, 9000, 16400])
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+def test_dropped_places_add_nothing_to_gradients(post, n, rows, groups):
+    """Infinities and NaN of dh, and without a norm after the block of y, in dropped places: the
+    gradients of y and of every parameter are those of finite numbers there."""
+    t, p = operands(rows, n, BF16, F32, groups)
+    p = valid(p, post, "rms")
+    gone = keep_of(0.5, rows, n) == 0
+    dz, dh = matrix(61, rows, n, BF16), normal(62, rows, n)
+    h, y = t["x"], t["y"].contiguous()
+    kw = dict(post=post, pre="rms", dropout=0.5, seed=SEED, offset=OFFSET, **p)
+    want = eb.block_norm_grad(dz, torch.where(gone, 0.0, dh), h,
+                              torch.where(gone, 0.0, y) if post == "none" else y, **kw)
+    assert all(v.isfinite().all() for v in want.values() if v is not None)
+    for bad in (float("inf"), float("nan")):
+        got = eb.block_norm_grad(dz, torch.where(gone, bad, dh), h,
+                                 torch.where(gone, bad, y) if post == "none" else y, **kw)
+        for name, value in want.items():
+            if name == "x":
+                assert torch.equal(got[name][~gone], value[~gone])
+                assert not got[name][gone].isfinite().any()
+            elif value is not None:
+                assert torch.equal(got[name], value), name
+
+
 @pytest.mark.parametrize("n", [1024, 1021, 20000])
 def test_in_place(n):
     t, p = operands(21, n, BF16, BF16, 3)
