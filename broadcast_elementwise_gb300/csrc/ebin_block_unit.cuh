@@ -10,7 +10,7 @@
 // rows a team there.  bf16, against a copy's 6756 GB/s:
 //   [8192,4096] norms on both sides   forward 49.0 us 5480 GB/s, gradient 69.1 us 5830
 //   [16380,1536] f32 stream, gate, scale, shift   forward 52.2 us 5790 GB/s
-//   [16388,1152] the same with dropout, gradient 63.7 us 3560 GB/s: Philox's rounds
+//   [16388,1152] the same with dropout, gradient 66.6 us 3400 GB/s: Philox's rounds
 //
 // RAGGED: rows that do not start and end on vectors.  A row's copies begin on the
 // vector that holds its first element; a lane takes its columns from two neighbouring
@@ -204,6 +204,16 @@ template <class T, class S, bool RAG> struct UnitLane {
                 return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
             else
                 return open2<E>(w[j]);
+        }
+        // pair j: 0 where its bits of a chunk's are
+        __device__ __forceinline__ void mask(int j, uint32_t bits) {
+            if constexpr (sizeof(E) == 4) {
+                if (!(bits >> (2 * j) & 1)) w[2 * j] = 0;
+                if (!(bits >> (2 * j + 1) & 1)) w[2 * j + 1] = 0;
+            } else {
+                w[j] &= (bits >> (2 * j) & 1 ? 0xFFFFu : 0u) |
+                        (bits >> (2 * j + 1) & 1 ? 0xFFFF0000u : 0u);
+            }
         }
     };
     // s: past() of the row in memory
@@ -828,7 +838,10 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
                     factor(by_y, i, f);
                     if (a.drop.least)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) f[j] = mask2(f[j], bits[i], j);
+                        for (int j = 0; j < 4; ++j) {
+                            f[j] = mask2(f[j], bits[i], j);
+                            d.mask(j, bits[i]);   // 0 times it may be NaN
+                        }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -839,8 +852,7 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
                     q[1] = __ffma2_rn(m, x, q[1]);
                     if constexpr (POST) {
                         float2 yy = y.pair(j);
-                        float2 dh = d.pair(j);
-                        if (a.drop.least) dh = mask2(dh, bits[i], j);   // 0 times it may be NaN
+                        const float2 dh = d.pair(j);
                         if constexpr (FULL) yy = l.live(i, j, __fadd2_rn(yy, two(-my.x)));
                         q[2] = __ffma2_rn(yy, yy, q[2]);
                         const float2 tt = __fmul2_rn(yy, f[j]);
@@ -909,28 +921,23 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
                 }
                 if (a.h) l.store(i, dx, out);
             }
-            float2 x8[4];   // y
-            if (POST || a.y) {
-                WordsT y;
-                read_y(i, y);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x8[j] = y.pair(j);
-            }
             if (a.drop.least) {
-                if constexpr (POST) {
+                if constexpr (!POST) bits[i] = l.kept(i, a.drop, (uint32_t)row, offset);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = mask2(v[j], bits[i], j);
-                } else {   // what is dropped adds nothing to the gate's, whatever y is there
-                    l.drop(i, a.drop, (uint32_t)row, offset, v, x8);
-                }
+                for (int j = 0; j < 4; ++j) v[j] = mask2(v[j], bits[i], j);
             }
             if constexpr (FULL && POST) add8(acc[kKinds - 1][i], v);
             float2 f[4];
             factor(by_y, i, f);
             if (POST || a.y) {
+                WordsT y;
+                read_y(i, y);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float2 x = x8[j];
+                    float2 x = y.pair(j);
+                    // What is dropped adds nothing to the gate's, whatever y is there.  Its bits
+                    // hold fewer registers than y over Philox's rounds (66.6 us, and 70.7).
+                    if (!POST && a.drop.least) x = mask2(x, bits[i], j);
                     if constexpr (POST) {
                         if constexpr (FULL) x = __fadd2_rn(x, two(-my.x));
                         x = __fmul2_rn(x, ry);
