@@ -303,7 +303,7 @@ BlockUnits block_units(int64_t group_rows, int64_t parts) {
 // unit costing its teams' steps and what three more would (its tables, its sums).  Of a
 // gradient's the least within a thirtieth of the best: SMs left over are where the last
 // sums begin ([8192,4096] bf16: 147 units 69.2 us, 152 units 71.6); but a step more of few
-// costs more than that gives ([16388,1152] in four groups: 148 units 66.1, 152 units 63.7).
+// costs more than that gives ([16388,1152] in four groups: 144 units 69.2, 152 units 66.6).
 BlockUnits cta_units(int64_t groups, int64_t group_rows, int64_t n, int vpt, bool gradient) {
     const int64_t warps = std::max<int64_t>(1, div_up(div_up(n, 256), vpt));
     const int64_t teams = std::max<int64_t>(1, kUnitWarps / warps);
