@@ -188,15 +188,19 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
     const size_t factors = (size_t)threads * 16 * g.factors;
     size_t smem = factors;
     if (vec) {
-        for (int k = 0; k < 4; ++k) {
-            g.at[k] = g.vectors;
-            if (there[k]) g.vectors += vpt * (k % 2 ? t_vectors : s_vectors);
+        // As much of a row as fits beside the factors, what is read most often first: all of it
+        // but for the widest ([2048,16384] bf16 with norms on both sides: h and dz, 196 us; without
+        // shared memory, element by element, 560).
+        const int order[4] = {0, 1, 3, 2};
+        for (int k : order) {
+            const int more = vpt * (k % 2 ? t_vectors : s_vectors);
+            const bool fits = (size_t)(g.vectors + more) * 16 * threads + factors <= kRowsSmem;
+            g.at[k] = there[k] && fits ? g.vectors : -1;
+            if (g.at[k] >= 0) g.vectors += more;
         }
         const size_t row = (size_t)g.vectors * 16 * threads;
-        if (row > 0) {
+        if (row > 0)
             g.slots = rows_slots(row, factors, std::min(std::max(1, 512 / threads), 16));
-            vec = g.slots > 0;   // rows too wide for shared memory are read where they lie
-        }
         smem += g.slots * row;
     }
     const int64_t grid = div_up(g.units, g.teams);

@@ -19,8 +19,8 @@ struct RowsGeom {
     int32_t teams;     // of a CTA: 1, or one for each warp
     int32_t slots;     // rows in shared memory: the one worked on and those on their way
     FastDiv gate, mod; // rows that share a row of gate, of scale and shift
-    // a gradient's: where h, dz, dh and y lie among a thread's vectors, how many these
-    // are, and the vectors of its factors (-1: all 1)
+    // a gradient's: where h, dz, dh and y lie among a thread's vectors (-1: read where they
+    // lie in memory), how many these are, and the vectors of its factors (-1: all 1)
     int32_t at[4], vectors;
     int32_t factor[2], factors;
     int64_t units;
@@ -537,8 +537,8 @@ k_block_rows(const BlockArgs a, const RowsGeom g) {
 // norm, those of u.  A column's factors (1 + scale) w_pre and branch_scale gate w_post
 // / (1 - p) lie in shared memory, each thread's its own.
 // GLOBAL: the sums of wide rows, which registers do not hold, are kept in the
-// unit's part of the workspace ([2048,16384] bf16 with a layer norm 164 us; with norms on
-// both sides, whose rows and factors shared memory does not hold together, 559).
+// unit's part of the workspace, those that are wanted ([2048,16384] bf16 with norms on both
+// sides 196 us, all four kinds 253; a layer norm with dropout 181 and 209).
 template <class T, class S, int VPT, bool VEC, bool GLOBAL>
 __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, const RowsGeom g) {
     using Lane = RowsLane<T, S, VEC>;
@@ -570,30 +570,32 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
     const uint2 offset = drop_offset(a.drop);
     const int ahead = g.slots - 1;
     int fill = 0, slot = 0, next = r0;
+    // whether an input's rows go through shared memory (of 8192 columns all that are there)
+    auto held = [&](int k, const void *p) { return GLOBAL ? g.at[k] >= 0 : p != nullptr; };
     auto fetch = [&]() {
         if constexpr (VEC) {
             if (next < r1) {
                 const uint32_t at = to + fill * g.vectors * threads * 16;
                 const uint32_t s_step = PartS::N * threads * 16, t_step = PartT::N * threads * 16;
-                if (a.x) {
+                if (held(0, a.x)) {
                     const S *const p = static_cast<const S *>(a.x) + next * a.ld_x;
 #pragma unroll
                     for (int i = 0; i < VPT; ++i)
                         PartS::fetch(l[i], at + g.at[0] * threads * 16 + i * s_step, threads, p);
                 }
-                if (a.dz) {
+                if (held(1, a.dz)) {
                     const T *const p = static_cast<const T *>(a.dz) + next * a.ld_dz;
 #pragma unroll
                     for (int i = 0; i < VPT; ++i)
                         PartT::fetch(l[i], at + g.at[1] * threads * 16 + i * t_step, threads, p);
                 }
-                if (a.dh) {
+                if (held(2, a.dh)) {
                     const S *const p = static_cast<const S *>(a.dh) + next * a.ld_dh;
 #pragma unroll
                     for (int i = 0; i < VPT; ++i)
                         PartS::fetch(l[i], at + g.at[2] * threads * 16 + i * s_step, threads, p);
                 }
-                if (a.y) {
+                if (held(3, a.y)) {
                     const T *const p = static_cast<const T *>(a.y) + next * a.ld_y;
 #pragma unroll
                     for (int i = 0; i < VPT; ++i)
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
     // sums of x y (y null: x) of chunk i
     auto add = [&](int kind, int i, const float2 *x, const float2 *y) {
         if constexpr (GLOBAL) {
-            if (!partial) return;
+            if (!partial || !(a.need >> kind & 1)) return;
             float2 s[4];
             float *const at = partial + kind * a.pad;
             if (begun) l[i].load(at, s);
@@ -686,19 +688,23 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
         const uint4 *const at = mine + slot * g.vectors * threads;
         slot = slot + 1 == g.slots ? 0 : slot + 1;
         auto open_h = [&](int i, float2 *v) {
-            if constexpr (VEC) PartS::open(at + (g.at[0] + i * PartS::N) * threads, threads, v);
+            if (VEC && held(0, a.x))
+                PartS::open(at + (g.at[0] + i * PartS::N) * threads, threads, v);
             else l[i].load(static_cast<const S *>(a.x) + row * a.ld_x, v);
         };
         auto open_dz = [&](int i, float2 *v) {
-            if constexpr (VEC) PartT::open(at + (g.at[1] + i * PartT::N) * threads, threads, v);
+            if (VEC && held(1, a.dz))
+                PartT::open(at + (g.at[1] + i * PartT::N) * threads, threads, v);
             else l[i].load(static_cast<const T *>(a.dz) + row * a.ld_dz, v);
         };
         auto open_dh = [&](int i, float2 *v) {
-            if constexpr (VEC) PartS::open(at + (g.at[2] + i * PartS::N) * threads, threads, v);
+            if (VEC && held(2, a.dh))
+                PartS::open(at + (g.at[2] + i * PartS::N) * threads, threads, v);
             else l[i].load(static_cast<const S *>(a.dh) + row * a.ld_dh, v);
         };
         auto open_y = [&](int i, float2 *v) {
-            if constexpr (VEC) PartT::open(at + (g.at[3] + i * PartT::N) * threads, threads, v);
+            if (VEC && held(3, a.y))
+                PartT::open(at + (g.at[3] + i * PartT::N) * threads, threads, v);
             else l[i].load(static_cast<const T *>(a.y) + row * a.ld_y, v);
         };
         // this warp's sums of the squares of h about their mean, of m with h less that
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(512, 1) k_block_rows_grad(const BlockArgs a, c
         for (int i = 0; i < VPT; ++i) {
             float2 s[4];
             if constexpr (GLOBAL) {
-                if (k == SUM_DZ_HH || k == SUM_DZ) continue;
+                if (k == SUM_DZ_HH || k == SUM_DZ || !(a.need >> k & 1)) continue;
                 l[i].load(partial + k * a.pad, s);
             } else {
 #pragma unroll

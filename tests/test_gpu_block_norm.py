@@ -328,7 +328,7 @@ def test_dropped_places_add_nothing_to_gradients(post, n, rows, groups):
                 assert torch.equal(got[name], value), name
 
 
-@pytest.mark.parametrize("n", [1024, 1021, 20000])
+@pytest.mark.parametrize("n", [1024, 1021, 16384, 20000])
 def test_in_place(n):
     t, p = operands(21, n, BF16, BF16, 3)
     kw = dict(post="rms", pre="layer", **p)
