@@ -73,7 +73,7 @@ __device__ __forceinline__ const void *block_row(const void *p, int64_t index, i
 
 // ------------------------------------------------------------------ any width
 
-constexpr int kBlockAnyThreads = 256;
+constexpr int kBlockAnyThreads = 1024;
 
 // The sum over the CTA of each v; every thread gets it.
 template <int K> __device__ __forceinline__ void cta_sums(float (&v)[K], float *s) {
@@ -127,10 +127,10 @@ __device__ __forceinline__ float block_keep(const BlockArgs &a, float v, int64_t
     return block_kept(a, row, j, offset) ? v * a.drop.scale : 0.0f;
 }
 
-// A CTA walks rows, a thread every 256th column of each, with one pass over the
+// A CTA walks rows, a thread every 1024th column of each, with one pass over the
 // row for each sum (from the L1 and L2 after the first): any width, any stride, any
-// alignment, for rows of more than 32768 columns ([1000,40000] bf16 329 us, a seventh of
-// the copy's rate).  A thread reads and writes the same columns in every pass, so an output
+// alignment, for rows of more than 32768 columns ([1000,40000] bf16 278 us, a sixth of
+// the copy's rate; 256 threads 329).  A thread reads and writes the same columns in every pass, so an output
 // may be an input.
 template <class T, class S>
 __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any(const BlockArgs a) {
@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any(const BlockArgs 
 
 // The gradient, for rows of more than 16384 columns: a CTA takes a unit, rows of one group;
 // its column sums stay in its part of the workspace, each column its thread's own, read
-// and written for every row ([1000,20000] bf16 2.1 ms).
+// and written for every row ([1000,20000] bf16 0.51 ms, with 256
+// threads and all four kinds 2.1).
 template <class T, class S>
 __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const BlockArgs a) {
     __shared__ float s[2 * (kBlockAnyThreads / 32)];
@@ -185,7 +186,8 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
     if (sums)
         for (int64_t j = threadIdx.x; j < a.n; j += kBlockAnyThreads)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sums[k * a.pad + j] = 0.0f;
+            for (int k = 0; k < 4; ++k)
+                if (a.need >> k & 1) sums[k * a.pad + j] = 0.0f;
     const float inv = 1.0f / (float)a.n;
     for (int64_t row = r0; row < r1; ++row) {
         const S *h = static_cast<const S *>(a.x) + (a.x ? row * a.ld_x : 0);
@@ -243,12 +245,13 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const Block
             if (sums) {
                 if (a.dz) {
                     const float g = to_f(dz[j]);
-                    sums[SUM_DZ_HH * a.pad + j] += g * normed(j);
-                    sums[SUM_DZ * a.pad + j] += g;
+                    if (a.need >> SUM_DZ_HH & 1) sums[SUM_DZ_HH * a.pad + j] += g * normed(j);
+                    if (a.need >> SUM_DZ & 1) sums[SUM_DZ * a.pad + j] += g;
                 }
                 // what is dropped adds nothing, whatever y is there
-                if (block_kept(a, row, j, offset)) sums[SUM_E_YH * a.pad + j] += e * yh;
-                sums[SUM_E * a.pad + j] += e;
+                if (a.need >> SUM_E_YH & 1 && block_kept(a, row, j, offset))
+                    sums[SUM_E_YH * a.pad + j] += e * yh;
+                if (a.need >> SUM_E & 1) sums[SUM_E * a.pad + j] += e;
             }
             float u = e * weigh(j);
             if (a.post != EBIN_NORM_NONE) u = my.y * (u - b[0] - yh * b[1]);
