@@ -326,6 +326,13 @@ __device__ __forceinline__ void rows_copy16(uint32_t to, const void *from) {
 __device__ __forceinline__ void rows_copy8(uint32_t to, const void *from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
 }
+// One element of SIZE bytes, at once.
+template <int SIZE> __device__ __forceinline__ void rows_move(uint32_t to, const char *from) {
+    if constexpr (SIZE == 4)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(*reinterpret_cast<const uint32_t *>(from)) : "memory");
+    else
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const uint16_t *>(from)) : "memory");
+}
 __device__ __forceinline__ void rows_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // until at most `left` of the newest groups are under way
 __device__ __forceinline__ void rows_wait(int left) {

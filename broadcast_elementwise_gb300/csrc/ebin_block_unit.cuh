@@ -16,9 +16,12 @@
 // vector that holds its first element; a lane takes its columns from two neighbouring
 // vectors and shifts them into place, and an output's vectors are made of two
 // neighbouring lanes' words.  Shifts and the ends of stores about double the instructions:
-// [8191,4097] bf16 116 us and 216, element by element 198 and 803.
+// [8191,4097] bf16 122 us and 237, element by element 198 and 803.  Of a tensor's first and last
+// rows the vectors that pass its ends are copied by elements: nothing outside is read
+// ([8185,4096], rows 4097 apart, bf16 100 us and 155, whole vectors everywhere 96 and 148).
 #pragma once
 
+#include "ebin_block_copy.h"
 #include "ebin_block_rows.cuh"
 
 namespace ebin {
@@ -162,23 +165,39 @@ template <class T, class S, bool RAG> struct UnitLane {
         if constexpr (bytes<E>() == 16) rows_copy16(to, from);
         else rows_copy8(to, from);
     }
-    // to: this lane's place in shared memory; row: at this lane's first column
-    template <class E>
-    __device__ __forceinline__ void fetch(int i, uint32_t to, const E *row) const {
+    // each(to, from) for the vectors of chunk i; to: this lane's place in shared memory; row: at
+    // this lane's first column
+    template <class E, class F>
+    __device__ __forceinline__ void vectors_of(int i, uint32_t to, const E *row,
+                                               const F &each) const {
         row += i * stride;
         to += i * chunk_step<E>();
         const int s = past(row);
         const char *const p = reinterpret_cast<const char *>(row) - s;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            // what begins within the row: such a vector holds some of it
             const int at = (first + i * stride + q * 128) * (int)sizeof(E) - s;
-            if (at < n * (int)sizeof(E))
-                copy<E>(to + q * piece_step<E>(), p + q * 128 * (int)sizeof(E));
-            if (RAG && q == P - 1 && lane == 31 && at + bytes<E>() < n * (int)sizeof(E))
-                copy<E>(to + q * piece_step<E>() + bytes<E>(),
-                        p + q * 128 * (int)sizeof(E) + bytes<E>());
+            const int count = row_vectors(at, bytes<E>(), n * (int)sizeof(E),
+                                          RAG && q == P - 1 && lane == 31);
+            if (count > 0) each(to + q * piece_step<E>(), p + q * 128 * (int)sizeof(E));
+            if (RAG && q == P - 1 && count > 1)
+                each(to + q * piece_step<E>() + bytes<E>(),
+                     p + q * 128 * (int)sizeof(E) + bytes<E>());
         }
+    }
+    template <class E>
+    __device__ __forceinline__ void fetch(int i, uint32_t to, const E *row) const {
+        vectors_of(i, to, row, [](uint32_t there, const char *from) { copy<E>(there, from); });
+    }
+    // the same of a row whose vectors may leave the tensor, [begin, end)
+    template <class E>
+    __device__ __forceinline__ void fetch_within(int i, uint32_t to, const E *row, const E *begin,
+                                                 const E *end) const {
+        vectors_of(i, to, row, [&](uint32_t there, const char *from) {
+            copy_within((uintptr_t)from, bytes<E>(), (int)sizeof(E), (uintptr_t)begin,
+                        (uintptr_t)end, [&] { copy<E>(there, from); },
+                        [&](int b) { rows_move<sizeof(E)>(there + b, from + b); });
+        });
     }
     // Columns past the row's end are never copied to: zero, once, for good (on vectors).
     template <class E> __device__ __forceinline__ void clear(int i, char *at) const {
@@ -489,6 +508,16 @@ __device__ __forceinline__ float2 unit_moments(UnitTeam &t, const L &l, const fl
     return make_float2(mean, rsqrtf(fmaf(t.sum(q), t.inv_n, eps)));
 }
 
+// The copies of a row whose vectors may leave the tensor, [begin, end): rare, and a call, so that
+// it takes no registers from the rows between.
+template <int VPT, class L, class E>
+__device__ __noinline__ void unit_fetch_within(const L l, uint32_t to, const E *row,
+                                               const E *begin, const E *end) {
+#pragma unroll 1
+    for (int i = 0; i < VPT; ++i)
+        if (!l.none(i)) l.fetch_within(i, to, row, begin, end);
+}
+
 // A tensor's rows on their way to shared memory: the next row, and its step.
 template <class E> struct UnitFrom {
     const E *row;
@@ -500,6 +529,14 @@ template <class E> struct UnitFrom {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (!l.none(i)) l.fetch(i, to, row);
+        row += step;
+    }
+    // of a row whose vectors may leave the tensor, `rows` rows from p on
+    template <int VPT, class L>
+    __device__ __forceinline__ void fetch_within(const L &l, uint32_t to, const void *p, int64_t ld,
+                                                 int64_t rows) {
+        const E *const begin = static_cast<const E *>(p);
+        unit_fetch_within<VPT>(l, to, row, begin, begin + ((rows - 1) * ld + l.n));
         row += step;
     }
 };
@@ -548,8 +585,13 @@ k_block_unit(const BlockArgs a, const RowsGeom g) {
     auto fetch = [&]() {
         if (next < r1) {
             if (RAG) __syncwarp();   // the slot has been read
-            from_x.template fetch<VPT>(l, to + fill + x_at);
-            if (a.y) from_y.template fetch<VPT>(l, to + fill + y_at);
+            if (RAG && __builtin_expect(row_at_edge(next, (int)a.rows), 0)) {
+                from_x.template fetch_within<VPT>(l, to + fill + x_at, a.x, a.ld_x, a.rows);
+                if (a.y) from_y.template fetch_within<VPT>(l, to + fill + y_at, a.y, a.ld_y, a.rows);
+            } else {
+                from_x.template fetch<VPT>(l, to + fill + x_at);
+                if (a.y) from_y.template fetch<VPT>(l, to + fill + y_at);
+            }
             next += step;
         }
         fill = fill == last ? 0 : fill + g.slot_bytes;
@@ -717,10 +759,18 @@ k_block_unit_grad(const BlockArgs a, const RowsGeom g) {
     auto fetch = [&]() {
         if (next < r1) {
             if (RAG) __syncwarp();   // the slot has been read
-            from_h.template fetch<VPT>(l, to + fill + h_at);
-            from_dz.template fetch<VPT>(l, to + fill + dz_at);
-            if (a.dh) from_dh.template fetch<VPT>(l, to + fill + dh_at);
-            if (a.y) from_y.template fetch<VPT>(l, to + fill + y_at);
+            if (RAG && __builtin_expect(row_at_edge(next, (int)a.rows), 0)) {
+                from_h.template fetch_within<VPT>(l, to + fill + h_at, a.x, a.ld_x, a.rows);
+                from_dz.template fetch_within<VPT>(l, to + fill + dz_at, a.dz, a.ld_dz, a.rows);
+                if (a.dh)
+                    from_dh.template fetch_within<VPT>(l, to + fill + dh_at, a.dh, a.ld_dh, a.rows);
+                if (a.y) from_y.template fetch_within<VPT>(l, to + fill + y_at, a.y, a.ld_y, a.rows);
+            } else {
+                from_h.template fetch<VPT>(l, to + fill + h_at);
+                from_dz.template fetch<VPT>(l, to + fill + dz_at);
+                if (a.dh) from_dh.template fetch<VPT>(l, to + fill + dh_at);
+                if (a.y) from_y.template fetch<VPT>(l, to + fill + y_at);
+            }
             next += step;
         }
         fill = fill == last ? 0 : fill + g.slot_bytes;
