@@ -1496,11 +1496,16 @@ def _block_checks(where, stream_of, branch_of, dtype, gate, w_post, b_post, w_pr
             if t.shape[1] != n or t.shape[0] < 1 or rows % t.shape[0]:
                 raise ValueError("%s: %s is [n] or [groups, n], the groups dividing the rows; got "
                                  "%s beside [%d, %d]" % (where, name, tuple(t.shape), rows, n))
-            groups = max(1, rows // t.shape[0])
+            # one row is a row for all, beside whatever groups
+            groups = None if t.shape[0] == 1 else max(1, rows // t.shape[0])
             kw["ld_" + name] = step
         if per in kw and kw[per] != groups:
             raise ValueError("%s: scale and shift have the same groups" % where)
         kw[per] = groups
+    both = kw.get("gate_rows"), kw.get("mod_rows")
+    if None not in both and both[0] != both[1]:
+        raise ValueError("%s: a gate for every %d rows beside a scale or shift for every %d; groups "
+                         "of gate, scale and shift are the same, or one row for all" % (where, *both))
     return rows, n, kw
 
 
@@ -1510,7 +1515,8 @@ def block_norm(x, y=None, *, gate=None, w_post=None, b_post=None, w_pre=None, b_
                seed: int = 0, offset: int = 0, offset_device=None, stream_scale: float = 1.0,
                branch_scale: float = 1.0, dtype=None, out=None, stream=None):
     """(h, z) of BlockNormPlan's formulas in one call: x [rows, n] the residual stream, y
-    [rows, n] a block's output (None: none), gate, scale and shift [n] or [groups, n];
+    [rows, n] a block's output (None: none), gate, scale and shift [n] or [groups, n] (the same
+    groups for each of them that has more than one);
     z is None with pre="none" and h without y.  ``dtype``: z's, where there is no y to
     give it (None: x's).  ``out``: (h, z), either of which may be an input of its type or
     None (a new tensor)."""

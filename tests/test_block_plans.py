@@ -245,6 +245,21 @@ def test_one_call_forms_check_their_arguments(on_cpu):
     assert len(on_cpu) == 5
 
 
+def test_one_row_is_a_row_for_all_beside_groups(on_cpu):
+    x, y = mat(8, 32), mat(8, 32)
+    for kw in (dict(gate=mat(1, 32), scale=mat(4, 32)), dict(gate=mat(2, 32), shift=mat(1, 32)),
+               dict(gate=mat(4, 32), scale=mat(1, 32), shift=mat(32)),
+               dict(gate=mat(3, 32)[1:2], scale=mat(4, 32), shift=mat(4, 32))):
+        eb.block_norm(x, y, **kw)
+        grads = eb.block_norm_grad(y, x, x, y, **kw)
+        assert all(grads[k].shape == t.shape for k, t in kw.items())
+    assert len(on_cpu) == 8
+    with pytest.raises(ValueError, match="every 4 rows beside a scale or shift for every 2"):
+        eb.block_norm(x, y, gate=mat(2, 32), scale=mat(4, 32))
+    with pytest.raises(ValueError, match="same groups"):
+        eb.block_norm(x, y, scale=mat(1, 32), shift=mat(4, 32))
+
+
 # ------------------------------------------------------------------ several axes
 
 def axes(sections=(8, 12, 12), order="blocks", **kw):

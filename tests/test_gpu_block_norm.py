@@ -228,6 +228,25 @@ def test_one_gate_beside_grouped_scales():
         check_gradient(t, p, "layer", "rms", 0.2)
 
 
+@pytest.mark.parametrize("one", [("gate",), ("scale", "shift"), ("gate", "scale", "shift")])
+@pytest.mark.parametrize("n", [264, 203])
+def test_one_row_is_a_row_for_all(one, n):
+    """A parameter [1, n] is the row [n], beside groups of the others."""
+    t, p = operands(48, n, BF16, F32, 4)
+    p.update({k: p[k][2:3] for k in one})
+    flat = dict(p, **{k: p[k][0] for k in one})
+    h, z = check_forward(t, p, "layer", "rms", 0.2)
+    kw = dict(post="layer", pre="rms", epsilon=1e-5, epsilon_post=1e-3, dropout=0.2, seed=SEED,
+              offset=OFFSET)
+    for a, b in zip(eb.block_norm(t["x"], t["y"], **kw, **flat), (h, z)):
+        assert torch.equal(a, b)
+    got = check_gradient(t, p, "layer", "rms", 0.2)
+    dz, dh = matrix(21, 48, n, BF16), matrix(22, 48, n, F32)
+    want = eb.block_norm_grad(dz, dh, t["x"], t["y"], **kw, **flat)
+    for k, v in want.items():
+        assert torch.equal(got[k].view(v.shape), v), k
+
+
 @pytest.mark.parametrize("given", [(), ("w_pre",), ("b_pre",), ("b_post",), ("w_post", "gate"),
                                    ("scale",), ("shift",), ("gate",), ("gate", "b_post", "shift")])
 @pytest.mark.parametrize("n", [200, 203])
