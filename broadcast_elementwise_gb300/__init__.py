@@ -1493,11 +1493,12 @@ def _block_checks(where, stream_of, branch_of, dtype, gate, w_post, b_post, w_pr
             groups = None
         else:
             step = _matrix(where, t, None, t.dtype, first.device)
-            if t.shape[1] != n or t.shape[0] < 1 or rows % t.shape[0]:
+            # no groups of no rows: an empty batch
+            if t.shape[1] != n or (rows % t.shape[0] if t.shape[0] else rows):
                 raise ValueError("%s: %s is [n] or [groups, n], the groups dividing the rows; got "
                                  "%s beside [%d, %d]" % (where, name, tuple(t.shape), rows, n))
             # one row is a row for all, beside whatever groups
-            groups = None if t.shape[0] == 1 else max(1, rows // t.shape[0])
+            groups = None if t.shape[0] == 1 else rows // t.shape[0] if rows else 1
             kw["ld_" + name] = step
         if per in kw and kw[per] != groups:
             raise ValueError("%s: scale and shift have the same groups" % where)

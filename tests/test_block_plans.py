@@ -260,6 +260,18 @@ def test_one_row_is_a_row_for_all_beside_groups(on_cpu):
         eb.block_norm(x, y, scale=mat(1, 32), shift=mat(4, 32))
 
 
+def test_an_empty_batch_has_no_groups(on_cpu):
+    x, none = mat(0, 32), mat(0, 32)
+    h, z = eb.block_norm(x, x, gate=none, scale=none, shift=none)
+    assert h.shape == z.shape == (0, 32)
+    grads = eb.block_norm_grad(x, x, x, x, gate=none, scale=mat(1, 32), shift=mat(32))
+    assert [tuple(grads[k].shape) for k in ("gate", "scale", "shift")] == [(0, 32), (1, 32), (32,)]
+    assert len(on_cpu) == 2
+    for gate in (none, mat(3, 32)):
+        with pytest.raises(ValueError, match="groups dividing the rows"):
+            eb.block_norm(mat(8, 32), mat(8, 32), gate=gate)
+
+
 # ------------------------------------------------------------------ several axes
 
 def axes(sections=(8, 12, 12), order="blocks", **kw):

@@ -476,6 +476,19 @@ def test_empty_shapes():
         assert g["gate"].shape == gate.shape
 
 
+def test_an_empty_batch():
+    """No sequences: no rows and no groups; a row for all has a gradient of 0."""
+    x, y, none = (torch.empty(0, 64, dtype=BF16, device="cuda") for _ in range(3))
+    one = torch.ones(1, 64, dtype=BF16, device="cuda")
+    for kw in (dict(gate=none, scale=none, shift=none), dict(gate=none, scale=one, shift=one),
+               dict(gate=one, scale=none), dict(gate=one[0], shift=none)):
+        h, z = eb.block_norm(x, y, pre="layer", **kw)
+        assert h.shape == z.shape == x.shape
+        g = eb.block_norm_grad(y, x, h, y, pre="layer", **kw)
+        for k, t in kw.items():
+            assert g[k].shape == t.shape and (g[k] == 0).all()
+
+
 def test_outputs_that_are_not_wanted():
     t, p = operands(33, 264, BF16, BF16, 0)
     kw = dict(weight_dtype=F32, mod_dtype=F32, post="rms", pre="layer")
