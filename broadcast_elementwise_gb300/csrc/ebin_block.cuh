@@ -17,6 +17,7 @@ struct BlockUnits {
 
 // The kernels of CTAs' units: chunks of 256 columns that a lane owns, threads and warps.
 constexpr int kUnitVpt = 4, kUnitThreads = 512, kUnitWarps = kUnitThreads / 32;
+constexpr int64_t kUnitColumns = 8192;   // the widest rows that they take
 // A gradient's chunks: what it keeps of a column fits 128 registers (with a layer norm
 // and none after the block three sums: [16388,1152] bf16 66 us, 80 with three chunks a lane).
 template <bool FULL, bool POST> constexpr int kUnitGradVpt = FULL && POST ? 1 : 2;

@@ -388,8 +388,10 @@ extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *
                 return EBIN_ERR_INVALID_ARG;
             }
             p->team = team_units(p->groups, p->group_rows, a.n);
-            p->workspace = sizeof(float) * 4 *
-                (size_t)(p->groups * std::max(p->cta.parts, p->team.parts) * pad_of(a.n));
+            // wider rows are no CTA's units
+            const int64_t parts = a.n > kUnitColumns ? p->team.parts
+                                                     : std::max(p->cta.parts, p->team.parts);
+            p->workspace = sizeof(float) * 4 * (size_t)(p->groups * parts * pad_of(a.n));
         }
     }
     *out = p;

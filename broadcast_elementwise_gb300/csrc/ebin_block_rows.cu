@@ -71,7 +71,7 @@ template <class E> static size_t unit_bytes(const RowsGeom &g, int vpt, bool vec
 // rows spreads over more SMs a row a team); a gradient, whose units each leave sums, half
 // its teams' unless there is but one group.
 static bool cta_takes(const BlockArgs &a, int chunks, int vpt, bool grad) {
-    if (chunks > 32) return false;
+    if (a.n > kUnitColumns) return false;
     const int64_t teams = kUnitWarps / div_up(chunks, vpt);
     return grad ? a.groups == 1 || 2 * a.cta.rows >= teams
                 : a.rows > 304 && a.cta.rows >= 2 * teams;

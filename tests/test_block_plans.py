@@ -127,6 +127,18 @@ def test_block_plan_refusals():
                 rotary_dim=0) == "invalid_attr"
 
 
+def test_workspace_of_wide_rows():
+    """No more than 2^28 sums of 4 bytes, but for a unit a group of all four kinds."""
+    for rows in (1, 17, 152, 456, 20000):
+        for n in (64, 4096, 8192, 8193, 16384, 40000, 1 << 20, 1 << 24):
+            for kw in ({}, dict(gate_rows=rows, mod_rows=rows), dict(gate_rows=1)):
+                groups = rows if kw.get("gate_rows") == 1 else 1
+                if groups * n // 32 > 2 ** 31 - 1:      # CTAs of the last step: refused
+                    continue
+                got = block(rows=rows, n=n, gradient=True, post="layer", **kw).workspace_bytes
+                assert 0 < got <= 4 * max(1 << 28, 4 * groups * (n + 3)), (rows, n, kw)
+
+
 def test_block_execute_refusals():
     def run(plan, x=0x100000, y=0x200000, h=0x300000, z=0x400000, **kw):
         eb.execute_block_norm(plan, x, y, h, z, stream=0, **kw)
