@@ -96,7 +96,8 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
     // Off the vectors the shifts pay for 16-bit rows of more than 2048 columns ([8191,4097]
     // bf16 116 us, a team a row 198; [20000,1543] f16 with dropout 151 and 136; [4095,2050] f32
     // 44 and 36).
-    if ((vec || (sizeof(S) == 2 && chunks > 8)) && cta_takes(a, chunks, kUnitVpt, false)) {
+    constexpr bool shifts = sizeof(S) == 2;
+    if ((vec || (shifts && chunks > 8)) && cta_takes(a, chunks, kUnitVpt, false)) {
         RowsGeom g = unit_geom(a, chunks, kUnitVpt);
         const bool scaled = a.branch_scale != 1.0f || a.drop.least;
         if (a.y && (a.gate || a.w_post || a.b_post || scaled)) g.tables |= TABLE_Y;
@@ -111,7 +112,8 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
         if (g.slots > 0) {
             *parts = a.cta.parts;
             const size_t smem = tables + g.slots * row;
-            if (!vec) return launch_rows<k_block_unit<T, S, true, true>>(a, g, g.units, smem, s);
+            if constexpr (shifts)
+                if (!vec) return launch_rows<k_block_unit<T, S, true, true>>(a, g, g.units, smem, s);
             return layer ? launch_rows<k_block_unit<T, S, true, false>>(a, g, g.units, smem, s)
                          : launch_rows<k_block_unit<T, S, false, false>>(a, g, g.units, smem, s);
         }

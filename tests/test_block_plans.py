@@ -1,6 +1,10 @@
 """Refusals of dropout, of the norms around a block and of several axes' plans, and the words that
 dropout draws.  CPU: the checks run before any device call, and the addresses given are
 never dereferenced."""
+import re
+import shutil
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -125,6 +129,19 @@ def test_block_plan_refusals():
     assert block(gradient=True).workspace_bytes > 0
     assert code(eb.HeadsPlan, "bfloat16", (1, 2, 3, 4), norm="layer",
                 rotary_dim=0) == "invalid_attr"
+
+
+def test_kernels_that_no_call_reaches_are_not_built():
+    """Forward, only 16-bit streams off the vectors go to the kernel that shifts rows."""
+    if shutil.which("nm") is None:
+        pytest.skip("no nm")
+    names = subprocess.run(["nm", "-C", eb.LIB_PATH], capture_output=True, text=True).stdout
+    built = set(re.findall(r"void ebin::k_block_unit<(\w+), (\w+), (true|false), (true|false)>\(",
+                           names))
+    pairs = [("float", "float"), ("__half", "__half"), ("__nv_bfloat16", "__nv_bfloat16"),
+             ("__half", "float"), ("__nv_bfloat16", "float")]
+    assert built == ({(t, s, layer, "false") for t, s in pairs for layer in ("true", "false")} |
+                     {(t, s, "true", "true") for t, s in pairs if s != "float"})
 
 
 def test_workspace_of_wide_rows():
