@@ -301,9 +301,13 @@ BlockUnits block_units(int64_t group_rows, int64_t parts) {
 
 // Units of a CTA an SM.  A count of parts is judged by when its last wave of 152 ends, a
 // unit costing its teams' steps and what three more would (its tables, its sums).  Of a
-// gradient's the least within a thirtieth of the best: SMs left over are where the last
-// sums begin ([8192,4096] bf16: 147 units 69.2 us, 152 units 71.6); but a step more of few
-// costs more than that gives ([16388,1152] in four groups: 144 units 69.2, 152 units 66.6).
+// gradient's the least within 3.5 % of the best where a CTA has two teams or more: SMs left
+// over are where the last sums begin.  us with RMS norms on both sides, bf16, against the best's:
+// [8192,4096] 69.0 and 70.5, [10000,4096] 83.1 and 86.6, [12288,4096] 100.7 and 102.4,
+// [16384,2048] 71.5 and 72.7, [24576,1536] 76.5 and 80.2, but [9000,3584] 70.9 and 69.1.  Within
+// 2.5 % [10000,4096] 86.3 and [24576,1536] 80.4; within 5 % [16384,1152] 50.7 (48.6),
+// [5000,4096] 48.0 (46.7) and [16388,1152] modulated 69.4 (66.9), steps of few.  With one team a
+// step more costs more than that gives: [4096,8192] 74.9 and 73.0, [6553,5120] 84.8 and 83.1.
 BlockUnits cta_units(int64_t groups, int64_t group_rows, int64_t n, int vpt, bool gradient) {
     const int64_t warps = std::max<int64_t>(1, div_up(div_up(n, 256), vpt));
     const int64_t teams = std::max<int64_t>(1, kUnitWarps / warps);
@@ -315,7 +319,7 @@ BlockUnits cta_units(int64_t groups, int64_t group_rows, int64_t n, int vpt, boo
     double least = cost(1);
     for (int64_t p = 2; p <= most; ++p) least = std::min(least, cost(p));
     int64_t p = 1;
-    while (cost(p) > (gradient ? 1.0 + 1.0 / 29 : 1.0) * least) ++p;
+    while (cost(p) > (gradient && teams > 1 ? 1.035 : 1.0) * least) ++p;
     return block_units(group_rows, p);
 }
 
