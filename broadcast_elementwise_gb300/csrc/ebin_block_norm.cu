@@ -161,10 +161,17 @@ int64_t rows_bytes(int64_t rows, int64_t n, int64_t ld, int64_t size) {
     return rows > 0 && n > 0 ? ((rows - 1) * ld + n) * size : 0;
 }
 
-// Whether output y may lie where it lies beside input x.
-bool apart(const Range &x, const Range &y, int64_t rows) {
+// Whether two ranges share nothing; of two matrices their rows of n elements count.
+bool disjoint(const Range &x, const Range &y, int64_t rows, int64_t n) {
     if (!x.p || !y.p || !ranges_overlap(x.p, x.bytes, y.p, y.bytes)) return true;
-    return x.p == y.p && x.size == y.size && x.ld > 0 && y.ld > 0 && (rows <= 1 || x.ld == y.ld);
+    return x.ld > 0 && y.ld > 0 &&
+           !rows_share(x.p, n * x.size, x.ld, y.p, n * y.size, y.ld, rows);
+}
+
+// Whether output y may lie where it lies beside input x.
+bool apart(const Range &x, const Range &y, int64_t rows, int64_t n) {
+    return disjoint(x, y, rows, n) ||
+           (x.p == y.p && x.size == y.size && x.ld > 0 && y.ld > 0 && (rows <= 1 || x.ld == y.ld));
 }
 
 // Columns of a row of sums: whole vectors.
@@ -436,8 +443,8 @@ extern "C" ebin_status ebin_block_norm_execute(ebin_block_norm_plan_t plan, cons
         {z, rows_bytes(at.rows, at.n, at.ld_z, p.isz), at.ld_z * p.isz, p.isz}};
     for (const Range &o : out)
         for (int i = 0; i < c; ++i)
-            if (!apart(in[i], o, at.rows)) return EBIN_ERR_ALIAS;
-    if (h && z && ranges_overlap(h, out[0].bytes, z, out[1].bytes)) return EBIN_ERR_ALIAS;
+            if (!apart(in[i], o, at.rows, at.n)) return EBIN_ERR_ALIAS;
+    if (!disjoint(out[0], out[1], at.rows, at.n)) return EBIN_ERR_ALIAS;
     if (!h && !z) return EBIN_OK;
     a.x = x;
     a.y = y;
@@ -516,11 +523,9 @@ extern "C" ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan,
     if (wanted) out[o++] = Range{workspace, (int64_t)p.workspace, 0, 0};
     for (int k = 0; k < o; ++k) {
         for (int i = 0; i < c; ++i)
-            if (!apart(in[i], out[k], at.rows)) return EBIN_ERR_ALIAS;
+            if (!apart(in[i], out[k], at.rows, at.n)) return EBIN_ERR_ALIAS;
         for (int i = 0; i < k; ++i)
-            if (out[i].p && out[k].p &&
-                ranges_overlap(out[i].p, out[i].bytes, out[k].p, out[k].bytes))
-                return EBIN_ERR_ALIAS;
+            if (!disjoint(out[i], out[k], at.rows, at.n)) return EBIN_ERR_ALIAS;
     }
     a.x = h;
     a.y = y;

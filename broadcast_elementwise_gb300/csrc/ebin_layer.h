@@ -26,6 +26,20 @@ inline bool ranges_overlap(const void *p, int64_t pb, const void *q, int64_t qb)
     return pb > 0 && qb > 0 && a < b + (uintptr_t)qb && b < a + (uintptr_t)pb;
 }
 
+// Whether two matrices of `rows` rows share a byte: rows of xb bytes that start ldx bytes
+// apart from x on, of yb bytes ldy apart from y on.  Columns of one wider buffer, side by side,
+// share none.
+inline bool rows_share(const void *x, int64_t xb, int64_t ldx, const void *y, int64_t yb,
+                       int64_t ldy, int64_t rows) {
+    if (xb <= 0 || yb <= 0 || rows <= 0 ||
+        !ranges_overlap(x, (rows - 1) * ldx + xb, y, (rows - 1) * ldy + yb))
+        return false;
+    if (ldx != ldy) return true;
+    // where y's rows begin behind those of x
+    const int64_t at = ((int64_t)((uintptr_t)y - (uintptr_t)x) % ldx + ldx) % ldx;
+    return at < xb || at + yb > ldx;
+}
+
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // a * b < EBIN_MAX_ELEMENTS for a, b >= 0, without overflow.

@@ -1020,7 +1020,8 @@ typedef struct ebin_block_norm_params {
  *   h          [rows, n], or NULL: not wanted
  *   z          [rows, n], or NULL: not wanted (it is not written with pre = NONE)
  * An output may be an input of its own type (the same pointer and row stride);
- * any other overlap with an output is ALIAS.
+ * any other overlap with an output is ALIAS.  Matrices of the same row stride in
+ * bytes whose rows lie side by side, columns of one wider buffer, do not overlap.
  * Errors: INVALID_ARG (a NULL buffer with work to do, a buffer off its element's
  * boundary, a gradient plan, a gate without a branch, a parameter of a norm that
  * is NONE; scale and shift are pre's), ALIAS, CUDA.

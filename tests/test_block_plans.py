@@ -184,6 +184,22 @@ def test_block_execute_refusals():
     assert code(run, block(stream_dtype="float32"), z=0x100000) == "alias"   # and another type
 
 
+def test_block_columns_of_one_buffer_that_overlap():
+    """Rows of 64 bytes, 160 bytes apart; side by side without sharing a byte they are accepted
+    (on the GPU)."""
+    p = block(ld_x=80, ld_y=80, ld_h=80, ld_z=80)
+
+    def run(x, y, h, z, plan=p):
+        eb.execute_block_norm(plan, x, y, h, z, stream=0)
+
+    x, y = 0x100000, 0x100000 + 64
+    for h, z in ((x, x), (x, x + 160), (x, x + 62), (x, y + 2), (x + 98, y), (x + 160 - 62, y),
+                 (y, y + 160), (x + 320 - 2, None)):
+        assert code(run, x, y, h, z) == "alias", (h - x, z and z - x)
+    wide = block(ld_x=80, ld_y=80, ld_h=84, ld_z=80)      # another stride crosses the columns
+    assert code(run, x, y, x + 128, None, plan=wide) == "alias"
+
+
 def test_block_grad_refusals():
     p = block(gradient=True, post="rms")
     good = dict(dz=0x100000, dh=0x110000, h=0x120000, y=0x130000, dx=0x140000, dy=0x150000,

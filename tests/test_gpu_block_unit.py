@@ -154,3 +154,28 @@ def test_bad_rows_stay_alone(rows, n, dtype, stream):
     kw = dict(pre="rms", dropout=0.5, seed=SEED, offset=OFFSET, **valid(p, "none", "rms"))
     for a, b in zip(eb.block_norm(t["x"], t["y"], **kw), eb.block_norm(t["x"], broken, **kw)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [7, 400, 5000])
+@pytest.mark.parametrize("n", [264, 523, 9001])
+def test_columns_of_one_buffer(rows, n):
+    """Inputs and outputs side by side in one buffer, each in place or beside the others."""
+    rows = min(rows, 4000000 // n)
+    t, p = operands(rows, n, BF16, BF16, 0)
+    kw = dict(post="rms", pre="layer", dropout=0.1, seed=SEED, offset=OFFSET, **p)
+    dz, dh = matrix(21, rows, n, BF16), matrix(22, rows, n, BF16)
+    want = eb.block_norm(t["x"], t["y"], **kw)
+    back = eb.block_norm_grad(dz, dh, t["x"], t["y"], **kw)
+    for names in ((0, 1), (1, 0), (2, 3), (3, 0)):
+        x, y, *_ = both = torch.cat((t["x"], t["y"], dz, dh), 1).split(n, 1)
+        h, z = (both[i] for i in names)
+        eb.block_norm(x, y, out=(h, z), **kw)
+        assert torch.equal(h, want[0]) and torch.equal(z, want[1])
+        for i in set(range(4)) - set(names):
+            assert torch.equal(both[i], (t["x"], t["y"], dz, dh)[i])
+        h, y, dz_, dh_ = both = torch.cat((t["x"], t["y"], dz, dh), 1).split(n, 1)
+        got = eb.block_norm_grad(dz_, dh_, h, y, out=[both[i] for i in names], **kw)
+        for k, v in back.items():
+            assert torch.equal(got[k], v), k
+        for i in set(range(4)) - set(names):
+            assert torch.equal(both[i], (t["x"], t["y"], dz, dh)[i])
