@@ -157,12 +157,13 @@ ebin_status prepare_dropout(const ebin_dropout_plan_s &p, const void *x, const v
         return EBIN_ERR_INVALID_ARG;
     const int64_t y_b = span_of(at.rows, at.n, p.ld_y) * p.isz;
     const bool one = at.rows <= 1;      // a single row has no stride
-    if (ranges_overlap(x, span_of(at.rows, at.n, p.ld_x) * p.isz, y, y_b) &&
-        !(x == y && (one || p.ld_x == p.ld_y)))
-        return EBIN_ERR_ALIAS;
-    if (residual && ranges_overlap(residual, span_of(at.rows, at.n, p.ld_r) * p.isz, y, y_b) &&
-        !(residual == y && (one || p.ld_r == p.ld_y)))
-        return EBIN_ERR_ALIAS;
+    // whether y may lie where it lies beside an input
+    auto apart = [&](const void *in, int64_t ld) {
+        const int64_t row = at.n * p.isz;
+        return (in == y && (one || ld == p.ld_y)) ||
+               !rows_share(in, row, ld * p.isz, y, row, p.ld_y * p.isz, at.rows);
+    };
+    if (!apart(x, p.ld_x) || (residual && !apart(residual, p.ld_r))) return EBIN_ERR_ALIAS;
     if ((bias && ranges_overlap(bias, at.n * (int64_t)ebin_dtype_size(at.dtype_bias), y, y_b)) ||
         (offset_device && ranges_overlap(offset_device, 8, y, y_b)))
         return EBIN_ERR_ALIAS;

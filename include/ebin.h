@@ -910,7 +910,7 @@ void ebin_dropout_plan_release(ebin_dropout_plan_t plan);
 /*
  * Run a forward plan on device buffers, enqueued on `stream`.  y may be x or
  * the residual itself (same pointer and stride); any other overlap of y with
- * an input is ALIAS.  offset_device: NULL, or a device word that is added to
+ * an input is ALIAS.  (Columns of one wider buffer, side by side, do not overlap.)  offset_device: NULL, or a device word that is added to
  * offset when the kernel runs, so that a captured graph whose program advances
  * the word draws anew with each replay.
  * Errors: INVALID_ARG (a NULL buffer with work to do, a gradient plan), ALIAS, CUDA.

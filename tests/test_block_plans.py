@@ -99,6 +99,18 @@ def test_dropout_execute_refusals():
         assert code(grad, p, **dict(good, **kw)) == "alias"
 
 
+def test_dropout_columns_of_one_buffer_that_overlap():
+    """As test_block_columns_of_one_buffer_that_overlap."""
+    p = drop(residual=True, ld_x=80, ld_residual=80, ld_y=80)
+    x, res = 0x100000, 0x100000 + 64
+    for y in (x + 2, x + 98, x + 160, res - 2, res - 160, res + 320 - 62):
+        assert code(eb.execute_dropout, p, x, y, 1, residual=res, stream=0) == "alias"
+    p = drop(residual=True, ld_x=80, ld_residual=80, ld_y=84)
+    assert code(eb.execute_dropout, p, x, x + 128, 1, residual=res, stream=0) == "alias"
+    p = drop(gradient=True, ld_x=80, ld_y=80)
+    assert code(eb.execute_dropout_grad, p, x, x + 62, 1, stream=0) == "alias"
+
+
 # ------------------------------------------------------------------ norms around a block
 
 def block(dtype="bfloat16", rows=4, n=32, **kw):

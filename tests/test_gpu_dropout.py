@@ -154,3 +154,18 @@ def test_streams_and_empty_shapes():
         assert eb.dropout(t, 0.5, 1).shape == t.shape
         dx, db = eb.dropout_grad(t, 0.5, 1, bias=True)
         assert dx.shape == t.shape and (db == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,n", [(40, 96), (300, 257)])
+def test_columns_of_one_buffer(rows, n, dtype):
+    x, res = normal(1, rows, n, dtype=dtype), normal(2, rows, n, dtype=dtype)
+    want = eb.dropout(x, 0.4, 3, 9, residual=res)
+    for i in range(3):
+        both = torch.cat((x, res, x), 1).split(n, 1)
+        assert eb.dropout(both[0], 0.4, 3, 9, residual=both[1], out=both[i]) is both[i]
+        for j, v in enumerate((x, res, x)):
+            assert torch.equal(both[j], want if j == i else v)
+    both = torch.cat((x, res), 1).split(n, 1)
+    eb.dropout_grad(both[0], 0.4, 3, 9, out=both[1])
+    assert torch.equal(both[0], x) and torch.equal(both[1], eb.dropout(x, 0.4, 3, 9))
