@@ -1524,6 +1524,8 @@ def block_norm(x, y=None, *, gate=None, w_post=None, b_post=None, w_pre=None, b_
     import torch
     where = "block_norm"
     h, z = (None, None) if out is None else out
+    if pre == "none" and z is not None:
+        raise ValueError("block_norm: there is no z with pre='none'")
     if dtype is None:
         dtype = x.dtype if y is None else y.dtype
     rows, n, kw = _block_checks(where, [("x", x), ("h", h)], [("y", y), ("z", z)], dtype, gate,

@@ -317,6 +317,15 @@ def test_one_row_is_a_row_for_all_beside_groups(on_cpu):
         eb.block_norm(x, y, scale=mat(1, 32), shift=mat(4, 32))
 
 
+def test_a_z_that_there_is_not(on_cpu):
+    """Nothing would write it, so it is not handed back as the result."""
+    x = mat(8, 32)
+    with pytest.raises(ValueError, match="no z"):
+        eb.block_norm(x, x, pre="none", out=(None, mat(8, 32)))
+    h = mat(8, 32)
+    assert eb.block_norm(x, x, pre="none", out=(h, None)) == (h, None)
+
+
 def test_an_empty_batch_has_no_groups(on_cpu):
     x, none = mat(0, 32), mat(0, 32)
     h, z = eb.block_norm(x, x, gate=none, scale=none, shift=none)
