@@ -130,8 +130,8 @@ __device__ __forceinline__ float block_keep(const BlockArgs &a, float v, int64_t
 
 // A CTA walks rows, a thread every 1024th column of each, with one pass over the
 // row for each sum (from the L1 and L2 after the first): any width, any stride, any
-// alignment, for rows of more than 32768 columns ([1000,40000] bf16 278 us, a sixth of
-// the copy's rate; 256 threads 329).  A thread reads and writes the same columns in every
+// alignment, for rows of more than 32768 columns ([1000,40000] bf16 310 us, a sixth of
+// the copy's rate; with 256 threads 1.2 times that).  A thread reads and writes the same columns in every
 // pass, so an output may be an input.
 template <class T, class S>
 __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any(const BlockArgs a) {
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any(const BlockArgs 
 
 // The gradient, for rows of more than 16384 columns: a CTA takes a unit, rows of one group;
 // its column sums stay in its part of the workspace, each column its thread's own, read
-// and written for every row ([1000,20000] bf16 0.51 ms, with 256 threads and
+// and written for every row ([1000,20000] bf16 0.55 ms, with 256 threads and
 // all four kinds 2.1).
 template <class T, class S>
 __global__ void __launch_bounds__(kBlockAnyThreads) k_block_any_grad(const BlockArgs a) {

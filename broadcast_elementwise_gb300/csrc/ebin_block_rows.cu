@@ -94,7 +94,7 @@ cudaError_t EBIN_NAME(launch_block_rows_, EBIN_DT)(const BlockArgs &a, bool vec,
     const bool layer = a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
     const int s_vectors = sizeof(S) == 4 ? 2 : 1, t_vectors = sizeof(T) == 4 ? 2 : 1;
     // Off the vectors the shifts pay for 16-bit rows of more than 2048 columns ([8191,4097]
-    // bf16 116 us, a team a row 198; [20000,1543] f16 with dropout 151 and 136; [4095,2050] f32
+    // bf16 122 us, a team a row 198; [20000,1543] f16 with dropout 151 and 136; [4095,2050] f32
     // 44 and 36).
     constexpr bool shifts = sizeof(S) == 2;
     if ((vec || (shifts && chunks > 8)) && cta_takes(a, chunks, kUnitVpt, false)) {

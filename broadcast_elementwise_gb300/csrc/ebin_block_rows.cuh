@@ -1,9 +1,11 @@
 // The norms around a block, a row a team of warps: each lane owns eight columns of every
 // chunk of 256 that its warp owns, and a row's data is read from memory once.  The
-// path of what the kernels of CTAs' units (ebin_block_unit.cuh) leave: forward few rows,
-// small groups, 32-bit rows off the vectors and rows of 8193 to 32768 columns; a
-// gradient's small groups, gradients without a norm before the next block, and rows of
-// 8193 to 16384 columns.
+// path of what the kernels of CTAs' units (ebin_block_unit.cuh) leave.  Forward: few rows,
+// small groups, rows whose factors leave no room for them in shared memory, rows of 8193
+// to 32768 columns, and off the vectors 32-bit streams and rows of at most 2048 columns.  Of
+// gradients: small groups, those without a norm before the next block, rows of 8193 to
+// 16384 columns, and, with a norm after the block and a layer norm or the gradient of a
+// shift or a bias, of 4097 and more ([4096,8192] bf16 with layer norms on both sides 176 us).
 #pragma once
 
 #include "ebin_block.cuh"

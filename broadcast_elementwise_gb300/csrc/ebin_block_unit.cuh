@@ -1,16 +1,22 @@
 // The norms around a block on many rows of at most 8192 columns: one CTA an SM takes a unit,
-// consecutive rows of one group, and its teams walk them in turn.  What a column's
+// consecutive rows of one group, and its teams walk them in turn.  (A gradient whose sums take
+// a chunk a lane, kUnitGradVpt: at most 4096.)  What a column's
 // elements are multiplied by and added to lies in shared memory in binary32, formed
 // once from the parameters: two 16-byte loads in place of one and eight conversions,
 // which a row of weights in the L1 costs for each use ([8192,4096] bf16 with both
 // norms' weights: 60 us so, 48 without the weights).
 //
-// Bound by memory, with the issue of instructions close behind: 512 threads of 128
-// registers an SM, each row through shared memory by asynchronous copies, up to three
-// rows a team there.  bf16, against a copy's 6756 GB/s:
+// 512 threads of 128 registers an SM, each row through shared memory by asynchronous copies, up
+// to three rows a team there.  bf16, against a copy's 6683 GB/s:
 //   [8192,4096] norms on both sides   forward 49.0 us 5480 GB/s, gradient 69.1 us 5830
 //   [16380,1536] f32 stream, gate, scale, shift   forward 52.2 us 5790 GB/s
-//   [16388,1152] the same with dropout, gradient 66.6 us 3400 GB/s: Philox's rounds
+//   [16388,1152] the same with dropout, gradient 66.6 us 3400 GB/s
+//   [8192,4096] layer norms on both sides   forward 59.7 us 4490 GB/s, gradient 144 us 2800
+// RMS norms and plain modulation are bound by memory, with the issue of instructions close behind.
+// The modulated gradient is not: 43 million warp instructions are 35 of its 67 us, the rest a
+// row's chain of two exchanges and three passes, with 15 warps an SM to cover it (a capture:
+// issue 55 %, memory 36 %, stalls at barriers 1.25, of fixed latency 1.38 and on shared memory
+// 1.02 an issue).
 //
 // RAGGED: rows that do not start and end on vectors.  A row's copies begin on the
 // vector that holds its first element; a lane takes its columns from two neighbouring

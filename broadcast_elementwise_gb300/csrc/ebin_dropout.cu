@@ -1,10 +1,13 @@
 // Dropout: y = residual + keep(x + bias) / (1 - p), and its gradient with the
 // bias's, in one pass; the mask comes from ebin_philox.cuh and is never stored.
 //
-// Bound by memory with the integer pipes close behind: the ten rounds take 20 wide
-// products and 20 exclusive ors for four elements.  [16384,8192] bf16 with bias and
-// residual 135 us, 5970 GB/s of the 6756 measured by a copy; a gradient of [8192,4096]
-// bf16 with the bias's 33 us; rows off the vectors 1.5 times that.
+// Time goes by elements, not by bytes: the ten rounds take 20 wide products and 20 exclusive
+// ors for four elements, and a warp has one row on its way and none while it draws (a capture
+// of the first below: issue 55 %, 8.7 warps waiting for memory an issue).  bf16, against the
+// bytes at a copy's 6683 GB/s:
+//   [16384,8192] with bias and residual 136 us (120), alone 123 (80), gradient 112 (80)
+//   [8192,4096] with bias and residual 39 us (30), alone 36 (20), gradient 31, with the bias's 34 (20)
+// [8192,4096] f32 alone 47 us (40); [4095,1543] f16, off the vectors, 12.7 (3.8).
 #include <new>
 
 #include "ebin_philox.cuh"
