@@ -219,3 +219,25 @@ def test_captured_and_in_place():
     graph.replay()
     want = eb.rotary(q, k, c, s, at, axes=(16, 16))
     assert torch.equal(qi, want[0]) and torch.equal(ki, want[1])
+
+
+WIDER = [
+    # interleaved heads of 5, 9, 32 and 64 vectors of 16-bit elements, parts of them turned
+    (2, 9, 5, 2, 40, "interleaved", (6, 7, 7), "dealt", 0),
+    (2, 9, 5, 2, 72, "interleaved", (12, 12, 12), "blocks", 0),
+    (2, 9, 5, 2, 72, "interleaved", (9, 4), "blocks", 0),
+    (2, 9, 5, 2, 256, "interleaved", (40, 44, 44), "dealt", 0),
+    (2, 9, 5, 2, 512, "interleaved", (64, 96, 96), "blocks", 0),
+    (2, 9, 5, 2, 512, "interleaved", (33, 0, 0, 100), "dealt", 0),
+    (1, 2049, 9, 5, 512, "interleaved", (64, 96, 96), "blocks", 0),
+    (1, 4100, 3, 17, 8, "interleaved", (1, 2, 1), "blocks", 0),
+    (1, 3000, 13, 1, 40, "half", (8, 6, 6), "dealt", 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("case", WIDER, ids=str)
+def test_heads_of_other_widths(case, dtype):
+    for gradient in (False, True):
+        test_rotary(case, dtype, gradient)
+    test_norm_and_its_gradient(case, dtype)

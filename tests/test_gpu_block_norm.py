@@ -511,3 +511,20 @@ def test_outputs_that_are_not_wanted():
         eb.execute_block_norm_grad(bwd, dz, dh, h, t["y"], out if only == "x" else None,
                                    out if only == "y" else None, **q, **kw)
         assert torch.equal(out, want[only]), only
+
+
+@pytest.mark.parametrize("dtype,stream", TYPES)
+@pytest.mark.parametrize("rows,n", [(30, 264), (30, 33), (5000, 1536), (2500, 4097), (9, 40000)])
+def test_the_stream_alone_scaled_and_normed(rows, n, dtype, stream):
+    """Without a branch h is stream_scale x, where a tensor for it is given: x itself too."""
+    t, p = operands(rows, n, dtype, stream, 0)
+    p = valid(p, "none", "layer", branch=False)
+    kw = dict(pre="layer", stream_scale=1.5, dtype=dtype, **p)
+    alone, z = eb.block_norm(t["x"], **kw)
+    assert alone is None
+    want = (1.5 * t["x"].double()).to(stream)
+    h, again = eb.block_norm(t["x"], out=(torch.empty_like(t["x"]), None), **kw)
+    assert torch.equal(h, want) and torch.equal(again, z)
+    x = t["x"].clone()
+    h, again = eb.block_norm(x, out=(x, None), **kw)
+    assert h is x and torch.equal(x, want) and torch.equal(again, z)
