@@ -45,6 +45,13 @@ struct BlockArgs {
 
 enum BlockSum : int { SUM_DZ_HH = 0, SUM_DZ = 1, SUM_E_YH = 2, SUM_E = 3 };
 
+// Whether a gradient's units take the full kernel: a layer norm, or a shift's or a bias's
+// gradient.
+inline bool unit_grad_full(int post, int pre, int need) {
+    return post == EBIN_NORM_LAYER || pre == EBIN_NORM_LAYER || need >> SUM_DZ & 1 ||
+           need >> SUM_E & 1;
+}
+
 struct BlockSumsArgs {
     float *partial;                // [groups * parts][4][pad]
     int64_t parts, groups, n, pad;

@@ -141,7 +141,9 @@ struct ebin_block_norm_plan_s {
     int64_t isz, ssz, wsz, msz;    // bytes of an element of the four types
     uint32_t least;
     int64_t groups = 1, group_rows = 0;
-    ebin::BlockUnits cta, team;          // the rows' units: a CTA's, and a gradient's teams'
+    // the rows' units: a CTA's (of a gradient with a norm after the block, by whether it is the
+    // full kernel's), and a gradient's teams'
+    ebin::BlockUnits cta[2], team;
     size_t workspace = 0;
 };
 
@@ -216,7 +218,7 @@ ebin_status prepare_block(const ebin_block_norm_plan_s &p, const ebin_block_norm
     a.w_f32 = at.dtype_w == EBIN_FLOAT32;
     a.mod_f32 = at.dtype_mod == EBIN_FLOAT32;
     a.drop = drop_args(p.least, w.seed, w.offset, w.offset_device);
-    a.cta = p.cta;
+    a.cta = p.cta[0];
     a.team = p.team;
     a.groups = p.groups;
     a.group_rows = p.group_rows;
@@ -388,11 +390,11 @@ extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *
     if (a.rows > 0) {
         p->group_rows = per ? per : a.rows;
         p->groups = a.rows / p->group_rows;
-        const bool layer = a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
-        const int vpt = !a.gradient ? kUnitVpt
-                      : layer && a.post != EBIN_NORM_NONE ? kUnitGradVpt<true, true>
-                                                          : kUnitGradVpt<true, false>;
-        p->cta = cta_units(p->groups, p->group_rows, a.n, vpt, a.gradient != 0);
+        const bool grad = a.gradient != 0;
+        p->cta[0] = cta_units(p->groups, p->group_rows, a.n,
+                              grad ? kUnitGradVpt<false, true> : kUnitVpt, grad);
+        p->cta[1] = grad && a.post != EBIN_NORM_NONE
+            ? cta_units(p->groups, p->group_rows, a.n, kUnitGradVpt<true, true>, true) : p->cta[0];
         if (a.gradient) {
             if (p->groups * div_up(a.n, kSumColumns) > 0x7FFFFFFF) {   // CTAs of the last step
                 delete p;
@@ -401,7 +403,7 @@ extern "C" ebin_status ebin_block_norm_plan_create(const ebin_block_norm_attrs *
             p->team = team_units(p->groups, p->group_rows, a.n);
             // wider rows are no CTA's units
             const int64_t parts = a.n > kUnitColumns ? p->team.parts
-                                                     : std::max(p->cta.parts, p->team.parts);
+                : std::max({p->cta[0].parts, p->cta[1].parts, p->team.parts});
             p->workspace = sizeof(float) * 4 * (size_t)(p->groups * parts * pad_of(a.n));
         }
     }
@@ -546,6 +548,7 @@ extern "C" ebin_status ebin_block_norm_grad_execute(ebin_block_norm_plan_t plan,
     if (g.gate || g.w_post) a.need |= 1 << SUM_E_YH;
     if (g.b_post || (g.gate && a.b_post)) a.need |= 1 << SUM_E;
     if (!wanted && !dx && !dy) return EBIN_OK;
+    a.cta = p.cta[unit_grad_full(a.post, a.pre, a.need)];
     int64_t parts;
     if (launch_block(p, a, true, &parts, s) != cudaSuccess) return EBIN_ERR_CUDA;
     if (!wanted) return EBIN_OK;

@@ -146,8 +146,7 @@ cudaError_t EBIN_NAME(launch_block_rows_grad_, EBIN_DT)(const BlockArgs &a, bool
     *parts = 0;
     const int chunks = (int)div_up(a.n, kChunk);
     if (chunks > 64) return cudaSuccess;
-    const bool full = a.need >> SUM_DZ & 1 || a.need >> SUM_E & 1 ||
-                      a.post == EBIN_NORM_LAYER || a.pre == EBIN_NORM_LAYER;
+    const bool full = unit_grad_full(a.post, a.pre, a.need);
     const bool has[2] = {a.scale || a.w_pre,
                          a.gate || a.w_post || a.branch_scale != 1.0f || a.drop.least};
     const bool there[4] = {a.x != nullptr, a.dz != nullptr, a.dh != nullptr, a.y != nullptr};

@@ -922,8 +922,8 @@ ebin_status ebin_dropout_execute(ebin_dropout_plan_t plan, const void *x, const 
 /*
  * The gradient: dx = keep(dy) / (1 - p) with the forward call's seed, offset
  * and word (the residual's gradient is dy itself), and dbias [n] binary32, the
- * sum over rows of dx before its rounding, in an order fixed by the plan and
- * the device.  dx may be dy itself.  workspace: at least
+ * sum over rows of dx before its rounding, in an order fixed by the plan, the
+ * device and the buffers' alignment.  dx may be dy itself.  workspace: at least
  * ebin_dropout_plan_workspace bytes, 16-byte aligned, not shared with work in
  * flight on another stream (NULL where that is 0).  With rows = 0 dbias is
  * zeroed.  Errors: as ebin_dropout_execute.
@@ -1048,7 +1048,8 @@ typedef struct ebin_block_norm_grads {
  *     dscale = sum dz (hh w_pre + b_pre),  dshift = sum dz
  *     dw_pre = sum dz (1 + scale) hh,      db_pre = sum dz (1 + scale)
  * the sums over the rows of a group or over all rows, in an order fixed by the
- * plan and the device, so the same inputs give the same bits.
+ * plan, the device, the buffers' alignment and which gradients are wanted, so the
+ * same call gives the same bits.
  *   dz, h      not read with pre = NONE
  *   y          read with post, or where dgate is wanted
  *   dx, dy     NULL: not wanted; either may be an input of its own type (the same

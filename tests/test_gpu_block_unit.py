@@ -51,6 +51,18 @@ def test_parameters_left_out(given, drop):
     check_gradient(t, p, "rms", "layer", drop, dh=False)
 
 
+@pytest.mark.parametrize("given", [("w_pre", "w_post"), ("w_pre", "b_pre", "w_post"),
+                                   ("w_pre", "w_post", "b_post"), ("scale", "shift")])
+@pytest.mark.parametrize("rows,groups,n", [(2500, 0, 4096), (9000, 3, 264), (2500, 0, 4097),
+                                           (3000, 0, 1023), (1300, 2, 8192)])
+def test_rms_norms_by_the_sums_that_are_wanted(rows, groups, n, given):
+    """A bias's or a shift's gradient takes another kernel, on units of another count."""
+    t, p = operands(rows, n, BF16, BF16, groups)
+    p = {k: v for k, v in p.items() if k in given}
+    check_gradient(t, p, "rms", "rms", 0.25)
+    check_gradient(t, p, "rms", "rms")
+
+
 @pytest.mark.parametrize("dtype,stream", TYPES)
 @pytest.mark.parametrize("rows,n", [(5000, 1536), (2500, 4096)])
 def test_strided_rows_and_no_branch(rows, n, dtype, stream):
